@@ -83,7 +83,8 @@ typedef enum {
   KVQ_FMT_NVFP4 = 1,        /* row codec: E2M1 + E4M3 per 16 + one FP32 scale per row */
   KVQ_FMT_INT4 = 2,         /* affine INT4, FP16 minimum and scale per group of G */
   KVQ_FMT_FP8 = 3,          /* E4M3 + one FP32 scale per row */
-  KVQ_FMT_NVFP4_TENSOR = 4  /* E2M1 + E4M3 per 16 along the kind's axis + one FP32 scale per tensor */
+  KVQ_FMT_NVFP4_TENSOR = 4, /* E2M1 + E4M3 per 16 along the kind's axis + one FP32 scale per tensor */
+  KVQ_FMT_FP8_PAGE = 5      /* pools: E4M3 + one power-of-two FP32 scale per (block of tokens, head) */
 } kvq_format;
 typedef enum { KVQ_KIND_KEY = 0, KVQ_KIND_VALUE = 1 } kvq_kind;
 
@@ -92,6 +93,7 @@ typedef enum { KVQ_KIND_KEY = 0, KVQ_KIND_VALUE = 1 } kvq_kind;
 #define KVQ_DEV_BAD_BLOCK 2u  /* block-table entry < 0 or past the pool (row skipped) */
 #define KVQ_DEV_BAD_POS 4u    /* position outside [0, rows) or not strictly increasing */
 #define KVQ_DEV_BAD_SEQLEN 8u /* seq_lens[s] outside [0, min(max_seq_len, blocks*block_size)] */
+#define KVQ_DEV_NO_SPACE 32u  /* page plan: the free list or the token arrays ran out (request refused) */
 #define KVQ_DEV_TIMEOUT 16u   /* decode attention: a bounded wait for a copy ran out (results unspecified) */
 
 /* A bf16 view: element (r, h, d) is ptr[r*row_pitch + h*head_pitch + d].
@@ -114,6 +116,9 @@ typedef struct {
  *   rscale [num_slots][num_heads]               FP32 row scales
  * Format FP8: codes [num_slots][num_heads][head_dim] E4M3 bytes, rscale as above,
  * bscale unused (may be NULL).
+ * Format FP8_PAGE: codes as FP8; rscale [num_slots / block_size][num_heads], one scale for
+ * the block_size tokens of a (block, head): value = e4m3 * rscale[slot / block_size][head].
+ * The library writes powers of two; its readers take any scale.
  * Slot = block * block_size + offset.  Every plane used must be 16-byte aligned. */
 typedef struct {
   uint8_t* codes;
@@ -128,7 +133,7 @@ typedef struct {
   int32_t block_size; /* tokens per page (16 in the pages' pools) */
   int32_t num_heads;
   int32_t head_dim;   /* a multiple of 16, at most 512 */
-  int32_t fmt;        /* format of the K plane: KVQ_FMT_NVFP4 or KVQ_FMT_FP8 */
+  int32_t fmt;        /* format of the K plane: KVQ_FMT_NVFP4, KVQ_FMT_FP8 or KVQ_FMT_FP8_PAGE */
   int32_t v_fmt;      /* format of the V plane; 0 = the same as fmt.  FP8 K with NVFP4 V
                          is the k8v4 split of the FreeToken page (fp8 store notes) */
 } kvq_pool;
@@ -163,7 +168,8 @@ typedef struct {
 } kvq_packed;
 
 /* Fused quantise + scatter of K and V into a paged pool (the encode hot path), each
- * in its plane's format (NVFP4, or FP8 E4M3 with one FP32 scale per row).
+ * in its plane's format (NVFP4, FP8 E4M3 with one FP32 scale per row, or FP8 E4M3 with one
+ * scale per (block, head)).
  * Source: FreeToken PR #408, Summary ("CUDA Graph-safe KV writes") and the fp8 store
  * notes (the destination slots are read from a device tensor; one launch under graph capture).
  *   k, v       bf16 [num_tokens][num_heads][head_dim] views; either may be NULL
@@ -172,6 +178,16 @@ typedef struct {
  *              negative id skips the token (padding); an id >= num_slots skips it
  *              and sets KVQ_DEV_BAD_SLOT.  Duplicate ids: undefined last writer.
  *   pool       planes written in place (only the rows of the given slots).
+ * Format FP8_PAGE appends to pages: rows of one page that stand next to each other in
+ * slot_ids raise the page's scale together.  With s0 the stored scale (none where it is
+ * not a positive finite number, or where these rows hold the page's first slot, which
+ * starts the page over):
+ *   s = max(s0, the smallest power of two p >= 2^-126 with max|x| <= 448 p)
+ *   codes E4M3(x * (1 / s)); where s > s0 > 0 the page's other rows become
+ *   E4M3(code * (s0 / s)), whatever they hold.
+ * All rows of a (page, head) in one call must stand next to each other (a skipped token
+ * ends a run): two runs on one page, like duplicate ids, leave that page's codes and
+ * scale unspecified.
  * One kernel launch (two when K and V planes have different formats); num_tokens ==
  * 0 launches nothing. */
 KVQ_API kvq_status kvq_quant_scatter(const kvq_bf16_in* k, const kvq_bf16_in* v, int32_t num_tokens,
@@ -187,7 +203,7 @@ KVQ_API kvq_status kvq_quant_scatter(const kvq_bf16_in* k, const kvq_bf16_in* v,
  *                s * max_seq_len + t receives token t of sequence s.  Either may be
  *                NULL (that tensor is not restored); not both.
  * NVFP4: y = bf16(e2m1 * block_scale * row_scale), the product rounded once in fp32;
- * FP8: y = bf16(e4m3 * row_scale).  One launch (two when K and V planes have
+ * FP8: y = bf16(e4m3 * row_scale); FP8_PAGE: the same with the page's scale.  One launch (two when K and V planes have
  * different formats).
  * Rows with a bad block id are skipped (KVQ_DEV_BAD_BLOCK); a sequence with a bad
  * length is skipped whole (KVQ_DEV_BAD_SEQLEN). */
@@ -242,7 +258,8 @@ KVQ_API kvq_status kvq_decode_residual(const kvq_packed* payload, const int32_t*
  * One query token per sequence.  For query head qh (KV head qh / (num_q_heads /
  * pool->num_heads)):
  *   out[s][qh] = softmax_t(scale * q[s][qh] . k_t) . v_t   over t < seq_lens[s],
- * with k_t, v_t the decoded pool rows (each plane in its own format, NVFP4 or FP8).
+ * with k_t, v_t the decoded pool rows (each plane in its own format: NVFP4, FP8 or
+ * FP8_PAGE).  What the pool holds behind a sequence's last token is never used.
  *   q    bf16 [num_seqs][num_q_heads][head_dim] through q->row_pitch (per sequence)
  *        and q->head_pitch (per head), inner stride 1; 16-byte aligned.
  *   out  bf16, indexed the same way through its own pitches.
@@ -303,9 +320,88 @@ KVQ_API kvq_status kvq_decode_attention_noalloc(const kvq_pool* pool, const int3
 KVQ_API size_t kvq_decode_attention_workspace(int32_t num_seqs, int32_t num_heads, int32_t num_q_heads,
                                               int32_t head_dim, int32_t max_seq_len);
 
+/* Options of kvq_attention; a zero field is off. */
+typedef struct {
+  float softcap;               /* logits become softcap * tanh(logit / softcap); >= 0, finite */
+  const float* alibi_slopes;   /* device f32 [num_q_heads]: slope * (key position - query position) is added
+                                  to the (capped) logit; finite */
+  int32_t window;              /* a query at position p sees keys t > p - window only; >= 0 */
+  const int32_t* prefix_lens;  /* device int32 [num_seqs]: every query of sequence s also sees the keys behind
+                                  it up to t < min(prefix_lens[s], seq_lens[s]) */
+  const int32_t* key_starts;   /* device int32 [num_tokens]: a query sees keys t >= key_starts[token] only
+                                  (the first token of its document, or the end of left padding) */
+} kvq_attn_options;
+
+/* Paged attention of several query tokens per sequence over a quantised pool: prompt
+ * chunks behind a cached prefix, draft tokens, single tokens with score options, any mix of
+ * them in one call.  Beside kvq_decode_attention, whose one query sees its whole sequence.
+ *   query_starts  device int32 [num_seqs + 1]: sequence s owns rows query_starts[s] ..
+ *                 query_starts[s + 1] - 1 of q and out, its LAST n tokens: row i of them sits
+ *                 at position p = seq_lens[s] - n + i.  Their K and V rows are in the pool
+ *                 already (kvq_plan_pages, kvq_quant_scatter).  n = 0 is fine.
+ *                 The starts do not decrease.
+ * With lo = max(0, p + 1 - window, key_starts[row]) and hi = max(p + 1, prefix), row and
+ * query head qh (KV head qh / (num_q_heads / pool->num_heads)) get
+ *   softmax over t in [lo, hi) of  cap(scale * q . k_t) + slope * (t - p),  times v_t;
+ * a row that sees no key gets zeros.  K and V rows that no row of a call sees are never
+ * used, whatever they hold.
+ *   q, out        bf16 [num_tokens][num_q_heads][head_dim] through their own pitches.
+ *   max_query_len at least the largest n (at most max_seq_len is used).
+ *   head_dim 64, 128 or 256; at most 16 query heads per KV head; scale positive, finite.
+ *   options       host struct, read during the call; NULL: plain causal attention.
+ *   workspace     device memory of kvq_attention_workspace(...) bytes, 16-byte aligned (may be
+ *                 NULL when that is 0); caller-owned.  Calls that may overlap on the GPU, and
+ *                 graphs that may replay at the same time, need one each.
+ * Accuracy as kvq_decode_attention (one f16 rounding of P, one bf16 rounding of out; products,
+ * maxima and sums in fp32); the cap is within 2^-20 of softcap absolutely.
+ * A sequence whose length is outside [0, min(max_seq_len, max_blocks * block_size)], or whose
+ * query rows are outside [0, num_tokens], more than max_query_len or more than its length,
+ * keeps its rows of out (KVQ_DEV_BAD_SEQLEN); rows that need a block entry outside the pool
+ * keep theirs (KVQ_DEV_BAD_BLOCK); rows of no sequence keep theirs.
+ * One or two kernel launches; may be captured in a CUDA graph. */
+KVQ_API kvq_status kvq_attention(const kvq_pool* pool, const int32_t* block_table, int32_t num_seqs,
+                                 int32_t max_blocks, const int32_t* seq_lens, int32_t max_seq_len,
+                                 const kvq_bf16_in* q, const int32_t* query_starts, int32_t num_tokens,
+                                 int32_t max_query_len, int32_t num_q_heads, float scale,
+                                 const kvq_attn_options* options, const kvq_bf16_out* out, void* workspace,
+                                 size_t workspace_bytes, uint32_t* dev_status, kvq_stream_t stream);
+
+/* Workspace bytes kvq_attention needs for these sizes on the current device (0 when the
+ * call runs without one).  Host-only query. */
+KVQ_API size_t kvq_attention_workspace(int32_t num_seqs, int32_t num_tokens, int32_t num_heads,
+                                       int32_t num_q_heads, int32_t head_dim, int32_t max_query_len,
+                                       int32_t max_seq_len);
+
+/* Page plan of a step: block tables, slot maps and lengths from request lengths, on the
+ * GPU, ready for kvq_quant_scatter, kvq_decode_attention and kvq_attention.
+ * Request s holds cached_lens[s] tokens (c) and gets new_lens[s] more (n).  It takes
+ * ceil((c + n) / block_size) - ceil(c / block_size) blocks off free_blocks, requests in order:
+ *   block_table  [num_seqs][max_blocks]: the entries of the new blocks are written, no other.
+ *   seq_lens     [num_seqs]: c + n.
+ *   query_starts [num_seqs + 1]: prefix sums of n (at most max_tokens).
+ *   slot_ids     [max_tokens]: token query_starts[s] + i goes to the slot of position c + i;
+ *                -1 behind the last token (kvq_quant_scatter skips those).
+ *   positions    [max_tokens]: c + i; -1 behind the last token.  May be NULL.
+ *   num_used     [1]: how many blocks of the free list are taken.
+ * All int32 (slot_ids int64) device memory; no output may overlap an input.
+ * A request is refused when a length is negative or c + n exceeds max_blocks * block_size
+ * (KVQ_DEV_BAD_SEQLEN), or when the free list or max_tokens does not reach for it
+ * (KVQ_DEV_NO_SPACE): its seq_lens entry and slots become -1, so that the calls after this
+ * one leave it alone, and its table row stays; later requests that need blocks are refused
+ * with it once the free list has run out.  A token whose block entry is negative gets
+ * slot -1 (KVQ_DEV_BAD_BLOCK).
+ * One kernel launch; may be captured in a CUDA graph. */
+KVQ_API kvq_status kvq_plan_pages(const int32_t* cached_lens, const int32_t* new_lens, int32_t num_seqs,
+                                  const int32_t* free_blocks, int32_t num_free, int32_t block_size,
+                                  int32_t* block_table, int32_t max_blocks, int32_t* seq_lens,
+                                  int32_t* query_starts, int64_t* slot_ids, int32_t* positions,
+                                  int32_t max_tokens, int32_t* num_used, uint32_t* dev_status,
+                                  kvq_stream_t stream);
+
 /* Bytes held by codes plus scale sidecars for rows x heads x dim in a format,
  * excluding allocator overhead (vllm-rlt PR #166 review: storage_bytes).  76 per
- * NVFP4 row at dim 128; INT4 G64: 4 + 32/64 bits per element for full groups.
+ * NVFP4 row at dim 128; INT4 G64: 4 + 32/64 bits per element for full groups; FP8_PAGE:
+ * group_size is the block size.
  * Returns 0 for an invalid request.  Host-only; needs no GPU. */
 KVQ_API size_t kvq_storage_bytes(kvq_format fmt, kvq_kind kind, int32_t group_size, int64_t rows,
                          int32_t heads, int32_t dim);

@@ -19,14 +19,15 @@ from typing import Optional
 import torch
 
 from . import _abi
-from ._abi import (DEV_BAD_BLOCK, DEV_BAD_POS, DEV_BAD_SEQLEN, DEV_BAD_SLOT, DEV_TIMEOUT, FMT_FP8, FMT_INT4,
-                   FMT_NVFP4_TENSOR,
+from ._abi import (DEV_BAD_BLOCK, DEV_BAD_POS, DEV_BAD_SEQLEN, DEV_BAD_SLOT, DEV_NO_SPACE, DEV_TIMEOUT, FMT_FP8,
+                   FMT_FP8_PAGE, FMT_INT4, FMT_NVFP4_TENSOR,
                    FMT_NVFP4, KIND_KEY, KIND_VALUE)
 
 __all__ = [
     "KvqError", "KvPool", "Nvfp4Pool", "Packed", "kvq_quant_scatter", "kvq_restore", "kvq_pack",
     "kvq_unpack", "kvq_encode_residual", "kvq_decode_residual", "kvq_decode_attention",
-    "kvq_decode_attention_workspace", "kvq_decode_attention_noalloc", "kvq_storage_bytes",
+    "kvq_decode_attention_workspace", "kvq_decode_attention_noalloc", "kvq_attention",
+    "kvq_attention_workspace", "kvq_plan_pages", "kvq_storage_bytes", "FMT_FP8_PAGE", "DEV_NO_SPACE",
     "kvq_status_string", "kvq_last_error", "library_path", "FMT_NVFP4", "FMT_INT4", "FMT_FP8", "FMT_NVFP4_TENSOR", "KIND_KEY",
     "KIND_VALUE", "DEV_BAD_SLOT", "DEV_BAD_BLOCK", "DEV_BAD_POS", "DEV_BAD_SEQLEN", "DEV_TIMEOUT",
 ]
@@ -97,7 +98,8 @@ class KvPool:
     its own format (fmt for K, v_fmt for V; v_fmt None = the same as fmt).
 
     NVFP4: codes [slots, H, D/2] u8, bscale [slots, H, D/16] u8 (E4M3), rscale [slots, H] f32.
-    FP8:   codes [slots, H, D] u8 (E4M3), rscale [slots, H] f32 (no block scales)."""
+    FP8:   codes [slots, H, D] u8 (E4M3), rscale [slots, H] f32 (no block scales).
+    FP8_PAGE: codes as FP8, rscale [slots / block_size, H] f32, one scale a (block, head)."""
 
     k_codes: torch.Tensor
     k_bscale: Optional[torch.Tensor]
@@ -126,6 +128,8 @@ class KvPool:
         def plane(f):
             if f == FMT_FP8:
                 return u8(num_slots, num_heads, head_dim), None, f32(num_slots, num_heads)
+            if f == FMT_FP8_PAGE:
+                return u8(num_slots, num_heads, head_dim), None, f32(num_slots // block_size, num_heads)
             return (u8(num_slots, num_heads, head_dim // 2), u8(num_slots, num_heads, head_dim // 16),
                     f32(num_slots, num_heads))
 
@@ -141,7 +145,7 @@ class KvPool:
 
     @property
     def head_dim(self) -> int:
-        return self.k_codes.size(2) * (1 if self.fmt == FMT_FP8 else 2)
+        return self.k_codes.size(2) * (1 if self.fmt in (FMT_FP8, FMT_FP8_PAGE) else 2)
 
     def _planes(self):
         return [t for t in (self.k_codes, self.k_bscale, self.k_rscale, self.v_codes, self.v_bscale,
@@ -162,6 +166,10 @@ class KvPool:
         for t in self._planes():
             if not t.is_contiguous():
                 raise ValueError("pool planes must be contiguous")
+        for f, sc, name in ((self.fmt, self.k_rscale, "k_rscale"),
+                            (self.fmt if self.v_fmt is None else self.v_fmt, self.v_rscale, "v_rscale")):
+            if f == FMT_FP8_PAGE and sc.numel() != self.num_slots // self.block_size * self.num_heads:
+                raise ValueError(f"{name} must be [blocks, heads] for FMT_FP8_PAGE")
         bs = lambda t: None if t is None else t.data_ptr()
         st = _abi.Pool(
             _abi.Plane(self.k_codes.data_ptr(), bs(self.k_bscale), self.k_rscale.data_ptr()),
@@ -245,7 +253,7 @@ class Packed:
 def kvq_quant_scatter(k: Optional[torch.Tensor], v: Optional[torch.Tensor], slot_ids: torch.Tensor,
                       pool: KvPool, dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Quantise + scatter of K/V [T, H, D] bf16 into pool slots slot_ids[T] (int64), in the
-    pool's format (NVFP4 or FP8)."""
+    pool's formats (NVFP4, FP8 or FP8_PAGE)."""
     src = k if k is not None else v
     if src is None:
         raise ValueError("k and v are both None")
@@ -258,6 +266,14 @@ def kvq_quant_scatter(k: Optional[torch.Tensor], v: Optional[torch.Tensor], slot
     _check(_lib().kvq_quant_scatter(
         ctypes.byref(kin) if kin is not None else None, ctypes.byref(vin) if vin is not None else None,
         T, _ptr(slot_ids), ctypes.byref(ps), _ptr(dev_status), _stream(stream)))
+
+
+def _workspace(nbytes: int, device, stream) -> torch.Tensor:
+    """Scratch of one call, kept from reuse until the call's own stream is done with it."""
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
 
 
 def _seq_view(t: torch.Tensor, S: int, Tmax: int, name: str):
@@ -355,7 +371,7 @@ def kvq_decode_attention(pool: KvPool, block_table: torch.Tensor, seq_lens: torc
     Hq = q.size(1)
     need = kvq_decode_attention_workspace(S, pool.num_heads, Hq, pool.head_dim, max_seq_len)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _workspace(need, q.device, stream)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     ps = pool._struct()
     _check(_lib().kvq_decode_attention(
@@ -380,6 +396,85 @@ def kvq_decode_attention_noalloc(pool: KvPool, block_table: torch.Tensor, seq_le
         ctypes.byref(ps), _ptr(block_table), S, max_blocks, _ptr(seq_lens), max_seq_len, ctypes.byref(qi),
         q.size(1), float(scale), ctypes.byref(oo), _ptr(dev_status), _stream(stream)))
     return out
+
+
+def kvq_attention_workspace(num_seqs: int, num_tokens: int, num_heads: int, num_q_heads: int, head_dim: int,
+                            max_query_len: int, max_seq_len: int) -> int:
+    return int(_lib().kvq_attention_workspace(num_seqs, num_tokens, num_heads, num_q_heads, head_dim,
+                                              max_query_len, max_seq_len))
+
+
+def _vec(t: Optional[torch.Tensor], dtype, name: str, n: Optional[int] = None):
+    """Pointer of a contiguous 1-d tensor of a dtype (and length n); None stays None."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.dim() != 1 or not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise ValueError(f"{name} must be a contiguous 1-d tensor" + ("" if n is None else f" of {n} entries"))
+    return t.data_ptr()
+
+
+def kvq_attention(pool: KvPool, block_table: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int,
+                  q: torch.Tensor, query_starts: torch.Tensor, max_query_len: int, scale: float,
+                  out: torch.Tensor, *, softcap: float = 0.0, alibi_slopes: Optional[torch.Tensor] = None,
+                  window: int = 0, prefix_lens: Optional[torch.Tensor] = None,
+                  key_starts: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  dev_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of the query rows q [T, Hq, D] bf16 (sequence s owns rows query_starts[s] to
+    query_starts[s + 1], its last tokens) over the pool's K/V into out [T, Hq, D] bf16; the
+    score options are those of kvq_attn_options.  A workspace tensor is allocated when none
+    is given."""
+    if block_table.dtype != torch.int32:
+        raise TypeError("block_table must be int32")
+    if not block_table.is_contiguous():
+        raise ValueError("block_table must be contiguous [S, max_blocks]")
+    S, max_blocks = block_table.shape
+    qi, oo = _bf16_in(q, "q"), _bf16_out(out, "out")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    T, Hq, D = q.shape
+    if D != pool.head_dim:
+        raise ValueError(f"q has head_dim {D}, the pool {pool.head_dim}")
+    lens = _vec(seq_lens, torch.int32, "seq_lens", S)
+    starts = _vec(query_starts, torch.int32, "query_starts", S + 1)
+    opts = None
+    if softcap != 0.0 or window != 0 or not (alibi_slopes is None and prefix_lens is None and key_starts is None):
+        opts = _abi.AttnOptions(float(softcap), _vec(alibi_slopes, torch.float32, "alibi_slopes", Hq), int(window),
+                                _vec(prefix_lens, torch.int32, "prefix_lens", S),
+                                _vec(key_starts, torch.int32, "key_starts", T))
+    if workspace is None:
+        need = kvq_attention_workspace(S, T, pool.num_heads, Hq, D, max_query_len, max_seq_len)
+        if need > 0:
+            workspace = _workspace(need, q.device, stream)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ps = pool._struct()
+    _check(_lib().kvq_attention(
+        ctypes.byref(ps), block_table.data_ptr(), S, max_blocks, lens, max_seq_len, ctypes.byref(qi), starts, T,
+        max_query_len, Hq, float(scale), None if opts is None else ctypes.byref(opts), ctypes.byref(oo),
+        _ptr(workspace), nbytes, _ptr(dev_status), _stream(stream)))
+    return out
+
+
+def kvq_plan_pages(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_blocks: torch.Tensor, block_size: int,
+                   block_table: torch.Tensor, seq_lens: torch.Tensor, query_starts: torch.Tensor,
+                   slot_ids: torch.Tensor, positions: Optional[torch.Tensor], num_used: torch.Tensor,
+                   dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Block tables, slot maps and lengths of a step from request lengths (see include/kvq.h):
+    block_table [S, max_blocks], seq_lens [S], query_starts [S + 1], slot_ids (int64) and
+    positions [max_tokens] and num_used [1] are written."""
+    if block_table.dtype != torch.int32:
+        raise TypeError("block_table must be int32")
+    if not block_table.is_contiguous():
+        raise ValueError("block_table must be contiguous [S, max_blocks]")
+    S, max_blocks = block_table.shape
+    i32, n = torch.int32, slot_ids.numel()
+    _check(_lib().kvq_plan_pages(
+        _vec(cached_lens, i32, "cached_lens", S), _vec(new_lens, i32, "new_lens", S), S,
+        _vec(free_blocks, i32, "free_blocks"), free_blocks.numel(), block_size, block_table.data_ptr(), max_blocks,
+        _vec(seq_lens, i32, "seq_lens", S), _vec(query_starts, i32, "query_starts", S + 1),
+        _vec(slot_ids, torch.int64, "slot_ids"), _vec(positions, i32, "positions", n), n,
+        _vec(num_used, i32, "num_used", 1), _ptr(dev_status), _stream(stream)))
 
 
 def kvq_storage_bytes(fmt: int, kind: int, group_size: int, rows: int, heads: int, dim: int) -> int:

@@ -21,6 +21,7 @@ FMT_NVFP4 = 1
 FMT_INT4 = 2
 FMT_FP8 = 3
 FMT_NVFP4_TENSOR = 4
+FMT_FP8_PAGE = 5
 KIND_KEY = 0
 KIND_VALUE = 1
 
@@ -29,6 +30,7 @@ DEV_BAD_BLOCK = 2
 DEV_BAD_POS = 4
 DEV_BAD_SEQLEN = 8
 DEV_TIMEOUT = 16
+DEV_NO_SPACE = 32
 
 
 class Bf16In(ctypes.Structure):
@@ -53,6 +55,16 @@ class Pool(ctypes.Structure):
         ("head_dim", ctypes.c_int32),
         ("fmt", ctypes.c_int32),
         ("v_fmt", ctypes.c_int32),
+    ]
+
+
+class AttnOptions(ctypes.Structure):
+    _fields_ = [
+        ("softcap", ctypes.c_float),
+        ("alibi_slopes", ctypes.c_void_p),
+        ("window", ctypes.c_int32),
+        ("prefix_lens", ctypes.c_void_p),
+        ("key_starts", ctypes.c_void_p),
     ]
 
 
@@ -93,6 +105,11 @@ SIGNATURES = {
     "kvq_decode_attention_workspace": (ctypes.c_size_t, [_I32, _I32, _I32, _I32, _I32]),
     "kvq_decode_attention_noalloc": (_ST, [ctypes.POINTER(Pool), _P, _I32, _I32, _P, _I32, ctypes.POINTER(Bf16In),
                                            _I32, ctypes.c_float, ctypes.POINTER(Bf16Out), _P, _P]),
+    "kvq_attention": (_ST, [ctypes.POINTER(Pool), _P, _I32, _I32, _P, _I32, ctypes.POINTER(Bf16In), _P, _I32,
+                            _I32, _I32, ctypes.c_float, ctypes.POINTER(AttnOptions), ctypes.POINTER(Bf16Out),
+                            _P, ctypes.c_size_t, _P, _P]),
+    "kvq_attention_workspace": (ctypes.c_size_t, [_I32] * 7),
+    "kvq_plan_pages": (_ST, [_P, _P, _I32, _P, _I32, _I32, _P, _I32, _P, _P, _P, _P, _I32, _P, _P, _P]),
     "kvq_storage_bytes": (ctypes.c_size_t, [_ST, _ST, _I32, _I64, _I32, _I32]),
     "kvq_status_string": (ctypes.c_char_p, [_ST]),
     "kvq_last_error": (ctypes.c_char_p, []),

@@ -40,429 +40,11 @@
 #include <atomic>
 #include <mutex>
 
-#include "kvq_device.cuh"
-#include "kvq_params.h"
+#include "attn_tile.cuh"
 
 namespace kvq {
 
 namespace {
-
-constexpr int kAttnWarps = 4;
-constexpr int kAttnThreads = 32 * kAttnWarps;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNegInf = -__builtin_huge_valf();
-
-__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t f32x2_to_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// Both E4M3 bytes of `two` (low byte -> low half) to f16x2, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-  uint32_t r;
-  const uint16_t in = static_cast<uint16_t>(two & 0xFFFFu);
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(in));
-  return r;
-}
-
-// The four E2M1 pairs of a word, byte i -> f16x2 i (low nibble in the low half),
-// exactly; the bytes go to the conversions as .b8 registers (no shifts or masks).
-__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-}
-
-// The two E4M3 pairs of a word, bytes 0-1 -> f16x2 0 and bytes 2-3 -> f16x2 1, exactly.
-__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t w, uint32_t (&h)[2]) {
-  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
-      : "=r"(h[0]), "=r"(h[1])
-      : "r"(w));
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-// The same with results below 2^-126 flushed to zero: used for probabilities, whose
-// row sum is at least 1, so a flushed term is below the sum's own rounding.
-__device__ __forceinline__ float ex2_ftz(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-__device__ __forceinline__ float rcp_approx(float x) {
-  float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-// Asynchronous 4- / 8-byte copies into shared memory (cp.async.ca; 16-byte copies use
-// cp_async16).  The checked build stores zeros instead of copying from outside a
-// registered range.
-template <int N>
-__device__ __forceinline__ void cp_async_small(void* smem_dst, const void* gsrc) {
-  static_assert(N == 4 || N == 8, "4 or 8 bytes");
-  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(smem_dst));
-  if (!KVQ_OK(gsrc, N, N)) {
-    if constexpr (N == 4) {
-      asm volatile("st.shared.b32 [%0], %1;" ::"r"(d), "r"(0u) : "memory");
-    } else {
-      asm volatile("st.shared.v2.b32 [%0], {%1, %1};" ::"r"(d), "r"(0u) : "memory");
-    }
-    return;
-  }
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(gsrc), "n"(N) : "memory");
-}
-
-template <int N>
-__device__ __forceinline__ void cp_async_n(void* smem_dst, const void* gsrc) {
-  if constexpr (N == 16) {
-    cp_async16(smem_dst, gsrc);
-  } else {
-    cp_async_small<N>(smem_dst, gsrc);
-  }
-}
-
-__device__ __forceinline__ int64_t shfl64(int64_t v, int src) {
-  const int lo = __shfl_sync(0xFFFFFFFFu, static_cast<int>(v & 0xFFFFFFFF), src);
-  const int hi = __shfl_sync(0xFFFFFFFFu, static_cast<int>(v >> 32), src);
-  return (static_cast<int64_t>(hi) << 32) | static_cast<uint32_t>(lo);
-}
-
-// Shared-memory layout of one 16-token tile of one KV head (both K and V).  Row
-// strides are chosen so that each access phase of a warp covers 32 distinct banks:
-// a K read is one lane's contiguous chunk (D/8 or D/4 bytes at lane c's offset) of
-// token 8j + g; a V read is D/16 or D/8 bytes at lane g's offset of token 2c (+1,
-// +8, +9), which needs a row stride of 4 mod 16 words (the code bytes + 16).
-template <int D, int kFK, int kFV>
-struct AttnTile {
-  static constexpr int kCK = kFK == 3 ? D : D / 2;  // code bytes per row
-  static constexpr int kCV = kFV == 3 ? D : D / 2;
-  static constexpr int kSK = kFK == 3 ? (D == 128 ? 144 : D) : (D == 256 ? 144 : D / 2);  // smem row strides
-  static constexpr int kSV = kCV + 16;
-  static constexpr int kBK = kFK == 3 ? 0 : D / 16;  // block-scale bytes per row
-  static constexpr int kBV = kFV == 3 ? 0 : D / 16;
-  static constexpr int kOffKC = 0;
-  static constexpr int kOffVC = kOffKC + 16 * kSK;
-  static constexpr int kOffKB = kOffVC + 16 * kSV;
-  static constexpr int kOffVB = kOffKB + 16 * kBK;
-  static constexpr int kOffKR = kOffVB + 16 * kBV;
-  static constexpr int kOffVR = kOffKR + 64;
-  static constexpr int kBytes = kOffVR + 64;
-  static constexpr int kStages = kBytes > 4096 ? 3 : 4;
-  static constexpr int kRing = kAttnWarps * kStages * kBytes;
-  // per warp: up to 16 query heads x (O, m, l); Q^T fragments [n-tile][k-step][lane]
-  // (8 B each, up to two n-tiles) + up to 16 head factors
-  static constexpr int kMerge = kAttnWarps * 16 * (D + 2) * 4;
-  static constexpr int kQ = (D / 16) * 32 * 16 + 64;
-  static constexpr int kSmem = kQ + (kRing > kMerge ? kRing : kMerge);
-};
-
-// NW words from shared memory at p (aligned to the access), in 16-, 8- or 4-byte loads.
-template <int NW>
-__device__ __forceinline__ void lds_words(const unsigned char* p, uint32_t (&w)[NW]) {
-  if constexpr (NW % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < NW / 4; ++i) {
-      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
-      w[4 * i] = v.x;
-      w[4 * i + 1] = v.y;
-      w[4 * i + 2] = v.z;
-      w[4 * i + 3] = v.w;
-    }
-  } else if constexpr (NW == 2) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    w[0] = v.x;
-    w[1] = v.y;
-  } else {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
-  }
-}
-
-// Transpose of an 8x8 f16 matrix held as one m16n8 fragment quarter: lane (g, c) gives
-// row g, columns 2c and 2c + 1, and receives row g, columns 2c and 2c + 1 of the
-// transpose.
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-  return r;
-}
-
-// Shared-memory view of one 16-token tile of one KV head: the code, block-scale and row
-// scale rows of token i start at kc / vc / kb / vb / kr / vr + i * stride (bytes).
-struct TileView {
-  const unsigned char *kc, *vc, *kb, *vb, *kr, *vr;
-  int sk, sv, sbk, sbv, sr;
-};
-
-// A warp's running softmax state over its tiles: per head (8nh + 2c + e) the reference
-// m (and m + 8), the partial sum l of this lane's tokens, the V row-scale reference R
-// (R64 = 64 R, rR = 1 / R), and the O^T accumulators o[mt][nh] (dims g*D/8 + 2mt,
-// e = 0, 1, and + 1, e = 2, 3, of heads 8nh + 2c and + 1), relative to R.
-template <int D, int kNH>
-struct AttnState {
-  float m[kNH][2], m8[kNH][2], l[kNH][2], R, R64, rR;
-  float o[D / 16][kNH][4];
-  __device__ __forceinline__ void init() {
-#pragma unroll
-    for (int nh = 0; nh < kNH; ++nh) {
-      m[nh][0] = m[nh][1] = m8[nh][0] = m8[nh][1] = kNegInf;
-      l[nh][0] = l[nh][1] = 0.0f;
-    }
-    R = R64 = rR = 0.0f;
-#pragma unroll
-    for (int mt = 0; mt < D / 16; ++mt)
-#pragma unroll
-      for (int nh = 0; nh < kNH; ++nh) o[mt][nh][0] = o[mt][nh][1] = o[mt][nh][2] = o[mt][nh][3] = 0.0f;
-  }
-};
-
-// One 16-token tile of one KV head into the warp's state: S^T = K Q^T, the softmax
-// update, O^T += V^T P'^T.  nvalid = tokens of the tile inside the sequence (16 but on
-// a split's last tile).  qb(nh, kb) gives the Q^T fragment, qmul the per-head query
-// factors (scale, log2 e, Q's power of two).
-template <int D, int kFK, int kFV, int kNH, typename QB>
-__device__ __forceinline__ void attn_tile(const TileView& tv, const QB& qb, const float (&qmul)[kNH][2], int lane,
-                                          int nvalid, AttnState<D, kNH>& st) {
-  constexpr int kKS = D / 16;
-  constexpr int kMT = D / 16;
-  const int g = lane >> 2;
-  const int c = lane & 3;
-  // S^T = K Q^T: rows g and g + 8 are tokens g and 8 + g (this lane's K rows), each
-  // K fragment serves every head n-tile
-  float sc[kNH][4];
-#pragma unroll
-  for (int nh = 0; nh < kNH; ++nh) sc[nh][0] = sc[nh][1] = sc[nh][2] = sc[nh][3] = 0.0f;
-  if constexpr (kFK == 3) {
-    uint32_t kw[2][D / 16];  // this lane's D/4 code bytes of tokens g and 8 + g
-    lds_words<D / 16>(tv.kc + g * tv.sk + c * (D / 4), kw[0]);
-    lds_words<D / 16>(tv.kc + (8 + g) * tv.sk + c * (D / 4), kw[1]);
-#pragma unroll
-    for (int kb = 0; kb < kKS; ++kb) {
-      uint32_t k0[2], k1[2];
-      e4m3x4_to_f16x2(kw[0][kb], k0);  // dims 4kb, 4kb+1 | 4kb+2, 4kb+3
-      e4m3x4_to_f16x2(kw[1][kb], k1);
-      const uint32_t a[4] = {k0[0], k1[0], k0[1], k1[1]};
-#pragma unroll
-      for (int nh = 0; nh < kNH; ++nh) {
-        const uint2 b = qb(nh, kb);
-        mma_f16_16816(sc[nh], a, b.x, b.y);
-      }
-    }
-  } else {
-    uint32_t kw[2][D / 32];  // this lane's D/8 code bytes of tokens g and 8 + g
-    lds_words<D / 32>(tv.kc + g * tv.sk + c * (D / 8), kw[0]);
-    lds_words<D / 32>(tv.kc + (8 + g) * tv.sk + c * (D / 8), kw[1]);
-    constexpr int kNB = D / 64 > 0 ? D / 64 : 1;  // blocks of this lane's dims
-    uint32_t bsb[2][kNB];                         // their scales, f16 in both halves
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint8_t* kbs = tv.kb + (8 * j + g) * tv.sbk + c * (D / 64);
-      if constexpr (kNB == 1) {
-        const uint32_t bsh = e4m3_to_f16x2(kbs[0]) & 0xFFFFu;
-        bsb[j][0] = bsh | (bsh << 16);
-      } else {  // pairs of scale bytes, one conversion each, halves spread by a permute
-#pragma unroll
-        for (int i = 0; i < kNB; i += 2) {
-          const uint32_t two = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(kbs + i));
-          bsb[j][i] = __byte_perm(two, 0u, 0x1010);
-          bsb[j][i + 1] = __byte_perm(two, 0u, 0x3232);
-        }
-      }
-    }
-#pragma unroll
-    for (int wi = 0; wi < D / 32; ++wi) {  // one code word = k-steps 2wi and 2wi + 1
-      uint32_t hk[2][4];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        e2m1x8_to_f16x2(kw[j][wi], hk[j]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) hk[j][i] = hmul2(hk[j][i], bsb[j][(2 * wi) / 4]);
-      }
-#pragma unroll
-      for (int hs = 0; hs < 2; ++hs) {
-        const uint32_t a[4] = {hk[0][2 * hs], hk[1][2 * hs], hk[0][2 * hs + 1], hk[1][2 * hs + 1]};
-#pragma unroll
-        for (int nh = 0; nh < kNH; ++nh) {
-          const uint2 b = qb(nh, 2 * wi + hs);
-          mma_f16_16816(sc[nh], a, b.x, b.y);
-        }
-      }
-    }
-  }
-  // scores times K's row scale; the query factor (scale, log2 e, Q's power of two,
-  // positive) enters with the reference in one FMA below, and the maxima are scaled
-  // by it once.  Tokens past the end are masked (only a split's last tile can hold
-  // any).
-  const float kr0 = *reinterpret_cast<const float*>(tv.kr + g * tv.sr);
-  const float kr1 = *reinterpret_cast<const float*>(tv.kr + (g + 8) * tv.sr);
-  const float vr0 = *reinterpret_cast<const float*>(tv.vr + g * tv.sr);
-  const float vr1 = *reinterpret_cast<const float*>(tv.vr + (g + 8) * tv.sr);
-  const bool dead0 = g >= nvalid, dead1 = g + 8 >= nvalid;  // past the sequence (last tile only)
-  // this lane's maxima (two tokens per head) first: the references move when any
-  // lane's exceed them, and only then are the tile's maxima reduced across lanes
-  float mt[kNH][2];
-  bool move = false;
-#pragma unroll
-  for (int nh = 0; nh < kNH; ++nh) {
-    sc[nh][0] *= kr0;
-    sc[nh][1] *= kr0;
-    sc[nh][2] *= kr1;
-    sc[nh][3] *= kr1;
-  }
-  if (nvalid < 16) {  // uniform: the tile ends inside the sequence
-#pragma unroll
-    for (int nh = 0; nh < kNH; ++nh) {
-      if (dead0) sc[nh][0] = sc[nh][1] = kNegInf;
-      if (dead1) sc[nh][2] = sc[nh][3] = kNegInf;
-    }
-  }
-#pragma unroll
-  for (int nh = 0; nh < kNH; ++nh) {
-    mt[nh][0] = fmaxf(sc[nh][0], sc[nh][2]) * qmul[nh][0];
-    mt[nh][1] = fmaxf(sc[nh][1], sc[nh][3]) * qmul[nh][1];
-    move = move || mt[nh][0] > st.m8[nh][0] || mt[nh][1] > st.m8[nh][1];
-  }
-  float rmax = fmaxf(vr0, vr1);
-  move = move || rmax > st.R64;
-  // references: the softmax reference m per head and the V row-scale reference st.R
-  // move only when a tile exceeds them by more than 2^8 and 2^6, so P' = exp2(s - m)
-  // * rs_v / st.R stays below 2^14 (f16 holds it) and O is rescaled on few tiles
-  if (__any_sync(0xFFFFFFFFu, move)) {
-#pragma unroll
-    for (int off = 4; off <= 16; off <<= 1) {
-#pragma unroll
-      for (int nh = 0; nh < kNH; ++nh) {
-        mt[nh][0] = fmaxf(mt[nh][0], __shfl_xor_sync(0xFFFFFFFFu, mt[nh][0], off));
-        mt[nh][1] = fmaxf(mt[nh][1], __shfl_xor_sync(0xFFFFFFFFu, mt[nh][1], off));
-      }
-      rmax = fmaxf(rmax, __shfl_xor_sync(0xFFFFFFFFu, rmax, off));
-    }
-    const float Rn = fmaxf(fmaxf(st.R, rmax), 0x1p-126f);
-    const float rr = st.R / Rn;
-#pragma unroll
-    for (int nh = 0; nh < kNH; ++nh) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float mn = fmaxf(st.m[nh][e], mt[nh][e]);
-        const float a = ex2(st.m[nh][e] - mn);  // 0 while m is -inf
-        const float f = a * rr;
-#pragma unroll
-        for (int q = 0; q < kMT; ++q) {
-          st.o[q][nh][e] *= f;
-          st.o[q][nh][e + 2] *= f;
-        }
-        st.l[nh][e] *= a;
-        st.m[nh][e] = mn;
-        st.m8[nh][e] = mn + 8.0f;
-      }
-    }
-    st.R = Rn;
-    st.R64 = Rn * 64.0f;
-    st.rR = rcp_approx(Rn);
-  }
-  // P'^T = exp2(s - m) * rs_v / st.R, transposed in registers into the B operand of
-  // O^T += V^T P'^T: pb[nh][0] holds tokens 2c, 2c + 1 of head 8nh + g, pb[nh][1]
-  // tokens 2c + 8, 2c + 9
-  const float r0 = vr0 * st.rR, r1 = vr1 * st.rR;
-  uint32_t pb[kNH][2];
-#pragma unroll
-  for (int nh = 0; nh < kNH; ++nh) {
-    const float p0 = ex2_ftz(__fmaf_rn(sc[nh][0], qmul[nh][0], -st.m[nh][0]));  // token g
-    const float p1 = ex2_ftz(__fmaf_rn(sc[nh][1], qmul[nh][1], -st.m[nh][1]));
-    const float p2 = ex2_ftz(__fmaf_rn(sc[nh][2], qmul[nh][0], -st.m[nh][0]));  // token g + 8
-    const float p3 = ex2_ftz(__fmaf_rn(sc[nh][3], qmul[nh][1], -st.m[nh][1]));
-    st.l[nh][0] += p0 + p2;
-    st.l[nh][1] += p1 + p3;
-    pb[nh][0] = transpose8x8(f32x2_to_f16x2(p0 * r0, p1 * r0));
-    pb[nh][1] = transpose8x8(f32x2_to_f16x2(p2 * r1, p3 * r1));
-  }
-  // O^T += V^T P'^T: m-tile mt, rows g and g + 8 = dims g * D/8 + 2mt and + 1; this
-  // lane supplies V for tokens (2c, 2c + 1) and (2c + 8, 2c + 9) at those dims
-  {
-    const int ta0 = 2 * c, ta1 = 2 * c + 8;
-    if constexpr (kFV == 3) {
-      uint32_t v0[D / 32], v1[D / 32], v2[D / 32], v3[D / 32];  // D/8 bytes of each token
-      lds_words<D / 32>(tv.vc + ta0 * tv.sv + g * (D / 8), v0);
-      lds_words<D / 32>(tv.vc + (ta0 + 1) * tv.sv + g * (D / 8), v1);
-      lds_words<D / 32>(tv.vc + ta1 * tv.sv + g * (D / 8), v2);
-      lds_words<D / 32>(tv.vc + (ta1 + 1) * tv.sv + g * (D / 8), v3);
-#pragma unroll
-      for (int q = 0; q < kMT; ++q) {  // dims 2q, 2q + 1: bytes of one half word
-        const int wd = q / 2, bo2 = 2 * (q % 2);
-        const uint32_t sel = bo2 | ((4 + bo2) << 4) | ((bo2 + 1) << 8) | ((5 + bo2) << 12);
-        uint32_t h01[2], h23[2];
-        e4m3x4_to_f16x2(__byte_perm(v0[wd], v1[wd], sel), h01);
-        e4m3x4_to_f16x2(__byte_perm(v2[wd], v3[wd], sel), h23);
-        const uint32_t a[4] = {h01[0], h01[1], h23[0], h23[1]};
-#pragma unroll
-        for (int nh = 0; nh < kNH; ++nh) mma_f16_16816(st.o[q][nh], a, pb[nh][0], pb[nh][1]);
-      }
-    } else {
-      constexpr int kW = D / 64;  // code words per lane per token (D/16 bytes)
-      uint32_t v0[kW], v1[kW], v2[kW], v3[kW];
-      lds_words<kW>(tv.vc + ta0 * tv.sv + g * (D / 16), v0);
-      lds_words<kW>(tv.vc + (ta0 + 1) * tv.sv + g * (D / 16), v1);
-      lds_words<kW>(tv.vc + ta1 * tv.sv + g * (D / 16), v2);
-      lds_words<kW>(tv.vc + (ta1 + 1) * tv.sv + g * (D / 16), v3);
-      // block scales of this lane's dims g * D/8 .. + D/8 - 1 for its four tokens: one
-      // 16-dim block (D <= 128) or two (D = 256), as f16x2 pairs (tokens ta, ta + 1)
-      constexpr int kVB = D / 8 > 16 ? D / 128 : 1;
-      const uint8_t* vbs = tv.vb;
-      uint32_t bs01[kVB], bs23[kVB];
-#pragma unroll
-      for (int q = 0; q < kVB; ++q) {
-        const int blk = (g * (D / 8)) / 16 + q;
-        bs01[q] = e4m3x2_to_f16x2(vbs[ta0 * tv.sbv + blk] | (vbs[(ta0 + 1) * tv.sbv + blk] << 8));
-        bs23[q] = e4m3x2_to_f16x2(vbs[ta1 * tv.sbv + blk] | (vbs[(ta1 + 1) * tv.sbv + blk] << 8));
-      }
-#pragma unroll
-      for (int i = 0; i < kW; ++i) {
-        // nibble transpose: X byte b = (dim 2(4i+b) of token a | the same dim of token
-        // b << 4), Y: the odd dims; then byte b of X / Y is m-tile 4i + b, row g / g + 8
-        const uint32_t x01 = (v0[i] & 0x0F0F0F0Fu) | ((v1[i] & 0x0F0F0F0Fu) << 4);
-        const uint32_t y01 = ((v0[i] >> 4) & 0x0F0F0F0Fu) | (v1[i] & 0xF0F0F0F0u);
-        const uint32_t x23 = (v2[i] & 0x0F0F0F0Fu) | ((v3[i] & 0x0F0F0F0Fu) << 4);
-        const uint32_t y23 = ((v2[i] >> 4) & 0x0F0F0F0Fu) | (v3[i] & 0xF0F0F0F0u);
-        uint32_t hx01[4], hy01[4], hx23[4], hy23[4];
-        e2m1x8_to_f16x2(x01, hx01);
-        e2m1x8_to_f16x2(y01, hy01);
-        e2m1x8_to_f16x2(x23, hx23);
-        e2m1x8_to_f16x2(y23, hy23);
-#pragma unroll
-        for (int bb = 0; bb < 4; ++bb) {
-          const int q = 4 * i + bb;             // m-tile: dims 2q, 2q + 1, one 16-block
-          const int vb = kVB == 1 ? 0 : q / 8;  // g * D/8 is a multiple of 16 when D = 256
-          const uint32_t a[4] = {hmul2(hx01[bb], bs01[vb]), hmul2(hy01[bb], bs01[vb]),
-                                 hmul2(hx23[bb], bs23[vb]), hmul2(hy23[bb], bs23[vb])};
-#pragma unroll
-          for (int nh = 0; nh < kNH; ++nh) mma_f16_16816(st.o[q][nh], a, pb[nh][0], pb[nh][1]);
-        }
-      }
-    }
-  }}
 
 template <int D, int kFK, int kFV, int kNH>
 __global__ void __launch_bounds__(kAttnThreads) decode_attn_kernel(const AttnParams p) {
@@ -553,9 +135,12 @@ __global__ void __launch_bounds__(kAttnThreads) decode_attn_kernel(const AttnPar
   bool bad = false;
   // pool row of token (lane & 15) of the warp's tile number `it` (-1 past the end); the
   // block-table load is issued a tile ahead of its copies, so its latency overlaps
-  // the current tile's arithmetic
-  auto row_of = [&](int it) -> int64_t {
+  // the current tile's arithmetic.  srow: the scale this lane copies (lanes 0-15 K's,
+  // 16-31 V's), the row's own or its page's
+  const bool lane_page = lane < 16 ? p.k_page : p.v_page;
+  auto row_of = [&](int it, int64_t& srow) -> int64_t {
     const int tile = warp + it * kAttnWarps;
+    srow = 0;
     if (tile >= ntile) return -1;
     int t = t_begin + tile * 16 + (lane & 15);
     if (t >= t_end) t = t_end - 1;  // a valid token's address; masked later
@@ -566,12 +151,14 @@ __global__ void __launch_bounds__(kAttnThreads) decode_attn_kernel(const AttnPar
       bad = true;
       blk = 0;
     }
-    return (blk * p.block_size + bo) * p.H + h;
+    const int64_t row = (blk * p.block_size + bo) * p.H + h;
+    srow = lane_page ? blk * p.H + h : row;
+    return row;
   };
   // copies of a tile (rows from row_of, uniform -1 when there is none) into stage st:
   // the 32 lanes take consecutive 16-byte pieces of the 16 rows (whole sectors), then
   // lanes 0-15 the K block and row scales and lanes 16-31 the V ones
-  auto issue = [&](int64_t row, int st) {
+  auto issue = [&](int64_t row, int64_t srow, int st) {
     if (__shfl_sync(0xFFFFFFFFu, row, 0) < 0) return;
     unsigned char* const sb = ring + st * T::kBytes;
     const int tt = lane & 15;
@@ -597,10 +184,10 @@ __global__ void __launch_bounds__(kAttnThreads) decode_attn_kernel(const AttnPar
     }
     if (lane < 16) {
       if constexpr (T::kBK > 0) cp_async_n<T::kBK>(sb + T::kOffKB + tt * T::kBK, p.k.bscale + row * T::kBK);
-      cp_async_small<4>(sb + T::kOffKR + tt * 4, p.k.rscale + row);
+      cp_async_small<4>(sb + T::kOffKR + tt * 4, p.k.rscale + srow);
     } else {
       if constexpr (T::kBV > 0) cp_async_n<T::kBV>(sb + T::kOffVB + tt * T::kBV, p.v.bscale + row * T::kBV);
-      cp_async_small<4>(sb + T::kOffVR + tt * 4, p.v.rscale + row);
+      cp_async_small<4>(sb + T::kOffVR + tt * 4, p.v.rscale + srow);
     }
   };
 
@@ -609,22 +196,25 @@ __global__ void __launch_bounds__(kAttnThreads) decode_attn_kernel(const AttnPar
 
 #pragma unroll
   for (int j = 0; j < T::kStages - 1; ++j) {
-    issue(row_of(j), j);
+    int64_t srow;
+    const int64_t row = row_of(j, srow);
+    issue(row, srow, j);
     cp_async_commit();
   }
   const int my_tiles = ntile > warp ? (ntile - warp + kAttnWarps - 1) / kAttnWarps : 0;
   for (int it = 0; it < my_tiles; ++it) {
-    const int64_t row_next = row_of(it + T::kStages - 1);  // the refill's rows, loaded early
+    int64_t srow_next;
+    const int64_t row_next = row_of(it + T::kStages - 1, srow_next);  // the refill's rows, loaded early
     cp_async_wait<T::kStages - 2>();
     __syncwarp();
     const unsigned char* const sb = ring + (it % T::kStages) * T::kBytes;
     const int t0 = t_begin + (warp + it * kAttnWarps) * 16;
 
     const TileView tv{sb + T::kOffKC, sb + T::kOffVC, sb + T::kOffKB, sb + T::kOffVB, sb + T::kOffKR, sb + T::kOffVR,
-                      T::kSK, T::kSV, T::kBK, T::kBV, 4};
-    attn_tile<D, kFK, kFV, kNH>(tv, qb, qmul, lane, t_end - t0, st);
+                      T::kSK, T::kSV, T::kBK, T::kBV, 4, 4};
+    attn_tile<D, kFK, kFV, kNH>(tv, qb, qmul, lane, t_end - t0, st, NoMod{});
     __syncwarp();  // every lane has read this stage before it is refilled
-    issue(row_next, (it + T::kStages - 1) % T::kStages);
+    issue(row_next, srow_next, (it + T::kStages - 1) % T::kStages);
     cp_async_commit();
   }
   cp_async_wait<0>();
@@ -823,7 +413,9 @@ struct PageStage {
   static constexpr int kSmem = kOffBar + 2 * kStages * 8 + 16;  // full + empty barriers, the bad flag
 };
 
-template <int D, int kFK, int kFV, int W, int H>
+// kPg: a plane may be page-scaled (p.k_page / p.v_page); its chunk's H scales are then
+// one 4 H-byte copy (a multiple of 16, H >= 4) that all 16 tokens of the chunk read.
+template <int D, int kFK, int kFV, int W, int H, bool kPg>
 __global__ void __launch_bounds__((W + 1) * 32, W == 8 ? 2 : 1) decode_attn_page_kernel(const AttnParams p) {
   using T = PageStage<D, kFK, kFV, W>;
   constexpr int kKS = D / 16;
@@ -869,6 +461,7 @@ __global__ void __launch_bounds__((W + 1) * 32, W == 8 ? 2 : 1) decode_attn_page
       const int t0 = t_begin + 16 * (P * k + lane);
       bool have = false;
       int64_t r0 = 0;  // pool row (slot, head 0) of the chunk's first token
+      int64_t pg = 0;  // its page
       if (lane < P && t0 < t_end) {
         uint32_t bi, bo;
         p.div_bs.divmod(static_cast<uint32_t>(t0), bi, bo);
@@ -878,9 +471,11 @@ __global__ void __launch_bounds__((W + 1) * 32, W == 8 ? 2 : 1) decode_attn_page
         } else {
           have = true;
           r0 = (blk * p.block_size + bo) * H;
+          pg = blk;
         }
       }
-      const uint32_t bytes = __reduce_add_sync(0xFFFFFFFFu, have ? 16u * H * T::kRow : 0u);
+      const uint32_t ksc = kPg && p.k_page ? 4u * H : 64u * H, vsc = kPg && p.v_page ? 4u * H : 64u * H;
+      const uint32_t bytes = __reduce_add_sync(0xFFFFFFFFu, have ? 16u * H * (T::kRow - 8) + ksc + vsc : 0u);
       const bool any_bad = __any_sync(0xFFFFFFFFu, bad);
       if (k >= T::kStages && !mbar_wait(empty0 + 8 * st, ((k / T::kStages) - 1) & 1)) timed_out = true;
       if (lane == 0) {
@@ -896,8 +491,8 @@ __global__ void __launch_bounds__((W + 1) * 32, W == 8 ? 2 : 1) decode_attn_page
         bulk_copy_g2s(sb + T::kOffVC + jr * T::kCV, p.v.codes + r0 * T::kCV, 16u * H * T::kCV, full);
         if constexpr (T::kBK > 0) bulk_copy_g2s(sb + T::kOffKB + jr * T::kBK, p.k.bscale + r0 * T::kBK, 16u * H * T::kBK, full);
         if constexpr (T::kBV > 0) bulk_copy_g2s(sb + T::kOffVB + jr * T::kBV, p.v.bscale + r0 * T::kBV, 16u * H * T::kBV, full);
-        bulk_copy_g2s(sb + T::kOffKR + jr * 4, p.k.rscale + r0, 16u * H * 4, full);
-        bulk_copy_g2s(sb + T::kOffVR + jr * 4, p.v.rscale + r0, 16u * H * 4, full);
+        bulk_copy_g2s(sb + T::kOffKR + jr * 4, p.k.rscale + (kPg && p.k_page ? pg * H : r0), ksc, full);
+        bulk_copy_g2s(sb + T::kOffVR + jr * 4, p.v.rscale + (kPg && p.v_page ? pg * H : r0), vsc, full);
       }
     }
     const bool bad_any = __any_sync(0xFFFFFFFFu, bad);
@@ -963,8 +558,9 @@ __global__ void __launch_bounds__((W + 1) * 32, W == 8 ? 2 : 1) decode_attn_page
       const int r = 16 * H * j + h;  // row of this chunk's token 0, head h; tokens H rows apart
       const TileView tv{sb + T::kOffKC + r * T::kCK, sb + T::kOffVC + r * T::kCV, sb + T::kOffKB + r * T::kBK,
                         sb + T::kOffVB + r * T::kBV, sb + T::kOffKR + r * 4, sb + T::kOffVR + r * 4,
-                        H * T::kCK, H * T::kCV, H * T::kBK, H * T::kBV, H * 4};
-      attn_tile<D, kFK, kFV, 1>(tv, qb, qmul, lane, t_end - t0, st);
+                        H * T::kCK, H * T::kCV, H * T::kBK, H * T::kBV,
+                        kPg && p.k_page ? 0 : H * 4, kPg && p.v_page ? 0 : H * 4};
+      attn_tile<D, kFK, kFV, 1>(tv, qb, qmul, lane, t_end - t0, st, NoMod{});
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(empty0 + 8 * stg);
@@ -1122,10 +718,10 @@ cudaError_t attn_dispatch_group(const AttnParams& p, cudaStream_t s) {
   return p.group <= 8 ? attn_dispatch_fmt<D, 1>(p, s) : attn_dispatch_fmt<D, 2>(p, s);
 }
 
-template <int D, int kFK, int kFV, int W, int H>
+template <int D, int kFK, int kFV, int W, int H, bool kPg = false>
 cudaError_t page_launch(const AttnParams& p, cudaStream_t s) {
   using T = PageStage<D, kFK, kFV, W>;
-  auto k = decode_attn_page_kernel<D, kFK, kFV, W, H>;
+  auto k = decode_attn_page_kernel<D, kFK, kFV, W, H, kPg>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
   if (e != cudaSuccess) return e;
   const dim3 grid(p.nsplit, 1, p.S);
@@ -1138,6 +734,13 @@ cudaError_t page_launch(const AttnParams& p, cudaStream_t s) {
 template <int D, int W, int H>
 cudaError_t page_dispatch_fmt(const AttnParams& p, cudaStream_t s) {
   const bool k8 = p.fmt_k == 3, v8 = p.fmt_v == 3;
+  if constexpr (H >= 4) {
+    if (p.k_page || p.v_page) {
+      if (k8 && !v8) return page_launch<D, 3, 1, W, H, true>(p, s);
+      if (!k8 && v8) return page_launch<D, 1, 3, W, H, true>(p, s);
+      return page_launch<D, 3, 3, W, H, true>(p, s);
+    }
+  }
   if (!k8 && !v8) return page_launch<D, 1, 1, W, H>(p, s);
   if (k8 && !v8) return page_launch<D, 3, 1, W, H>(p, s);
   if (!k8 && v8) return page_launch<D, 1, 3, W, H>(p, s);
@@ -1232,10 +835,11 @@ int attn_num_splits(int32_t S, int32_t H, int32_t max_seq_len) {
 
 // The page-major kernel serves pages of whole 16-token chunks (block_size a multiple of
 // 16), head_dim 64 or 128, up to 8 query heads per KV head, and H in {1, 2, 4, 8, 16}
-// (W = 8 consumer warps, or 16 at H = 16, P = W / H chunks per stage).
-bool attn_page_ok(int32_t block_size, int32_t H, int32_t D, int32_t group) {
+// (W = 8 consumer warps, or 16 at H = 16, P = W / H chunks per stage).  The H scales of
+// a page are one bulk copy only from H = 4 (16 bytes).
+bool attn_page_ok(int32_t block_size, int32_t H, int32_t D, int32_t group, bool page_scaled) {
   return block_size % 16 == 0 && (D == 64 || D == 128) && group <= 8 &&
-         (H == 1 || H == 2 || H == 4 || H == 8 || H == 16);
+         (H == 1 || H == 2 || H == 4 || H == 8 || H == 16) && (!page_scaled || H >= 4);
 }
 
 // Splits of the page-major kernel: one block per (split, sequence), 2 resident per SM
@@ -1283,7 +887,7 @@ size_t attn_workspace_bytes(int32_t S, int32_t H, int32_t Hq, int32_t D, int32_t
 
 cudaError_t launch_decode_attention(const AttnParams& p_in, cudaStream_t s) {
   AttnParams p = p_in;
-  if (attn_page_ok(p.block_size, p.H, p.D, p.group)) {
+  if (attn_page_ok(p.block_size, p.H, p.D, p.group, p.k_page || p.v_page)) {
     p.nsplit = attn_page_splits(p.S, p.H, p.max_len);
     p.split_len = attn_split_len(p.max_len, p.nsplit, 16);
     switch (p.D) {

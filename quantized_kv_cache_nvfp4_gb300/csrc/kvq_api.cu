@@ -129,13 +129,13 @@ kvq_status check_head_dim(int32_t H, int32_t D) {
 }
 
 // A pool's format and planes (the bscale plane only for NVFP4).
-bool pool_fmt_ok(int32_t f) { return f == KVQ_FMT_NVFP4 || f == KVQ_FMT_FP8; }
+bool pool_fmt_ok(int32_t f) { return f == KVQ_FMT_NVFP4 || f == KVQ_FMT_FP8 || f == KVQ_FMT_FP8_PAGE; }
 
 kvq_status check_pool_fmt(const kvq_pool* pool) {
   if (!pool_fmt_ok(pool->fmt))
-    return fail(KVQ_ERR_INVALID_ARG, "pool fmt must be KVQ_FMT_NVFP4 or KVQ_FMT_FP8 (got %d)", pool->fmt);
+    return fail(KVQ_ERR_INVALID_ARG, "pool fmt must be KVQ_FMT_NVFP4, KVQ_FMT_FP8 or KVQ_FMT_FP8_PAGE (got %d)", pool->fmt);
   if (pool->v_fmt != 0 && !pool_fmt_ok(pool->v_fmt))
-    return fail(KVQ_ERR_INVALID_ARG, "pool v_fmt must be 0, KVQ_FMT_NVFP4 or KVQ_FMT_FP8 (got %d)",
+    return fail(KVQ_ERR_INVALID_ARG, "pool v_fmt must be 0, KVQ_FMT_NVFP4, KVQ_FMT_FP8 or KVQ_FMT_FP8_PAGE (got %d)",
                 pool->v_fmt);
   return KVQ_OK;
 }
@@ -151,7 +151,15 @@ kvq_status check_pool_plane(int32_t fmt, const kvq_plane* pl) {
   if (fmt == KVQ_FMT_NVFP4 && (st = check_plane(pl->bscale, "pool bscale")) != KVQ_OK) return st;
   return check_plane(pl->rscale, "pool rscale");
 }
-int64_t code_bytes_per_row(int32_t fmt, int32_t D) { return fmt == KVQ_FMT_FP8 ? D : D / 2; }
+int64_t code_bytes_per_row(int32_t fmt, int32_t D) { return fmt == KVQ_FMT_NVFP4 ? D / 2 : D; }
+
+// Checked build: the planes of a pool tensor.
+void dbg_plane(const kvq_pool* pool, const kvq_plane* pl, int32_t fmt) {
+  const int64_t rh = pool->num_slots * pool->num_heads;
+  dbg_add(pl->codes, rh * code_bytes_per_row(fmt, pool->head_dim), "pool codes");
+  if (fmt == KVQ_FMT_NVFP4) dbg_add(pl->bscale, rh * (pool->head_dim / 16), "pool bscale");
+  dbg_add(pl->rscale, fmt == KVQ_FMT_FP8_PAGE ? rh / pool->block_size * 4 : rh * 4, "pool rscale");
+}
 
 int lanes_for(int32_t D) {
   int nb = D / 16, L = 1;
@@ -318,13 +326,24 @@ kvq_status scatter_impl(const kvq_bf16_in* k, const kvq_bf16_in* v, int32_t num_
   for (int j = 0; j < 2; ++j) {
     if (src[j] == nullptr) continue;
     dbg_add(src[j]->ptr, view_bytes(num_tokens, src[j]->row_pitch, pool->num_heads, src[j]->head_pitch, pool->head_dim), names[j]);
-    const int64_t rh = pool->num_slots * pool->num_heads;
-    dbg_add(dst[j]->codes, rh * code_bytes_per_row(fmt, pool->head_dim), "pool codes");
-    if (fmt == KVQ_FMT_NVFP4) dbg_add(dst[j]->bscale, rh * (pool->head_dim / 16), "pool bscale");
-    dbg_add(dst[j]->rscale, rh * 4, "pool rscale");
+    dbg_plane(pool, dst[j], fmt);
   }
   dbg_add(slot_ids, 8ll * num_tokens, "slot_ids");
   dbg_add(dev_status, 4, "status");
+  if (fmt == KVQ_FMT_FP8_PAGE) {
+    PageEncodeParams e{};
+    e.ten[0] = p.ten[0];
+    e.ten[1] = p.ten[1];
+    e.ntensors = ntensors;
+    e.T = num_tokens;
+    e.H = pool->num_heads;
+    e.nb = p.nb;
+    e.slot_ids = slot_ids;
+    e.num_slots = pool->num_slots;
+    e.block_size = pool->block_size;
+    e.status = dev_status;
+    return launched(launch_page_encode(e, v8, reinterpret_cast<cudaStream_t>(stream)));
+  }
   return launched(launch_nvfp4_encode(p, kEncScatter, fmt, v8, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -375,10 +394,7 @@ kvq_status restore_impl(const kvq_pool* pool, const int32_t* block_table, int32_
   for (int j = 0; j < 2; ++j) {
     if (out[j] == nullptr) continue;
     dbg_add(out[j]->ptr, view_bytes(static_cast<int64_t>(num_seqs) * max_seq_len, out[j]->row_pitch, pool->num_heads, out[j]->head_pitch, pool->head_dim), names[j]);
-    const int64_t rh = pool->num_slots * pool->num_heads;
-    dbg_add(src[j]->codes, rh * code_bytes_per_row(fmt, pool->head_dim), "pool codes");
-    if (fmt == KVQ_FMT_NVFP4) dbg_add(src[j]->bscale, rh * (pool->head_dim / 16), "pool bscale");
-    dbg_add(src[j]->rscale, rh * 4, "pool rscale");
+    dbg_plane(pool, src[j], fmt);
   }
   dbg_add(block_table, 4ll * num_seqs * max_blocks, "block_table");
   dbg_add(seq_lens, 4ll * num_seqs, "seq_lens");
@@ -735,6 +751,15 @@ KVQ_API size_t kvq_decode_attention_workspace(int32_t num_seqs, int32_t num_head
 
 namespace {
 
+// Plane formats as the attention kernels take them: page-scaled FP8 is FP8 with another
+// scale index.
+void set_plane_fmts(AttnParams& p, int32_t fk, int32_t fv) {
+  p.k_page = fk == KVQ_FMT_FP8_PAGE;
+  p.v_page = fv == KVQ_FMT_FP8_PAGE;
+  p.fmt_k = p.k_page ? KVQ_FMT_FP8 : fk;
+  p.fmt_v = p.v_page ? KVQ_FMT_FP8 : fv;
+}
+
 // Decode attention behind both entry points: the same argument checks, then the split
 // partials go to the caller's workspace, or (builtin) to the library's own scratch.
 kvq_status decode_attention_impl(const kvq_pool* pool, const int32_t* block_table, int32_t num_seqs,
@@ -790,8 +815,7 @@ kvq_status decode_attention_impl(const kvq_pool* pool, const int32_t* block_tabl
   }
   p.k = AttnPlane{pool->k.codes, pool->k.bscale, pool->k.rscale};
   p.v = AttnPlane{pool->v.codes, pool->v.bscale, pool->v.rscale};
-  p.fmt_k = fk;
-  p.fmt_v = fv;
+  set_plane_fmts(p, fk, fv);
   p.q = static_cast<const uint16_t*>(q->ptr);
   p.q_row_pitch = q->row_pitch;
   p.q_head_pitch = q->head_pitch;
@@ -815,13 +839,8 @@ kvq_status decode_attention_impl(const kvq_pool* pool, const int32_t* block_tabl
   p.scale = scale;
   p.status = dev_status;
   dbg_clear();
-  const int64_t rh = pool->num_slots * H;
-  dbg_add(pool->k.codes, rh * code_bytes_per_row(fk, D), "k codes");
-  if (fk == KVQ_FMT_NVFP4) dbg_add(pool->k.bscale, rh * (D / 16), "k bscale");
-  dbg_add(pool->k.rscale, rh * 4, "k rscale");
-  dbg_add(pool->v.codes, rh * code_bytes_per_row(fv, D), "v codes");
-  if (fv == KVQ_FMT_NVFP4) dbg_add(pool->v.bscale, rh * (D / 16), "v bscale");
-  dbg_add(pool->v.rscale, rh * 4, "v rscale");
+  dbg_plane(pool, &pool->k, fk);
+  dbg_plane(pool, &pool->v, fv);
   dbg_add(q->ptr, view_bytes(num_seqs, q->row_pitch, num_q_heads, q->head_pitch, D), "q");
   dbg_add(out->ptr, view_bytes(num_seqs, out->row_pitch, num_q_heads, out->head_pitch, D), "out");
   dbg_add(block_table, 4ll * num_seqs * max_blocks, "block_table");
@@ -855,6 +874,179 @@ KVQ_API kvq_status kvq_decode_attention_noalloc(const kvq_pool* pool, const int3
                                scale, out, nullptr, 0, true, dev_status, stream);
 }
 
+KVQ_API size_t kvq_attention_workspace(int32_t num_seqs, int32_t num_tokens, int32_t num_heads,
+                                       int32_t num_q_heads, int32_t head_dim, int32_t max_query_len,
+                                       int32_t max_seq_len) {
+  return query_attn_workspace_bytes(num_seqs, num_tokens, num_heads, num_q_heads, head_dim, max_query_len,
+                                    max_seq_len);
+}
+
+KVQ_API kvq_status kvq_attention(const kvq_pool* pool, const int32_t* block_table, int32_t num_seqs,
+                                 int32_t max_blocks, const int32_t* seq_lens, int32_t max_seq_len,
+                                 const kvq_bf16_in* q, const int32_t* query_starts, int32_t num_tokens,
+                                 int32_t max_query_len, int32_t num_q_heads, float scale,
+                                 const kvq_attn_options* options, const kvq_bf16_out* out, void* workspace,
+                                 size_t workspace_bytes, uint32_t* dev_status, kvq_stream_t stream) {
+  if (pool == nullptr || q == nullptr || out == nullptr)
+    return fail(KVQ_ERR_INVALID_ARG, "pool, q and out must not be NULL");
+  if (check_pool_fmt(pool) != KVQ_OK) return KVQ_ERR_INVALID_ARG;
+  kvq_status st = check_head_dim(pool->num_heads, pool->head_dim);
+  if (st != KVQ_OK) return st;
+  const int32_t D = pool->head_dim, H = pool->num_heads;
+  if (D != 64 && D != 128 && D != 256)
+    return fail(KVQ_ERR_UNSUPPORTED, "attention supports head_dim 64, 128 or 256 (got %d)", D);
+  if (pool->block_size <= 0 || pool->num_slots < 0 || pool->num_slots % pool->block_size != 0)
+    return fail(KVQ_ERR_INVALID_ARG, "num_slots must be a non-negative multiple of block_size");
+  if (num_seqs < 0 || max_blocks < 0 || max_seq_len < 0 || num_tokens < 0 || max_query_len < 0)
+    return fail(KVQ_ERR_INVALID_ARG, "negative num_seqs, max_blocks, max_seq_len, num_tokens or max_query_len");
+  if (num_q_heads <= 0 || num_q_heads % H != 0)
+    return fail(KVQ_ERR_INVALID_ARG, "num_q_heads must be a positive multiple of num_heads");
+  if (num_q_heads / H > 16) return fail(KVQ_ERR_UNSUPPORTED, "at most 16 query heads per KV head");
+  if (!(scale > 0.0f && scale <= 3.4028235e38f))
+    return fail(KVQ_ERR_INVALID_ARG, "scale must be positive and finite (got %g)", static_cast<double>(scale));
+  const kvq_attn_options none = {0.0f, nullptr, 0, nullptr, nullptr};
+  const kvq_attn_options& o = options != nullptr ? *options : none;
+  if (!(o.softcap >= 0.0f && o.softcap <= 3.4028235e38f))
+    return fail(KVQ_ERR_INVALID_ARG, "softcap must be 0 or positive and finite (got %g)",
+                static_cast<double>(o.softcap));
+  if (o.window < 0) return fail(KVQ_ERR_INVALID_ARG, "negative window");
+  if (num_seqs > 65535 || H > 65535) return fail(KVQ_ERR_UNSUPPORTED, "num_seqs and num_heads must be <= 65535");
+  if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return KVQ_OK;
+  if (!fits_u31(static_cast<int64_t>(num_tokens) * num_q_heads) ||
+      !fits_u31(static_cast<int64_t>(max_query_len) * num_q_heads))
+    return fail(KVQ_ERR_UNSUPPORTED, "num_tokens x num_q_heads too large");
+  bool v8 = true;
+  if ((st = check_view(q->ptr, q->row_pitch, q->head_pitch, "q", v8)) != KVQ_OK) return st;
+  if ((st = check_view(out->ptr, out->row_pitch, out->head_pitch, "out", v8)) != KVQ_OK) return st;
+  const int32_t fk = plane_fmt(pool, 0), fv = plane_fmt(pool, 1);
+  if ((st = check_pool_plane(fk, &pool->k)) != KVQ_OK) return st;
+  if ((st = check_pool_plane(fv, &pool->v)) != KVQ_OK) return st;
+  if ((st = check_dev(block_table, "block_table")) != KVQ_OK) return st;
+  if ((st = check_dev(seq_lens, "seq_lens")) != KVQ_OK) return st;
+  if ((st = check_dev(query_starts, "query_starts")) != KVQ_OK) return st;
+  if (o.alibi_slopes != nullptr && (st = check_dev(o.alibi_slopes, "alibi_slopes")) != KVQ_OK) return st;
+  if (o.prefix_lens != nullptr && (st = check_dev(o.prefix_lens, "prefix_lens")) != KVQ_OK) return st;
+  if (o.key_starts != nullptr && (st = check_dev(o.key_starts, "key_starts")) != KVQ_OK) return st;
+  if (dev_status != nullptr && (st = check_dev(dev_status, "dev_status")) != KVQ_OK) return st;
+  const size_t need = kvq_attention_workspace(num_seqs, num_tokens, H, num_q_heads, D, max_query_len, max_seq_len);
+  if (need > 0) {
+    if ((st = check_dev(workspace, "workspace")) != KVQ_OK) return st;
+    if (!aligned(workspace, 16)) return fail(KVQ_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    if (workspace_bytes < need)
+      return fail(KVQ_ERR_INVALID_ARG, "workspace too small: %zu bytes, need %zu", workspace_bytes, need);
+  }
+  QueryAttnParams p{};
+  AttnParams& a = p.a;
+  a.k = AttnPlane{pool->k.codes, pool->k.bscale, pool->k.rscale};
+  a.v = AttnPlane{pool->v.codes, pool->v.bscale, pool->v.rscale};
+  set_plane_fmts(a, fk, fv);
+  a.q = static_cast<const uint16_t*>(q->ptr);
+  a.q_row_pitch = q->row_pitch;
+  a.q_head_pitch = q->head_pitch;
+  a.out = static_cast<uint16_t*>(out->ptr);
+  a.o_row_pitch = out->row_pitch;
+  a.o_head_pitch = out->head_pitch;
+  a.ws = static_cast<float*>(workspace);
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.max_blocks = max_blocks;
+  const int64_t cap = static_cast<int64_t>(max_blocks) * pool->block_size;
+  a.seq_cap = static_cast<int32_t>(cap < max_seq_len ? cap : max_seq_len);
+  a.block_size = pool->block_size;
+  a.div_bs = FastDiv(static_cast<uint32_t>(pool->block_size));
+  a.num_blocks = pool->num_slots / pool->block_size;
+  a.S = num_seqs;
+  a.H = H;
+  a.Hq = num_q_heads;
+  a.D = D;
+  a.group = num_q_heads / H;
+  a.max_len = max_seq_len;
+  a.scale = scale;
+  a.status = dev_status;
+  p.starts = query_starts;
+  p.num_tokens = num_tokens;
+  p.max_q = max_query_len < max_seq_len ? max_query_len : max_seq_len;
+  if (p.max_q == 0) return KVQ_OK;
+  p.softcap = o.softcap;
+  p.slopes = o.alibi_slopes;
+  p.window = o.window;
+  p.prefix = o.prefix_lens;
+  p.key_starts = o.key_starts;
+  dbg_clear();
+  dbg_plane(pool, &pool->k, fk);
+  dbg_plane(pool, &pool->v, fv);
+  dbg_add(q->ptr, view_bytes(num_tokens, q->row_pitch, num_q_heads, q->head_pitch, D), "q");
+  dbg_add(out->ptr, view_bytes(num_tokens, out->row_pitch, num_q_heads, out->head_pitch, D), "out");
+  dbg_add(block_table, 4ll * num_seqs * max_blocks, "block_table");
+  dbg_add(seq_lens, 4ll * num_seqs, "seq_lens");
+  dbg_add(query_starts, 4ll * (num_seqs + 1), "query_starts");
+  dbg_add(o.alibi_slopes, 4ll * num_q_heads, "alibi_slopes");
+  dbg_add(o.prefix_lens, 4ll * num_seqs, "prefix_lens");
+  dbg_add(o.key_starts, 4ll * num_tokens, "key_starts");
+  if (need > 0) dbg_add(workspace, static_cast<int64_t>(need), "workspace");
+  dbg_add(dev_status, 4, "status");
+  return launched(launch_query_attention(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+KVQ_API kvq_status kvq_plan_pages(const int32_t* cached_lens, const int32_t* new_lens, int32_t num_seqs,
+                                  const int32_t* free_blocks, int32_t num_free, int32_t block_size,
+                                  int32_t* block_table, int32_t max_blocks, int32_t* seq_lens,
+                                  int32_t* query_starts, int64_t* slot_ids, int32_t* positions,
+                                  int32_t max_tokens, int32_t* num_used, uint32_t* dev_status,
+                                  kvq_stream_t stream) {
+  if (num_seqs < 0 || num_free < 0 || max_blocks < 0 || max_tokens < 0)
+    return fail(KVQ_ERR_INVALID_ARG, "negative num_seqs, num_free, max_blocks or max_tokens");
+  if (block_size <= 0) return fail(KVQ_ERR_INVALID_ARG, "block_size must be positive (got %d)", block_size);
+  if (!fits_u31(static_cast<int64_t>(max_blocks) * block_size))
+    return fail(KVQ_ERR_UNSUPPORTED, "max_blocks x block_size too large");
+  kvq_status st;
+  if ((st = check_dev(query_starts, "query_starts")) != KVQ_OK) return st;
+  if ((st = check_dev(num_used, "num_used")) != KVQ_OK) return st;
+  if (num_seqs > 0) {
+    if ((st = check_dev(cached_lens, "cached_lens")) != KVQ_OK) return st;
+    if ((st = check_dev(new_lens, "new_lens")) != KVQ_OK) return st;
+    if ((st = check_dev(seq_lens, "seq_lens")) != KVQ_OK) return st;
+    if (max_blocks > 0 && (st = check_dev(block_table, "block_table")) != KVQ_OK) return st;
+    const int32_t* in[2] = {cached_lens, new_lens};
+    for (int i = 0; i < 2; ++i)  // every thread block reads the lengths while one writes seq_lens
+      if (in[i] < seq_lens + num_seqs && seq_lens < in[i] + num_seqs)
+        return fail(KVQ_ERR_INVALID_ARG, "seq_lens must not overlap cached_lens or new_lens");
+  }
+  if (num_free > 0 && (st = check_dev(free_blocks, "free_blocks")) != KVQ_OK) return st;
+  if (max_tokens > 0 && (st = check_dev(slot_ids, "slot_ids")) != KVQ_OK) return st;
+  if (max_tokens > 0 && positions != nullptr && (st = check_dev(positions, "positions")) != KVQ_OK) return st;
+  if (dev_status != nullptr && (st = check_dev(dev_status, "dev_status")) != KVQ_OK) return st;
+  PlanParams p{};
+  p.cached = cached_lens;
+  p.fresh = new_lens;
+  p.S = num_seqs;
+  p.free_blocks = free_blocks;
+  p.num_free = num_free;
+  p.block_size = block_size;
+  p.div_bs = FastDiv(static_cast<uint32_t>(block_size));
+  p.table = block_table;
+  p.max_blocks = max_blocks;
+  p.seq_lens = seq_lens;
+  p.starts = query_starts;
+  p.slots = slot_ids;
+  p.positions = positions;
+  p.max_tokens = max_tokens;
+  p.used = num_used;
+  p.status = dev_status;
+  dbg_clear();
+  dbg_add(cached_lens, 4ll * num_seqs, "cached_lens");
+  dbg_add(new_lens, 4ll * num_seqs, "new_lens");
+  dbg_add(free_blocks, 4ll * num_free, "free_blocks");
+  dbg_add(block_table, 4ll * num_seqs * max_blocks, "block_table");
+  dbg_add(seq_lens, 4ll * num_seqs, "seq_lens");
+  dbg_add(query_starts, 4ll * (num_seqs + 1), "query_starts");
+  dbg_add(slot_ids, 8ll * max_tokens, "slot_ids");
+  dbg_add(positions, 4ll * max_tokens, "positions");
+  dbg_add(num_used, 4, "num_used");
+  dbg_add(dev_status, 4, "status");
+  return launched(launch_plan_pages(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 KVQ_API size_t kvq_storage_bytes(kvq_format fmt, kvq_kind kind, int32_t group_size, int64_t rows,
                                  int32_t heads, int32_t dim) {
   if (rows < 0 || heads <= 0 || dim <= 0) return 0;
@@ -864,6 +1056,10 @@ KVQ_API size_t kvq_storage_bytes(kvq_format fmt, kvq_kind kind, int32_t group_si
     return static_cast<size_t>(rh * (dim / 2 + dim / 16 + 4));
   }
   if (fmt == KVQ_FMT_FP8) return static_cast<size_t>(rh * (dim + 4));
+  if (fmt == KVQ_FMT_FP8_PAGE) {  // group_size: tokens per block
+    if (group_size <= 0) return 0;
+    return static_cast<size_t>(rh * dim + (rows + group_size - 1) / group_size * heads * 4);
+  }
   if (fmt == KVQ_FMT_NVFP4_TENSOR) {
     if (dim % 16 != 0 || (kind != KVQ_KIND_KEY && kind != KVQ_KIND_VALUE)) return 0;
     const int64_t blocks = kind == KVQ_KIND_KEY ? ((rows + 15) / 16) * heads * dim : rh * (dim / 16);

@@ -173,7 +173,47 @@ struct HostRange {
 HostRange* pending(int* n);  // the list for the next launch (at most 32 entries)
 }  // namespace dbg
 
-// Launchers (return the cudaGetLastError() of the launch).  fmt: 1 NVFP4, 3 FP8.
+// ---------------------------------------------------------------------------
+// FP8 with one scale per (block of tokens, head): scatter.
+// ---------------------------------------------------------------------------
+struct PageEncodeParams {
+  EncodeTensor ten[2];      // dst.rscale: [blocks][H]
+  int32_t ntensors;
+  int32_t T, H, nb;         // tokens, heads, D / 16
+  const int64_t* slot_ids;  // [T]
+  int64_t num_slots;
+  int32_t block_size;
+  int32_t chunk;            // tokens whose leaders one warp serves (set by the launcher, <= 32)
+  uint32_t* status;
+};
+cudaError_t launch_page_encode(const PageEncodeParams& p, bool v8, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// Block tables and slot maps from request lengths.
+// ---------------------------------------------------------------------------
+struct PlanParams {
+  const int32_t* cached;    // [S]
+  const int32_t* fresh;     // [S] new tokens
+  int32_t S;
+  const int32_t* free_blocks;
+  int32_t num_free;
+  int32_t block_size;
+  FastDiv div_bs;
+  int32_t* table;           // [S][max_blocks]
+  int32_t max_blocks;
+  int32_t* seq_lens;        // [S]
+  int32_t* starts;          // [S + 1]
+  int64_t* slots;           // [max_tokens]
+  int32_t* positions;       // [max_tokens] or nullptr
+  int32_t max_tokens;
+  int32_t per_block;        // tokens per thread block (set by the launcher)
+  int32_t* used;            // [1]
+  uint32_t* status;
+};
+cudaError_t launch_plan_pages(const PlanParams& p, cudaStream_t s);
+
+// Launchers (return the cudaGetLastError() of the launch).  fmt: 1 NVFP4, 3 FP8 (decode
+// also 5, page-scaled FP8).
 cudaError_t launch_nvfp4_encode(const EncodeParams& p, int mode, int fmt, bool v8,
                                 cudaStream_t s);
 cudaError_t launch_nvfp4_decode(const DecodeParams& p, int mode, int fmt, bool v8,
@@ -206,12 +246,13 @@ cudaError_t launch_tensor_nvfp4_unpack(const TensorNvfp4Params& p, cudaStream_t 
 struct AttnPlane {
   const uint8_t* codes;   // [slots][H][D/2] (NVFP4) or [slots][H][D] (FP8)
   const uint8_t* bscale;  // [slots][H][D/16] (NVFP4)
-  const float* rscale;    // [slots][H]
+  const float* rscale;    // [slots][H], or [blocks][H] (page-scaled)
 };
 
 struct AttnParams {
   AttnPlane k, v;
-  int32_t fmt_k, fmt_v;
+  int32_t fmt_k, fmt_v;     // 1 NVFP4, 3 FP8
+  bool k_page, v_page;      // FP8 with one scale per (block, head)
   const uint16_t* q;        // bf16 [S][Hq][D] through the pitches below
   int64_t q_row_pitch, q_head_pitch;
   uint16_t* out;            // bf16, same indexing through its own pitches
@@ -242,6 +283,24 @@ cudaError_t launch_decode_attention(const AttnParams& p, cudaStream_t s);
 // entry point that allocates nothing): its device address and size in bytes.
 cudaError_t attn_builtin_scratch(void** ptr, size_t* bytes);
 size_t attn_builtin_scratch_bytes();
+
+// ---------------------------------------------------------------------------
+// Paged attention of several query tokens per sequence.
+// ---------------------------------------------------------------------------
+struct QueryAttnParams {
+  AttnParams a;              // q / out rows are tokens; max_len, nsplit, ws as above
+  const int32_t* starts;     // [S + 1]: tokens of sequence s are starts[s] .. starts[s + 1] - 1
+  int32_t num_tokens;        // rows of q and out
+  int32_t max_q;             // most query tokens of a sequence
+  float softcap;             // 0: none
+  const float* slopes;       // [Hq] or nullptr
+  int32_t window;            // 0: none
+  const int32_t* prefix;     // [S] or nullptr
+  const int32_t* key_starts; // [num_tokens] or nullptr
+};
+size_t query_attn_workspace_bytes(int32_t S, int32_t num_tokens, int32_t H, int32_t Hq, int32_t D,
+                                  int32_t max_q, int32_t max_len);
+cudaError_t launch_query_attention(const QueryAttnParams& p, cudaStream_t s);
 cudaError_t launch_payload_decode(const UnpackParams& p, int lanes, bool v8, cudaStream_t s);
 
 int num_sms();

@@ -220,13 +220,14 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) nvfp4_encode_kernel(cons
 // Restore one row (or skip it): resolve the slot through the block table.
 struct RestoreRow {
   int64_t srow;  // pool row (slot * H + h), or -1 to skip
+  int64_t prow;  // its page's scale (block * H + h)
   uint16_t* y;   // first element of the output row
   const DecodeTensor* ten;
 };
 
 template <int kMode>
 __device__ __forceinline__ RestoreRow resolve_row(const DecodeParams& p, uint32_t row, int li) {
-  RestoreRow r{-1, nullptr, nullptr};
+  RestoreRow r{-1, 0, nullptr, nullptr};
   const int tensor = row >= p.rows_per_tensor ? 1 : 0;
   const uint32_t rr = row - (tensor ? p.rows_per_tensor : 0u);
   uint32_t orow, h;
@@ -249,6 +250,7 @@ __device__ __forceinline__ RestoreRow resolve_row(const DecodeParams& p, uint32_
       return r;
     }
     r.srow = (static_cast<int64_t>(blk) * p.block_size + off) * p.H + h;
+    r.prow = static_cast<int64_t>(blk) * p.H + h;
   } else {
     r.srow = rr;
   }
@@ -286,7 +288,7 @@ __device__ __forceinline__ RowFetch fetch_row(const DecodeParams& p, uint32_t ro
 }
 
 __device__ __forceinline__ RestoreRow finish_row(const DecodeParams& p, const RowFetch& f, int li) {
-  RestoreRow r{-1, nullptr, nullptr};
+  RestoreRow r{-1, 0, nullptr, nullptr};
   const int tensor = f.row >= p.rows_per_tensor ? 1 : 0;
   const uint32_t rr = f.row - (tensor ? p.rows_per_tensor : 0u);
   uint32_t orow, h, s, t, bi, off;
@@ -304,6 +306,7 @@ __device__ __forceinline__ RestoreRow finish_row(const DecodeParams& p, const Ro
   }
   const DecodeTensor& T = p.ten[tensor];
   r.srow = (static_cast<int64_t>(f.blk) * p.block_size + off) * p.H + h;
+  r.prow = static_cast<int64_t>(f.blk) * p.H + h;
   r.y = T.y + static_cast<int64_t>(orow) * T.row_pitch + static_cast<int64_t>(h) * T.head_pitch;
   r.ten = &T;
   return r;
@@ -326,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) nvfp4_decode_kernel(cons
   // FP8 restore: the next iteration's index loads are issued an iteration ahead (its
   // rows are short, so the index chain is a large part of each row's latency; for
   // NVFP4 it measured neither faster nor slower and the rows resolve in place)
-  constexpr bool kAhead = kMode == kDecRestore && kFmt == 3;
+  constexpr bool kAhead = kMode == kDecRestore && kFmt != 1;
   RowFetch fn[R];
   if constexpr (kAhead) {
 #pragma unroll
@@ -338,23 +341,23 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) nvfp4_decode_kernel(cons
     for (int r = 0; r < R; ++r) {
       const uint32_t row = row0 + r * stride;
       if constexpr (kAhead) {
-        rr[r] = (row < total) ? finish_row(p, fn[r], li) : RestoreRow{-1, nullptr, nullptr};
+        rr[r] = (row < total) ? finish_row(p, fn[r], li) : RestoreRow{-1, 0, nullptr, nullptr};
       } else {
-        rr[r] = (row < total) ? resolve_row<kMode>(p, row, li) : RestoreRow{-1, nullptr, nullptr};
+        rr[r] = (row < total) ? resolve_row<kMode>(p, row, li) : RestoreRow{-1, 0, nullptr, nullptr};
       }
     }
     if constexpr (kAhead) {
 #pragma unroll
       for (int r = 0; r < R; ++r) fn[r] = fetch_row(p, row0 + (R + r) * stride, total);
     }
-    if constexpr (kFmt == 3) {  // FP8 E4M3 rows: 16 code bytes per block, one scale
+    if constexpr (kFmt != 1) {  // FP8 E4M3: 16 code bytes per block, one scale (5: the page's)
       uint32_t c8[R][BPL][4];
       float rs8[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (rr[r].srow < 0) continue;
         const DecodeTensor& T = *rr[r].ten;
-        rs8[r] = LDX(T.rscale + rr[r].srow);
+        rs8[r] = LDX(T.rscale + (kFmt == 5 ? rr[r].prow : rr[r].srow));
 #pragma unroll
         for (int j = 0; j < BPL; ++j) load16B(T.codes + rr[r].srow * (16 * p.nb) + 16 * (b0 + j), c8[r][j]);
       }
@@ -495,6 +498,7 @@ cudaError_t launch_nvfp4_encode(const EncodeParams& p, int mode, int fmt, bool v
 
 cudaError_t launch_nvfp4_decode(const DecodeParams& p, int mode, int fmt, bool v8, cudaStream_t s) {
   if (mode != kDecRestore) return cudaErrorInvalidValue;
+  if (fmt == 5) return dec_dispatch<kDecRestore, 5>(p, v8, s);
   return fmt == 3 ? dec_dispatch<kDecRestore, 3>(p, v8, s) : dec_dispatch<kDecRestore, 1>(p, v8, s);
 }
 

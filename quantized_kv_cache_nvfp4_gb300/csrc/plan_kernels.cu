@@ -1,0 +1,167 @@
+// plan_kernels.cu -- block tables and slot maps from request lengths.
+//
+// Request s holds c tokens and gets n: it takes ceil((c + n) / B) - ceil(c / B) blocks off
+// the free list, in request order, and its i-th new token sits at position c + i.
+//   starts[s] = sum of n over the requests before s          (prefix sum)
+//   first[s]  = sum of their block needs                     (prefix sum)
+//   block of page j of request s = table[s][j] for j < ceil(c / B), else
+//                                  free_blocks[first[s] + j - ceil(c / B)]
+// One launch.  Every thread block scans the requests again, 1024 at a time (8 bytes a
+// request, from L2 after the first block), and fills its own range of the token arrays;
+// the scan of a few thousand requests costs less than a second launch would.  A new page
+// always begins with a new token at offset 0, so that token's thread writes the table
+// entry, and no thread reads an entry that another writes.  Bound: launch and scan
+// latency for a decode step, the 12 bytes written per token for large prompts.
+#include "kvq_device.cuh"
+#include "kvq_params.h"
+
+namespace kvq {
+
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+// Exclusive prefix sum over the block; `total` receives the sum.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part, int64_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) part[warp] = x;
+  __syncthreads();
+  int64_t p = part[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, p, o);
+    if (lane >= o) p += y;
+  }
+  total = __shfl_sync(0xFFFFFFFFu, p, 31);
+  const int64_t base = __shfl_sync(0xFFFFFFFFu, p, warp == 0 ? 0 : warp - 1);
+  __syncthreads();  // part is free again
+  return x - v + (warp == 0 ? 0 : base);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_pages_kernel(const PlanParams p) {
+  __shared__ int64_t part[32];
+  __shared__ int32_t sh_start[kPlanThreads];  // first token, at most max_tokens
+  __shared__ int32_t sh_cached[kPlanThreads];
+  __shared__ int32_t sh_first[kPlanThreads];  // first free block, -1: refused
+  const int tid = threadIdx.x;
+  const bool lead = blockIdx.x == 0;  // writes what is not per token
+  const int64_t my_begin = static_cast<int64_t>(blockIdx.x) * p.per_block;
+  const int64_t my_end = min(my_begin + p.per_block, static_cast<int64_t>(p.max_tokens));
+  int64_t tok0 = 0, blk0 = 0;  // totals of the requests before this round
+  int64_t used = 0;
+
+  for (int s0 = 0; s0 < p.S; s0 += kPlanThreads) {
+    const int s = s0 + tid;
+    int32_t c = 0, n = 0;
+    if (s < p.S) {
+      c = LDX(p.cached + s);
+      n = LDX(p.fresh + s);
+    }
+    const bool bad_len = c < 0 || n < 0 ||
+                         static_cast<int64_t>(c) + n > static_cast<int64_t>(p.max_blocks) * p.block_size;
+    int64_t round_tok, round_blk;
+    const int64_t start = tok0 + block_scan(n > 0 ? n : 0, part, round_tok);
+    bool ok = !bad_len && start + n <= p.max_tokens;
+    int32_t need = 0;
+    if (ok) {
+      const uint32_t b = p.block_size;
+      // c + n < 2^31 is not implied: 64-bit sums, divided exactly
+      need = static_cast<int32_t>((static_cast<uint64_t>(c) + n + b - 1) / b - (static_cast<uint64_t>(c) + b - 1) / b);
+    }
+    const int64_t first = blk0 + block_scan(need, part, round_blk);
+    const bool fits = need == 0 || first + need <= p.num_free;
+    const bool out_of_space = !bad_len && (!ok || !fits);
+    ok = ok && fits;
+    sh_start[tid] = static_cast<int32_t>(min(start, static_cast<int64_t>(p.max_tokens)));
+    sh_cached[tid] = c;
+    sh_first[tid] = ok ? (need > 0 ? static_cast<int32_t>(first) : 0) : -1;
+    if (lead) {
+      if (s < p.S) {
+        STX(p.seq_lens + s, ok ? c + n : -1);
+        STX(p.starts + s, sh_start[tid]);
+        if (bad_len) set_status(p.status, 8u);
+        if (out_of_space) set_status(p.status, 32u);
+      }
+      if (ok && need > 0) used = max(used, first + need);
+    }
+    __syncthreads();
+    const int nreq = min(p.S - s0, kPlanThreads);
+    const int64_t round_end = min(tok0 + round_tok, my_end);
+    for (int64_t t = max(tok0, my_begin) + tid; t < round_end; t += kPlanThreads) {
+      int lo = 0, hi = nreq - 1;  // the last request that starts at or before t
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (sh_start[mid] <= t) lo = mid; else hi = mid - 1;
+      }
+      int64_t slot = -1;
+      int32_t pos = -1;
+      if (sh_first[lo] >= 0) {
+        const int32_t cc = sh_cached[lo];
+        const uint32_t q = static_cast<uint32_t>(cc) + static_cast<uint32_t>(t - sh_start[lo]);
+        uint32_t page, off;
+        p.div_bs.divmod(q, page, off);
+        const uint32_t held = cc > 0 ? p.div_bs.div(static_cast<uint32_t>(cc) - 1) + 1 : 0;
+        int32_t* const entry = p.table + static_cast<int64_t>(s0 + lo) * p.max_blocks + page;
+        int32_t blk;
+        if (page < held) {
+          blk = LDX(entry);
+        } else {
+          blk = LDX(p.free_blocks + sh_first[lo] + (page - held));
+          if (off == 0) STX(entry, blk);
+        }
+        pos = static_cast<int32_t>(q);
+        if (blk < 0) {
+          set_status(p.status, 2u);
+        } else {
+          slot = static_cast<int64_t>(blk) * p.block_size + off;
+        }
+      }
+      STX(p.slots + t, slot);
+      if (p.positions != nullptr) STX(p.positions + t, pos);
+    }
+    tok0 += round_tok;
+    blk0 += round_blk;
+    if (!lead && tok0 >= my_end) return;
+    __syncthreads();  // the shared arrays are free again
+  }
+  for (int64_t t = max(tok0, my_begin) + tid; t < my_end; t += kPlanThreads) {  // past the last token
+    STX(p.slots + t, static_cast<int64_t>(-1));
+    if (p.positions != nullptr) STX(p.positions + t, -1);
+  }
+  if (lead) {
+    if (tid == 0) STX(p.starts + p.S, static_cast<int32_t>(min(tok0, static_cast<int64_t>(p.max_tokens))));
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) used = max(used, __shfl_xor_sync(0xFFFFFFFFu, used, o));
+    if ((tid & 31) == 0) part[tid >> 5] = used;
+    __syncthreads();
+    if (tid == 0) {
+      for (int i = 1; i < kPlanThreads / 32; ++i) used = max(used, part[i]);
+      STX(p.used, static_cast<int32_t>(used));
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_plan_pages(const PlanParams& p_in, cudaStream_t s) {
+  PlanParams p = p_in;
+  // four tokens a thread, or more where that would be over two blocks an SM
+  int64_t per = 4 * kPlanThreads;
+  const int64_t most = 2 * num_sms();
+  if (p.max_tokens > per * most) per = ((p.max_tokens + most - 1) / most + kPlanThreads - 1) / kPlanThreads * kPlanThreads;
+  p.per_block = static_cast<int32_t>(per);
+  int64_t blocks = (p.max_tokens + per - 1) / per;
+  if (blocks < 1) blocks = 1;
+  cudaError_t e = cudaSuccess;
+  KVQ_LAUNCH("plan_pages_kernel", s, plan_pages_kernel<<<static_cast<unsigned>(blocks), kPlanThreads, 0, s>>>(p);
+             e = cudaGetLastError());
+  return e;
+}
+
+}  // namespace kvq

@@ -1,0 +1,480 @@
+// query_attn_kernels.cu -- paged attention of several query tokens per sequence.
+//
+// Sequence s has n = starts[s + 1] - starts[s] query tokens, its last ones: token i sits
+// at position pos = seq_lens[s] - n + i and sees the keys t of [lo, hi),
+//   hi = max(pos + 1, min(prefix, len)),  lo = max(0, pos + 1 - window, key_start),
+// with logits  cap(scale q . k_t) + slope (t - pos),  cap(x) = softcap tanh(x / softcap).
+// A row that sees no key is 0.
+//
+// Rows kernel (few rows): a CTA takes 8 or 16 rows (token i, query head of the group) of
+// one KV head and one split of the keys that any of its rows sees; its 4 warps take
+// 16-token tiles in turn through cp.async rings, with the tile arithmetic of the decode
+// kernels (attn_tile.cuh), the score modifier between its two products.  Splits of a
+// sequence merge through the caller's workspace in a second small kernel.
+#include "attn_tile.cuh"
+
+namespace kvq {
+
+namespace {
+
+constexpr float kNoKey = -1e30f;  // the softmax reference before the first key
+
+// tanh(x) = 1 - 2 / (1 + e^2x): an absolute error of a few 2^-23, which is what a capped
+// logit needs (tanh.approx is off by 2^-11 of the cap).
+__device__ __forceinline__ float tanh_abs(float x) {
+  return __fmaf_rn(-2.0f, rcp_approx(1.0f + ex2(2.0f * kLog2e * x)), 1.0f);
+}
+
+// Range of keys that query token `tok` at position pos sees.
+__device__ __forceinline__ void key_range(const QueryAttnParams& p, int s, int tok, int pos, int len, int& lo, int& hi) {
+  lo = 0;
+  hi = pos + 1;
+  if (p.prefix != nullptr) hi = max(hi, min(LDX(p.prefix + s), len));
+  if (p.window > 0) lo = max(lo, pos + 1 - p.window);
+  if (p.key_starts != nullptr) lo = max(lo, LDX(p.key_starts + tok));
+}
+
+// First query token and number of query tokens of sequence s; false where they do not fit
+// the arrays or the sequence.
+__device__ __forceinline__ bool query_range(const QueryAttnParams& p, int s, int& q0, int& n, int& len) {
+  q0 = LDX(p.starts + s);
+  const int q1 = LDX(p.starts + s + 1);
+  len = LDX(p.a.seq_lens + s);
+  n = 0;
+  if (q0 < 0 || q1 < q0 || q1 > p.num_tokens || q1 - q0 > p.max_q || len < 0 || len > p.a.seq_cap || q1 - q0 > len)
+    return false;
+  n = q1 - q0;
+  return true;
+}
+
+// Logits of a tile's scores: sc[nh][e] belongs to row 8 nh + 2c + (e & 1) and token
+// t0 + g + 8 (e >> 1).
+template <int kNH>
+struct QueryMod {
+  static constexpr bool kActive = true;
+  float fac[kNH][2], slope[kNH][2];
+  int lo[kNH][2], hi[kNH][2], pos[kNH][2];
+  float cap, icap;
+  bool biased;
+  int t;  // token of e = 0, 1
+
+  __device__ __forceinline__ void operator()(float (&sc)[kNH][4]) const {
+#pragma unroll
+    for (int nh = 0; nh < kNH; ++nh)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = e & 1, tt = t + 8 * (e >> 1);
+        float x = sc[nh][e] * fac[nh][r];
+        if (cap > 0.0f) x = cap * tanh_abs(x * icap);
+        if (biased) x = __fmaf_rn(slope[nh][r], static_cast<float>(tt - pos[nh][r]), x);
+        x *= kLog2e;
+        sc[nh][e] = tt >= lo[nh][r] && tt < hi[nh][r] ? x : kNegInf;
+      }
+  }
+};
+
+template <int D, int kFK, int kFV, int kNH>
+__global__ void __launch_bounds__(kAttnThreads) query_rows_kernel(const QueryAttnParams qp) {
+  using T = AttnTile<D, kFK, kFV>;
+  const AttnParams& p = qp.a;
+  constexpr int kKS = D / 16;
+  constexpr int kMT = D / 16;
+  constexpr int kRows = 8 * kNH;
+  constexpr bool kQReg = kNH * kKS <= 8;
+  extern __shared__ __align__(16) unsigned char smem[];
+
+  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
+  const int g = lane >> 2;
+  const int c = lane & 3;
+  const int s = blockIdx.z, h = blockIdx.y;
+  const int tile = blockIdx.x / p.nsplit, split = blockIdx.x - tile * p.nsplit;
+  const int row0 = tile * kRows;  // first row (i * group + head) of the CTA
+
+  int q0, nq, len;
+  const bool ok = query_range(qp, s, q0, nq, len);
+  if (!ok && threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) set_status(p.status, 8u);
+  const int rows = nq * p.group;
+  if (row0 >= rows) return;
+
+  // lane r < kRows: row r's range; the CTA's keys are the union
+  int lo = 0x7FFFFFFF, hi = 0;
+  if (lane < kRows && row0 + lane < rows) {
+    const int i = (row0 + lane) / p.group;
+    int l, u;
+    key_range(qp, s, q0 + i, len - nq + i, len, l, u);
+    if (l < u) {
+      lo = l;
+      hi = u;
+    }
+  }
+  const int lo_min = __reduce_min_sync(0xFFFFFFFFu, lo);
+  const int hi_max = __reduce_max_sync(0xFFFFFFFFu, hi);
+  int t_begin = 0, t_end = 0;
+  if (lo_min < hi_max) {  // equal splits, in whole tiles for the four warps
+    const int per = ((hi_max - lo_min + p.nsplit - 1) / p.nsplit + 63) / 64 * 64;
+    t_begin = static_cast<int>(min(static_cast<int64_t>(lo_min) + static_cast<int64_t>(split) * per, static_cast<int64_t>(hi_max)));
+    t_end = min(t_begin + per, hi_max);
+  }
+  const int ntile = (t_end - t_begin + 15) / 16;
+
+  // ---- Q^T fragments, scaled by a power of two into f16, built once by warp 0 ----
+  uint2* const qfrag = reinterpret_cast<uint2*>(smem);
+  float* const qfac = reinterpret_cast<float*>(smem + kNH * kKS * 32 * 8);
+  if (warp == 0) {
+#pragma unroll
+    for (int nh = 0; nh < kNH; ++nh) {
+      const int row = row0 + 8 * nh + g;
+      uint32_t w[D / 8];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) w[i] = 0u;
+      if (row < rows) {
+        const int i = row / p.group;
+        const uint16_t* q = p.q + static_cast<int64_t>(q0 + i) * p.q_row_pitch +
+                            static_cast<int64_t>(h * p.group + row - i * p.group) * p.q_head_pitch + c * (D / 4);
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          uint32_t v4[4];
+          load16B(q + 8 * j, v4);
+          w[4 * j] = v4[0];
+          w[4 * j + 1] = v4[1];
+          w[4 * j + 2] = v4[2];
+          w[4 * j + 3] = v4[3];
+        }
+      }
+      float am = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) am = fmaxf(am, fmaxf(fabsf(bf16lo(w[i])), fabsf(bf16hi(w[i]))));
+      am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+      am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+      int k = 0;
+      if (am > 0.0f) k = 14 - (static_cast<int>((__float_as_uint(am) >> 23) & 0xFF) - 127);
+      k = max(-100, min(120, k));
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+      if (c == 0) qfac[8 * nh + g] = p.scale * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+#pragma unroll
+      for (int kb = 0; kb < kKS; ++kb)
+        qfrag[(nh * kKS + kb) * 32 + lane] = make_uint2(f32x2_to_f16x2(bf16lo(w[2 * kb]) * up, bf16hi(w[2 * kb]) * up),
+                                                        f32x2_to_f16x2(bf16lo(w[2 * kb + 1]) * up, bf16hi(w[2 * kb + 1]) * up));
+    }
+  }
+  __syncthreads();
+  QueryMod<kNH> mod;
+  mod.cap = qp.softcap;
+  mod.icap = qp.softcap > 0.0f ? 1.0f / qp.softcap : 0.0f;
+  mod.biased = qp.slopes != nullptr;
+#pragma unroll
+  for (int nh = 0; nh < kNH; ++nh)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 8 * nh + 2 * c + e;
+      mod.fac[nh][e] = qfac[r];
+      mod.lo[nh][e] = __shfl_sync(0xFFFFFFFFu, lo, r);
+      mod.hi[nh][e] = __shfl_sync(0xFFFFFFFFu, hi, r);
+      const int row = min(row0 + r, rows - 1), i = row / p.group;
+      mod.pos[nh][e] = len - nq + i;
+      mod.slope[nh][e] = mod.biased ? LDX(qp.slopes + h * p.group + row - i * p.group) : 0.0f;
+    }
+  float one[kNH][2];
+#pragma unroll
+  for (int nh = 0; nh < kNH; ++nh) one[nh][0] = one[nh][1] = 1.0f;
+  uint2 qreg[kQReg ? kNH : 1][kQReg ? kKS : 1];
+  if constexpr (kQReg) {
+#pragma unroll
+    for (int nh = 0; nh < kNH; ++nh)
+#pragma unroll
+      for (int kb = 0; kb < kKS; ++kb) qreg[nh][kb] = qfrag[(nh * kKS + kb) * 32 + lane];
+  }
+  auto qb = [&](int nh, int kb) -> uint2 {
+    if constexpr (kQReg) {
+      return qreg[nh][kb];
+    } else {
+      return qfrag[(nh * kKS + kb) * 32 + lane];
+    }
+  };
+
+  // ---- the warp's tiles through its cp.async ring ----
+  unsigned char* const ring = smem + T::kQ + warp * T::kStages * T::kBytes;
+  bool bad = false;
+  const bool lane_page = lane < 16 ? p.k_page : p.v_page;
+  auto row_of = [&](int it, int64_t& srow) -> int64_t {
+    const int kt = warp + it * kAttnWarps;
+    srow = 0;
+    if (kt >= ntile) return -1;
+    int t = t_begin + kt * 16 + (lane & 15);
+    if (t >= t_end) t = t_end - 1;  // a token that is read anyway; masked later
+    uint32_t bi, bo;
+    p.div_bs.divmod(static_cast<uint32_t>(t), bi, bo);
+    int64_t blk = LDX(p.block_table + static_cast<int64_t>(s) * p.max_blocks + bi);
+    if (blk < 0 || blk >= p.num_blocks) {
+      bad = true;
+      blk = 0;
+    }
+    const int64_t row = (blk * p.block_size + bo) * p.H + h;
+    srow = lane_page ? blk * p.H + h : row;
+    return row;
+  };
+  auto issue = [&](int64_t row, int64_t srow, int st) {
+    if (__shfl_sync(0xFFFFFFFFu, row, 0) < 0) return;
+    unsigned char* const sb = ring + st * T::kBytes;
+    const int tt = lane & 15;
+    constexpr int kPK = T::kCK / 16, kPV = T::kCV / 16;
+#pragma unroll
+    for (int i = lane; i < 16 * kPK; i += 32) {
+      const int64_t rr = shfl64(row, i / kPK);
+      cp_async16(sb + T::kOffKC + (i / kPK) * T::kSK + (i % kPK) * 16, p.k.codes + rr * T::kCK + (i % kPK) * 16);
+    }
+#pragma unroll
+    for (int i = lane; i < 16 * kPV; i += 32) {
+      const int64_t rr = shfl64(row, i / kPV);
+      cp_async16(sb + T::kOffVC + (i / kPV) * T::kSV + (i % kPV) * 16, p.v.codes + rr * T::kCV + (i % kPV) * 16);
+    }
+    if (lane < 16) {
+      if constexpr (T::kBK > 0) cp_async_n<T::kBK>(sb + T::kOffKB + tt * T::kBK, p.k.bscale + row * T::kBK);
+      cp_async_small<4>(sb + T::kOffKR + tt * 4, p.k.rscale + srow);
+    } else {
+      if constexpr (T::kBV > 0) cp_async_n<T::kBV>(sb + T::kOffVB + tt * T::kBV, p.v.bscale + row * T::kBV);
+      cp_async_small<4>(sb + T::kOffVR + tt * 4, p.v.rscale + srow);
+    }
+  };
+
+  AttnState<D, kNH> st;
+  st.init(kNoKey);
+#pragma unroll
+  for (int j = 0; j < T::kStages - 1; ++j) {
+    int64_t srow;
+    const int64_t row = row_of(j, srow);
+    issue(row, srow, j);
+    cp_async_commit();
+  }
+  const int my_tiles = ntile > warp ? (ntile - warp + kAttnWarps - 1) / kAttnWarps : 0;
+  for (int it = 0; it < my_tiles; ++it) {
+    int64_t srow_next;
+    const int64_t row_next = row_of(it + T::kStages - 1, srow_next);
+    cp_async_wait<T::kStages - 2>();
+    __syncwarp();
+    const unsigned char* const sb = ring + (it % T::kStages) * T::kBytes;
+    const int t0 = t_begin + (warp + it * kAttnWarps) * 16;
+    const TileView tv{sb + T::kOffKC, sb + T::kOffVC, sb + T::kOffKB, sb + T::kOffVB, sb + T::kOffKR, sb + T::kOffVR,
+                      T::kSK, T::kSV, T::kBK, T::kBV, 4, 4};
+    mod.t = t0 + g;
+    attn_tile<D, kFK, kFV, kNH>(tv, qb, one, lane, t_end - t0, st, mod);
+    __syncwarp();
+    issue(row_next, srow_next, (it + T::kStages - 1) % T::kStages);
+    cp_async_commit();
+  }
+  cp_async_wait<0>();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) set_status(p.status, 2u);
+#pragma unroll
+  for (int off = 4; off <= 16; off <<= 1)
+#pragma unroll
+    for (int nh = 0; nh < kNH; ++nh) {
+      st.l[nh][0] += __shfl_xor_sync(0xFFFFFFFFu, st.l[nh][0], off);
+      st.l[nh][1] += __shfl_xor_sync(0xFFFFFFFFu, st.l[nh][1], off);
+    }
+  const bool cta_bad = __syncthreads_or(bad ? 1 : 0) != 0;  // the ring is free after this
+
+  float* const mo = reinterpret_cast<float*>(smem + T::kQ) + warp * kRows * (D + 2);
+#pragma unroll
+  for (int q = 0; q < kMT; ++q)
+#pragma unroll
+    for (int nh = 0; nh < kNH; ++nh)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        mo[(8 * nh + 2 * c + (e & 1)) * (D + 2) + g * (D / 8) + 2 * q + (e >> 1)] = st.o[q][nh][e] * st.R;
+  if (g == 0) {
+#pragma unroll
+    for (int nh = 0; nh < kNH; ++nh)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mo[(8 * nh + 2 * c + e) * (D + 2) + D] = st.m[nh][e];
+        mo[(8 * nh + 2 * c + e) * (D + 2) + D + 1] = st.l[nh][e];
+      }
+  }
+  __syncthreads();
+  const float* const mall = reinterpret_cast<const float*>(smem + T::kQ);
+  const int live = min(kRows, rows - row0);
+  for (int idx = threadIdx.x; idx < live * D; idx += kAttnThreads) {
+    const int row = idx / D, d = idx % D;
+    float M = kNoKey;
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) M = fmaxf(M, mall[(w * kRows + row) * (D + 2) + D]);
+    float L = 0.0f, O = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) {
+      const float f = ex2(mall[(w * kRows + row) * (D + 2) + D] - M);
+      L += mall[(w * kRows + row) * (D + 2) + D + 1] * f;
+      O += mall[(w * kRows + row) * (D + 2) + d] * f;
+    }
+    const int i = (row0 + row) / p.group;
+    const int qh = h * p.group + row0 + row - i * p.group;
+    const int64_t tok = q0 + i;
+    if (p.nsplit == 1) {
+      if (cta_bad) continue;
+      const float y = L > 0.0f ? O / L : 0.0f;
+      STX(p.out + tok * p.o_row_pitch + static_cast<int64_t>(qh) * p.o_head_pitch + d,
+          static_cast<uint16_t>(pack_bf16x2(y, 0.0f) & 0xFFFFu));
+    } else {
+      float* const wsr = p.ws + ((tok * p.Hq + qh) * p.nsplit + split) * (D + 2);
+      STX(wsr + d, O);
+      if (d == 0) {
+        STX(wsr + D, M);
+        STX(wsr + D + 1, cta_bad ? __int_as_float(0x7FC00000) : L);  // NaN marks a bad block entry
+      }
+    }
+  }
+}
+
+// Merge of the splits of each (token, query head), one warp each, as the decode merge:
+// o = sum_k O_k 2^(M_k - M) / sum_k L_k 2^(M_k - M).  The warp first finds its token's
+// sequence (32-way search over starts): rows of no sequence, or of a refused one, have no
+// partials and stay as they are, as do rows with a NaN mark.
+constexpr int kMergeWarps = 4;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) query_merge_kernel(const QueryAttnParams qp) {
+  const AttnParams& p = qp.a;
+  constexpr int kDL = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
+  const bool live = row < static_cast<int64_t>(qp.num_tokens) * p.Hq;
+  const int tok = live ? static_cast<int>(row / p.Hq) : 0, qh = static_cast<int>(row - static_cast<int64_t>(tok) * p.Hq);
+  int lo = 0, hi = p.S;  // the last s < S with starts[s] <= tok lies in [lo, hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + lane * step;
+    const bool below = at < hi && LDX(qp.starts + at) <= tok;
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, below);
+    const int last = m != 0u ? 31 - __clz(m) : 0;
+    hi = min(hi, lo + (last + 1) * step);
+    lo += last * step;
+  }
+  int q0, n, len;
+  const bool owned = query_range(qp, lo, q0, n, len) && tok >= q0 && tok < q0 + n;
+  // launched as a programmatic dependent of the attention kernel: wait for its results
+  // (every block does, so that this grid's end implies the other's)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!live || !owned) return;
+  const float* const base = p.ws + row * p.nsplit * (D + 2);
+  float M = kNoKey;
+  bool bad = false;
+  for (int k = lane; k < p.nsplit; k += 32) {
+    M = fmaxf(M, LDX(base + k * (D + 2) + D));
+    bad = bad || isnan(LDX(base + k * (D + 2) + D + 1));
+  }
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
+  if (__any_sync(0xFFFFFFFFu, bad)) return;
+  float L = 0.0f;
+  float o[kDL];
+#pragma unroll
+  for (int i = 0; i < kDL; ++i) o[i] = 0.0f;
+  for (int k0 = 0; k0 < p.nsplit; k0 += 32) {
+    float f = 0.0f;
+    if (k0 + lane < p.nsplit) {
+      f = ex2(LDX(base + (k0 + lane) * (D + 2) + D) - M);
+      L += LDX(base + (k0 + lane) * (D + 2) + D + 1) * f;
+    }
+    const int nk = min(32, p.nsplit - k0);
+#pragma unroll 8
+    for (int k = 0; k < nk; ++k) {
+      const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
+      const float* const ok = base + (k0 + k) * (D + 2) + kDL * lane;
+#pragma unroll
+      for (int i = 0; i < kDL; i += 2) {
+        const float2 v = LDX(reinterpret_cast<const float2*>(ok + i));
+        o[i] = __fmaf_rn(v.x, fk, o[i]);
+        o[i + 1] = __fmaf_rn(v.y, fk, o[i + 1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, off);
+  uint16_t* const out = p.out + static_cast<int64_t>(tok) * p.o_row_pitch + static_cast<int64_t>(qh) * p.o_head_pitch;
+#pragma unroll
+  for (int i = 0; i < kDL; i += 2) {
+    const float y0 = L > 0.0f ? o[i] / L : 0.0f;
+    const float y1 = L > 0.0f ? o[i + 1] / L : 0.0f;
+    STX(reinterpret_cast<uint32_t*>(out + kDL * lane + i), pack_bf16x2(y0, y1));
+  }
+}
+
+template <int D>
+cudaError_t launch_query_merge(const QueryAttnParams& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  const int64_t rows = static_cast<int64_t>(p.num_tokens) * p.a.Hq;
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps));
+  cfg.blockDim = dim3(32 * kMergeWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, query_merge_kernel<D>, p);
+}
+
+template <int D, int kFK, int kFV, int kNH>
+cudaError_t rows_launch(const QueryAttnParams& p, cudaStream_t s) {
+  using T = AttnTile<D, kFK, kFV>;
+  auto k = query_rows_kernel<D, kFK, kFV, kNH>;
+  if (T::kSmem > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaError_t e = cudaSuccess;
+  const int64_t tiles = (static_cast<int64_t>(p.max_q) * p.a.group + 8 * kNH - 1) / (8 * kNH);
+  const dim3 grid(static_cast<unsigned>(tiles * p.a.nsplit), p.a.H, p.a.S);
+  KVQ_LAUNCH("query_rows_kernel", s, k<<<grid, kAttnThreads, T::kSmem, s>>>(p); e = cudaGetLastError());
+  if (e != cudaSuccess || p.a.nsplit == 1) return e;
+  KVQ_LAUNCH("query_merge_kernel", s, e = launch_query_merge<D>(p, s));
+  return e;
+}
+
+template <int D, int kNH>
+cudaError_t rows_dispatch_fmt(const QueryAttnParams& p, cudaStream_t s) {
+  const bool k8 = p.a.fmt_k == 3, v8 = p.a.fmt_v == 3;
+  if (!k8 && !v8) return rows_launch<D, 1, 1, kNH>(p, s);
+  if (k8 && !v8) return rows_launch<D, 3, 1, kNH>(p, s);
+  if (!k8 && v8) return rows_launch<D, 1, 3, kNH>(p, s);
+  return rows_launch<D, 3, 3, kNH>(p, s);
+}
+
+template <int D>
+cudaError_t rows_dispatch(const QueryAttnParams& p, int rows, cudaStream_t s) {
+  return rows <= 8 ? rows_dispatch_fmt<D, 1>(p, s) : rows_dispatch_fmt<D, 2>(p, s);
+}
+
+// Splits of the rows kernel, from upper bounds that hold for every call of these sizes.
+int rows_splits(int32_t S, int32_t H, int32_t max_q, int32_t group, int32_t max_len) {
+  const int64_t rows = static_cast<int64_t>(max_q) * group;
+  const int64_t tiles = rows <= 8 ? 1 : (rows + 15) / 16;
+  const int64_t ctas = static_cast<int64_t>(S) * tiles;
+  return ctas > (1 << 24) ? 1 : attn_num_splits(static_cast<int32_t>(ctas), H, max_len);
+}
+
+}  // namespace
+
+size_t query_attn_workspace_bytes(int32_t S, int32_t num_tokens, int32_t H, int32_t Hq, int32_t D, int32_t max_q,
+                                  int32_t max_len) {
+  if (S <= 0 || num_tokens <= 0 || H <= 0 || Hq < H || D <= 0 || max_q <= 0 || max_len <= 0) return 0;
+  if (max_q > max_len) max_q = max_len;  // as the call does
+  const int n = rows_splits(S, H, max_q, Hq / H, max_len);
+  if (n <= 1) return 0;
+  return static_cast<size_t>(num_tokens) * Hq * n * (D + 2) * sizeof(float);
+}
+
+cudaError_t launch_query_attention(const QueryAttnParams& p_in, cudaStream_t s) {
+  QueryAttnParams p = p_in;
+  const int rows = p.max_q * p.a.group;
+  p.a.nsplit = rows_splits(p.a.S, p.a.H, p.max_q, p.a.group, p.a.max_len);
+  switch (p.a.D) {
+    case 64: return rows_dispatch<64>(p, rows, s);
+    case 128: return rows_dispatch<128>(p, rows, s);
+    case 256: return rows_dispatch<256>(p, rows, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace kvq
