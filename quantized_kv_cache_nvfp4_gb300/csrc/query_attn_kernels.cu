@@ -6,46 +6,16 @@
 // with logits  cap(scale q . k_t) + slope (t - pos),  cap(x) = softcap tanh(x / softcap).
 // A row that sees no key is 0.
 //
-// Rows kernel (few rows): a CTA takes 8 or 16 rows (token i, query head of the group) of
+// Rows kernel (few rows; many go to query_tile_kernels.cu): a CTA takes 8 or 16 rows (token i, query head of the group) of
 // one KV head and one split of the keys that any of its rows sees; its 4 warps take
 // 16-token tiles in turn through cp.async rings, with the tile arithmetic of the decode
 // kernels (attn_tile.cuh), the score modifier between its two products.  Splits of a
 // sequence merge through the caller's workspace in a second small kernel.
-#include "attn_tile.cuh"
+#include "query_attn.cuh"
 
 namespace kvq {
 
 namespace {
-
-constexpr float kNoKey = -1e30f;  // the softmax reference before the first key
-
-// tanh(x) = 1 - 2 / (1 + e^2x): an absolute error of a few 2^-23, which is what a capped
-// logit needs (tanh.approx is off by 2^-11 of the cap).
-__device__ __forceinline__ float tanh_abs(float x) {
-  return __fmaf_rn(-2.0f, rcp_approx(1.0f + ex2(2.0f * kLog2e * x)), 1.0f);
-}
-
-// Range of keys that query token `tok` at position pos sees.
-__device__ __forceinline__ void key_range(const QueryAttnParams& p, int s, int tok, int pos, int len, int& lo, int& hi) {
-  lo = 0;
-  hi = pos + 1;
-  if (p.prefix != nullptr) hi = max(hi, min(LDX(p.prefix + s), len));
-  if (p.window > 0) lo = max(lo, pos + 1 - p.window);
-  if (p.key_starts != nullptr) lo = max(lo, LDX(p.key_starts + tok));
-}
-
-// First query token and number of query tokens of sequence s; false where they do not fit
-// the arrays or the sequence.
-__device__ __forceinline__ bool query_range(const QueryAttnParams& p, int s, int& q0, int& n, int& len) {
-  q0 = LDX(p.starts + s);
-  const int q1 = LDX(p.starts + s + 1);
-  len = LDX(p.a.seq_lens + s);
-  n = 0;
-  if (q0 < 0 || q1 < q0 || q1 > p.num_tokens || q1 - q0 > p.max_q || len < 0 || len > p.a.seq_cap || q1 - q0 > len)
-    return false;
-  n = q1 - q0;
-  return true;
-}
 
 // Logits of a tile's scores: sc[nh][e] belongs to row 8 nh + 2c + (e & 1) and token
 // t0 + g + 8 (e >> 1).
@@ -415,6 +385,13 @@ cudaError_t launch_query_merge(const QueryAttnParams& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, query_merge_kernel<D>, p);
 }
 
+template <int D>
+cudaError_t merge_launch(const QueryAttnParams& p, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  KVQ_LAUNCH("query_merge_kernel", s, e = launch_query_merge<D>(p, s));
+  return e;
+}
+
 template <int D, int kFK, int kFV, int kNH>
 cudaError_t rows_launch(const QueryAttnParams& p, cudaStream_t s) {
   using T = AttnTile<D, kFK, kFV>;
@@ -428,8 +405,7 @@ cudaError_t rows_launch(const QueryAttnParams& p, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(tiles * p.a.nsplit), p.a.H, p.a.S);
   KVQ_LAUNCH("query_rows_kernel", s, k<<<grid, kAttnThreads, T::kSmem, s>>>(p); e = cudaGetLastError());
   if (e != cudaSuccess || p.a.nsplit == 1) return e;
-  KVQ_LAUNCH("query_merge_kernel", s, e = launch_query_merge<D>(p, s));
-  return e;
+  return merge_launch<D>(p, s);
 }
 
 template <int D, int kNH>
@@ -446,12 +422,39 @@ cudaError_t rows_dispatch(const QueryAttnParams& p, int rows, cudaStream_t s) {
   return rows <= 8 ? rows_dispatch_fmt<D, 1>(p, s) : rows_dispatch_fmt<D, 2>(p, s);
 }
 
-// Splits of the rows kernel, from upper bounds that hold for every call of these sizes.
-int rows_splits(int32_t S, int32_t H, int32_t max_q, int32_t group, int32_t max_len) {
+// Which kernel serves a call, and its split count, from sizes alone (the workspace query
+// sees the same ones).  The tile kernel from kTileFrom rows a sequence and KV head on.
+constexpr int kTileFrom = 65;
+
+struct QueryPlan {
+  bool tiles;
+  int nsplit;
+};
+
+QueryPlan query_plan(int32_t S, int32_t H, int32_t D, int32_t max_q, int32_t group, int32_t max_len) {
   const int64_t rows = static_cast<int64_t>(max_q) * group;
-  const int64_t tiles = rows <= 8 ? 1 : (rows + 15) / 16;
-  const int64_t ctas = static_cast<int64_t>(S) * tiles;
-  return ctas > (1 << 24) ? 1 : attn_num_splits(static_cast<int32_t>(ctas), H, max_len);
+  if (rows < kTileFrom) {
+    const int64_t tiles = rows <= 8 ? 1 : (rows + 15) / 16;
+    return QueryPlan{false, attn_num_splits(static_cast<int32_t>(S * tiles), H, max_len)};
+  }
+  // one CTA an SM: the split count whose last wave is fullest, at least 512 tokens a split,
+  // at most two waves
+  const int64_t ctas = static_cast<int64_t>(S) * H * ((rows + query_tile_rows(D) - 1) / query_tile_rows(D));
+  const int64_t slots = num_sms();
+  int64_t cap = (max_len + 511) / 512;
+  if (2 * slots / ctas < cap) cap = 2 * slots / ctas;
+  if (cap > 64) cap = 64;
+  int best = 1;
+  double best_fill = 0.0;
+  for (int64_t n = 1; n <= cap; ++n) {
+    const int64_t waves = (ctas * n + slots - 1) / slots;
+    const double fill = static_cast<double>(ctas * n) / static_cast<double>(waves * slots);
+    if (fill > best_fill + 0.01) {
+      best_fill = fill;
+      best = static_cast<int>(n);
+    }
+  }
+  return QueryPlan{true, best};
 }
 
 }  // namespace
@@ -460,7 +463,7 @@ size_t query_attn_workspace_bytes(int32_t S, int32_t num_tokens, int32_t H, int3
                                   int32_t max_len) {
   if (S <= 0 || num_tokens <= 0 || H <= 0 || Hq < H || D <= 0 || max_q <= 0 || max_len <= 0) return 0;
   if (max_q > max_len) max_q = max_len;  // as the call does
-  const int n = rows_splits(S, H, max_q, Hq / H, max_len);
+  const int n = query_plan(S, H, D, max_q, Hq / H, max_len).nsplit;
   if (n <= 1) return 0;
   return static_cast<size_t>(num_tokens) * Hq * n * (D + 2) * sizeof(float);
 }
@@ -468,11 +471,22 @@ size_t query_attn_workspace_bytes(int32_t S, int32_t num_tokens, int32_t H, int3
 cudaError_t launch_query_attention(const QueryAttnParams& p_in, cudaStream_t s) {
   QueryAttnParams p = p_in;
   const int rows = p.max_q * p.a.group;
-  p.a.nsplit = rows_splits(p.a.S, p.a.H, p.max_q, p.a.group, p.a.max_len);
+  const QueryPlan plan = query_plan(p.a.S, p.a.H, p.a.D, p.max_q, p.a.group, p.a.max_len);
+  p.a.nsplit = plan.nsplit;
+  if (!plan.tiles) {
+    switch (p.a.D) {
+      case 64: return rows_dispatch<64>(p, rows, s);
+      case 128: return rows_dispatch<128>(p, rows, s);
+      case 256: return rows_dispatch<256>(p, rows, s);
+    }
+    return cudaErrorInvalidValue;
+  }
+  const cudaError_t e = launch_query_tiles(p, s);
+  if (e != cudaSuccess || p.a.nsplit == 1) return e;
   switch (p.a.D) {
-    case 64: return rows_dispatch<64>(p, rows, s);
-    case 128: return rows_dispatch<128>(p, rows, s);
-    case 256: return rows_dispatch<256>(p, rows, s);
+    case 64: return merge_launch<64>(p, s);
+    case 128: return merge_launch<128>(p, s);
+    case 256: return merge_launch<256>(p, s);
   }
   return cudaErrorInvalidValue;
 }

@@ -1,0 +1,734 @@
+// query_tile_kernels.cu -- paged attention of many query rows per KV head on tcgen05.
+//
+// The mathematics and the row layout are those of query_attn_kernels.cu.  A CTA takes kNT
+// tiles of 128 rows (row = query token * group + query head of the group) of one KV head
+// and walks the keys that any of its rows sees, kBN tokens at a time:
+//   S = Q K^T   tcgen05.mma kind::f16, f16 operands in shared memory, S in tensor memory;
+//   P'          softmax warps, one thread a row: p = 2^(y - M) from the logits y, their sum
+//               l, P' = p * (V's scale) as f16 over S's columns of tensor memory;
+//   O += P' V   P' from tensor memory, V from shared memory, O in tensor memory.
+// K and V enter as the f16 values of their codes (exact: E4M3, or E2M1 times its E4M3 block
+// scale); K's FP32 scale multiplies the score, V's the probability, so codes are converted
+// once for kNT * 128 rows.  The reference M covers logit and V's scale together: it moves,
+// and O and l are rescaled, only when a tile's largest logit plus log2 of its largest V
+// scale exceeds M by 8, so P' stays below 2^8 and most tiles leave O alone.
+//
+// Warps: 4 kNT softmax warps; 4 producer warps, which gather the tile's rows through the
+// block table (any block size), convert them and store them in the 128-byte-swizzled
+// layout the matrix unit reads (K with the head dimension contiguous, V the same rows read
+// "MN-major"); one warp that issues the products.  Loads of the next tile are in flight in
+// registers while the current one is converted.  The tiles of a CTA take turns on the
+// tensor cores, so one's softmax runs while the other's products do.
+#include "query_attn.cuh"
+
+namespace kvq {
+
+namespace {
+
+// ---- tcgen05 / tensor memory -------------------------------------------------------
+__device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Arrives on the mbarrier once all products issued so far by this thread are complete.
+__device__ __forceinline__ void tc_commit(uint32_t mbar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mbar) : "memory");
+}
+// D (tensor memory) (+)= A B: both from shared memory, or A from tensor memory.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      : "memory");
+}
+// 32 columns of this warp's 32 lanes, one lane a row; the wait is part of the load.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
+      "%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
+      "%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Shared-memory operand descriptor, 128-byte swizzle: rows of 128 bytes in groups of 8
+// (1024 bytes apart); `lbo` is the distance of the next 64 elements along the contiguous
+// axis where that axis is M or N.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
+         (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t dup_f32x2(float x) { return pack_f32x2(__float_as_uint(x), __float_as_uint(x)); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// ---- shapes ------------------------------------------------------------------------
+template <int D>
+struct QTile {
+  static constexpr int kBN = D == 256 ? 64 : 128;       // tokens per step
+  static constexpr int kNT = D == 256 ? 1 : 2;          // 128-row tiles per CTA (tensor memory: 512 columns)
+  static constexpr int kStages = D == 64 ? 4 : 2;
+  static constexpr int kRows = 128 * kNT;
+  static constexpr int kSoft = 4 * kNT;                 // softmax warps
+  static constexpr int kWarps = kSoft + 4 + 1;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kQBytes = 128 * D * 2;           // per row tile
+  static constexpr int kKVBytes = kBN * D * 2;          // per stage and tensor
+  // scale slots: a step's are written a step ahead of its K, while the softmax warps may
+  // still read those of kStages steps before
+  static constexpr int kScaleSlots = kStages + 2;
+  static constexpr int kOffK = kNT * kQBytes;
+  static constexpr int kOffV = kOffK + kStages * kKVBytes;
+  static constexpr int kOffKS = kOffV + kStages * kKVBytes;        // [slots][kBN] K scales
+  static constexpr int kOffVS = kOffKS + kScaleSlots * kBN * 4;    // [slots][kBN] V scales
+  static constexpr int kOffVM = kOffVS + kScaleSlots * kBN * 4;    // [slots][4] their maxima per producer warp
+  static constexpr int kOffRow = kOffVM + kScaleSlots * 4 * 4;     // [2][kBN] pool rows (int64)
+  static constexpr int kOffBar = kOffRow + 2 * kBN * 8;
+  static constexpr int kNumBars = 4 * kStages + kScaleSlots + 3 * kNT;
+  static constexpr int kOffMisc = kOffBar + 8 * kNumBars;          // tensor memory address, key range, flags
+  static constexpr int kSmem = kOffMisc + 32 + 1024;               // + alignment of the base
+  static_assert(kSmem > 114 * 1024 && kSmem <= 227 * 1024, "one block per SM, since each takes all of tensor memory");
+  // tensor-memory columns
+  static constexpr int kColS = 0;                        // kNT x kBN
+  static constexpr int kColO = 256;                      // kNT x D
+};
+
+struct TileMisc {
+  uint32_t tmem;
+  int lo, hi;   // keys that any row sees
+  int bad;      // a block entry outside the pool
+  int give_up;  // a wait ran out
+};
+
+// A wait that gives up (after about 0.1 s, or soon after another one did).
+__device__ __forceinline__ void tile_wait(uint32_t bar, uint32_t parity, volatile TileMisc* misc, uint32_t* status) {
+  for (int n = 0; n < kMbarTries; ++n) {
+    if (mbar_try_wait(bar, parity)) return;
+    if ((n & 15) == 15 && misc->give_up != 0) return;
+  }
+  misc->give_up = 1;
+  set_status(status, 16u);
+}
+
+// ---- logits ------------------------------------------------------------------------
+enum LogitMode : int { kPlain = 0, kCapped = 1, kBiased = 2 };
+
+struct RowLogit {
+  float f;       // query factor times log2 e (plain, biased without cap)
+  float fz;      // capped: 2 log2 e / softcap times the query factor
+  float c2;      // capped: softcap log2 e
+  bool cap;
+  float slope;   // times log2 e
+  int pos;
+  int lo, hi;
+};
+
+// Base-2 logit of a scaled score x = s * ks at column col of a tile that starts at t0 (tf =
+// t0 - pos as a float).
+template <int kMode>
+__device__ __forceinline__ float logit(const RowLogit& r, float x, float tf, int col) {
+  float y;
+  if (kMode == kCapped || (kMode == kBiased && r.cap)) {
+    y = __fmaf_rn(-2.0f * r.c2, rcp_approx(1.0f + ex2(x * r.fz)), r.c2);
+  } else {
+    y = x * r.f;
+  }
+  if (kMode == kBiased) y = __fmaf_rn(r.slope, tf + static_cast<float>(col), y);
+  return y;
+}
+
+// Largest logit of a tile's row (-inf where it sees no key of the tile).
+template <int kMode, bool kMask, int kBN>
+__device__ __forceinline__ float tile_max(const RowLogit& r, uint32_t taddr, const float* ks, int t0) {
+  const int lo = r.lo - t0, hi = r.hi - t0;
+  const float tf = static_cast<float>(t0 - r.pos);
+  float m0 = kNegInf, m1 = kNegInf;
+#pragma unroll 1
+  for (int c0 = 0; c0 < kBN; c0 += 32) {
+    uint32_t v[32];
+    tmem_ld32(taddr + c0, v);
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(ks + c0 + i);
+      uint32_t x0, x1, x2, x3;
+      unpack_f32x2(mul_f32x2(pack_f32x2(v[i], v[i + 1]), k4.x), x0, x1);
+      unpack_f32x2(mul_f32x2(pack_f32x2(v[i + 2], v[i + 3]), k4.y), x2, x3);
+      float y[4] = {__uint_as_float(x0), __uint_as_float(x1), __uint_as_float(x2), __uint_as_float(x3)};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (kMode == kBiased) y[e] = logit<kMode>(r, y[e], tf, c0 + i + e);
+        if (kMask) y[e] = c0 + i + e >= lo && c0 + i + e < hi ? y[e] : kNegInf;
+      }
+      m0 = max3(m0, y[0], y[1]);
+      m1 = max3(m1, y[2], y[3]);
+    }
+  }
+  const float m = fmaxf(m0, m1);
+  // without a bias the logit grows with the score, so it is taken once
+  if (kMode == kBiased || (kMask && m == kNegInf)) return m;
+  return logit<kMode>(r, m, 0.0f, 0);
+}
+
+// P' of a tile's row over the first half of its score columns; returns the row sum of p.
+template <int kMode, bool kMask, int kBN>
+__device__ __forceinline__ float tile_probs(const RowLogit& r, uint32_t taddr, const float* ks, const float* vs, int t0,
+                                            float M) {
+  const int lo = r.lo - t0, hi = r.hi - t0;
+  const float tf = static_cast<float>(t0 - r.pos);
+  const uint64_t f2 = dup_f32x2(r.f), nM = dup_f32x2(-M);
+  uint64_t l0 = 0, l1 = 0;  // two pairs of partial sums
+#pragma unroll 1
+  for (int c0 = 0; c0 < kBN; c0 += 32) {
+    uint32_t v[32], h[16];
+    tmem_ld32(taddr + c0, v);
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(ks + c0 + i);
+      const ulonglong2 v4 = *reinterpret_cast<const ulonglong2*>(vs + c0 + i);
+      uint64_t xa = mul_f32x2(pack_f32x2(v[i], v[i + 1]), k4.x);
+      uint64_t xb = mul_f32x2(pack_f32x2(v[i + 2], v[i + 3]), k4.y);
+      if (kMode == kPlain) {
+        xa = fma_f32x2(xa, f2, nM);
+        xb = fma_f32x2(xb, f2, nM);
+      }
+      uint32_t x[4];
+      unpack_f32x2(xa, x[0], x[1]);
+      unpack_f32x2(xb, x[2], x[3]);
+      float p[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float y = __uint_as_float(x[e]);
+        if (kMode != kPlain) y = logit<kMode>(r, y, tf, c0 + i + e) - M;
+        if (kMask) y = c0 + i + e >= lo && c0 + i + e < hi ? y : kNegInf;
+        p[e] = ex2_ftz(y);
+      }
+      const uint64_t pa = pack_f32x2(__float_as_uint(p[0]), __float_as_uint(p[1]));
+      const uint64_t pb = pack_f32x2(__float_as_uint(p[2]), __float_as_uint(p[3]));
+      l0 = add_f32x2(l0, pa);
+      l1 = add_f32x2(l1, pb);
+      uint32_t q[4];
+      unpack_f32x2(mul_f32x2(pa, v4.x), q[0], q[1]);
+      unpack_f32x2(mul_f32x2(pb, v4.y), q[2], q[3]);
+      // one rounding of P' to f16: relative 2^-11 of the largest |v| the row attends to
+      h[i / 2] = f32x2_to_f16x2(__uint_as_float(q[0]), __uint_as_float(q[1]));
+      h[i / 2 + 1] = f32x2_to_f16x2(__uint_as_float(q[2]), __uint_as_float(q[3]));
+    }
+    tmem_st16(taddr + c0 / 2, h);  // columns whose scores are already read
+  }
+  uint32_t a, b, c, d;
+  unpack_f32x2(l0, a, b);
+  unpack_f32x2(l1, c, d);
+  return (__uint_as_float(a) + __uint_as_float(b)) + (__uint_as_float(c) + __uint_as_float(d));
+}
+
+template <int kMode, int kBN>
+__device__ __forceinline__ float tile_max_any(bool mask, const RowLogit& r, uint32_t ta, const float* ks, int t0) {
+  return mask ? tile_max<kMode, true, kBN>(r, ta, ks, t0) : tile_max<kMode, false, kBN>(r, ta, ks, t0);
+}
+template <int kMode, int kBN>
+__device__ __forceinline__ float tile_probs_any(bool mask, const RowLogit& r, uint32_t ta, const float* ks, const float* vs,
+                                                int t0, float M) {
+  return mask ? tile_probs<kMode, true, kBN>(r, ta, ks, vs, t0, M) : tile_probs<kMode, false, kBN>(r, ta, ks, vs, t0, M);
+}
+
+// ---- producers: one tensor's rows of a step ------------------------------------------
+// 128 threads; thread i takes 16-byte pieces of the code rows, kPer pieces of kPieces a row.
+template <int D, int kFmt>
+struct TileLoad {
+  static constexpr int kBN = QTile<D>::kBN;
+  static constexpr int kCB = kFmt == 3 ? D : D / 2;     // code bytes per row
+  static constexpr int kPieces = kCB / 16;              // per row
+  static constexpr int kPer = kBN * kPieces / 128;      // per thread
+  uint32_t w[kPer][4];
+  uint32_t bs[kFmt == 3 ? 1 : kPer];                    // NVFP4: the piece's two block scales
+
+  __device__ __forceinline__ void load(const AttnPlane& pl, const int64_t* rows, int tid) {
+    const int c = tid % kPieces;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int64_t row = rows[(i * 128 + tid) / kPieces];
+      w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;
+      if constexpr (kFmt != 3) bs[i] = 0u;
+      if (row >= 0) {
+        load16B(pl.codes + row * kCB + 16 * c, w[i]);
+        if constexpr (kFmt != 3) bs[i] = LDX(reinterpret_cast<const uint16_t*>(pl.bscale + row * (D / 16) + 2 * c));
+      }
+    }
+  }
+  // f16 values into the swizzled tile at shared address dst: panels of 64 dims, [kBN][128 B]
+  __device__ __forceinline__ void store(uint32_t dst, int tid) const {
+    const int c = tid % kPieces;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int r = (i * 128 + tid) / kPieces;
+      if constexpr (kFmt == 3) {  // 16 dims: two 16-byte chunks
+        uint32_t h[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t h2[2];
+          e4m3x4_to_f16x2(w[i][j], h2);
+          h[2 * j] = h2[0];
+          h[2 * j + 1] = h2[1];
+        }
+        const uint32_t base = dst + (c / 4) * (kBN * 128) + r * 128;
+        const uint32_t ch = 2 * (c % 4);
+        // odd panels store their second chunk first: eight lanes then cover all banks
+        const bool sw = (c / 4) & 1;
+        const uint32_t a0 = base + (((ch + (sw ? 1 : 0)) ^ (r & 7)) * 16), a1 = base + (((ch + (sw ? 0 : 1)) ^ (r & 7)) * 16);
+        sts16(a0, sw ? h[4] : h[0], sw ? h[5] : h[1], sw ? h[6] : h[2], sw ? h[7] : h[3]);
+        sts16(a1, sw ? h[0] : h[4], sw ? h[1] : h[5], sw ? h[2] : h[6], sw ? h[3] : h[7]);
+      } else {  // 32 dims: four chunks, two block scales
+        const uint32_t two = e4m3x2_to_f16x2(bs[i]);
+        const uint32_t s0 = __byte_perm(two, 0u, 0x1010), s1 = __byte_perm(two, 0u, 0x3232);
+        const uint32_t base = dst + (c / 2) * (kBN * 128) + r * 128;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t h[4];
+          e2m1x8_to_f16x2(w[i][j], h);
+          const uint32_t s = j < 2 ? s0 : s1;
+          sts16(base + (((4 * (c % 2) + j) ^ (r & 7)) * 16), hmul2(h[0], s), hmul2(h[1], s), hmul2(h[2], s), hmul2(h[3], s));
+        }
+      }
+    }
+  }
+};
+
+template <int D, int kFK, int kFV>
+__global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const QueryAttnParams qp) {
+  using T = QTile<D>;
+  constexpr int kBN = T::kBN, kNT = T::kNT, kStages = T::kStages;
+  const AttnParams& p = qp.a;
+  extern __shared__ unsigned char tile_smem_raw[];
+  const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(tile_smem_raw));
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  unsigned char* const smem = tile_smem_raw + (sbase - raw);
+  TileMisc* const misc = reinterpret_cast<TileMisc*>(smem + T::kOffMisc);
+
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int s = blockIdx.z, h = blockIdx.y;
+  // the last rows first: under a causal mask they see the most keys
+  const int ntiles = gridDim.x / p.nsplit;
+  const int ct = ntiles - 1 - static_cast<int>(blockIdx.x) / p.nsplit, split = blockIdx.x % p.nsplit;
+  const int row0 = ct * T::kRows;
+
+  int q0, nq, len;
+  const bool ok = query_range(qp, s, q0, nq, len);
+  if (!ok && threadIdx.x == 0 && blockIdx.x == 0 && h == 0) set_status(p.status, 8u);
+  const int rows = nq * p.group;
+  if (row0 >= rows) return;
+
+  const uint32_t bar0 = sbase + T::kOffBar;
+  const uint32_t k_full = bar0, k_empty = k_full + 8 * kStages, v_full = k_empty + 8 * kStages, v_empty = v_full + 8 * kStages;
+  const uint32_t sc_full = v_empty + 8 * kStages, s_full = sc_full + 8 * T::kScaleSlots;
+  const uint32_t p_ready = s_full + 8 * kNT, o_done = p_ready + 8 * kNT;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(k_full + 8 * i, 4);
+      mbar_init(k_empty + 8 * i, 1);
+      mbar_init(v_full + 8 * i, 4);
+      mbar_init(v_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < T::kScaleSlots; ++i) mbar_init(sc_full + 8 * i, 4);
+    for (int i = 0; i < kNT; ++i) {
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(p_ready + 8 * i, 4);
+      mbar_init(o_done + 8 * i, 1);
+    }
+    misc->lo = 0x7FFFFFFF;
+    misc->hi = 0;
+    misc->bad = 0;
+    misc->give_up = 0;
+    mbar_init_fence();
+  }
+  __syncthreads();
+  if (warp == T::kWarps - 1) {
+    tmem_alloc(sbase + T::kOffMisc, 512);
+    tmem_relinquish();
+  }
+
+  // ---- softmax threads: their row's keys, and Q as f16 (scaled by a power of two so that
+  // the row's largest element lies in [2^14, 2^15): exact) ----
+  RowLogit rl;
+  int row = -1;  // the thread's row within the sequence; -1: none
+  bool sees = false;
+  if (warp < T::kSoft) {
+    const int r = threadIdx.x;  // row of the CTA
+    if (row0 + r < rows) row = row0 + r;
+    rl.lo = 0;
+    rl.hi = 0x7FFFFFFF;  // a thread without a row masks nothing
+    rl.pos = 0;
+    rl.slope = 0.0f;
+    float fac = 0.0f;
+    const uint32_t qs = sbase + (r / 128) * T::kQBytes + (r % 128) * 128;
+    if (row >= 0) {
+      const int i = row / p.group, head = h * p.group + row - i * p.group;
+      rl.pos = len - nq + i;
+      int lo, hi;
+      key_range(qp, s, q0 + i, rl.pos, len, lo, hi);
+      sees = lo < hi;
+      if (sees) {
+        rl.lo = lo;
+        rl.hi = hi;
+      }
+      if (qp.slopes != nullptr) rl.slope = LDX(qp.slopes + head) * kLog2e;
+      const uint16_t* const q = p.q + static_cast<int64_t>(q0 + i) * p.q_row_pitch + static_cast<int64_t>(head) * p.q_head_pitch;
+      float am = 0.0f;
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) {
+        uint32_t w[4];
+        load16B(q + 8 * c, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) am = max3(am, fabsf(bf16lo(w[j])), fabsf(bf16hi(w[j])));
+      }
+      int k = 0;
+      if (am > 0.0f) k = 14 - (static_cast<int>((__float_as_uint(am) >> 23) & 0xFF) - 127);
+      k = max(-100, min(120, k));
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+      fac = p.scale * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) {
+        uint32_t w[4];
+        load16B(q + 8 * c, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = f32x2_to_f16x2(bf16lo(w[j]) * up, bf16hi(w[j]) * up);
+        sts16(qs + (c / 8) * (128 * 128) + (((c % 8) ^ (r & 7)) * 16), w[0], w[1], w[2], w[3]);
+      }
+    } else {
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) sts16(qs + (c / 8) * (128 * 128) + (((c % 8) ^ (r & 7)) * 16), 0u, 0u, 0u, 0u);
+    }
+    rl.f = fac * kLog2e;
+    rl.cap = qp.softcap > 0.0f;
+    rl.c2 = qp.softcap * kLog2e;
+    rl.fz = rl.cap ? 2.0f * kLog2e / qp.softcap * fac : 0.0f;
+    const int lo = __reduce_min_sync(0xFFFFFFFFu, sees ? rl.lo : 0x7FFFFFFF);
+    const int hi = __reduce_max_sync(0xFFFFFFFFu, sees ? rl.hi : 0);
+    if (lane == 0) {
+      atomicMin(&misc->lo, lo);
+      atomicMax(&misc->hi, hi);
+    }
+    fence_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc->tmem;
+  const int key_lo = misc->lo, key_hi = misc->hi;
+  int t_begin = 0, t_end = 0;
+  if (key_lo < key_hi) {  // equal splits in whole steps
+    const int per = ((key_hi - key_lo + p.nsplit - 1) / p.nsplit + kBN - 1) / kBN * kBN;
+    t_begin = static_cast<int>(min(static_cast<int64_t>(key_lo) + static_cast<int64_t>(split) * per, static_cast<int64_t>(key_hi)));
+    t_end = min(t_begin + per, key_hi);
+  }
+  const int steps = (t_end - t_begin + kBN - 1) / kBN;
+
+  if (warp == T::kWarps - 1) {
+    // ---- the issuing thread ----
+    if (lane == 0 && steps > 0) {
+      constexpr uint32_t kBase = (1u << 4) | (8u << 24);  // f16 x f16 -> f32, M = 128
+      constexpr uint32_t kIdS = kBase | (static_cast<uint32_t>(kBN / 8) << 17);
+      constexpr uint32_t kIdO = kBase | (1u << 16) | (static_cast<uint32_t>(D / 8) << 17);  // B is MN-major
+      auto scores = [&](int i, int j) {
+        const uint32_t qa = sbase + i * T::kQBytes, ka = sbase + T::kOffK + (j % kStages) * T::kKVBytes;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tc_mma_ss(tmem + T::kColS + i * kBN, smem_desc(qa + (k / 4) * (128 * 128) + (k % 4) * 32, 16),
+                    smem_desc(ka + (k / 4) * (kBN * 128) + (k % 4) * 32, 16), kIdS, k > 0);
+        tc_commit(s_full + 8 * i);
+        if (i == kNT - 1) tc_commit(k_empty + 8 * (j % kStages));
+      };
+      tile_wait(k_full, 0, misc, p.status);
+      tc_fence_after();
+      for (int i = 0; i < kNT; ++i) scores(i, 0);
+      for (int j = 0; j < steps; ++j) {
+        const int st = j % kStages;
+        for (int i = 0; i < kNT; ++i) {
+          tile_wait(p_ready + 8 * i, j & 1, misc, p.status);
+          if (i == 0) tile_wait(v_full + 8 * st, (j / kStages) & 1, misc, p.status);
+          tc_fence_after();
+          const uint32_t va = sbase + T::kOffV + st * T::kKVBytes;
+#pragma unroll
+          for (int k = 0; k < kBN / 16; ++k)
+            tc_mma_ts(tmem + T::kColO + i * D, tmem + T::kColS + i * kBN + 8 * k, smem_desc(va + k * 2048, kBN * 128), kIdO,
+                      j > 0 || k > 0);
+          if (i == kNT - 1) tc_commit(v_empty + 8 * st);
+          if (j + 1 < steps) {
+            if (i == 0) {
+              tile_wait(k_full + 8 * ((j + 1) % kStages), ((j + 1) / kStages) & 1, misc, p.status);
+              tc_fence_after();
+            }
+            scores(i, j + 1);
+          } else {
+            tc_commit(o_done + 8 * i);
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= T::kSoft) {
+    // ---- producers ----
+    const int tid = threadIdx.x - 32 * T::kSoft;
+    const int pw = tid >> 5;
+    int64_t* const rowbuf = reinterpret_cast<int64_t*>(smem + T::kOffRow);
+    float* const ksb = reinterpret_cast<float*>(smem + T::kOffKS);
+    float* const vsb = reinterpret_cast<float*>(smem + T::kOffVS);
+    float* const vmb = reinterpret_cast<float*>(smem + T::kOffVM);
+    // pool rows and scales of step j, one token a thread
+    auto resolve = [&](int j) {
+      if (j < steps) {
+        float ks = 0.0f, vs = 0.0f;
+        if (tid < kBN) {
+          const int t = t_begin + j * kBN + tid;
+          int64_t r = -1;
+          if (t < t_end) {
+            uint32_t bi, bo;
+            p.div_bs.divmod(static_cast<uint32_t>(t), bi, bo);
+            const int64_t blk = LDX(p.block_table + static_cast<int64_t>(s) * p.max_blocks + bi);
+            if (blk < 0 || blk >= p.num_blocks) {
+              misc->bad = 1;
+            } else {
+              r = (blk * p.block_size + bo) * p.H + h;
+              ks = LDX(p.k.rscale + (p.k_page ? blk * p.H + h : r));
+              vs = LDX(p.v.rscale + (p.v_page ? blk * p.H + h : r));
+            }
+          }
+          rowbuf[(j & 1) * kBN + tid] = r;
+          ksb[(j % T::kScaleSlots) * kBN + tid] = ks;
+          vsb[(j % T::kScaleSlots) * kBN + tid] = vs;
+        }
+        const float m = group_max<32>(vs);
+        if (lane == 0) vmb[(j % T::kScaleSlots) * 4 + pw] = m;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sc_full + 8 * (j % T::kScaleSlots));
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+    };
+    TileLoad<D, kFK> lk;
+    TileLoad<D, kFV> lv;
+    if (steps > 0) {
+      resolve(0);
+      lk.load(p.k, rowbuf, tid);
+      lv.load(p.v, rowbuf, tid);
+    }
+    for (int j = 0; j < steps; ++j) {
+      const int st = j % kStages;
+      const int64_t* const next = rowbuf + ((j + 1) & 1) * kBN;
+      resolve(j + 1);
+      if (j >= kStages) tile_wait(k_empty + 8 * st, ((j / kStages) - 1) & 1, misc, p.status);
+      lk.store(sbase + T::kOffK + st * T::kKVBytes, tid);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(k_full + 8 * st);
+      if (j + 1 < steps) lk.load(p.k, next, tid);
+      if (j >= kStages) tile_wait(v_empty + 8 * st, ((j / kStages) - 1) & 1, misc, p.status);
+      lv.store(sbase + T::kOffV + st * T::kKVBytes, tid);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(v_full + 8 * st);
+      if (j + 1 < steps) lv.load(p.v, next, tid);
+    }
+  } else {
+    // ---- softmax: one thread a row ----
+    const int i = warp / 4;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + T::kColS + i * kBN, to = tmem + lanes + T::kColO + i * D;
+    const int mode = qp.slopes != nullptr ? kBiased : rl.cap ? kCapped : kPlain;
+    float M = kNoKey, L = 0.0f;
+    for (int j = 0; j < steps; ++j) {
+      const int slot = j % T::kScaleSlots;
+      const int t0 = t_begin + j * kBN;
+      tile_wait(sc_full + 8 * slot, (j / T::kScaleSlots) & 1, misc, p.status);
+      tile_wait(s_full + 8 * i, j & 1, misc, p.status);
+      tc_fence_after();
+      __syncwarp();
+      const float* const ks = reinterpret_cast<const float*>(smem + T::kOffKS) + slot * kBN;
+      const float* const vs = reinterpret_cast<const float*>(smem + T::kOffVS) + slot * kBN;
+      const float4 vm = *reinterpret_cast<const float4*>(smem + T::kOffVM + 16 * slot);
+      const bool mask = __any_sync(0xFFFFFFFFu, rl.lo > t0 || rl.hi < t0 + kBN);
+      const bool none = __all_sync(0xFFFFFFFFu, rl.lo >= t0 + kBN || rl.hi <= t0 || row < 0 || !sees);
+      if (none) {  // no row of the warp sees a key of this step
+        uint32_t z[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) z[e] = 0u;
+#pragma unroll
+        for (int c = 0; c < kBN / 2; c += 16) tmem_st16(ts + c, z);
+      } else {
+        float mx;
+        if (mode == kPlain) mx = tile_max_any<kPlain, kBN>(mask, rl, ts, ks, t0);
+        else if (mode == kCapped) mx = tile_max_any<kCapped, kBN>(mask, rl, ts, ks, t0);
+        else mx = tile_max_any<kBiased, kBN>(mask, rl, ts, ks, t0);
+        // V's scales enter P', so the reference covers them (their range is clamped far
+        // outside what rows of ordinary size need)
+        const float lv = fminf(fmaxf(lg2(max3(fmaxf(vm.x, vm.y), vm.z, vm.w)), -100.0f), 100.0f);
+        const bool move = mx + lv > M + 8.0f;
+        if (__any_sync(0xFFFFFFFFu, move)) {
+          const float Mn = move ? mx + lv : M;
+          const float a = ex2(M - Mn);
+          M = Mn;
+          L *= a;
+          if (j > 0) {  // the products of the steps before are complete: s_full came after them
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(to + c, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+              tmem_st32(to + c, o);
+            }
+          }
+        }
+        if (mode == kPlain) L += tile_probs_any<kPlain, kBN>(mask, rl, ts, ks, vs, t0, M);
+        else if (mode == kCapped) L += tile_probs_any<kCapped, kBN>(mask, rl, ts, ks, vs, t0, M);
+        else L += tile_probs_any<kBiased, kBN>(mask, rl, ts, ks, vs, t0, M);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_ready + 8 * i);
+    }
+    if (steps > 0) {
+      tile_wait(o_done + 8 * i, 0, misc, p.status);
+      tc_fence_after();
+      __syncwarp();
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const bool bad = *reinterpret_cast<volatile int*>(&misc->bad) != 0;
+    if (!sees) L = 0.0f;
+    const int qi = row >= 0 ? row / p.group : 0;
+    const int head = h * p.group + (row >= 0 ? row - qi * p.group : 0);
+    const int64_t tok = q0 + qi;
+    uint16_t* const out = p.out + tok * p.o_row_pitch + static_cast<int64_t>(head) * p.o_head_pitch;
+    float* const wsr = p.ws + ((tok * p.Hq + head) * p.nsplit + split) * (D + 2);
+    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      uint32_t o[32];
+      __syncwarp();
+      if (steps > 0) {
+        tmem_ld32(to + c, o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0u;
+      }
+      if (row < 0) continue;
+      if (p.nsplit == 1) {
+        if (bad) continue;
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            w[b] = L > 0.0f ? pack_bf16x2(__uint_as_float(o[e + 2 * b]) * inv, __uint_as_float(o[e + 2 * b + 1]) * inv) : 0u;
+          store16B(out + c + e, w);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)  // (D + 2) * 4 bytes is a multiple of 8
+          STX(reinterpret_cast<float2*>(wsr + c + e),
+              sees ? make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])) : make_float2(0.0f, 0.0f));
+      }
+    }
+    if (row >= 0 && p.nsplit > 1)
+      STX(reinterpret_cast<float2*>(wsr + D), make_float2(sees ? M : kNoKey, bad ? __int_as_float(0x7FC00000) : L));
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == T::kWarps - 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && misc->bad != 0) set_status(p.status, 2u);
+}
+
+template <int D, int kFK, int kFV>
+cudaError_t tile_launch(const QueryAttnParams& p, cudaStream_t s) {
+  using T = QTile<D>;
+  auto k = query_tile_kernel<D, kFK, kFV>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (static_cast<int64_t>(p.max_q) * p.a.group + T::kRows - 1) / T::kRows;
+  const dim3 grid(static_cast<unsigned>(tiles * p.a.nsplit), p.a.H, p.a.S);
+  KVQ_LAUNCH("query_tile_kernel", s, k<<<grid, T::kThreads, T::kSmem, s>>>(p); e = cudaGetLastError());
+  return e;
+}
+
+template <int D>
+cudaError_t tile_dispatch(const QueryAttnParams& p, cudaStream_t s) {
+  const bool k8 = p.a.fmt_k == 3, v8 = p.a.fmt_v == 3;
+  if (!k8 && !v8) return tile_launch<D, 1, 1>(p, s);
+  if (k8 && !v8) return tile_launch<D, 3, 1>(p, s);
+  if (!k8 && v8) return tile_launch<D, 1, 3>(p, s);
+  return tile_launch<D, 3, 3>(p, s);
+}
+
+}  // namespace
+
+int query_tile_rows(int32_t D) { return D == 256 ? QTile<256>::kRows : QTile<128>::kRows; }
+
+cudaError_t launch_query_tiles(const QueryAttnParams& p, cudaStream_t s) {
+  switch (p.a.D) {
+    case 64: return tile_dispatch<64>(p, s);
+    case 128: return tile_dispatch<128>(p, s);
+    case 256: return tile_dispatch<256>(p, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace kvq
