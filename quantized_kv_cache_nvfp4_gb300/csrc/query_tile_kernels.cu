@@ -13,12 +13,12 @@
 // and O and l are rescaled, only when a tile's largest logit plus log2 of its largest V
 // scale exceeds M by 8, so P' stays below 2^8 and most tiles leave O alone.
 //
-// Warps: 4 kNT softmax warps; 4 producer warps, which gather the tile's rows through the
-// block table (any block size), convert them and store them in the 128-byte-swizzled
-// layout the matrix unit reads (K with the head dimension contiguous, V the same rows read
-// "MN-major"); one warp that issues the products.  Loads of the next tile are in flight in
-// registers while the current one is converted.  The tiles of a CTA take turns on the
-// tensor cores, so one's softmax runs while the other's products do.
+// Warps: 4 kNT softmax warps; one that looks the step's tokens up in the block table (any
+// block size) some steps ahead; 4 producer warps, which load the rows, convert them and
+// store them in the 128-byte-swizzled layout the matrix unit reads (K with the head
+// dimension contiguous, V the same rows read "MN-major"); one that issues the products.  Loads of the next step are in flight in registers while the current one is
+// converted.  The tiles of a CTA take turns on the tensor cores, so one's softmax runs
+// while the other's products do.
 #include "query_attn.cuh"
 
 namespace kvq {
@@ -94,9 +94,13 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 // Shared-memory operand descriptor, 128-byte swizzle: rows of 128 bytes in groups of 8
 // (1024 bytes apart); `lbo` is the distance of the next 64 elements along the contiguous
 // axis where that axis is M or N.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo) {
-  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
-         (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// Only the low word differs between operands, and a step along an operand adds to it.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+  return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+__device__ __forceinline__ uint64_t smem_desc(uint32_t lo, uint32_t step_bytes) {
+  constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+  return (static_cast<uint64_t>(hi) << 32) | (lo + (step_bytes >> 4));
 }
 
 __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
@@ -108,6 +112,11 @@ __device__ __forceinline__ uint64_t dup_f32x2(float x) { return pack_f32x2(__flo
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ float lg2(float x) {
@@ -127,21 +136,21 @@ struct QTile {
   static constexpr int kStages = D == 64 ? 4 : 2;
   static constexpr int kRows = 128 * kNT;
   static constexpr int kSoft = 4 * kNT;                 // softmax warps
-  static constexpr int kWarps = kSoft + 4 + 1;
+  static constexpr int kIssuer = kSoft + 4;             // the warp that issues the products
+  static constexpr int kResolver = kIssuer + 1;         // the warp that looks the tokens up
+  static constexpr int kWarps = kResolver + 1;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kQBytes = 128 * D * 2;           // per row tile
   static constexpr int kKVBytes = kBN * D * 2;          // per stage and tensor
-  // scale slots: a step's are written a step ahead of its K, while the softmax warps may
-  // still read those of kStages steps before
-  static constexpr int kScaleSlots = kStages + 2;
+  static constexpr int kSlots = 4;                      // steps whose rows and scales are held
   static constexpr int kOffK = kNT * kQBytes;
   static constexpr int kOffV = kOffK + kStages * kKVBytes;
   static constexpr int kOffKS = kOffV + kStages * kKVBytes;        // [slots][kBN] K scales
-  static constexpr int kOffVS = kOffKS + kScaleSlots * kBN * 4;    // [slots][kBN] V scales
-  static constexpr int kOffVM = kOffVS + kScaleSlots * kBN * 4;    // [slots][4] their maxima per producer warp
-  static constexpr int kOffRow = kOffVM + kScaleSlots * 4 * 4;     // [2][kBN] pool rows (int64)
-  static constexpr int kOffBar = kOffRow + 2 * kBN * 8;
-  static constexpr int kNumBars = 4 * kStages + kScaleSlots + 3 * kNT;
+  static constexpr int kOffVS = kOffKS + kSlots * kBN * 4;    // [slots][kBN] V scales
+  static constexpr int kOffVM = kOffVS + kSlots * kBN * 4;         // [slots] the largest V scale
+  static constexpr int kOffRow = kOffVM + 16 * kSlots;             // [slots][kBN] pool rows (int64)
+  static constexpr int kOffBar = kOffRow + kSlots * kBN * 8;
+  static constexpr int kNumBars = 4 * kStages + 2 * kSlots + 3 * kNT;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;          // tensor memory address, key range, flags
   static constexpr int kSmem = kOffMisc + 32 + 1024;               // + alignment of the base
   static_assert(kSmem > 114 * 1024 && kSmem <= 227 * 1024, "one block per SM, since each takes all of tensor memory");
@@ -186,7 +195,7 @@ template <int kMode>
 __device__ __forceinline__ float logit(const RowLogit& r, float x, float tf, int col) {
   float y;
   if (kMode == kCapped || (kMode == kBiased && r.cap)) {
-    y = __fmaf_rn(-2.0f * r.c2, rcp_approx(1.0f + ex2(x * r.fz)), r.c2);
+    y = __fmaf_rn(-2.0f * r.c2, rcp_ftz(1.0f + ex2_ftz(x * r.fz)), r.c2);
   } else {
     y = x * r.f;
   }
@@ -278,14 +287,118 @@ __device__ __forceinline__ float tile_probs(const RowLogit& r, uint32_t taddr, c
   return (__uint_as_float(a) + __uint_as_float(b)) + (__uint_as_float(c) + __uint_as_float(d));
 }
 
-template <int kMode, int kBN>
-__device__ __forceinline__ float tile_max_any(bool mask, const RowLogit& r, uint32_t ta, const float* ks, int t0) {
-  return mask ? tile_max<kMode, true, kBN>(r, ta, ks, t0) : tile_max<kMode, false, kBN>(r, ta, ks, t0);
+// The same where both planes are page-scaled and pages are whole groups of 16 columns: K's
+// scale and V's (as its log2) are one pair a group, gs[group] = {ks, log2 vs}.  The scale of
+// the scores is then part of the row's factor, and P' = 2^(y - M + log2 vs) needs no product;
+// the group's sum of P' is divided by vs for l.
+template <int kMode, bool kMask, int kBN>
+__device__ __forceinline__ float tile_max_pages(const RowLogit& r, uint32_t taddr, const float2* gs, int t0) {
+  const int lo = r.lo - t0, hi = r.hi - t0;
+  const float tf = static_cast<float>(t0 - r.pos);
+  float best = kNegInf;
+#pragma unroll 1
+  for (int c0 = 0; c0 < kBN; c0 += 32) {
+    uint32_t v[32];
+    tmem_ld32(taddr + c0, v);
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const float ks = gs[c0 / 16 + g].x;
+      float m[2] = {kNegInf, kNegInf};
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int col = c0 + 16 * g + i;
+        float x = __uint_as_float(v[16 * g + i]);
+        if (kMode == kBiased) x = logit<kMode>(r, x * ks, tf, col);
+        if (kMask) x = col >= lo && col < hi ? x : kNegInf;
+        m[i % 2] = fmaxf(m[i % 2], x);
+      }
+      const float mg = fmaxf(m[0], m[1]);
+      best = fmaxf(best, kMode == kBiased || (kMask && mg == kNegInf) ? mg : mg * ks);
+    }
+  }
+  if (kMode == kBiased || (kMask && best == kNegInf)) return best;
+  return logit<kMode>(r, best, 0.0f, 0);
 }
-template <int kMode, int kBN>
-__device__ __forceinline__ float tile_probs_any(bool mask, const RowLogit& r, uint32_t ta, const float* ks, const float* vs,
-                                                int t0, float M) {
-  return mask ? tile_probs<kMode, true, kBN>(r, ta, ks, vs, t0, M) : tile_probs<kMode, false, kBN>(r, ta, ks, vs, t0, M);
+
+template <int kMode, bool kMask, int kBN>
+__device__ __forceinline__ float tile_probs_pages(const RowLogit& r, uint32_t taddr, const float2* gs, int t0, float M) {
+  const int lo = r.lo - t0, hi = r.hi - t0;
+  const float tf = static_cast<float>(t0 - r.pos);
+  const uint64_t c2 = dup_f32x2(-2.0f * r.c2), one2 = dup_f32x2(1.0f);
+  float L = 0.0f;
+#pragma unroll 1
+  for (int c0 = 0; c0 < kBN; c0 += 32) {
+    uint32_t v[32], h[16];
+    tmem_ld32(taddr + c0, v);
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const float2 s = gs[c0 / 16 + g];
+      const float ref = s.y - M;
+      const uint64_t f2 = dup_f32x2((kMode == kPlain ? r.f : r.fz) * s.x);
+      const uint64_t add2 = dup_f32x2(kMode == kPlain ? ref : r.c2 + ref);
+      uint64_t l[2] = {0, 0};
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const int col = c0 + 16 * g + i;
+        const uint64_t x2 = pack_f32x2(v[16 * g + i], v[16 * g + i + 1]);
+        float y0, y1;
+        uint32_t a, b;
+        if (kMode == kBiased) {
+          y0 = logit<kMode>(r, __uint_as_float(v[16 * g + i]) * s.x, tf, col) + ref;
+          y1 = logit<kMode>(r, __uint_as_float(v[16 * g + i + 1]) * s.x, tf, col + 1) + ref;
+        } else {
+          uint64_t y2;
+          if (kMode == kPlain) {
+            y2 = fma_f32x2(x2, f2, add2);
+          } else {  // (c2 + ref) - 2 c2 / (1 + 2^(x fz ks))
+            uint32_t e0, e1;
+            unpack_f32x2(mul_f32x2(x2, f2), e0, e1);
+            unpack_f32x2(add_f32x2(pack_f32x2(__float_as_uint(ex2_ftz(__uint_as_float(e0))),
+                                              __float_as_uint(ex2_ftz(__uint_as_float(e1)))), one2), e0, e1);
+            y2 = fma_f32x2(pack_f32x2(__float_as_uint(rcp_ftz(__uint_as_float(e0))),
+                                      __float_as_uint(rcp_ftz(__uint_as_float(e1)))), c2, add2);
+          }
+          unpack_f32x2(y2, a, b);
+          y0 = __uint_as_float(a);
+          y1 = __uint_as_float(b);
+        }
+        if (kMask) {
+          y0 = col >= lo && col < hi ? y0 : kNegInf;
+          y1 = col + 1 >= lo && col + 1 < hi ? y1 : kNegInf;
+        }
+        const float p0 = ex2_ftz(y0), p1 = ex2_ftz(y1);
+        l[(i / 2) % 2] = add_f32x2(l[(i / 2) % 2], pack_f32x2(__float_as_uint(p0), __float_as_uint(p1)));
+        // one rounding of P' to f16: relative 2^-11 of the largest |v| the row attends to
+        h[8 * g + i / 2] = f32x2_to_f16x2(p0, p1);
+      }
+      uint32_t a, b;
+      unpack_f32x2(add_f32x2(l[0], l[1]), a, b);
+      L = __fmaf_rn(__uint_as_float(a) + __uint_as_float(b), ex2_ftz(-s.y), L);
+    }
+    tmem_st16(taddr + c0 / 2, h);  // columns whose scores are already read
+  }
+  return L;
+}
+
+// Where a step's scales are: K's and V's by token, or the groups' pairs.
+struct StepScales {
+  const float *ks, *vs;
+  const float2* gs;
+};
+
+template <int kMode, int kBN, bool kPages>
+__device__ __forceinline__ float tile_max_any(bool mask, const RowLogit& r, uint32_t ta, const StepScales& sc, int t0) {
+  if constexpr (kPages)
+    return mask ? tile_max_pages<kMode, true, kBN>(r, ta, sc.gs, t0) : tile_max_pages<kMode, false, kBN>(r, ta, sc.gs, t0);
+  else
+    return mask ? tile_max<kMode, true, kBN>(r, ta, sc.ks, t0) : tile_max<kMode, false, kBN>(r, ta, sc.ks, t0);
+}
+template <int kMode, int kBN, bool kPages>
+__device__ __forceinline__ float tile_probs_any(bool mask, const RowLogit& r, uint32_t ta, const StepScales& sc, int t0, float M) {
+  if constexpr (kPages)
+    return mask ? tile_probs_pages<kMode, true, kBN>(r, ta, sc.gs, t0, M) : tile_probs_pages<kMode, false, kBN>(r, ta, sc.gs, t0, M);
+  else
+    return mask ? tile_probs<kMode, true, kBN>(r, ta, sc.ks, sc.vs, t0, M) : tile_probs<kMode, false, kBN>(r, ta, sc.ks, sc.vs, t0, M);
 }
 
 // ---- producers: one tensor's rows of a step ------------------------------------------
@@ -350,7 +463,8 @@ struct TileLoad {
   }
 };
 
-template <int D, int kFK, int kFV>
+// kPages: both planes page-scaled, block_size a multiple of 16 (FP8 codes).
+template <int D, int kFK, int kFV, bool kPages>
 __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const QueryAttnParams qp) {
   using T = QTile<D>;
   constexpr int kBN = T::kBN, kNT = T::kNT, kStages = T::kStages;
@@ -376,7 +490,7 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
 
   const uint32_t bar0 = sbase + T::kOffBar;
   const uint32_t k_full = bar0, k_empty = k_full + 8 * kStages, v_full = k_empty + 8 * kStages, v_empty = v_full + 8 * kStages;
-  const uint32_t sc_full = v_empty + 8 * kStages, s_full = sc_full + 8 * T::kScaleSlots;
+  const uint32_t sc_full = v_empty + 8 * kStages, sc_empty = sc_full + 8 * T::kSlots, s_full = sc_empty + 8 * T::kSlots;
   const uint32_t p_ready = s_full + 8 * kNT, o_done = p_ready + 8 * kNT;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -385,7 +499,10 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
       mbar_init(v_full + 8 * i, 4);
       mbar_init(v_empty + 8 * i, 1);
     }
-    for (int i = 0; i < T::kScaleSlots; ++i) mbar_init(sc_full + 8 * i, 4);
+    for (int i = 0; i < T::kSlots; ++i) {
+      mbar_init(sc_full + 8 * i, 1);
+      mbar_init(sc_empty + 8 * i, 4 + T::kSoft);  // the producer and the softmax warps
+    }
     for (int i = 0; i < kNT; ++i) {
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_ready + 8 * i, 4);
@@ -398,7 +515,7 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
     mbar_init_fence();
   }
   __syncthreads();
-  if (warp == T::kWarps - 1) {
+  if (warp == T::kIssuer) {
     tmem_alloc(sbase + T::kOffMisc, 512);
     tmem_relinquish();
   }
@@ -473,24 +590,95 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
   const int key_lo = misc->lo, key_hi = misc->hi;
   int t_begin = 0, t_end = 0;
   if (key_lo < key_hi) {  // equal splits in whole steps
-    const int per = ((key_hi - key_lo + p.nsplit - 1) / p.nsplit + kBN - 1) / kBN * kBN;
-    t_begin = static_cast<int>(min(static_cast<int64_t>(key_lo) + static_cast<int64_t>(split) * per, static_cast<int64_t>(key_hi)));
+    const int first = kPages ? key_lo & ~15 : key_lo;  // groups of 16 columns lie in one page
+    const int per = ((key_hi - first + p.nsplit - 1) / p.nsplit + kBN - 1) / kBN * kBN;
+    t_begin = static_cast<int>(min(static_cast<int64_t>(first) + static_cast<int64_t>(split) * per, static_cast<int64_t>(key_hi)));
     t_end = min(t_begin + per, key_hi);
   }
   const int steps = (t_end - t_begin + kBN - 1) / kBN;
 
-  if (warp == T::kWarps - 1) {
+  if (warp == T::kResolver) {
+    // ---- pool rows and scales of each step's tokens, up to kSlots steps ahead ----
+    int64_t* const rowbuf = reinterpret_cast<int64_t*>(smem + T::kOffRow);
+    float* const ksb = reinterpret_cast<float*>(smem + T::kOffKS);
+    float* const vsb = reinterpret_cast<float*>(smem + T::kOffVS);
+    float2* const gsb = reinterpret_cast<float2*>(smem + T::kOffKS);  // [slots][groups], in K's place
+    float* const vmb = reinterpret_cast<float*>(smem + T::kOffVM);
+    constexpr int kPer = kBN / 32;  // tokens a lane
+    const int32_t* const table = p.block_table + static_cast<int64_t>(s) * p.max_blocks;
+    // a step's table entries are on their way two steps ahead of its scales' use, its
+    // scales one step ahead: the two dependent loads never wait for each other
+    int32_t blk[kPer];
+    int64_t row[kPer];
+    float ks[kPer], vs[kPer];
+    auto entries = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int t = t_begin + j * kBN + 32 * i + lane;
+        blk[i] = t < t_end ? LDX(table + p.div_bs.div(static_cast<uint32_t>(t))) : -1;
+      }
+    };
+    auto scales = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int t = t_begin + j * kBN + 32 * i + lane;
+        row[i] = -1;
+        ks[i] = vs[i] = 0.0f;
+        if (t >= t_end || t < key_lo) continue;
+        if (blk[i] < 0 || blk[i] >= p.num_blocks) {
+          misc->bad = 1;
+          continue;
+        }
+        uint32_t bi, bo;
+        p.div_bs.divmod(static_cast<uint32_t>(t), bi, bo);
+        const int64_t pg = static_cast<int64_t>(blk[i]);
+        row[i] = (pg * p.block_size + bo) * p.H + h;
+        ks[i] = LDX(p.k.rscale + (p.k_page ? pg * p.H + h : row[i]));
+        vs[i] = LDX(p.v.rscale + (p.v_page ? pg * p.H + h : row[i]));
+      }
+    };
+    entries(0);
+    scales(0);
+    entries(1);
+    for (int j = 0; j < steps; ++j) {
+      const int slot = j % T::kSlots;
+      if (j >= T::kSlots) tile_wait(sc_empty + 8 * slot, ((j / T::kSlots) - 1) & 1, misc, p.status);
+      float m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        rowbuf[slot * kBN + 32 * i + lane] = row[i];
+        if constexpr (kPages) {
+          // a group's scales are those of any of its tokens (the others hold the same, or 0
+          // outside the keys); a V scale of 0 becomes the least normal number, so that l
+          // counts the page's probabilities
+          const float kg = group_max<16>(ks[i]), vg = fmaxf(group_max<16>(vs[i]), 0x1p-126f);
+          if (lane % 16 == 0) gsb[slot * (kBN / 16) + 2 * i + lane / 16] = make_float2(kg, lg2(vg));
+        } else {
+          ksb[slot * kBN + 32 * i + lane] = ks[i];
+          vsb[slot * kBN + 32 * i + lane] = vs[i];
+        }
+        m = fmaxf(m, vs[i]);
+      }
+      scales(j + 1);  // nothing past t_end is read
+      entries(j + 2);
+      m = group_max<32>(m);
+      if (lane == 0) vmb[4 * slot] = m;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sc_full + 8 * slot);
+    }
+  } else if (warp >= T::kIssuer) {
     // ---- the issuing thread ----
     if (lane == 0 && steps > 0) {
       constexpr uint32_t kBase = (1u << 4) | (8u << 24);  // f16 x f16 -> f32, M = 128
       constexpr uint32_t kIdS = kBase | (static_cast<uint32_t>(kBN / 8) << 17);
       constexpr uint32_t kIdO = kBase | (1u << 16) | (static_cast<uint32_t>(D / 8) << 17);  // B is MN-major
       auto scores = [&](int i, int j) {
-        const uint32_t qa = sbase + i * T::kQBytes, ka = sbase + T::kOffK + (j % kStages) * T::kKVBytes;
+        const uint32_t qa = desc_lo(sbase + i * T::kQBytes, 16);
+        const uint32_t ka = desc_lo(sbase + T::kOffK + (j % kStages) * T::kKVBytes, 16);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          tc_mma_ss(tmem + T::kColS + i * kBN, smem_desc(qa + (k / 4) * (128 * 128) + (k % 4) * 32, 16),
-                    smem_desc(ka + (k / 4) * (kBN * 128) + (k % 4) * 32, 16), kIdS, k > 0);
+          tc_mma_ss(tmem + T::kColS + i * kBN, smem_desc(qa, (k / 4) * (128 * 128) + (k % 4) * 32),
+                    smem_desc(ka, (k / 4) * (kBN * 128) + (k % 4) * 32), kIdS, k > 0);
         tc_commit(s_full + 8 * i);
         if (i == kNT - 1) tc_commit(k_empty + 8 * (j % kStages));
       };
@@ -499,15 +687,14 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
       for (int i = 0; i < kNT; ++i) scores(i, 0);
       for (int j = 0; j < steps; ++j) {
         const int st = j % kStages;
+        tile_wait(v_full + 8 * st, (j / kStages) & 1, misc, p.status);
         for (int i = 0; i < kNT; ++i) {
           tile_wait(p_ready + 8 * i, j & 1, misc, p.status);
-          if (i == 0) tile_wait(v_full + 8 * st, (j / kStages) & 1, misc, p.status);
           tc_fence_after();
-          const uint32_t va = sbase + T::kOffV + st * T::kKVBytes;
+          const uint32_t va = desc_lo(sbase + T::kOffV + st * T::kKVBytes, kBN * 128);
 #pragma unroll
           for (int k = 0; k < kBN / 16; ++k)
-            tc_mma_ts(tmem + T::kColO + i * D, tmem + T::kColS + i * kBN + 8 * k, smem_desc(va + k * 2048, kBN * 128), kIdO,
-                      j > 0 || k > 0);
+            tc_mma_ts(tmem + T::kColO + i * D, tmem + T::kColS + i * kBN + 8 * k, smem_desc(va, k * 2048), kIdO, j > 0 || k > 0);
           if (i == kNT - 1) tc_commit(v_empty + 8 * st);
           if (j + 1 < steps) {
             if (i == 0) {
@@ -525,64 +712,40 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
   } else if (warp >= T::kSoft) {
     // ---- producers ----
     const int tid = threadIdx.x - 32 * T::kSoft;
-    const int pw = tid >> 5;
-    int64_t* const rowbuf = reinterpret_cast<int64_t*>(smem + T::kOffRow);
-    float* const ksb = reinterpret_cast<float*>(smem + T::kOffKS);
-    float* const vsb = reinterpret_cast<float*>(smem + T::kOffVS);
-    float* const vmb = reinterpret_cast<float*>(smem + T::kOffVM);
-    // pool rows and scales of step j, one token a thread
-    auto resolve = [&](int j) {
-      if (j < steps) {
-        float ks = 0.0f, vs = 0.0f;
-        if (tid < kBN) {
-          const int t = t_begin + j * kBN + tid;
-          int64_t r = -1;
-          if (t < t_end) {
-            uint32_t bi, bo;
-            p.div_bs.divmod(static_cast<uint32_t>(t), bi, bo);
-            const int64_t blk = LDX(p.block_table + static_cast<int64_t>(s) * p.max_blocks + bi);
-            if (blk < 0 || blk >= p.num_blocks) {
-              misc->bad = 1;
-            } else {
-              r = (blk * p.block_size + bo) * p.H + h;
-              ks = LDX(p.k.rscale + (p.k_page ? blk * p.H + h : r));
-              vs = LDX(p.v.rscale + (p.v_page ? blk * p.H + h : r));
-            }
-          }
-          rowbuf[(j & 1) * kBN + tid] = r;
-          ksb[(j % T::kScaleSlots) * kBN + tid] = ks;
-          vsb[(j % T::kScaleSlots) * kBN + tid] = vs;
-        }
-        const float m = group_max<32>(vs);
-        if (lane == 0) vmb[(j % T::kScaleSlots) * 4 + pw] = m;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sc_full + 8 * (j % T::kScaleSlots));
-      }
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-    };
+    const int64_t* const rowbuf = reinterpret_cast<const int64_t*>(smem + T::kOffRow);
     TileLoad<D, kFK> lk;
     TileLoad<D, kFV> lv;
+    // K of step j + 1 is loaded into registers while K and V of step j are stored, V likewise
+    auto rows = [&](int j) {
+      tile_wait(sc_full + 8 * (j % T::kSlots), (j / T::kSlots) & 1, misc, p.status);
+      return rowbuf + (j % T::kSlots) * kBN;
+    };
     if (steps > 0) {
-      resolve(0);
-      lk.load(p.k, rowbuf, tid);
-      lv.load(p.v, rowbuf, tid);
+      const int64_t* const first = rows(0);
+      lk.load(p.k, first, tid);
+      lv.load(p.v, first, tid);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sc_empty);
     }
     for (int j = 0; j < steps; ++j) {
       const int st = j % kStages;
-      const int64_t* const next = rowbuf + ((j + 1) & 1) * kBN;
-      resolve(j + 1);
       if (j >= kStages) tile_wait(k_empty + 8 * st, ((j / kStages) - 1) & 1, misc, p.status);
       lk.store(sbase + T::kOffK + st * T::kKVBytes, tid);
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(k_full + 8 * st);
-      if (j + 1 < steps) lk.load(p.k, next, tid);
+      const int64_t* const next = j + 1 < steps ? rows(j + 1) : nullptr;
+      if (next != nullptr) lk.load(p.k, next, tid);
       if (j >= kStages) tile_wait(v_empty + 8 * st, ((j / kStages) - 1) & 1, misc, p.status);
       lv.store(sbase + T::kOffV + st * T::kKVBytes, tid);
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(v_full + 8 * st);
-      if (j + 1 < steps) lv.load(p.v, next, tid);
+      if (next != nullptr) {
+        lv.load(p.v, next, tid);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sc_empty + 8 * ((j + 1) % T::kSlots));
+      }
     }
   } else {
     // ---- softmax: one thread a row ----
@@ -592,15 +755,16 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
     const int mode = qp.slopes != nullptr ? kBiased : rl.cap ? kCapped : kPlain;
     float M = kNoKey, L = 0.0f;
     for (int j = 0; j < steps; ++j) {
-      const int slot = j % T::kScaleSlots;
+      const int slot = j % T::kSlots;
       const int t0 = t_begin + j * kBN;
-      tile_wait(sc_full + 8 * slot, (j / T::kScaleSlots) & 1, misc, p.status);
+      tile_wait(sc_full + 8 * slot, (j / T::kSlots) & 1, misc, p.status);
       tile_wait(s_full + 8 * i, j & 1, misc, p.status);
       tc_fence_after();
       __syncwarp();
-      const float* const ks = reinterpret_cast<const float*>(smem + T::kOffKS) + slot * kBN;
-      const float* const vs = reinterpret_cast<const float*>(smem + T::kOffVS) + slot * kBN;
-      const float4 vm = *reinterpret_cast<const float4*>(smem + T::kOffVM + 16 * slot);
+      const StepScales sc{reinterpret_cast<const float*>(smem + T::kOffKS) + slot * kBN,
+                          reinterpret_cast<const float*>(smem + T::kOffVS) + slot * kBN,
+                          reinterpret_cast<const float2*>(smem + T::kOffKS) + slot * (kBN / 16)};
+      const float vm = *reinterpret_cast<const float*>(smem + T::kOffVM + 16 * slot);
       const bool mask = __any_sync(0xFFFFFFFFu, rl.lo > t0 || rl.hi < t0 + kBN);
       const bool none = __all_sync(0xFFFFFFFFu, rl.lo >= t0 + kBN || rl.hi <= t0 || row < 0 || !sees);
       if (none) {  // no row of the warp sees a key of this step
@@ -611,12 +775,12 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
         for (int c = 0; c < kBN / 2; c += 16) tmem_st16(ts + c, z);
       } else {
         float mx;
-        if (mode == kPlain) mx = tile_max_any<kPlain, kBN>(mask, rl, ts, ks, t0);
-        else if (mode == kCapped) mx = tile_max_any<kCapped, kBN>(mask, rl, ts, ks, t0);
-        else mx = tile_max_any<kBiased, kBN>(mask, rl, ts, ks, t0);
+        if (mode == kPlain) mx = tile_max_any<kPlain, kBN, kPages>(mask, rl, ts, sc, t0);
+        else if (mode == kCapped) mx = tile_max_any<kCapped, kBN, kPages>(mask, rl, ts, sc, t0);
+        else mx = tile_max_any<kBiased, kBN, kPages>(mask, rl, ts, sc, t0);
         // V's scales enter P', so the reference covers them (their range is clamped far
         // outside what rows of ordinary size need)
-        const float lv = fminf(fmaxf(lg2(max3(fmaxf(vm.x, vm.y), vm.z, vm.w)), -100.0f), 100.0f);
+        const float lv = fminf(fmaxf(lg2(vm), -100.0f), 100.0f);
         const bool move = mx + lv > M + 8.0f;
         if (__any_sync(0xFFFFFFFFu, move)) {
           const float Mn = move ? mx + lv : M;
@@ -634,14 +798,17 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
             }
           }
         }
-        if (mode == kPlain) L += tile_probs_any<kPlain, kBN>(mask, rl, ts, ks, vs, t0, M);
-        else if (mode == kCapped) L += tile_probs_any<kCapped, kBN>(mask, rl, ts, ks, vs, t0, M);
-        else L += tile_probs_any<kBiased, kBN>(mask, rl, ts, ks, vs, t0, M);
+        if (mode == kPlain) L += tile_probs_any<kPlain, kBN, kPages>(mask, rl, ts, sc, t0, M);
+        else if (mode == kCapped) L += tile_probs_any<kCapped, kBN, kPages>(mask, rl, ts, sc, t0, M);
+        else L += tile_probs_any<kBiased, kBN, kPages>(mask, rl, ts, sc, t0, M);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_ready + 8 * i);
+      if (lane == 0) {
+        mbar_arrive(p_ready + 8 * i);
+        mbar_arrive(sc_empty + 8 * slot);
+      }
     }
     if (steps > 0) {
       tile_wait(o_done + 8 * i, 0, misc, p.status);
@@ -690,17 +857,17 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == T::kWarps - 1) {
+  if (warp == T::kIssuer) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
   if (threadIdx.x == 0 && misc->bad != 0) set_status(p.status, 2u);
 }
 
-template <int D, int kFK, int kFV>
+template <int D, int kFK, int kFV, bool kPages = false>
 cudaError_t tile_launch(const QueryAttnParams& p, cudaStream_t s) {
   using T = QTile<D>;
-  auto k = query_tile_kernel<D, kFK, kFV>;
+  auto k = query_tile_kernel<D, kFK, kFV, kPages>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (static_cast<int64_t>(p.max_q) * p.a.group + T::kRows - 1) / T::kRows;
@@ -712,6 +879,7 @@ cudaError_t tile_launch(const QueryAttnParams& p, cudaStream_t s) {
 template <int D>
 cudaError_t tile_dispatch(const QueryAttnParams& p, cudaStream_t s) {
   const bool k8 = p.a.fmt_k == 3, v8 = p.a.fmt_v == 3;
+  if (p.a.k_page && p.a.v_page && p.a.block_size % 16 == 0) return tile_launch<D, 3, 3, true>(p, s);
   if (!k8 && !v8) return tile_launch<D, 1, 1>(p, s);
   if (k8 && !v8) return tile_launch<D, 3, 1>(p, s);
   if (!k8 && v8) return tile_launch<D, 1, 3>(p, s);
