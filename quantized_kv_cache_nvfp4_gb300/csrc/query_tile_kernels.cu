@@ -37,23 +37,35 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t cols) {
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// Arrives on the mbarrier once all products issued so far by this thread are complete.
-__device__ __forceinline__ void tc_commit(uint32_t mbar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mbar) : "memory");
+// The warp that issues the products runs its loop as a whole (addresses and descriptors are
+// then uniform registers, which the instructions want; one thread's own loop measured twice
+// the issue time), and one lane of it, `leader`, issues.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t leader;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
+  return leader;
 }
-// D (tensor memory) (+)= A B: both from shared memory, or A from tensor memory.
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// Arrives on the mbarrier once all products issued so far by this thread are complete.
+__device__ __forceinline__ void tc_commit(uint32_t leader, uint32_t mbar) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %0, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(leader),
+      "r"(mbar)
       : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+// D (tensor memory) (+)= A B: both from shared memory, or A from tensor memory.
+__device__ __forceinline__ void tc_mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %0, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%1], %2, %3, %4, p;\n\t}" ::"r"(leader),
+      "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %0, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], %3, %4, p;\n\t}" ::"r"(leader),
+      "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
       : "memory");
 }
 // 32 columns of this warp's 32 lanes, one lane a row; the wait is part of the load.
@@ -475,7 +487,8 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
   unsigned char* const smem = tile_smem_raw + (sbase - raw);
   TileMisc* const misc = reinterpret_cast<TileMisc*>(smem + T::kOffMisc);
 
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform for the compiler too
   const int s = blockIdx.z, h = blockIdx.y;
   // the last rows first: under a causal mask they see the most keys
   const int ntiles = gridDim.x / p.nsplit;
@@ -586,7 +599,7 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = misc->tmem;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, misc->tmem, 0);
   const int key_lo = misc->lo, key_hi = misc->hi;
   int t_begin = 0, t_end = 0;
   if (key_lo < key_hi) {  // equal splits in whole steps
@@ -667,8 +680,9 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
       if (lane == 0) mbar_arrive(sc_full + 8 * slot);
     }
   } else if (warp >= T::kIssuer) {
-    // ---- the issuing thread ----
-    if (lane == 0 && steps > 0) {
+    // ---- the products ----
+    if (steps > 0) {
+      const uint32_t leader = elect_one();
       constexpr uint32_t kBase = (1u << 4) | (8u << 24);  // f16 x f16 -> f32, M = 128
       constexpr uint32_t kIdS = kBase | (static_cast<uint32_t>(kBN / 8) << 17);
       constexpr uint32_t kIdO = kBase | (1u << 16) | (static_cast<uint32_t>(D / 8) << 17);  // B is MN-major
@@ -677,10 +691,10 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
         const uint32_t ka = desc_lo(sbase + T::kOffK + (j % kStages) * T::kKVBytes, 16);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          tc_mma_ss(tmem + T::kColS + i * kBN, smem_desc(qa, (k / 4) * (128 * 128) + (k % 4) * 32),
+          tc_mma_ss(leader, tmem + T::kColS + i * kBN, smem_desc(qa, (k / 4) * (128 * 128) + (k % 4) * 32),
                     smem_desc(ka, (k / 4) * (kBN * 128) + (k % 4) * 32), kIdS, k > 0);
-        tc_commit(s_full + 8 * i);
-        if (i == kNT - 1) tc_commit(k_empty + 8 * (j % kStages));
+        tc_commit(leader, s_full + 8 * i);
+        if (i == kNT - 1) tc_commit(leader, k_empty + 8 * (j % kStages));
       };
       tile_wait(k_full, 0, misc, p.status);
       tc_fence_after();
@@ -694,8 +708,8 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
           const uint32_t va = desc_lo(sbase + T::kOffV + st * T::kKVBytes, kBN * 128);
 #pragma unroll
           for (int k = 0; k < kBN / 16; ++k)
-            tc_mma_ts(tmem + T::kColO + i * D, tmem + T::kColS + i * kBN + 8 * k, smem_desc(va, k * 2048), kIdO, j > 0 || k > 0);
-          if (i == kNT - 1) tc_commit(v_empty + 8 * st);
+            tc_mma_ts(leader, tmem + T::kColO + i * D, tmem + T::kColS + i * kBN + 8 * k, smem_desc(va, k * 2048), kIdO, j > 0 || k > 0);
+          if (i == kNT - 1) tc_commit(leader, v_empty + 8 * st);
           if (j + 1 < steps) {
             if (i == 0) {
               tile_wait(k_full + 8 * ((j + 1) % kStages), ((j + 1) / kStages) & 1, misc, p.status);
@@ -703,7 +717,7 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
             }
             scores(i, j + 1);
           } else {
-            tc_commit(o_done + 8 * i);
+            tc_commit(leader, o_done + 8 * i);
           }
         }
       }
