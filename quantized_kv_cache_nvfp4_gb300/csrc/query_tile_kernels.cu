@@ -189,11 +189,21 @@ __device__ __forceinline__ void tile_wait(uint32_t bar, uint32_t parity, volatil
 }
 
 // ---- logits ------------------------------------------------------------------------
-enum LogitMode : int { kPlain = 0, kCapped = 1, kBiased = 2 };
+enum LogitMode : int { kPlain = 0, kCapped = 1, kBiased = 2, kNearCap = 3 };
+
+// A capped logit costs 2^x and a reciprocal beside the probability's own 2^x, and the unit
+// that computes these is then the kernel's bound (8 results a clock and scheduler for 2^x).
+// Where every score of a warp's step is below 3/4 of the cap (kNearCap), tanh comes from an
+// odd polynomial of degree 9 instead: the minimax fit on [-3/4, 3/4] (iteratively reweighted
+// least squares on a Chebyshev grid), off by at most 0.3 * 2^-20 with its binary32 rounding.
+constexpr float kTanhRange = 0.75f;
+constexpr float kTanh0 = 0.9999971985816956f, kTanh1 = -0.33323076367378235f, kTanh2 = 0.13226091861724854f,
+                kTanh3 = -0.049280449748039246f, kTanh4 = 0.012318833731114864f;
 
 struct RowLogit {
   float f;       // query factor times log2 e (plain, biased without cap)
   float fz;      // capped: 2 log2 e / softcap times the query factor
+  float fu;      // capped: the query factor over softcap
   float c2;      // capped: softcap log2 e
   bool cap;
   float slope;   // times log2 e
@@ -215,12 +225,54 @@ __device__ __forceinline__ float logit(const RowLogit& r, float x, float tf, int
   return y;
 }
 
+// y - M + add for a pair of scores x in kPlain (f2 the factor), kCapped (f2 = 2 log2 e / cap
+// times the factor, y = c2 - 2 c2 / (1 + 2^(x f2)), c2 part of add) or kNearCap (f2 the factor
+// over cap, y = c2 tanh(x f2)).
+struct CapPairs {
+  uint64_t one, m2c, k[5];  // 1, -2 c2, and the polynomial's coefficients times c2
+  template <int kMode>
+  __device__ __forceinline__ void init(float c2) {
+    if (kMode == kCapped) {
+      one = dup_f32x2(1.0f);
+      m2c = dup_f32x2(-2.0f * c2);
+    }
+    if (kMode == kNearCap) {
+      k[0] = dup_f32x2(kTanh0 * c2);
+      k[1] = dup_f32x2(kTanh1 * c2);
+      k[2] = dup_f32x2(kTanh2 * c2);
+      k[3] = dup_f32x2(kTanh3 * c2);
+      k[4] = dup_f32x2(kTanh4 * c2);
+    }
+  }
+  template <int kMode>
+  __device__ __forceinline__ uint64_t logit2(uint64_t x, uint64_t f2, uint64_t add) const {
+    if constexpr (kMode == kPlain) {
+      return fma_f32x2(x, f2, add);
+    } else if constexpr (kMode == kNearCap) {
+      const uint64_t u = mul_f32x2(x, f2), t = mul_f32x2(u, u);
+      uint64_t P = fma_f32x2(k[4], t, k[3]);
+      P = fma_f32x2(P, t, k[2]);
+      P = fma_f32x2(P, t, k[1]);
+      P = fma_f32x2(P, t, k[0]);
+      return fma_f32x2(u, P, add);
+    } else {
+      uint32_t a, b;
+      unpack_f32x2(mul_f32x2(x, f2), a, b);
+      unpack_f32x2(add_f32x2(pack_f32x2(__float_as_uint(ex2_ftz(__uint_as_float(a))), __float_as_uint(ex2_ftz(__uint_as_float(b)))),
+                             one), a, b);
+      return fma_f32x2(pack_f32x2(__float_as_uint(rcp_ftz(__uint_as_float(a))), __float_as_uint(rcp_ftz(__uint_as_float(b)))),
+                       m2c, add);
+    }
+  }
+};
+
 // Largest logit of a tile's row (-inf where it sees no key of the tile).
+// most: the largest |score| (kCapped only).
 template <int kMode, bool kMask, int kBN>
-__device__ __forceinline__ float tile_max(const RowLogit& r, uint32_t taddr, const float* ks, int t0) {
+__device__ __forceinline__ float tile_max(const RowLogit& r, uint32_t taddr, const float* ks, int t0, float& most) {
   const int lo = r.lo - t0, hi = r.hi - t0;
   const float tf = static_cast<float>(t0 - r.pos);
-  float m0 = kNegInf, m1 = kNegInf;
+  float m0 = kNegInf, m1 = kNegInf, a0 = 0.0f;
 #pragma unroll 1
   for (int c0 = 0; c0 < kBN; c0 += 32) {
     uint32_t v[32];
@@ -232,6 +284,7 @@ __device__ __forceinline__ float tile_max(const RowLogit& r, uint32_t taddr, con
       unpack_f32x2(mul_f32x2(pack_f32x2(v[i], v[i + 1]), k4.x), x0, x1);
       unpack_f32x2(mul_f32x2(pack_f32x2(v[i + 2], v[i + 3]), k4.y), x2, x3);
       float y[4] = {__uint_as_float(x0), __uint_as_float(x1), __uint_as_float(x2), __uint_as_float(x3)};
+      if (kMode == kCapped) a0 = max3(max3(a0, fabsf(y[0]), fabsf(y[1])), fabsf(y[2]), fabsf(y[3]));
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (kMode == kBiased) y[e] = logit<kMode>(r, y[e], tf, c0 + i + e);
@@ -242,6 +295,7 @@ __device__ __forceinline__ float tile_max(const RowLogit& r, uint32_t taddr, con
     }
   }
   const float m = fmaxf(m0, m1);
+  most = a0;
   // without a bias the logit grows with the score, so it is taken once
   if (kMode == kBiased || (kMask && m == kNegInf)) return m;
   return logit<kMode>(r, m, 0.0f, 0);
@@ -253,7 +307,10 @@ __device__ __forceinline__ float tile_probs(const RowLogit& r, uint32_t taddr, c
                                             float M) {
   const int lo = r.lo - t0, hi = r.hi - t0;
   const float tf = static_cast<float>(t0 - r.pos);
-  const uint64_t f2 = dup_f32x2(r.f), nM = dup_f32x2(-M);
+  const uint64_t f2 = dup_f32x2(kMode == kPlain ? r.f : kMode == kNearCap ? r.fu : r.fz);
+  const uint64_t add = dup_f32x2(kMode == kCapped ? r.c2 - M : -M);
+  CapPairs cp;
+  cp.init<kMode>(r.c2);
   uint64_t l0 = 0, l1 = 0;  // two pairs of partial sums
 #pragma unroll 1
   for (int c0 = 0; c0 < kBN; c0 += 32) {
@@ -265,9 +322,9 @@ __device__ __forceinline__ float tile_probs(const RowLogit& r, uint32_t taddr, c
       const ulonglong2 v4 = *reinterpret_cast<const ulonglong2*>(vs + c0 + i);
       uint64_t xa = mul_f32x2(pack_f32x2(v[i], v[i + 1]), k4.x);
       uint64_t xb = mul_f32x2(pack_f32x2(v[i + 2], v[i + 3]), k4.y);
-      if (kMode == kPlain) {
-        xa = fma_f32x2(xa, f2, nM);
-        xb = fma_f32x2(xb, f2, nM);
+      if (kMode != kBiased) {
+        xa = cp.logit2<kMode>(xa, f2, add);
+        xb = cp.logit2<kMode>(xb, f2, add);
       }
       uint32_t x[4];
       unpack_f32x2(xa, x[0], x[1]);
@@ -276,7 +333,7 @@ __device__ __forceinline__ float tile_probs(const RowLogit& r, uint32_t taddr, c
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float y = __uint_as_float(x[e]);
-        if (kMode != kPlain) y = logit<kMode>(r, y, tf, c0 + i + e) - M;
+        if (kMode == kBiased) y = logit<kMode>(r, y, tf, c0 + i + e) - M;
         if (kMask) y = c0 + i + e >= lo && c0 + i + e < hi ? y : kNegInf;
         p[e] = ex2_ftz(y);
       }
@@ -304,10 +361,11 @@ __device__ __forceinline__ float tile_probs(const RowLogit& r, uint32_t taddr, c
 // the scores is then part of the row's factor, and P' = 2^(y - M + log2 vs) needs no product;
 // the group's sum of P' is divided by vs for l.
 template <int kMode, bool kMask, int kBN>
-__device__ __forceinline__ float tile_max_pages(const RowLogit& r, uint32_t taddr, const float2* gs, int t0) {
+__device__ __forceinline__ float tile_max_pages(const RowLogit& r, uint32_t taddr, const float2* gs, int t0, float& most) {
   const int lo = r.lo - t0, hi = r.hi - t0;
   const float tf = static_cast<float>(t0 - r.pos);
   float best = kNegInf;
+  most = 0.0f;
 #pragma unroll 1
   for (int c0 = 0; c0 < kBN; c0 += 32) {
     uint32_t v[32];
@@ -315,16 +373,18 @@ __device__ __forceinline__ float tile_max_pages(const RowLogit& r, uint32_t tadd
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       const float ks = gs[c0 / 16 + g].x;
-      float m[2] = {kNegInf, kNegInf};
+      float m[2] = {kNegInf, kNegInf}, a = 0.0f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int col = c0 + 16 * g + i;
         float x = __uint_as_float(v[16 * g + i]);
+        if (kMode == kCapped) a = fmaxf(a, fabsf(x));
         if (kMode == kBiased) x = logit<kMode>(r, x * ks, tf, col);
         if (kMask) x = col >= lo && col < hi ? x : kNegInf;
         m[i % 2] = fmaxf(m[i % 2], x);
       }
       const float mg = fmaxf(m[0], m[1]);
+      if (kMode == kCapped) most = fmaxf(most, a * ks);
       best = fmaxf(best, kMode == kBiased || (kMask && mg == kNegInf) ? mg : mg * ks);
     }
   }
@@ -336,7 +396,8 @@ template <int kMode, bool kMask, int kBN>
 __device__ __forceinline__ float tile_probs_pages(const RowLogit& r, uint32_t taddr, const float2* gs, int t0, float M) {
   const int lo = r.lo - t0, hi = r.hi - t0;
   const float tf = static_cast<float>(t0 - r.pos);
-  const uint64_t c2 = dup_f32x2(-2.0f * r.c2), one2 = dup_f32x2(1.0f);
+  CapPairs cp;
+  cp.init<kMode>(r.c2);
   float L = 0.0f;
 #pragma unroll 1
   for (int c0 = 0; c0 < kBN; c0 += 32) {
@@ -346,8 +407,8 @@ __device__ __forceinline__ float tile_probs_pages(const RowLogit& r, uint32_t ta
     for (int g = 0; g < 2; ++g) {
       const float2 s = gs[c0 / 16 + g];
       const float ref = s.y - M;
-      const uint64_t f2 = dup_f32x2((kMode == kPlain ? r.f : r.fz) * s.x);
-      const uint64_t add2 = dup_f32x2(kMode == kPlain ? ref : r.c2 + ref);
+      const uint64_t f2 = dup_f32x2((kMode == kPlain ? r.f : kMode == kNearCap ? r.fu : r.fz) * s.x);
+      const uint64_t add = dup_f32x2(kMode == kCapped ? r.c2 + ref : ref);
       uint64_t l[2] = {0, 0};
 #pragma unroll
       for (int i = 0; i < 16; i += 2) {
@@ -359,18 +420,7 @@ __device__ __forceinline__ float tile_probs_pages(const RowLogit& r, uint32_t ta
           y0 = logit<kMode>(r, __uint_as_float(v[16 * g + i]) * s.x, tf, col) + ref;
           y1 = logit<kMode>(r, __uint_as_float(v[16 * g + i + 1]) * s.x, tf, col + 1) + ref;
         } else {
-          uint64_t y2;
-          if (kMode == kPlain) {
-            y2 = fma_f32x2(x2, f2, add2);
-          } else {  // (c2 + ref) - 2 c2 / (1 + 2^(x fz ks))
-            uint32_t e0, e1;
-            unpack_f32x2(mul_f32x2(x2, f2), e0, e1);
-            unpack_f32x2(add_f32x2(pack_f32x2(__float_as_uint(ex2_ftz(__uint_as_float(e0))),
-                                              __float_as_uint(ex2_ftz(__uint_as_float(e1)))), one2), e0, e1);
-            y2 = fma_f32x2(pack_f32x2(__float_as_uint(rcp_ftz(__uint_as_float(e0))),
-                                      __float_as_uint(rcp_ftz(__uint_as_float(e1)))), c2, add2);
-          }
-          unpack_f32x2(y2, a, b);
+          unpack_f32x2(cp.logit2<kMode>(x2, f2, add), a, b);
           y0 = __uint_as_float(a);
           y1 = __uint_as_float(b);
         }
@@ -399,11 +449,11 @@ struct StepScales {
 };
 
 template <int kMode, int kBN, bool kPages>
-__device__ __forceinline__ float tile_max_any(bool mask, const RowLogit& r, uint32_t ta, const StepScales& sc, int t0) {
+__device__ __forceinline__ float tile_max_any(bool mask, const RowLogit& r, uint32_t ta, const StepScales& sc, int t0, float& most) {
   if constexpr (kPages)
-    return mask ? tile_max_pages<kMode, true, kBN>(r, ta, sc.gs, t0) : tile_max_pages<kMode, false, kBN>(r, ta, sc.gs, t0);
+    return mask ? tile_max_pages<kMode, true, kBN>(r, ta, sc.gs, t0, most) : tile_max_pages<kMode, false, kBN>(r, ta, sc.gs, t0, most);
   else
-    return mask ? tile_max<kMode, true, kBN>(r, ta, sc.ks, t0) : tile_max<kMode, false, kBN>(r, ta, sc.ks, t0);
+    return mask ? tile_max<kMode, true, kBN>(r, ta, sc.ks, t0, most) : tile_max<kMode, false, kBN>(r, ta, sc.ks, t0, most);
 }
 template <int kMode, int kBN, bool kPages>
 __device__ __forceinline__ float tile_probs_any(bool mask, const RowLogit& r, uint32_t ta, const StepScales& sc, int t0, float M) {
@@ -587,6 +637,7 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
     rl.f = fac * kLog2e;
     rl.cap = qp.softcap > 0.0f;
     rl.c2 = qp.softcap * kLog2e;
+    rl.fu = rl.cap ? fac / qp.softcap : 0.0f;
     rl.fz = rl.cap ? 2.0f * kLog2e / qp.softcap * fac : 0.0f;
     const int lo = __reduce_min_sync(0xFFFFFFFFu, sees ? rl.lo : 0x7FFFFFFF);
     const int hi = __reduce_max_sync(0xFFFFFFFFu, sees ? rl.hi : 0);
@@ -788,10 +839,10 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
 #pragma unroll
         for (int c = 0; c < kBN / 2; c += 16) tmem_st16(ts + c, z);
       } else {
-        float mx;
-        if (mode == kPlain) mx = tile_max_any<kPlain, kBN, kPages>(mask, rl, ts, sc, t0);
-        else if (mode == kCapped) mx = tile_max_any<kCapped, kBN, kPages>(mask, rl, ts, sc, t0);
-        else mx = tile_max_any<kBiased, kBN, kPages>(mask, rl, ts, sc, t0);
+        float mx, most;
+        if (mode == kPlain) mx = tile_max_any<kPlain, kBN, kPages>(mask, rl, ts, sc, t0, most);
+        else if (mode == kCapped) mx = tile_max_any<kCapped, kBN, kPages>(mask, rl, ts, sc, t0, most);
+        else mx = tile_max_any<kBiased, kBN, kPages>(mask, rl, ts, sc, t0, most);
         // V's scales enter P', so the reference covers them (their range is clamped far
         // outside what rows of ordinary size need)
         const float lv = fminf(fmaxf(lg2(vm), -100.0f), 100.0f);
@@ -813,6 +864,8 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
           }
         }
         if (mode == kPlain) L += tile_probs_any<kPlain, kBN, kPages>(mask, rl, ts, sc, t0, M);
+        else if (mode == kCapped && __all_sync(0xFFFFFFFFu, most * rl.fu <= kTanhRange))
+          L += tile_probs_any<kNearCap, kBN, kPages>(mask, rl, ts, sc, t0, M);
         else if (mode == kCapped) L += tile_probs_any<kCapped, kBN, kPages>(mask, rl, ts, sc, t0, M);
         else L += tile_probs_any<kBiased, kBN, kPages>(mask, rl, ts, sc, t0, M);
       }
