@@ -189,7 +189,7 @@ __device__ __forceinline__ void tile_wait(uint32_t bar, uint32_t parity, volatil
 }
 
 // ---- logits ------------------------------------------------------------------------
-enum LogitMode : int { kPlain = 0, kCapped = 1, kBiased = 2, kNearCap = 3 };
+enum LogitMode : int { kPlain, kCapped, kNearCap, kBiased, kBoth /* cap and bias */ };
 
 // A capped logit costs 2^x and a reciprocal beside the probability's own 2^x, and the unit
 // that computes these is then the kernel's bound (8 results a clock and scheduler for 2^x).
@@ -205,7 +205,7 @@ struct RowLogit {
   float fz;      // capped: 2 log2 e / softcap times the query factor
   float fu;      // capped: the query factor over softcap
   float c2;      // capped: softcap log2 e
-  bool cap;
+  bool cap;      // whether there is one
   float slope;   // times log2 e
   int pos;
   int lo, hi;
@@ -216,12 +216,12 @@ struct RowLogit {
 template <int kMode>
 __device__ __forceinline__ float logit(const RowLogit& r, float x, float tf, int col) {
   float y;
-  if (kMode == kCapped || (kMode == kBiased && r.cap)) {
+  if (kMode == kCapped || kMode == kBoth) {
     y = __fmaf_rn(-2.0f * r.c2, rcp_ftz(1.0f + ex2_ftz(x * r.fz)), r.c2);
   } else {
     y = x * r.f;
   }
-  if (kMode == kBiased) y = __fmaf_rn(r.slope, tf + static_cast<float>(col), y);
+  if (kMode == kBoth) y = __fmaf_rn(r.slope, tf + static_cast<float>(col), y);
   return y;
 }
 
@@ -246,7 +246,7 @@ struct CapPairs {
   }
   template <int kMode>
   __device__ __forceinline__ uint64_t logit2(uint64_t x, uint64_t f2, uint64_t add) const {
-    if constexpr (kMode == kPlain) {
+    if constexpr (kMode == kPlain || kMode == kBiased) {
       return fma_f32x2(x, f2, add);
     } else if constexpr (kMode == kNearCap) {
       const uint64_t u = mul_f32x2(x, f2), t = mul_f32x2(u, u);
@@ -266,6 +266,11 @@ struct CapPairs {
   }
 };
 
+// slope * col + base for the columns col and col + 1 (kBiased).
+__device__ __forceinline__ uint64_t bias2(uint64_t slope, int col, uint64_t base) {
+  return fma_f32x2(slope, pack_f32x2(__float_as_uint(static_cast<float>(col)), __float_as_uint(static_cast<float>(col + 1))), base);
+}
+
 // Largest logit of a tile's row (-inf where it sees no key of the tile).
 // most: the largest |score| (kCapped only).
 template <int kMode, bool kMask, int kBN>
@@ -273,21 +278,29 @@ __device__ __forceinline__ float tile_max(const RowLogit& r, uint32_t taddr, con
   const int lo = r.lo - t0, hi = r.hi - t0;
   const float tf = static_cast<float>(t0 - r.pos);
   float m0 = kNegInf, m1 = kNegInf, a0 = 0.0f;
+  const uint64_t f2 = dup_f32x2(r.f), s2 = dup_f32x2(r.slope);
 #pragma unroll 1
   for (int c0 = 0; c0 < kBN; c0 += 32) {
+    const uint64_t base = dup_f32x2(r.slope * (tf + static_cast<float>(c0)));
     uint32_t v[32];
     tmem_ld32(taddr + c0, v);
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
       const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(ks + c0 + i);
+      uint64_t xa = mul_f32x2(pack_f32x2(v[i], v[i + 1]), k4.x);
+      uint64_t xb = mul_f32x2(pack_f32x2(v[i + 2], v[i + 3]), k4.y);
+      if (kMode == kBiased) {
+        xa = fma_f32x2(xa, f2, bias2(s2, i, base));
+        xb = fma_f32x2(xb, f2, bias2(s2, i + 2, base));
+      }
       uint32_t x0, x1, x2, x3;
-      unpack_f32x2(mul_f32x2(pack_f32x2(v[i], v[i + 1]), k4.x), x0, x1);
-      unpack_f32x2(mul_f32x2(pack_f32x2(v[i + 2], v[i + 3]), k4.y), x2, x3);
+      unpack_f32x2(xa, x0, x1);
+      unpack_f32x2(xb, x2, x3);
       float y[4] = {__uint_as_float(x0), __uint_as_float(x1), __uint_as_float(x2), __uint_as_float(x3)};
       if (kMode == kCapped) a0 = max3(max3(a0, fabsf(y[0]), fabsf(y[1])), fabsf(y[2]), fabsf(y[3]));
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if (kMode == kBiased) y[e] = logit<kMode>(r, y[e], tf, c0 + i + e);
+        if (kMode == kBoth) y[e] = logit<kMode>(r, y[e], tf, c0 + i + e);
         if (kMask) y[e] = c0 + i + e >= lo && c0 + i + e < hi ? y[e] : kNegInf;
       }
       m0 = max3(m0, y[0], y[1]);
@@ -297,7 +310,7 @@ __device__ __forceinline__ float tile_max(const RowLogit& r, uint32_t taddr, con
   const float m = fmaxf(m0, m1);
   most = a0;
   // without a bias the logit grows with the score, so it is taken once
-  if (kMode == kBiased || (kMask && m == kNegInf)) return m;
+  if (kMode == kBiased || kMode == kBoth || (kMask && m == kNegInf)) return m;
   return logit<kMode>(r, m, 0.0f, 0);
 }
 
@@ -307,13 +320,14 @@ __device__ __forceinline__ float tile_probs(const RowLogit& r, uint32_t taddr, c
                                             float M) {
   const int lo = r.lo - t0, hi = r.hi - t0;
   const float tf = static_cast<float>(t0 - r.pos);
-  const uint64_t f2 = dup_f32x2(kMode == kPlain ? r.f : kMode == kNearCap ? r.fu : r.fz);
+  const uint64_t f2 = dup_f32x2(kMode == kNearCap ? r.fu : kMode == kCapped ? r.fz : r.f), s2 = dup_f32x2(r.slope);
   const uint64_t add = dup_f32x2(kMode == kCapped ? r.c2 - M : -M);
   CapPairs cp;
   cp.init<kMode>(r.c2);
   uint64_t l0 = 0, l1 = 0;  // two pairs of partial sums
 #pragma unroll 1
   for (int c0 = 0; c0 < kBN; c0 += 32) {
+    const uint64_t base = dup_f32x2(__fmaf_rn(r.slope, tf + static_cast<float>(c0), -M));
     uint32_t v[32], h[16];
     tmem_ld32(taddr + c0, v);
 #pragma unroll
@@ -322,7 +336,10 @@ __device__ __forceinline__ float tile_probs(const RowLogit& r, uint32_t taddr, c
       const ulonglong2 v4 = *reinterpret_cast<const ulonglong2*>(vs + c0 + i);
       uint64_t xa = mul_f32x2(pack_f32x2(v[i], v[i + 1]), k4.x);
       uint64_t xb = mul_f32x2(pack_f32x2(v[i + 2], v[i + 3]), k4.y);
-      if (kMode != kBiased) {
+      if (kMode == kBiased) {
+        xa = fma_f32x2(xa, f2, bias2(s2, i, base));
+        xb = fma_f32x2(xb, f2, bias2(s2, i + 2, base));
+      } else if (kMode != kBoth) {
         xa = cp.logit2<kMode>(xa, f2, add);
         xb = cp.logit2<kMode>(xb, f2, add);
       }
@@ -333,7 +350,7 @@ __device__ __forceinline__ float tile_probs(const RowLogit& r, uint32_t taddr, c
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float y = __uint_as_float(x[e]);
-        if (kMode == kBiased) y = logit<kMode>(r, y, tf, c0 + i + e) - M;
+        if (kMode == kBoth) y = logit<kMode>(r, y, tf, c0 + i + e) - M;
         if (kMask) y = c0 + i + e >= lo && c0 + i + e < hi ? y : kNegInf;
         p[e] = ex2_ftz(y);
       }
@@ -364,6 +381,7 @@ template <int kMode, bool kMask, int kBN>
 __device__ __forceinline__ float tile_max_pages(const RowLogit& r, uint32_t taddr, const float2* gs, int t0, float& most) {
   const int lo = r.lo - t0, hi = r.hi - t0;
   const float tf = static_cast<float>(t0 - r.pos);
+  const uint64_t s2 = dup_f32x2(r.slope);
   float best = kNegInf;
   most = 0.0f;
 #pragma unroll 1
@@ -374,21 +392,26 @@ __device__ __forceinline__ float tile_max_pages(const RowLogit& r, uint32_t tadd
     for (int g = 0; g < 2; ++g) {
       const float ks = gs[c0 / 16 + g].x;
       float m[2] = {kNegInf, kNegInf}, a = 0.0f;
+      const uint64_t f2 = dup_f32x2(r.f * ks);
+      const uint64_t base = dup_f32x2(r.slope * (tf + static_cast<float>(c0 + 16 * g)));
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int col = c0 + 16 * g + i;
+        if (kMode == kBiased && i % 2 == 0)
+          unpack_f32x2(fma_f32x2(pack_f32x2(v[16 * g + i], v[16 * g + i + 1]), f2, bias2(s2, i, base)), v[16 * g + i],
+                       v[16 * g + i + 1]);
         float x = __uint_as_float(v[16 * g + i]);
         if (kMode == kCapped) a = fmaxf(a, fabsf(x));
-        if (kMode == kBiased) x = logit<kMode>(r, x * ks, tf, col);
+        if (kMode == kBoth) x = logit<kMode>(r, x * ks, tf, col);
         if (kMask) x = col >= lo && col < hi ? x : kNegInf;
         m[i % 2] = fmaxf(m[i % 2], x);
       }
       const float mg = fmaxf(m[0], m[1]);
       if (kMode == kCapped) most = fmaxf(most, a * ks);
-      best = fmaxf(best, kMode == kBiased || (kMask && mg == kNegInf) ? mg : mg * ks);
+      best = fmaxf(best, kMode == kBiased || kMode == kBoth || (kMask && mg == kNegInf) ? mg : mg * ks);
     }
   }
-  if (kMode == kBiased || (kMask && best == kNegInf)) return best;
+  if (kMode == kBiased || kMode == kBoth || (kMask && best == kNegInf)) return best;
   return logit<kMode>(r, best, 0.0f, 0);
 }
 
@@ -398,6 +421,7 @@ __device__ __forceinline__ float tile_probs_pages(const RowLogit& r, uint32_t ta
   const float tf = static_cast<float>(t0 - r.pos);
   CapPairs cp;
   cp.init<kMode>(r.c2);
+  const uint64_t s2 = dup_f32x2(r.slope);
   float L = 0.0f;
 #pragma unroll 1
   for (int c0 = 0; c0 < kBN; c0 += 32) {
@@ -407,7 +431,8 @@ __device__ __forceinline__ float tile_probs_pages(const RowLogit& r, uint32_t ta
     for (int g = 0; g < 2; ++g) {
       const float2 s = gs[c0 / 16 + g];
       const float ref = s.y - M;
-      const uint64_t f2 = dup_f32x2((kMode == kPlain ? r.f : kMode == kNearCap ? r.fu : r.fz) * s.x);
+      const uint64_t f2 = dup_f32x2((kMode == kNearCap ? r.fu : kMode == kCapped ? r.fz : r.f) * s.x);
+      const uint64_t base = dup_f32x2(__fmaf_rn(r.slope, tf + static_cast<float>(c0 + 16 * g), ref));
       const uint64_t add = dup_f32x2(kMode == kCapped ? r.c2 + ref : ref);
       uint64_t l[2] = {0, 0};
 #pragma unroll
@@ -416,11 +441,11 @@ __device__ __forceinline__ float tile_probs_pages(const RowLogit& r, uint32_t ta
         const uint64_t x2 = pack_f32x2(v[16 * g + i], v[16 * g + i + 1]);
         float y0, y1;
         uint32_t a, b;
-        if (kMode == kBiased) {
+        if (kMode == kBoth) {
           y0 = logit<kMode>(r, __uint_as_float(v[16 * g + i]) * s.x, tf, col) + ref;
           y1 = logit<kMode>(r, __uint_as_float(v[16 * g + i + 1]) * s.x, tf, col + 1) + ref;
         } else {
-          unpack_f32x2(cp.logit2<kMode>(x2, f2, add), a, b);
+          unpack_f32x2(kMode == kBiased ? fma_f32x2(x2, f2, bias2(s2, i, base)) : cp.logit2<kMode>(x2, f2, add), a, b);
           y0 = __uint_as_float(a);
           y1 = __uint_as_float(b);
         }
@@ -817,7 +842,7 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
     const int i = warp / 4;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + T::kColS + i * kBN, to = tmem + lanes + T::kColO + i * D;
-    const int mode = qp.slopes != nullptr ? kBiased : rl.cap ? kCapped : kPlain;
+    const int mode = qp.slopes != nullptr ? (rl.cap ? kBoth : kBiased) : rl.cap ? kCapped : kPlain;
     float M = kNoKey, L = 0.0f;
     for (int j = 0; j < steps; ++j) {
       const int slot = j % T::kSlots;
@@ -842,7 +867,8 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
         float mx, most;
         if (mode == kPlain) mx = tile_max_any<kPlain, kBN, kPages>(mask, rl, ts, sc, t0, most);
         else if (mode == kCapped) mx = tile_max_any<kCapped, kBN, kPages>(mask, rl, ts, sc, t0, most);
-        else mx = tile_max_any<kBiased, kBN, kPages>(mask, rl, ts, sc, t0, most);
+        else if (mode == kBiased) mx = tile_max_any<kBiased, kBN, kPages>(mask, rl, ts, sc, t0, most);
+        else mx = tile_max_any<kBoth, kBN, kPages>(mask, rl, ts, sc, t0, most);
         // V's scales enter P', so the reference covers them (their range is clamped far
         // outside what rows of ordinary size need)
         const float lv = fminf(fmaxf(lg2(vm), -100.0f), 100.0f);
@@ -867,7 +893,8 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
         else if (mode == kCapped && __all_sync(0xFFFFFFFFu, most * rl.fu <= kTanhRange))
           L += tile_probs_any<kNearCap, kBN, kPages>(mask, rl, ts, sc, t0, M);
         else if (mode == kCapped) L += tile_probs_any<kCapped, kBN, kPages>(mask, rl, ts, sc, t0, M);
-        else L += tile_probs_any<kBiased, kBN, kPages>(mask, rl, ts, sc, t0, M);
+        else if (mode == kBiased) L += tile_probs_any<kBiased, kBN, kPages>(mask, rl, ts, sc, t0, M);
+        else L += tile_probs_any<kBoth, kBN, kPages>(mask, rl, ts, sc, t0, M);
       }
       tmem_wait_st();
       tc_fence_before();
