@@ -386,33 +386,6 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_attn_merge_kernel(con
 // Warps of one head (P > 1) merge through shared memory at the end; each head's result
 // (or split partial) is written by its chunk-0 warp.
 // ---------------------------------------------------------------------------------
-template <int D, int kFK, int kFV, int W>
-struct PageStage {
-  static constexpr int kCK = kFK == 3 ? D : D / 2;
-  static constexpr int kCV = kFV == 3 ? D : D / 2;
-  static constexpr int kBK = kFK == 3 ? 0 : D / 16;
-  static constexpr int kBV = kFV == 3 ? 0 : D / 16;
-  static constexpr int kRow = kCK + kCV + kBK + kBV + 8;  // pool bytes per (token, KV head)
-  // a stage: 16 W (token, head) rows of every plane; chunk j's rows start at 16 H j
-  static constexpr int kOffKC = 0;
-  static constexpr int kOffVC = kOffKC + 16 * W * kCK;
-  static constexpr int kOffKB = kOffVC + 16 * W * kCV;
-  static constexpr int kOffVB = kOffKB + 16 * W * kBK;
-  static constexpr int kOffKR = kOffVB + 16 * W * kBV;
-  static constexpr int kOffVR = kOffKR + 16 * W * 4;
-  static constexpr int kBytes = kOffVR + 16 * W * 4;
-  // 2 blocks per SM at W = 8, 1 at W = 16
-  static constexpr int kBudget = W == 8 ? 108 * 1024 : 216 * 1024;
-  static constexpr int kStagesFit = kBudget / kBytes;
-  static constexpr int kStages = kStagesFit > 6 ? 6 : (kStagesFit < 2 ? 2 : kStagesFit);
-  static constexpr int kRing = kStages * kBytes;
-  // end-of-block merge: per consumer warp and lane, O (D/16 m-tiles x 4) + m, l (2 each)
-  static constexpr int kLaneFloats = (D / 16) * 4 + 4;
-  static constexpr int kMerge = W * 32 * kLaneFloats * 4;
-  static constexpr int kOffBar = kRing > kMerge ? kRing : kMerge;
-  static constexpr int kSmem = kOffBar + 2 * kStages * 8 + 16;  // full + empty barriers, the bad flag
-};
-
 // kPg: a plane may be page-scaled (p.k_page / p.v_page); its chunk's H scales are then
 // one 4 H-byte copy (a multiple of 16, H >= 4) that all 16 tokens of the chunk read.
 template <int D, int kFK, int kFV, int W, int H, bool kPg>

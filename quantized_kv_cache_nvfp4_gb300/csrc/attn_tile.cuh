@@ -76,6 +76,12 @@ __device__ __forceinline__ float ex2_ftz(float x) {
   return r;
 }
 
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 __device__ __forceinline__ float rcp_approx(float x) {
   float r;
   asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -213,13 +219,13 @@ struct AttnState {
 
 // One 16-token tile of one KV head into the warp's state: S^T = K Q^T, the softmax
 // update, O^T += V^T P'^T.  nvalid = tokens of the tile inside the sequence (16 but on
-// a split's last tile); the rest of the tile may hold anything, NaN codes and scales
-// among it.  qb(nh, kb) gives the Q^T fragment, qmul the per-head query factors (scale,
+// a split's last tile), nfirst those before it (active mods only); the rest of the tile
+// may hold anything, NaN codes and scales among it.  qb(nh, kb) gives the Q^T fragment, qmul the per-head query factors (scale,
 // log2 e, Q's power of two).  An active mod turns the scores (rows 8nh + 2c and + 1,
 // tokens g and g + 8) into base-2 logits with the masked ones at -inf; qmul is then 1.
 template <int D, int kFK, int kFV, int kNH, typename QB, typename Mod>
 __device__ __forceinline__ void attn_tile(const TileView& tv, const QB& qb, const float (&qmul)[kNH][2], int lane,
-                                          int nvalid, AttnState<D, kNH>& st, const Mod& mod) {
+                                          int nvalid, AttnState<D, kNH>& st, const Mod& mod, int nfirst = 0) {
   constexpr int kKS = D / 16;
   constexpr int kMT = D / 16;
   const int g = lane >> 2;
@@ -294,7 +300,10 @@ __device__ __forceinline__ void attn_tile(const TileView& tv, const QB& qb, cons
   const float kr1 = *reinterpret_cast<const float*>(tv.kr + (g + 8) * tv.skr);
   float vr0 = *reinterpret_cast<const float*>(tv.vr + g * tv.svr);
   float vr1 = *reinterpret_cast<const float*>(tv.vr + (g + 8) * tv.svr);
-  const bool dead0 = g >= nvalid, dead1 = g + 8 >= nvalid;  // past the sequence (last tile only)
+  // tokens outside the sequence (a split's first and last tiles only)
+  const bool edge = nvalid < 16 || (Mod::kActive && nfirst > 0);
+  const bool dead0 = g >= nvalid || (Mod::kActive && g < nfirst);
+  const bool dead1 = g + 8 >= nvalid || (Mod::kActive && g + 8 < nfirst);
   // this lane's maxima (two tokens per head) first: the references move when any
   // lane's exceed them, and only then are the tile's maxima reduced across lanes
   float mt[kNH][2];
@@ -307,7 +316,7 @@ __device__ __forceinline__ void attn_tile(const TileView& tv, const QB& qb, cons
     sc[nh][3] *= kr1;
   }
   if constexpr (Mod::kActive) mod(sc);
-  if (nvalid < 16) {  // uniform: the tile ends inside the sequence
+  if (edge) {  // uniform
 #pragma unroll
     for (int nh = 0; nh < kNH; ++nh) {
       if (dead0) sc[nh][0] = sc[nh][1] = kNegInf;
@@ -386,13 +395,14 @@ __device__ __forceinline__ void attn_tile(const TileView& tv, const QB& qb, cons
       lds_words<D / 32>(tv.vc + (ta0 + 1) * tv.sv + g * (D / 8), v1);
       lds_words<D / 32>(tv.vc + ta1 * tv.sv + g * (D / 8), v2);
       lds_words<D / 32>(tv.vc + (ta1 + 1) * tv.sv + g * (D / 8), v3);
-      if (nvalid < 16) {  // 0 * NaN would reach O: tokens past the end decode to 0
+      if (edge) {  // 0 * NaN would reach O: tokens outside decode to 0
+        auto in = [&](int t) { return t < nvalid && (!Mod::kActive || t >= nfirst); };
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-          v0[i] = ta0 < nvalid ? v0[i] : 0u;
-          v1[i] = ta0 + 1 < nvalid ? v1[i] : 0u;
-          v2[i] = ta1 < nvalid ? v2[i] : 0u;
-          v3[i] = ta1 + 1 < nvalid ? v3[i] : 0u;
+          v0[i] = in(ta0) ? v0[i] : 0u;
+          v1[i] = in(ta0 + 1) ? v1[i] : 0u;
+          v2[i] = in(ta1) ? v2[i] : 0u;
+          v3[i] = in(ta1 + 1) ? v3[i] : 0u;
         }
       }
 #pragma unroll
@@ -423,9 +433,10 @@ __device__ __forceinline__ void attn_tile(const TileView& tv, const QB& qb, cons
         const int blk = (g * (D / 8)) / 16 + q;
         bs01[q] = e4m3x2_to_f16x2(vbs[ta0 * tv.sbv + blk] | (vbs[(ta0 + 1) * tv.sbv + blk] << 8));
         bs23[q] = e4m3x2_to_f16x2(vbs[ta1 * tv.sbv + blk] | (vbs[(ta1 + 1) * tv.sbv + blk] << 8));
-        if (nvalid < 16) {  // as above, by the block scales (E2M1 holds no NaN)
-          bs01[q] &= (ta0 < nvalid ? 0x0000FFFFu : 0u) | (ta0 + 1 < nvalid ? 0xFFFF0000u : 0u);
-          bs23[q] &= (ta1 < nvalid ? 0x0000FFFFu : 0u) | (ta1 + 1 < nvalid ? 0xFFFF0000u : 0u);
+        if (edge) {  // as above, by the block scales (E2M1 holds no NaN)
+          auto in = [&](int t) { return t < nvalid && (!Mod::kActive || t >= nfirst); };
+          bs01[q] &= (in(ta0) ? 0x0000FFFFu : 0u) | (in(ta0 + 1) ? 0xFFFF0000u : 0u);
+          bs23[q] &= (in(ta1) ? 0x0000FFFFu : 0u) | (in(ta1 + 1) ? 0xFFFF0000u : 0u);
         }
       }
 #pragma unroll
@@ -453,6 +464,35 @@ __device__ __forceinline__ void attn_tile(const TileView& tv, const QB& qb, cons
       }
     }
   }}
+
+// A stage of the page-major kernels: 16 W (token, head) rows of every plane, and the ring
+// that holds kStages of them.  kNH: head n-tiles of a warp (its share of the merge).
+template <int D, int kFK, int kFV, int W, int kBlocks = (W == 8 ? 2 : 1), int kNH = 1, int kExtra = 0>
+struct PageStage {
+  static constexpr int kCK = kFK == 3 ? D : D / 2;
+  static constexpr int kCV = kFV == 3 ? D : D / 2;
+  static constexpr int kBK = kFK == 3 ? 0 : D / 16;
+  static constexpr int kBV = kFV == 3 ? 0 : D / 16;
+  static constexpr int kRow = kCK + kCV + kBK + kBV + 8;  // pool bytes per (token, KV head)
+  // a stage: 16 W (token, head) rows of every plane; chunk j's rows start at 16 H j
+  static constexpr int kOffKC = 0;
+  static constexpr int kOffVC = kOffKC + 16 * W * kCK;
+  static constexpr int kOffKB = kOffVC + 16 * W * kCV;
+  static constexpr int kOffVB = kOffKB + 16 * W * kBK;
+  static constexpr int kOffKR = kOffVB + 16 * W * kBV;
+  static constexpr int kOffVR = kOffKR + 16 * W * 4;
+  static constexpr int kBytes = kOffVR + 16 * W * 4;
+  // kBlocks blocks per SM; kExtra bytes of a block go to something else
+  static constexpr int kBudget = (kBlocks == 2 ? 108 * 1024 : 216 * 1024) - kExtra;
+  static constexpr int kStagesFit = kBudget / kBytes;
+  static constexpr int kStages = kStagesFit > 6 ? 6 : (kStagesFit < 2 ? 2 : kStagesFit);
+  static constexpr int kRing = kStages * kBytes;
+  // end-of-block merge: per consumer warp and lane, O (D/16 m-tiles x 4) + m, l (2 each), per n-tile
+  static constexpr int kLaneFloats = kNH * ((D / 16) * 4 + 4);
+  static constexpr int kMerge = W * 32 * kLaneFloats * 4;
+  static constexpr int kOffBar = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kSmem = kOffBar + 2 * kStages * 8 + 16;  // full + empty barriers, the bad flag
+};
 
 }  // namespace
 

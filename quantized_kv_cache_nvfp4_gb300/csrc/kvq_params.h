@@ -301,6 +301,10 @@ struct QueryAttnParams {
 size_t query_attn_workspace_bytes(int32_t S, int32_t num_tokens, int32_t H, int32_t Hq, int32_t D,
                                   int32_t max_q, int32_t max_len);
 cudaError_t launch_query_attention(const QueryAttnParams& p, cudaStream_t s);
+// The page-major kernel of few rows; two: 16 rows a block (else 8).
+cudaError_t launch_query_pages_64(const QueryAttnParams& p, bool two, cudaStream_t s);
+cudaError_t launch_query_pages_128(const QueryAttnParams& p, bool two, cudaStream_t s);
+cudaError_t launch_query_pages_256(const QueryAttnParams& p, cudaStream_t s);  // 8
 int query_tile_rows(int32_t D);  // rows a CTA of the tile kernel takes
 cudaError_t launch_query_tiles(const QueryAttnParams& p, cudaStream_t s);
 cudaError_t launch_payload_decode(const UnpackParams& p, int lanes, bool v8, cudaStream_t s);

@@ -17,32 +17,6 @@ namespace kvq {
 
 namespace {
 
-// Logits of a tile's scores: sc[nh][e] belongs to row 8 nh + 2c + (e & 1) and token
-// t0 + g + 8 (e >> 1).
-template <int kNH>
-struct QueryMod {
-  static constexpr bool kActive = true;
-  float fac[kNH][2], slope[kNH][2];
-  int lo[kNH][2], hi[kNH][2], pos[kNH][2];
-  float cap, icap;
-  bool biased;
-  int t;  // token of e = 0, 1
-
-  __device__ __forceinline__ void operator()(float (&sc)[kNH][4]) const {
-#pragma unroll
-    for (int nh = 0; nh < kNH; ++nh)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = e & 1, tt = t + 8 * (e >> 1);
-        float x = sc[nh][e] * fac[nh][r];
-        if (cap > 0.0f) x = cap * tanh_abs(x * icap);
-        if (biased) x = __fmaf_rn(slope[nh][r], static_cast<float>(tt - pos[nh][r]), x);
-        x *= kLog2e;
-        sc[nh][e] = tt >= lo[nh][r] && tt < hi[nh][r] ? x : kNegInf;
-      }
-  }
-};
-
 template <int D, int kFK, int kFV, int kNH>
 __global__ void __launch_bounds__(kAttnThreads) query_rows_kernel(const QueryAttnParams qp) {
   using T = AttnTile<D, kFK, kFV>;
@@ -67,17 +41,8 @@ __global__ void __launch_bounds__(kAttnThreads) query_rows_kernel(const QueryAtt
   const int rows = nq * p.group;
   if (row0 >= rows) return;
 
-  // lane r < kRows: row r's range; the CTA's keys are the union
-  int lo = 0x7FFFFFFF, hi = 0;
-  if (lane < kRows && row0 + lane < rows) {
-    const int i = (row0 + lane) / p.group;
-    int l, u;
-    key_range(qp, s, q0 + i, len - nq + i, len, l, u);
-    if (l < u) {
-      lo = l;
-      hi = u;
-    }
-  }
+  int lo, hi;  // lane r < kRows: row r's range; the CTA's keys are the union
+  lane_range(qp, lane, kRows, s, q0, nq, len, row0, rows, lo, hi);
   const int lo_min = __reduce_min_sync(0xFFFFFFFFu, lo);
   const int hi_max = __reduce_max_sync(0xFFFFFFFFu, hi);
   int t_begin = 0, t_end = 0;
@@ -88,73 +53,23 @@ __global__ void __launch_bounds__(kAttnThreads) query_rows_kernel(const QueryAtt
   }
   const int ntile = (t_end - t_begin + 15) / 16;
 
-  // ---- Q^T fragments, scaled by a power of two into f16, built once by warp 0 ----
+  // ---- Q^T fragments: in registers, or warp 0's in shared memory ----
   uint2* const qfrag = reinterpret_cast<uint2*>(smem);
-  float* const qfac = reinterpret_cast<float*>(smem + kNH * kKS * 32 * 8);
-  if (warp == 0) {
+  uint2 qreg[kQReg ? kNH : 1][kKS];
+  float row_fac[kNH];
 #pragma unroll
-    for (int nh = 0; nh < kNH; ++nh) {
-      const int row = row0 + 8 * nh + g;
-      uint32_t w[D / 8];
+  for (int nh = 0; nh < kNH; ++nh) {
+    uint2(&f)[kKS] = qreg[kQReg ? nh : 0];
+    row_fac[nh] = query_fragments<D>(p, lane, h, q0, row0 + 8 * nh + g, rows, f);
+    if (!kQReg && warp == 0) {
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) w[i] = 0u;
-      if (row < rows) {
-        const int i = row / p.group;
-        const uint16_t* q = p.q + static_cast<int64_t>(q0 + i) * p.q_row_pitch +
-                            static_cast<int64_t>(h * p.group + row - i * p.group) * p.q_head_pitch + c * (D / 4);
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          uint32_t v4[4];
-          load16B(q + 8 * j, v4);
-          w[4 * j] = v4[0];
-          w[4 * j + 1] = v4[1];
-          w[4 * j + 2] = v4[2];
-          w[4 * j + 3] = v4[3];
-        }
-      }
-      float am = 0.0f;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) am = fmaxf(am, fmaxf(fabsf(bf16lo(w[i])), fabsf(bf16hi(w[i]))));
-      am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-      am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-      int k = 0;
-      if (am > 0.0f) k = 14 - (static_cast<int>((__float_as_uint(am) >> 23) & 0xFF) - 127);
-      k = max(-100, min(120, k));
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
-      if (c == 0) qfac[8 * nh + g] = p.scale * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-#pragma unroll
-      for (int kb = 0; kb < kKS; ++kb)
-        qfrag[(nh * kKS + kb) * 32 + lane] = make_uint2(f32x2_to_f16x2(bf16lo(w[2 * kb]) * up, bf16hi(w[2 * kb]) * up),
-                                                        f32x2_to_f16x2(bf16lo(w[2 * kb + 1]) * up, bf16hi(w[2 * kb + 1]) * up));
+      for (int kb = 0; kb < kKS; ++kb) qfrag[(nh * kKS + kb) * 32 + lane] = f[kb];
     }
   }
-  __syncthreads();
+  if (!kQReg) __syncthreads();
   QueryMod<kNH> mod;
-  mod.cap = qp.softcap;
-  mod.icap = qp.softcap > 0.0f ? 1.0f / qp.softcap : 0.0f;
-  mod.biased = qp.slopes != nullptr;
-#pragma unroll
-  for (int nh = 0; nh < kNH; ++nh)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = 8 * nh + 2 * c + e;
-      mod.fac[nh][e] = qfac[r];
-      mod.lo[nh][e] = __shfl_sync(0xFFFFFFFFu, lo, r);
-      mod.hi[nh][e] = __shfl_sync(0xFFFFFFFFu, hi, r);
-      const int row = min(row0 + r, rows - 1), i = row / p.group;
-      mod.pos[nh][e] = len - nq + i;
-      mod.slope[nh][e] = mod.biased ? LDX(qp.slopes + h * p.group + row - i * p.group) : 0.0f;
-    }
-  float one[kNH][2];
-#pragma unroll
-  for (int nh = 0; nh < kNH; ++nh) one[nh][0] = one[nh][1] = 1.0f;
-  uint2 qreg[kQReg ? kNH : 1][kQReg ? kKS : 1];
-  if constexpr (kQReg) {
-#pragma unroll
-    for (int nh = 0; nh < kNH; ++nh)
-#pragma unroll
-      for (int kb = 0; kb < kKS; ++kb) qreg[nh][kb] = qfrag[(nh * kKS + kb) * 32 + lane];
-  }
+  float qmul[kNH][2];
+  mod.init(qp, lane, h, row0, rows, len - nq, lo, hi, row_fac, qmul);
   auto qb = [&](int nh, int kb) -> uint2 {
     if constexpr (kQReg) {
       return qreg[nh][kb];
@@ -228,7 +143,8 @@ __global__ void __launch_bounds__(kAttnThreads) query_rows_kernel(const QueryAtt
     const TileView tv{sb + T::kOffKC, sb + T::kOffVC, sb + T::kOffKB, sb + T::kOffVB, sb + T::kOffKR, sb + T::kOffVR,
                       T::kSK, T::kSV, T::kBK, T::kBV, 4, 4};
     mod.t = t0 + g;
-    attn_tile<D, kFK, kFV, kNH>(tv, qb, one, lane, t_end - t0, st, mod);
+    mod.t0 = t0;
+    attn_tile<D, kFK, kFV, kNH>(tv, qb, qmul, lane, t_end - t0, st, mod);
     __syncwarp();
     issue(row_next, srow_next, (it + T::kStages - 1) % T::kStages);
     cp_async_commit();
@@ -385,10 +301,13 @@ cudaError_t launch_query_merge(const QueryAttnParams& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, query_merge_kernel<D>, p);
 }
 
-template <int D>
-cudaError_t merge_launch(const QueryAttnParams& p, cudaStream_t s) {
+cudaError_t merge_splits(const QueryAttnParams& p, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
-  KVQ_LAUNCH("query_merge_kernel", s, e = launch_query_merge<D>(p, s));
+  if (p.a.nsplit == 1) return e;
+  KVQ_LAUNCH("query_merge_kernel", s,
+             e = p.a.D == 64    ? launch_query_merge<64>(p, s)
+                 : p.a.D == 128 ? launch_query_merge<128>(p, s)
+                                : launch_query_merge<256>(p, s));
   return e;
 }
 
@@ -404,8 +323,7 @@ cudaError_t rows_launch(const QueryAttnParams& p, cudaStream_t s) {
   const int64_t tiles = (static_cast<int64_t>(p.max_q) * p.a.group + 8 * kNH - 1) / (8 * kNH);
   const dim3 grid(static_cast<unsigned>(tiles * p.a.nsplit), p.a.H, p.a.S);
   KVQ_LAUNCH("query_rows_kernel", s, k<<<grid, kAttnThreads, T::kSmem, s>>>(p); e = cudaGetLastError());
-  if (e != cudaSuccess || p.a.nsplit == 1) return e;
-  return merge_launch<D>(p, s);
+  return e;
 }
 
 template <int D, int kNH>
@@ -422,26 +340,9 @@ cudaError_t rows_dispatch(const QueryAttnParams& p, int rows, cudaStream_t s) {
   return rows <= 8 ? rows_dispatch_fmt<D, 1>(p, s) : rows_dispatch_fmt<D, 2>(p, s);
 }
 
-// Which kernel serves a call, and its split count, from sizes alone (the workspace query
-// sees the same ones).  The tile kernel from kTileFrom rows a sequence and KV head on.
-constexpr int kTileFrom = 65;
-
-struct QueryPlan {
-  bool tiles;
-  int nsplit;
-};
-
-QueryPlan query_plan(int32_t S, int32_t H, int32_t D, int32_t max_q, int32_t group, int32_t max_len) {
-  const int64_t rows = static_cast<int64_t>(max_q) * group;
-  if (rows < kTileFrom) {
-    const int64_t tiles = rows <= 8 ? 1 : (rows + 15) / 16;
-    return QueryPlan{false, attn_num_splits(static_cast<int32_t>(S * tiles), H, max_len)};
-  }
-  // one CTA an SM: the split count whose last wave is fullest, at least 512 tokens a split,
-  // at most two waves
-  const int64_t ctas = static_cast<int64_t>(S) * H * ((rows + query_tile_rows(D) - 1) / query_tile_rows(D));
-  const int64_t slots = num_sms();
-  int64_t cap = (max_len + 511) / 512;
+// The split count of ctas blocks over slots resident ones: the count whose last wave is
+// fullest, the smallest on ties, at most `cap` and at most two waves.
+int fill_splits(int64_t ctas, int64_t slots, int64_t cap) {
   if (2 * slots / ctas < cap) cap = 2 * slots / ctas;
   if (cap > 64) cap = 64;
   int best = 1;
@@ -454,7 +355,35 @@ QueryPlan query_plan(int32_t S, int32_t H, int32_t D, int32_t max_q, int32_t gro
       best = static_cast<int>(n);
     }
   }
-  return QueryPlan{true, best};
+  return best;
+}
+
+// Kernels and their split counts.  The tile kernel from 17 rows a sequence and KV head on (its
+// cost hardly grows up to 128 rows; the others take 16 at a time); below, whole pages where
+// the layout allows it, else the rows kernel.
+constexpr int kTileFrom = 17;
+
+bool page_kernel_ok(const AttnParams& a) {
+  return a.block_size % 16 == 0 && (a.H == 1 || a.H == 2 || a.H == 4 || a.H == 8) &&
+         (a.H >= 4 || !(a.k_page || a.v_page));
+}
+
+int tile_splits(int32_t S, int32_t H, int32_t D, int64_t rows, int32_t span) {
+  // one CTA an SM, at least 512 tokens a split
+  const int64_t ctas = static_cast<int64_t>(S) * H * ((rows + query_tile_rows(D) - 1) / query_tile_rows(D));
+  return fill_splits(ctas, num_sms(), (span + 511) / 512);
+}
+bool page_two(int32_t D, int64_t rows) { return rows > 8 && D != 256; }  // 16 rows a block spill at head_dim 256
+int page_splits(int32_t S, int32_t D, int64_t rows, int32_t span) {
+  // two blocks an SM (one with 16 rows or head_dim 256), at least 128 tokens a split
+  const int64_t per = page_two(D, rows) ? 16 : 8;
+  const int64_t slots = static_cast<int64_t>(per == 16 || D == 256 ? 1 : 2) * num_sms();
+  return fill_splits(static_cast<int64_t>(S) * ((rows + per - 1) / per), slots, (span + 127) / 128);
+}
+int row_splits(int32_t S, int32_t H, int64_t rows, int32_t span) {
+  // four CTAs an SM, at least 256 tokens a split
+  const int64_t ctas = static_cast<int64_t>(S) * H * (rows <= 8 ? 1 : (rows + 15) / 16);
+  return fill_splits(ctas, 4ll * num_sms(), (span + 255) / 256);
 }
 
 }  // namespace
@@ -463,7 +392,16 @@ size_t query_attn_workspace_bytes(int32_t S, int32_t num_tokens, int32_t H, int3
                                   int32_t max_len) {
   if (S <= 0 || num_tokens <= 0 || H <= 0 || Hq < H || D <= 0 || max_q <= 0 || max_len <= 0) return 0;
   if (max_q > max_len) max_q = max_len;  // as the call does
-  const int n = query_plan(S, H, D, max_q, Hq / H, max_len).nsplit;
+  // whichever kernel serves the call: the choice also depends on the pool, the splits on the
+  // window, which only lowers them (fill_splits grows with its cap)
+  const int64_t rows = static_cast<int64_t>(max_q) * (Hq / H);
+  int n;
+  if (rows >= kTileFrom) {
+    n = tile_splits(S, H, D, rows, max_len);
+  } else {
+    const int np = page_splits(S, D, rows, max_len), nr = row_splits(S, H, rows, max_len);
+    n = np > nr ? np : nr;
+  }
   if (n <= 1) return 0;
   return static_cast<size_t>(num_tokens) * Hq * n * (D + 2) * sizeof(float);
 }
@@ -471,24 +409,27 @@ size_t query_attn_workspace_bytes(int32_t S, int32_t num_tokens, int32_t H, int3
 cudaError_t launch_query_attention(const QueryAttnParams& p_in, cudaStream_t s) {
   QueryAttnParams p = p_in;
   const int rows = p.max_q * p.a.group;
-  const QueryPlan plan = query_plan(p.a.S, p.a.H, p.a.D, p.max_q, p.a.group, p.a.max_len);
-  p.a.nsplit = plan.nsplit;
-  if (!plan.tiles) {
-    switch (p.a.D) {
-      case 64: return rows_dispatch<64>(p, rows, s);
-      case 128: return rows_dispatch<128>(p, rows, s);
-      case 256: return rows_dispatch<256>(p, rows, s);
+  // tokens that a sequence's rows can see: less than all of them under a window
+  const int64_t seen = static_cast<int64_t>(p.window) + p.max_q;
+  const int32_t span = p.window > 0 && p.prefix == nullptr && seen < p.a.max_len ? static_cast<int32_t>(seen) : p.a.max_len;
+  if (rows < kTileFrom) {
+    cudaError_t e;
+    if (page_kernel_ok(p.a)) {
+      p.a.nsplit = page_splits(p.a.S, p.a.D, rows, span);
+      e = p.a.D == 64    ? launch_query_pages_64(p, page_two(64, rows), s)
+          : p.a.D == 128 ? launch_query_pages_128(p, page_two(128, rows), s)
+                         : launch_query_pages_256(p, s);
+    } else {
+      p.a.nsplit = row_splits(p.a.S, p.a.H, rows, span);
+      e = p.a.D == 64    ? rows_dispatch<64>(p, rows, s)
+          : p.a.D == 128 ? rows_dispatch<128>(p, rows, s)
+                         : rows_dispatch<256>(p, rows, s);
     }
-    return cudaErrorInvalidValue;
+    return e == cudaSuccess ? merge_splits(p, s) : e;
   }
+  p.a.nsplit = tile_splits(p.a.S, p.a.H, p.a.D, rows, span);
   const cudaError_t e = launch_query_tiles(p, s);
-  if (e != cudaSuccess || p.a.nsplit == 1) return e;
-  switch (p.a.D) {
-    case 64: return merge_launch<64>(p, s);
-    case 128: return merge_launch<128>(p, s);
-    case 256: return merge_launch<256>(p, s);
-  }
-  return cudaErrorInvalidValue;
+  return e == cudaSuccess ? merge_splits(p, s) : e;
 }
 
 }  // namespace kvq

@@ -126,11 +126,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float rcp_ftz(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 __device__ __forceinline__ float lg2(float x) {
   float r;
   asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -162,7 +157,7 @@ struct QTile {
   static constexpr int kOffVM = kOffVS + kSlots * kBN * 4;         // [slots] the largest V scale
   static constexpr int kOffRow = kOffVM + 16 * kSlots;             // [slots][kBN] pool rows (int64)
   static constexpr int kOffBar = kOffRow + kSlots * kBN * 8;
-  static constexpr int kNumBars = 4 * kStages + 2 * kSlots + 3 * kNT;
+  static constexpr int kNumBars = 4 * kStages + 2 * kSlots + 3 * kNT + 1;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;          // tensor memory address, key range, flags
   static constexpr int kSmem = kOffMisc + 32 + 1024;               // + alignment of the base
   static_assert(kSmem > 114 * 1024 && kSmem <= 227 * 1024, "one block per SM, since each takes all of tensor memory");
@@ -576,10 +571,12 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
   const int rows = nq * p.group;
   if (row0 >= rows) return;
 
+  const int nt = kNT == 2 && rows - row0 <= 128 ? 1 : kNT;  // row tiles that hold rows
+
   const uint32_t bar0 = sbase + T::kOffBar;
   const uint32_t k_full = bar0, k_empty = k_full + 8 * kStages, v_full = k_empty + 8 * kStages, v_empty = v_full + 8 * kStages;
   const uint32_t sc_full = v_empty + 8 * kStages, sc_empty = sc_full + 8 * T::kSlots, s_full = sc_empty + 8 * T::kSlots;
-  const uint32_t p_ready = s_full + 8 * kNT, o_done = p_ready + 8 * kNT;
+  const uint32_t p_ready = s_full + 8 * kNT, o_done = p_ready + 8 * kNT, q_full = o_done + 8 * kNT;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(k_full + 8 * i, 4);
@@ -589,13 +586,14 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
     }
     for (int i = 0; i < T::kSlots; ++i) {
       mbar_init(sc_full + 8 * i, 1);
-      mbar_init(sc_empty + 8 * i, 4 + T::kSoft);  // the producer and the softmax warps
+      mbar_init(sc_empty + 8 * i, 4 + 4 * nt);  // the producer and the softmax warps
     }
     for (int i = 0; i < kNT; ++i) {
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_ready + 8 * i, 4);
       mbar_init(o_done + 8 * i, 1);
     }
+    mbar_init(q_full, 4 * nt);
     misc->lo = 0x7FFFFFFF;
     misc->hi = 0;
     misc->bad = 0;
@@ -608,22 +606,22 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
     tmem_relinquish();
   }
 
-  // ---- softmax threads: their row's keys, and Q as f16 (scaled by a power of two so that
-  // the row's largest element lies in [2^14, 2^15): exact) ----
+  // ---- softmax threads: the keys that their row sees (lookup and loads of K and V wait for
+  // them, not for Q) ----
   RowLogit rl;
   int row = -1;  // the thread's row within the sequence; -1: none
+  int head = 0;
+  int64_t tok = 0;
   bool sees = false;
-  if (warp < T::kSoft) {
-    const int r = threadIdx.x;  // row of the CTA
-    if (row0 + r < rows) row = row0 + r;
-    rl.lo = 0;
-    rl.hi = 0x7FFFFFFF;  // a thread without a row masks nothing
-    rl.pos = 0;
-    rl.slope = 0.0f;
-    float fac = 0.0f;
-    const uint32_t qs = sbase + (r / 128) * T::kQBytes + (r % 128) * 128;
+  rl.lo = 0;
+  rl.hi = 0x7FFFFFFF;  // a thread without a row masks nothing
+  rl.pos = 0;
+  if (warp < 4 * nt) {
+    if (row0 + static_cast<int>(threadIdx.x) < rows) row = row0 + threadIdx.x;
     if (row >= 0) {
-      const int i = row / p.group, head = h * p.group + row - i * p.group;
+      const int i = row / p.group;
+      head = h * p.group + row - i * p.group;
+      tok = q0 + i;
       rl.pos = len - nq + i;
       int lo, hi;
       key_range(qp, s, q0 + i, rl.pos, len, lo, hi);
@@ -632,45 +630,13 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
         rl.lo = lo;
         rl.hi = hi;
       }
-      if (qp.slopes != nullptr) rl.slope = LDX(qp.slopes + head) * kLog2e;
-      const uint16_t* const q = p.q + static_cast<int64_t>(q0 + i) * p.q_row_pitch + static_cast<int64_t>(head) * p.q_head_pitch;
-      float am = 0.0f;
-#pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
-        uint32_t w[4];
-        load16B(q + 8 * c, w);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) am = max3(am, fabsf(bf16lo(w[j])), fabsf(bf16hi(w[j])));
-      }
-      int k = 0;
-      if (am > 0.0f) k = 14 - (static_cast<int>((__float_as_uint(am) >> 23) & 0xFF) - 127);
-      k = max(-100, min(120, k));
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
-      fac = p.scale * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-#pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
-        uint32_t w[4];
-        load16B(q + 8 * c, w);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = f32x2_to_f16x2(bf16lo(w[j]) * up, bf16hi(w[j]) * up);
-        sts16(qs + (c / 8) * (128 * 128) + (((c % 8) ^ (r & 7)) * 16), w[0], w[1], w[2], w[3]);
-      }
-    } else {
-#pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) sts16(qs + (c / 8) * (128 * 128) + (((c % 8) ^ (r & 7)) * 16), 0u, 0u, 0u, 0u);
     }
-    rl.f = fac * kLog2e;
-    rl.cap = qp.softcap > 0.0f;
-    rl.c2 = qp.softcap * kLog2e;
-    rl.fu = rl.cap ? fac / qp.softcap : 0.0f;
-    rl.fz = rl.cap ? 2.0f * kLog2e / qp.softcap * fac : 0.0f;
     const int lo = __reduce_min_sync(0xFFFFFFFFu, sees ? rl.lo : 0x7FFFFFFF);
     const int hi = __reduce_max_sync(0xFFFFFFFFu, sees ? rl.hi : 0);
     if (lane == 0) {
       atomicMin(&misc->lo, lo);
       atomicMax(&misc->hi, hi);
     }
-    fence_async_smem();
   }
   tc_fence_before();
   __syncthreads();
@@ -770,22 +736,23 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
           tc_mma_ss(leader, tmem + T::kColS + i * kBN, smem_desc(qa, (k / 4) * (128 * 128) + (k % 4) * 32),
                     smem_desc(ka, (k / 4) * (kBN * 128) + (k % 4) * 32), kIdS, k > 0);
         tc_commit(leader, s_full + 8 * i);
-        if (i == kNT - 1) tc_commit(leader, k_empty + 8 * (j % kStages));
+        if (i == nt - 1) tc_commit(leader, k_empty + 8 * (j % kStages));
       };
+      tile_wait(q_full, 0, misc, p.status);
       tile_wait(k_full, 0, misc, p.status);
       tc_fence_after();
-      for (int i = 0; i < kNT; ++i) scores(i, 0);
+      for (int i = 0; i < nt; ++i) scores(i, 0);
       for (int j = 0; j < steps; ++j) {
         const int st = j % kStages;
         tile_wait(v_full + 8 * st, (j / kStages) & 1, misc, p.status);
-        for (int i = 0; i < kNT; ++i) {
+        for (int i = 0; i < nt; ++i) {
           tile_wait(p_ready + 8 * i, j & 1, misc, p.status);
           tc_fence_after();
           const uint32_t va = desc_lo(sbase + T::kOffV + st * T::kKVBytes, kBN * 128);
 #pragma unroll
           for (int k = 0; k < kBN / 16; ++k)
             tc_mma_ts(leader, tmem + T::kColO + i * D, tmem + T::kColS + i * kBN + 8 * k, smem_desc(va, k * 2048), kIdO, j > 0 || k > 0);
-          if (i == kNT - 1) tc_commit(leader, v_empty + 8 * st);
+          if (i == nt - 1) tc_commit(leader, v_empty + 8 * st);
           if (j + 1 < steps) {
             if (i == 0) {
               tile_wait(k_full + 8 * ((j + 1) % kStages), ((j + 1) / kStages) & 1, misc, p.status);
@@ -837,8 +804,57 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
         if (lane == 0) mbar_arrive(sc_empty + 8 * ((j + 1) % T::kSlots));
       }
     }
-  } else {
-    // ---- softmax: one thread a row ----
+  } else if (warp < 4 * nt) {
+    // ---- softmax: one thread a row.  First its row of Q as f16, scaled by a power of two so
+    // that the largest element lies in [2^14, 2^15): exact ----
+    {
+      const int r = threadIdx.x;
+      const uint32_t qs = sbase + (r / 128) * T::kQBytes + (r % 128) * 128;
+      const uint16_t* const q = p.q + tok * p.q_row_pitch + static_cast<int64_t>(head) * p.q_head_pitch;
+      rl.slope = row >= 0 && qp.slopes != nullptr ? LDX(qp.slopes + head) * kLog2e : 0.0f;
+      constexpr int kC = D / 8, kHold = kC < 16 ? kC : 16;  // 16-byte pieces; those in flight at once
+      uint32_t w[kHold][4];
+      auto load = [&](int c0) {
+#pragma unroll
+        for (int c = 0; c < kHold; ++c) {
+          w[c][0] = w[c][1] = w[c][2] = w[c][3] = 0u;
+          if (row >= 0) load16B(q + 8 * (c0 + c), w[c]);
+        }
+      };
+      float am = 0.0f;
+#pragma unroll
+      for (int c0 = 0; c0 < kC; c0 += kHold) {
+        load(c0);
+#pragma unroll
+        for (int c = 0; c < kHold; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) am = max3(am, fabsf(bf16lo(w[c][e])), fabsf(bf16hi(w[c][e])));
+      }
+      int k = 0;
+      if (am > 0.0f) k = 14 - (static_cast<int>((__float_as_uint(am) >> 23) & 0xFF) - 127);
+      k = max(-100, min(120, k));
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+      const float fac = row >= 0 ? p.scale * __uint_as_float(static_cast<uint32_t>(127 - k) << 23) : 0.0f;
+#pragma unroll
+      for (int c0 = 0; c0 < kC; c0 += kHold) {
+        if (kC > kHold) load(c0);
+#pragma unroll
+        for (int c = 0; c < kHold; ++c) {
+          uint32_t f[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e] = f32x2_to_f16x2(bf16lo(w[c][e]) * up, bf16hi(w[c][e]) * up);
+          sts16(qs + ((c0 + c) / 8) * (128 * 128) + ((((c0 + c) % 8) ^ (r & 7)) * 16), f[0], f[1], f[2], f[3]);
+        }
+      }
+      rl.f = fac * kLog2e;
+      rl.cap = qp.softcap > 0.0f;
+      rl.c2 = qp.softcap * kLog2e;
+      rl.fu = rl.cap ? fac / qp.softcap : 0.0f;
+      rl.fz = rl.cap ? 2.0f * kLog2e / qp.softcap * fac : 0.0f;
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    }
     const int i = warp / 4;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + T::kColS + i * kBN, to = tmem + lanes + T::kColO + i * D;
@@ -912,9 +928,6 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const bool bad = *reinterpret_cast<volatile int*>(&misc->bad) != 0;
     if (!sees) L = 0.0f;
-    const int qi = row >= 0 ? row / p.group : 0;
-    const int head = h * p.group + (row >= 0 ? row - qi * p.group : 0);
-    const int64_t tok = q0 + qi;
     uint16_t* const out = p.out + tok * p.o_row_pitch + static_cast<int64_t>(head) * p.o_head_pitch;
     float* const wsr = p.ws + ((tok * p.Hq + head) * p.nsplit + split) * (D + 2);
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
