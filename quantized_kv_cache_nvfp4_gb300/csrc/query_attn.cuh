@@ -32,68 +32,98 @@ __device__ __forceinline__ bool query_range(const QueryAttnParams& p, int s, int
   return true;
 }
 
-// Logits of a tile's scores: sc[nh][e] belongs to row 8 nh + 2c + (e & 1) and token t +
+// Logits of a tile's scores: sc[nh][e] belongs to row 8 nh + 2c + (e & 1) and token t0 + g +
 // 8 (e >> 1).  Without a cap and a bias the scores stay as they are (qmul then carries the
 // row's factor and log2 e); with one of them they become base-2 logits (qmul is 1).  The
-// mask is skipped on tiles that every row of the warp sees whole.
+// mask is skipped on tiles that every row of the block sees whole; what it and the bias need
+// stays in shared memory, since registers are what these kernels run out of.
 template <int kNH>
 struct QueryMod {
   static constexpr bool kActive = true;
-  float fac[kNH][2], slope[kNH][2];
-  int lo[kNH][2], hi[kNH][2], pos[kNH][2];
-  int lo_all, hi_all;  // keys that every row sees
-  float cap, icap;
-  bool biased, linear;
-  int t, t0;  // token of e = 0, 1; first token of the tile
+  // Shared: the rows' key ranges, and for each row of the warp's head {slope log2 e, position}
+  // (a position is exact below 2^24; the bias of farther keys is rounded anyway).
+  struct Tables {
+    int2 range[8 * kNH];
+    float2 bias[16][8 * kNH];
+  };
+  const Tables* tab;
+  int hw;               // the head's place in tab->bias
+  float f[kNH][2];      // the row's factor: times 2 log2 e / cap, else times log2 e
+  int lo_all, hi_all;   // keys that every row sees
+  float c2;             // cap log2 e, 0: no cap
+  bool biased;
+  int t0, g;            // first token of the tile; this lane's tokens are t0 + g and + 8
 
-  // The values of this lane's rows, and qmul.  Row r of the CTA has its lo and hi in lane r
-  // and its factor in row_fac[r / 8] of the four lanes with g = r % 8.
-  __device__ __forceinline__ void init(const QueryAttnParams& qp, int lane, int h, int row0, int rows, int first_pos,
-                                       int lane_lo, int lane_hi, const float (&row_fac)[kNH], float (&qmul)[kNH][2]) {
+  // Fills the tables (a barrier follows): the block's ranges (row r's in lane r) by one warp,
+  // the head's biases by one warp of each head.
+  static __device__ __forceinline__ void fill(Tables* tab, const QueryAttnParams& qp, int lane, int h, int hw, int row0,
+                                              int rows, int first_pos, int lo, int hi, bool ranges, bool biases) {
+    if (lane >= 8 * kNH) return;
+    if (ranges) tab->range[lane] = make_int2(lo, hi);
+    if (biases && qp.slopes != nullptr) {
+      const int row = min(row0 + lane, rows - 1), i = row / qp.a.group;
+      tab->bias[hw][lane] = make_float2(LDX(qp.slopes + h * qp.a.group + row - i * qp.a.group) * kLog2e,
+                                        static_cast<float>(first_pos + i));
+    }
+  }
+  // row_fac[nh]: the factor of row 8 nh + g; lo, hi: the range of row `lane`.
+  __device__ __forceinline__ void init(const Tables* t, const QueryAttnParams& qp, int lane, int head_place, int row0, int rows,
+                                       int lo, int hi, const float (&row_fac)[kNH], float (&qmul)[kNH][2]) {
     const int c = lane & 3;
-    cap = qp.softcap;
-    icap = cap > 0.0f ? 1.0f / cap : 0.0f;
+    tab = t;
+    hw = head_place;
+    g = lane >> 2;
+    c2 = qp.softcap * kLog2e;
     biased = qp.slopes != nullptr;
-    linear = !biased && !(cap > 0.0f);
+    const bool linear = !biased && !(c2 > 0.0f);
+    const float unit = c2 > 0.0f ? 2.0f * kLog2e / qp.softcap : kLog2e;
     const bool live = lane < 8 * kNH && row0 + lane < rows;
-    lo_all = __reduce_max_sync(0xFFFFFFFFu, live ? lane_lo : 0);  // INT_MAX with a row that sees nothing
-    hi_all = __reduce_min_sync(0xFFFFFFFFu, live ? lane_hi : 0x7FFFFFFF);
+    lo_all = __reduce_max_sync(0xFFFFFFFFu, live ? lo : 0);  // INT_MAX with a row that sees nothing
+    hi_all = __reduce_min_sync(0xFFFFFFFFu, live ? hi : 0x7FFFFFFF);
 #pragma unroll
     for (int nh = 0; nh < kNH; ++nh)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = 8 * nh + 2 * c + e;
-        fac[nh][e] = __shfl_sync(0xFFFFFFFFu, row_fac[nh], 4 * (2 * c + e));
-        qmul[nh][e] = linear ? fac[nh][e] * kLog2e : 1.0f;
-        lo[nh][e] = __shfl_sync(0xFFFFFFFFu, lane_lo, r);
-        hi[nh][e] = __shfl_sync(0xFFFFFFFFu, lane_hi, r);
-        const int row = min(row0 + r, rows - 1), i = row / qp.a.group;
-        pos[nh][e] = first_pos + i;
-        slope[nh][e] = biased ? LDX(qp.slopes + h * qp.a.group + row - i * qp.a.group) : 0.0f;
+        f[nh][e] = __shfl_sync(0xFFFFFFFFu, row_fac[nh], 4 * (2 * c + e)) * unit;
+        qmul[nh][e] = linear ? f[nh][e] : 1.0f;
       }
   }
   __device__ __forceinline__ void operator()(float (&sc)[kNH][4]) const {
-    if (!linear) {
+    const int c = threadIdx.x & 3;
+    if (c2 > 0.0f) {
+      // c2 tanh(x) = c2 - 2 c2 / (1 + e^2x): an absolute error of a few 2^-23 of the cap, which
+      // is what a capped logit needs (tanh.approx is off by 2^-11 of it)
 #pragma unroll
       for (int nh = 0; nh < kNH; ++nh)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = sc[nh][e] * fac[nh][e & 1];
-          // tanh(x) = 1 - 2 / (1 + e^2x): an absolute error of a few 2^-23, which is what a
-          // capped logit needs (tanh.approx is off by 2^-11 of the cap)
-          if (cap > 0.0f) x = cap * __fmaf_rn(-2.0f, rcp_ftz(1.0f + ex2_ftz(2.0f * kLog2e * icap * x)), 1.0f);
-          if (biased) x = __fmaf_rn(slope[nh][e & 1], static_cast<float>(t + 8 * (e >> 1) - pos[nh][e & 1]), x);
-          sc[nh][e] = x * kLog2e;
-        }
+        for (int e = 0; e < 4; ++e)
+          sc[nh][e] = __fmaf_rn(-2.0f * c2, rcp_ftz(1.0f + ex2_ftz(sc[nh][e] * f[nh][e & 1])), c2);
+    } else if (biased) {
+#pragma unroll
+      for (int nh = 0; nh < kNH; ++nh)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[nh][e] *= f[nh][e & 1];
+    }
+    if (biased) {
+      const float t[2] = {static_cast<float>(t0 + g), static_cast<float>(t0 + g + 8)};
+#pragma unroll
+      for (int nh = 0; nh < kNH; ++nh) {
+        const float4 b = *reinterpret_cast<const float4*>(&tab->bias[hw][8 * nh + 2 * c]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          sc[nh][e] = __fmaf_rn(e & 1 ? b.z : b.x, t[e >> 1] - (e & 1 ? b.w : b.y), sc[nh][e]);
+      }
     }
     if (t0 < lo_all || t0 + 16 > hi_all) {  // uniform
 #pragma unroll
-      for (int nh = 0; nh < kNH; ++nh)
+      for (int nh = 0; nh < kNH; ++nh) {
+        const int4 q = *reinterpret_cast<const int4*>(&tab->range[8 * nh + 2 * c]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int tt = t + 8 * (e >> 1);
-          if (tt < lo[nh][e & 1] || tt >= hi[nh][e & 1]) sc[nh][e] = kNegInf;
+          const int tt = t0 + g + 8 * (e >> 1);
+          if (tt < (e & 1 ? q.z : q.x) || tt >= (e & 1 ? q.w : q.y)) sc[nh][e] = kNegInf;
         }
+      }
     }
   }
 };

@@ -66,10 +66,12 @@ __global__ void __launch_bounds__(kAttnThreads) query_rows_kernel(const QueryAtt
       for (int kb = 0; kb < kKS; ++kb) qfrag[(nh * kKS + kb) * 32 + lane] = f[kb];
     }
   }
-  if (!kQReg) __syncthreads();
+  __shared__ __align__(16) typename QueryMod<kNH>::Tables tab;
+  QueryMod<kNH>::fill(&tab, qp, lane, h, 0, row0, rows, len - nq, lo, hi, warp == 0, warp == 0);
+  __syncthreads();
   QueryMod<kNH> mod;
   float qmul[kNH][2];
-  mod.init(qp, lane, h, row0, rows, len - nq, lo, hi, row_fac, qmul);
+  mod.init(&tab, qp, lane, 0, row0, rows, lo, hi, row_fac, qmul);
   auto qb = [&](int nh, int kb) -> uint2 {
     if constexpr (kQReg) {
       return qreg[nh][kb];
@@ -142,7 +144,6 @@ __global__ void __launch_bounds__(kAttnThreads) query_rows_kernel(const QueryAtt
     const int t0 = t_begin + (warp + it * kAttnWarps) * 16;
     const TileView tv{sb + T::kOffKC, sb + T::kOffVC, sb + T::kOffKB, sb + T::kOffVB, sb + T::kOffKR, sb + T::kOffVR,
                       T::kSK, T::kSV, T::kBK, T::kBV, 4, 4};
-    mod.t = t0 + g;
     mod.t0 = t0;
     attn_tile<D, kFK, kFV, kNH>(tv, qb, qmul, lane, t_end - t0, st, mod);
     __syncwarp();

@@ -47,6 +47,20 @@ __global__ void __launch_bounds__(32 * (QueryPage<D, kFK, kFV, kNH>::kW + 1), Qu
   const int row0 = tile * kRows;
   const int H = p.H, P = W / H;
 
+  const uint32_t ring_s = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+  const uint32_t full0 = ring_s + T::kOffBar, empty0 = full0 + 8 * T::kStages;
+  int* const bad_flag = reinterpret_cast<int*>(smem + T::kOffBar + 16 * T::kStages);
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int st = 0; st < T::kStages; ++st) {
+      mbar_init(full0 + 8 * st, 1);
+      mbar_init(empty0 + 8 * st, W);
+    }
+    *bad_flag = 0;
+    mbar_init_fence();
+  }
+  __syncthreads();
+
   int q0, nq, len;
   const bool ok = query_range(qp, s, q0, nq, len);
   if (!ok && threadIdx.x == 0 && blockIdx.x == 0) set_status(p.status, 8u);
@@ -64,20 +78,6 @@ __global__ void __launch_bounds__(32 * (QueryPage<D, kFK, kFV, kNH>::kW + 1), Qu
   }
   if (t_begin == hi_max) t_begin &= ~15;  // an empty split
   const int nstage = t_end > t_begin ? (t_end - t_begin + 16 * P - 1) / (16 * P) : 0;
-
-  const uint32_t ring_s = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-  const uint32_t full0 = ring_s + T::kOffBar, empty0 = full0 + 8 * T::kStages;
-  int* const bad_flag = reinterpret_cast<int*>(smem + T::kOffBar + 16 * T::kStages);
-  if (threadIdx.x == 0) {
-#pragma unroll
-    for (int st = 0; st < T::kStages; ++st) {
-      mbar_init(full0 + 8 * st, 1);
-      mbar_init(empty0 + 8 * st, W);
-    }
-    *bad_flag = 0;
-    mbar_init_fence();
-  }
-  __syncthreads();
 
   if (warp == W) {
     // ---- producer: lane j < P resolves chunk j of each stage, its table entry loaded a stage
@@ -149,10 +149,12 @@ __global__ void __launch_bounds__(32 * (QueryPage<D, kFK, kFV, kNH>::kW + 1), Qu
       for (int kb = 0; kb < kKS; ++kb) qfrag[(nh * kKS + kb) * 32 + lane] = f[kb];
     }
   }
-  if (!kQReg) asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
+  __shared__ __align__(16) typename QueryMod<kNH>::Tables tab;
+  QueryMod<kNH>::fill(&tab, qp, lane, h, h, row0, rows, len - nq, lo, hi, warp == 0, j == 0);
+  asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
   QueryMod<kNH> mod;
   float qmul[kNH][2];
-  mod.init(qp, lane, h, row0, rows, len - nq, lo, hi, row_fac, qmul);
+  mod.init(&tab, qp, lane, h, row0, rows, lo, hi, row_fac, qmul);
   auto qb = [&](int nh, int kb) -> uint2 {
     if constexpr (kQReg) {
       return qreg[nh][kb];
@@ -174,7 +176,6 @@ __global__ void __launch_bounds__(32 * (QueryPage<D, kFK, kFV, kNH>::kW + 1), Qu
       const TileView tv{sb + T::kOffKC + r * T::kCK, sb + T::kOffVC + r * T::kCV, sb + T::kOffKB + r * T::kBK,
                         sb + T::kOffVB + r * T::kBV, sb + T::kOffKR + r * 4, sb + T::kOffVR + r * 4,
                         H * T::kCK, H * T::kCV, H * T::kBK, H * T::kBV, p.k_page ? 0 : H * 4, p.v_page ? 0 : H * 4};
-      mod.t = t0 + g;
       mod.t0 = t0;
       attn_tile<D, kFK, kFV, kNH>(tv, qb, qmul, lane, t_end - t0, st, mod, lo_min - t0);
     }
