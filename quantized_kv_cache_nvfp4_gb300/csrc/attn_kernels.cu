@@ -841,6 +841,17 @@ int attn_page_splits(int32_t S, int32_t H, int32_t max_seq_len) {
   return best;
 }
 
+// Splits of a page-scaled pool's calls: 2 blocks an SM (1 at H = 16 or head_dim 256), at least
+// 64 tokens a split, so that short sequences spread over the GPU too.  One where whole pages
+// cannot serve the call.  At most two waves, 4 SMs x 64 query heads x 130 (or 2 SMs x 128 x 130,
+// SMs x 128 x 258) partials of 4 bytes: 20.2 MB on 152 SMs.
+int attn_page_scaled_splits(int32_t S, int32_t H, int32_t Hq, int32_t D, int32_t max_seq_len) {
+  const bool ok = D == 256 ? (H == 4 || H == 8) : (H == 4 || H == 8 || H == 16) && Hq / H <= 8;
+  if (!ok || S <= 0 || max_seq_len <= 0) return 1;
+  const int64_t ctas = static_cast<int64_t>(S) * (D == 256 && Hq / H > 8 ? 2 : 1);
+  return fill_splits(ctas, static_cast<int64_t>(H == 16 || D == 256 ? 1 : 2) * num_sms(), max_seq_len, 64, 384);
+}
+
 // Tokens per split: the splits cover max_seq_len in multiples of `unit` tokens.
 static int attn_split_len(int32_t max_seq_len, int nsplit, int unit) {
   const int64_t per = (static_cast<int64_t>(max_seq_len) + nsplit - 1) / nsplit;
@@ -854,14 +865,28 @@ size_t attn_workspace_bytes(int32_t S, int32_t H, int32_t Hq, int32_t D, int32_t
   int n = attn_num_splits(S, H, max_seq_len);
   const int np = attn_page_splits(S, H, max_seq_len);
   if (np > n) n = np;
+  const int ns = attn_page_scaled_splits(S, H, Hq, D, max_seq_len);
+  if (ns > n) n = ns;
   if (n <= 1) return 0;
   return static_cast<size_t>(S) * Hq * n * (D + 2) * sizeof(float);
 }
 
 cudaError_t launch_decode_attention(const AttnParams& p_in, cudaStream_t s) {
   AttnParams p = p_in;
+  if ((p.k_page || p.v_page) && p.D == 256 && p.block_size % 16 == 0 && (p.H == 4 || p.H == 8)) {
+    // head_dim 256: the whole-page kernel of kvq_attention, one query token a sequence (2 x 65536
+    // tokens, H4: 91 us by the head-major kernel below)
+    QueryAttnParams q{};
+    q.a = p;
+    q.a.nsplit = attn_page_scaled_splits(p.S, p.H, p.Hq, p.D, p.max_len);
+    q.num_tokens = p.S;
+    q.max_q = 1;
+    const cudaError_t e = launch_query_pages_256(q, s);
+    return e == cudaSuccess ? launch_query_merge_splits(q, s) : e;
+  }
   if (attn_page_ok(p.block_size, p.H, p.D, p.group, p.k_page || p.v_page)) {
-    p.nsplit = attn_page_splits(p.S, p.H, p.max_len);
+    p.nsplit = p.k_page || p.v_page ? attn_page_scaled_splits(p.S, p.H, p.Hq, p.D, p.max_len)
+                                    : attn_page_splits(p.S, p.H, p.max_len);
     p.split_len = attn_split_len(p.max_len, p.nsplit, 16);
     switch (p.D) {
       case 64: return page_dispatch<64>(p, s);

@@ -289,7 +289,8 @@ size_t attn_builtin_scratch_bytes();
 // ---------------------------------------------------------------------------
 struct QueryAttnParams {
   AttnParams a;              // q / out rows are tokens; max_len, nsplit, ws as above
-  const int32_t* starts;     // [S + 1]: tokens of sequence s are starts[s] .. starts[s + 1] - 1
+  const int32_t* starts;     // [S + 1]: tokens of sequence s are starts[s] .. starts[s + 1] - 1;
+                             // nullptr: token s is sequence s's only one
   int32_t num_tokens;        // rows of q and out
   int32_t max_q;             // most query tokens of a sequence
   float softcap;             // 0: none
@@ -301,6 +302,12 @@ struct QueryAttnParams {
 size_t query_attn_workspace_bytes(int32_t S, int32_t num_tokens, int32_t H, int32_t Hq, int32_t D,
                                   int32_t max_q, int32_t max_len);
 cudaError_t launch_query_attention(const QueryAttnParams& p, cudaStream_t s);
+cudaError_t launch_query_merge_splits(const QueryAttnParams& p, cudaStream_t s);  // of a.nsplit > 1
+// The split count of ctas blocks over slots resident ones, for splits of `tokens`: the count
+// that fills one wave best with at least min_one tokens a split (the smallest on ties); two
+// waves, with at least min_two, where they are fuller by 8% (a second wave costs more starts and
+// a larger merge).
+int fill_splits(int64_t ctas, int64_t slots, int32_t tokens, int32_t min_one, int32_t min_two);
 // The page-major kernel of few rows; two: 16 rows a block (else 8).
 cudaError_t launch_query_pages_64(const QueryAttnParams& p, bool two, cudaStream_t s);
 cudaError_t launch_query_pages_128(const QueryAttnParams& p, bool two, cudaStream_t s);

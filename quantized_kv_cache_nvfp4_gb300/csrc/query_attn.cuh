@@ -20,12 +20,18 @@ __device__ __forceinline__ void key_range(const QueryAttnParams& p, int s, int t
 }
 
 // First query token and number of query tokens of sequence s; false where they do not fit
-// the arrays or the sequence.
+// the arrays or the sequence.  Without starts (decode) token s is sequence s's only one.
 __device__ __forceinline__ bool query_range(const QueryAttnParams& p, int s, int& q0, int& n, int& len) {
-  q0 = LDX(p.starts + s);
-  const int q1 = LDX(p.starts + s + 1);
   len = LDX(p.a.seq_lens + s);
   n = 0;
+  if (p.starts == nullptr) {
+    q0 = s;
+    if (len < 0 || len > p.a.seq_cap) return false;
+    n = 1;
+    return true;
+  }
+  q0 = LDX(p.starts + s);
+  const int q1 = LDX(p.starts + s + 1);
   if (q0 < 0 || q1 < q0 || q1 > p.num_tokens || q1 - q0 > p.max_q || len < 0 || len > p.a.seq_cap || q1 - q0 > len)
     return false;
   n = q1 - q0;

@@ -11,6 +11,8 @@
 // 16-token tiles in turn through cp.async rings, with the tile arithmetic of the decode
 // kernels (attn_tile.cuh), the score modifier between its two products.  Splits of a
 // sequence merge through the caller's workspace in a second small kernel.
+#include <algorithm>
+
 #include "query_attn.cuh"
 
 namespace kvq {
@@ -228,6 +230,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) query_merge_kernel(const Que
   const bool live = row < static_cast<int64_t>(qp.num_tokens) * p.Hq;
   const int tok = live ? static_cast<int>(row / p.Hq) : 0, qh = static_cast<int>(row - static_cast<int64_t>(tok) * p.Hq);
   int lo = 0, hi = p.S;  // the last s < S with starts[s] <= tok lies in [lo, hi)
+  if (qp.starts == nullptr) lo = hi = tok;
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32;
     const int at = lo + lane * step;
@@ -302,16 +305,6 @@ cudaError_t launch_query_merge(const QueryAttnParams& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, query_merge_kernel<D>, p);
 }
 
-cudaError_t merge_splits(const QueryAttnParams& p, cudaStream_t s) {
-  cudaError_t e = cudaSuccess;
-  if (p.a.nsplit == 1) return e;
-  KVQ_LAUNCH("query_merge_kernel", s,
-             e = p.a.D == 64    ? launch_query_merge<64>(p, s)
-                 : p.a.D == 128 ? launch_query_merge<128>(p, s)
-                                : launch_query_merge<256>(p, s));
-  return e;
-}
-
 template <int D, int kFK, int kFV, int kNH>
 cudaError_t rows_launch(const QueryAttnParams& p, cudaStream_t s) {
   using T = AttnTile<D, kFK, kFV>;
@@ -341,24 +334,6 @@ cudaError_t rows_dispatch(const QueryAttnParams& p, int rows, cudaStream_t s) {
   return rows <= 8 ? rows_dispatch_fmt<D, 1>(p, s) : rows_dispatch_fmt<D, 2>(p, s);
 }
 
-// The split count of ctas blocks over slots resident ones: the count whose last wave is
-// fullest, the smallest on ties, at most `cap` and at most two waves.
-int fill_splits(int64_t ctas, int64_t slots, int64_t cap) {
-  if (2 * slots / ctas < cap) cap = 2 * slots / ctas;
-  if (cap > 64) cap = 64;
-  int best = 1;
-  double best_fill = 0.0;
-  for (int64_t n = 1; n <= cap; ++n) {
-    const int64_t waves = (ctas * n + slots - 1) / slots;
-    const double fill = static_cast<double>(ctas * n) / static_cast<double>(waves * slots);
-    if (fill > best_fill + 0.01) {
-      best_fill = fill;
-      best = static_cast<int>(n);
-    }
-  }
-  return best;
-}
-
 // Kernels and their split counts.  The tile kernel from 17 rows a sequence and KV head on (its
 // cost hardly grows up to 128 rows; the others take 16 at a time); below, whole pages where
 // the layout allows it, else the rows kernel.
@@ -372,29 +347,57 @@ bool page_kernel_ok(const AttnParams& a) {
 int tile_splits(int32_t S, int32_t H, int32_t D, int64_t rows, int32_t span) {
   // one CTA an SM, at least 512 tokens a split
   const int64_t ctas = static_cast<int64_t>(S) * H * ((rows + query_tile_rows(D) - 1) / query_tile_rows(D));
-  return fill_splits(ctas, num_sms(), (span + 511) / 512);
+  return fill_splits(ctas, num_sms(), span, 512, 512);
 }
 bool page_two(int32_t D, int64_t rows) { return rows > 8 && D != 256; }  // 16 rows a block spill at head_dim 256
 int page_splits(int32_t S, int32_t D, int64_t rows, int32_t span) {
-  // two blocks an SM (one with 16 rows or head_dim 256), at least 128 tokens a split
+  // two blocks an SM (one with 16 rows or head_dim 256)
   const int64_t per = page_two(D, rows) ? 16 : 8;
   const int64_t slots = static_cast<int64_t>(per == 16 || D == 256 ? 1 : 2) * num_sms();
-  return fill_splits(static_cast<int64_t>(S) * ((rows + per - 1) / per), slots, (span + 127) / 128);
+  return fill_splits(static_cast<int64_t>(S) * ((rows + per - 1) / per), slots, span, 64, 384);
 }
 int row_splits(int32_t S, int32_t H, int64_t rows, int32_t span) {
-  // four CTAs an SM, at least 256 tokens a split
+  // four CTAs an SM
   const int64_t ctas = static_cast<int64_t>(S) * H * (rows <= 8 ? 1 : (rows + 15) / 16);
-  return fill_splits(ctas, 4ll * num_sms(), (span + 255) / 256);
+  return fill_splits(ctas, 4ll * num_sms(), span, 256, 256);
 }
 
 }  // namespace
+
+int fill_splits(int64_t ctas, int64_t slots, int32_t tokens, int32_t min_one, int32_t min_two) {
+  auto most = [&](int64_t waves, int32_t least) {
+    int64_t cap = (static_cast<int64_t>(tokens) + least - 1) / least;
+    if (waves * slots / ctas < cap) cap = waves * slots / ctas;
+    return cap > 256 ? int64_t{256} : cap;
+  };
+  auto fill = [&](int64_t n) {
+    const int64_t waves = (ctas * n + slots - 1) / slots;
+    return static_cast<double>(ctas * n) / static_cast<double>(waves * slots);
+  };
+  int64_t best = 1;
+  for (int64_t n = 2; n <= most(1, min_one); ++n)
+    if (fill(n) > 1.01 * fill(best)) best = n;
+  int64_t two = best;
+  for (int64_t n = best + 1; n <= most(2, min_two); ++n)
+    if (fill(n) > 1.01 * fill(two)) two = n;
+  return static_cast<int>(fill(two) > 1.08 * fill(best) ? two : best);
+}
+
+cudaError_t launch_query_merge_splits(const QueryAttnParams& p, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  if (p.a.nsplit == 1) return e;
+  KVQ_LAUNCH("query_merge_kernel", s,
+             e = p.a.D == 64    ? launch_query_merge<64>(p, s)
+                 : p.a.D == 128 ? launch_query_merge<128>(p, s)
+                                : launch_query_merge<256>(p, s));
+  return e;
+}
 
 size_t query_attn_workspace_bytes(int32_t S, int32_t num_tokens, int32_t H, int32_t Hq, int32_t D, int32_t max_q,
                                   int32_t max_len) {
   if (S <= 0 || num_tokens <= 0 || H <= 0 || Hq < H || D <= 0 || max_q <= 0 || max_len <= 0) return 0;
   if (max_q > max_len) max_q = max_len;  // as the call does
-  // whichever kernel serves the call: the choice also depends on the pool, the splits on the
-  // window, which only lowers them (fill_splits grows with its cap)
+  // whichever kernel serves the call: the choice also depends on the pool
   const int64_t rows = static_cast<int64_t>(max_q) * (Hq / H);
   int n;
   if (rows >= kTileFrom) {
@@ -410,27 +413,28 @@ size_t query_attn_workspace_bytes(int32_t S, int32_t num_tokens, int32_t H, int3
 cudaError_t launch_query_attention(const QueryAttnParams& p_in, cudaStream_t s) {
   QueryAttnParams p = p_in;
   const int rows = p.max_q * p.a.group;
-  // tokens that a sequence's rows can see: less than all of them under a window
+  // tokens that a sequence's rows can see: less than all of them under a window (never more
+  // splits than the workspace query counted, which knows the window not)
   const int64_t seen = static_cast<int64_t>(p.window) + p.max_q;
   const int32_t span = p.window > 0 && p.prefix == nullptr && seen < p.a.max_len ? static_cast<int32_t>(seen) : p.a.max_len;
   if (rows < kTileFrom) {
     cudaError_t e;
     if (page_kernel_ok(p.a)) {
-      p.a.nsplit = page_splits(p.a.S, p.a.D, rows, span);
+      p.a.nsplit = std::min(page_splits(p.a.S, p.a.D, rows, span), page_splits(p.a.S, p.a.D, rows, p.a.max_len));
       e = p.a.D == 64    ? launch_query_pages_64(p, page_two(64, rows), s)
           : p.a.D == 128 ? launch_query_pages_128(p, page_two(128, rows), s)
                          : launch_query_pages_256(p, s);
     } else {
-      p.a.nsplit = row_splits(p.a.S, p.a.H, rows, span);
+      p.a.nsplit = std::min(row_splits(p.a.S, p.a.H, rows, span), row_splits(p.a.S, p.a.H, rows, p.a.max_len));
       e = p.a.D == 64    ? rows_dispatch<64>(p, rows, s)
           : p.a.D == 128 ? rows_dispatch<128>(p, rows, s)
                          : rows_dispatch<256>(p, rows, s);
     }
-    return e == cudaSuccess ? merge_splits(p, s) : e;
+    return e == cudaSuccess ? launch_query_merge_splits(p, s) : e;
   }
-  p.a.nsplit = tile_splits(p.a.S, p.a.H, p.a.D, rows, span);
+  p.a.nsplit = std::min(tile_splits(p.a.S, p.a.H, p.a.D, rows, span), tile_splits(p.a.S, p.a.H, p.a.D, rows, p.a.max_len));
   const cudaError_t e = launch_query_tiles(p, s);
-  return e == cudaSuccess ? merge_splits(p, s) : e;
+  return e == cudaSuccess ? launch_query_merge_splits(p, s) : e;
 }
 
 }  // namespace kvq

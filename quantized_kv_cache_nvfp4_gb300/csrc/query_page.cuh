@@ -76,7 +76,6 @@ __global__ void __launch_bounds__(32 * (QueryPage<D, kFK, kFV, kNH>::kW + 1), Qu
     t_begin = static_cast<int>(min(static_cast<int64_t>(first) + static_cast<int64_t>(split) * per, static_cast<int64_t>(hi_max)));
     t_end = min(t_begin + per, hi_max);
   }
-  if (t_begin == hi_max) t_begin &= ~15;  // an empty split
   const int nstage = t_end > t_begin ? (t_end - t_begin + 16 * P - 1) / (16 * P) : 0;
 
   if (warp == W) {
