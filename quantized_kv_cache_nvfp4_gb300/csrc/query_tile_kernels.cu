@@ -81,6 +81,26 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
       : "r"(taddr)
       : "memory");
 }
+// 64 columns: half as many waits for tensor memory as 32 at a time.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&v)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,"
+      "%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,"
+      "%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, "
+      "[%64];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+        "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+        "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]),
+        "=r"(v[32]), "=r"(v[33]), "=r"(v[34]), "=r"(v[35]), "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]),
+        "=r"(v[40]), "=r"(v[41]), "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]),
+        "=r"(v[48]), "=r"(v[49]), "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]),
+        "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63])
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -380,26 +400,35 @@ __device__ __forceinline__ float tile_max_pages(const RowLogit& r, uint32_t tadd
   float best = kNegInf;
   most = 0.0f;
 #pragma unroll 1
-  for (int c0 = 0; c0 < kBN; c0 += 32) {
-    uint32_t v[32];
-    tmem_ld32(taddr + c0, v);
+  for (int c0 = 0; c0 < kBN; c0 += 64) {
+    uint32_t v[64];
+    tmem_ld64(taddr + c0, v);
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
+    for (int g = 0; g < 4; ++g) {
       const float ks = gs[c0 / 16 + g].x;
       float m[2] = {kNegInf, kNegInf}, a = 0.0f;
       const uint64_t f2 = dup_f32x2(r.f * ks);
       const uint64_t base = dup_f32x2(r.slope * (tf + static_cast<float>(c0 + 16 * g)));
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < 16; i += 2) {
         const int col = c0 + 16 * g + i;
-        if (kMode == kBiased && i % 2 == 0)
-          unpack_f32x2(fma_f32x2(pack_f32x2(v[16 * g + i], v[16 * g + i + 1]), f2, bias2(s2, i, base)), v[16 * g + i],
-                       v[16 * g + i + 1]);
-        float x = __uint_as_float(v[16 * g + i]);
-        if (kMode == kCapped) a = fmaxf(a, fabsf(x));
-        if (kMode == kBoth) x = logit<kMode>(r, x * ks, tf, col);
-        if (kMask) x = col >= lo && col < hi ? x : kNegInf;
-        m[i % 2] = fmaxf(m[i % 2], x);
+        float x0 = __uint_as_float(v[16 * g + i]), x1 = __uint_as_float(v[16 * g + i + 1]);
+        if (kMode == kBiased) {
+          uint32_t b0, b1;
+          unpack_f32x2(fma_f32x2(pack_f32x2(v[16 * g + i], v[16 * g + i + 1]), f2, bias2(s2, i, base)), b0, b1);
+          x0 = __uint_as_float(b0);
+          x1 = __uint_as_float(b1);
+        }
+        if (kMode == kCapped) a = max3(a, fabsf(x0), fabsf(x1));
+        if (kMode == kBoth) {
+          x0 = logit<kMode>(r, x0 * ks, tf, col);
+          x1 = logit<kMode>(r, x1 * ks, tf, col + 1);
+        }
+        if (kMask) {
+          x0 = col >= lo && col < hi ? x0 : kNegInf;
+          x1 = col + 1 >= lo && col + 1 < hi ? x1 : kNegInf;
+        }
+        m[i / 2 % 2] = max3(m[i / 2 % 2], x0, x1);
       }
       const float mg = fmaxf(m[0], m[1]);
       if (kMode == kCapped) most = fmaxf(most, a * ks);
@@ -419,11 +448,11 @@ __device__ __forceinline__ float tile_probs_pages(const RowLogit& r, uint32_t ta
   const uint64_t s2 = dup_f32x2(r.slope);
   float L = 0.0f;
 #pragma unroll 1
-  for (int c0 = 0; c0 < kBN; c0 += 32) {
-    uint32_t v[32], h[16];
-    tmem_ld32(taddr + c0, v);
+  for (int c0 = 0; c0 < kBN; c0 += 64) {
+    uint32_t v[64], h[32];
+    tmem_ld64(taddr + c0, v);
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
+    for (int g = 0; g < 4; ++g) {
       const float2 s = gs[c0 / 16 + g];
       const float ref = s.y - M;
       const uint64_t f2 = dup_f32x2((kMode == kNearCap ? r.fu : kMode == kCapped ? r.fz : r.f) * s.x);
@@ -457,7 +486,7 @@ __device__ __forceinline__ float tile_probs_pages(const RowLogit& r, uint32_t ta
       unpack_f32x2(add_f32x2(l[0], l[1]), a, b);
       L = __fmaf_rn(__uint_as_float(a) + __uint_as_float(b), ex2_ftz(-s.y), L);
     }
-    tmem_st16(taddr + c0 / 2, h);  // columns whose scores are already read
+    tmem_st32(taddr + c0 / 2, h);  // columns whose scores are already read
   }
   return L;
 }
@@ -484,21 +513,36 @@ __device__ __forceinline__ float tile_probs_any(bool mask, const RowLogit& r, ui
 }
 
 // ---- producers: one tensor's rows of a step ------------------------------------------
-// 128 threads; thread i takes 16-byte pieces of the code rows, kPer pieces of kPieces a row.
+// 128 threads; a thread takes the same 16-byte piece of kPer code rows, kRowStep rows apart.
+// Eight threads that store together hold the pieces of one 64-dim panel in as many
+// neighbouring rows as make their swizzled chunks cover all banks (FP8: 4 pieces of two
+// chunks, 2 rows; NVFP4: 2 pieces of four chunks, 4 rows).  kRowStep is a multiple of 8, so a
+// thread's swizzle is the same for all its rows and its addresses differ by constants.
 template <int D, int kFmt>
 struct TileLoad {
   static constexpr int kBN = QTile<D>::kBN;
   static constexpr int kCB = kFmt == 3 ? D : D / 2;     // code bytes per row
   static constexpr int kPieces = kCB / 16;              // per row
   static constexpr int kPer = kBN * kPieces / 128;      // per thread
+  static constexpr int kRowStep = 128 / kPieces;
+  static constexpr int kPanelPieces = kFmt == 3 ? 4 : 2;  // pieces of a 64-dim panel
+  static constexpr int kRowsTogether = 8 / kPanelPieces;
+  static constexpr int kPanels = kPieces / kPanelPieces;
+  static_assert(kRowStep % 8 == 0, "the swizzle repeats every 8 rows");
   uint32_t w[kPer][4];
   uint32_t bs[kFmt == 3 ? 1 : kPer];                    // NVFP4: the piece's two block scales
 
+  static __device__ __forceinline__ int piece(int tid) { return tid % kPanelPieces; }  // within the panel
+  static __device__ __forceinline__ int panel(int tid) { return tid / 8 % kPanels; }
+  static __device__ __forceinline__ int row0(int tid) {
+    return tid / (8 * kPanels) * kRowsTogether + tid / kPanelPieces % kRowsTogether;
+  }
   __device__ __forceinline__ void load(const AttnPlane& pl, const int64_t* rows, int tid) {
-    const int c = tid % kPieces;
+    const int c = panel(tid) * kPanelPieces + piece(tid);
+    const int64_t* const mine = rows + row0(tid);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int64_t row = rows[(i * 128 + tid) / kPieces];
+      const int64_t row = mine[i * kRowStep];
       w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;
       if constexpr (kFmt != 3) bs[i] = 0u;
       if (row >= 0) {
@@ -509,36 +553,32 @@ struct TileLoad {
   }
   // f16 values into the swizzled tile at shared address dst: panels of 64 dims, [kBN][128 B]
   __device__ __forceinline__ void store(uint32_t dst, int tid) const {
-    const int c = tid % kPieces;
+    const int r = row0(tid);
+    const uint32_t base = dst + panel(tid) * (kBN * 128) + r * 128;
+    constexpr int kChunks = 8 / kPanelPieces;  // of a piece
+    uint32_t at[kChunks];
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j) at[j] = base + (((kChunks * piece(tid) + j) ^ (r & 7)) * 16);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int r = (i * 128 + tid) / kPieces;
+      const uint32_t down = i * kRowStep * 128;
       if constexpr (kFmt == 3) {  // 16 dims: two 16-byte chunks
-        uint32_t h[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t h2[2];
-          e4m3x4_to_f16x2(w[i][j], h2);
-          h[2 * j] = h2[0];
-          h[2 * j + 1] = h2[1];
+        for (int j = 0; j < 2; ++j) {
+          uint32_t h0[2], h1[2];
+          e4m3x4_to_f16x2(w[i][2 * j], h0);
+          e4m3x4_to_f16x2(w[i][2 * j + 1], h1);
+          sts16(at[j] + down, h0[0], h0[1], h1[0], h1[1]);
         }
-        const uint32_t base = dst + (c / 4) * (kBN * 128) + r * 128;
-        const uint32_t ch = 2 * (c % 4);
-        // odd panels store their second chunk first: eight lanes then cover all banks
-        const bool sw = (c / 4) & 1;
-        const uint32_t a0 = base + (((ch + (sw ? 1 : 0)) ^ (r & 7)) * 16), a1 = base + (((ch + (sw ? 0 : 1)) ^ (r & 7)) * 16);
-        sts16(a0, sw ? h[4] : h[0], sw ? h[5] : h[1], sw ? h[6] : h[2], sw ? h[7] : h[3]);
-        sts16(a1, sw ? h[0] : h[4], sw ? h[1] : h[5], sw ? h[2] : h[6], sw ? h[3] : h[7]);
       } else {  // 32 dims: four chunks, two block scales
         const uint32_t two = e4m3x2_to_f16x2(bs[i]);
         const uint32_t s0 = __byte_perm(two, 0u, 0x1010), s1 = __byte_perm(two, 0u, 0x3232);
-        const uint32_t base = dst + (c / 2) * (kBN * 128) + r * 128;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint32_t h[4];
           e2m1x8_to_f16x2(w[i][j], h);
           const uint32_t s = j < 2 ? s0 : s1;
-          sts16(base + (((4 * (c % 2) + j) ^ (r & 7)) * 16), hmul2(h[0], s), hmul2(h[1], s), hmul2(h[2], s), hmul2(h[3], s));
+          sts16(at[j] + down, hmul2(h[0], s), hmul2(h[1], s), hmul2(h[2], s), hmul2(h[3], s));
         }
       }
     }
