@@ -101,6 +101,11 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&v)[64]) {
       : "r"(taddr)
       : "memory");
 }
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[N]) {
+  if constexpr (N == 64) tmem_ld64(taddr, v);
+  else tmem_ld32(taddr, v);
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -119,6 +124,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[N]) {
+  if constexpr (N == 32) tmem_st32(taddr, v);
+  else tmem_st16(taddr, v);
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -177,7 +187,7 @@ struct QTile {
   static constexpr int kOffVM = kOffVS + kSlots * kBN * 4;         // [slots] the largest V scale
   static constexpr int kOffRow = kOffVM + 16 * kSlots;             // [slots][kBN] pool rows (int64)
   static constexpr int kOffBar = kOffRow + kSlots * kBN * 8;
-  static constexpr int kNumBars = 4 * kStages + 2 * kSlots + 3 * kNT + 1;
+  static constexpr int kNumBars = 4 * kStages + 2 * kSlots + 4 * kNT + 1;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;          // tensor memory address, key range, flags
   static constexpr int kSmem = kOffMisc + 32 + 1024;               // + alignment of the base
   static_assert(kSmem > 114 * 1024 && kSmem <= 227 * 1024, "one block per SM, since each takes all of tensor memory");
@@ -238,6 +248,17 @@ __device__ __forceinline__ float logit(const RowLogit& r, float x, float tf, int
   }
   if (kMode == kBoth) y = __fmaf_rn(r.slope, tf + static_cast<float>(col), y);
   return y;
+}
+
+// The first half of a step's P' is in tensor memory: its products may begin while the second
+// half is computed.  Not where the planes are page-scaled and a step has 128 columns: those
+// take 64 columns at a time, and one hand-over is faster then (624 against 639 us on 4096
+// queries in 12288 tokens at head_dim 128; at 256, 845 against 929 us the other way).
+__device__ __forceinline__ void half_ready(uint32_t bar) {
+  tmem_wait_st();
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 // y - M + add for a pair of scores x in kPlain (f2 the factor), kCapped (f2 = 2 log2 e / cap
@@ -332,7 +353,7 @@ __device__ __forceinline__ float tile_max(const RowLogit& r, uint32_t taddr, con
 // P' of a tile's row over the first half of its score columns; returns the row sum of p.
 template <int kMode, bool kMask, int kBN>
 __device__ __forceinline__ float tile_probs(const RowLogit& r, uint32_t taddr, const float* ks, const float* vs, int t0,
-                                            float M) {
+                                            float M, uint32_t half) {
   const int lo = r.lo - t0, hi = r.hi - t0;
   const float tf = static_cast<float>(t0 - r.pos);
   const uint64_t f2 = dup_f32x2(kMode == kNearCap ? r.fu : kMode == kCapped ? r.fz : r.f), s2 = dup_f32x2(r.slope);
@@ -381,6 +402,7 @@ __device__ __forceinline__ float tile_probs(const RowLogit& r, uint32_t taddr, c
       h[i / 2 + 1] = f32x2_to_f16x2(__uint_as_float(q[2]), __uint_as_float(q[3]));
     }
     tmem_st16(taddr + c0 / 2, h);  // columns whose scores are already read
+    if (c0 + 32 == kBN / 2) half_ready(half);
   }
   uint32_t a, b, c, d;
   unpack_f32x2(l0, a, b);
@@ -394,17 +416,18 @@ __device__ __forceinline__ float tile_probs(const RowLogit& r, uint32_t taddr, c
 // the group's sum of P' is divided by vs for l.
 template <int kMode, bool kMask, int kBN>
 __device__ __forceinline__ float tile_max_pages(const RowLogit& r, uint32_t taddr, const float2* gs, int t0, float& most) {
+  constexpr int kCols = kBN == 128 ? 64 : 32;  // at a time
   const int lo = r.lo - t0, hi = r.hi - t0;
   const float tf = static_cast<float>(t0 - r.pos);
   const uint64_t s2 = dup_f32x2(r.slope);
   float best = kNegInf;
   most = 0.0f;
 #pragma unroll 1
-  for (int c0 = 0; c0 < kBN; c0 += 64) {
-    uint32_t v[64];
-    tmem_ld64(taddr + c0, v);
+  for (int c0 = 0; c0 < kBN; c0 += kCols) {
+    uint32_t v[kCols];
+    tmem_ld(taddr + c0, v);
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < kCols / 16; ++g) {
       const float ks = gs[c0 / 16 + g].x;
       float m[2] = {kNegInf, kNegInf}, a = 0.0f;
       const uint64_t f2 = dup_f32x2(r.f * ks);
@@ -440,7 +463,8 @@ __device__ __forceinline__ float tile_max_pages(const RowLogit& r, uint32_t tadd
 }
 
 template <int kMode, bool kMask, int kBN>
-__device__ __forceinline__ float tile_probs_pages(const RowLogit& r, uint32_t taddr, const float2* gs, int t0, float M) {
+__device__ __forceinline__ float tile_probs_pages(const RowLogit& r, uint32_t taddr, const float2* gs, int t0, float M, uint32_t half) {
+  constexpr int kCols = kBN == 128 ? 64 : 32;  // at a time
   const int lo = r.lo - t0, hi = r.hi - t0;
   const float tf = static_cast<float>(t0 - r.pos);
   CapPairs cp;
@@ -448,11 +472,11 @@ __device__ __forceinline__ float tile_probs_pages(const RowLogit& r, uint32_t ta
   const uint64_t s2 = dup_f32x2(r.slope);
   float L = 0.0f;
 #pragma unroll 1
-  for (int c0 = 0; c0 < kBN; c0 += 64) {
-    uint32_t v[64], h[32];
-    tmem_ld64(taddr + c0, v);
+  for (int c0 = 0; c0 < kBN; c0 += kCols) {
+    uint32_t v[kCols], h[kCols / 2];
+    tmem_ld(taddr + c0, v);
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < kCols / 16; ++g) {
       const float2 s = gs[c0 / 16 + g];
       const float ref = s.y - M;
       const uint64_t f2 = dup_f32x2((kMode == kNearCap ? r.fu : kMode == kCapped ? r.fz : r.f) * s.x);
@@ -486,7 +510,8 @@ __device__ __forceinline__ float tile_probs_pages(const RowLogit& r, uint32_t ta
       unpack_f32x2(add_f32x2(l[0], l[1]), a, b);
       L = __fmaf_rn(__uint_as_float(a) + __uint_as_float(b), ex2_ftz(-s.y), L);
     }
-    tmem_st32(taddr + c0 / 2, h);  // columns whose scores are already read
+    tmem_st(taddr + c0 / 2, h);  // columns whose scores are already read
+    if (kBN == 64 && c0 == 0) half_ready(half);
   }
   return L;
 }
@@ -505,11 +530,11 @@ __device__ __forceinline__ float tile_max_any(bool mask, const RowLogit& r, uint
     return mask ? tile_max<kMode, true, kBN>(r, ta, sc.ks, t0, most) : tile_max<kMode, false, kBN>(r, ta, sc.ks, t0, most);
 }
 template <int kMode, int kBN, bool kPages>
-__device__ __forceinline__ float tile_probs_any(bool mask, const RowLogit& r, uint32_t ta, const StepScales& sc, int t0, float M) {
+__device__ __forceinline__ float tile_probs_any(bool mask, const RowLogit& r, uint32_t ta, const StepScales& sc, int t0, float M, uint32_t half) {
   if constexpr (kPages)
-    return mask ? tile_probs_pages<kMode, true, kBN>(r, ta, sc.gs, t0, M) : tile_probs_pages<kMode, false, kBN>(r, ta, sc.gs, t0, M);
+    return mask ? tile_probs_pages<kMode, true, kBN>(r, ta, sc.gs, t0, M, half) : tile_probs_pages<kMode, false, kBN>(r, ta, sc.gs, t0, M, half);
   else
-    return mask ? tile_probs<kMode, true, kBN>(r, ta, sc.ks, sc.vs, t0, M) : tile_probs<kMode, false, kBN>(r, ta, sc.ks, sc.vs, t0, M);
+    return mask ? tile_probs<kMode, true, kBN>(r, ta, sc.ks, sc.vs, t0, M, half) : tile_probs<kMode, false, kBN>(r, ta, sc.ks, sc.vs, t0, M, half);
 }
 
 // ---- producers: one tensor's rows of a step ------------------------------------------
@@ -590,6 +615,7 @@ template <int D, int kFK, int kFV, bool kPages>
 __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const QueryAttnParams qp) {
   using T = QTile<D>;
   constexpr int kBN = T::kBN, kNT = T::kNT, kStages = T::kStages;
+  constexpr bool kHalves = !(kPages && kBN == 128);
   const AttnParams& p = qp.a;
   extern __shared__ unsigned char tile_smem_raw[];
   const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(tile_smem_raw));
@@ -617,6 +643,7 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
   const uint32_t k_full = bar0, k_empty = k_full + 8 * kStages, v_full = k_empty + 8 * kStages, v_empty = v_full + 8 * kStages;
   const uint32_t sc_full = v_empty + 8 * kStages, sc_empty = sc_full + 8 * T::kSlots, s_full = sc_empty + 8 * T::kSlots;
   const uint32_t p_ready = s_full + 8 * kNT, o_done = p_ready + 8 * kNT, q_full = o_done + 8 * kNT;
+  const uint32_t p_half = q_full + 8;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(k_full + 8 * i, 4);
@@ -631,6 +658,7 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
     for (int i = 0; i < kNT; ++i) {
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_ready + 8 * i, 4);
+      mbar_init(p_half + 8 * i, 4);
       mbar_init(o_done + 8 * i, 1);
     }
     mbar_init(q_full, 4 * nt);
@@ -786,11 +814,18 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
         const int st = j % kStages;
         tile_wait(v_full + 8 * st, (j / kStages) & 1, misc, p.status);
         for (int i = 0; i < nt; ++i) {
-          tile_wait(p_ready + 8 * i, j & 1, misc, p.status);
-          tc_fence_after();
           const uint32_t va = desc_lo(sbase + T::kOffV + st * T::kKVBytes, kBN * 128);
+          tile_wait((kHalves ? p_half : p_ready) + 8 * i, j & 1, misc, p.status);
+          tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < kBN / 16; ++k)
+          for (int k = 0; k < kBN / 32; ++k)
+            tc_mma_ts(leader, tmem + T::kColO + i * D, tmem + T::kColS + i * kBN + 8 * k, smem_desc(va, k * 2048), kIdO, j > 0 || k > 0);
+          if constexpr (kHalves) {
+            tile_wait(p_ready + 8 * i, j & 1, misc, p.status);
+            tc_fence_after();
+          }
+#pragma unroll
+          for (int k = kBN / 32; k < kBN / 16; ++k)
             tc_mma_ts(leader, tmem + T::kColO + i * D, tmem + T::kColS + i * kBN + 8 * k, smem_desc(va, k * 2048), kIdO, j > 0 || k > 0);
           if (i == nt - 1) tc_commit(leader, v_empty + 8 * st);
           if (j + 1 < steps) {
@@ -919,6 +954,7 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
         for (int e = 0; e < 16; ++e) z[e] = 0u;
 #pragma unroll
         for (int c = 0; c < kBN / 2; c += 16) tmem_st16(ts + c, z);
+        if (kHalves) half_ready(p_half + 8 * i);
       } else {
         float mx, most;
         if (mode == kPlain) mx = tile_max_any<kPlain, kBN, kPages>(mask, rl, ts, sc, t0, most);
@@ -945,12 +981,12 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
             }
           }
         }
-        if (mode == kPlain) L += tile_probs_any<kPlain, kBN, kPages>(mask, rl, ts, sc, t0, M);
+        if (mode == kPlain) L += tile_probs_any<kPlain, kBN, kPages>(mask, rl, ts, sc, t0, M, p_half + 8 * i);
         else if (mode == kCapped && __all_sync(0xFFFFFFFFu, most * rl.fu <= kTanhRange))
-          L += tile_probs_any<kNearCap, kBN, kPages>(mask, rl, ts, sc, t0, M);
-        else if (mode == kCapped) L += tile_probs_any<kCapped, kBN, kPages>(mask, rl, ts, sc, t0, M);
-        else if (mode == kBiased) L += tile_probs_any<kBiased, kBN, kPages>(mask, rl, ts, sc, t0, M);
-        else L += tile_probs_any<kBoth, kBN, kPages>(mask, rl, ts, sc, t0, M);
+          L += tile_probs_any<kNearCap, kBN, kPages>(mask, rl, ts, sc, t0, M, p_half + 8 * i);
+        else if (mode == kCapped) L += tile_probs_any<kCapped, kBN, kPages>(mask, rl, ts, sc, t0, M, p_half + 8 * i);
+        else if (mode == kBiased) L += tile_probs_any<kBiased, kBN, kPages>(mask, rl, ts, sc, t0, M, p_half + 8 * i);
+        else L += tile_probs_any<kBoth, kBN, kPages>(mask, rl, ts, sc, t0, M, p_half + 8 * i);
       }
       tmem_wait_st();
       tc_fence_before();
