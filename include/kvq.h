@@ -322,7 +322,7 @@ KVQ_API size_t kvq_decode_attention_workspace(int32_t num_seqs, int32_t num_head
 
 /* Options of kvq_attention; a zero field is off. */
 typedef struct {
-  float softcap;               /* logits become softcap * tanh(logit / softcap); >= 0, finite */
+  float softcap;               /* logits become softcap * tanh(logit / softcap); 0, or 2^-10 to 2^10 */
   const float* alibi_slopes;   /* device f32 [num_q_heads]: slope * (key position - query position) is added
                                   to the (capped) logit; finite */
   int32_t window;              /* a query at position p sees keys t > p - window only; >= 0 */
@@ -343,8 +343,9 @@ typedef struct {
  * With lo = max(0, p + 1 - window, key_starts[row]) and hi = max(p + 1, prefix), row and
  * query head qh (KV head qh / (num_q_heads / pool->num_heads)) get
  *   softmax over t in [lo, hi) of  cap(scale * q . k_t) + slope * (t - p),  times v_t;
- * a row that sees no key gets zeros.  K and V rows that no row of a call sees are never
- * used, whatever they hold.
+ * a row that sees no key gets zeros.  Cache rows outside the span of the keys that a
+ * sequence's rows see (unwritten rows behind it, left padding before it) are never used,
+ * whatever they hold.
  *   q, out        bf16 [num_tokens][num_q_heads][head_dim] through their own pitches.
  *   max_query_len at least the largest n (at most max_seq_len is used).
  *   head_dim 64, 128 or 256; at most 16 query heads per KV head; scale positive, finite.
@@ -353,7 +354,8 @@ typedef struct {
  *                 NULL when that is 0); caller-owned.  Calls that may overlap on the GPU, and
  *                 graphs that may replay at the same time, need one each.
  * Accuracy as kvq_decode_attention (one f16 rounding of P, one bf16 rounding of out; products,
- * maxima and sums in fp32); the cap is within 2^-20 of softcap absolutely.
+ * maxima and sums in fp32), for V scales between 2^-100 and 2^100; the cap is within 2^-20 of
+ * softcap absolutely.  Waits are bounded as there (KVQ_DEV_TIMEOUT).
  * A sequence whose length is outside [0, min(max_seq_len, max_blocks * block_size)], or whose
  * query rows are outside [0, num_tokens], more than max_query_len or more than its length,
  * keeps its rows of out (KVQ_DEV_BAD_SEQLEN); rows that need a block entry outside the pool

@@ -909,6 +909,8 @@ KVQ_API kvq_status kvq_attention(const kvq_pool* pool, const int32_t* block_tabl
   if (!(o.softcap >= 0.0f && o.softcap <= 3.4028235e38f))
     return fail(KVQ_ERR_INVALID_ARG, "softcap must be 0 or positive and finite (got %g)",
                 static_cast<double>(o.softcap));
+  if (o.softcap > 0.0f && (o.softcap < 0x1p-10f || o.softcap > 0x1p+10f))
+    return fail(KVQ_ERR_UNSUPPORTED, "softcap outside 2^-10 .. 2^10 (got %g)", static_cast<double>(o.softcap));
   if (o.window < 0) return fail(KVQ_ERR_INVALID_ARG, "negative window");
   if (num_seqs > 65535 || H > 65535) return fail(KVQ_ERR_UNSUPPORTED, "num_seqs and num_heads must be <= 65535");
   if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return KVQ_OK;

@@ -309,7 +309,7 @@ template <int D, int kFK, int kFV, int kNH>
 cudaError_t rows_launch(const QueryAttnParams& p, cudaStream_t s) {
   using T = AttnTile<D, kFK, kFV>;
   auto k = query_rows_kernel<D, kFK, kFV, kNH>;
-  if (T::kSmem > 48 * 1024) {
+  if (T::kSmem + sizeof(typename QueryMod<kNH>::Tables) > 48 * 1024) {  // what needs no opt-in
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
     if (e != cudaSuccess) return e;
   }

@@ -516,6 +516,10 @@ __device__ __forceinline__ float tile_probs_pages(const RowLogit& r, uint32_t ta
   return L;
 }
 
+// log2 of a step's largest V scale as the reference takes it, clamped far outside what rows of
+// ordinary size need.
+__device__ __forceinline__ float scale_log2(float v) { return fminf(fmaxf(lg2(v), -100.0f), 100.0f); }
+
 // Where a step's scales are: K's and V's by token, or the groups' pairs.
 struct StepScales {
   const float *ks, *vs;
@@ -768,23 +772,25 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
       if (j >= T::kSlots) tile_wait(sc_empty + 8 * slot, ((j / T::kSlots) - 1) & 1, misc, p.status);
       float m = 0.0f;
 #pragma unroll
+      for (int i = 0; i < kPer; ++i) m = fmaxf(m, vs[i]);
+      m = group_max<32>(m);
+#pragma unroll
       for (int i = 0; i < kPer; ++i) {
         rowbuf[slot * kBN + 32 * i + lane] = row[i];
         if constexpr (kPages) {
           // a group's scales are those of any of its tokens (the others hold the same, or 0
-          // outside the keys); a V scale of 0 becomes the least normal number, so that l
-          // counts the page's probabilities
-          const float kg = group_max<16>(ks[i]), vg = fmaxf(group_max<16>(vs[i]), 0x1p-126f);
-          if (lane % 16 == 0) gsb[slot * (kBN / 16) + 2 * i + lane / 16] = make_float2(kg, lg2(vg));
+          // outside the keys).  A V scale below 2^-60 of the step's largest (0 among them) counts
+          // as that much: its P' is 0 in f16 either way, and l keeps its probabilities
+          const float kg = group_max<16>(ks[i]), vg = group_max<16>(vs[i]);
+          if (lane % 16 == 0)
+            gsb[slot * (kBN / 16) + 2 * i + lane / 16] = make_float2(kg, fmaxf(lg2(fmaxf(vg, 0x1p-126f)), scale_log2(m) - 60.0f));
         } else {
           ksb[slot * kBN + 32 * i + lane] = ks[i];
           vsb[slot * kBN + 32 * i + lane] = vs[i];
         }
-        m = fmaxf(m, vs[i]);
       }
       scales(j + 1);  // nothing past t_end is read
       entries(j + 2);
-      m = group_max<32>(m);
       if (lane == 0) vmb[4 * slot] = m;
       __syncwarp();
       if (lane == 0) mbar_arrive(sc_full + 8 * slot);
@@ -961,9 +967,8 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
         else if (mode == kCapped) mx = tile_max_any<kCapped, kBN, kPages>(mask, rl, ts, sc, t0, most);
         else if (mode == kBiased) mx = tile_max_any<kBiased, kBN, kPages>(mask, rl, ts, sc, t0, most);
         else mx = tile_max_any<kBoth, kBN, kPages>(mask, rl, ts, sc, t0, most);
-        // V's scales enter P', so the reference covers them (their range is clamped far
-        // outside what rows of ordinary size need)
-        const float lv = fminf(fmaxf(lg2(vm), -100.0f), 100.0f);
+        // V's scales enter P', so the reference covers them
+        const float lv = scale_log2(vm);
         const bool move = mx + lv > M + 8.0f;
         if (__any_sync(0xFFFFFFFFu, move)) {
           const float Mn = move ? mx + lv : M;

@@ -47,10 +47,10 @@ def _store_both(pool, k, v, slots):
 
 
 @pytest.mark.parametrize("D", [16, 48, 64, 128, 256, 512])
-@pytest.mark.parametrize("bs", [1, 7, 16, 64])
+@pytest.mark.parametrize("bs", [1, 7, 16, 64, 200])
 def test_prompt_then_steps(D, bs):
     """A prompt, then single tokens whose growing values rescale the page they land in."""
-    H, T, nb = 3, 100, 30
+    H, T, nb = 3, 300 if bs == 200 else 100, 30
     pool = kvq.KvPool.empty(nb * bs * (8 if bs == 1 else 1), H, D, bs, fill=0xFF, fmt=PG)
     table = np.random.RandomState(D).permutation(pool.num_slots // bs)
     slot = lambda p: int(table[p // bs]) * bs + p % bs
@@ -79,6 +79,44 @@ def test_ragged_requests_of_many_pages(tokens):
     qkv = synth.normal_bf16((T, 3 * H, D), 3, synth.STREAM_K)
     assert _store_both(pool, qkv[:, H:2 * H], _rows(T, H, D, 4), slots) == 0
     assert _store_both(pool, None, _rows(T, H, D, 5, 100.0), slots) == 0
+
+
+def test_rows_on_16_byte_boundaries():
+    """Views whose rows start 16 bytes past a 32-byte boundary."""
+    H, D, bs, T = 2, 64, 16, 40
+    pool = kvq.KvPool.empty(4 * bs, H, D, bs, fill=0, fmt=PG)
+    wide = synth.normal_bf16((T, H, D + 8), 6, synth.STREAM_K).to(DEV)
+    want = _host(pool)
+    kvq.kvq_quant_scatter(wide[:, :, 8:], wide[:, :, :D], torch.arange(5, 5 + T, device=DEV), pool)
+    torch.cuda.synchronize()
+    x = wide.cpu().double().numpy()
+    R.page_store(want[0], want[1], x[:, :, 8:], np.arange(5, 5 + T), bs)
+    R.page_store(want[2], want[3], x[:, :, :D], np.arange(5, 5 + T), bs)
+    for a, b in zip(_host(pool), want):
+        np.testing.assert_array_equal(a.view(np.uint8), b.view(np.uint8))
+
+
+def test_scatter_under_graph_capture_appends_on_every_replay():
+    H, D, bs = 2, 128, 16
+    pool = kvq.KvPool.empty(2 * bs, H, D, bs, fill=0, fmt=PG)
+    want = _host(pool)
+    x = torch.zeros((1, H, D), dtype=torch.bfloat16, device=DEV)
+    slot = torch.zeros(1, dtype=torch.int64, device=DEV)
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        kvq.kvq_quant_scatter(x, x, slot, pool)
+    for t in range(20):
+        row = _rows(1, H, D, t, 1.5 ** t)
+        x.copy_(row)
+        slot.fill_(t)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for j in (0, 2):
+            R.page_store(want[j], want[j + 1], row.double().numpy(), np.array([t]), bs)
+    for a, b in zip(_host(pool), want):
+        np.testing.assert_array_equal(a.view(np.uint8), b.view(np.uint8))
 
 
 def test_extreme_values_and_scales():
@@ -174,7 +212,8 @@ def _decode_case(lens, H, group, D, bs, fmt_k, fmt_v, seed):
 
 @pytest.mark.parametrize("fmt_k,fmt_v", [(PG, PG), (PG, NV), (F8, PG), (F8, F8), (NV, NV)])
 @pytest.mark.parametrize("H,group,D,bs", [(8, 4, 128, 16), (4, 8, 64, 32), (16, 1, 128, 16), (2, 4, 128, 16),
-                                          (3, 7, 64, 16), (2, 12, 256, 16), (8, 4, 128, 24)])
+                                          (3, 7, 64, 16), (2, 12, 256, 16), (8, 4, 128, 24),
+                                          (4, 3, 256, 16), (8, 16, 256, 32)])
 def test_decode_attention_over_pages_with_rubbish_behind_the_sequences(fmt_k, fmt_v, H, group, D, bs):
     """Both decode kernels (and their splits); whatever lies behind a sequence's last token,
     NaN codes and scales here, must not reach its output."""
@@ -206,3 +245,82 @@ def test_decode_attention_over_pages_with_rubbish_behind_the_sequences(fmt_k, fm
         bound = 2.0 ** -8 * np.abs(ref[s]) + 2.0 ** -10 * vmax[:, None]
         err = np.abs(got[s] - ref[s])
         assert (err <= bound).all(), (s, np.max(err / bound))
+
+
+@pytest.mark.parametrize("H,D", [(8, 128), (4, 256), (2, 64)])
+def test_decode_bad_sequences_keep_their_rows(H, D):
+    lens = [300, 40, 17]
+    pool, table, lt, q, v, Tmax = _decode_case(lens, H, 2, D, 16, PG, PG, 3)
+    scale = D ** -0.5
+    call = lambda t, n, o, st: kvq.kvq_decode_attention(pool, t.to(DEV), n.to(DEV), Tmax, q.to(DEV), scale, o, dev_status=st)
+    good = poison_bf16(tuple(q.shape))
+    call(table, lt, good, None)
+    for bad_len in (-1, 10 ** 6):
+        n, out, st = lt.clone(), poison_bf16(tuple(q.shape)), status_word()
+        n[1] = bad_len
+        call(table, n, out, st)
+        assert int(st.item()) == kvq.DEV_BAD_SEQLEN and (out[1].contiguous().view(torch.uint8) == 0xA5).all()
+        assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
+    t, out, st = table.clone(), poison_bf16(tuple(q.shape)), status_word()
+    t[1, 1] = -7
+    call(t, lt, out, st)
+    assert int(st.item()) == kvq.DEV_BAD_BLOCK and (out[1].contiguous().view(torch.uint8) == 0xA5).all()
+    assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
+
+
+@pytest.mark.parametrize("H,D", [(8, 128), (4, 256)])
+def test_decode_without_a_workspace_and_in_a_graph(H, D):
+    lens = [2000, 3, 900]
+    pool, table, lt, q, v, Tmax = _decode_case(lens, H, 4, D, 16, PG, PG, 5)
+    table, lt, q = table.to(DEV), lt.to(DEV), q.to(DEV)
+    a, b, c = (torch.zeros_like(q) for _ in range(3))
+    kvq.kvq_decode_attention(pool, table, lt, Tmax, q, 0.1, a)
+    kvq.kvq_decode_attention_noalloc(pool, table, lt, Tmax, q, 0.1, b)
+    ws = torch.empty(kvq.kvq_decode_attention_workspace(3, H, 4 * H, D, Tmax), dtype=torch.uint8, device=DEV)
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        kvq.kvq_decode_attention(pool, table, lt, Tmax, q, 0.1, c, ws)
+    for _ in range(3):
+        c.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, b) and torch.equal(a, c)
+
+
+def test_nothing_to_attend():
+    pool = kvq.KvPool.empty(64, 8, 128, 16, fill=0, fmt=PG)
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, device=DEV)
+    q = torch.ones((3, 8, 128), dtype=torch.bfloat16, device=DEV)
+    out = poison_bf16((3, 8, 128))
+    kvq.kvq_decode_attention(pool, z(3, 2), z(3), 0, q, 0.1, out)
+    assert (out == 0).all()
+    kvq.kvq_decode_attention(pool, z(0, 2), z(0), 32, q[:0], 0.1, out[:0])
+
+
+def test_cache_past_4_gib():
+    """Codes at byte offsets above 2^32: store, restore, decode and prompt attention there give
+    what the same rows give at the pool's start."""
+    H, D, bs, T = 8, 128, 16, 200
+    nb = (5 << 30) // (bs * H * D)
+    pool = kvq.KvPool.empty(nb * bs, H, D, bs, fmt=PG)
+    k, v = _rows(T, H, D, 1).to(DEV), _rows(T, H, D, 2).to(DEV)
+    q = synth.normal_bf16((T, 2 * H, D), 3, 9).to(DEV)
+    lens = torch.tensor([T], dtype=torch.int32, device=DEV)
+    got = []
+    for first in (0, nb - 13):
+        table = torch.arange(first, first + 13, dtype=torch.int32, device=DEV).view(1, 13)
+        p = torch.arange(T, device=DEV)
+        st = status_word()
+        kvq.kvq_quant_scatter(k, v, table[0, p // bs].long() * bs + p % bs, pool, st)
+        ko, vo = (torch.zeros((1, T, H, D), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        kvq.kvq_restore(pool, table, lens, T, ko, vo, st)
+        one, few, many = (torch.zeros((n, 2 * H, D), dtype=torch.bfloat16, device=DEV) for n in (1, 4, T))
+        kvq.kvq_decode_attention(pool, table, lens, T, q[:1], 0.1, one, dev_status=st)
+        for n, o in ((4, few), (T, many)):
+            starts = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+            kvq.kvq_attention(pool, table, lens, T, q[:n], starts, n, 0.1, o, dev_status=st)
+        assert int(st.item()) == 0
+        got.append((ko, vo, one, few, many))
+    for a, b in zip(*got):
+        assert torch.equal(a, b) and a.abs().sum() > 0

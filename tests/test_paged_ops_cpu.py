@@ -83,6 +83,9 @@ def test_attention_refusals(kvq_lib_path):
     for cap in (-1.0, float("inf"), float("nan")):
         st, why = call(opt=_abi.AttnOptions(cap, None, 0, None, None))
         assert st == 1 and b"softcap" in why
+    for cap in (2.0 ** -11, 2000.0):
+        st, why = call(opt=_abi.AttnOptions(cap, None, 0, None, None))
+        assert st == 2 and b"softcap" in why
     st, why = call(opt=_abi.AttnOptions(0.0, None, -1, None, None))
     assert st == 1 and b"window" in why
     assert call(qq=None)[0] == 1

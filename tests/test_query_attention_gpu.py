@@ -228,6 +228,43 @@ def test_pitches_and_views():
     assert torch.equal(o2[:c.starts[-1]], ref[:c.starts[-1]])
 
 
+@pytest.mark.parametrize("new", [1, 3, 120])
+@pytest.mark.parametrize("q_scale,cap", [(1.0, 50.0), (1.0, 2.0), (6.0, 8.0), (30.0, 1.0)])
+def test_cap_from_nearly_linear_to_saturated(new, q_scale, cap):
+    """Scores far below the cap, around 3/4 of it (where the tile kernel changes its tanh) and far
+    above it."""
+    for f in (PG, NV):
+        c = Case([333], [new], 2, 4, 128, fmt_k=f, seed=12)
+        c.q = (c.q.float() * q_scale).to(torch.bfloat16)
+        out, st = c.run(softcap=cap)
+        assert st == 0
+        c.check(out, softcap=cap)
+
+
+def test_stored_scales_that_are_no_powers_of_two_and_zero_pages():
+    for new in (1, 90):
+        c = Case([150], [new], 2, 4, 128, seed=13)
+        for t in (c.pool.k_rscale, c.pool.v_rscale):
+            t.mul_(1.37)
+        first = int(c.table[0, 0])
+        c.pool.v_rscale[first] = 0.0  # a page of zeros that still takes its part of the sum
+        c.pool.k_rscale[int(c.table[0, 3])] = 0.0
+        out, st = c.run()
+        assert st == 0
+        c.check(out)
+
+
+@pytest.mark.parametrize("bs,H", [(16, 8), (16, 1), (8, 8), (64, 4)])
+@pytest.mark.parametrize("new", [1, 5])
+def test_few_rows_by_pages_and_by_rows(bs, H, new):
+    for fmts in ((PG, PG), (F8, NV), (NV, F8), (NV, NV)):
+        c = Case([70, 1000, new, 0], [new, new, new, 0], H, 2, 128, bs, *fmts, seed=14)
+        for opts in ({}, {"window": 90}, {"slopes": np.linspace(0.01, 0.5, 2 * H).astype(np.float32)}):
+            out, st = c.run(**opts)
+            assert st == 0
+            c.check(out, **opts)
+
+
 def test_large_values():
     """Scores and rows far from 1: scales near the ends of what V's scales allow."""
     for f in (PG, F8, NV):
