@@ -700,6 +700,13 @@ cudaError_t page_launch(const AttnParams& p, cudaStream_t s) {
   const dim3 grid(p.nsplit, 1, p.S);
   KVQ_LAUNCH("decode_attn_page_kernel", s, k<<<grid, (W + 1) * 32, T::kSmem, s>>>(p); e = cudaGetLastError());
   if (e != cudaSuccess || p.nsplit == 1) return e;
+  if constexpr (kPg) {  // page-scaled calls split further: the merge that shares splits among warps
+    QueryAttnParams q{};
+    q.a = p;
+    q.num_tokens = p.S;
+    q.max_q = 1;
+    return launch_query_merge_splits(q, s);
+  }
   KVQ_LAUNCH("decode_attn_merge_kernel", s, e = launch_merge<D>(p, s));
   return e;
 }

@@ -303,10 +303,10 @@ size_t query_attn_workspace_bytes(int32_t S, int32_t num_tokens, int32_t H, int3
                                   int32_t max_q, int32_t max_len);
 cudaError_t launch_query_attention(const QueryAttnParams& p, cudaStream_t s);
 cudaError_t launch_query_merge_splits(const QueryAttnParams& p, cudaStream_t s);  // of a.nsplit > 1
-// The split count of ctas blocks over slots resident ones, for splits of `tokens`: the count
-// that fills one wave best with at least min_one tokens a split (the smallest on ties); two
-// waves, with at least min_two, where they are fuller by 8% (a second wave costs more starts and
-// a larger merge).
+// The split count of ctas blocks over slots resident ones, for sequences of up to `tokens`: as
+// many as one wave holds, with at least min_one tokens a split, or as two waves hold, with at
+// least min_two, where those are fuller by 8% (a second wave costs more starts and a larger
+// merge).  At most 256.
 int fill_splits(int64_t ctas, int64_t slots, int32_t tokens, int32_t min_one, int32_t min_two);
 // The page-major kernel of few rows; two: 16 rows a block (else 8).
 cudaError_t launch_query_pages_64(const QueryAttnParams& p, bool two, cudaStream_t s);

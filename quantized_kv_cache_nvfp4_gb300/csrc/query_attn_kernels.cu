@@ -215,18 +215,22 @@ __global__ void __launch_bounds__(kAttnThreads) query_rows_kernel(const QueryAtt
   }
 }
 
-// Merge of the splits of each (token, query head), one warp each, as the decode merge:
-// o = sum_k O_k 2^(M_k - M) / sum_k L_k 2^(M_k - M).  The warp first finds its token's
-// sequence (32-way search over starts): rows of no sequence, or of a refused one, have no
-// partials and stay as they are, as do rows with a NaN mark.
+// Merge of the splits of each (token, query head): o = sum_k O_k 2^(M_k - M) / sum_k L_k 2^(M_k -
+// M), by kPer warps a row, which share the splits (one warp walking 76 splits of two rows took
+// longer than their attention's last wave).  A row's warps first find its token's sequence
+// (32-way search over starts): rows of no sequence, or of a refused one, have no partials and
+// stay as they are, as do rows with a NaN mark.
 constexpr int kMergeWarps = 4;
 
-template <int D>
+template <int D, int kPer>
 __global__ void __launch_bounds__(32 * kMergeWarps) query_merge_kernel(const QueryAttnParams qp) {
   const AttnParams& p = qp.a;
   constexpr int kDL = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
+  constexpr int kRows = kMergeWarps / kPer;  // a block
+  __shared__ float2 part_ml[kMergeWarps];
+  __shared__ float part_o[kPer > 1 ? kMergeWarps : 1][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % kPer;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + warp / kPer;
   const bool live = row < static_cast<int64_t>(qp.num_tokens) * p.Hq;
   const int tok = live ? static_cast<int>(row / p.Hq) : 0, qh = static_cast<int>(row - static_cast<int64_t>(tok) * p.Hq);
   int lo = 0, hi = p.S;  // the last s < S with starts[s] <= tok lies in [lo, hi)
@@ -245,30 +249,53 @@ __global__ void __launch_bounds__(32 * kMergeWarps) query_merge_kernel(const Que
   // launched as a programmatic dependent of the attention kernel: wait for its results
   // (every block does, so that this grid's end implies the other's)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!live || !owned) return;
+  const bool mine = live && owned;  // the same for all of a row's warps
+  if (kPer == 1 && !mine) return;
   const float* const base = p.ws + row * p.nsplit * (D + 2);
-  float M = kNoKey;
+  const int per = (p.nsplit + kPer - 1) / kPer;
+  const int k_begin = mine ? min(part * per, p.nsplit) : 0, k_end = mine ? min(k_begin + per, p.nsplit) : 0;
+  // the O rows of the first kPre splits are loaded together with M and L: one wait for memory
+  constexpr int kPre = 64 / kDL;
+  float2 pre[kPre][kDL / 2];
+#pragma unroll
+  for (int k = 0; k < kPre; ++k)
+#pragma unroll
+    for (int i = 0; i < kDL / 2; ++i)
+      pre[k][i] = k_begin + k < k_end ? LDX(reinterpret_cast<const float2*>(base + (k_begin + k) * (D + 2) + kDL * lane + 2 * i))
+                                      : make_float2(0.0f, 0.0f);
+  float M = kNoKey, L = 0.0f;
   bool bad = false;
-  for (int k = lane; k < p.nsplit; k += 32) {
-    M = fmaxf(M, LDX(base + k * (D + 2) + D));
-    bad = bad || isnan(LDX(base + k * (D + 2) + D + 1));
+  for (int k = k_begin + lane; k < k_end; k += 32) {
+    const float2 ml = LDX(reinterpret_cast<const float2*>(base + k * (D + 2) + D));
+    M = fmaxf(M, ml.x);
+    bad = bad || isnan(ml.y);
   }
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
-  if (__any_sync(0xFFFFFFFFu, bad)) return;
-  float L = 0.0f;
   float o[kDL];
 #pragma unroll
   for (int i = 0; i < kDL; ++i) o[i] = 0.0f;
-  for (int k0 = 0; k0 < p.nsplit; k0 += 32) {
+  for (int k0 = k_begin; k0 < k_end; k0 += 32) {
     float f = 0.0f;
-    if (k0 + lane < p.nsplit) {
-      f = ex2(LDX(base + (k0 + lane) * (D + 2) + D) - M);
-      L += LDX(base + (k0 + lane) * (D + 2) + D + 1) * f;
+    if (k0 + lane < k_end) {
+      const float2 ml = LDX(reinterpret_cast<const float2*>(base + (k0 + lane) * (D + 2) + D));
+      f = ex2(ml.x - M);
+      L += ml.y * f;
     }
-    const int nk = min(32, p.nsplit - k0);
+    if (k0 == k_begin) {
+#pragma unroll
+      for (int k = 0; k < kPre; ++k) {
+        const float fk = __shfl_sync(0xFFFFFFFFu, f, k);  // 0 past the last split
+#pragma unroll
+        for (int i = 0; i < kDL / 2; ++i) {
+          o[2 * i] = __fmaf_rn(pre[k][i].x, fk, o[2 * i]);
+          o[2 * i + 1] = __fmaf_rn(pre[k][i].y, fk, o[2 * i + 1]);
+        }
+      }
+    }
+    const int nk = min(32, k_end - k0);
 #pragma unroll 8
-    for (int k = 0; k < nk; ++k) {
+    for (int k = k0 == k_begin ? kPre : 0; k < nk; ++k) {
       const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
       const float* const ok = base + (k0 + k) * (D + 2) + kDL * lane;
 #pragma unroll
@@ -281,6 +308,30 @@ __global__ void __launch_bounds__(32 * kMergeWarps) query_merge_kernel(const Que
   }
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, off);
+  bad = __any_sync(0xFFFFFFFFu, bad);
+  if constexpr (kPer > 1) {
+    if (bad) L = __int_as_float(0x7FC00000);
+    if (lane == 0) part_ml[warp] = make_float2(M, L);
+#pragma unroll
+    for (int i = 0; i < kDL; ++i) part_o[warp][kDL * lane + i] = o[i];
+    __syncthreads();
+    if (part != 0 || !mine) return;
+#pragma unroll
+    for (int w = 1; w < kPer; ++w) M = fmaxf(M, part_ml[warp + w].x);
+    L = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kDL; ++i) o[i] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kPer; ++w) {
+      const float2 ml = part_ml[warp + w];
+      const float f = ex2(ml.x - M);
+      L += ml.y * f;
+#pragma unroll
+      for (int i = 0; i < kDL; ++i) o[i] = __fmaf_rn(part_o[warp + w][kDL * lane + i], f, o[i]);
+    }
+    bad = isnan(L);
+  }
+  if (bad) return;
   uint16_t* const out = p.out + static_cast<int64_t>(tok) * p.o_row_pitch + static_cast<int64_t>(qh) * p.o_head_pitch;
 #pragma unroll
   for (int i = 0; i < kDL; i += 2) {
@@ -290,11 +341,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps) query_merge_kernel(const Que
   }
 }
 
-template <int D>
+template <int D, int kPer>
 cudaError_t launch_query_merge(const QueryAttnParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   const int64_t rows = static_cast<int64_t>(p.num_tokens) * p.a.Hq;
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps));
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kMergeWarps / kPer - 1) / (kMergeWarps / kPer)));
   cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -302,7 +353,12 @@ cudaError_t launch_query_merge(const QueryAttnParams& p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, query_merge_kernel<D>, p);
+  return cudaLaunchKernelEx(&cfg, query_merge_kernel<D, kPer>, p);
+}
+
+template <int D>
+cudaError_t launch_query_merge(const QueryAttnParams& p, cudaStream_t s) {
+  return p.a.nsplit >= 12 ? launch_query_merge<D, 4>(p, s) : launch_query_merge<D, 1>(p, s);
 }
 
 template <int D, int kFK, int kFV, int kNH>
@@ -365,22 +421,17 @@ int row_splits(int32_t S, int32_t H, int64_t rows, int32_t span) {
 }  // namespace
 
 int fill_splits(int64_t ctas, int64_t slots, int32_t tokens, int32_t min_one, int32_t min_two) {
+  // within a number of waves more splits fill them better, so each bound is its best count
   auto most = [&](int64_t waves, int32_t least) {
-    int64_t cap = (static_cast<int64_t>(tokens) + least - 1) / least;
-    if (waves * slots / ctas < cap) cap = waves * slots / ctas;
-    return cap > 256 ? int64_t{256} : cap;
+    const int64_t cap = std::min((static_cast<int64_t>(tokens) + least - 1) / least, waves * slots / ctas);
+    return std::max(int64_t{1}, std::min(cap, int64_t{256}));
   };
   auto fill = [&](int64_t n) {
     const int64_t waves = (ctas * n + slots - 1) / slots;
     return static_cast<double>(ctas * n) / static_cast<double>(waves * slots);
   };
-  int64_t best = 1;
-  for (int64_t n = 2; n <= most(1, min_one); ++n)
-    if (fill(n) > 1.01 * fill(best)) best = n;
-  int64_t two = best;
-  for (int64_t n = best + 1; n <= most(2, min_two); ++n)
-    if (fill(n) > 1.01 * fill(two)) two = n;
-  return static_cast<int>(fill(two) > 1.08 * fill(best) ? two : best);
+  const int64_t one = most(1, min_one), two = most(2, min_two);
+  return static_cast<int>(two > one && fill(two) > 1.08 * fill(one) ? two : one);
 }
 
 cudaError_t launch_query_merge_splits(const QueryAttnParams& p, cudaStream_t s) {
