@@ -157,12 +157,17 @@ class KvPool:
     def _struct(self) -> _abi.Pool:
         """The C struct of the pool, built once and kept while its planes are the same
         tensors (a plane replaced by another tensor rebuilds it)."""
-        planes = (self.k_codes, self.k_bscale, self.k_rscale, self.v_codes, self.v_bscale, self.v_rscale)
-        key = tuple(None if t is None else (id(t), t.data_ptr()) for t in planes) + (
-            self.block_size, self.fmt, self.v_fmt)
+        kc, kb, kr, vc, vb, vr = (self.k_codes, self.k_bscale, self.k_rscale, self.v_codes, self.v_bscale,
+                                  self.v_rscale)
         cached = self.__dict__.get("_c_struct")
-        if cached is not None and cached[0] == key:
-            return cached[1]
+        if cached is not None:
+            st, t, p, f = cached
+            if ((id(kc), id(kb), id(kr), id(vc), id(vb), id(vr)) == t and kc.data_ptr() == p[0]
+                    and kr.data_ptr() == p[1] and vc.data_ptr() == p[2] and vr.data_ptr() == p[3]
+                    and (kb is None or kb.data_ptr() == p[4]) and (vb is None or vb.data_ptr() == p[5])
+                    and (self.block_size, self.fmt, self.v_fmt) == f):
+                return st
+        bs = lambda t: None if t is None else t.data_ptr()
         for t in self._planes():
             if not t.is_contiguous():
                 raise ValueError("pool planes must be contiguous")
@@ -170,13 +175,15 @@ class KvPool:
                             (self.fmt if self.v_fmt is None else self.v_fmt, self.v_rscale, "v_rscale")):
             if f == FMT_FP8_PAGE and sc.numel() != self.num_slots // self.block_size * self.num_heads:
                 raise ValueError(f"{name} must be [blocks, heads] for FMT_FP8_PAGE")
-        bs = lambda t: None if t is None else t.data_ptr()
         st = _abi.Pool(
             _abi.Plane(self.k_codes.data_ptr(), bs(self.k_bscale), self.k_rscale.data_ptr()),
             _abi.Plane(self.v_codes.data_ptr(), bs(self.v_bscale), self.v_rscale.data_ptr()),
             self.num_slots, self.block_size, self.num_heads, self.head_dim, self.fmt,
             0 if self.v_fmt is None else self.v_fmt)
-        self.__dict__["_c_struct"] = (key, st)
+        self.__dict__["_c_struct"] = (
+            st, (id(kc), id(kb), id(kr), id(vc), id(vb), id(vr)),
+            (kc.data_ptr(), kr.data_ptr(), vc.data_ptr(), vr.data_ptr(), bs(kb), bs(vb)),
+            (self.block_size, self.fmt, self.v_fmt))
         return st
 
 
@@ -369,9 +376,10 @@ def kvq_decode_attention(pool: KvPool, block_table: torch.Tensor, seq_lens: torc
     S, max_blocks = block_table.shape
     qi, oo = _bf16_in(q, "q"), _bf16_out(out, "out")
     Hq = q.size(1)
-    need = kvq_decode_attention_workspace(S, pool.num_heads, Hq, pool.head_dim, max_seq_len)
-    if workspace is None and need > 0:
-        workspace = _workspace(need, q.device, stream)
+    if workspace is None:
+        need = kvq_decode_attention_workspace(S, pool.num_heads, Hq, pool.head_dim, max_seq_len)
+        if need > 0:
+            workspace = _workspace(need, q.device, stream)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     ps = pool._struct()
     _check(_lib().kvq_decode_attention(
