@@ -297,7 +297,7 @@ KVQ_API kvq_status kvq_decode_attention(const kvq_pool* pool, const int32_t* blo
  * The pages have no counterpart to this entry point; it exists for such callers.
  *   Limit    the partials need kvq_decode_attention_workspace(...) bytes; a call
  *            that needs more than 48 MiB returns KVQ_ERR_UNSUPPORTED.  The split
- *            policy keeps every supported shape under 40.2 MB on a 152-SM GPU.
+ *            policy keeps every supported shape under 40.5 MB on a 152-SM GPU.
  *   Set-up   the first call on a device looks up the scratch array's device address
  *            (with that device current) and keeps it; make that first call before
  *            any stream capture.  A failed lookup returns KVQ_ERR_CUDA.

@@ -848,15 +848,13 @@ int attn_page_splits(int32_t S, int32_t H, int32_t max_seq_len) {
   return best;
 }
 
-// Splits of a page-scaled pool's calls: 2 blocks an SM (1 at H = 16 or head_dim 256), at least
-// 64 tokens a split, so that short sequences spread over the GPU too.  One where whole pages
-// cannot serve the call.  At most two waves, 4 SMs x 64 query heads x 130 (or 2 SMs x 128 x 130,
-// SMs x 128 x 258) partials of 4 bytes: 20.2 MB on 152 SMs.
+// Splits of a page-scaled pool's calls in the page-major kernel: 2 blocks an SM (1 at H = 16), at
+// least 64 tokens a split, so that short sequences spread over the GPU too.  At most two waves,
+// 4 SMs x 64 query heads x 130 (or 2 SMs x 128 x 130) partials of 4 bytes: 20.2 MB on 152 SMs.
 int attn_page_scaled_splits(int32_t S, int32_t H, int32_t Hq, int32_t D, int32_t max_seq_len) {
-  const bool ok = D == 256 ? (H == 4 || H == 8) : (H == 4 || H == 8 || H == 16) && Hq / H <= 8;
+  const bool ok = (D == 64 || D == 128) && (H == 4 || H == 8 || H == 16) && Hq / H <= 8;
   if (!ok || S <= 0 || max_seq_len <= 0) return 1;
-  const int64_t ctas = static_cast<int64_t>(S) * (D == 256 && Hq / H > 8 ? 2 : 1);
-  return fill_splits(ctas, static_cast<int64_t>(H == 16 || D == 256 ? 1 : 2) * num_sms(), max_seq_len, 64, 384);
+  return fill_splits(S, static_cast<int64_t>(H == 16 ? 1 : 2) * num_sms(), max_seq_len, 64, 384);
 }
 
 // Tokens per split: the splits cover max_seq_len in multiples of `unit` tokens.
@@ -874,22 +872,26 @@ size_t attn_workspace_bytes(int32_t S, int32_t H, int32_t Hq, int32_t D, int32_t
   if (np > n) n = np;
   const int ns = attn_page_scaled_splits(S, H, Hq, D, max_seq_len);
   if (ns > n) n = ns;
-  if (n <= 1) return 0;
-  return static_cast<size_t>(S) * Hq * n * (D + 2) * sizeof(float);
+  const size_t bytes = n <= 1 ? 0 : static_cast<size_t>(S) * Hq * n * (D + 2) * sizeof(float);
+  // (the format is not known here: the whole-page kernel's partials count too, at most 8 SMs x 64
+  // query heads x 130, or 4 SMs x 128 x 130, or 4 SMs x 64 x 258 of 4 bytes, 40.5 MB on 152 SMs)
+  if ((H != 4 && H != 8) || Hq / H > 16 || (D != 256 && Hq / H <= 8)) return bytes;
+  const size_t pages = query_pages_workspace_bytes(S, S, Hq, D, Hq / H, max_seq_len);
+  return pages > bytes ? pages : bytes;
 }
 
 cudaError_t launch_decode_attention(const AttnParams& p_in, cudaStream_t s) {
   AttnParams p = p_in;
-  if ((p.k_page || p.v_page) && p.D == 256 && p.block_size % 16 == 0 && (p.H == 4 || p.H == 8)) {
-    // head_dim 256: the whole-page kernel of kvq_attention, one query token a sequence (2 x 65536
-    // tokens, H4: 91 us by the head-major kernel below)
+  if ((p.k_page || p.v_page) && (p.D == 256 || p.group > 8) && p.group <= 16 && p.H <= 8 &&
+      query_pages_ok(p.block_size, p.H, true)) {
+    // what the page-major kernel does not take: the whole-page kernel of kvq_attention, one query
+    // token a sequence (head_dim 256, 2 x 65536 tokens, H4: 57 us; 91 us by the head-major kernel
+    // below)
     QueryAttnParams q{};
     q.a = p;
-    q.a.nsplit = attn_page_scaled_splits(p.S, p.H, p.Hq, p.D, p.max_len);
     q.num_tokens = p.S;
     q.max_q = 1;
-    const cudaError_t e = launch_query_pages_256(q, s);
-    return e == cudaSuccess ? launch_query_merge_splits(q, s) : e;
+    return launch_query_pages(q, p.max_len, s);
   }
   if (attn_page_ok(p.block_size, p.H, p.D, p.group, p.k_page || p.v_page)) {
     p.nsplit = p.k_page || p.v_page ? attn_page_scaled_splits(p.S, p.H, p.Hq, p.D, p.max_len)

@@ -298,11 +298,20 @@ struct QueryAttnParams {
   int32_t window;            // 0: none
   const int32_t* prefix;     // [S] or nullptr
   const int32_t* key_starts; // [num_tokens] or nullptr
+  int32_t* parts;            // whole pages: [S] parts of each sequence in use, behind the partials
+                             // (a.nsplit are laid out for each row); nullptr: a.nsplit equal ones
+  int32_t blocks, wave;      // whole pages with parts: thread blocks to share among the sequences,
+                             // and of them as many as are resident at a time
 };
 size_t query_attn_workspace_bytes(int32_t S, int32_t num_tokens, int32_t H, int32_t Hq, int32_t D,
                                   int32_t max_q, int32_t max_len);
 cudaError_t launch_query_attention(const QueryAttnParams& p, cudaStream_t s);
 cudaError_t launch_query_merge_splits(const QueryAttnParams& p, cudaStream_t s);  // of a.nsplit > 1
+// The whole-page kernel and its merge for up to 16 rows a KV head (span: the most keys a sequence's
+// rows see), and the workspace bytes of its partials.
+bool query_pages_ok(int32_t block_size, int32_t H, bool page_scaled);
+cudaError_t launch_query_pages(const QueryAttnParams& p, int32_t span, cudaStream_t s);
+size_t query_pages_workspace_bytes(int32_t S, int32_t num_tokens, int32_t Hq, int32_t D, int64_t rows, int32_t max_len);
 // The split count of ctas blocks over slots resident ones, for sequences of up to `tokens`: as
 // many as one wave holds, with at least min_one tokens a split, or as two waves hold, with at
 // least min_two, where those are fuller by 8% (a second wave costs more starts and a larger

@@ -252,8 +252,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps) query_merge_kernel(const Que
   const bool mine = live && owned;  // the same for all of a row's warps
   if (kPer == 1 && !mine) return;
   const float* const base = p.ws + row * p.nsplit * (D + 2);
-  const int per = (p.nsplit + kPer - 1) / kPer;
-  const int k_begin = mine ? min(part * per, p.nsplit) : 0, k_end = mine ? min(k_begin + per, p.nsplit) : 0;
+  const int nsplit = !mine ? 0 : qp.parts != nullptr ? LDX(qp.parts + lo) : p.nsplit;
+  const bool done = qp.parts != nullptr && nsplit == 1;  // written by the attention kernel
+  if (kPer == 1 && done) return;
+  const int per = (nsplit + kPer - 1) / kPer;
+  const int k_begin = done ? 0 : min(part * per, nsplit), k_end = done ? 0 : min(k_begin + per, nsplit);
   // the O rows of the first kPre splits are loaded together with M and L: one wait for memory
   constexpr int kPre = 64 / kDL;
   float2 pre[kPre][kDL / 2];
@@ -315,7 +318,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) query_merge_kernel(const Que
 #pragma unroll
     for (int i = 0; i < kDL; ++i) part_o[warp][kDL * lane + i] = o[i];
     __syncthreads();
-    if (part != 0 || !mine) return;
+    if (part != 0 || !mine || done) return;
 #pragma unroll
     for (int w = 1; w < kPer; ++w) M = fmaxf(M, part_ml[warp + w].x);
     L = 0.0f;
@@ -358,7 +361,9 @@ cudaError_t launch_query_merge(const QueryAttnParams& p, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch_query_merge(const QueryAttnParams& p, cudaStream_t s) {
-  return p.a.nsplit >= 12 ? launch_query_merge<D, 4>(p, s) : launch_query_merge<D, 1>(p, s);
+  // four warps a row for 12 splits and more (shared blocks: the most, twice the usual count; 1600
+  // rows of 6 took 10.2 us by four, 5.6 by one)
+  return p.a.nsplit >= (p.parts != nullptr ? 24 : 12) ? launch_query_merge<D, 4>(p, s) : launch_query_merge<D, 1>(p, s);
 }
 
 template <int D, int kFK, int kFV, int kNH>
@@ -395,22 +400,35 @@ cudaError_t rows_dispatch(const QueryAttnParams& p, int rows, cudaStream_t s) {
 // the layout allows it, else the rows kernel.
 constexpr int kTileFrom = 17;
 
-bool page_kernel_ok(const AttnParams& a) {
-  return a.block_size % 16 == 0 && (a.H == 1 || a.H == 2 || a.H == 4 || a.H == 8) &&
-         (a.H >= 4 || !(a.k_page || a.v_page));
-}
-
 int tile_splits(int32_t S, int32_t H, int32_t D, int64_t rows, int32_t span) {
   // one CTA an SM, at least 512 tokens a split
   const int64_t ctas = static_cast<int64_t>(S) * H * ((rows + query_tile_rows(D) - 1) / query_tile_rows(D));
   return fill_splits(ctas, num_sms(), span, 512, 512);
 }
 bool page_two(int32_t D, int64_t rows) { return rows > 8 && D != 256; }  // 16 rows a block spill at head_dim 256
-int page_splits(int32_t S, int32_t D, int64_t rows, int32_t span) {
+
+// The whole-page kernel's blocks.  Several sequences share one or two waves of them by length
+// (page_job): in equal parts their longest sets the time.  GPU us in equal parts and shared, one
+// token each: lengths of 1 to L, NVFP4 with bias, 16 x 5000 34.4, 29.9; page-scaled, 24 x 6000 42.3,
+// 35.9; 100 x 6000 150, 124; 250 x 6000 425, 278; all equal to 3000, 50 55.8, 59.2; 140 137, 142.
+// Not where there is little to share (below 96 keys a resident block: every block reads all
+// lengths first, 1 us), for more tiles than a wave holds, or for more than 512 sequences.
+struct PagePlan {
+  int nsplit;  // partials a row
+  int blocks;  // when balanced, else 0
+  int wave;
+};
+PagePlan page_plan(int32_t S, int32_t D, int64_t rows, int32_t span) {
   // two blocks an SM (one with 16 rows or head_dim 256)
   const int64_t per = page_two(D, rows) ? 16 : 8;
   const int64_t slots = static_cast<int64_t>(per == 16 || D == 256 ? 1 : 2) * num_sms();
-  return fill_splits(static_cast<int64_t>(S) * ((rows + per - 1) / per), slots, span, 64, 384);
+  const int64_t ctas = static_cast<int64_t>(S) * ((rows + per - 1) / per);
+  const int n = fill_splits(ctas, slots, span, 64, 384);
+  if (S == 1 || S > 512 || ctas > slots || ctas * span < 96 * slots || (n == 1 && span < 1024)) return PagePlan{n, 0, 0};
+  const int64_t blocks = 4 * ctas > slots ? 2 * slots : slots;
+  const int64_t most = std::min((static_cast<int64_t>(span) + 63) / 64, 2 * blocks / ctas);
+  return PagePlan{static_cast<int>(std::min(std::max(most, static_cast<int64_t>(n)), int64_t{256})),
+                  static_cast<int>(blocks), static_cast<int>(slots)};
 }
 int row_splits(int32_t S, int32_t H, int64_t rows, int32_t span) {
   // four CTAs an SM
@@ -444,6 +462,34 @@ cudaError_t launch_query_merge_splits(const QueryAttnParams& p, cudaStream_t s) 
   return e;
 }
 
+bool query_pages_ok(int32_t block_size, int32_t H, bool page_scaled) {
+  return block_size % 16 == 0 && (H == 1 || H == 2 || H == 4 || H == 8) && (H >= 4 || !page_scaled);
+}
+
+size_t query_pages_workspace_bytes(int32_t S, int32_t num_tokens, int32_t Hq, int32_t D, int64_t rows, int32_t max_len) {
+  const PagePlan plan = page_plan(S, D, rows, max_len);
+  if (plan.nsplit <= 1) return 0;
+  return static_cast<size_t>(num_tokens) * Hq * plan.nsplit * (D + 2) * sizeof(float) + (plan.blocks > 0 ? 4 * static_cast<size_t>(S) : 0);
+}
+
+cudaError_t launch_query_pages(const QueryAttnParams& p_in, int32_t span, cudaStream_t s) {
+  QueryAttnParams p = p_in;
+  const int64_t rows = static_cast<int64_t>(p.max_q) * p.a.group;
+  // the workspace query knows the longest sequence but no window: never more partials than it
+  // counted
+  const PagePlan plan = page_plan(p.a.S, p.a.D, rows, span), most = page_plan(p.a.S, p.a.D, rows, p.a.max_len);
+  p.a.nsplit = std::min(plan.nsplit, most.nsplit);
+  if (plan.blocks > 0 && most.blocks > 0 && p.a.nsplit > 1) {
+    p.parts = reinterpret_cast<int32_t*>(p.a.ws + static_cast<int64_t>(p.num_tokens) * p.a.Hq * p.a.nsplit * (p.a.D + 2));
+    p.blocks = plan.blocks;
+    p.wave = plan.wave;
+  }
+  const cudaError_t e = p.a.D == 64    ? launch_query_pages_64(p, page_two(64, rows), s)
+                        : p.a.D == 128 ? launch_query_pages_128(p, page_two(128, rows), s)
+                                       : launch_query_pages_256(p, s);
+  return e == cudaSuccess ? launch_query_merge_splits(p, s) : e;
+}
+
 size_t query_attn_workspace_bytes(int32_t S, int32_t num_tokens, int32_t H, int32_t Hq, int32_t D, int32_t max_q,
                                   int32_t max_len) {
   if (S <= 0 || num_tokens <= 0 || H <= 0 || Hq < H || D <= 0 || max_q <= 0 || max_len <= 0) return 0;
@@ -454,11 +500,10 @@ size_t query_attn_workspace_bytes(int32_t S, int32_t num_tokens, int32_t H, int3
   if (rows >= kTileFrom) {
     n = tile_splits(S, H, D, rows, max_len);
   } else {
-    const int np = page_splits(S, D, rows, max_len), nr = row_splits(S, H, rows, max_len);
-    n = np > nr ? np : nr;
+    n = row_splits(S, H, rows, max_len);
   }
-  if (n <= 1) return 0;
-  return static_cast<size_t>(num_tokens) * Hq * n * (D + 2) * sizeof(float);
+  const size_t bytes = n <= 1 ? 0 : static_cast<size_t>(num_tokens) * Hq * n * (D + 2) * sizeof(float);
+  return rows >= kTileFrom ? bytes : std::max(bytes, query_pages_workspace_bytes(S, num_tokens, Hq, D, rows, max_len));
 }
 
 cudaError_t launch_query_attention(const QueryAttnParams& p_in, cudaStream_t s) {
@@ -469,18 +514,11 @@ cudaError_t launch_query_attention(const QueryAttnParams& p_in, cudaStream_t s) 
   const int64_t seen = static_cast<int64_t>(p.window) + p.max_q;
   const int32_t span = p.window > 0 && p.prefix == nullptr && seen < p.a.max_len ? static_cast<int32_t>(seen) : p.a.max_len;
   if (rows < kTileFrom) {
-    cudaError_t e;
-    if (page_kernel_ok(p.a)) {
-      p.a.nsplit = std::min(page_splits(p.a.S, p.a.D, rows, span), page_splits(p.a.S, p.a.D, rows, p.a.max_len));
-      e = p.a.D == 64    ? launch_query_pages_64(p, page_two(64, rows), s)
-          : p.a.D == 128 ? launch_query_pages_128(p, page_two(128, rows), s)
-                         : launch_query_pages_256(p, s);
-    } else {
-      p.a.nsplit = std::min(row_splits(p.a.S, p.a.H, rows, span), row_splits(p.a.S, p.a.H, rows, p.a.max_len));
-      e = p.a.D == 64    ? rows_dispatch<64>(p, rows, s)
-          : p.a.D == 128 ? rows_dispatch<128>(p, rows, s)
-                         : rows_dispatch<256>(p, rows, s);
-    }
+    if (query_pages_ok(p.a.block_size, p.a.H, p.a.k_page || p.a.v_page)) return launch_query_pages(p, span, s);
+    p.a.nsplit = std::min(row_splits(p.a.S, p.a.H, rows, span), row_splits(p.a.S, p.a.H, rows, p.a.max_len));
+    const cudaError_t e = p.a.D == 64    ? rows_dispatch<64>(p, rows, s)
+                          : p.a.D == 128 ? rows_dispatch<128>(p, rows, s)
+                                         : rows_dispatch<256>(p, rows, s);
     return e == cudaSuccess ? launch_query_merge_splits(p, s) : e;
   }
   p.a.nsplit = std::min(tile_splits(p.a.S, p.a.H, p.a.D, rows, span), tile_splits(p.a.S, p.a.H, p.a.D, rows, p.a.max_len));

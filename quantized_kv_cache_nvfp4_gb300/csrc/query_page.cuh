@@ -17,6 +17,92 @@ namespace kvq {
 
 namespace {
 
+// The job of block `cta` where sequences share the blocks by length: with T row tiles and w =
+// (stages of its keys + 2 for a block's start) a sequence has T p blocks,
+//   p = 1 + floor(w (n - sum T) / sum T w),
+// at most a.nsplit and one for 64 keys; blocks go to the sequences in order.  n is one wave of
+// blocks, or two where the longest share of one is above 1.3 times the mean by 4 stages and more (a
+// second wave's starts and partials cost 12 to 19% on equal lengths of 3000).  One warp; its notes take
+// 8 S bytes of shared memory.
+struct PageJob {
+  int s, tile, part, parts;  // parts 0: nothing to do
+};
+template <int kRows>
+__device__ __forceinline__ PageJob page_job(const QueryAttnParams& qp, int lane, int unit, int cta, int2* note) {
+  const int S = qp.a.S;
+  auto sum = [](int64_t v) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+  };
+  int64_t tiles = 0, work = 0;
+#pragma unroll 4
+  for (int s = lane; s < S; s += 32) {  // note: {w, T}
+    int q0, n, len;
+    int2 wt = make_int2(0, 0);
+    if (query_range(qp, s, q0, n, len)) {
+      wt.y = (n * qp.a.group + kRows - 1) / kRows;
+      const int64_t near = static_cast<int64_t>(qp.window) + n;
+      const int span = qp.window > 0 && qp.prefix == nullptr && near < len ? static_cast<int>(near) : len;
+      wt.x = static_cast<int>((static_cast<uint32_t>(span) + unit - 1) / unit) + 2;
+    } else if (cta == 0) {
+      set_status(qp.a.status, 8u);
+    }
+    note[s] = wt;
+    tiles += wt.y;
+    work += static_cast<int64_t>(wt.x) * wt.y;
+  }
+  tiles = sum(tiles);
+  work = max(sum(work), int64_t{1});
+  int64_t spare = max(qp.wave - tiles, int64_t{0});
+  float per_w = static_cast<float>(spare) / static_cast<float>(work);
+  auto parts_of = [&](int2 wt) {
+    // the quotient in 32 bits, at most one low or one high, then put right
+    const int64_t all = wt.x * spare;
+    int q = static_cast<int>(static_cast<float>(wt.x) * per_w);
+    if (q * work > all) --q;
+    if ((q + 1) * work <= all) ++q;
+    const int most = static_cast<int>((static_cast<uint32_t>(wt.x - 2) * unit + 63u) / 64u);
+    return max(1, min(min(most, qp.a.nsplit), 1 + q));
+  };
+  if (qp.blocks > qp.wave) {
+    int longest = 0;
+    for (int s = lane; s < S; s += 32) {
+      const int2 wt = note[s];
+      if (wt.y > 0) {
+        const int n = parts_of(wt);
+        longest = max(longest, (wt.x + n - 1) / n);
+      }
+    }
+    longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+    if (static_cast<float>(longest - 4) * static_cast<float>(qp.wave) > 1.3f * static_cast<float>(work)) {
+      spare = max(qp.blocks - tiles, int64_t{0});
+      per_w = static_cast<float>(spare) / static_cast<float>(work);
+    }
+  }
+  int64_t before = 0;
+  for (int s0 = 0; s0 < S; s0 += 32) {
+    const int2 wt = s0 + lane < S ? note[s0 + lane] : make_int2(0, 0);
+    const int parts = wt.y > 0 ? parts_of(wt) : 0;
+    const int64_t mine = static_cast<int64_t>(wt.y) * parts;
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const int64_t at = cta - before - (upto - mine);
+    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, at >= 0 && at < mine);
+    if (hit != 0u) {
+      const int src = __ffs(hit) - 1;
+      const int off = __shfl_sync(0xFFFFFFFFu, static_cast<int>(at), src), n = __shfl_sync(0xFFFFFFFFu, parts, src);
+      return PageJob{s0 + src, off / n, off % n, n};
+    }
+    before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+  }
+  return PageJob{0, 0, 0, 0};
+}
+
 template <int D, int kFK, int kFV, int kNH>
 struct QueryPage {
   static constexpr int kW = 8;
@@ -42,10 +128,8 @@ __global__ void __launch_bounds__(32 * (QueryPage<D, kFK, kFV, kNH>::kW + 1), Qu
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
-  const int s = blockIdx.z;
-  const int tile = blockIdx.x / p.nsplit, split = blockIdx.x - tile * p.nsplit;
-  const int row0 = tile * kRows;
   const int H = p.H, P = W / H;
+  __shared__ PageJob job;
 
   const uint32_t ring_s = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
   const uint32_t full0 = ring_s + T::kOffBar, empty0 = full0 + 8 * T::kStages;
@@ -59,11 +143,28 @@ __global__ void __launch_bounds__(32 * (QueryPage<D, kFK, kFV, kNH>::kW + 1), Qu
     *bad_flag = 0;
     mbar_init_fence();
   }
+  if (warp == W) {
+    PageJob mine;
+    if (qp.parts != nullptr) {
+      mine = page_job<kRows>(qp, lane, 16 * P, blockIdx.x, reinterpret_cast<int2*>(smem));
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // its notes lie where copies will land
+    } else {
+      const int t = static_cast<int>(blockIdx.x) / p.nsplit;
+      mine = PageJob{static_cast<int>(blockIdx.z), t, static_cast<int>(blockIdx.x) - t * p.nsplit, p.nsplit};
+    }
+    if (lane == 0) {
+      job = mine;
+      if (qp.parts != nullptr && mine.parts > 0 && mine.tile == 0 && mine.part == 0) STX(qp.parts + mine.s, mine.parts);
+    }
+  }
   __syncthreads();
+  const int s = job.s, split = job.part, nsplit = job.parts;
+  const int row0 = job.tile * kRows;
+  if (nsplit == 0) return;
 
   int q0, nq, len;
   const bool ok = query_range(qp, s, q0, nq, len);
-  if (!ok && threadIdx.x == 0 && blockIdx.x == 0) set_status(p.status, 8u);
+  if (!ok && threadIdx.x == 0 && blockIdx.x == 0) set_status(p.status, 8u);  // (page_job did it before)
   const int rows = nq * p.group;
   if (row0 >= rows) return;
   int lo, hi;
@@ -72,7 +173,7 @@ __global__ void __launch_bounds__(32 * (QueryPage<D, kFK, kFV, kNH>::kW + 1), Qu
   int t_begin = 0, t_end = 0;
   if (lo_min < hi_max) {  // equal splits in whole stages, from a chunk's start
     const int first = lo_min & ~15, unit = 16 * P;
-    const int per = ((hi_max - first + p.nsplit - 1) / p.nsplit + unit - 1) / unit * unit;
+    const int per = ((hi_max - first + nsplit - 1) / nsplit + unit - 1) / unit * unit;
     t_begin = static_cast<int>(min(static_cast<int64_t>(first) + static_cast<int64_t>(split) * per, static_cast<int64_t>(hi_max)));
     t_end = min(t_begin + per, hi_max);
   }
@@ -262,7 +363,7 @@ __global__ void __launch_bounds__(32 * (QueryPage<D, kFK, kFV, kNH>::kW + 1), Qu
       const int i = row / p.group, qh = h * p.group + row - i * p.group;
       const int64_t tok = q0 + i;
       const float L = st.l[nh][e];
-      if (p.nsplit == 1) {
+      if (nsplit == 1) {
         if (cta_bad) continue;
         uint16_t* const out = p.out + tok * p.o_row_pitch + static_cast<int64_t>(qh) * p.o_head_pitch;
 #pragma unroll
@@ -289,7 +390,7 @@ cudaError_t query_page_launch(const QueryAttnParams& p, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, QP::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (static_cast<int64_t>(p.max_q) * p.a.group + 8 * kNH - 1) / (8 * kNH);
-  const dim3 grid(static_cast<unsigned>(tiles * p.a.nsplit), 1, p.a.S);
+  const dim3 grid(p.parts != nullptr ? p.blocks : static_cast<unsigned>(tiles * p.a.nsplit), 1, p.parts != nullptr ? 1 : p.a.S);
   KVQ_LAUNCH("query_page_kernel", s, k<<<grid, 32 * (QP::kW + 1), QP::kSmem, s>>>(p); e = cudaGetLastError());
   return e;
 }

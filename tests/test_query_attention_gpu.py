@@ -188,6 +188,40 @@ def test_long_sequences_split(lens, new):
         c.check(out, **opts)
 
 
+@pytest.mark.parametrize("S,longest,new,H,group,D", [
+    (40, 1500, 1, 2, 4, 128), (90, 1100, 1, 8, 1, 64), (33, 1300, 4, 4, 4, 128), (40, 1200, 1, 4, 2, 256),
+    (2, 20000, 3, 1, 4, 64), (230, 1030, 1, 4, 1, 64), (20, 900, 1, 4, 16, 128)])
+def test_ragged_batches(S, longest, new, H, group, D):
+    """Sequences of very different lengths, one of them alone the longest, empty and refused ones
+    among them: however the work is shared, every row is whole."""
+    rng = np.random.default_rng(S)
+    lens = rng.integers(1, longest // 8, S) + new
+    lens[S // 2:] //= 4
+    lens[-1], lens[0] = longest, new
+    n = np.minimum(rng.integers(0, new + 1, S) if new > 1 else np.ones(S, int), lens)
+    n[-1] = new
+    c = Case([int(x) for x in lens], [int(x) for x in n], H, group, D, seed=S)
+    for opts in ({}, {"window": 333}, {"slopes": np.linspace(0.001, 0.1, H * group).astype(np.float32), "softcap": 30.0}):
+        out, st = c.run(**opts)
+        assert st == 0 and c.untouched(out, slice(c.starts[-1], c.T))
+        c.check(out, **opts)
+        again, _ = c.run(**opts)
+        assert torch.equal(out, again)
+    if S > 2:
+        wrong = list(c.lens)
+        wrong[S // 3] = wrong[-2] = -1
+        out, st = c.run(lens=wrong, max_len=longest)
+        assert st == 8 and c.untouched(out, slice(c.starts[S - 2], c.starts[S - 1]))
+        assert c.untouched(out, slice(c.starts[S // 3], c.starts[S // 3 + 1]))
+        c.check(out, seqs=[s for s in range(S - 2) if s != S // 3] + [S - 1])
+    if max(c.new) == min(c.new) == 1:
+        st, out = status_word(), poison_bf16((S, H * group, D))
+        kvq.kvq_decode_attention(c.pool, c.table.to(DEV), torch.tensor(c.lens, dtype=torch.int32, device=DEV), longest,
+                                 c.q[:S].to(DEV), c.scale, out, dev_status=st)
+        assert int(st.item()) == 0
+        c.check(out)
+
+
 @pytest.mark.parametrize("new", [[1, 1, 1], [70, 40, 50]])
 def test_bad_sequences_keep_their_rows(new):
     c = Case([100, 80, 60], new, 2, 4, 128, seed=6)
