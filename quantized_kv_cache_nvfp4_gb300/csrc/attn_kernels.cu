@@ -706,9 +706,10 @@ cudaError_t page_launch(const AttnParams& p, cudaStream_t s) {
     q.num_tokens = p.S;
     q.max_q = 1;
     return launch_query_merge_splits(q, s);
+  } else {
+    KVQ_LAUNCH("decode_attn_merge_kernel", s, e = launch_merge<D>(p, s));
+    return e;
   }
-  KVQ_LAUNCH("decode_attn_merge_kernel", s, e = launch_merge<D>(p, s));
-  return e;
 }
 
 template <int D, int W, int H>
@@ -875,18 +876,18 @@ size_t attn_workspace_bytes(int32_t S, int32_t H, int32_t Hq, int32_t D, int32_t
   const size_t bytes = n <= 1 ? 0 : static_cast<size_t>(S) * Hq * n * (D + 2) * sizeof(float);
   // (the format is not known here: the whole-page kernel's partials count too, at most 8 SMs x 64
   // query heads x 130, or 4 SMs x 128 x 130, or 4 SMs x 64 x 258 of 4 bytes, 40.5 MB on 152 SMs)
-  if ((H != 4 && H != 8) || Hq / H > 16 || (D != 256 && Hq / H <= 8)) return bytes;
+  if ((H != 4 && H != 8) || Hq / H > 16) return bytes;
   const size_t pages = query_pages_workspace_bytes(S, S, Hq, D, Hq / H, max_seq_len);
   return pages > bytes ? pages : bytes;
 }
 
 cudaError_t launch_decode_attention(const AttnParams& p_in, cudaStream_t s) {
   AttnParams p = p_in;
-  if ((p.k_page || p.v_page) && (p.D == 256 || p.group > 8) && p.group <= 16 && p.H <= 8 &&
-      query_pages_ok(p.block_size, p.H, true)) {
-    // what the page-major kernel does not take: the whole-page kernel of kvq_attention, one query
-    // token a sequence (head_dim 256, 2 x 65536 tokens, H4: 57 us; 91 us by the head-major kernel
-    // below)
+  if ((p.k_page || p.v_page) && p.H <= 8 && query_pages_ok(p.block_size, p.H, true) &&
+      (p.D == 256 || p.group > 8 || query_pages_share(p.S, p.D, p.group, p.max_len))) {
+    // what the page-major kernel does not take, or takes in equal parts only: the whole-page
+    // kernel of kvq_attention, one query token a sequence (head_dim 256, 2 x 65536 tokens, H4: 58 us;
+    // 91 us by the head-major kernel below)
     QueryAttnParams q{};
     q.a = p;
     q.num_tokens = p.S;

@@ -310,6 +310,7 @@ cudaError_t launch_query_merge_splits(const QueryAttnParams& p, cudaStream_t s);
 // The whole-page kernel and its merge for up to 16 rows a KV head (span: the most keys a sequence's
 // rows see), and the workspace bytes of its partials.
 bool query_pages_ok(int32_t block_size, int32_t H, bool page_scaled);
+bool query_pages_share(int32_t S, int32_t D, int64_t rows, int32_t span);  // blocks by length
 cudaError_t launch_query_pages(const QueryAttnParams& p, int32_t span, cudaStream_t s);
 size_t query_pages_workspace_bytes(int32_t S, int32_t num_tokens, int32_t Hq, int32_t D, int64_t rows, int32_t max_len);
 // The split count of ctas blocks over slots resident ones, for sequences of up to `tokens`: as

@@ -410,9 +410,13 @@ bool page_two(int32_t D, int64_t rows) { return rows > 8 && D != 256; }  // 16 r
 // The whole-page kernel's blocks.  Several sequences share one or two waves of them by length
 // (page_job): in equal parts their longest sets the time.  GPU us in equal parts and shared, one
 // token each: lengths of 1 to L, NVFP4 with bias, 16 x 5000 34.4, 29.9; page-scaled, 24 x 6000 42.3,
-// 35.9; 100 x 6000 150, 124; 250 x 6000 425, 278; all equal to 3000, 50 55.8, 59.2; 140 137, 142.
-// Not where there is little to share (below 96 keys a resident block: every block reads all
-// lengths first, 1 us), for more tiles than a wave holds, or for more than 512 sequences.
+// 35.9; 50 x 6000 76.7, 55.7; 100 x 6000 145, 120; 250 x 6000 396, 329; all of one length, 32 x 8192
+// 86.4, 88.9; 50 x 6000 98.3, 101; 250 x 6000 449, 482.  Not where there is little to share: below
+// 96 keys a resident block (every block reads all lengths first, 1 us), or below 4096 keys
+// where it takes two waves (100 x 1500: ragged 45.7, 45.6, of one length 56.9, 67.4); nor for more
+// tiles than a wave holds, or for more than 512 sequences.  One line of all the work in equal
+// shares, several sequences' parts to a block, was better for many (250 x 6000 269) and worse for
+// few (16 x 6000 30, against 25.9): a second part's start costs as much as five stages.
 struct PagePlan {
   int nsplit;  // partials a row
   int blocks;  // when balanced, else 0
@@ -424,8 +428,10 @@ PagePlan page_plan(int32_t S, int32_t D, int64_t rows, int32_t span) {
   const int64_t slots = static_cast<int64_t>(per == 16 || D == 256 ? 1 : 2) * num_sms();
   const int64_t ctas = static_cast<int64_t>(S) * ((rows + per - 1) / per);
   const int n = fill_splits(ctas, slots, span, 64, 384);
-  if (S == 1 || S > 512 || ctas > slots || ctas * span < 96 * slots || (n == 1 && span < 1024)) return PagePlan{n, 0, 0};
-  const int64_t blocks = 4 * ctas > slots ? 2 * slots : slots;
+  if (S == 1 || S > 512 || ctas > slots || ctas * span < 96 * slots) return PagePlan{n, 0, 0};
+  const bool two = 4 * ctas > slots;
+  if (two && span < 4096) return PagePlan{n, 0, 0};
+  const int64_t blocks = two ? 2 * slots : slots;
   const int64_t most = std::min((static_cast<int64_t>(span) + 63) / 64, 2 * blocks / ctas);
   return PagePlan{static_cast<int>(std::min(std::max(most, static_cast<int64_t>(n)), int64_t{256})),
                   static_cast<int>(blocks), static_cast<int>(slots)};
@@ -465,6 +471,8 @@ cudaError_t launch_query_merge_splits(const QueryAttnParams& p, cudaStream_t s) 
 bool query_pages_ok(int32_t block_size, int32_t H, bool page_scaled) {
   return block_size % 16 == 0 && (H == 1 || H == 2 || H == 4 || H == 8) && (H >= 4 || !page_scaled);
 }
+
+bool query_pages_share(int32_t S, int32_t D, int64_t rows, int32_t span) { return page_plan(S, D, rows, span).blocks > 0; }
 
 size_t query_pages_workspace_bytes(int32_t S, int32_t num_tokens, int32_t Hq, int32_t D, int64_t rows, int32_t max_len) {
   const PagePlan plan = page_plan(S, D, rows, max_len);

@@ -190,7 +190,7 @@ def test_long_sequences_split(lens, new):
 
 @pytest.mark.parametrize("S,longest,new,H,group,D", [
     (40, 1500, 1, 2, 4, 128), (90, 1100, 1, 8, 1, 64), (33, 1300, 4, 4, 4, 128), (40, 1200, 1, 4, 2, 256),
-    (2, 20000, 3, 1, 4, 64), (230, 1030, 1, 4, 1, 64), (20, 900, 1, 4, 16, 128)])
+    (2, 20000, 3, 1, 4, 64), (90, 4200, 1, 2, 1, 64), (230, 1030, 1, 4, 1, 64), (20, 900, 1, 4, 16, 128)])
 def test_ragged_batches(S, longest, new, H, group, D):
     """Sequences of very different lengths, one of them alone the longest, empty and refused ones
     among them: however the work is shared, every row is whole."""
