@@ -17,6 +17,11 @@
  *   - FP8 E4M3 row codec: one E4M3 byte per element and a single FP32 scale for
  *     each (token, KV head) row, in a code buffer with the geometry of the bf16 one.
  *     Source: FreeToken PR #408, the fp8 store notes.
+ *   - FP8 E4M3 pages: E4M3 bytes with one power-of-two FP32 scale per (block of tokens,
+ *     head), raised as tokens are appended.
+ * Attention reads the pool as it is: kvq_decode_attention (one query a sequence) and
+ * kvq_attention (several, with score options); kvq_plan_pages makes a step's block tables
+ * and slot ids on the GPU.
  *
  * Conventions shared by every entry point
  *   Memory   every pointer argument that a kernel touches is DEVICE memory

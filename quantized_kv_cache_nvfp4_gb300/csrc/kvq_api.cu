@@ -1,5 +1,5 @@
 // kvq_api.cu -- the C ABI declared in include/kvq.h: argument checks on the host,
-// then one kernel launch on the caller's stream.  Nothing here allocates, frees or
+// then one or two kernel launches on the caller's stream.  Nothing here allocates, frees or
 // synchronises, so every entry point can be captured in a CUDA graph.
 #include <cuda_runtime.h>
 
