@@ -865,18 +865,18 @@ static int attn_split_len(int32_t max_seq_len, int nsplit, int unit) {
   return len > 0 ? static_cast<int>(len) : unit;
 }
 
-size_t attn_workspace_bytes(int32_t S, int32_t H, int32_t Hq, int32_t D, int32_t max_seq_len) {
+size_t attn_workspace_bytes(int32_t S, int32_t H, int32_t Hq, int32_t D, int32_t max_seq_len, bool page_scaled) {
   if (S <= 0 || H <= 0 || Hq <= 0 || D <= 0 || max_seq_len <= 0) return 0;
   // either kernel may serve the call (the choice also depends on the pool's block size)
   int n = attn_num_splits(S, H, max_seq_len);
   const int np = attn_page_splits(S, H, max_seq_len);
   if (np > n) n = np;
-  const int ns = attn_page_scaled_splits(S, H, Hq, D, max_seq_len);
+  const int ns = page_scaled ? attn_page_scaled_splits(S, H, Hq, D, max_seq_len) : 1;
   if (ns > n) n = ns;
   const size_t bytes = n <= 1 ? 0 : static_cast<size_t>(S) * Hq * n * (D + 2) * sizeof(float);
-  // (the format is not known here: the whole-page kernel's partials count too, at most 8 SMs x 64
-  // query heads x 130, or 4 SMs x 128 x 130, or 4 SMs x 64 x 258 of 4 bytes, 40.5 MB on 152 SMs)
-  if ((H != 4 && H != 8) || Hq / H > 16) return bytes;
+  // the whole-page kernel's partials: at most 8 SMs x 64 query heads x 130, or 4 SMs x 128 x 130, or
+  // 4 SMs x 64 x 258 of 4 bytes, 40.5 MB on 152 SMs
+  if (!page_scaled || (H != 4 && H != 8) || Hq / H > 16) return bytes;
   const size_t pages = query_pages_workspace_bytes(S, S, Hq, D, Hq / H, max_seq_len);
   return pages > bytes ? pages : bytes;
 }

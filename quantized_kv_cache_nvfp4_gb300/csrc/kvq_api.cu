@@ -744,7 +744,7 @@ KVQ_API kvq_status kvq_decode_residual(const kvq_packed* payload, const int32_t*
 // of 64: whole 16-token tiles for each of the 4 warps).
 KVQ_API size_t kvq_decode_attention_workspace(int32_t num_seqs, int32_t num_heads, int32_t num_q_heads,
                                               int32_t head_dim, int32_t max_seq_len) {
-  return attn_workspace_bytes(num_seqs, num_heads, num_q_heads, head_dim, max_seq_len);
+  return attn_workspace_bytes(num_seqs, num_heads, num_q_heads, head_dim, max_seq_len, true);  // any format
 }
 
 }  // extern "C"
@@ -800,7 +800,8 @@ kvq_status decode_attention_impl(const kvq_pool* pool, const int32_t* block_tabl
 
   AttnParams p{};
   p.max_len = max_seq_len;
-  const size_t need = kvq_decode_attention_workspace(num_seqs, H, num_q_heads, D, max_seq_len);
+  const bool page_scaled = fk == KVQ_FMT_FP8_PAGE || fv == KVQ_FMT_FP8_PAGE;
+  const size_t need = attn_workspace_bytes(num_seqs, H, num_q_heads, D, max_seq_len, page_scaled);
   if (builtin && need > 0) {
     if (need > attn_builtin_scratch_bytes())
       return fail(KVQ_ERR_UNSUPPORTED, "split partials need %zu bytes, more than the built-in %zu", need,

@@ -277,7 +277,8 @@ struct AttnParams {
 // least 256 tokens.
 int attn_num_splits(int32_t S, int32_t H, int32_t max_seq_len);
 // Workspace bytes for the split partials of a call, whichever kernel serves it.
-size_t attn_workspace_bytes(int32_t S, int32_t H, int32_t Hq, int32_t D, int32_t max_seq_len);
+// page_scaled: of pools with page-scaled planes (at least what the others need)
+size_t attn_workspace_bytes(int32_t S, int32_t H, int32_t Hq, int32_t D, int32_t max_seq_len, bool page_scaled);
 cudaError_t launch_decode_attention(const AttnParams& p, cudaStream_t s);
 // The library's built-in split scratch (device memory in the library image, for the
 // entry point that allocates nothing): its device address and size in bytes.

@@ -288,6 +288,23 @@ def test_decode_without_a_workspace_and_in_a_graph(H, D):
         assert torch.equal(a, b) and torch.equal(a, c)
 
 
+def test_short_sequences_over_row_scales_need_no_workspace():
+    """Only page-scaled pools split below 256 tokens."""
+    lens = [200, 17, 256, 3]
+    for fmt in (F8, NV):
+        pool, table, lt, q, _, Tmax = _decode_case(lens, 8, 4, 128, 16, fmt, None, 3)
+        out, ref = poison_bf16(tuple(q.shape)), poison_bf16(tuple(q.shape))
+        args = (pool, table.to(DEV), lt.to(DEV), Tmax, q.to(DEV), 0.1)
+        kvq.kvq_decode_attention(*args, out, workspace=torch.empty(0, dtype=torch.uint8, device=DEV))
+        kvq.kvq_decode_attention(*args, ref)
+        assert torch.equal(out, ref)
+    pool, table, lt, q, _, Tmax = _decode_case(lens, 8, 4, 128, 16, PG, None, 3)
+    assert kvq.kvq_decode_attention_workspace(4, 8, 32, 128, Tmax) > 0
+    with pytest.raises(Exception, match="workspace"):
+        kvq.kvq_decode_attention(pool, table.to(DEV), lt.to(DEV), Tmax, q.to(DEV), 0.1, poison_bf16(tuple(q.shape)),
+                                 workspace=torch.empty(0, dtype=torch.uint8, device=DEV))
+
+
 def test_nothing_to_attend():
     pool = kvq.KvPool.empty(64, 8, 128, 16, fill=0, fmt=PG)
     z = lambda *s: torch.zeros(s, dtype=torch.int32, device=DEV)
