@@ -10,7 +10,9 @@
 // one KV head and one split of the keys that any of its rows sees; its 4 warps take
 // 16-token tiles in turn through cp.async rings, with the tile arithmetic of the decode
 // kernels (attn_tile.cuh), the score modifier between its two products.  Splits of a
-// sequence merge through the caller's workspace in a second small kernel.
+// sequence merge through the caller's workspace in a second small kernel.  Bound: issue and
+// latency of the tile arithmetic, and gathers of 64 to 256 bytes (16 x 5000 tokens over NVFP4 with
+// bias, 64 query heads, 8-token pages: 44.3 us; 38.3 by whole pages of 16 tokens).
 #include <algorithm>
 
 #include "query_attn.cuh"
@@ -220,15 +222,17 @@ __global__ void __launch_bounds__(kAttnThreads) query_rows_kernel(const QueryAtt
 // longer than their attention's last wave).  A row's warps first find its token's sequence
 // (32-way search over starts): rows of no sequence, or of a refused one, have no partials and
 // stay as they are, as do rows with a NaN mark.
-constexpr int kMergeWarps = 4;
+template <int kPer>
+constexpr int kMergeWarps = kPer > 4 ? kPer : 4;  // of a block
 
 template <int D, int kPer>
-__global__ void __launch_bounds__(32 * kMergeWarps) query_merge_kernel(const QueryAttnParams qp) {
+__global__ void __launch_bounds__(32 * kMergeWarps<kPer>) query_merge_kernel(const QueryAttnParams qp) {
   const AttnParams& p = qp.a;
   constexpr int kDL = D / 32;
-  constexpr int kRows = kMergeWarps / kPer;  // a block
-  __shared__ float2 part_ml[kMergeWarps];
-  __shared__ float part_o[kPer > 1 ? kMergeWarps : 1][D];
+  constexpr int kWarps = kMergeWarps<kPer>;
+  constexpr int kRows = kWarps / kPer;  // a block
+  __shared__ float2 part_ml[kWarps];
+  __shared__ float part_o[kPer > 1 ? kWarps : 1][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % kPer;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + warp / kPer;
   const bool live = row < static_cast<int64_t>(qp.num_tokens) * p.Hq;
@@ -348,8 +352,9 @@ template <int D, int kPer>
 cudaError_t launch_query_merge(const QueryAttnParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   const int64_t rows = static_cast<int64_t>(p.num_tokens) * p.a.Hq;
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + kMergeWarps / kPer - 1) / (kMergeWarps / kPer)));
-  cfg.blockDim = dim3(32 * kMergeWarps);
+  constexpr int kWarps = kMergeWarps<kPer>;
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kWarps / kPer - 1) / (kWarps / kPer)));
+  cfg.blockDim = dim3(32 * kWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -361,9 +366,13 @@ cudaError_t launch_query_merge(const QueryAttnParams& p, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch_query_merge(const QueryAttnParams& p, cudaStream_t s) {
-  // four warps a row for 12 splits and more (shared blocks: the most, twice the usual count; 1600
-  // rows of 6 took 10.2 us by four, 5.6 by one)
-  return p.a.nsplit >= (p.parts != nullptr ? 24 : 12) ? launch_query_merge<D, 4>(p, s) : launch_query_merge<D, 1>(p, s);
+  // Warps a row by its splits (of shared blocks the usual count, half the most).  us of the whole
+  // call by fewer warps and by these: 188 splits of 32 rows 21.5 by four, 16.8 by 8, 15.2 by 16; 76 of
+  // 256 rows 32.8 by four, 31.0 by 8, 34.2 by 16; 6 of 1600 rows, the merge alone, 10.2 by four, 5.6 by one
+  const int n = p.parts != nullptr ? p.a.nsplit / 2 : p.a.nsplit;
+  if (n >= 96) return launch_query_merge<D, 16>(p, s);
+  if (n >= 32) return launch_query_merge<D, 8>(p, s);
+  return n >= 12 ? launch_query_merge<D, 4>(p, s) : launch_query_merge<D, 1>(p, s);
 }
 
 template <int D, int kFK, int kFV, int kNH>
@@ -397,11 +406,14 @@ cudaError_t rows_dispatch(const QueryAttnParams& p, int rows, cudaStream_t s) {
 
 // Kernels and their split counts.  The tile kernel from 17 rows a sequence and KV head on (its
 // cost hardly grows up to 128 rows; the others take 16 at a time); below, whole pages where
-// the layout allows it, else the rows kernel.
+// the layout allows it, else the rows kernel.  16 sequences of 3000 page-scaled tokens, 8 KV heads,
+// head_dim 128, tile and whole-page kernel: 16 rows 52.0, 34.1 us; 20 rows 52.0, 53.3; 32 rows 52.3,
+// 55.9.
 constexpr int kTileFrom = 17;
 
 int tile_splits(int32_t S, int32_t H, int32_t D, int64_t rows, int32_t span) {
-  // one CTA an SM, at least 512 tokens a split
+  // one CTA an SM, at least 512 tokens a split (160 rows a KV head of one sequence: 3000 tokens
+  // 25.6 us, 25.2 at 256, 31.9 at 1024; 12,000 tokens 32.6, 32.7, 35.7)
   const int64_t ctas = static_cast<int64_t>(S) * H * ((rows + query_tile_rows(D) - 1) / query_tile_rows(D));
   return fill_splits(ctas, num_sms(), span, 512, 512);
 }
@@ -423,7 +435,8 @@ struct PagePlan {
   int wave;
 };
 PagePlan page_plan(int32_t S, int32_t D, int64_t rows, int32_t span) {
-  // two blocks an SM (one with 16 rows or head_dim 256)
+  // two blocks an SM (one with 16 rows or head_dim 256); at least 64 keys a split (one sequence
+  // of 500 10.3 us, 11.7 at 96, 13.3 at 128; of 2000 10.7, 12.2, 13.6)
   const int64_t per = page_two(D, rows) ? 16 : 8;
   const int64_t slots = static_cast<int64_t>(per == 16 || D == 256 ? 1 : 2) * num_sms();
   const int64_t ctas = static_cast<int64_t>(S) * ((rows + per - 1) / per);
@@ -437,7 +450,8 @@ PagePlan page_plan(int32_t S, int32_t D, int64_t rows, int32_t span) {
                   static_cast<int>(blocks), static_cast<int>(slots)};
 }
 int row_splits(int32_t S, int32_t H, int64_t rows, int32_t span) {
-  // four CTAs an SM
+  // four CTAs an SM; at least 256 tokens a split (8 KV heads, 1 x 1000 tokens 9.1 us, 7.6 at 128;
+  // 1 x 12,000 11.8, 16.9; 4 x 3000 11.7, 15.9)
   const int64_t ctas = static_cast<int64_t>(S) * H * (rows <= 8 ? 1 : (rows + 15) / 16);
   return fill_splits(ctas, 4ll * num_sms(), span, 256, 256);
 }
