@@ -422,7 +422,10 @@ __device__ __forceinline__ float tile_probs(const RowLogit& r, uint32_t taddr, c
 // The same where both planes are page-scaled and pages are whole groups of 16 columns: K's
 // scale and V's (as its log2) are one pair a group, gs[group] = {ks, log2 vs}.  The scale of
 // the scores is then part of the row's factor, and P' = 2^(y - M + log2 vs) needs no product;
-// the group's sum of P' is divided by vs for l.
+// the group's sum of P' is divided by vs for l.  M may come from steps with much larger scales (a
+// page of zeros has 2^-126), and l has to keep p where P' vanishes: with mx the step's largest
+// logit of the row, log2 vs - M counts as -mx - 40 where it is below that.  P' is then at most
+// 2^-40, 0 in f16 either way, and the sum loses nothing above 2^-86 of the step's largest p.
 template <int kMode, bool kMask, int kBN>
 __device__ __forceinline__ float tile_max_pages(const RowLogit& r, uint32_t taddr, const float2* gs, int t0, float& most) {
   constexpr int kCols = kBN == 128 ? 64 : 32;  // at a time
@@ -472,7 +475,7 @@ __device__ __forceinline__ float tile_max_pages(const RowLogit& r, uint32_t tadd
 }
 
 template <int kMode, bool kMask, int kBN>
-__device__ __forceinline__ float tile_probs_pages(const RowLogit& r, uint32_t taddr, const float2* gs, int t0, float M, uint32_t half) {
+__device__ __forceinline__ float tile_probs_pages(const RowLogit& r, uint32_t taddr, const float2* gs, int t0, float M, float mx, uint32_t half) {
   constexpr int kCols = kBN == 128 ? 64 : 32;  // at a time
   const int lo = r.lo - t0, hi = r.hi - t0;
   const float tf = static_cast<float>(t0 - r.pos);
@@ -480,6 +483,7 @@ __device__ __forceinline__ float tile_probs_pages(const RowLogit& r, uint32_t ta
   cp.init<kMode>(r.c2);
   const uint64_t s2 = dup_f32x2(r.slope);
   float L = 0.0f;
+  const float least = -40.0f - mx;
 #pragma unroll 1
   for (int c0 = 0; c0 < kBN; c0 += kCols) {
     uint32_t v[kCols], h[kCols / 2];
@@ -487,7 +491,7 @@ __device__ __forceinline__ float tile_probs_pages(const RowLogit& r, uint32_t ta
 #pragma unroll
     for (int g = 0; g < kCols / 16; ++g) {
       const float2 s = gs[c0 / 16 + g];
-      const float ref = s.y - M;
+      const float ref = fmaxf(s.y - M, least);
       const uint64_t f2 = dup_f32x2((kMode == kNearCap ? r.fu : kMode == kCapped ? r.fz : r.f) * s.x);
       const uint64_t base = dup_f32x2(__fmaf_rn(r.slope, tf + static_cast<float>(c0 + 16 * g), ref));
       const uint64_t add = dup_f32x2(kMode == kCapped ? r.c2 + ref : ref);
@@ -517,7 +521,7 @@ __device__ __forceinline__ float tile_probs_pages(const RowLogit& r, uint32_t ta
       }
       uint32_t a, b;
       unpack_f32x2(add_f32x2(l[0], l[1]), a, b);
-      L = __fmaf_rn(__uint_as_float(a) + __uint_as_float(b), ex2_ftz(-s.y), L);
+      L = __fmaf_rn(__uint_as_float(a) + __uint_as_float(b), ex2_ftz(-(ref + M)), L);
     }
     tmem_st(taddr + c0 / 2, h);  // columns whose scores are already read
     if (kBN == 64 && c0 == 0) half_ready(half);
@@ -543,9 +547,10 @@ __device__ __forceinline__ float tile_max_any(bool mask, const RowLogit& r, uint
     return mask ? tile_max<kMode, true, kBN>(r, ta, sc.ks, t0, most) : tile_max<kMode, false, kBN>(r, ta, sc.ks, t0, most);
 }
 template <int kMode, int kBN, bool kPages>
-__device__ __forceinline__ float tile_probs_any(bool mask, const RowLogit& r, uint32_t ta, const StepScales& sc, int t0, float M, uint32_t half) {
+__device__ __forceinline__ float tile_probs_any(bool mask, const RowLogit& r, uint32_t ta, const StepScales& sc, int t0, float M, float mx, uint32_t half) {
   if constexpr (kPages)
-    return mask ? tile_probs_pages<kMode, true, kBN>(r, ta, sc.gs, t0, M, half) : tile_probs_pages<kMode, false, kBN>(r, ta, sc.gs, t0, M, half);
+    return mask ? tile_probs_pages<kMode, true, kBN>(r, ta, sc.gs, t0, M, mx, half)
+                : tile_probs_pages<kMode, false, kBN>(r, ta, sc.gs, t0, M, mx, half);
   else
     return mask ? tile_probs<kMode, true, kBN>(r, ta, sc.ks, sc.vs, t0, M, half) : tile_probs<kMode, false, kBN>(r, ta, sc.ks, sc.vs, t0, M, half);
 }
@@ -788,11 +793,9 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
         rowbuf[slot * kBN + 32 * i + lane] = row[i];
         if constexpr (kPages) {
           // a group's scales are those of any of its tokens (the others hold the same, or 0
-          // outside the keys).  A V scale below 2^-60 of the step's largest (0 among them) counts
-          // as that much: its P' is 0 in f16 either way, and l keeps its probabilities
+          // outside the keys); a V scale of 0 counts as 2^-126
           const float kg = group_max<16>(ks[i]), vg = group_max<16>(vs[i]);
-          if (lane % 16 == 0)
-            gsb[slot * (kBN / 16) + 2 * i + lane / 16] = make_float2(kg, fmaxf(lg2(fmaxf(vg, 0x1p-126f)), scale_log2(m) - 60.0f));
+          if (lane % 16 == 0) gsb[slot * (kBN / 16) + 2 * i + lane / 16] = make_float2(kg, lg2(fmaxf(vg, 0x1p-126f)));
         } else {
           ksb[slot * kBN + 32 * i + lane] = ks[i];
           vsb[slot * kBN + 32 * i + lane] = vs[i];
@@ -995,12 +998,12 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
             }
           }
         }
-        if (mode == kPlain) L += tile_probs_any<kPlain, kBN, kPages>(mask, rl, ts, sc, t0, M, p_half + 8 * i);
+        if (mode == kPlain) L += tile_probs_any<kPlain, kBN, kPages>(mask, rl, ts, sc, t0, M, mx, p_half + 8 * i);
         else if (mode == kCapped && __all_sync(0xFFFFFFFFu, most * rl.fu <= kTanhRange))
-          L += tile_probs_any<kNearCap, kBN, kPages>(mask, rl, ts, sc, t0, M, p_half + 8 * i);
-        else if (mode == kCapped) L += tile_probs_any<kCapped, kBN, kPages>(mask, rl, ts, sc, t0, M, p_half + 8 * i);
-        else if (mode == kBiased) L += tile_probs_any<kBiased, kBN, kPages>(mask, rl, ts, sc, t0, M, p_half + 8 * i);
-        else L += tile_probs_any<kBoth, kBN, kPages>(mask, rl, ts, sc, t0, M, p_half + 8 * i);
+          L += tile_probs_any<kNearCap, kBN, kPages>(mask, rl, ts, sc, t0, M, mx, p_half + 8 * i);
+        else if (mode == kCapped) L += tile_probs_any<kCapped, kBN, kPages>(mask, rl, ts, sc, t0, M, mx, p_half + 8 * i);
+        else if (mode == kBiased) L += tile_probs_any<kBiased, kBN, kPages>(mask, rl, ts, sc, t0, M, mx, p_half + 8 * i);
+        else L += tile_probs_any<kBoth, kBN, kPages>(mask, rl, ts, sc, t0, M, mx, p_half + 8 * i);
       }
       tmem_wait_st();
       tc_fence_before();
