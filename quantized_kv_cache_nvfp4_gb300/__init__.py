@@ -276,11 +276,12 @@ def kvq_quant_scatter(k: Optional[torch.Tensor], v: Optional[torch.Tensor], slot
 
 
 def _workspace(nbytes: int, device, stream) -> torch.Tensor:
-    """Scratch of one call, kept from reuse until the call's own stream is done with it."""
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws
+    """Scratch of one call, allocated on the call's own stream: a block that the allocator hands
+    out was freed there, so its former use comes before this one, and its next use after."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def _seq_view(t: torch.Tensor, S: int, Tmax: int, name: str):
