@@ -279,6 +279,7 @@ KVQ_API kvq_status kvq_decode_residual(const kvq_packed* payload, const int32_t*
  * relative to a reference of V's row scales) and the output once to bf16, so
  * |out - exact| <= 2^-9 |exact| + 2^-11 max|v| plus fp32 rounding, where exact is
  * the attention of the decoded rows.
+ * A NaN in a row of q, or in a K row that it sees, makes its output NaN.
  * An empty sequence writes zeros.  A bad length (KVQ_DEV_BAD_SEQLEN) or a block
  * entry outside the pool (KVQ_DEV_BAD_BLOCK) leaves that sequence's output untouched.
  * Every wait of the kernel on a copy into shared memory is bounded (about 0.1 s); one
@@ -361,6 +362,8 @@ typedef struct {
  * Accuracy as kvq_decode_attention (one f16 rounding of P, one bf16 rounding of out; products,
  * maxima and sums in fp32), for V scales between 2^-100 and 2^100; the cap is within 2^-20 of
  * softcap absolutely.  Waits are bounded as there (KVQ_DEV_TIMEOUT).
+ * A NaN in a row of q, or in a K row that a query sees, makes NaN of that query's output and of
+ * no other's; one in a V row may reach every query of its sequence.
  * A sequence whose length is outside [0, min(max_seq_len, max_blocks * block_size)], or whose
  * query rows are outside [0, num_tokens], more than max_query_len or more than its length,
  * keeps its rows of out (KVQ_DEV_BAD_SEQLEN); rows that need a block entry outside the pool

@@ -273,15 +273,15 @@ __global__ void __launch_bounds__(kAttnThreads) decode_attn_kernel(const AttnPar
     const int qh = h * p.group + row;
     if (p.nsplit == 1) {
       if (cta_bad) continue;  // a bad sequence leaves its output untouched
-      const float y = L > 0.0f ? O / L : 0.0f;
+      const float y = L == 0.0f ? 0.0f : O / L;  // a NaN stays one
       STX(p.out + static_cast<int64_t>(s) * p.o_row_pitch + static_cast<int64_t>(qh) * p.o_head_pitch + d,
           static_cast<uint16_t>(pack_bf16x2(y, 0.0f) & 0xFFFFu));
     } else {
       float* const wsr = p.ws + ((static_cast<int64_t>(s) * p.Hq + qh) * p.nsplit + split) * (D + 2);
       STX(wsr + d, O);
       if (d == 0) {
-        STX(wsr + D, M);
-        STX(wsr + D + 1, cta_bad ? __int_as_float(0x7FC00000) : L);  // NaN marks a bad sequence
+        STX(wsr + D, cta_bad ? __int_as_float(0x7FC00000) : M);  // NaN marks a bad sequence (M never is one)
+        STX(wsr + D + 1, L);
       }
     }
   }
@@ -291,8 +291,8 @@ __global__ void __launch_bounds__(kAttnThreads) decode_attn_kernel(const AttnPar
 // sum_k L_k 2^(M_k - M), one warp per (sequence, query head).  Lane k holds split k's
 // M and L (32 splits at a time), the warp reduces them, and each lane sums its D/32
 // dims over the splits.  The O rows of the first kPre splits are loaded together with
-// M and L, so a call with up to kPre splits waits for memory once.  A NaN L (bad
-// sequence) leaves the output untouched.
+// M and L, so a call with up to kPre splits waits for memory once.  A NaN M (bad
+// sequence) leaves the output untouched; a NaN L is a NaN score's and reaches the output.
 constexpr int kMergeWarps = 4;
 
 template <int D>
@@ -319,8 +319,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_attn_merge_kernel(con
   for (int k0 = 0; k0 < p.nsplit; k0 += 32) {
     const int k = k0 + lane;
     if (k < p.nsplit) {
-      M = fmaxf(M, LDX(base + k * (D + 2) + D));
-      bad = bad || isnan(LDX(base + k * (D + 2) + D + 1));
+      const float mk = LDX(base + k * (D + 2) + D);
+      M = fmaxf(M, mk);
+      bad = bad || isnan(mk);
     }
   }
 #pragma unroll
@@ -368,8 +369,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_attn_merge_kernel(con
   uint16_t* const out = p.out + static_cast<int64_t>(s) * p.o_row_pitch + static_cast<int64_t>(qh) * p.o_head_pitch;
 #pragma unroll
   for (int i = 0; i < kDL; i += 2) {
-    const float y0 = L > 0.0f ? o[i] / L : 0.0f;
-    const float y1 = L > 0.0f ? o[i + 1] / L : 0.0f;
+    const float y0 = L == 0.0f ? 0.0f : o[i] / L;
+    const float y1 = L == 0.0f ? 0.0f : o[i + 1] / L;
     STX(reinterpret_cast<uint32_t*>(out + kDL * lane + i), pack_bf16x2(y0, y1));
   }
 }
@@ -623,8 +624,8 @@ __global__ void __launch_bounds__((W + 1) * 32, W == 8 ? 2 : 1) decode_attn_page
 #pragma unroll
       for (int q = 0; q < kMT; ++q) {
         const int d = g * (D / 8) + 2 * q;
-        const float y0 = L[e] > 0.0f ? O[q][e] / L[e] : 0.0f;
-        const float y1 = L[e] > 0.0f ? O[q][e + 2] / L[e] : 0.0f;
+        const float y0 = L[e] == 0.0f ? 0.0f : O[q][e] / L[e];
+        const float y1 = L[e] == 0.0f ? 0.0f : O[q][e + 2] / L[e];
         STX(reinterpret_cast<uint32_t*>(out + d), pack_bf16x2(y0, y1));
       }
     } else {
@@ -636,8 +637,8 @@ __global__ void __launch_bounds__((W + 1) * 32, W == 8 ? 2 : 1) decode_attn_page
         STX(wsr + d + 1, O[q][e + 2]);
       }
       if (g == 0) {
-        STX(wsr + D, M[e]);
-        STX(wsr + D + 1, cta_bad ? __int_as_float(0x7FC00000) : L[e]);  // NaN marks a bad sequence
+        STX(wsr + D, cta_bad ? __int_as_float(0x7FC00000) : M[e]);  // NaN marks a bad sequence
+        STX(wsr + D + 1, L[e]);
       }
     }
   }

@@ -203,15 +203,15 @@ __global__ void __launch_bounds__(kAttnThreads) query_rows_kernel(const QueryAtt
     const int64_t tok = q0 + i;
     if (p.nsplit == 1) {
       if (cta_bad) continue;
-      const float y = L > 0.0f ? O / L : 0.0f;
+      const float y = L == 0.0f ? 0.0f : O / L;
       STX(p.out + tok * p.o_row_pitch + static_cast<int64_t>(qh) * p.o_head_pitch + d,
           static_cast<uint16_t>(pack_bf16x2(y, 0.0f) & 0xFFFFu));
     } else {
       float* const wsr = p.ws + ((tok * p.Hq + qh) * p.nsplit + split) * (D + 2);
       STX(wsr + d, O);
       if (d == 0) {
-        STX(wsr + D, M);
-        STX(wsr + D + 1, cta_bad ? __int_as_float(0x7FC00000) : L);  // NaN marks a bad block entry
+        STX(wsr + D, cta_bad ? __int_as_float(0x7FC00000) : M);  // NaN marks a bad block entry (M never is one)
+        STX(wsr + D + 1, L);
       }
     }
   }
@@ -221,7 +221,8 @@ __global__ void __launch_bounds__(kAttnThreads) query_rows_kernel(const QueryAtt
 // M), by kPer warps a row, which share the splits (one warp walking 76 splits of two rows took
 // longer than their attention's last wave).  A row's warps first find its token's sequence
 // (32-way search over starts): rows of no sequence, or of a refused one, have no partials and
-// stay as they are, as do rows with a NaN mark.
+// stay as they are, as do rows with a NaN mark in place of an M.  A NaN L is a NaN score's and
+// reaches the output.
 template <int kPer>
 constexpr int kMergeWarps = kPer > 4 ? kPer : 4;  // of a block
 
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps<kPer>) query_merge_kernel(con
   for (int k = k_begin + lane; k < k_end; k += 32) {
     const float2 ml = LDX(reinterpret_cast<const float2*>(base + k * (D + 2) + D));
     M = fmaxf(M, ml.x);
-    bad = bad || isnan(ml.y);
+    bad = bad || isnan(ml.x);
   }
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
@@ -317,8 +318,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps<kPer>) query_merge_kernel(con
   for (int off = 16; off >= 1; off >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, off);
   bad = __any_sync(0xFFFFFFFFu, bad);
   if constexpr (kPer > 1) {
-    if (bad) L = __int_as_float(0x7FC00000);
-    if (lane == 0) part_ml[warp] = make_float2(M, L);
+    if (lane == 0) part_ml[warp] = make_float2(bad ? __int_as_float(0x7FC00000) : M, L);
 #pragma unroll
     for (int i = 0; i < kDL; ++i) part_o[warp][kDL * lane + i] = o[i];
     __syncthreads();
@@ -331,19 +331,19 @@ __global__ void __launch_bounds__(32 * kMergeWarps<kPer>) query_merge_kernel(con
 #pragma unroll
     for (int w = 0; w < kPer; ++w) {
       const float2 ml = part_ml[warp + w];
+      bad = bad || isnan(ml.x);
       const float f = ex2(ml.x - M);
       L += ml.y * f;
 #pragma unroll
       for (int i = 0; i < kDL; ++i) o[i] = __fmaf_rn(part_o[warp + w][kDL * lane + i], f, o[i]);
     }
-    bad = isnan(L);
   }
   if (bad) return;
   uint16_t* const out = p.out + static_cast<int64_t>(tok) * p.o_row_pitch + static_cast<int64_t>(qh) * p.o_head_pitch;
 #pragma unroll
   for (int i = 0; i < kDL; i += 2) {
-    const float y0 = L > 0.0f ? o[i] / L : 0.0f;
-    const float y1 = L > 0.0f ? o[i + 1] / L : 0.0f;
+    const float y0 = L == 0.0f ? 0.0f : o[i] / L;
+    const float y1 = L == 0.0f ? 0.0f : o[i + 1] / L;
     STX(reinterpret_cast<uint32_t*>(out + kDL * lane + i), pack_bf16x2(y0, y1));
   }
 }

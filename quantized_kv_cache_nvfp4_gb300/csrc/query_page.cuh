@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(32 * (QueryPage<D, kFK, kFV, kNH>::kW + 1), Qu
         uint16_t* const out = p.out + tok * p.o_row_pitch + static_cast<int64_t>(qh) * p.o_head_pitch;
 #pragma unroll
         for (int q = 0; q < kMT; ++q) {
-          const float y0 = L > 0.0f ? st.o[q][nh][e] / L : 0.0f, y1 = L > 0.0f ? st.o[q][nh][e + 2] / L : 0.0f;
+          const float y0 = L == 0.0f ? 0.0f : st.o[q][nh][e] / L, y1 = L == 0.0f ? 0.0f : st.o[q][nh][e + 2] / L;
           STX(reinterpret_cast<uint32_t*>(out + g * (D / 8) + 2 * q), pack_bf16x2(y0, y1));
         }
       } else {
@@ -383,8 +383,8 @@ __global__ void __launch_bounds__(32 * (QueryPage<D, kFK, kFV, kNH>::kW + 1), Qu
 #pragma unroll
         for (int q = 0; q < kMT; ++q)
           STX(reinterpret_cast<float2*>(wsr + g * (D / 8) + 2 * q), make_float2(st.o[q][nh][e], st.o[q][nh][e + 2]));
-        if (g == 0)  // NaN marks a bad block entry
-          STX(reinterpret_cast<float2*>(wsr + D), make_float2(st.m[nh][e], cta_bad ? __int_as_float(0x7FC00000) : L));
+        if (g == 0)  // a NaN M marks a bad block entry
+          STX(reinterpret_cast<float2*>(wsr + D), make_float2(cta_bad ? __int_as_float(0x7FC00000) : st.m[nh][e], L));
       }
     }
 }

@@ -165,6 +165,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// The larger one, NaN if either is (a select for this took 2% of the capped chunk's time).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ float lg2(float x) {
   float r;
   asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -491,7 +497,7 @@ __device__ __forceinline__ float tile_probs_pages(const RowLogit& r, uint32_t ta
 #pragma unroll
     for (int g = 0; g < kCols / 16; ++g) {
       const float2 s = gs[c0 / 16 + g];
-      const float ref = fmaxf(s.y - M, least);
+      const float ref = max_nan(s.y - M, least);
       const uint64_t f2 = dup_f32x2((kMode == kNearCap ? r.fu : kMode == kCapped ? r.fz : r.f) * s.x);
       const uint64_t base = dup_f32x2(__fmaf_rn(r.slope, tf + static_cast<float>(c0 + 16 * g), ref));
       const uint64_t add = dup_f32x2(kMode == kCapped ? r.c2 + ref : ref);
@@ -792,10 +798,13 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
       for (int i = 0; i < kPer; ++i) {
         rowbuf[slot * kBN + 32 * i + lane] = row[i];
         if constexpr (kPages) {
-          // a group's scales are those of any of its tokens (the others hold the same, or 0
-          // outside the keys); a V scale of 0 counts as 2^-126
-          const float kg = group_max<16>(ks[i]), vg = group_max<16>(vs[i]);
-          if (lane % 16 == 0) gsb[slot * (kBN / 16) + 2 * i + lane / 16] = make_float2(kg, lg2(fmaxf(vg, 0x1p-126f)));
+          // a group's scales are those of any of its tokens within the keys (0 without one); a V
+          // scale of 0 counts as 2^-126
+          const uint32_t has = __ballot_sync(0xFFFFFFFFu, row[i] >= 0) & (lane < 16 ? 0xFFFFu : 0xFFFF0000u);
+          const int from = has != 0u ? __ffs(has) - 1 : lane;
+          const float kg = __shfl_sync(0xFFFFFFFFu, ks[i], from), vg = __shfl_sync(0xFFFFFFFFu, vs[i], from);
+          if (lane % 16 == 0)
+            gsb[slot * (kBN / 16) + 2 * i + lane / 16] = make_float2(kg, lg2(vg < 0x1p-126f ? 0x1p-126f : vg));
         } else {
           ksb[slot * kBN + 32 * i + lane] = ks[i];
           vsb[slot * kBN + 32 * i + lane] = vs[i];
@@ -1023,7 +1032,7 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
     if (!sees) L = 0.0f;
     uint16_t* const out = p.out + tok * p.o_row_pitch + static_cast<int64_t>(head) * p.o_head_pitch;
     float* const wsr = p.ws + ((tok * p.Hq + head) * p.nsplit + split) * (D + 2);
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;  // a NaN stays one
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
       uint32_t o[32];
@@ -1042,7 +1051,7 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
           uint32_t w[4];
 #pragma unroll
           for (int b = 0; b < 4; ++b)
-            w[b] = L > 0.0f ? pack_bf16x2(__uint_as_float(o[e + 2 * b]) * inv, __uint_as_float(o[e + 2 * b + 1]) * inv) : 0u;
+            w[b] = L != 0.0f ? pack_bf16x2(__uint_as_float(o[e + 2 * b]) * inv, __uint_as_float(o[e + 2 * b + 1]) * inv) : 0u;
           store16B(out + c + e, w);
         }
       } else {
@@ -1053,7 +1062,7 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
       }
     }
     if (row >= 0 && p.nsplit > 1)
-      STX(reinterpret_cast<float2*>(wsr + D), make_float2(sees ? M : kNoKey, bad ? __int_as_float(0x7FC00000) : L));
+      STX(reinterpret_cast<float2*>(wsr + D), make_float2(bad ? __int_as_float(0x7FC00000) : sees ? M : kNoKey, L));
     tc_fence_before();
   }
   __syncthreads();
