@@ -38,6 +38,20 @@ __device__ __forceinline__ bool query_range(const QueryAttnParams& p, int s, int
   return true;
 }
 
+// Whether the keys [lo, hi) of sequence s need a block entry outside the pool.  Only rows of a
+// block that met such an entry ask.
+__device__ __forceinline__ bool needs_bad_block(const AttnParams& p, int s, int lo, int hi) {
+  if (lo >= hi) return false;
+  const int32_t* const table = p.block_table + static_cast<int64_t>(s) * p.max_blocks;
+  const uint32_t last = p.div_bs.div(static_cast<uint32_t>(hi) - 1);
+#pragma unroll 1
+  for (uint32_t b = p.div_bs.div(static_cast<uint32_t>(lo)); b <= last; ++b) {
+    const int32_t blk = LDX(table + b);
+    if (blk < 0 || blk >= p.num_blocks) return true;
+  }
+  return false;
+}
+
 // Logits of a tile's scores: sc[nh][e] belongs to row 8 nh + 2c + (e & 1) and token t0 + g +
 // 8 (e >> 1).  Without a cap and a bias the scores stay as they are (qmul then carries the
 // row's factor and log2 e); with one of them they become base-2 logits (qmul is 1).  The

@@ -99,15 +99,46 @@ __global__ void __launch_bounds__(kAttnThreads) query_rows_kernel(const QueryAtt
     int64_t blk = LDX(p.block_table + static_cast<int64_t>(s) * p.max_blocks + bi);
     if (blk < 0 || blk >= p.num_blocks) {
       bad = true;
-      blk = 0;
+      return -2;
     }
     const int64_t row = (blk * p.block_size + bo) * p.H + h;
     srow = lane_page ? blk * p.H + h : row;
     return row;
   };
+  // a tile with tokens of bad block entries: those become zeros, which rows that do not see
+  // them may meet
+  auto issue_around_gaps = [&](int64_t row, int64_t srow, unsigned char* sb) {
+    for (int j = 0; j < 16; ++j) {
+      const int64_t rr = shfl64(row, j);
+      for (int i = lane; i < T::kCK / 16; i += 32) {
+        if (rr >= 0) cp_async16(sb + T::kOffKC + j * T::kSK + i * 16, p.k.codes + rr * T::kCK + i * 16);
+        else *reinterpret_cast<uint4*>(sb + T::kOffKC + j * T::kSK + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      for (int i = lane; i < T::kCV / 16; i += 32) {
+        if (rr >= 0) cp_async16(sb + T::kOffVC + j * T::kSV + i * 16, p.v.codes + rr * T::kCV + i * 16);
+        else *reinterpret_cast<uint4*>(sb + T::kOffVC + j * T::kSV + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    const int tt = lane & 15;
+    if (row < 0) {
+      unsigned char* const b = lane < 16 ? sb + T::kOffKB + tt * T::kBK : sb + T::kOffVB + tt * T::kBV;
+      for (int i = 0; i < (lane < 16 ? T::kBK : T::kBV); ++i) b[i] = 0;
+      *reinterpret_cast<float*>(sb + (lane < 16 ? T::kOffKR : T::kOffVR) + tt * 4) = 0.0f;
+    } else if (lane < 16) {
+      if constexpr (T::kBK > 0) cp_async_n<T::kBK>(sb + T::kOffKB + tt * T::kBK, p.k.bscale + row * T::kBK);
+      cp_async_small<4>(sb + T::kOffKR + tt * 4, p.k.rscale + srow);
+    } else {
+      if constexpr (T::kBV > 0) cp_async_n<T::kBV>(sb + T::kOffVB + tt * T::kBV, p.v.bscale + row * T::kBV);
+      cp_async_small<4>(sb + T::kOffVR + tt * 4, p.v.rscale + srow);
+    }
+  };
   auto issue = [&](int64_t row, int64_t srow, int st) {
-    if (__shfl_sync(0xFFFFFFFFu, row, 0) < 0) return;
+    if (__shfl_sync(0xFFFFFFFFu, row, 0) == -1) return;
     unsigned char* const sb = ring + st * T::kBytes;
+    if (__any_sync(0xFFFFFFFFu, row < 0)) {
+      issue_around_gaps(row, srow, sb);
+      return;
+    }
     const int tt = lane & 15;
     constexpr int kPK = T::kCK / 16, kPV = T::kCV / 16;
 #pragma unroll
@@ -201,8 +232,10 @@ __global__ void __launch_bounds__(kAttnThreads) query_rows_kernel(const QueryAtt
     const int i = (row0 + row) / p.group;
     const int qh = h * p.group + row0 + row - i * p.group;
     const int64_t tok = q0 + i;
+    const int2 seen = tab.range[row];
+    const bool row_bad = cta_bad && needs_bad_block(p, s, max(seen.x, t_begin), min(seen.y, t_end));
     if (p.nsplit == 1) {
-      if (cta_bad) continue;
+      if (row_bad) continue;
       const float y = L == 0.0f ? 0.0f : O / L;
       STX(p.out + tok * p.o_row_pitch + static_cast<int64_t>(qh) * p.o_head_pitch + d,
           static_cast<uint16_t>(pack_bf16x2(y, 0.0f) & 0xFFFFu));
@@ -210,7 +243,7 @@ __global__ void __launch_bounds__(kAttnThreads) query_rows_kernel(const QueryAtt
       float* const wsr = p.ws + ((tok * p.Hq + qh) * p.nsplit + split) * (D + 2);
       STX(wsr + d, O);
       if (d == 0) {
-        STX(wsr + D, cta_bad ? __int_as_float(0x7FC00000) : M);  // NaN marks a bad block entry (M never is one)
+        STX(wsr + D, row_bad ? __int_as_float(0x7FC00000) : M);  // NaN marks a bad block entry (M never is one)
         STX(wsr + D + 1, L);
       }
     }

@@ -217,6 +217,24 @@ __global__ void __launch_bounds__(32 * (QueryPage<D, kFK, kFV, kNH>::kW + 1), Qu
       const uint32_t bytes = __reduce_add_sync(0xFFFFFFFFu, have ? 16u * H * (T::kRow - 8) + ksc + vsc : 0u);
       const bool any_bad = __any_sync(0xFFFFFFFFu, bad);
       if (k >= T::kStages && !mbar_wait(empty0 + 8 * st, ((k / T::kStages) - 1) & 1)) timed_out = true;
+      const uint32_t gaps = __ballot_sync(0xFFFFFFFFu, lane < P && t0 < t_end && !have);
+      if (gaps != 0u) {  // zeros where rows that do not see them meet them
+        auto clear = [&](uint32_t at, uint32_t n) {
+          for (uint32_t o = 16u * lane; o < n; o += 512u)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(ring_s + st * T::kBytes + at + o), "r"(0u) : "memory");
+        };
+        for (uint32_t left = gaps; left != 0u; left &= left - 1) {
+          const uint32_t jr = 16u * H * (__ffs(left) - 1);
+          clear(T::kOffKC + jr * T::kCK, 16u * H * T::kCK);
+          clear(T::kOffVC + jr * T::kCV, 16u * H * T::kCV);
+          clear(T::kOffKB + jr * T::kBK, 16u * H * T::kBK);
+          clear(T::kOffVB + jr * T::kBV, 16u * H * T::kBV);
+          clear(T::kOffKR + jr * 4, ksc);
+          clear(T::kOffVR + jr * 4, vsc);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // copies land here later
+        __syncwarp();
+      }
       if (lane == 0) {
         if (any_bad) *bad_flag = 1;  // published by the arrival below
         mbar_arrive_expect_tx(full0 + 8 * st, bytes);
@@ -370,8 +388,10 @@ __global__ void __launch_bounds__(32 * (QueryPage<D, kFK, kFV, kNH>::kW + 1), Qu
       const int i = row / p.group, qh = h * p.group + row - i * p.group;
       const int64_t tok = q0 + i;
       const float L = st.l[nh][e];
+      const int2 seen = tab.range[8 * nh + 2 * c + e];
+      const bool bad = cta_bad && needs_bad_block(p, s, max(seen.x, t_begin), min(seen.y, t_end));
       if (nsplit == 1) {
-        if (cta_bad) continue;
+        if (bad) continue;
         uint16_t* const out = p.out + tok * p.o_row_pitch + static_cast<int64_t>(qh) * p.o_head_pitch;
 #pragma unroll
         for (int q = 0; q < kMT; ++q) {
@@ -384,7 +404,7 @@ __global__ void __launch_bounds__(32 * (QueryPage<D, kFK, kFV, kNH>::kW + 1), Qu
         for (int q = 0; q < kMT; ++q)
           STX(reinterpret_cast<float2*>(wsr + g * (D / 8) + 2 * q), make_float2(st.o[q][nh][e], st.o[q][nh][e + 2]));
         if (g == 0)  // a NaN M marks a bad block entry
-          STX(reinterpret_cast<float2*>(wsr + D), make_float2(cta_bad ? __int_as_float(0x7FC00000) : st.m[nh][e], L));
+          STX(reinterpret_cast<float2*>(wsr + D), make_float2(bad ? __int_as_float(0x7FC00000) : st.m[nh][e], L));
       }
     }
 }

@@ -1028,7 +1028,8 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
       __syncwarp();
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const bool bad = *reinterpret_cast<volatile int*>(&misc->bad) != 0;
+    const bool bad = *reinterpret_cast<volatile int*>(&misc->bad) != 0 && sees &&
+                     needs_bad_block(p, s, max(rl.lo, t_begin), min(rl.hi, t_end));
     if (!sees) L = 0.0f;
     uint16_t* const out = p.out + tok * p.o_row_pitch + static_cast<int64_t>(head) * p.o_head_pitch;
     float* const wsr = p.ws + ((tok * p.Hq + head) * p.nsplit + split) * (D + 2);
