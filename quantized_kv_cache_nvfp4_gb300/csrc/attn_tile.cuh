@@ -15,6 +15,7 @@ constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kNoKey = -1e30f;  // the softmax reference before the first key, under a mask
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -198,9 +199,15 @@ struct NoMod {
 // m (and m + 8), the partial sum l of this lane's tokens, the V row-scale reference R
 // (R64 = 64 R, rR = 1 / R), and the O^T accumulators o[mt][nh] (dims g*D/8 + 2mt,
 // e = 0, 1, and + 1, e = 2, 3, of heads 8nh + 2c and + 1), relative to R.
+// Under a mask R may come from rows of V that a query does not see.  A query whose own V scales
+// are 2^6 and more below R takes m lower by the difference in powers of two (its shift), so that
+// P' keeps its precision; m8 - 8 is then the reference of its logits.  While any query of the
+// warp is shifted, every tile sets the references anew.  (Where all rows see the same keys, as the
+// heads of one token do, none of this runs: in every tile that moves m it cost 5%.)
 template <int D, int kNH>
 struct AttnState {
   float m[kNH][2], m8[kNH][2], l[kNH][2], R, R64, rR;
+  bool shifted;
   float o[D / 16][kNH][4];
   // m0: the reference before any key; finite where a tile may hold no key that a row sees
   __device__ __forceinline__ void init(float m0 = kNegInf) {
@@ -210,6 +217,7 @@ struct AttnState {
       l[nh][0] = l[nh][1] = 0.0f;
     }
     R = R64 = rR = 0.0f;
+    shifted = false;
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
@@ -344,7 +352,7 @@ __device__ __forceinline__ void attn_tile(const TileView& tv, const QB& qb, cons
     move = move || mt[nh][0] > st.m8[nh][0] || mt[nh][1] > st.m8[nh][1];
   }
   float rmax = fmaxf(vr0, vr1);
-  move = move || rmax > st.R64;
+  move = move || rmax > st.R64 || (Mod::kActive && st.shifted);
   // references: the softmax reference m per head and the V row-scale reference st.R
   // move only when a tile exceeds them by more than 2^8 and 2^6, so P' = exp2(s - m)
   // * rs_v / st.R stays below 2^14 (f16 holds it) and O is rescaled on few tiles
@@ -358,13 +366,58 @@ __device__ __forceinline__ void attn_tile(const TileView& tv, const QB& qb, cons
       }
       rmax = fmaxf(rmax, __shfl_xor_sync(0xFFFFFFFFu, rmax, off));
     }
-    const float Rn = fmaxf(fmaxf(st.R, rmax), 0x1p-126f);
+    // with a mask R holds until a scale exceeds it by 2^6: the smallest shift then tells
+    bool mixed = false;
+    if constexpr (Mod::kActive) mixed = mod.mixed;
+    const bool jump = !mixed || rmax > st.R64 || st.R == 0.0f;
+    const float Rn = jump ? fmaxf(fmaxf(st.R, rmax), 0x1p-126f) : st.R;
     const float rr = st.R / Rn;
+    int shift[kNH][2] = {};
+    bool reset = false;  // the shifts
+    if (mixed) {
+      reset = jump || st.shifted;
+#pragma unroll
+      for (int nh = 0; nh < kNH; ++nh)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) reset = reset || (st.m[nh][e] == kNoKey && mt[nh][e] > kNoKey);
+      reset = __any_sync(0xFFFFFFFFu, reset);
+      if (reset) {
+        auto exponent = [](float x) { return static_cast<int>(__float_as_uint(x) >> 23); };
+        bool any = false;
+#pragma unroll
+        for (int nh = 0; nh < kNH; ++nh)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // the largest scale that the query sees in this tile, and saw before
+            float own = fmaxf(sc[nh][e] > kNegInf ? vr0 : 0.0f, sc[nh][2 + e] > kNegInf ? vr1 : 0.0f);
+#pragma unroll
+            for (int off = 4; off <= 16; off <<= 1) own = fmaxf(own, __shfl_xor_sync(0xFFFFFFFFu, own, off));
+            int top = exponent(own);
+            if (st.m[nh][e] > kNoKey) {
+              const float was = st.shifted ? rintf(st.m8[nh][e] - 8.0f - st.m[nh][e]) : 0.0f;
+              top = max(top, exponent(st.R) - static_cast<int>(was));
+            }
+            const int below = min(exponent(Rn) - top, 100);
+            shift[nh][e] = below >= 6 && fmaxf(st.m[nh][e], mt[nh][e]) > kNoKey ? below : 0;
+            any = any || shift[nh][e] > 0;
+            if (st.shifted) mt[nh][e] = fmaxf(mt[nh][e], st.m8[nh][e] - 8.0f);
+          }
+        any = __any_sync(0xFFFFFFFFu, any);
+        if (!st.shifted) {
+#pragma unroll
+          for (int nh = 0; nh < kNH; ++nh)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) mt[nh][e] = fmaxf(mt[nh][e], st.m[nh][e]);
+        }
+        st.shifted = any;
+      }
+    }
 #pragma unroll
     for (int nh = 0; nh < kNH; ++nh) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float mn = fmaxf(st.m[nh][e], mt[nh][e]);
+        const float ref = reset ? mt[nh][e] : fmaxf(st.m[nh][e], mt[nh][e]);  // of the logits
+        const float mn = Mod::kActive ? ref - static_cast<float>(shift[nh][e]) : ref;
         const float a = ex2(st.m[nh][e] - mn);  // 0 while m is -inf
         const float f = a * rr;
 #pragma unroll
@@ -374,7 +427,7 @@ __device__ __forceinline__ void attn_tile(const TileView& tv, const QB& qb, cons
         }
         st.l[nh][e] *= a;
         st.m[nh][e] = mn;
-        st.m8[nh][e] = mn + 8.0f;
+        st.m8[nh][e] = ref + 8.0f;
       }
     }
     st.R = Rn;

@@ -8,8 +8,6 @@ namespace kvq {
 
 namespace {
 
-constexpr float kNoKey = -1e30f;  // the softmax reference before the first key
-
 // Range of keys that query token `tok` at position pos sees.
 __device__ __forceinline__ void key_range(const QueryAttnParams& p, int s, int tok, int pos, int len, int& lo, int& hi) {
   lo = 0;
@@ -70,6 +68,7 @@ struct QueryMod {
   int hw;               // the head's place in tab->bias
   float f[kNH][2];      // the row's factor: times 2 log2 e / cap, else times log2 e
   int lo_all, hi_all;   // keys that every row sees
+  bool mixed;           // and whether some see others too
   float c2;             // cap log2 e, 0: no cap
   bool biased;
   int t0, g;            // first token of the tile; this lane's tokens are t0 + g and + 8
@@ -100,6 +99,7 @@ struct QueryMod {
     const bool live = lane < 8 * kNH && row0 + lane < rows;
     lo_all = __reduce_max_sync(0xFFFFFFFFu, live ? lo : 0);  // INT_MAX with a row that sees nothing
     hi_all = __reduce_min_sync(0xFFFFFFFFu, live ? hi : 0x7FFFFFFF);
+    mixed = __any_sync(0xFFFFFFFFu, live && (lo != lo_all || hi != hi_all));
 #pragma unroll
     for (int nh = 0; nh < kNH; ++nh)
 #pragma unroll

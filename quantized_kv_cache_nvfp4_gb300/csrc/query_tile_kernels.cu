@@ -322,13 +322,20 @@ __device__ __forceinline__ uint64_t bias2(uint64_t slope, int col, uint64_t base
   return fma_f32x2(slope, pack_f32x2(__float_as_uint(static_cast<float>(col)), __float_as_uint(static_cast<float>(col + 1))), base);
 }
 
+// log2 of the largest V scale as the reference takes it, clamped far outside what rows of
+// ordinary size need.
+__device__ __forceinline__ float scale_log2(float v) { return fminf(fmaxf(lg2(v), -100.0f), 100.0f); }
+
 // Largest logit of a tile's row (-inf where it sees no key of the tile).
-// most: the largest |score| (kCapped only).
+// most: the largest |score| (kCapped only).  lv: log2 of the largest V scale of the keys that the
+// row sees, where the mask leaves some out (a row that took louder ones into its reference would
+// lose its own P' to f16's range).
 template <int kMode, bool kMask, int kBN>
-__device__ __forceinline__ float tile_max(const RowLogit& r, uint32_t taddr, const float* ks, int t0, float& most) {
+__device__ __forceinline__ float tile_max(const RowLogit& r, uint32_t taddr, const float* ks, const float* vs, int t0, float& most,
+                                          float& lv) {
   const int lo = r.lo - t0, hi = r.hi - t0;
   const float tf = static_cast<float>(t0 - r.pos);
-  float m0 = kNegInf, m1 = kNegInf, a0 = 0.0f;
+  float m0 = kNegInf, m1 = kNegInf, a0 = 0.0f, v0 = 0.0f;
   const uint64_t f2 = dup_f32x2(r.f), s2 = dup_f32x2(r.slope);
 #pragma unroll 1
   for (int c0 = 0; c0 < kBN; c0 += 32) {
@@ -352,7 +359,11 @@ __device__ __forceinline__ float tile_max(const RowLogit& r, uint32_t taddr, con
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (kMode == kBoth) y[e] = logit<kMode>(r, y[e], tf, c0 + i + e);
-        if (kMask) y[e] = c0 + i + e >= lo && c0 + i + e < hi ? y[e] : kNegInf;
+        if (kMask) {
+          const bool in = c0 + i + e >= lo && c0 + i + e < hi;
+          y[e] = in ? y[e] : kNegInf;
+          v0 = fmaxf(v0, in ? vs[c0 + i + e] : 0.0f);
+        }
       }
       m0 = max3(m0, y[0], y[1]);
       m1 = max3(m1, y[2], y[3]);
@@ -360,6 +371,7 @@ __device__ __forceinline__ float tile_max(const RowLogit& r, uint32_t taddr, con
   }
   const float m = fmaxf(m0, m1);
   most = a0;
+  if (kMask) lv = scale_log2(v0);
   // without a bias the logit grows with the score, so it is taken once
   if (kMode == kBiased || kMode == kBoth || (kMask && m == kNegInf)) return m;
   return logit<kMode>(r, m, 0.0f, 0);
@@ -433,13 +445,15 @@ __device__ __forceinline__ float tile_probs(const RowLogit& r, uint32_t taddr, c
 // logit of the row, log2 vs - M counts as -mx - 40 where it is below that.  P' is then at most
 // 2^-40, 0 in f16 either way, and the sum loses nothing above 2^-86 of the step's largest p.
 template <int kMode, bool kMask, int kBN>
-__device__ __forceinline__ float tile_max_pages(const RowLogit& r, uint32_t taddr, const float2* gs, int t0, float& most) {
+__device__ __forceinline__ float tile_max_pages(const RowLogit& r, uint32_t taddr, const float2* gs, int t0, float& most,
+                                                float& lv) {
   constexpr int kCols = kBN == 128 ? 64 : 32;  // at a time
   const int lo = r.lo - t0, hi = r.hi - t0;
   const float tf = static_cast<float>(t0 - r.pos);
   const uint64_t s2 = dup_f32x2(r.slope);
   float best = kNegInf;
   most = 0.0f;
+  if (kMask) lv = -100.0f;
 #pragma unroll 1
   for (int c0 = 0; c0 < kBN; c0 += kCols) {
     uint32_t v[kCols];
@@ -447,6 +461,7 @@ __device__ __forceinline__ float tile_max_pages(const RowLogit& r, uint32_t tadd
 #pragma unroll
     for (int g = 0; g < kCols / 16; ++g) {
       const float ks = gs[c0 / 16 + g].x;
+      if (kMask) lv = fmaxf(lv, c0 + 16 * g < hi && c0 + 16 * g + 16 > lo ? fminf(gs[c0 / 16 + g].y, 100.0f) : -100.0f);
       float m[2] = {kNegInf, kNegInf}, a = 0.0f;
       const uint64_t f2 = dup_f32x2(r.f * ks);
       const uint64_t base = dup_f32x2(r.slope * (tf + static_cast<float>(c0 + 16 * g)));
@@ -535,10 +550,6 @@ __device__ __forceinline__ float tile_probs_pages(const RowLogit& r, uint32_t ta
   return L;
 }
 
-// log2 of a step's largest V scale as the reference takes it, clamped far outside what rows of
-// ordinary size need.
-__device__ __forceinline__ float scale_log2(float v) { return fminf(fmaxf(lg2(v), -100.0f), 100.0f); }
-
 // Where a step's scales are: K's and V's by token, or the groups' pairs.
 struct StepScales {
   const float *ks, *vs;
@@ -546,11 +557,13 @@ struct StepScales {
 };
 
 template <int kMode, int kBN, bool kPages>
-__device__ __forceinline__ float tile_max_any(bool mask, const RowLogit& r, uint32_t ta, const StepScales& sc, int t0, float& most) {
+__device__ __forceinline__ float tile_max_any(bool mask, const RowLogit& r, uint32_t ta, const StepScales& sc, int t0, float& most,
+                                              float& lv) {
   if constexpr (kPages)
-    return mask ? tile_max_pages<kMode, true, kBN>(r, ta, sc.gs, t0, most) : tile_max_pages<kMode, false, kBN>(r, ta, sc.gs, t0, most);
+    return mask ? tile_max_pages<kMode, true, kBN>(r, ta, sc.gs, t0, most, lv) : tile_max_pages<kMode, false, kBN>(r, ta, sc.gs, t0, most, lv);
   else
-    return mask ? tile_max<kMode, true, kBN>(r, ta, sc.ks, t0, most) : tile_max<kMode, false, kBN>(r, ta, sc.ks, t0, most);
+    return mask ? tile_max<kMode, true, kBN>(r, ta, sc.ks, sc.vs, t0, most, lv)
+                : tile_max<kMode, false, kBN>(r, ta, sc.ks, sc.vs, t0, most, lv);
 }
 template <int kMode, int kBN, bool kPages>
 __device__ __forceinline__ float tile_probs_any(bool mask, const RowLogit& r, uint32_t ta, const StepScales& sc, int t0, float M, float mx, uint32_t half) {
@@ -983,13 +996,12 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
         for (int c = 0; c < kBN / 2; c += 16) tmem_st16(ts + c, z);
         if (kHalves) half_ready(p_half + 8 * i);
       } else {
-        float mx, most;
-        if (mode == kPlain) mx = tile_max_any<kPlain, kBN, kPages>(mask, rl, ts, sc, t0, most);
-        else if (mode == kCapped) mx = tile_max_any<kCapped, kBN, kPages>(mask, rl, ts, sc, t0, most);
-        else if (mode == kBiased) mx = tile_max_any<kBiased, kBN, kPages>(mask, rl, ts, sc, t0, most);
-        else mx = tile_max_any<kBoth, kBN, kPages>(mask, rl, ts, sc, t0, most);
+        float mx, most, lv = scale_log2(vm);
+        if (mode == kPlain) mx = tile_max_any<kPlain, kBN, kPages>(mask, rl, ts, sc, t0, most, lv);
+        else if (mode == kCapped) mx = tile_max_any<kCapped, kBN, kPages>(mask, rl, ts, sc, t0, most, lv);
+        else if (mode == kBiased) mx = tile_max_any<kBiased, kBN, kPages>(mask, rl, ts, sc, t0, most, lv);
+        else mx = tile_max_any<kBoth, kBN, kPages>(mask, rl, ts, sc, t0, most, lv);
         // V's scales enter P', so the reference covers them
-        const float lv = scale_log2(vm);
         const bool move = mx + lv > M + 8.0f;
         if (__any_sync(0xFFFFFFFFu, move)) {
           const float Mn = move ? mx + lv : M;
