@@ -58,8 +58,9 @@ __device__ __forceinline__ bool needs_bad_block(const AttnParams& p, int s, int 
 template <int kNH>
 struct QueryMod {
   static constexpr bool kActive = true;
-  // Shared: the rows' key ranges, and for each row of the warp's head {slope log2 e, position}
-  // (a position is exact below 2^24; the bias of farther keys is rounded anyway).
+  // Shared: the rows' key ranges, and for each row of the warp's head {slope log2 e, position};
+  // positions count from the block's first row's, so that near keys' distances are exact at any
+  // position (those of keys farther than 2^24 are rounded).
   struct Tables {
     int2 range[8 * kNH];
     float2 bias[16][8 * kNH];
@@ -71,26 +72,28 @@ struct QueryMod {
   bool mixed;           // and whether some see others too
   float c2;             // cap log2 e, 0: no cap
   bool biased;
+  int base;             // position of the block's first row
   int t0, g;            // first token of the tile; this lane's tokens are t0 + g and + 8
 
   // Fills the tables (a barrier follows): the block's ranges (row r's in lane r) by one warp,
   // the head's biases by one warp of each head.
   static __device__ __forceinline__ void fill(Tables* tab, const QueryAttnParams& qp, int lane, int h, int hw, int row0,
-                                              int rows, int first_pos, int lo, int hi, bool ranges, bool biases) {
+                                              int rows, int lo, int hi, bool ranges, bool biases) {
     if (lane >= 8 * kNH) return;
     if (ranges) tab->range[lane] = make_int2(lo, hi);
     if (biases && qp.slopes != nullptr) {
       const int row = min(row0 + lane, rows - 1), i = row / qp.a.group;
       tab->bias[hw][lane] = make_float2(LDX(qp.slopes + h * qp.a.group + row - i * qp.a.group) * kLog2e,
-                                        static_cast<float>(first_pos + i));
+                                        static_cast<float>(i - row0 / qp.a.group));
     }
   }
   // row_fac[nh]: the factor of row 8 nh + g; lo, hi: the range of row `lane`.
   __device__ __forceinline__ void init(const Tables* t, const QueryAttnParams& qp, int lane, int head_place, int row0, int rows,
-                                       int lo, int hi, const float (&row_fac)[kNH], float (&qmul)[kNH][2]) {
+                                       int first_pos, int lo, int hi, const float (&row_fac)[kNH], float (&qmul)[kNH][2]) {
     const int c = lane & 3;
     tab = t;
     hw = head_place;
+    base = first_pos + row0 / qp.a.group;
     g = lane >> 2;
     c2 = qp.softcap * kLog2e;
     biased = qp.slopes != nullptr;
@@ -125,7 +128,7 @@ struct QueryMod {
         for (int e = 0; e < 4; ++e) sc[nh][e] *= f[nh][e & 1];
     }
     if (biased) {
-      const float t[2] = {static_cast<float>(t0 + g), static_cast<float>(t0 + g + 8)};
+      const float t[2] = {static_cast<float>(t0 - base + g), static_cast<float>(t0 - base + g + 8)};
 #pragma unroll
       for (int nh = 0; nh < kNH; ++nh) {
         const float4 b = *reinterpret_cast<const float4*>(&tab->bias[hw][8 * nh + 2 * c]);

@@ -71,11 +71,11 @@ __global__ void __launch_bounds__(kAttnThreads) query_rows_kernel(const QueryAtt
     }
   }
   __shared__ __align__(16) typename QueryMod<kNH>::Tables tab;
-  QueryMod<kNH>::fill(&tab, qp, lane, h, 0, row0, rows, len - nq, lo, hi, warp == 0, warp == 0);
+  QueryMod<kNH>::fill(&tab, qp, lane, h, 0, row0, rows, lo, hi, warp == 0, warp == 0);
   __syncthreads();
   QueryMod<kNH> mod;
   float qmul[kNH][2];
-  mod.init(&tab, qp, lane, 0, row0, rows, lo, hi, row_fac, qmul);
+  mod.init(&tab, qp, lane, 0, row0, rows, len - nq, lo, hi, row_fac, qmul);
   auto qb = [&](int nh, int kb) -> uint2 {
     if constexpr (kQReg) {
       return qreg[nh][kb];

@@ -275,11 +275,11 @@ __global__ void __launch_bounds__(32 * (QueryPage<D, kFK, kFV, kNH>::kW + 1), Qu
     }
   }
   __shared__ __align__(16) typename QueryMod<kNH>::Tables tab;
-  QueryMod<kNH>::fill(&tab, qp, lane, h, h, row0, rows, len - nq, lo, hi, warp == 0, j == 0);
+  QueryMod<kNH>::fill(&tab, qp, lane, h, h, row0, rows, lo, hi, warp == 0, j == 0);
   asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
   QueryMod<kNH> mod;
   float qmul[kNH][2];
-  mod.init(&tab, qp, lane, h, row0, rows, lo, hi, row_fac, qmul);
+  mod.init(&tab, qp, lane, h, row0, rows, len - nq, lo, hi, row_fac, qmul);
   auto qb = [&](int nh, int kb) -> uint2 {
     if constexpr (kQReg) {
       return qreg[nh][kb];
