@@ -269,7 +269,8 @@ KVQ_API kvq_status kvq_decode_residual(const kvq_packed* payload, const int32_t*
  *        and q->head_pitch (per head), inner stride 1; 16-byte aligned.
  *   out  bf16, indexed the same way through its own pitches.
  *   head_dim 64, 128 or 256; num_q_heads a multiple of num_heads, at most 16 query
- *   heads per KV head.  seq_lens[s] <= min(max_seq_len, max_blocks * block_size).
+ *   heads per KV head.  seq_lens[s] <= min(max_seq_len, max_blocks * block_size), which may
+ *   be up to 2^31 - 65536 tokens (KVQ_ERR_UNSUPPORTED above).
  *   scale  positive and finite (KVQ_ERR_INVALID_ARG otherwise).
  *   workspace  device memory of kvq_decode_attention_workspace(...) bytes, 16-byte
  *              aligned (may be NULL when that is 0); caller-owned, reused by the next
@@ -354,6 +355,7 @@ typedef struct {
  * whatever they hold.
  *   q, out        bf16 [num_tokens][num_q_heads][head_dim] through their own pitches.
  *   max_query_len at least the largest n (at most max_seq_len is used).
+ *   min(max_seq_len, max_blocks * block_size) up to 2^31 - 65536 tokens (KVQ_ERR_UNSUPPORTED above).
  *   head_dim 64, 128 or 256; at most 16 query heads per KV head; scale positive, finite.
  *   options       host struct, read during the call; NULL: plain causal attention.
  *   workspace     device memory of kvq_attention_workspace(...) bytes, 16-byte aligned (may be

@@ -37,6 +37,7 @@
 //    largest element in [2^14, 2^15), undone in the score multiplier.
 //  * The warps of a CTA merge through shared memory; several splits of a sequence
 //    merge through the caller's workspace in a second small kernel.
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
@@ -63,7 +64,7 @@ __global__ void __launch_bounds__(kAttnThreads) decode_attn_kernel(const AttnPar
   const int len = LDX(p.seq_lens + s);
   const bool bad_len = len < 0 || len > p.seq_cap;
   const int t_begin = split * p.split_len;
-  const int t_end = bad_len ? t_begin : min(t_begin + p.split_len, len);
+  const int t_end = bad_len ? t_begin : t_begin + min(p.split_len, len - t_begin);
   const int ntile = t_end > t_begin ? (t_end - t_begin + 15) / 16 : 0;
   if (bad_len && threadIdx.x == 0 && split == 0 && h == 0) set_status(p.status, 8u);
 
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__((W + 1) * 32, W == 8 ? 2 : 1) decode_attn_page
   const int len = LDX(p.seq_lens + s);
   const bool bad_len = len < 0 || len > p.seq_cap;
   const int t_begin = split * p.split_len;
-  const int t_end = bad_len ? t_begin : min(t_begin + p.split_len, len);
+  const int t_end = bad_len ? t_begin : t_begin + min(p.split_len, len - t_begin);
   const int nstage = t_end > t_begin ? (t_end - t_begin + 16 * P - 1) / (16 * P) : 0;
   if (bad_len && threadIdx.x == 0 && split == 0) set_status(p.status, 8u);
 
@@ -796,7 +797,7 @@ int attn_num_splits(int32_t S, int32_t H, int32_t max_seq_len) {
   const int64_t pairs = static_cast<int64_t>(S) * H;
   if (pairs <= 0 || max_seq_len <= 0) return 1;
   const int64_t slots = static_cast<int64_t>(kAttnCtasPerSm) * num_sms();  // CTAs resident at once
-  int64_t cap = (max_seq_len + 255) / 256;                                  // >= 256 tokens per split
+  int64_t cap = (static_cast<int64_t>(max_seq_len) + 255) / 256;                                  // >= 256 tokens per split
   const int64_t waves_cap = (kAttnMaxWaves * slots) / pairs;                  // <= kAttnMaxWaves waves
   if (waves_cap < cap) cap = waves_cap;
   if (cap > 64) cap = 64;
@@ -831,7 +832,7 @@ bool attn_page_ok(int32_t block_size, int32_t H, int32_t D, int32_t group, bool 
 int attn_page_splits(int32_t S, int32_t H, int32_t max_seq_len) {
   if (S <= 0 || H <= 0 || max_seq_len <= 0) return 1;
   const int64_t slots = static_cast<int64_t>(H == 16 ? 1 : 2) * num_sms();
-  int64_t cap = (max_seq_len + 255) / 256;
+  int64_t cap = (static_cast<int64_t>(max_seq_len) + 255) / 256;
   const int64_t scratch_cap = (static_cast<int64_t>(kAttnCtasPerSm) * kAttnMaxWaves * num_sms()) /
                               (static_cast<int64_t>(S) * H);
   if (scratch_cap < cap) cap = scratch_cap;
@@ -863,7 +864,7 @@ int attn_page_scaled_splits(int32_t S, int32_t H, int32_t Hq, int32_t D, int32_t
 static int attn_split_len(int32_t max_seq_len, int nsplit, int unit) {
   const int64_t per = (static_cast<int64_t>(max_seq_len) + nsplit - 1) / nsplit;
   const int64_t len = ((per + unit - 1) / unit) * unit;
-  return len > 0 ? static_cast<int>(len) : unit;
+  return len > 0 ? static_cast<int>(std::min(len, int64_t{0x7FFFFFC0})) : unit;  // a multiple of both units
 }
 
 size_t attn_workspace_bytes(int32_t S, int32_t H, int32_t Hq, int32_t D, int32_t max_seq_len, bool page_scaled) {

@@ -3,6 +3,8 @@
 // synchronises, so every entry point can be captured in a CUDA graph.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -751,6 +753,9 @@ KVQ_API size_t kvq_decode_attention_workspace(int32_t num_seqs, int32_t num_head
 
 namespace {
 
+// Token positions are int32, and the kernels' run a few tiles past a sequence's end.
+constexpr int64_t kMaxSeqTokens = 0x7FFF0000;
+
 // Plane formats as the attention kernels take them: page-scaled FP8 is FP8 with another
 // scale index.
 void set_plane_fmts(AttnParams& p, int32_t fk, int32_t fv) {
@@ -785,6 +790,8 @@ kvq_status decode_attention_impl(const kvq_pool* pool, const int32_t* block_tabl
   if (!(scale > 0.0f && scale <= 3.4028235e38f))
     return fail(KVQ_ERR_INVALID_ARG, "scale must be positive and finite (got %g)", static_cast<double>(scale));
   if (num_seqs > 65535 || H > 65535) return fail(KVQ_ERR_UNSUPPORTED, "num_seqs and num_heads must be <= 65535");
+  if (std::min(static_cast<int64_t>(max_blocks) * pool->block_size, static_cast<int64_t>(max_seq_len)) > kMaxSeqTokens)
+    return fail(KVQ_ERR_UNSUPPORTED, "sequences of more than 2^31 - 65536 tokens");
   if (num_seqs == 0) return KVQ_OK;
   if (!fits_u31(static_cast<int64_t>(num_seqs) * num_q_heads * D))
     return fail(KVQ_ERR_UNSUPPORTED, "num_seqs x num_q_heads x head_dim too large");
@@ -914,6 +921,8 @@ KVQ_API kvq_status kvq_attention(const kvq_pool* pool, const int32_t* block_tabl
     return fail(KVQ_ERR_UNSUPPORTED, "softcap outside 2^-10 .. 2^10 (got %g)", static_cast<double>(o.softcap));
   if (o.window < 0) return fail(KVQ_ERR_INVALID_ARG, "negative window");
   if (num_seqs > 65535 || H > 65535) return fail(KVQ_ERR_UNSUPPORTED, "num_seqs and num_heads must be <= 65535");
+  if (std::min(static_cast<int64_t>(max_blocks) * pool->block_size, static_cast<int64_t>(max_seq_len)) > kMaxSeqTokens)
+    return fail(KVQ_ERR_UNSUPPORTED, "sequences of more than 2^31 - 65536 tokens");
   if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return KVQ_OK;
   if (!fits_u31(static_cast<int64_t>(num_tokens) * num_q_heads) ||
       !fits_u31(static_cast<int64_t>(max_query_len) * num_q_heads))

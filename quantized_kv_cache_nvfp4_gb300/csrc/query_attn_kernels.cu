@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kAttnThreads) query_rows_kernel(const QueryAtt
   if (lo_min < hi_max) {  // equal splits, in whole tiles for the four warps
     const int per = ((hi_max - lo_min + p.nsplit - 1) / p.nsplit + 63) / 64 * 64;
     t_begin = static_cast<int>(min(static_cast<int64_t>(lo_min) + static_cast<int64_t>(split) * per, static_cast<int64_t>(hi_max)));
-    t_end = min(t_begin + per, hi_max);
+    t_end = t_begin + min(per, hi_max - t_begin);
   }
   const int ntile = (t_end - t_begin + 15) / 16;
 

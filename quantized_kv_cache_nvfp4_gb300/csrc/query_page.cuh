@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(32 * (QueryPage<D, kFK, kFV, kNH>::kW + 1), Qu
     const int first = lo_min & ~15, unit = 16 * P;
     const int per = ((hi_max - first + nsplit - 1) / nsplit + unit - 1) / unit * unit;
     t_begin = static_cast<int>(min(static_cast<int64_t>(first) + static_cast<int64_t>(split) * per, static_cast<int64_t>(hi_max)));
-    t_end = min(t_begin + per, hi_max);
+    t_end = t_begin + min(per, hi_max - t_begin);
   }
   const int nstage = t_end > t_begin ? (t_end - t_begin + 16 * P - 1) / (16 * P) : 0;
 

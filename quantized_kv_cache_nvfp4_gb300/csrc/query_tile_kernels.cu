@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
     const int first = kPages ? key_lo & ~15 : key_lo;  // groups of 16 columns lie in one page
     const int per = ((key_hi - first + p.nsplit - 1) / p.nsplit + kBN - 1) / kBN * kBN;
     t_begin = static_cast<int>(min(static_cast<int64_t>(first) + static_cast<int64_t>(split) * per, static_cast<int64_t>(key_hi)));
-    t_end = min(t_begin + per, key_hi);
+    t_end = t_begin + min(per, key_hi - t_begin);
   }
   const int steps = (t_end - t_begin + kBN - 1) / kBN;
 

@@ -17,9 +17,9 @@ from test_query_attention_gpu import decoded
 PG, F8, NV = kvq.FMT_FP8_PAGE, kvq.FMT_FP8, kvq.FMT_NVFP4
 
 
-def far_case(L, n, H, group, D, bs, fmt, window, slopes=None, softcap=0.0, seed=71):
+def far_case(L, n, H, group, D, bs, fmt, window, slopes=None, softcap=0.0, seed=71, real=4):
     """(out, status, reference, bound) of n query tokens at the end of a sequence of L tokens."""
-    real = 4  # the last pages, which the window reaches; page 0 of the pool stands for the others
+    # real: the last pages, which the window reaches; page 0 of the pool stands for the others
     mb = -(-L // bs)
     table = torch.zeros((1, mb), dtype=torch.int32)
     table[0, mb - real:] = torch.arange(1, real + 1, dtype=torch.int32)
@@ -53,3 +53,49 @@ def test_bias_at_far_positions(L, H, group, D, bs, fmt, n):
     for cap in (0.0, 20.0):
         got, st, ref, bound = far_case(L, n, H, group, D, bs, fmt, 200, slopes, cap)
         assert st == 0 and (np.abs(got - ref) <= bound).all(), np.nanmax(np.abs(got - ref) / bound)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,group,D,fmt", [(8, 2, 128, PG), (2, 4, 64, NV), (3, 4, 128, F8)])
+@pytest.mark.parametrize("n", [1, 3, 60])
+def test_the_longest_sequences(H, group, D, fmt, n):
+    """Every position up to the last one allowed."""
+    got, st, ref, bound = far_case(2 ** 31 - 65536, n, H, group, D, 16384, fmt, 300, real=2)
+    assert st == 0 and (np.abs(got - ref) <= bound).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,group,D,bs,fmt", [(8, 2, 128, 16, NV), (8, 2, 128, 16, PG), (3, 2, 64, 16, F8), (2, 2, 256, 8, NV)])
+def test_no_limit_given(H, group, D, bs, fmt):
+    """max_seq_len of INT_MAX: the block table alone limits the lengths."""
+    from test_query_attention_gpu import Case
+
+    for S in (3, 300):
+        c = Case([20 + s % 30 for s in range(S)], [1] * S, H, group, D, bs, fmt, seed=72)
+        out, st = c.run(max_len=2 ** 31 - 1)
+        assert st == 0
+        c.check(out, seqs=range(0, S, 17))
+        out, st = poison_bf16((S, H * group, D)), status_word()
+        ws = torch.empty(max(16, kvq.kvq_decode_attention_workspace(S, H, H * group, D, 2 ** 31 - 1)), dtype=torch.uint8, device=DEV)
+        kvq.kvq_decode_attention(c.pool, c.table.to(DEV), torch.tensor(c.lens, dtype=torch.int32, device=DEV), 2 ** 31 - 1,
+                                 c.q[:S].to(DEV), c.scale, out, ws, st)
+        assert int(st.item()) == 0
+        c.check(out, seqs=range(0, S, 17))
+
+
+def test_longer_ones_are_refused(kvq_lib_path):
+    import ctypes
+
+    from quantized_kv_cache_nvfp4_gb300 import _abi
+
+    lib = _abi.load()
+    q, o = _abi.Bf16In(None, 1024, 128), _abi.Bf16Out(None, 1024, 128)
+    for fmt in (PG, F8, NV):
+        pool = _abi.Pool(_abi.Plane(), _abi.Plane(), 64, 16, 2, 128, fmt)
+        for blocks, most, want in ((1 << 27, 2 ** 31 - 1, 2), (1 << 27, 2 ** 31 - 65535, 2), (1 << 27, 2 ** 31 - 65536, 1), (4, 2 ** 31 - 1, 1)):
+            st = lib.kvq_attention(ctypes.byref(pool), None, 1, blocks, None, most, ctypes.byref(q), None, 8, 8, 8, 0.1, None,
+                                   ctypes.byref(o), None, 0, None, None)
+            assert st == want and (b"tokens" in lib.kvq_last_error()) == (want == 2)
+            st = lib.kvq_decode_attention(ctypes.byref(pool), None, 1, blocks, None, most, ctypes.byref(q), 8, 0.1, ctypes.byref(o),
+                                          None, 0, None, None)
+            assert st == want and (b"tokens" in lib.kvq_last_error()) == (want == 2)
