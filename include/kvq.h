@@ -187,9 +187,9 @@ typedef struct {
  * slot_ids raise the page's scale together.  With s0 the stored scale (none where it is
  * not a positive finite number, or where these rows hold the page's first slot, which
  * starts the page over):
- *   s = max(s0, the smallest power of two p >= 2^-126 with max|x| <= 448 p)
- *   codes E4M3(x * (1 / s)); where s > s0 > 0 the page's other rows become
- *   E4M3(code * (s0 / s)), whatever they hold.
+ *   s = max(s0, the smallest power of two p >= 2^-126 with |x| <= 448 p for every finite x)
+ *   codes E4M3(x * (1 / s)), an infinity as the largest code of its sign; where s > s0 > 0
+ *   the page's other rows become E4M3(code * (s0 / s)), whatever they hold.
  * All rows of a (page, head) in one call must stand next to each other (a skipped token
  * ends a run): two runs on one page, like duplicate ids, leave that page's codes and
  * scale unspecified.

@@ -5,7 +5,9 @@
 // float code loses nothing but its smallest binade to the factor below 2).  For the rows
 // that a call writes into a page, with s0 the page's stored scale (none where the call
 // writes the page's first slot, which starts the page over):
-//   need = the smallest power of two with amax <= 448 need (at least 2^-126)
+//   need = the smallest power of two with amax <= 448 need (at least 2^-126), amax the largest
+//          finite |x| (an infinity saturates: as part of amax it would round the page's other rows
+//          to 0 for good)
 //   s    = max(s0, need)
 //   code = E4M3(x / s);  the page's other rows, where s > s0 > 0:  E4M3(code * (s0 / s))
 // The second rounding of a held row is exact but for codes that fall below E4M3's normal
@@ -135,6 +137,20 @@ __global__ void __launch_bounds__(kPageThreads) page_encode_kernel(const PageEnc
       }
     }
     am = group_max<32>(am);
+    if (am > 3.4028235e38f) {  // an infinity among them, the same in all lanes: once more without
+      am = 0.0f;
+      for (int r = sub; r < n; r += R) {
+        uint32_t v[8];
+        if (!act) continue;
+        load32B<kV8, true>(x + r * ten.row_pitch, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float lo = fabsf(bf16lo(v[i])), hi = fabsf(bf16hi(v[i]));
+          am = fmaxf(am, fmaxf(lo <= 3.4028235e38f ? lo : 0.0f, hi <= 3.4028235e38f ? hi : 0.0f));
+        }
+      }
+      am = group_max<32>(am);
+    }
     if (!(s0 > 0.0f && s0 <= 3.4028235e38f)) s0 = 0.0f;  // no scale stored yet
     const float need = page_scale_need(am);
     const float s = fmaxf(s0, need);
