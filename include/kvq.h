@@ -395,7 +395,8 @@ KVQ_API size_t kvq_attention_workspace(int32_t num_seqs, int32_t num_tokens, int
  *                -1 behind the last token (kvq_quant_scatter skips those).
  *   positions    [max_tokens]: c + i; -1 behind the last token.  May be NULL.
  *   num_used     [1]: how many blocks of the free list are taken.
- * All int32 (slot_ids int64) device memory; no output may overlap an input.
+ * All int32 (slot_ids int64) device memory; no output may overlap another of the arrays
+ * (KVQ_ERR_INVALID_ARG).
  * A request is refused when a length is negative or c + n exceeds max_blocks * block_size
  * (KVQ_DEV_BAD_SEQLEN), or when the free list or max_tokens does not reach for it
  * (KVQ_DEV_NO_SPACE): its seq_lens entry and slots become -1, so that the calls after this

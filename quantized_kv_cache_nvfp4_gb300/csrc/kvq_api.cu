@@ -1019,15 +1019,28 @@ KVQ_API kvq_status kvq_plan_pages(const int32_t* cached_lens, const int32_t* new
     if ((st = check_dev(new_lens, "new_lens")) != KVQ_OK) return st;
     if ((st = check_dev(seq_lens, "seq_lens")) != KVQ_OK) return st;
     if (max_blocks > 0 && (st = check_dev(block_table, "block_table")) != KVQ_OK) return st;
-    const int32_t* in[2] = {cached_lens, new_lens};
-    for (int i = 0; i < 2; ++i)  // every thread block reads the lengths while one writes seq_lens
-      if (in[i] < seq_lens + num_seqs && seq_lens < in[i] + num_seqs)
-        return fail(KVQ_ERR_INVALID_ARG, "seq_lens must not overlap cached_lens or new_lens");
   }
   if (num_free > 0 && (st = check_dev(free_blocks, "free_blocks")) != KVQ_OK) return st;
   if (max_tokens > 0 && (st = check_dev(slot_ids, "slot_ids")) != KVQ_OK) return st;
   if (max_tokens > 0 && positions != nullptr && (st = check_dev(positions, "positions")) != KVQ_OK) return st;
   if (dev_status != nullptr && (st = check_dev(dev_status, "dev_status")) != KVQ_OK) return st;
+  // every thread block reads the inputs (and the held entries of the table) while others write
+  const int64_t S = num_seqs;
+  const struct {
+    const void* at;
+    int64_t bytes;
+    const char* name;
+  } arrays[] = {{cached_lens, 4 * S, "cached_lens"},     {new_lens, 4 * S, "new_lens"},
+                {free_blocks, 4ll * num_free, "free_blocks"}, {block_table, 4 * S * max_blocks, "block_table"},
+                {seq_lens, 4 * S, "seq_lens"},           {query_starts, 4 * (S + 1), "query_starts"},
+                {slot_ids, 8ll * max_tokens, "slot_ids"},  {positions, positions != nullptr ? 4ll * max_tokens : 0, "positions"},
+                {num_used, 4, "num_used"},               {dev_status, dev_status != nullptr ? 4 : 0, "dev_status"}};
+  for (int o = 3; o < 10; ++o)  // the outputs
+    for (int i = 0; i < o; ++i) {
+      const char *a = static_cast<const char*>(arrays[i].at), *b = static_cast<const char*>(arrays[o].at);
+      if (arrays[i].bytes > 0 && arrays[o].bytes > 0 && a < b + arrays[o].bytes && b < a + arrays[i].bytes)
+        return fail(KVQ_ERR_INVALID_ARG, "%s must not overlap %s", arrays[o].name, arrays[i].name);
+    }
   PlanParams p{};
   p.cached = cached_lens;
   p.fresh = new_lens;
