@@ -9,9 +9,11 @@
 //   O += P' V   P' from tensor memory, V from shared memory, O in tensor memory.
 // K and V enter as the f16 values of their codes (exact: E4M3, or E2M1 times its E4M3 block
 // scale); K's FP32 scale multiplies the score, V's the probability, so codes are converted
-// once for kNT * 128 rows.  The reference M covers logit and V's scale together: it moves,
-// and O and l are rescaled, only when a tile's largest logit plus log2 of its largest V
-// scale exceeds M by 8, so P' stays below 2^8 and most tiles leave O alone.
+// once for kNT * 128 rows.  The reference M covers logit and V's scale together: it is set 6 below
+// a tile's largest logit plus log2 of its largest V scale, and moves, and O and l are rescaled,
+// only when those exceed it by 14.  P' is then 2^6 to 2^14 for the largest, which f16 holds, most
+// tiles leave O alone, and keys of 2^-30 of the largest weight still count (set at the largest
+// itself, half a million keys of 2^-26 behind one sink vanished from O, though not from l).
 //
 // Warps: 4 kNT softmax warps; one that looks the step's tokens up in the block table (any
 // block size) some steps ahead; 4 producer warps, which load the rows, convert them and
@@ -1002,9 +1004,9 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
         else if (mode == kBiased) mx = tile_max_any<kBiased, kBN, kPages>(mask, rl, ts, sc, t0, most, lv);
         else mx = tile_max_any<kBoth, kBN, kPages>(mask, rl, ts, sc, t0, most, lv);
         // V's scales enter P', so the reference covers them
-        const bool move = mx + lv > M + 8.0f;
+        const bool move = mx + lv > M + 14.0f;
         if (__any_sync(0xFFFFFFFFu, move)) {
-          const float Mn = move ? mx + lv : M;
+          const float Mn = move ? mx + lv - 6.0f : M;
           const float a = ex2(M - Mn);
           M = Mn;
           L *= a;
