@@ -278,8 +278,9 @@ KVQ_API kvq_status kvq_decode_residual(const kvq_packed* payload, const int32_t*
  * Accuracy: K, V and Q enter the f16 MMA exactly (Q through a power-of-two
  * prescale); products and sums are fp32; P is rounded once to f16 (relative 2^-11,
  * relative to a reference of V's row scales) and the output once to bf16, so
- * |out - exact| <= 2^-9 |exact| + 2^-11 max|v| plus fp32 rounding, where exact is
- * the attention of the decoded rows.
+ * |out - exact| <= 2^-9 |exact| + (2^-11 + 2^-24 n) max|v| plus fp32 rounding, where exact is
+ * the attention of the decoded rows and n counts the keys of less than 2^-14 of the largest
+ * weight (P in f16 ends at 2^-25; only many thousands of such keys in one split show).
  * A NaN in a row of q, or in a K row that it sees, makes its output NaN.
  * An empty sequence writes zeros.  A bad length (KVQ_DEV_BAD_SEQLEN) or a block
  * entry outside the pool (KVQ_DEV_BAD_BLOCK) leaves that sequence's output untouched.
@@ -362,7 +363,9 @@ typedef struct {
  *                 NULL when that is 0); caller-owned.  Calls that may overlap on the GPU, and
  *                 graphs that may replay at the same time, need one each.
  * Accuracy as kvq_decode_attention (one f16 rounding of P, one bf16 rounding of out; products,
- * maxima and sums in fp32), for V scales between 2^-100 and 2^100; the cap is within 2^-20 of
+ * maxima and sums in fp32), max|v| being that of the keys that the row sees, with 2^-30 n in place
+ * of 2^-24 n (2^-25 n for a row whose mask hides keys of larger V from it), for V scales between
+ * 2^-64 and 2^64, 0 and the 2^-126 that a store gives a page of zeros; the cap is within 2^-20 of
  * softcap absolutely.  Waits are bounded as there (KVQ_DEV_TIMEOUT).
  * A NaN in a row of q, or in a K row that a query sees, makes NaN of that query's output and of
  * no other's; one in a V row may reach every query of its sequence.

@@ -196,27 +196,27 @@ struct NoMod {
 };
 
 // A warp's running softmax state over its tiles: per head (8nh + 2c + e) the reference
-// m (and m + 8), the partial sum l of this lane's tokens, the V row-scale reference R
-// (R64 = 64 R, rR = 1 / R), and the O^T accumulators o[mt][nh] (dims g*D/8 + 2mt,
+// m (and the logit from which on it moves), the partial sum l of this lane's tokens, the V row-scale reference R
+// (Rlag: from where on it moves, rR = 1 / R), and the O^T accumulators o[mt][nh] (dims g*D/8 + 2mt,
 // e = 0, 1, and + 1, e = 2, 3, of heads 8nh + 2c and + 1), relative to R.
 // Under a mask R may come from rows of V that a query does not see.  A query whose own V scales
-// are 2^6 and more below R takes m lower by the difference in powers of two (its shift), so that
-// P' keeps its precision; m8 - 8 is then the reference of its logits.  While any query of the
+// are 2^kLagR and more below R takes m lower by the difference in powers of two (its shift), so
+// that P' keeps its precision; mlag tells the reference of its logits.  While any query of the
 // warp is shifted, every tile sets the references anew.  (Where all rows see the same keys, as the
 // heads of one token do, none of this runs: in every tile that moves m it cost 5%.)
 template <int D, int kNH>
 struct AttnState {
-  float m[kNH][2], m8[kNH][2], l[kNH][2], R, R64, rR;
+  float m[kNH][2], mlag[kNH][2], l[kNH][2], R, Rlag, rR;
   bool shifted;
   float o[D / 16][kNH][4];
   // m0: the reference before any key; finite where a tile may hold no key that a row sees
   __device__ __forceinline__ void init(float m0 = kNegInf) {
 #pragma unroll
     for (int nh = 0; nh < kNH; ++nh) {
-      m[nh][0] = m[nh][1] = m8[nh][0] = m8[nh][1] = m0;
+      m[nh][0] = m[nh][1] = mlag[nh][0] = mlag[nh][1] = m0;
       l[nh][0] = l[nh][1] = 0.0f;
     }
-    R = R64 = rR = 0.0f;
+    R = Rlag = rR = 0.0f;
     shifted = false;
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt)
@@ -231,11 +231,18 @@ struct AttnState {
 // may hold anything, NaN codes and scales among it.  qb(nh, kb) gives the Q^T fragment, qmul the per-head query factors (scale,
 // log2 e, Q's power of two).  An active mod turns the scores (rows 8nh + 2c and + 1,
 // tokens g and g + 8) into base-2 logits with the masked ones at -inf; qmul is then 1.
+//
+// How far the references lag: m is set kUp below a row's largest logit and moves when a tile
+// exceeds that by kLag, R when a V scale exceeds it by 2^kLagR, so P' = exp2(s - m) * rs_v / R
+// stays below 2^14 and f16 holds it, and O is rescaled on few tiles.  A key whose P' falls below
+// f16's 2^-25 counts in the row sum but not in O: below 2^-31 of the largest weight with a
+// modifier, whose rows may look back over a whole long cache in one block, 2^-25 without.
 template <int D, int kFK, int kFV, int kNH, typename QB, typename Mod>
 __device__ __forceinline__ void attn_tile(const TileView& tv, const QB& qb, const float (&qmul)[kNH][2], int lane,
                                           int nvalid, AttnState<D, kNH>& st, const Mod& mod, int nfirst = 0) {
   constexpr int kKS = D / 16;
   constexpr int kMT = D / 16;
+  constexpr int kUp = Mod::kActive ? 6 : 0, kLag = Mod::kActive ? 4 : 8, kLagR = Mod::kActive ? 4 : 6;
   const int g = lane >> 2;
   const int c = lane & 3;
   // S^T = K Q^T: rows g and g + 8 are tokens g and 8 + g (this lane's K rows), each
@@ -349,13 +356,10 @@ __device__ __forceinline__ void attn_tile(const TileView& tv, const QB& qb, cons
   for (int nh = 0; nh < kNH; ++nh) {
     mt[nh][0] = fmaxf(sc[nh][0], sc[nh][2]) * qmul[nh][0];
     mt[nh][1] = fmaxf(sc[nh][1], sc[nh][3]) * qmul[nh][1];
-    move = move || mt[nh][0] > st.m8[nh][0] || mt[nh][1] > st.m8[nh][1];
+    move = move || mt[nh][0] > st.mlag[nh][0] || mt[nh][1] > st.mlag[nh][1];
   }
   float rmax = fmaxf(vr0, vr1);
-  move = move || rmax > st.R64 || (Mod::kActive && st.shifted);
-  // references: the softmax reference m per head and the V row-scale reference st.R
-  // move only when a tile exceeds them by more than 2^8 and 2^6, so P' = exp2(s - m)
-  // * rs_v / st.R stays below 2^14 (f16 holds it) and O is rescaled on few tiles
+  move = move || rmax > st.Rlag || (Mod::kActive && st.shifted);
   if (__any_sync(0xFFFFFFFFu, move)) {
 #pragma unroll
     for (int off = 4; off <= 16; off <<= 1) {
@@ -366,10 +370,10 @@ __device__ __forceinline__ void attn_tile(const TileView& tv, const QB& qb, cons
       }
       rmax = fmaxf(rmax, __shfl_xor_sync(0xFFFFFFFFu, rmax, off));
     }
-    // with a mask R holds until a scale exceeds it by 2^6: the smallest shift then tells
+    // with a mask R holds until a scale exceeds it by 2^kLagR: the smallest shift then tells
     bool mixed = false;
     if constexpr (Mod::kActive) mixed = mod.mixed;
-    const bool jump = !mixed || rmax > st.R64 || st.R == 0.0f;
+    const bool jump = !mixed || rmax > st.Rlag || st.R == 0.0f;
     const float Rn = jump ? fmaxf(fmaxf(st.R, rmax), 0x1p-126f) : st.R;
     const float rr = st.R / Rn;
     int shift[kNH][2] = {};
@@ -394,20 +398,20 @@ __device__ __forceinline__ void attn_tile(const TileView& tv, const QB& qb, cons
             for (int off = 4; off <= 16; off <<= 1) own = fmaxf(own, __shfl_xor_sync(0xFFFFFFFFu, own, off));
             int top = exponent(own);
             if (st.m[nh][e] > kNoKey) {
-              const float was = st.shifted ? rintf(st.m8[nh][e] - 8.0f - st.m[nh][e]) : 0.0f;
+              const float was = st.shifted ? rintf((st.mlag[nh][e] - kLag) - (st.m[nh][e] + kUp)) : 0.0f;
               top = max(top, exponent(st.R) - static_cast<int>(was));
             }
             const int below = min(exponent(Rn) - top, 100);
-            shift[nh][e] = below >= 6 && fmaxf(st.m[nh][e], mt[nh][e]) > kNoKey ? below : 0;
+            shift[nh][e] = below >= kLagR && fmaxf(st.m[nh][e], mt[nh][e]) > kNoKey ? below : 0;
             any = any || shift[nh][e] > 0;
-            if (st.shifted) mt[nh][e] = fmaxf(mt[nh][e], st.m8[nh][e] - 8.0f);
+            if (st.shifted) mt[nh][e] = fmaxf(mt[nh][e], st.mlag[nh][e] - kLag);
           }
         any = __any_sync(0xFFFFFFFFu, any);
         if (!st.shifted) {
 #pragma unroll
           for (int nh = 0; nh < kNH; ++nh)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) mt[nh][e] = fmaxf(mt[nh][e], st.m[nh][e]);
+            for (int e = 0; e < 2; ++e) mt[nh][e] = fmaxf(mt[nh][e], st.m[nh][e] + kUp);
         }
         st.shifted = any;
       }
@@ -416,8 +420,8 @@ __device__ __forceinline__ void attn_tile(const TileView& tv, const QB& qb, cons
     for (int nh = 0; nh < kNH; ++nh) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float ref = reset ? mt[nh][e] : fmaxf(st.m[nh][e], mt[nh][e]);  // of the logits
-        const float mn = Mod::kActive ? ref - static_cast<float>(shift[nh][e]) : ref;
+        const float ref = reset ? mt[nh][e] : fmaxf(st.m[nh][e] + kUp, mt[nh][e]);  // of the logits
+        const float mn = Mod::kActive ? ref - static_cast<float>(shift[nh][e] + kUp) : ref;
         const float a = ex2(st.m[nh][e] - mn);  // 0 while m is -inf
         const float f = a * rr;
 #pragma unroll
@@ -427,11 +431,11 @@ __device__ __forceinline__ void attn_tile(const TileView& tv, const QB& qb, cons
         }
         st.l[nh][e] *= a;
         st.m[nh][e] = mn;
-        st.m8[nh][e] = ref + 8.0f;
+        st.mlag[nh][e] = ref + kLag;
       }
     }
     st.R = Rn;
-    st.R64 = Rn * 64.0f;
+    st.Rlag = Rn * static_cast<float>(1 << kLagR);
     st.rR = rcp_approx(Rn);
   }
   // P'^T = exp2(s - m) * rs_v / st.R, transposed in registers into the B operand of

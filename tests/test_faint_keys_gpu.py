@@ -1,4 +1,4 @@
-"""Many query rows behind a long context of keys that are each far fainter than one sink: together
+"""Query rows behind a long context of keys that are each far fainter than one sink: together
 they are the output.  A block table of one page over and over stands in for the long cache."""
 
 import math
@@ -13,13 +13,12 @@ from kvq_testutil import DEV, poison_bf16, status_word
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("D,H,S,fmt", [(128, 8, 20, kvq.FMT_FP8_PAGE), (64, 8, 20, kvq.FMT_NVFP4), (256, 8, 20, kvq.FMT_FP8_PAGE)])
-def test_keys_behind_a_sink(D, H, S, fmt):
+def behind_a_sink(D, H, S, fmt, bs, new):
     """V is 1 but for the sink, whose V is 0.  With w = 2^-26.5 a key and n of them the output is
     n w / (1 + n w), about 2^-8.5.  P' of such a key is 2^-20.5 or more in f16, off by at most
     2^-25, so the output is off by at most 2^-4.5 of itself + 2^-8 of itself; without the keys it
     would be 0."""
-    bs, n, new = 16, 1 << 18, 20
+    n = 1 << 18
     pool = kvq.KvPool.empty(2 * bs, H, D, bs, fill=0, fmt=fmt)
     k, v = torch.zeros((2 * bs, H, D)), torch.ones((2 * bs, H, D))
     k[0, :, 0] = 6.0  # the sink: exact in both formats
@@ -40,3 +39,14 @@ def test_keys_behind_a_sink(D, H, S, fmt):
     want = np.tile(seen * w / (1 + seen * w), S)[:, None, None]
     got = out.double().cpu().numpy()
     assert (np.abs(got - want) <= (2.0 ** -4.5 + 2.0 ** -8) * want).all(), (got.min(), got.max(), want.min())
+
+
+@pytest.mark.parametrize("D,H,S,fmt", [(128, 8, 20, kvq.FMT_FP8_PAGE), (64, 8, 20, kvq.FMT_NVFP4), (256, 8, 20, kvq.FMT_FP8_PAGE)])
+def test_many_rows(D, H, S, fmt):
+    behind_a_sink(D, H, S, fmt, 16, 20)
+
+
+@pytest.mark.parametrize("D,H,S,fmt,bs,new", [(128, 8, 400, kvq.FMT_FP8_PAGE, 16, 1), (64, 8, 400, kvq.FMT_NVFP4, 16, 3),
+                                              (128, 8, 400, kvq.FMT_FP8, 8, 1), (256, 8, 200, kvq.FMT_FP8, 16, 2)])
+def test_few_rows_of_sequences_that_are_not_split(D, H, S, fmt, bs, new):
+    behind_a_sink(D, H, S, fmt, bs, new)

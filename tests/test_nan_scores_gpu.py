@@ -1,5 +1,11 @@
 """A NaN in q or in a K row reaches the outputs of the queries that see it, whichever kernel and
-split count serve them, and no other output: neither zeros nor a row left as it was."""
+split count serve them, and no other output: neither zeros nor a row left as it was.
+
+The other outputs are held to the definition, as in test_query_attention_gpu.py, and not to the
+bits of a run without the NaN: the rows of a warp move their softmax references together, when
+any one of them asks for it, and a row that is NaN asks for none.  Another reference scales P' by
+another 2^x before its rounding to f16, so both results are within 2^-9 |o| + 2^-11 vmax of o,
+and up to twice that from each other."""
 
 import numpy as np
 import pytest
@@ -17,17 +23,20 @@ LAYOUTS = [(2, 4, 16), (3, 2, 16), (2, 4, 8)]
 LENGTHS = [([90, 40], [2, 2]), ([6000, 300], [2, 1]), ([150, 90], [60, 33]), ([6000, 300], [60, 33])]
 
 
-def same(a, b):
-    return torch.equal(a.contiguous().view(torch.int16), b.contiguous().view(torch.int16))
+class poison_k:
+    """NaN in token t's K row of one head, within the block of the with statement."""
 
+    def __init__(self, c, s, t, head):
+        slot = int(c.slots[s][t])
+        plane, col, self.nan = (c.pool.k_bscale, 1, 0x7F) if c.pool.fmt == NV else (c.pool.k_codes, 5, 0xFF)
+        self.at = plane[slot, head, col:col + 1]
 
-def poison_k(c, s, t, head):
-    """NaN in token t's K row of one head."""
-    slot = int(c.slots[s][t])
-    if c.pool.fmt == NV:
-        c.pool.k_bscale[slot, head, 1] = 0x7F
-    else:
-        c.pool.k_codes[slot, head, 5] = 0xFF
+    def __enter__(self):
+        self.was = self.at.clone()
+        self.at.fill_(self.nan)
+
+    def __exit__(self, *_):
+        self.at.copy_(self.was)
 
 
 @pytest.mark.parametrize("lens,new", LENGTHS)
@@ -46,23 +55,18 @@ def test_attention(lens, new, H, group, bs, fmt, opts):
     out, st = c.run(q=q.to(DEV), **opts)
     assert st == 0 and out[row, qh].isnan().all()
     out[row, qh] = want[row, qh]
-    assert same(out, want)
-    # the key of sequence 0's first query: every query of it sees that key, or a window's worth
-    t, head = lens[0] - new[0], H - 1
-    poison_k(c, 0, t, head)
+    c.check(out, **opts)
+    assert c.untouched(out, slice(c.starts[-1], c.T))
+    head = H - 1
     heads = slice(head * group, (head + 1) * group)
-    out, st = c.run(**opts)
-    assert st == 0 and out[:new[0], heads].isnan().all()
-    out[:new[0], heads] = want[:new[0], heads]
-    assert same(out, want)
-    if not opts:
-        # the key of its last query, which only that one sees
-        c = Case(lens, new, H, group, 128, bs, fmt, seed=41)
-        poison_k(c, 0, lens[0] - 1, head)
-        out, st = c.run()
-        assert st == 0 and out[new[0] - 1, heads].isnan().all()
-        out[new[0] - 1, heads] = want[new[0] - 1, heads]
-        assert same(out, want)
+    # the key of sequence 0's first query, which all its queries see; that of its last, which no
+    # other sees
+    for t, first in ((lens[0] - new[0], 0), (lens[0] - 1, new[0] - 1)):
+        with poison_k(c, 0, t, head):
+            out, st = c.run(**opts)
+        assert st == 0 and out[first:new[0], heads].isnan().all()
+        out[first:new[0], heads] = want[first:new[0], heads]
+        c.check(out, **opts)
 
 
 @pytest.mark.parametrize("n", [2, 60])
@@ -95,14 +99,13 @@ def test_decode(lens, H, group, D, bs, fmt):
     out = call()
     assert out[1, 2].isnan().all() and (out[2] == 0).all()
     out[1, 2] = want[1, 2]
-    assert same(out, want)
-    q[1, 2, D - 1] = 1.0
-    want = call()
-    poison_k(c, 0, lens[0] // 2, 1)
-    out = call()
+    c.check(out, seqs=[0, 1])
+    q[1, 2, D - 1] = c.q[1, 2, D - 1].to(DEV)
+    with poison_k(c, 0, lens[0] // 2, 1):
+        out = call()
     assert out[0, group:2 * group].isnan().all()
     out[0, group:2 * group] = want[0, group:2 * group]
-    assert same(out, want)
+    c.check(out, seqs=[0, 1])
 
 
 def test_bad_entries_are_told_from_nan():
