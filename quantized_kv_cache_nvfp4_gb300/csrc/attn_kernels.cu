@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kAttnThreads) decode_attn_kernel(const AttnPar
       am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
       int k = 0;
       if (am > 0.0f) k = 14 - (static_cast<int>((__float_as_uint(am) >> 23) & 0xFF) - 127);
-      k = max(-100, min(120, k));
+      k = max(-113, min(120, k));
       const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
       if (c == 0) qfac[row] = p.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
 #pragma unroll
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__((W + 1) * 32, W == 8 ? 2 : 1) decode_attn_page
     am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
     int kq = 0;
     if (am > 0.0f) kq = 14 - (static_cast<int>((__float_as_uint(am) >> 23) & 0xFF) - 127);
-    kq = max(-100, min(120, kq));
+    kq = max(-113, min(120, kq));
     const float up = __uint_as_float(static_cast<uint32_t>(127 + kq) << 23);
     qfac = p.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - kq) << 23);
 #pragma unroll

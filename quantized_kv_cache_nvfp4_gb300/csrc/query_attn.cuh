@@ -197,7 +197,7 @@ __device__ __forceinline__ float query_fragments(const AttnParams& p, int lane, 
   am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
   int k = 0;
   if (am > 0.0f) k = 14 - (static_cast<int>((__float_as_uint(am) >> 23) & 0xFF) - 127);
-  k = max(-100, min(120, k));
+  k = max(-113, min(120, k));
   const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
 #pragma unroll
   for (int kb = 0; kb < D / 16; ++kb)

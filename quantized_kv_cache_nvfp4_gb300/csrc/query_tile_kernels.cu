@@ -949,7 +949,7 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
       }
       int k = 0;
       if (am > 0.0f) k = 14 - (static_cast<int>((__float_as_uint(am) >> 23) & 0xFF) - 127);
-      k = max(-100, min(120, k));
+      k = max(-113, min(120, k));
       const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
       const float fac = row >= 0 ? p.scale * __uint_as_float(static_cast<uint32_t>(127 - k) << 23) : 0.0f;
 #pragma unroll
