@@ -123,7 +123,8 @@ typedef struct {
  * bscale unused (may be NULL).
  * Format FP8_PAGE: codes as FP8; rscale [num_slots / block_size][num_heads], one scale for
  * the block_size tokens of a (block, head): value = e4m3 * rscale[slot / block_size][head].
- * The library writes powers of two; its readers take any scale.
+ * The library writes powers of two; kvq_restore takes any scale, attention any that is finite
+ * and not negative.
  * Slot = block * block_size + offset.  Every plane used must be 16-byte aligned. */
 typedef struct {
   uint8_t* codes;
@@ -351,7 +352,10 @@ typedef struct {
  * With lo = max(0, p + 1 - window, key_starts[row]) and hi = max(p + 1, prefix), row and
  * query head qh (KV head qh / (num_q_heads / pool->num_heads)) get
  *   softmax over t in [lo, hi) of  cap(scale * q . k_t) + slope * (t - p),  times v_t;
- * a row that sees no key gets zeros.  Cache rows outside the span of the keys that a
+ * a row that sees no key gets zeros.  The options combine as written: with prefix_lens a
+ * query also sees keys of later documents below the prefix, since key_starts bounds its document
+ * on the left only, and alibi_slopes favours the keys ahead of it (t > p) over those behind;
+ * neither happens without a prefix.  Cache rows outside the span of the keys that a
  * sequence's rows see (unwritten rows behind it, left padding before it) are never used,
  * whatever they hold.
  *   q, out        bf16 [num_tokens][num_q_heads][head_dim] through their own pitches.
@@ -365,7 +369,8 @@ typedef struct {
  * Accuracy as kvq_decode_attention (one f16 rounding of P, one bf16 rounding of out; products,
  * maxima and sums in fp32), max|v| being that of the keys that the row sees, with 2^-30 n in place
  * of 2^-24 n (2^-25 n for a row whose mask hides keys of larger V from it), for V scales between
- * 2^-64 and 2^64, 0 and the 2^-126 that a store gives a page of zeros; the cap is within 2^-20 of
+ * 2^-64 and 2^64, 0 and the 2^-126 that a store gives a page of zeros, and K scales up to 2^64;
+ * the cap is within 2^-20 of
  * softcap absolutely.  Waits are bounded as there (KVQ_DEV_TIMEOUT).
  * A NaN in a row of q, or in a K row that a query sees, makes NaN of that query's output and of
  * no other's; one in a V row may reach every query of its sequence.

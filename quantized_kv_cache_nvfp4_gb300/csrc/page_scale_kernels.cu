@@ -11,8 +11,8 @@
 //   s    = max(s0, need)
 //   code = E4M3(x / s);  the page's other rows, where s > s0 > 0:  E4M3(code * (s0 / s))
 // The second rounding of a held row is exact but for codes that fall below E4M3's normal
-// range, so a page filled token by token holds what one call would have written, give or
-// take half a subnormal step.
+// range.  Each raise of the scale rounds those again, so a page filled token by token holds
+// what one call would have written, or is off by one subnormal step of the final scale.
 //
 // Mapping: rows of one page that stand next to each other in slot_ids form a run; one
 // warp serves (run, head, tensor), so no two warps write one (page, head) and no atomics
