@@ -18,8 +18,11 @@ PG, F8, NV = kvq.FMT_FP8_PAGE, kvq.FMT_FP8, kvq.FMT_NVFP4
 
 def scale_v(c, s, first, last, factor):
     """V of tokens first .. last - 1 (whole pages where a scale is a page's) times a power of two."""
-    slots = torch.tensor(c.slots[s][first:last], device=DEV)
-    c.pool.v_rscale[torch.unique(slots // c.bs) if c.pool.v_fmt in (None, PG) and c.pool.fmt == PG else slots] *= factor
+    rows = c.slots[s][first:last]
+    if (c.pool.fmt if c.pool.v_fmt is None else c.pool.v_fmt) == PG:
+        rows = np.unique(rows // c.bs)
+    assert rows.size == 0 or rows.max() < c.pool.v_rscale.size(0)
+    c.pool.v_rscale[torch.tensor(rows, device=DEV)] *= factor
 
 
 def check_rows(c, out, **opts):
