@@ -369,7 +369,7 @@ typedef struct {
  * Accuracy as kvq_decode_attention (one f16 rounding of P, one bf16 rounding of out; products,
  * maxima and sums in fp32), max|v| being that of the keys that the row sees, with 2^-30 n in place
  * of 2^-24 n (2^-25 n for a row whose mask hides keys of larger V from it), for V scales between
- * 2^-64 and 2^64, 0 and the 2^-126 that a store gives a page of zeros, and K scales up to 2^64;
+ * 2^-48 and 2^48, 0 and the 2^-126 that a store gives a page of zeros, and K scales up to 2^64;
  * the cap is within 2^-20 of
  * softcap absolutely.  Waits are bounded as there (KVQ_DEV_TIMEOUT).
  * A NaN in a row of q, or in a K row that a query sees, makes NaN of that query's output and of
