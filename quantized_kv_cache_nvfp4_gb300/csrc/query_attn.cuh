@@ -36,16 +36,17 @@ __device__ __forceinline__ bool query_range(const QueryAttnParams& p, int s, int
   return true;
 }
 
-// Whether the keys [lo, hi) of sequence s need a block entry outside the pool.  Only rows of a
-// block that met such an entry ask.
+// Whether the keys [lo, hi) of sequence s need a block entry outside the pool, for a whole warp
+// (32 entries at a time: pages may be single tokens).  Only rows of a block that met such an entry
+// ask.
 __device__ __forceinline__ bool needs_bad_block(const AttnParams& p, int s, int lo, int hi) {
   if (lo >= hi) return false;
   const int32_t* const table = p.block_table + static_cast<int64_t>(s) * p.max_blocks;
-  const uint32_t last = p.div_bs.div(static_cast<uint32_t>(hi) - 1);
+  const uint32_t last = p.div_bs.div(static_cast<uint32_t>(hi) - 1), lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (uint32_t b = p.div_bs.div(static_cast<uint32_t>(lo)); b <= last; ++b) {
-    const int32_t blk = LDX(table + b);
-    if (blk < 0 || blk >= p.num_blocks) return true;
+  for (uint32_t b = p.div_bs.div(static_cast<uint32_t>(lo)); b <= last; b += 32) {
+    const int32_t blk = b + lane <= last ? LDX(table + b + lane) : 0;
+    if (__any_sync(0xFFFFFFFFu, b + lane <= last && (blk < 0 || blk >= p.num_blocks))) return true;
   }
   return false;
 }

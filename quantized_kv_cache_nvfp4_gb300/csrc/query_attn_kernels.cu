@@ -195,7 +195,13 @@ __global__ void __launch_bounds__(kAttnThreads) query_rows_kernel(const QueryAtt
       st.l[nh][0] += __shfl_xor_sync(0xFFFFFFFFu, st.l[nh][0], off);
       st.l[nh][1] += __shfl_xor_sync(0xFFFFFFFFu, st.l[nh][1], off);
     }
-  const bool cta_bad = __syncthreads_or(bad ? 1 : 0) != 0;  // the ring is free after this
+  __shared__ uint32_t bad_rows;
+  if (threadIdx.x == 0) bad_rows = 0u;
+  if (__syncthreads_or(bad ? 1 : 0) != 0) {  // (the ring is free after this)
+    for (int r = warp; r < min(kRows, rows - row0); r += kAttnWarps)
+      if (needs_bad_block(p, s, max(tab.range[r].x, t_begin), min(tab.range[r].y, t_end)) && lane == 0)
+        atomicOr(&bad_rows, 1u << r);
+  }
 
   float* const mo = reinterpret_cast<float*>(smem + T::kQ) + warp * kRows * (D + 2);
 #pragma unroll
@@ -232,8 +238,7 @@ __global__ void __launch_bounds__(kAttnThreads) query_rows_kernel(const QueryAtt
     const int i = (row0 + row) / p.group;
     const int qh = h * p.group + row0 + row - i * p.group;
     const int64_t tok = q0 + i;
-    const int2 seen = tab.range[row];
-    const bool row_bad = cta_bad && needs_bad_block(p, s, max(seen.x, t_begin), min(seen.y, t_end));
+    const bool row_bad = ((bad_rows >> row) & 1u) != 0u;
     if (p.nsplit == 1) {
       if (row_bad) continue;
       const float y = L == 0.0f ? 0.0f : O / L;

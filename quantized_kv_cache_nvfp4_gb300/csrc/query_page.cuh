@@ -378,6 +378,11 @@ __global__ void __launch_bounds__(32 * (QueryPage<D, kFK, kFV, kNH>::kW + 1), Qu
       }
     }
   }
+  uint32_t bad_rows = 0;
+  if (cta_bad) {
+    for (int r = 0; r < min(kRows, rows - row0); ++r)
+      if (needs_bad_block(p, s, max(tab.range[r].x, t_begin), min(tab.range[r].y, t_end))) bad_rows |= 1u << r;
+  }
   // rows 8 nh + 2c + e; dims g*D/8 + 2q and + 1
 #pragma unroll
   for (int nh = 0; nh < kNH; ++nh)
@@ -388,8 +393,7 @@ __global__ void __launch_bounds__(32 * (QueryPage<D, kFK, kFV, kNH>::kW + 1), Qu
       const int i = row / p.group, qh = h * p.group + row - i * p.group;
       const int64_t tok = q0 + i;
       const float L = st.l[nh][e];
-      const int2 seen = tab.range[8 * nh + 2 * c + e];
-      const bool bad = cta_bad && needs_bad_block(p, s, max(seen.x, t_begin), min(seen.y, t_end));
+      const bool bad = ((bad_rows >> (8 * nh + 2 * c + e)) & 1u) != 0u;
       if (nsplit == 1) {
         if (bad) continue;
         uint16_t* const out = p.out + tok * p.o_row_pitch + static_cast<int64_t>(qh) * p.o_head_pitch;

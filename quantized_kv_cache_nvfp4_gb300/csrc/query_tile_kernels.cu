@@ -1042,8 +1042,13 @@ __global__ void __launch_bounds__(QTile<D>::kThreads, 1) query_tile_kernel(const
       __syncwarp();
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const bool bad = *reinterpret_cast<volatile int*>(&misc->bad) != 0 && sees &&
-                     needs_bad_block(p, s, max(rl.lo, t_begin), min(rl.hi, t_end));
+    bool bad = false;
+    if (*reinterpret_cast<volatile int*>(&misc->bad) != 0) {
+      for (int l = 0; l < 32; ++l) {
+        const int lo = __shfl_sync(0xFFFFFFFFu, sees ? rl.lo : t_end, l), hi = __shfl_sync(0xFFFFFFFFu, rl.hi, l);
+        if (needs_bad_block(p, s, max(lo, t_begin), min(hi, t_end)) && lane == l) bad = true;
+      }
+    }
     if (!sees) L = 0.0f;
     uint16_t* const out = p.out + tok * p.o_row_pitch + static_cast<int64_t>(head) * p.o_head_pitch;
     float* const wsr = p.ws + ((tok * p.Hq + head) * p.nsplit + split) * (D + 2);

@@ -71,3 +71,25 @@ def test_rubbish_in_the_pool_stays_out(new):
         assert st == kvq.DEV_BAD_BLOCK and c.untouched(out, slice(0, 1)) and torch.isfinite(out[1:new:2]).all()
         if new > 1:
             assert (out[1:new:2].float() - want[1:new:2].float()).abs().max() <= 2.0 ** -6 * want[:new].float().abs().max()
+
+
+@pytest.mark.parametrize("bs,H,new", [(1, 2, 1), (1, 2, 60), (16, 2, 3)])
+def test_a_bad_entry_at_the_end_of_a_long_table(bs, H, new):
+    """Half a million tokens of one page over and over, the last entry bad: the rows' walk over
+    their entries is a warp's and ends soon."""
+    L, D = 1 << 19, 64
+    pool = kvq.KvPool.empty(4 * bs, H, D, bs, fill=0, fmt=F8)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)
+    table = torch.zeros((1, L // bs), dtype=torch.int32, device=DEV)
+    table[0, -1] = -1
+    q = torch.ones((new, H * 2, D), dtype=torch.bfloat16, device=DEV)
+    out, st = torch.full_like(q, 7.0), i32([0])
+    ks = i32([0] * new)
+    ks[0] = L  # sees nothing
+    kvq.kvq_attention(pool, table, i32([L]), L, q, i32([0, new]), new, 0.1, out, key_starts=ks, dev_status=st)
+    torch.cuda.synchronize()
+    assert (out[0] == 0).all()
+    need = torch.arange(L - new, L, device=DEV) >= (L // bs - 1) * bs
+    need[0] = False
+    want = torch.where(need, 7.0, 0.0)
+    assert (out[:, 0, 0].float() == want).all() and int(st.item()) == (kvq.DEV_BAD_BLOCK if new > 1 else 0)
