@@ -344,6 +344,8 @@ typedef struct {
 /* Paged attention of several query tokens per sequence over a quantised pool: prompt
  * chunks behind a cached prefix, draft tokens, single tokens with score options, any mix of
  * them in one call.  Beside kvq_decode_attention, whose one query sees its whole sequence.
+ * (max_query_len picks the kernel for all sequences of a call: many single tokens beside a long
+ * chunk are faster as two calls.)
  *   query_starts  device int32 [num_seqs + 1]: sequence s owns rows query_starts[s] ..
  *                 query_starts[s + 1] - 1 of q and out, its LAST n tokens: row i of them sits
  *                 at position p = seq_lens[s] - n + i.  Their K and V rows are in the pool

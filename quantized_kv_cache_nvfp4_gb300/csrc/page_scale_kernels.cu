@@ -20,7 +20,7 @@
 // each; 32 / L rows go at once, and the first kHold such passes stay in registers between
 // the maximum and the codes, so pages up to 8 * 32 / L rows are read once.
 // Bound: HBM, 2 D bytes read and D written per row.  Measured: 37 prompts of 55,500 tokens in
-// all, 8 heads, head_dim 128, 32-token pages: 63.3 us, 5.39 TB/s, 80% of a plain copy's rate;
+// all, 8 heads, head_dim 128, 32-token pages: 63.2 us, 5.40 TB/s, 80% of a plain copy's rate;
 // 64 single tokens into half-filled pages 3.3 us, one launch and one chain of loads.  More
 // resident blocks (fewer registers, 102 against 72 us with events around each call) measured
 // slower.

@@ -12,7 +12,7 @@
 // kernels (attn_tile.cuh), the score modifier between its two products.  Splits of a
 // sequence merge through the caller's workspace in a second small kernel.  Bound: issue and
 // latency of the tile arithmetic, and gathers of 64 to 256 bytes (16 x 5000 tokens over NVFP4 with
-// bias, 64 query heads, 8-token pages: 44.3 us; 38.3 by whole pages of 16 tokens).
+// bias, 64 query heads, 8-token pages: 46.5 us; 39.5 by whole pages of 16 tokens).
 #include <algorithm>
 
 #include "query_attn.cuh"
@@ -458,7 +458,8 @@ int tile_splits(int32_t S, int32_t H, int32_t D, int64_t rows, int32_t span) {
 bool page_two(int32_t D, int64_t rows) { return rows > 8 && D != 256; }  // 16 rows a block spill at head_dim 256
 
 // The whole-page kernel's blocks.  Several sequences share one or two waves of them by length
-// (page_job): in equal parts their longest sets the time.  GPU us in equal parts and shared, one
+// (page_job): in equal parts their longest sets the time.  GPU us in equal parts and shared (as the
+// rule was taken), one
 // token each: lengths of 1 to L, NVFP4 with bias, 16 x 5000 34.4, 29.9; page-scaled, 24 x 6000 42.3,
 // 35.9; 50 x 6000 76.7, 55.7; 100 x 6000 145, 120; 250 x 6000 396, 329; all of one length, 32 x 8192
 // 86.4, 88.9; 50 x 6000 98.3, 101; 250 x 6000 449, 482.  Not where there is little to share: below

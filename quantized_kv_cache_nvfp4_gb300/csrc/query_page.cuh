@@ -11,9 +11,9 @@
 // strides' constants measured no gain, and there are a quarter of the instances.
 //
 // Bound: HBM with up to 8 rows a KV head and plain logits over FP8 planes (32 x 8192 tokens, 8 KV heads, 32 query
-// heads, head_dim 128, page scales: 88.9 us, 6.05 TB/s, 89% of a plain copy's rate); issue and
+// heads, head_dim 128, page scales: 88.0 us, 6.12 TB/s, 90% of a plain copy's rate); issue and
 // latency of a 16-token tile's arithmetic once options join in or the planes are NVFP4 (16 ragged sequences of up to 5000 tokens over
-// NVFP4 with bias: 30.1 us, 2.0 TB/s; 32 of up to 4 draft tokens, capped, window 1024: 27.2 us).
+// NVFP4 with bias: 30.6 us, 2.0 TB/s; 32 of up to 4 draft tokens, capped, window 1024: 27.0 us).
 // Blocks of every head and whole pages move 16 KB and more with one copy, where a block of one
 // head would gather rows of 64 to 256 bytes (47 us for each of the last two).
 #pragma once

@@ -25,9 +25,12 @@
 // Bound: the softmax warps (an exponential, a maximum, a sum and a conversion for each score, and
 // the waits of their tensor-memory loads), with the tensor cores busy about half the time.
 // Measured at 4096 queries behind 8192 cached tokens, 8 KV heads, 32 query heads, page-scaled:
-// head_dim 128 618 us, 1112 Tflop/s (57% of the library GEMM rate), 800 over NVFP4 (its block scales
-// join the conversion), 860 capped (799 Tflop/s), 820 with bias; head_dim 64 568, 256 855 us.  The
-// rows kernel took 4706 us for the capped one.  Other arrangements measured slower: P' kept in registers for
+// head_dim 128 632 us, 1087 Tflop/s (56% of the library GEMM rate), 817 over NVFP4 (its block scales
+// join the conversion), 860 capped (799 Tflop/s), 838 with bias; head_dim 64 559, 256 869 us.  (Row
+// references that leave out hidden keys' scales, and sums that keep keys of tiny V, cost 2 to 3%
+// of the plain and biased ones.)  The 14 warps of head_dim 64 and 128 leave 128 registers a thread,
+// and the head_dim 128 instances spill 132 to 136 bytes.  The rows kernel took 4706 us for the
+// capped one.  Other arrangements measured slower: P' kept in registers for
 // one pass (1104 against 912 us at that step: spills), 16 and 32 tensor-memory columns at a time
 // in two buffers (1120, 975), an issuing warp for each tile (996).
 #include "query_attn.cuh"
