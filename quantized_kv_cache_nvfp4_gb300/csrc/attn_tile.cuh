@@ -196,9 +196,10 @@ struct NoMod {
 };
 
 // A warp's running softmax state over its tiles: per head (8nh + 2c + e) the reference
-// m (and the logit from which on it moves), the partial sum l of this lane's tokens, the V row-scale reference R
-// (Rlag: from where on it moves, rR = 1 / R), and the O^T accumulators o[mt][nh] (dims g*D/8 + 2mt,
-// e = 0, 1, and + 1, e = 2, 3, of heads 8nh + 2c and + 1), relative to R.
+// m (mlag: the logit from which on it moves), the partial sum l of this lane's tokens, the V
+// row-scale reference R (Rlag: the scale from which on it moves, rR = 1 / R), and the O^T
+// accumulators o[mt][nh] (dims g*D/8 + 2mt, e = 0, 1, and + 1, e = 2, 3, of heads 8nh + 2c and
+// + 1), relative to R.
 // Under a mask R may come from rows of V that a query does not see.  A query whose own V scales
 // are 2^kLagR and more below R takes m lower by the difference in powers of two (its shift), so
 // that P' keeps its precision; mlag tells the reference of its logits.  While any query of the
