@@ -21,7 +21,9 @@
  *     head), raised as tokens are appended.
  * Attention reads the pool as it is: kvq_decode_attention (one query a sequence) and
  * kvq_attention (several, with score options); kvq_plan_pages makes a step's block tables
- * and slot ids on the GPU.
+ * and slot ids on the GPU.  Over long contexts: kvq_append stores turned keys and keeps
+ * their bounds, kvq_select_blocks lists the blocks that a query wants, and
+ * kvq_sparse_attention reads those alone.
  *
  * Conventions shared by every entry point
  *   Memory   every pointer argument that a kernel touches is DEVICE memory
@@ -96,7 +98,7 @@ typedef enum { KVQ_KIND_KEY = 0, KVQ_KIND_VALUE = 1 } kvq_kind;
 /* Bits ORed into *dev_status by the kernels. */
 #define KVQ_DEV_BAD_SLOT 1u   /* slot id >= num_slots (row skipped) */
 #define KVQ_DEV_BAD_BLOCK 2u  /* block-table entry < 0 or past the pool (row skipped) */
-#define KVQ_DEV_BAD_POS 4u    /* position outside [0, rows) or not strictly increasing */
+#define KVQ_DEV_BAD_POS 4u    /* position outside [0, rows) or not strictly increasing; append: past the angles */
 #define KVQ_DEV_BAD_SEQLEN 8u /* seq_lens[s] outside [0, min(max_seq_len, blocks*block_size)] */
 #define KVQ_DEV_NO_SPACE 32u  /* page plan: the free list or the token arrays ran out (request refused) */
 #define KVQ_DEV_TIMEOUT 16u   /* decode attention: a bounded wait for a copy ran out (results unspecified) */
@@ -199,6 +201,43 @@ typedef struct {
 KVQ_API kvq_status kvq_quant_scatter(const kvq_bf16_in* k, const kvq_bf16_in* v, int32_t num_tokens,
                              const int64_t* slot_ids, const kvq_pool* pool,
                              uint32_t* dev_status, kvq_stream_t stream);
+
+/* Rotation of kvq_append: position p turns each pair (a, b) of the first rot_dim channels to
+ * (a c - b s, b c + a s), c and s being the cosine and sine of the pair's angle at p. */
+typedef struct {
+  const float* cos_sin;     /* device f32 [num_positions][rot_dim], 16-byte aligned: the rot_dim / 2 cosines of a
+                               position, then its sines (scaled frequencies and factors are the caller's
+                               matter); NULL: nothing is turned */
+  int32_t num_positions;
+  int32_t rot_dim;          /* a multiple of 16, at most head_dim; channels behind it pass */
+  int32_t interleaved;      /* 0: pairs (i, i + rot_dim / 2); else (2i, 2i + 1) */
+  const int32_t* positions; /* device int32 [num_tokens] */
+} kvq_rotation;
+
+/* Append to a paged pool with the position rotation on the way: K turned, then K and V
+ * quantised and scattered as kvq_quant_scatter does, Q turned beside them, and the bounds of each
+ * block's keys kept for kvq_select_blocks.  One kernel launch; may be captured in a CUDA graph.
+ *   k, v, slot_ids, pool  as kvq_quant_scatter (each plane in its own format; k or v may be NULL).
+ *              K is turned in binary32 (every product and sum rounded once, no FMA) and goes
+ *              through the codec from there, without a rounding to bf16.
+ *   rotation   host struct, read during the call; NULL: K goes in as it is.
+ *   q, q_out   bf16 [num_tokens][num_q_heads][head_dim]: q_out = bf16(turned q); both NULL or
+ *              neither; needs a rotation.  q_out may be exactly q (same pointer and pitches);
+ *              otherwise it overlaps no element of q, k or v (KVQ_ERR_INVALID_ARG).
+ *   key_bounds NULL, or device bf16 [num_slots / block_size][num_heads][2][head_dim], 16-byte
+ *              aligned: [0] and [1] become the least and the largest bf16(turned k) of the block's rows, channel
+ *              by channel: of this call's rows alone where they hold the block's first slot, else
+ *              of them and what was there.  A NaN does not count.  Needs k.
+ * A token whose position is negative is skipped whole (kvq_plan_pages marks those behind the last
+ * with -1), as is one at num_positions or beyond (KVQ_DEV_BAD_POS); one whose slot is negative or
+ * past the pool (KVQ_DEV_BAD_SLOT) has its q turned only.
+ * All rows of a block in one call must stand next to each other in slot_ids, as for FP8_PAGE pools,
+ * where that is the pool's format or key_bounds is given (else what the block holds of scale, codes
+ * or bounds is unspecified).  The inputs overlap no output but q_out. */
+KVQ_API kvq_status kvq_append(const kvq_bf16_in* k, const kvq_bf16_in* v, int32_t num_tokens, const int64_t* slot_ids,
+                              const kvq_pool* pool, const kvq_rotation* rotation, const kvq_bf16_in* q,
+                              const kvq_bf16_out* q_out, int32_t num_q_heads, void* key_bounds, uint32_t* dev_status,
+                              kvq_stream_t stream);
 
 /* Paged restore: gather and dequantise pool rows back to bf16 (the decode side).  Source: FreeToken PR #408, Summary ("Triton restore paths"); vllm-rlt
  * PR #166 review (pack_paged / unpack_paged over [pages, page_size, heads, dim]).
@@ -393,6 +432,66 @@ KVQ_API kvq_status kvq_attention(const kvq_pool* pool, const int32_t* block_tabl
 KVQ_API size_t kvq_attention_workspace(int32_t num_seqs, int32_t num_tokens, int32_t num_heads,
                                        int32_t num_q_heads, int32_t head_dim, int32_t max_query_len,
                                        int32_t max_seq_len);
+
+/* Blocks of the cache that a query token wants, for each KV head: those with the highest bound on a
+ * score.  With the g = num_q_heads / num_heads query heads of KV head h and the bounds lo, hi of a
+ * block's keys (kvq_append),
+ *   score(block) = sum_d [ (sum_g max(q_gd, 0)) hi_d + (sum_g min(q_gd, 0)) lo_d ]  >=  sum_g q_g . k_t
+ * for every key t of the block (up to the rounding of the bounds).  A query at position p chooses among blocks
+ * 0 to p / block_size: the first_blocks first and the last_blocks last of them in any case, then the
+ * highest scores until topk are listed (all of them where there are no more than topk); equal scores
+ * go by the lower index.
+ *   key_bounds     device bf16 [num_blocks][num_heads][2][head_dim], 16-byte aligned.
+ *   block_table, seq_lens, max_seq_len, q, query_starts, num_tokens, max_query_len  as kvq_attention.
+ *   selected       device int32 [num_tokens][num_heads][topk]: block numbers within the sequence
+ *                  (indexes of its block_table row), ascending, -1 behind the last.  Rows of no
+ *                  sequence, and of a refused one (KVQ_DEV_BAD_SEQLEN), keep theirs.
+ *   head_dim 64, 128 or 256; at most 16 query heads per KV head; first_blocks + last_blocks <=
+ *   topk; sequences of up to 32768 blocks (any number where topk reaches for all of them).
+ *   workspace      device memory of kvq_select_blocks_workspace(...) bytes, 16-byte aligned;
+ *                  caller-owned; one for each call that may run at the same time.
+ * The list is that of the exact scores: what binary32 cannot tell apart is scored again in
+ * binary64 (equal up to its rounding counts as equal).  A NaN score ranks below all numbers, and a
+ * block whose table entry lies outside the pool below that (KVQ_DEV_BAD_BLOCK, where scores are needed).
+ * Two kernel launches (one where topk reaches for all blocks of max_seq_len); may be captured in
+ * a CUDA graph. */
+KVQ_API kvq_status kvq_select_blocks(const void* key_bounds, int64_t num_blocks, int32_t block_size, int32_t num_heads,
+                                     int32_t head_dim, const int32_t* block_table, int32_t num_seqs, int32_t max_blocks,
+                                     const int32_t* seq_lens, int32_t max_seq_len, const kvq_bf16_in* q,
+                                     const int32_t* query_starts, int32_t num_tokens, int32_t max_query_len,
+                                     int32_t num_q_heads, int32_t first_blocks, int32_t last_blocks, int32_t topk,
+                                     int32_t* selected, void* workspace, size_t workspace_bytes, uint32_t* dev_status,
+                                     kvq_stream_t stream);
+
+/* Workspace bytes kvq_select_blocks needs for these sizes.  Host-only query. */
+KVQ_API size_t kvq_select_blocks_workspace(int32_t num_tokens, int32_t num_heads, int32_t max_seq_len, int32_t block_size);
+
+/* Attention over listed blocks of the cache: kvq_attention's causal form (no window, prefix, key
+ * starts or ALiBi bias) with, for each query token and KV head, only the keys of its listed blocks.
+ *   selected   device int32 [num_tokens][num_heads][topk], as kvq_select_blocks writes it or from
+ *              elsewhere: block numbers within the sequence, in any order; an entry that is negative
+ *              or behind the query's own block counts for nothing, one that stands there twice
+ *              counts twice.  topk at most 4096.
+ * A query at position p sees the keys t <= p of its blocks; a row that sees none gets zeros.  Keys
+ * of other blocks are not read.
+ *   softcap    0, or 2^-10 to 2^10: logits become softcap * tanh(logit / softcap).
+ *   workspace  device memory of kvq_sparse_attention_workspace(...) bytes, 16-byte aligned (may be
+ *              NULL when that is 0); caller-owned; one for each call that may run at the same time.
+ * All else (pool formats, head_dim, heads, accuracy, refused sequences, NaN) as kvq_attention;
+ * rows (token, KV head) whose list needs a block entry outside the pool keep what they held
+ * (KVQ_DEV_BAD_BLOCK).  One or two kernel launches; may be captured in a CUDA graph. */
+KVQ_API kvq_status kvq_sparse_attention(const kvq_pool* pool, const int32_t* block_table, int32_t num_seqs,
+                                        int32_t max_blocks, const int32_t* seq_lens, int32_t max_seq_len,
+                                        const kvq_bf16_in* q, const int32_t* query_starts, int32_t num_tokens,
+                                        int32_t max_query_len, int32_t num_q_heads, const int32_t* selected,
+                                        int32_t topk, float scale, float softcap, const kvq_bf16_out* out,
+                                        void* workspace, size_t workspace_bytes, uint32_t* dev_status,
+                                        kvq_stream_t stream);
+
+/* Workspace bytes kvq_sparse_attention needs for these sizes on the current device (0 when the
+ * call runs without one).  Host-only query. */
+KVQ_API size_t kvq_sparse_attention_workspace(int32_t num_tokens, int32_t num_heads, int32_t num_q_heads, int32_t head_dim,
+                                              int32_t block_size, int32_t topk);
 
 /* Page plan of a step: block tables, slot maps and lengths from request lengths, on the
  * GPU, ready for kvq_quant_scatter, kvq_decode_attention and kvq_attention.

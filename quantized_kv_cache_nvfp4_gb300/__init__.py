@@ -27,7 +27,8 @@ __all__ = [
     "KvqError", "KvPool", "Nvfp4Pool", "Packed", "kvq_quant_scatter", "kvq_restore", "kvq_pack",
     "kvq_unpack", "kvq_encode_residual", "kvq_decode_residual", "kvq_decode_attention",
     "kvq_decode_attention_workspace", "kvq_decode_attention_noalloc", "kvq_attention",
-    "kvq_attention_workspace", "kvq_plan_pages", "kvq_storage_bytes", "FMT_FP8_PAGE", "DEV_NO_SPACE",
+    "kvq_attention_workspace", "kvq_append", "kvq_select_blocks", "kvq_select_blocks_workspace", "kvq_sparse_attention",
+    "kvq_sparse_attention_workspace", "kvq_plan_pages", "kvq_storage_bytes", "FMT_FP8_PAGE", "DEV_NO_SPACE",
     "kvq_status_string", "kvq_last_error", "library_path", "FMT_NVFP4", "FMT_INT4", "FMT_FP8", "FMT_NVFP4_TENSOR", "KIND_KEY",
     "KIND_VALUE", "DEV_BAD_SLOT", "DEV_BAD_BLOCK", "DEV_BAD_POS", "DEV_BAD_SEQLEN", "DEV_TIMEOUT",
 ]
@@ -462,6 +463,137 @@ def kvq_attention(pool: KvPool, block_table: torch.Tensor, seq_lens: torch.Tenso
         ctypes.byref(ps), block_table.data_ptr(), S, max_blocks, lens, max_seq_len, ctypes.byref(qi), starts, T,
         max_query_len, Hq, float(scale), None if opts is None else ctypes.byref(opts), ctypes.byref(oo),
         _ptr(workspace), nbytes, _ptr(dev_status), _stream(stream)))
+    return out
+
+
+def kvq_append(k: Optional[torch.Tensor], v: Optional[torch.Tensor], slot_ids: Optional[torch.Tensor], pool: KvPool, *,
+               cos_sin: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+               interleaved: bool = False, q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+               key_bounds: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
+               stream=None) -> Optional[torch.Tensor]:
+    """K/V [T, H, D] bf16 into pool slots slot_ids [T] (int64), K turned by the angles of its
+    positions [T] (int32): cos_sin [num_positions, rot_dim] f32 holds a position's cosines, then its
+    sines.  q [T, Hq, D] is turned into q_out (which may be q; returned).  key_bounds
+    [blocks, H, 2, D] bf16 keeps the least and largest key of each block (see include/kvq.h)."""
+    src = k if k is not None else v if v is not None else q
+    if src is None:
+        raise ValueError("k, v and q are all None")
+    T, H, D = src.size(0), pool.num_heads, pool.head_dim
+    for t, name, heads in ((k, "k", H), (v, "v", H), (q, "q", None), (q_out, "q_out", None if q is None else q.size(1))):
+        if t is not None and (t.dim() != 3 or t.size(0) != T or t.size(2) != D or (heads is not None and t.size(1) != heads)):
+            raise ValueError(f"{name} must be [{T}, {'heads' if heads is None else heads}, {D}]")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    rot = None
+    if cos_sin is not None:
+        if positions is None:
+            raise ValueError("cos_sin needs positions")
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous [positions, rot_dim] float32 tensor")
+        rot = _abi.Rotation(cos_sin.data_ptr(), cos_sin.size(0), cos_sin.size(1), int(interleaved),
+                            _vec(positions, torch.int32, "positions", T))
+    if key_bounds is not None:
+        _bounds_shape(key_bounds, pool.num_slots // pool.block_size, H, D)
+    slots = None if k is None and v is None else _vec(slot_ids, torch.int64, "slot_ids", T)
+    kin = _bf16_in(k, "k") if k is not None else None
+    vin = _bf16_in(v, "v") if v is not None else None
+    qin, qo = (_bf16_in(q, "q"), _bf16_out(q_out, "q_out")) if q is not None else (None, None)
+    ps = pool._struct()
+    ref = lambda x: None if x is None else ctypes.byref(x)
+    _check(_lib().kvq_append(ref(kin), ref(vin), T, slots, ctypes.byref(ps), ref(rot), ref(qin), ref(qo),
+                             0 if q is None else q.size(1), _ptr(key_bounds), _ptr(dev_status), _stream(stream)))
+    return q_out
+
+
+def _bounds_shape(t: torch.Tensor, blocks: Optional[int], H: Optional[int], D: Optional[int]) -> None:
+    if t.dtype != torch.bfloat16:
+        raise TypeError("key_bounds must be bfloat16")
+    if (t.dim() != 4 or not t.is_contiguous() or t.size(2) != 2
+            or any(n is not None and t.size(i) != n for i, n in ((0, blocks), (1, H), (3, D)))):
+        raise ValueError("key_bounds must be a contiguous [blocks, heads, 2, head_dim] tensor")
+
+
+def kvq_select_blocks_workspace(num_tokens: int, num_heads: int, max_seq_len: int, block_size: int) -> int:
+    return int(_lib().kvq_select_blocks_workspace(num_tokens, num_heads, max_seq_len, block_size))
+
+
+def kvq_select_blocks(key_bounds: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int,
+                      block_size: int, q: torch.Tensor, query_starts: torch.Tensor, max_query_len: int,
+                      selected: torch.Tensor, *, first_blocks: int = 1, last_blocks: int = 1,
+                      workspace: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """The blocks with the highest score bounds for each query row q [T, Hq, D] bf16 and KV head, into
+    selected [T, H, topk] int32 (ascending, -1 behind the last), from key_bounds
+    [blocks, H, 2, D] bf16 as kvq_append keeps them.  A workspace tensor is allocated when none
+    is given."""
+    if block_table.dtype != torch.int32:
+        raise TypeError("block_table must be int32")
+    if not block_table.is_contiguous():
+        raise ValueError("block_table must be contiguous [S, max_blocks]")
+    S, max_blocks = block_table.shape
+    T, Hq, D = q.shape
+    _bounds_shape(key_bounds, None, None, D)
+    H = key_bounds.size(1)
+    sel = _lists(selected, T, H)
+    qi = _bf16_in(q, "q")
+    if workspace is None:
+        need = kvq_select_blocks_workspace(T, H, max_seq_len, block_size)
+        if need > 0:
+            workspace = _workspace(need, q.device, stream)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib().kvq_select_blocks(
+        key_bounds.data_ptr(), key_bounds.size(0), block_size, H, D, block_table.data_ptr(), S, max_blocks,
+        _vec(seq_lens, torch.int32, "seq_lens", S), max_seq_len, ctypes.byref(qi),
+        _vec(query_starts, torch.int32, "query_starts", S + 1), T, max_query_len, Hq, first_blocks, last_blocks,
+        selected.size(2), sel, _ptr(workspace), nbytes, _ptr(dev_status), _stream(stream)))
+    return selected
+
+
+def _lists(t: torch.Tensor, T: int, H: int):
+    if t.dtype != torch.int32:
+        raise TypeError("selected must be int32")
+    if t.dim() != 3 or t.size(0) != T or t.size(1) != H or not t.is_contiguous():
+        raise ValueError(f"selected must be a contiguous [{T}, {H}, topk] tensor")
+    return t.data_ptr()
+
+
+def kvq_sparse_attention_workspace(num_tokens: int, num_heads: int, num_q_heads: int, head_dim: int, block_size: int,
+                                   topk: int) -> int:
+    return int(_lib().kvq_sparse_attention_workspace(num_tokens, num_heads, num_q_heads, head_dim, block_size, topk))
+
+
+def kvq_sparse_attention(pool: KvPool, block_table: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int,
+                         q: torch.Tensor, query_starts: torch.Tensor, max_query_len: int, selected: torch.Tensor,
+                         scale: float, out: torch.Tensor, *, softcap: float = 0.0,
+                         workspace: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
+                         stream=None) -> torch.Tensor:
+    """kvq_attention over the listed blocks alone: selected [T, H, topk] int32 as kvq_select_blocks
+    writes it.  A workspace tensor is allocated when none is given."""
+    if block_table.dtype != torch.int32:
+        raise TypeError("block_table must be int32")
+    if not block_table.is_contiguous():
+        raise ValueError("block_table must be contiguous [S, max_blocks]")
+    S, max_blocks = block_table.shape
+    qi, oo = _bf16_in(q, "q"), _bf16_out(out, "out")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    T, Hq, D = q.shape
+    if D != pool.head_dim:
+        raise ValueError(f"q has head_dim {D}, the pool {pool.head_dim}")
+    H = pool.num_heads
+    sel = _lists(selected, T, H)
+    topk = selected.size(2)
+    if workspace is None:
+        need = kvq_sparse_attention_workspace(T, H, Hq, D, pool.block_size, topk)
+        if need > 0:
+            workspace = _workspace(need, q.device, stream)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ps = pool._struct()
+    _check(_lib().kvq_sparse_attention(
+        ctypes.byref(ps), block_table.data_ptr(), S, max_blocks, _vec(seq_lens, torch.int32, "seq_lens", S),
+        max_seq_len, ctypes.byref(qi), _vec(query_starts, torch.int32, "query_starts", S + 1), T, max_query_len, Hq,
+        sel, topk, float(scale), float(softcap), ctypes.byref(oo), _ptr(workspace), nbytes, _ptr(dev_status),
+        _stream(stream)))
     return out
 
 

@@ -68,6 +68,16 @@ class AttnOptions(ctypes.Structure):
     ]
 
 
+class Rotation(ctypes.Structure):
+    _fields_ = [
+        ("cos_sin", ctypes.c_void_p),
+        ("num_positions", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("positions", ctypes.c_void_p),
+    ]
+
+
 class Packed(ctypes.Structure):
     _fields_ = [
         ("fmt", ctypes.c_int32),
@@ -109,6 +119,15 @@ SIGNATURES = {
                             _I32, _I32, ctypes.c_float, ctypes.POINTER(AttnOptions), ctypes.POINTER(Bf16Out),
                             _P, ctypes.c_size_t, _P, _P]),
     "kvq_attention_workspace": (ctypes.c_size_t, [_I32] * 7),
+    "kvq_append": (_ST, [ctypes.POINTER(Bf16In), ctypes.POINTER(Bf16In), _I32, _P, ctypes.POINTER(Pool),
+                         ctypes.POINTER(Rotation), ctypes.POINTER(Bf16In), ctypes.POINTER(Bf16Out), _I32, _P, _P, _P]),
+    "kvq_select_blocks": (_ST, [_P, _I64, _I32, _I32, _I32, _P, _I32, _I32, _P, _I32, ctypes.POINTER(Bf16In), _P,
+                                _I32, _I32, _I32, _I32, _I32, _I32, _P, _P, ctypes.c_size_t, _P, _P]),
+    "kvq_select_blocks_workspace": (ctypes.c_size_t, [_I32] * 4),
+    "kvq_sparse_attention": (_ST, [ctypes.POINTER(Pool), _P, _I32, _I32, _P, _I32, ctypes.POINTER(Bf16In), _P, _I32,
+                                   _I32, _I32, _P, _I32, ctypes.c_float, ctypes.c_float, ctypes.POINTER(Bf16Out), _P,
+                                   ctypes.c_size_t, _P, _P]),
+    "kvq_sparse_attention_workspace": (ctypes.c_size_t, [_I32] * 6),
     "kvq_plan_pages": (_ST, [_P, _P, _I32, _P, _I32, _I32, _P, _I32, _P, _P, _P, _P, _I32, _P, _P, _P]),
     "kvq_storage_bytes": (ctypes.c_size_t, [_ST, _ST, _I32, _I64, _I32, _I32]),
     "kvq_status_string": (ctypes.c_char_p, [_ST]),

@@ -742,6 +742,221 @@ KVQ_API kvq_status kvq_decode_residual(const kvq_packed* payload, const int32_t*
                                         reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// Whether two strided views [rows][heads][dim] of bf16 may share an element: never where their
+// spans are apart, nor where both have one row pitch and each row's span lies in a part of that
+// pitch of its own (views of a fused projection's output).
+static bool views_meet(const void* a, int64_t a_row, int64_t a_head, int64_t a_heads, const void* b, int64_t b_row,
+                       int64_t b_head, int64_t b_heads, int64_t rows, int64_t dim) {
+  const int64_t ra = 2 * ((a_heads - 1) * a_head + dim), rb = 2 * ((b_heads - 1) * b_head + dim);  // of one row
+  const int64_t a0 = reinterpret_cast<int64_t>(a), b0 = reinterpret_cast<int64_t>(b);
+  const int64_t sa = 2 * (rows - 1) * a_row + ra, sb = 2 * (rows - 1) * b_row + rb;
+  if (a0 + sa <= b0 || b0 + sb <= a0) return false;
+  const int64_t pitch = 2 * a_row;
+  if (a_row != b_row || pitch <= 0) return true;
+  const int64_t off = ((b0 - a0) % pitch + pitch) % pitch;  // b's rows begin this far behind a's
+  return off < ra || off + rb > pitch;
+}
+
+KVQ_API kvq_status kvq_append(const kvq_bf16_in* k, const kvq_bf16_in* v, int32_t num_tokens, const int64_t* slot_ids,
+                              const kvq_pool* pool, const kvq_rotation* rotation, const kvq_bf16_in* q,
+                              const kvq_bf16_out* q_out, int32_t num_q_heads, void* key_bounds, uint32_t* dev_status,
+                              kvq_stream_t stream) {
+  if (pool == nullptr) return fail(KVQ_ERR_INVALID_ARG, "pool is NULL");
+  if (k == nullptr && v == nullptr && q == nullptr) return fail(KVQ_ERR_INVALID_ARG, "k, v and q are all NULL");
+  if (check_pool_fmt(pool) != KVQ_OK) return KVQ_ERR_INVALID_ARG;
+  kvq_status st = check_head_dim(pool->num_heads, pool->head_dim);
+  if (st != KVQ_OK) return st;
+  const int32_t D = pool->head_dim, H = pool->num_heads;
+  if (num_tokens < 0) return fail(KVQ_ERR_INVALID_ARG, "negative num_tokens");
+  if (pool->block_size <= 0 || pool->num_slots < 0 || pool->num_slots % pool->block_size != 0)
+    return fail(KVQ_ERR_INVALID_ARG, "num_slots must be a non-negative multiple of block_size");
+  if (!fits_u31(static_cast<int64_t>(num_tokens) * H * 2))
+    return fail(KVQ_ERR_UNSUPPORTED, "num_tokens x num_heads too large");
+  if (key_bounds != nullptr && k == nullptr) return fail(KVQ_ERR_INVALID_ARG, "key_bounds needs k");
+  const bool turns = rotation != nullptr && rotation->cos_sin != nullptr;
+  if ((q != nullptr) != (q_out != nullptr)) return fail(KVQ_ERR_INVALID_ARG, "q and q_out come together");
+  if (q != nullptr) {
+    if (!turns) return fail(KVQ_ERR_INVALID_ARG, "q needs a rotation");
+    if (num_q_heads <= 0) return fail(KVQ_ERR_INVALID_ARG, "num_q_heads must be positive (got %d)", num_q_heads);
+    if (!fits_u31(static_cast<int64_t>(num_tokens) * num_q_heads))
+      return fail(KVQ_ERR_UNSUPPORTED, "num_tokens x num_q_heads too large");
+  }
+  if (turns) {
+    if (rotation->rot_dim <= 0 || rotation->rot_dim % 16 != 0 || rotation->rot_dim > D)
+      return fail(KVQ_ERR_INVALID_ARG, "rot_dim must be a positive multiple of 16, at most head_dim (got %d)",
+                  rotation->rot_dim);
+    if (rotation->num_positions < 0) return fail(KVQ_ERR_INVALID_ARG, "negative num_positions");
+  }
+  if (num_tokens == 0) return KVQ_OK;
+  AppendParams p{};
+  bool v8 = true;
+  const kvq_bf16_in* src[2] = {k, v};
+  const kvq_plane* dst[2] = {&pool->k, &pool->v};
+  const char* names[2] = {"k", "v"};
+  for (int j = 0; j < 2; ++j) {
+    if (src[j] == nullptr) continue;
+    if ((st = check_view(src[j]->ptr, src[j]->row_pitch, src[j]->head_pitch, names[j], v8)) != KVQ_OK) return st;
+    const int32_t fmt = plane_fmt(pool, j);
+    if ((st = check_pool_plane(fmt, dst[j])) != KVQ_OK) return st;
+    AppendTensor& t = p.ten[p.ntensors++];
+    t.x = static_cast<const uint16_t*>(src[j]->ptr);
+    t.row_pitch = src[j]->row_pitch;
+    t.head_pitch = src[j]->head_pitch;
+    t.dst = Nvfp4Planes{dst[j]->codes, dst[j]->bscale, dst[j]->rscale};
+    t.fmt = fmt;
+    t.key = j == 0;
+  }
+  if (p.ntensors > 0 && (st = check_dev(slot_ids, "slot_ids")) != KVQ_OK) return st;
+  if (key_bounds != nullptr && (st = check_plane(key_bounds, "key_bounds")) != KVQ_OK) return st;
+  if (turns) {
+    if ((st = check_plane(rotation->cos_sin, "cos_sin")) != KVQ_OK) return st;
+    if ((st = check_dev(rotation->positions, "positions")) != KVQ_OK) return st;
+  }
+  if (q != nullptr) {
+    if ((st = check_view(q->ptr, q->row_pitch, q->head_pitch, "q", v8)) != KVQ_OK) return st;
+    if ((st = check_view(q_out->ptr, q_out->row_pitch, q_out->head_pitch, "q_out", v8)) != KVQ_OK) return st;
+    const bool same = q->ptr == q_out->ptr && q->row_pitch == q_out->row_pitch && q->head_pitch == q_out->head_pitch;
+    auto meets = [&](const kvq_bf16_in* x, int32_t heads) {
+      return x != nullptr && views_meet(q_out->ptr, q_out->row_pitch, q_out->head_pitch, num_q_heads, x->ptr,
+                                        x->row_pitch, x->head_pitch, heads, num_tokens, D);
+    };
+    if (!same && meets(q, num_q_heads))
+      return fail(KVQ_ERR_INVALID_ARG, "q_out overlaps q without being the same view");
+    if (meets(k, H) || meets(v, H)) return fail(KVQ_ERR_INVALID_ARG, "q_out overlaps k or v");
+    p.q = static_cast<const uint16_t*>(q->ptr);
+    p.q_row_pitch = q->row_pitch;
+    p.q_head_pitch = q->head_pitch;
+    p.q_out = static_cast<uint16_t*>(q_out->ptr);
+    p.qo_row_pitch = q_out->row_pitch;
+    p.qo_head_pitch = q_out->head_pitch;
+    p.Hq = num_q_heads;
+  }
+  if (dev_status != nullptr && (st = check_dev(dev_status, "dev_status")) != KVQ_OK) return st;
+  p.T = num_tokens;
+  p.H = H;
+  p.nb = D / 16;
+  p.slot_ids = slot_ids;
+  p.num_slots = pool->num_slots;
+  p.block_size = pool->block_size;
+  if (turns) {
+    p.cos_sin = rotation->cos_sin;
+    p.positions = rotation->positions;
+    p.num_positions = rotation->num_positions;
+    p.rot = rotation->rot_dim;
+    p.pairs = rotation->interleaved != 0;
+  }
+  p.bounds = static_cast<uint16_t*>(key_bounds);
+  p.status = dev_status;
+  dbg_clear();
+  for (int j = 0; j < 2; ++j) {
+    if (src[j] == nullptr) continue;
+    dbg_add(src[j]->ptr, view_bytes(num_tokens, src[j]->row_pitch, H, src[j]->head_pitch, D), names[j]);
+    dbg_plane(pool, dst[j], plane_fmt(pool, j));
+  }
+  if (p.ntensors > 0) dbg_add(slot_ids, 8ll * num_tokens, "slot_ids");
+  if (turns) {
+    dbg_add(rotation->cos_sin, 4ll * rotation->num_positions * rotation->rot_dim, "cos_sin");
+    dbg_add(rotation->positions, 4ll * num_tokens, "positions");
+  }
+  if (q != nullptr) {
+    dbg_add(q->ptr, view_bytes(num_tokens, q->row_pitch, num_q_heads, q->head_pitch, D), "q");
+    dbg_add(q_out->ptr, view_bytes(num_tokens, q_out->row_pitch, num_q_heads, q_out->head_pitch, D), "q_out");
+  }
+  dbg_add(key_bounds, pool->num_slots / pool->block_size * H * 4 * D, "key_bounds");
+  dbg_add(dev_status, 4, "status");
+  return launched(launch_append(p, v8, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+KVQ_API size_t kvq_select_blocks_workspace(int32_t num_tokens, int32_t num_heads, int32_t max_seq_len, int32_t block_size) {
+  if (block_size <= 0 || max_seq_len <= 0) return 0;
+  return select_workspace_bytes(num_tokens, num_heads,
+                                static_cast<int32_t>((static_cast<int64_t>(max_seq_len) + block_size - 1) / block_size));
+}
+
+KVQ_API kvq_status kvq_select_blocks(const void* key_bounds, int64_t num_blocks, int32_t block_size, int32_t num_heads,
+                                     int32_t head_dim, const int32_t* block_table, int32_t num_seqs, int32_t max_blocks,
+                                     const int32_t* seq_lens, int32_t max_seq_len, const kvq_bf16_in* q,
+                                     const int32_t* query_starts, int32_t num_tokens, int32_t max_query_len,
+                                     int32_t num_q_heads, int32_t first_blocks, int32_t last_blocks, int32_t topk,
+                                     int32_t* selected, void* workspace, size_t workspace_bytes, uint32_t* dev_status,
+                                     kvq_stream_t stream) {
+  if (q == nullptr) return fail(KVQ_ERR_INVALID_ARG, "q is NULL");
+  kvq_status st = check_head_dim(num_heads, head_dim);
+  if (st != KVQ_OK) return st;
+  const int32_t D = head_dim, H = num_heads;
+  if (D != 64 && D != 128 && D != 256)
+    return fail(KVQ_ERR_UNSUPPORTED, "block selection supports head_dim 64, 128 or 256 (got %d)", D);
+  if (block_size <= 0 || num_blocks < 0)
+    return fail(KVQ_ERR_INVALID_ARG, "block_size must be positive and num_blocks not negative");
+  if (num_seqs < 0 || max_blocks < 0 || max_seq_len < 0 || num_tokens < 0 || max_query_len < 0)
+    return fail(KVQ_ERR_INVALID_ARG, "negative num_seqs, max_blocks, max_seq_len, num_tokens or max_query_len");
+  if (num_q_heads <= 0 || num_q_heads % H != 0)
+    return fail(KVQ_ERR_INVALID_ARG, "num_q_heads must be a positive multiple of num_heads");
+  if (num_q_heads / H > 16) return fail(KVQ_ERR_UNSUPPORTED, "at most 16 query heads per KV head");
+  if (topk <= 0) return fail(KVQ_ERR_INVALID_ARG, "topk must be positive (got %d)", topk);
+  if (first_blocks < 0 || last_blocks < 0 || static_cast<int64_t>(first_blocks) + last_blocks > topk)
+    return fail(KVQ_ERR_INVALID_ARG, "first_blocks and last_blocks must not be negative, nor more than topk together");
+  if (num_seqs > 65535 || H > 65535) return fail(KVQ_ERR_UNSUPPORTED, "num_seqs and num_heads must be <= 65535");
+  const int64_t cap = std::min(static_cast<int64_t>(max_blocks) * block_size, static_cast<int64_t>(max_seq_len));
+  if (cap > 0x7FFF0000) return fail(KVQ_ERR_UNSUPPORTED, "sequences of more than 2^31 - 65536 tokens");
+  const int32_t most = static_cast<int32_t>((cap + block_size - 1) / block_size);
+  if (most > topk && most > kSelectMostBlocks)
+    return fail(KVQ_ERR_UNSUPPORTED, "sequences of more than %d blocks (got %d)", kSelectMostBlocks, most);
+  if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return KVQ_OK;
+  const int32_t max_q = std::min(max_query_len, num_tokens);
+  if (!fits_u31(static_cast<int64_t>(num_tokens) * num_q_heads) || !fits_u31(static_cast<int64_t>(max_q) * H))
+    return fail(KVQ_ERR_UNSUPPORTED, "num_tokens x num_q_heads too large");
+  bool v8 = true;
+  if ((st = check_view(q->ptr, q->row_pitch, q->head_pitch, "q", v8)) != KVQ_OK) return st;
+  if ((st = check_plane(key_bounds, "key_bounds")) != KVQ_OK) return st;
+  if ((st = check_dev(block_table, "block_table")) != KVQ_OK) return st;
+  if ((st = check_dev(seq_lens, "seq_lens")) != KVQ_OK) return st;
+  if ((st = check_dev(query_starts, "query_starts")) != KVQ_OK) return st;
+  if ((st = check_dev(selected, "selected")) != KVQ_OK) return st;
+  if (dev_status != nullptr && (st = check_dev(dev_status, "dev_status")) != KVQ_OK) return st;
+  const size_t need = kvq_select_blocks_workspace(num_tokens, H, max_seq_len, block_size);
+  if (most > topk) {
+    if ((st = check_dev(workspace, "workspace")) != KVQ_OK) return st;
+    if (!aligned(workspace, 16)) return fail(KVQ_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    if (workspace_bytes < need)
+      return fail(KVQ_ERR_INVALID_ARG, "workspace too small: %zu bytes, need %zu", workspace_bytes, need);
+  }
+  SelectParams p{};
+  p.bounds = static_cast<const uint16_t*>(key_bounds);
+  p.num_blocks = num_blocks;
+  p.div_bs = FastDiv(static_cast<uint32_t>(block_size));
+  p.table = block_table;
+  p.max_blocks = max_blocks;
+  p.seq_lens = seq_lens;
+  p.starts = query_starts;
+  p.S = num_seqs;
+  p.num_tokens = num_tokens;
+  p.max_q = max_q;
+  p.seq_cap = static_cast<int32_t>(cap);
+  p.H = H;
+  p.D = D;
+  p.group = num_q_heads / H;
+  p.q = static_cast<const uint16_t*>(q->ptr);
+  p.q_row_pitch = q->row_pitch;
+  p.q_head_pitch = q->head_pitch;
+  p.topk = topk;
+  p.first = first_blocks;
+  p.last = last_blocks;
+  p.selected = selected;
+  p.most = most;
+  p.status = dev_status;
+  dbg_clear();
+  dbg_add(key_bounds, num_blocks * H * 4 * D, "key_bounds");
+  dbg_add(q->ptr, view_bytes(num_tokens, q->row_pitch, num_q_heads, q->head_pitch, D), "q");
+  dbg_add(block_table, 4ll * num_seqs * max_blocks, "block_table");
+  dbg_add(seq_lens, 4ll * num_seqs, "seq_lens");
+  dbg_add(query_starts, 4ll * (num_seqs + 1), "query_starts");
+  dbg_add(selected, 4ll * num_tokens * H * topk, "selected");
+  if (most > topk) dbg_add(workspace, static_cast<int64_t>(need), "workspace");
+  dbg_add(dev_status, 4, "status");
+  return launched(launch_select_blocks(p, workspace, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 // Splits and tokens per split of a decode-attention call (tokens per split a multiple
 // of 64: whole 16-token tiles for each of the 4 warps).
 KVQ_API size_t kvq_decode_attention_workspace(int32_t num_seqs, int32_t num_heads, int32_t num_q_heads,
@@ -998,6 +1213,116 @@ KVQ_API kvq_status kvq_attention(const kvq_pool* pool, const int32_t* block_tabl
   if (need > 0) dbg_add(workspace, static_cast<int64_t>(need), "workspace");
   dbg_add(dev_status, 4, "status");
   return launched(launch_query_attention(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+KVQ_API size_t kvq_sparse_attention_workspace(int32_t num_tokens, int32_t num_heads, int32_t num_q_heads, int32_t head_dim,
+                                              int32_t block_size, int32_t topk) {
+  return sparse_attn_workspace_bytes(num_tokens, num_heads, num_q_heads, head_dim, block_size, topk);
+}
+
+KVQ_API kvq_status kvq_sparse_attention(const kvq_pool* pool, const int32_t* block_table, int32_t num_seqs,
+                                        int32_t max_blocks, const int32_t* seq_lens, int32_t max_seq_len,
+                                        const kvq_bf16_in* q, const int32_t* query_starts, int32_t num_tokens,
+                                        int32_t max_query_len, int32_t num_q_heads, const int32_t* selected,
+                                        int32_t topk, float scale, float softcap, const kvq_bf16_out* out,
+                                        void* workspace, size_t workspace_bytes, uint32_t* dev_status,
+                                        kvq_stream_t stream) {
+  if (pool == nullptr || q == nullptr || out == nullptr)
+    return fail(KVQ_ERR_INVALID_ARG, "pool, q and out must not be NULL");
+  if (check_pool_fmt(pool) != KVQ_OK) return KVQ_ERR_INVALID_ARG;
+  kvq_status st = check_head_dim(pool->num_heads, pool->head_dim);
+  if (st != KVQ_OK) return st;
+  const int32_t D = pool->head_dim, H = pool->num_heads;
+  if (D != 64 && D != 128 && D != 256)
+    return fail(KVQ_ERR_UNSUPPORTED, "attention supports head_dim 64, 128 or 256 (got %d)", D);
+  if (pool->block_size <= 0 || pool->num_slots < 0 || pool->num_slots % pool->block_size != 0)
+    return fail(KVQ_ERR_INVALID_ARG, "num_slots must be a non-negative multiple of block_size");
+  if (num_seqs < 0 || max_blocks < 0 || max_seq_len < 0 || num_tokens < 0 || max_query_len < 0)
+    return fail(KVQ_ERR_INVALID_ARG, "negative num_seqs, max_blocks, max_seq_len, num_tokens or max_query_len");
+  if (num_q_heads <= 0 || num_q_heads % H != 0)
+    return fail(KVQ_ERR_INVALID_ARG, "num_q_heads must be a positive multiple of num_heads");
+  if (num_q_heads / H > 16) return fail(KVQ_ERR_UNSUPPORTED, "at most 16 query heads per KV head");
+  if (topk <= 0) return fail(KVQ_ERR_INVALID_ARG, "topk must be positive (got %d)", topk);
+  if (topk > kSparseMostBlocks)
+    return fail(KVQ_ERR_UNSUPPORTED, "lists of more than %d blocks (got %d)", kSparseMostBlocks, topk);
+  if (!(scale > 0.0f && scale <= 3.4028235e38f))
+    return fail(KVQ_ERR_INVALID_ARG, "scale must be positive and finite (got %g)", static_cast<double>(scale));
+  if (!(softcap >= 0.0f && softcap <= 3.4028235e38f))
+    return fail(KVQ_ERR_INVALID_ARG, "softcap must be 0 or positive and finite (got %g)", static_cast<double>(softcap));
+  if (softcap > 0.0f && (softcap < 0x1p-10f || softcap > 0x1p+10f))
+    return fail(KVQ_ERR_UNSUPPORTED, "softcap outside 2^-10 .. 2^10 (got %g)", static_cast<double>(softcap));
+  if (num_seqs > 65535 || H > 65535) return fail(KVQ_ERR_UNSUPPORTED, "num_seqs and num_heads must be <= 65535");
+  const int64_t cap = std::min(static_cast<int64_t>(max_blocks) * pool->block_size, static_cast<int64_t>(max_seq_len));
+  if (cap > kMaxSeqTokens || static_cast<int64_t>(topk) * pool->block_size > kMaxSeqTokens)
+    return fail(KVQ_ERR_UNSUPPORTED, "sequences or lists of more than 2^31 - 65536 tokens");
+  if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return KVQ_OK;
+  const int32_t max_q = std::min(max_query_len, num_tokens);
+  if (!fits_u31(static_cast<int64_t>(num_tokens) * num_q_heads) || !fits_u31(static_cast<int64_t>(max_q) * 256))
+    return fail(KVQ_ERR_UNSUPPORTED, "num_tokens too large");
+  bool v8 = true;
+  if ((st = check_view(q->ptr, q->row_pitch, q->head_pitch, "q", v8)) != KVQ_OK) return st;
+  if ((st = check_view(out->ptr, out->row_pitch, out->head_pitch, "out", v8)) != KVQ_OK) return st;
+  const int32_t fk = plane_fmt(pool, 0), fv = plane_fmt(pool, 1);
+  if ((st = check_pool_plane(fk, &pool->k)) != KVQ_OK) return st;
+  if ((st = check_pool_plane(fv, &pool->v)) != KVQ_OK) return st;
+  if ((st = check_dev(block_table, "block_table")) != KVQ_OK) return st;
+  if ((st = check_dev(seq_lens, "seq_lens")) != KVQ_OK) return st;
+  if ((st = check_dev(query_starts, "query_starts")) != KVQ_OK) return st;
+  if ((st = check_dev(selected, "selected")) != KVQ_OK) return st;
+  if (dev_status != nullptr && (st = check_dev(dev_status, "dev_status")) != KVQ_OK) return st;
+  const size_t need = kvq_sparse_attention_workspace(num_tokens, H, num_q_heads, D, pool->block_size, topk);
+  if (need > 0) {
+    if ((st = check_dev(workspace, "workspace")) != KVQ_OK) return st;
+    if (!aligned(workspace, 16)) return fail(KVQ_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    if (workspace_bytes < need)
+      return fail(KVQ_ERR_INVALID_ARG, "workspace too small: %zu bytes, need %zu", workspace_bytes, need);
+  }
+  SparseAttnParams sp{};
+  QueryAttnParams& p = sp.q;
+  AttnParams& a = p.a;
+  a.k = AttnPlane{pool->k.codes, pool->k.bscale, pool->k.rscale};
+  a.v = AttnPlane{pool->v.codes, pool->v.bscale, pool->v.rscale};
+  set_plane_fmts(a, fk, fv);
+  a.q = static_cast<const uint16_t*>(q->ptr);
+  a.q_row_pitch = q->row_pitch;
+  a.q_head_pitch = q->head_pitch;
+  a.out = static_cast<uint16_t*>(out->ptr);
+  a.o_row_pitch = out->row_pitch;
+  a.o_head_pitch = out->head_pitch;
+  a.ws = static_cast<float*>(workspace);
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.max_blocks = max_blocks;
+  a.seq_cap = static_cast<int32_t>(cap);
+  a.block_size = pool->block_size;
+  a.div_bs = FastDiv(static_cast<uint32_t>(pool->block_size));
+  a.num_blocks = pool->num_slots / pool->block_size;
+  a.S = num_seqs;
+  a.H = H;
+  a.Hq = num_q_heads;
+  a.D = D;
+  a.group = num_q_heads / H;
+  a.max_len = max_seq_len;
+  a.scale = scale;
+  a.status = dev_status;
+  p.starts = query_starts;
+  p.num_tokens = num_tokens;
+  p.max_q = max_q;
+  p.softcap = softcap;
+  sp.selected = selected;
+  sp.topk = topk;
+  dbg_clear();
+  dbg_plane(pool, &pool->k, fk);
+  dbg_plane(pool, &pool->v, fv);
+  dbg_add(q->ptr, view_bytes(num_tokens, q->row_pitch, num_q_heads, q->head_pitch, D), "q");
+  dbg_add(out->ptr, view_bytes(num_tokens, out->row_pitch, num_q_heads, out->head_pitch, D), "out");
+  dbg_add(block_table, 4ll * num_seqs * max_blocks, "block_table");
+  dbg_add(seq_lens, 4ll * num_seqs, "seq_lens");
+  dbg_add(query_starts, 4ll * (num_seqs + 1), "query_starts");
+  dbg_add(selected, 4ll * num_tokens * H * topk, "selected");
+  if (need > 0) dbg_add(workspace, static_cast<int64_t>(need), "workspace");
+  dbg_add(dev_status, 4, "status");
+  return launched(launch_sparse_attention(sp, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 KVQ_API kvq_status kvq_plan_pages(const int32_t* cached_lens, const int32_t* new_lens, int32_t num_seqs,

@@ -189,6 +189,71 @@ struct PageEncodeParams {
 cudaError_t launch_page_encode(const PageEncodeParams& p, bool v8, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
+// K and V rows into a pool, K and Q turned by their positions' angles.
+// ---------------------------------------------------------------------------
+struct AppendTensor {
+  const uint16_t* x;        // bf16 [T][H][D] through the pitches
+  int64_t row_pitch;
+  int64_t head_pitch;
+  Nvfp4Planes dst;          // dst.rscale: [slots][H], or [blocks][H] (fmt 5)
+  int32_t fmt;              // 1 NVFP4, 3 FP8, 5 page-scaled FP8
+  bool key;                 // turned, and counted in the bounds
+};
+struct AppendParams {
+  AppendTensor ten[2];
+  int32_t ntensors;         // 0 to 2
+  int32_t T, H, nb;         // tokens, KV heads, D / 16
+  const int64_t* slot_ids;  // [T]
+  int64_t num_slots;
+  int32_t block_size;
+  const float* cos_sin;     // [num_positions][rot]: cosines, then sines; nullptr: nothing is turned
+  const int32_t* positions; // [T]
+  int32_t num_positions;
+  int32_t rot;              // channels turned
+  bool pairs;               // neighbours form a pair, else channels rot / 2 apart
+  uint16_t* bounds;         // bf16 [blocks][H][2][D] or nullptr
+  const uint16_t* q;        // bf16 [T][Hq][D] or nullptr
+  int64_t q_row_pitch, q_head_pitch;
+  uint16_t* q_out;
+  int64_t qo_row_pitch, qo_head_pitch;
+  int32_t Hq;
+  uint32_t* status;
+  int32_t chunk;            // set by the launcher: tokens whose runs one warp serves (<= 32),
+  int32_t q_heads, q_parts; // heads of a token that one warp turns, and how many such parts it has,
+  int64_t row_blocks;       // thread blocks of K and V; those behind turn Q
+};
+cudaError_t launch_append(const AppendParams& p, bool v8, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// Blocks of the highest score bounds.
+// ---------------------------------------------------------------------------
+struct SelectParams {
+  const uint16_t* bounds;   // bf16 [num_blocks][H][2][D]: least, largest keys
+  int64_t num_blocks;
+  FastDiv div_bs;
+  const int32_t* table;     // [S][max_blocks]
+  int32_t max_blocks;
+  const int32_t* seq_lens;  // [S]
+  const int32_t* starts;    // [S + 1]
+  int32_t S, num_tokens, max_q, seq_cap;
+  int32_t H, D, group;
+  const uint16_t* q;        // bf16 [num_tokens][H group][D] through the pitches
+  int64_t q_row_pitch, q_head_pitch;
+  int32_t topk, first, last;
+  int32_t* selected;        // [num_tokens][H][topk]
+  int32_t most;             // most blocks a query sees
+  uint32_t* status;
+  uint32_t* keys;           // set by the launcher: scores [num_tokens][H][pitch], as ordered keys
+  int32_t pitch;
+  float* tops;              // largest |bound| of each 32 blocks, [num_tokens][H][tops_pitch], at a sequence's first token
+  int32_t tops_pitch;
+  float err;                // of a score, relative to |q|_1 max |bound|
+};
+constexpr int kSelectMostBlocks = 32768;
+size_t select_workspace_bytes(int32_t T, int32_t H, int32_t most);
+cudaError_t launch_select_blocks(const SelectParams& p, void* workspace, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
 // Block tables and slot maps from request lengths.
 // ---------------------------------------------------------------------------
 struct PlanParams {
@@ -323,6 +388,15 @@ int fill_splits(int64_t ctas, int64_t slots, int32_t tokens, int32_t min_one, in
 cudaError_t launch_query_pages_64(const QueryAttnParams& p, bool two, cudaStream_t s);
 cudaError_t launch_query_pages_128(const QueryAttnParams& p, bool two, cudaStream_t s);
 cudaError_t launch_query_pages_256(const QueryAttnParams& p, cudaStream_t s);  // 8
+// Attention over listed blocks.
+struct SparseAttnParams {
+  QueryAttnParams q;         // no bias, window, prefix or key starts
+  const int32_t* selected;   // [num_tokens][H][topk]
+  int32_t topk;
+};
+constexpr int kSparseMostBlocks = 4096;
+size_t sparse_attn_workspace_bytes(int32_t T, int32_t H, int32_t Hq, int32_t D, int32_t block_size, int32_t topk);
+cudaError_t launch_sparse_attention(const SparseAttnParams& p, cudaStream_t s);
 int query_tile_rows(int32_t D);  // rows a CTA of the tile kernel takes
 cudaError_t launch_query_tiles(const QueryAttnParams& p, cudaStream_t s);
 cudaError_t launch_payload_decode(const UnpackParams& p, int lanes, bool v8, cudaStream_t s);
