@@ -245,9 +245,10 @@ struct SelectParams {
   uint32_t* status;
   uint32_t* keys;           // set by the launcher: scores [num_tokens][H][pitch], as ordered keys
   int32_t pitch;
-  float* tops;              // largest |bound| of each 32 blocks, [num_tokens][H][tops_pitch], at a sequence's first token
-  int32_t tops_pitch;
-  float err;                // of a score, relative to |q|_1 max |bound|
+  float* sizes;             // what a part of a row's scores may be off by, over err: [num_tokens][H][sizes_pitch]
+  int32_t sizes_pitch;
+  int32_t sizes_step;       // blocks of a part
+  float err;
 };
 constexpr int kSelectMostBlocks = 32768;
 size_t select_workspace_bytes(int32_t T, int32_t H, int32_t most);

@@ -75,11 +75,12 @@ def test_a_list_for_all_needs_no_scores():
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
-@pytest.mark.parametrize("blocks", [60, 700, 5000])
-def test_near_ties(D, blocks):
+@pytest.mark.parametrize("blocks", [60, 700, 1500, 5000])
+@pytest.mark.parametrize("new", [1, 12])
+def test_near_ties(D, blocks, new):
     """Scores that differ by less than binary32 resolves: one channel adds 2^20 to all, another
     tells the blocks apart by multiples of 2^-8; then by differences that only the last bits of binary64 show."""
-    c = Case([16 * blocks], [1], 2, 2, D, 16, seed=D)
+    c = Case([16 * blocks], [new], 2, 2, D, 16, seed=D)
     r = np.random.RandomState(blocks)
     for step, count in ((2.0 ** -8, 200), (2.0 ** -26, 250)):
         b = np.zeros(c.bounds.shape, np.float32)
@@ -94,8 +95,9 @@ def test_near_ties(D, blocks):
             c.check(topk, 1, 1)
 
 
-def test_equal_scores_go_by_index():
-    c = Case([16 * 300], [2], 2, 4, 128, 16)
+@pytest.mark.parametrize("blocks,new", [(300, 2), (300, 70), (2000, 3), (5000, 9)])
+def test_equal_scores_go_by_index(blocks, new):
+    c = Case([16 * blocks], [new], 2, 4, 128, 16)
     c.bounds[:] = c.bounds[0]
     c.check(40)
     c.bounds[::3] = c.bounds[0] * 1.5
@@ -106,16 +108,17 @@ def test_equal_scores_go_by_index():
     c.check(7)
 
 
-@pytest.mark.parametrize("D", [64, 256])
-def test_large_small_and_absent_numbers(D):
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new", [3, 20])
+def test_large_small_and_absent_numbers(D, new):
     """Sums that overflow binary32 and cancel in binary64, subnormal ones, infinities and NaN."""
-    c = Case([16 * 90], [3], 2, 2, D, 16, seed=1)
+    c = Case([16 * 90], [new], 2, 2, D, 16, seed=1)
     c.q[0] = (c.q[0].float() * 2.0 ** 100).to(torch.bfloat16)
     c.q[1] = (c.q[1].float() * 2.0 ** -126).to(torch.bfloat16)
-    for f in (1.0, 2.0 ** 100, 2.0 ** -126):
+    for f in (1.0, 2.0 ** 100, 2.0 ** -100, 2.0 ** -126):
         c.bounds = (c.bounds.float() * f).to(torch.bfloat16)
         c.check(12)
-    c = Case([16 * 90], [3], 2, 2, D, 16, seed=2)
+    c = Case([16 * 90], [new], 2, 2, D, 16, seed=2)
     c.bounds[c.table[0, 10], 0, 1, 3] = float("inf")
     c.bounds[c.table[0, 11], 0, 0, 3] = float("-inf")
     c.bounds[c.table[0, 12], 0, 1, 3] = float("nan")
@@ -127,8 +130,9 @@ def test_large_small_and_absent_numbers(D):
         c.check(topk)
 
 
-def test_blocks_outside_the_pool_come_last():
-    c = Case([16 * 50, 16 * 30], [1, 2], 2, 4, 128, 16)
+@pytest.mark.parametrize("new", [[1, 2], [30, 2]])
+def test_blocks_outside_the_pool_come_last(new):
+    c = Case([16 * 50, 16 * 30], new, 2, 4, 128, 16)
     c.table[0, 5], c.table[0, 49], c.table[1, 7] = -1, c.bounds.size(0), 10 ** 9
     c.check(10, status=kvq.DEV_BAD_BLOCK)
     c.check(49, status=kvq.DEV_BAD_BLOCK)
