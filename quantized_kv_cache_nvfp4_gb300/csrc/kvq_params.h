@@ -245,9 +245,10 @@ struct SelectParams {
   uint32_t* status;
   uint32_t* keys;           // set by the launcher: scores [num_tokens][H][pitch], as ordered keys
   int32_t pitch;
-  float* sizes;             // what a part of a row's scores may be off by, over err: [num_tokens][H][sizes_pitch]
+  float* sizes;             // what parts of a row's scores may be off by, over err: [num_tokens][H][sizes_pitch]
   int32_t sizes_pitch;
-  int32_t sizes_step;       // blocks of a part
+  int32_t sizes_n;          // parts in use
+  int32_t segment;          // tile kernel: blocks of a part
   float err;
 };
 constexpr int kSelectMostBlocks = 32768;

@@ -16,9 +16,9 @@
 // fifty has such blocks; exact ties go the same way to the index.  What binary32 cannot bound (sums that
 // may overflow) all goes to binary64.
 //
-// Few queries a sequence (score_kernel): a warp streams blocks' bounds by bulk copies and takes the
-// dot products in registers.  Bound: HBM.  From kTileQueries queries on (score_tile_kernel): a product
-// of 64 queries and 128 blocks on the tensor cores, q split into two bf16 parts.
+// Both score kernels take the dot products on the tensor cores, q split into bf16 parts: with the blocks
+// as rows and the parts as columns for few queries a sequence (score_kernel; bound: HBM), by tiles of 64
+// queries and 128 blocks from kTileQueries on (score_tile_kernel).
 #include <algorithm>
 
 #include "kvq_device.cuh"
@@ -42,12 +42,38 @@ __device__ __forceinline__ float key_score(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) != 0u ? k & 0x7FFFFFFFu : ~k);
 }
 
-constexpr int kScoreWarps = 4;
-constexpr int kScoreQueries = 8;  // of one pass over the bounds
-constexpr int kScoreBytes = 16384;  // of bounds that a warp has in flight
+// A bf16 (the upper half of u) in binary64, by its bits: conversions run at the rate of the
+// binary64 unit, two a cycle and SM.
+__device__ __forceinline__ double wide(uint32_t u) {
+  const uint32_t e = (u >> 23) & 0xFFu;
+  if (e == 0u || e == 0xFFu) return static_cast<double>(__uint_as_float(u));  // zeros, subnormal numbers, infinities, NaN
+  return __hiloint2double(static_cast<int>((u & 0x80000000u) | (((u & 0x7FFFFFFFu) >> 3) + (896u << 20))), 0);
+}
+
+constexpr int kScoreQueries = 8;  // of a sequence, at most; more go to the tile kernel
+constexpr int kTileQueries = kScoreQueries + 1;
+
+// The score kernel's shared memory, for hc KV heads a thread block: stages of 16 `part` blocks of the
+// cache (rows of the heads' bounds, 16 bytes apart: conflict-free ldmatrix), q as operand fragments, a
+// row of zeros, the warps' sizes.
 template <int D>
-constexpr int kScoreBlocks = kScoreBytes / (4 * D);  // cache blocks of a warp
-constexpr int kTileQueries = 9;  // queries a sequence from which on the tile kernel takes the call
+constexpr int kScoreWarps = D == 256 ? 4 : 8;  // and one that copies
+struct ScorePlan {
+  int hc, part, row, stage, stages, groups, frag, smem;
+  __host__ __device__ ScorePlan(int H, int D, int max_q) {
+    const int warps = D == 256 ? 4 : 8;
+    hc = H < warps ? H : warps;
+    part = warps / hc;  // warps of a head
+    row = hc * 4 * D + 16;
+    stage = 16 * part * row;
+    groups = max_q <= 4 ? 1 : 2;  // of 8 operand columns: 2 queries in three parts, or 4 in two
+    frag = hc * groups * (D / 8) * 256;
+    const int rest = 4 * D + warps * kScoreQueries * 4;
+    stages = (227 * 1024 - 512 - frag - rest) / stage;
+    if (stages > 6) stages = 6;
+    smem = stages * stage + frag + rest;
+  }
+};
 
 // First query token and number of query tokens of sequence s (see query_range, query_attn.cuh).
 __device__ __forceinline__ bool select_range(const SelectParams& p, int s, int& q0, int& n, int& len) {
@@ -95,141 +121,239 @@ __device__ __forceinline__ void sum_heads(const SelectParams& p, int tok, int h,
   }
 }
 
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Scores of a run of blocks of one (sequence, KV head) for all its query tokens.  Each lane of a warp
-// copies its blocks' bounds to shared memory, all at once (16 KB a warp in flight); then the warp
-// reads one block's with one load a lane, and adds up the sums of 8 blocks over its lanes by 9
-// shuffles (halving the sums with the lanes).
+// Scores of a segment of a sequence's blocks for up to 8 KV heads and up to 8 query tokens.  A producer
+// warp copies the heads' bounds of whole blocks (one run of memory each) through a ring of stages;
+// consumer warp w serves head w % hc and 16 blocks of a stage: mma.sync m16n8k16 with the blocks as rows
+// and the queries as columns, q+ and q- in three bf16 parts (q exactly, up to 2 queries) or two (what
+// is left below 2^-18 of it), a column each.  The products of a step of 16 channels are added up by the
+// tensor cores, the steps in binary32 registers, which keeps the bound on the roundings 16 times
+// smaller than one chain would.  (Dot products by FMA, 8 blocks a warp and a reduction over its
+// lanes, took 73 us of 32 x 2048 blocks and 8 heads at head_dim 128, the copies alone 44.)
 template <int D>
-__global__ void __launch_bounds__(32 * kScoreWarps, 3) score_kernel(const SelectParams p) {
-  constexpr int kC = D / 16;  // values of a lane
-  constexpr int kB = kScoreBlocks<D>, kGroups = kB / 8;
+__global__ void __launch_bounds__(32 * (kScoreWarps<D> + 1), 1) score_kernel(const SelectParams p) {
+  constexpr int kW = kScoreWarps<D>, kSteps = 2 * D / 16;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ __align__(16) float coef[kScoreQueries][2 * D];
-  __shared__ __align__(8) uint64_t bars[kScoreWarps][kGroups];
+  __shared__ __align__(8) uint64_t bars[2][6];
+  __shared__ uint32_t have[6][4];  // bit j of [x]: block 32 x + j of the stage has bounds
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = blockIdx.y, s = blockIdx.z;
+  const int segment = blockIdx.x, s = blockIdx.z;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int q0, n, len;
   if (!select_range(p, s, q0, n, len) || n == 0) return;
   const int blocks = static_cast<int>(p.div_bs.div(static_cast<uint32_t>(len - 1))) + 1;
-  const int c0 = static_cast<int>(blockIdx.x) * kScoreWarps * kB;
-  if (blocks <= p.topk || c0 >= blocks) return;
-  const int b0 = c0 + warp * kB;
-  unsigned char* const ring = smem + warp * kScoreBytes;
-  const uint32_t ring_s = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-  const uint32_t bar0 = static_cast<uint32_t>(__cvta_generic_to_shared(&bars[warp][0]));
-  if (lane == 0) {
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) mbar_init(bar0 + 8 * g, 1);
+  if (blocks <= p.topk) return;
+  const ScorePlan plan(p.H, D, p.max_q);
+  const bool three = p.max_q <= 2;
+  const int h0 = static_cast<int>(blockIdx.y) * plan.hc, hn = min(plan.hc, p.H - h0);  // heads h0 .. h0 + hn - 1
+  // equal segments in groups of 16 blocks; a stage takes `part` of them
+  const int groups = (blocks + 15) / 16, per = (groups + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+  const int first = 16 * min(segment * per, groups), last = min(blocks, first + 16 * per);
+  const int stage_blocks = 16 * plan.part, count = first < last ? (last - first + stage_blocks - 1) / stage_blocks : 0;
+  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+  const uint32_t full0 = static_cast<uint32_t>(__cvta_generic_to_shared(&bars[0][0]));
+  const uint32_t empty0 = static_cast<uint32_t>(__cvta_generic_to_shared(&bars[1][0]));
+  unsigned char* const frag = smem + plan.stages * plan.stage;  // [head][column group][step][lane] {k 2c, 2c + 1 | + 8, + 9}
+  const int off_zero = plan.stages * plan.stage + plan.frag;
+  if (threadIdx.x == 0) {
+    for (int st = 0; st < plan.stages; ++st) {
+      mbar_init(full0 + 8 * st, 1);
+      mbar_init(empty0 + 8 * st, kW);
+    }
     mbar_init_fence();
   }
-  __syncwarp();
-  uint32_t have[(kB + 31) / 32];  // bit j: block b0 + 32 x + j has bounds
-#pragma unroll
-  for (int x = 0; x < (kB + 31) / 32; ++x) {
-    const int j = 32 * x + lane, b = b0 + j;
-    const bool in = j < kB && b < blocks;
-    const int64_t blk = in ? LDX(p.table + static_cast<int64_t>(s) * p.max_blocks + b) : -1;
-    const bool ok = in && blk >= 0 && blk < p.num_blocks;
-    if (__any_sync(0xFFFFFFFFu, in && !ok) && lane == 0) set_status(p.status, 2u);
-    have[x] = __ballot_sync(0xFFFFFFFFu, ok);
-    if (lane % 8 == 0 && j < kB)
-      mbar_arrive_expect_tx(bar0 + 8 * (j / 8), 4u * D * __popc((have[x] >> lane) & 0xFFu));
-    __syncwarp();
-    if (ok) bulk_copy_g2s(ring_s + j * 4 * D, p.bounds + (blk * p.H + h) * (2 * D), 4u * D, bar0 + 8 * (j / 8));
-  }
-  uint32_t top[D / 32] = {};  // largest |bound| of the lane's channels, packed
+  __syncthreads();
   bool timed_out = false;
-  for (int i0 = 0; i0 < n; i0 += kScoreQueries) {
-    const int ni = min(kScoreQueries, n - i0);
-    if (i0 > 0) __syncthreads();
-    for (int at = threadIdx.x; at < ni * (D / 8); at += 32 * kScoreWarps) {
-      const int i = at / (D / 8), d = 8 * (at - i * (D / 8));
-      float minus[8], plus[8];
-      sum_heads(p, q0 + i0 + i, h, d, minus, plus);
+  if (warp == kW) {
+    // ---- producer: lanes take a stage's blocks, whose table entries are loaded a stage ahead ----
+    constexpr int kX = kW / 2;  // 16 kW blocks at most
+    const uint32_t bytes = 4u * D * hn;
+    auto entry = [&](int k, int x) -> int32_t {
+      const int j = 32 * x + lane, b = first + k * stage_blocks + j;
+      return j < stage_blocks && b < last ? LDX(p.table + static_cast<int64_t>(s) * p.max_blocks + b) : -1;
+    };
+    int32_t next[kX];
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        coef[i][d + x] = minus[x];
-        coef[i][D + d + x] = plus[x];
+    for (int x = 0; x < kX; ++x) next[x] = entry(0, x);
+    int st = 0, turn = 0;
+    for (int k = 0; k < count; ++k) {
+      int64_t blk[kX];
+      uint32_t ok[kX], sum = 0u;
+#pragma unroll
+      for (int x = 0; x < kX; ++x) {
+        const int j = 32 * x + lane;
+        blk[x] = next[x] >= 0 && next[x] < p.num_blocks ? next[x] : -1;
+        const bool in = j < stage_blocks && first + k * stage_blocks + j < last;
+        if (__any_sync(0xFFFFFFFFu, in && blk[x] < 0) && lane == 0) set_status(p.status, 2u);
+        ok[x] = __ballot_sync(0xFFFFFFFFu, blk[x] >= 0);
+        sum += __popc(ok[x]);
+        next[x] = entry(k + 1, x);
+      }
+      if (k >= plan.stages && !mbar_wait(empty0 + 8 * st, turn ^ 1)) timed_out = true;
+      if (lane == 0) {
+#pragma unroll
+        for (int x = 0; x < kX; ++x) have[st][x] = ok[x];  // published by the arrival
+        mbar_arrive_expect_tx(full0 + 8 * st, bytes * sum);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int x = 0; x < kX; ++x)
+        if (blk[x] >= 0)
+          bulk_copy_g2s(base + st * plan.stage + (32 * x + lane) * plan.row, p.bounds + (blk[x] * p.H + h0) * (2 * D), bytes,
+                        full0 + 8 * st);
+      if (++st == plan.stages) {
+        st = 0;
+        turn ^= 1;
       }
     }
-    __syncthreads();
+    if (__any_sync(0xFFFFFFFFu, timed_out) && lane == 0) set_status(p.status, 16u);
+    return;  // the others' barriers leave this warp out
+  }
+  auto together = [] { asm volatile("bar.sync 1, %0;" ::"n"(32 * kW) : "memory"); };
+  for (int at = threadIdx.x; at < (plan.frag + 4 * D) / 16; at += 32 * kW)
+    reinterpret_cast<uint4*>(frag)[at] = make_uint4(0u, 0u, 0u, 0u);
+  together();
+  for (int at = threadIdx.x; at < n * hn * (D / 8); at += 32 * kW) {
+    const int d = 8 * (at % (D / 8)), ih = at / (D / 8), i = ih / hn, h = ih - i * hn;
+    float v[2][8];  // q-, q+
+    sum_heads(p, q0 + i, h0 + h, d, v[0], v[1]);
+    const int col = three ? 4 * (i % 2) : 2 * (i % 4), group = three ? i / 2 : i / 4;
+    unsigned char* const to = frag + (h * plan.groups + group) * (kSteps * 256);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int k = j * D + d;
+      unsigned char* const at_k = to + (k / 16) * 256 + (k % 16 / 8) * 4;
+#pragma unroll
+      for (int part = 0; part < 3; ++part) {
+        if (part == 2 && !three) break;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t w = pack_bf16x2(v[j][2 * x], v[j][2 * x + 1]);
+          v[j][2 * x] = __fsub_rn(v[j][2 * x], bf16lo(w));
+          v[j][2 * x + 1] = __fsub_rn(v[j][2 * x + 1], bf16hi(w));
+          *reinterpret_cast<uint32_t*>(at_k + ((col + part) * 4 + x) * 8) = w;
+        }
+      }
+    }
+  }
+  together();
+  const int h = warp % plan.hc, part = warp / plan.hc, g = lane >> 2, c = lane & 3;
+  const bool works = h < hn && part < plan.part;
+  const bool two = plan.groups == 2;
+  const uint2* const q_at = reinterpret_cast<const uint2*>(frag + h * plan.groups * (kSteps * 256)) + lane;
+  uint32_t top[kSteps][2] = {};  // largest |bound| of the lane's channels, packed
+  int st = 0, turn = 0;
 #pragma unroll 1
-    for (int g8 = 0; g8 < kGroups; ++g8) {
-      if (b0 + 8 * g8 >= blocks) break;
-      if (i0 == 0 && !mbar_wait(bar0 + 8 * g8, 0)) timed_out = true;
-      const uint32_t here = (have[g8 / 4] >> (8 * (g8 % 4))) & 0xFFu;
-      uint32_t w[8][D / 32];
+  for (int k = 0; k < count; ++k) {
+    if (!mbar_wait(full0 + 8 * st, turn)) timed_out = true;
+    const int b0 = first + k * stage_blocks + 16 * part;
+    if (works && b0 < last) {  // the same in the whole warp
+      const uint32_t here = have[st][part / 2] >> (16 * (part % 2)) & 0xFFFFu;
+      const int r = lane & 15;
+      const uint32_t at = base + (lane >> 4) * 16 +
+                          ((here >> r) & 1u ? st * plan.stage + (16 * part + r) * plan.row + h * 4 * D : off_zero);
+      float acc[2][4] = {};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t* const at = reinterpret_cast<const uint32_t*>(ring + (8 * g8 + j) * 4 * D) + lane * (D / 32);
+      for (int t = 0; t < kSteps; ++t) {
+        uint32_t a[4];
+        ldmatrix_x4(a, at + 32 * t);
 #pragma unroll
-        for (int x = 0; x < D / 32; x += 2) {
-          const uint2 v = *reinterpret_cast<const uint2*>(at + x);
-          const bool ok = (here >> j) & 1u;
-          w[j][x] = ok ? v.x : 0u;
-          w[j][x + 1] = ok ? v.y : 0u;
+        for (int x = 0; x < 4; ++x)
+          asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(top[t][x / 2]) : "r"(top[t][x / 2]), "r"(a[x]));
+        const uint2 b = q_at[t * 32];
+        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        mma_bf16_16816(d, a, b.x, b.y);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[0][e] = __fadd_rn(acc[0][e], d[e]);
+        if (two) {
+          const uint2 b2 = q_at[(kSteps + t) * 32];
+          float d2[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          mma_bf16_16816(d2, a, b2.x, b2.y);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[1][e] = __fadd_rn(acc[1][e], d2[e]);
         }
       }
-      if (i0 == 0) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int x = 0; x < D / 32; ++x)
-            asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(top[x]) : "r"(top[x]), "r"(w[j][x]));
-      }
-      for (int i = 0; i < ni; ++i) {
-        const uint64_t* const c = reinterpret_cast<const uint64_t*>(&coef[i][lane * kC]);
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint64_t acc = 0ull;
-#pragma unroll
-          for (int x = 0; x < D / 32; ++x) acc = fma_f32x2(pack_f32x2(w[j][x] << 16, w[j][x] & 0xFFFF0000u), c[x], acc);
-          uint32_t a, b;
-          unpack_f32x2(acc, a, b);
-          v[j] = __fadd_rn(__uint_as_float(a), __uint_as_float(b));
+      for (int gr = 0; gr < 2; ++gr) {
+        if (gr == 1 && !two) break;
+        float v[2] = {__fadd_rn(acc[gr][0], acc[gr][1]), __fadd_rn(acc[gr][2], acc[gr][3])};  // rows g, g + 8
+        int i = 4 * gr + c;
+        if (three) {
+          v[0] = __fadd_rn(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 1));
+          v[1] = __fadd_rn(v[1], __shfl_xor_sync(0xFFFFFFFFu, v[1], 1));
+          i = c / 2;
         }
+        uint32_t* const to = p.keys + (static_cast<int64_t>(q0 + i) * p.H + h0 + h) * p.pitch + b0 + g;
 #pragma unroll
-        for (int o = 16, m = 4; m >= 1; o >>= 1, m >>= 1) {
-          const bool up = (lane & o) != 0;
-#pragma unroll
-          for (int j = 0; j < m; ++j) {
-            const float give = up ? v[j] : v[j + m], keep = up ? v[j + m] : v[j];
-            v[j] = __fadd_rn(keep, __shfl_xor_sync(0xFFFFFFFFu, give, o));
-          }
-        }
-        v[0] = __fadd_rn(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 2));
-        v[0] = __fadd_rn(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 1));
-        const int j = lane >> 2, b = b0 + 8 * g8 + j;
-        if ((lane & 3) == 0 && b < blocks)
-          STX(p.keys + (static_cast<int64_t>(q0 + i0 + i) * p.H + h) * p.pitch + b,
-              (here >> j) & 1u ? score_key(v[0]) : kKeyBad);
+        for (int e = 0; e < 2; ++e)
+          if (i < n && b0 + g + 8 * e < last && !(three && e != (c & 1)))
+            STX(to + 8 * e, (here >> (g + 8 * e)) & 1u ? score_key(v[e]) : kKeyBad);
       }
     }
-    if (b0 < blocks) {
-      for (int i = 0; i < ni; ++i) {
-        float a = 0.0f;
-#pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-          // 0 only where there is nothing to round: a product that underflows counts 2^-149
-          const float c0 = fabsf(coef[i][lane * kC + 2 * x]), c1 = fabsf(coef[i][lane * kC + 2 * x + 1]);
-          const float t0 = fabsf(bf16lo(top[x])), t1 = fabsf(bf16hi(top[x]));
-          a += c0 * t0 + (c0 > 0.0f && t0 > 0.0f ? 0x1p-149f : 0.0f);
-          a += c1 * t1 + (c1 > 0.0f && t1 > 0.0f ? 0x1p-149f : 0.0f);
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-        if (lane == 0)
-          STX(p.sizes + (static_cast<int64_t>(q0 + i0 + i) * p.H + h) * p.sizes_pitch + b0 / kB, a);
-      }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty0 + 8 * st);
+    if (++st == plan.stages) {
+      st = 0;
+      turn ^= 1;
     }
+  }
+  // ---- sizes: sum_d |q_d| top_d.  Lanes of one c hold the same channels: their maxima, then lane g
+  // adds up query g's.  2^-100 on both sides covers what the tensor cores may take for zero (subnormal
+  // parts); 0 only for a query of zeros.
+  float* const sizes = reinterpret_cast<float*>(smem + off_zero + 4 * D);  // [warp][query]
+  float size = 0.0f;
+  bool none = true;
+  const int col = three ? 4 * (g % 2) : 2 * (g % 4), group = three ? g / 2 : g / 4;
+  const uint2* const mine = reinterpret_cast<const uint2*>(frag + (h * plan.groups + (group < plan.groups ? group : 0)) * (kSteps * 256)) +
+                            col * 4 + c;
+#pragma unroll
+  for (int t = 0; t < kSteps; ++t) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      uint32_t m = top[t][x];
+#pragma unroll
+      for (int o = 4; o <= 16; o <<= 1) {
+        const uint32_t y = __shfl_xor_sync(0xFFFFFFFFu, m, o);
+        asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(y));
+      }
+      const uint32_t w = x == 0 ? mine[t * 32].x : mine[t * 32].y;
+      none = none && (w & 0x7FFF7FFFu) == 0u;
+      size += (fabsf(bf16lo(w)) * 1.01f + 0x1p-100f) * (fabsf(bf16lo(m)) + 0x1p-100f);
+      size += (fabsf(bf16hi(w)) * 1.01f + 0x1p-100f) * (fabsf(bf16hi(m)) + 0x1p-100f);
+    }
+  }
+  if (!works || g >= n) none = true;
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    size += __shfl_xor_sync(0xFFFFFFFFu, size, o);
+    none = __shfl_xor_sync(0xFFFFFFFFu, none ? 1 : 0, o) != 0 && none;
+  }
+  if (c == 0) sizes[warp * kScoreQueries + g] = none ? 0.0f : fmaxf(size, 0x1p-149f);
+  together();
+  for (int at = threadIdx.x; at < n * hn; at += 32 * kW) {
+    const int i = at / hn, hh = at - i * hn;
+    float a = 0.0f;
+    bool nan = false;
+    for (int x = 0; x < plan.part; ++x) {
+      const float y = sizes[(x * plan.hc + hh) * kScoreQueries + i];
+      nan = nan || isnan(y);
+      a = fmaxf(a, y);
+    }
+    STX(p.sizes + (static_cast<int64_t>(q0 + i) * p.H + h0 + hh) * p.sizes_pitch + segment,
+        nan ? __int_as_float(0x7FC00000) : a);
   }
   if (__any_sync(0xFFFFFFFFu, timed_out) && lane == 0) set_status(p.status, 16u);
 }
@@ -248,28 +372,15 @@ struct ScoreTile {
   static constexpr int kStage = kN * kPitch;
   static constexpr int kOffTop = kOffB + 2 * kStage;  // largest |bound| of each channel, f32
   static constexpr int kSmem = kOffTop + 2 * D * 4;
-  static constexpr int kWarps = 8;
+  static constexpr int kWarps = 8;  // and one that copies
 };
 
-__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t at) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(at));
-}
-__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 template <int D>
-__global__ void __launch_bounds__(32 * ScoreTile<D>::kWarps, 1) score_tile_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(32 * (ScoreTile<D>::kWarps + 1), 1) score_tile_kernel(const SelectParams p) {
   using T = ScoreTile<D>;
   constexpr int kMT = T::kM / 32, kNT = T::kN / 32, kThreads = 32 * T::kWarps;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ __align__(8) uint64_t bars[2];
+  __shared__ __align__(8) uint64_t bars[4];  // full and empty, a stage each
   __shared__ uint32_t have[2][T::kN / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int qt = static_cast<int>(blockIdx.x) / p.H, h = static_cast<int>(blockIdx.x) - qt * p.H, s = blockIdx.z;
@@ -279,45 +390,66 @@ __global__ void __launch_bounds__(32 * ScoreTile<D>::kWarps, 1) score_tile_kerne
   const int nq = min(T::kM, n - qt * T::kM), tok0 = q0 + qt * T::kM;
   // blocks that this tile's last query sees
   const int blocks = static_cast<int>(p.div_bs.div(static_cast<uint32_t>(len - n + qt * T::kM + nq - 1))) + 1;
-  const int first = static_cast<int>(blockIdx.y) * p.sizes_step;
-  if (blocks <= p.topk || first >= blocks) return;
-  const int last = min(blocks, first + p.sizes_step), tiles = (last - first + T::kN - 1) / T::kN;
+  const int first = static_cast<int>(blockIdx.y) * p.segment;
+  if (blocks <= p.topk) return;
+  if (first >= blocks) {  // nothing of this segment: nothing to round
+    for (int i = threadIdx.x; i < nq; i += static_cast<int>(blockDim.x))
+      STX(p.sizes + (static_cast<int64_t>(tok0 + i) * p.H + h) * p.sizes_pitch + blockIdx.y, 0.0f);
+    return;
+  }
+  const int last = min(blocks, first + p.segment), tiles = (last - first + T::kN - 1) / T::kN;
   const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-  const uint32_t bar0 = static_cast<uint32_t>(__cvta_generic_to_shared(bars));
+  const uint32_t full0 = static_cast<uint32_t>(__cvta_generic_to_shared(bars)), empty0 = full0 + 16;
   if (threadIdx.x == 0) {
-    mbar_init(bar0, 1);
-    mbar_init(bar0 + 8, 1);
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      mbar_init(full0 + 8 * st, 1);
+      mbar_init(empty0 + 8 * st, T::kWarps);
+    }
     mbar_init_fence();
   }
   __syncthreads();
-  // warp 0: copies of tile t into its stage
-  auto fetch = [&](int t) {
-    const int st = t & 1;
-    int64_t blk[T::kN / 32];
-    uint32_t count = 0u;
-#pragma unroll
-    for (int x = 0; x < T::kN / 32; ++x) {
+  bool timed_out = false;
+  if (warp == T::kWarps) {
+    // ---- producer: a tile's table entries are loaded while the one before it is copied ----
+    constexpr int kX = T::kN / 32;
+    auto entry = [&](int t, int x) -> int32_t {
       const int b = first + t * T::kN + 32 * x + lane;
-      const bool in = b < last;
-      blk[x] = in ? LDX(p.table + static_cast<int64_t>(s) * p.max_blocks + b) : -1;
-      if (blk[x] < 0 || blk[x] >= p.num_blocks) blk[x] = -1;
-      if (__any_sync(0xFFFFFFFFu, in && blk[x] < 0) && lane == 0) set_status(p.status, 2u);
-      const uint32_t ok = __ballot_sync(0xFFFFFFFFu, blk[x] >= 0);
-      if (lane == 0) have[st][x] = ok;
-      count += __popc(ok);
-    }
-    if (lane == 0) mbar_arrive_expect_tx(bar0 + 8 * st, count * 4u * D);
-    __syncwarp();
+      return b < last ? LDX(p.table + static_cast<int64_t>(s) * p.max_blocks + b) : -1;
+    };
+    int32_t next[kX];
 #pragma unroll
-    for (int x = 0; x < T::kN / 32; ++x) {
-      const uint32_t at = base + T::kOffB + st * T::kStage + (32 * x + lane) * T::kPitch;
-      if (blk[x] >= 0) bulk_copy_g2s(at, p.bounds + (blk[x] * p.H + h) * (2 * D), 4u * D, bar0 + 8 * st);
+    for (int x = 0; x < kX; ++x) next[x] = entry(0, x);
+    for (int t = 0; t < tiles; ++t) {
+      const int st = t & 1;
+      int64_t blk[kX];
+      uint32_t ok[kX], count = 0u;
+#pragma unroll
+      for (int x = 0; x < kX; ++x) {
+        blk[x] = next[x] >= 0 && next[x] < p.num_blocks ? next[x] : -1;
+        if (__any_sync(0xFFFFFFFFu, blk[x] < 0 && first + t * T::kN + 32 * x + lane < last) && lane == 0)
+          set_status(p.status, 2u);
+        ok[x] = __ballot_sync(0xFFFFFFFFu, blk[x] >= 0);
+        count += __popc(ok[x]);
+        next[x] = entry(t + 1, x);
+      }
+      if (t >= 2 && !mbar_wait(empty0 + 8 * st, ((t >> 1) - 1) & 1)) timed_out = true;
+      if (lane == 0) {
+#pragma unroll
+        for (int x = 0; x < kX; ++x) have[st][x] = ok[x];  // published by the arrival
+        mbar_arrive_expect_tx(full0 + 8 * st, count * 4u * D);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int x = 0; x < kX; ++x) {
+        const uint32_t at = base + T::kOffB + st * T::kStage + (32 * x + lane) * T::kPitch;
+        if (blk[x] >= 0) bulk_copy_g2s(at, p.bounds + (blk[x] * p.H + h) * (2 * D), 4u * D, full0 + 8 * st);
+      }
     }
-  };
-  if (warp == 0) {
-    fetch(0);
-    if (tiles > 1) fetch(1);
+    if (__any_sync(0xFFFFFFFFu, timed_out) && lane == 0) set_status(p.status, 16u);
+    return;  // the others' barriers leave this warp out
   }
+  auto together = [] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
   for (int at = threadIdx.x; at < T::kM * (D / 8); at += kThreads) {
     const int i = at / (D / 8), d = 8 * (at - i * (D / 8));
     float v[2][8];  // q-, q+
@@ -341,17 +473,16 @@ __global__ void __launch_bounds__(32 * ScoreTile<D>::kWarps, 1) score_tile_kerne
       *reinterpret_cast<uint4*>(row + T::kOffLo) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
   }
-  __syncthreads();
+  together();
 
   const int m0 = (warp & 1) * (T::kM / 2), n0 = (warp >> 1) * (T::kN / 4);
   const uint32_t a_at = base + (m0 + (lane & 15)) * T::kPitch + (lane >> 4) * 16;
   const uint32_t b_row = (n0 + (lane & 7) + ((lane >> 4) << 3)) * T::kPitch + ((lane >> 3) & 1) * 16;
   uint32_t top[2 * D / kThreads > 0 ? 2 * D / kThreads : 1] = {};
   constexpr int kWords = D;  // of a row
-  bool timed_out = false;
   for (int t = 0; t < tiles; ++t) {
     const int st = t & 1;
-    if (!mbar_wait(bar0 + 8 * st, (t >> 1) & 1)) timed_out = true;
+    if (!mbar_wait(full0 + 8 * st, (t >> 1) & 1)) timed_out = true;
     const unsigned char* const tile = smem + T::kOffB + st * T::kStage;
     // rows without bounds: zeros, which no copy writes
     uint32_t gaps = 0u;
@@ -364,7 +495,7 @@ __global__ void __launch_bounds__(32 * ScoreTile<D>::kWarps, 1) score_tile_kerne
           *reinterpret_cast<uint4*>(smem + T::kOffB + st * T::kStage + r * T::kPitch + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // copies land here later
-      __syncthreads();
+      together();
     }
     float acc[kMT][kNT][4];
 #pragma unroll
@@ -382,16 +513,24 @@ __global__ void __launch_bounds__(32 * ScoreTile<D>::kWarps, 1) score_tile_kerne
       }
 #pragma unroll
       for (int b = 0; b < kNT / 2; ++b) ldmatrix_x4(bb[b], b_at + b * 16 * T::kPitch + 32 * k);
+      float step[kMT][kNT][4];  // chains of two, as many at a time as there are
 #pragma unroll
       for (int a = 0; a < kMT; ++a)
 #pragma unroll
         for (int b = 0; b < kNT; ++b) {
-          float step[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          mma_bf16_16816(step, lo[a], bb[b / 2][2 * (b % 2)], bb[b / 2][2 * (b % 2) + 1]);
-          mma_bf16_16816(step, hi[a], bb[b / 2][2 * (b % 2)], bb[b / 2][2 * (b % 2) + 1]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[a][b][e] = __fadd_rn(acc[a][b][e], step[e]);
+          step[a][b][0] = step[a][b][1] = step[a][b][2] = step[a][b][3] = 0.0f;
+          mma_bf16_16816(step[a][b], lo[a], bb[b / 2][2 * (b % 2)], bb[b / 2][2 * (b % 2) + 1]);
         }
+#pragma unroll
+      for (int a = 0; a < kMT; ++a)
+#pragma unroll
+        for (int b = 0; b < kNT; ++b) mma_bf16_16816(step[a][b], hi[a], bb[b / 2][2 * (b % 2)], bb[b / 2][2 * (b % 2) + 1]);
+#pragma unroll
+      for (int a = 0; a < kMT; ++a)
+#pragma unroll
+        for (int b = 0; b < kNT; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[a][b][e] = __fadd_rn(acc[a][b][e], step[a][b][e]);
     }
     // largest |bound| of each channel: thread x has words x, x + kThreads
 #pragma unroll
@@ -419,8 +558,8 @@ __global__ void __launch_bounds__(32 * ScoreTile<D>::kWarps, 1) score_tile_kerne
                                      ok & 2u ? score_key(acc[a][b][2 * e + 1]) : kKeyBad);
           STX(reinterpret_cast<uint2*>(to), v);  // pitch is even: the pair lies in the row
         }
-    __syncthreads();  // the stage is free
-    if (warp == 0 && t + 2 < tiles) fetch(t + 2);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty0 + 8 * st);  // this warp has read the stage, and its notes
   }
   // ---- sizes: sum_d |q_d| top_d; what the tensor cores may take for zero (subnormal parts) is
   // covered by 2^-100 on both sides ----
@@ -436,7 +575,7 @@ __global__ void __launch_bounds__(32 * ScoreTile<D>::kWarps, 1) score_tile_kerne
         tops[2 * word + 1] = share == 0 ? b : fmaxf(tops[2 * word + 1], b);
       }
     }
-    __syncthreads();
+    together();
   }
   for (int i = warp; i < nq; i += T::kWarps) {
     float size = 0.0f;
@@ -487,6 +626,13 @@ struct RowReduce {
   __device__ __forceinline__ uint32_t min(uint32_t v) {
     return run(v, [](uint32_t x) { return __reduce_min_sync(0xFFFFFFFFu, x); }, 0xFFFFFFFFu);
   }
+  __device__ __forceinline__ void sync() {
+    if constexpr (kThreads == 32) {
+      __syncwarp();
+    } else {
+      __syncthreads();
+    }
+  }
   // Sum over the threads before this one.
   __device__ __forceinline__ uint32_t before(uint32_t v) {
     constexpr int kWarps = kThreads / 32;
@@ -507,6 +653,13 @@ struct RowReduce {
       return upto - v + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? at[lane] : 0u);
     }
   }
+};
+
+// Blocks to score again, where they are few.
+constexpr uint32_t kFewTies = 32u;
+struct FewTies {
+  uint64_t score[kFewTies];
+  int32_t block[kFewTies];
 };
 
 // The border of the k highest keys: at least k keys are >= hi, fewer are above it; lo is the
@@ -566,7 +719,9 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) select_kernel
   const int64_t at_row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kThreads;  // i H + h
   const int i = static_cast<int>(at_row / p.H), h = static_cast<int>(at_row - static_cast<int64_t>(i) * p.H), s = blockIdx.y;
   __shared__ uint32_t slots[2][32];
+  __shared__ FewTies ties_of[kRows];
   RowReduce<kThreads> red{slots, 0};
+  FewTies& few = ties_of[threadIdx.x / kThreads];
   int q0, n, len;
   const bool ok = select_range(p, s, q0, n, len);
   if (!ok && threadIdx.x == 0 && blockIdx.x == 0) set_status(p.status, 8u);
@@ -596,7 +751,7 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) select_kernel
   // the error bound of the scores
   float size = 0.0f;
   bool bounded = true;
-  for (int at = lane; at * p.sizes_step < vis; at += 32) {
+  for (int at = lane; at < p.sizes_n; at += 32) {
     const float x = LDX(p.sizes + row * p.sizes_pitch + at);
     bounded = bounded && x <= 1e38f;  // not: sums that may overflow, NaN
     size = fmaxf(size, x);
@@ -610,6 +765,7 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) select_kernel
 
   uint32_t listed = 0u;  // bits of this thread's blocks
   if (k > 0u) {
+    bool done = false;
     Border at = find_border<kThreads, P>(key, k, red);
     const bool scored = at.hi > kKeyNan;  // not: blocks without a score fill the list
     const float hi = key_score(at.hi), lo = at.lo > kKeyNan ? key_score(at.lo) : -__int_as_float(0x7F800000);
@@ -627,80 +783,120 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) select_kernel
           again |= 1u << j;
         }
       }
-      // the lane's channels of q+ or q-, in binary64
+      // the lane's channels of q+ or q-, in binary64 (a warp's 32 x D / 16 x heads additions take
+      // D heads cycles of this GPU's binary64 unit)
       double qd[kC];
+      auto load_q = [&]() {
 #pragma unroll
-      for (int x = 0; x < kC; ++x) qd[x] = 0.0;
-#pragma unroll 1
-      for (int j = 0; j < p.group; ++j) {
-        uint32_t w[D / 32];
-        load_bounds<D>(p.q + (q0 + i) * p.q_row_pitch + (static_cast<int64_t>(h) * p.group + j) * p.q_head_pitch +
-                           (lane % 16) * kC, w);
-#pragma unroll
-        for (int x = 0; x < kC; ++x) {
-          const float v = x % 2 == 0 ? bf16lo(w[x / 2]) : bf16hi(w[x / 2]);
-          qd[x] += (lane < 16 ? !(v > 0.0f) : v > 0.0f) ? static_cast<double>(v) : 0.0;
-        }
-      }
-#pragma unroll 1
-      for (int stage = 0; stage < 2; ++stage) {
-        uint32_t left = again;
-        while (true) {
-          const uint32_t who = __ballot_sync(0xFFFFFFFFu, left != 0u);
-          if (who == 0u) break;
-          const int src = __ffs(who) - 1;
-          const int j = __shfl_sync(0xFFFFFFFFu, __ffs(left) - 1, src);
-          const int b = (warp * 32 + src) * P + j;
-          // one that has a score lies in the pool
-          const int64_t blk = LDX(p.table + static_cast<int64_t>(s) * p.max_blocks + b);
+        for (int x = 0; x < kC; ++x) qd[x] = 0.0;
+#pragma unroll 4
+        for (int j = 0; j < p.group; ++j) {
           uint32_t w[D / 32];
-          load_bounds<D>(p.bounds + (blk * p.H + h) * (2 * D) + lane * kC, w);
-          double sum = 0.0;
+          load_bounds<D>(p.q + (q0 + i) * p.q_row_pitch + (static_cast<int64_t>(h) * p.group + j) * p.q_head_pitch +
+                             (lane % 16) * kC, w);
 #pragma unroll
-          for (int x = 0; x < D / 32; ++x) {
-            sum = fma(qd[2 * x], static_cast<double>(bf16lo(w[x])), sum);
-            sum = fma(qd[2 * x + 1], static_cast<double>(bf16hi(w[x])), sum);
-          }
-#pragma unroll
-          for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-          uint64_t u = static_cast<uint64_t>(__double_as_longlong(sum + 0.0));
-          u = (u >> 63) != 0ull ? ~u : u | 0x8000000000000000ull;
-          const uint32_t bits = static_cast<uint32_t>(stage == 0 ? u >> 33 : (u >> 2) & 0x7FFFFFFFull);
-          const uint32_t fresh = isnan(sum) ? kKeyNan64 : kKeyNan64 + 1u + bits;
-          if (lane == src) {
-            left &= left - 1u;
-#pragma unroll
-            for (int x = 0; x < P; ++x)
-              if (x == j) key[x] = fresh;
+          for (int x = 0; x < kC; ++x) {
+            const uint32_t v = x % 2 == 0 ? w[x / 2] << 16 : w[x / 2] & 0xFFFF0000u;
+            qd[x] += (lane < 16) != (__uint_as_float(v) > 0.0f) ? wide(v) : 0.0;
           }
         }
-        at = find_border<kThreads, P>(key, k, red);
-        if (at.count == k || stage == 1 || at.hi <= kKeyNan64) break;
-        again = 0u;
+      };
+      // the exact score of a block that has one (it lies in the pool), as an ordered integer above 0;
+      // NaN: 0
+      auto score64 = [&](int b) -> uint64_t {
+        const int64_t blk = LDX(p.table + static_cast<int64_t>(s) * p.max_blocks + b);
+        uint32_t w[D / 32];
+        load_bounds<D>(p.bounds + (blk * p.H + h) * (2 * D) + lane * kC, w);
+        double sum = 0.0;
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-          if (key[j] == at.hi) {
-            again |= 1u << j;
-          } else {
-            key[j] = key[j] > at.hi ? kKeyListed : 0u;
+        for (int x = 0; x < D / 32; ++x) {
+          sum = fma(qd[2 * x], wide(w[x] << 16), sum);
+          sum = fma(qd[2 * x + 1], wide(w[x] & 0xFFFF0000u), sum);
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        const uint64_t u = static_cast<uint64_t>(__double_as_longlong(sum + 0.0));
+        return isnan(sum) ? 0ull : (u >> 63) != 0ull ? ~u : u | 0x8000000000000000ull;
+      };
+      uint32_t certain = 0u;
+#pragma unroll
+      for (int j = 0; j < P; ++j) certain += key[j] == kKeyListed ? 1u : 0u;
+      const uint32_t m = red.sum(__popc(again)), need = k - red.sum(certain);
+      if (m <= kFewTies && m >= need) {
+        // few: their scores to shared memory, a warp one at a time, and each one's rank among them
+        const uint32_t place = red.before(__popc(again));
+        uint32_t left = again;
+        for (uint32_t x = place; left != 0u; left &= left - 1u, ++x) few.block[x] = b0 + __ffs(left) - 1;
+        red.sync();
+        if (warp < static_cast<int>(m)) load_q();
+        for (uint32_t x = warp; x < m; x += kThreads / 32) {
+          const uint64_t u = score64(few.block[x]);
+          if (lane == 0) few.score[x] = u;
+        }
+        red.sync();
+        left = again;
+        for (uint32_t x = place; left != 0u; left &= left - 1u, ++x) {
+          const uint64_t mine = few.score[x];
+          uint32_t rank = 0u;
+          for (uint32_t y = 0; y < m; ++y) {  // the list is in the order of the blocks
+            const uint64_t other = few.score[y];
+            rank += other > mine || (other == mine && y < x) ? 1u : 0u;
+          }
+          if (rank < need) listed |= left & (0u - left);
+        }
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+          if (key[j] == kKeyListed) listed |= 1u << j;
+        done = true;
+      } else {
+        load_q();
+#pragma unroll 1
+        for (int stage = 0; stage < 2; ++stage) {
+          uint32_t left = again;
+          while (true) {
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, left != 0u);
+            if (who == 0u) break;
+            const int src = __ffs(who) - 1;
+            const int j = __shfl_sync(0xFFFFFFFFu, __ffs(left) - 1, src);
+            const uint64_t u = score64((warp * 32 + src) * P + j);
+            const uint32_t bits = static_cast<uint32_t>(stage == 0 ? u >> 33 : (u >> 2) & 0x7FFFFFFFull);
+            const uint32_t fresh = u == 0ull ? kKeyNan64 : kKeyNan64 + 1u + bits;
+            if (lane == src) {
+              left &= left - 1u;
+#pragma unroll
+              for (int x = 0; x < P; ++x)
+                if (x == j) key[x] = fresh;
+            }
+          }
+          at = find_border<kThreads, P>(key, k, red);
+          if (at.count == k || stage == 1 || at.hi <= kKeyNan64) break;
+          again = 0u;
+#pragma unroll
+          for (int j = 0; j < P; ++j) {
+            if (key[j] == at.hi) {
+              again |= 1u << j;
+            } else {
+              key[j] = key[j] > at.hi ? kKeyListed : 0u;
+            }
           }
         }
       }
     }
-    // the keys above the border, and of those on it the first
-    uint32_t ties = 0u;
+    if (!done) {  // the keys above the border, and of those on it the first
+      uint32_t ties = 0u;
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-      if (key[j] > at.hi) listed |= 1u << j;
-      if (key[j] == at.hi) ties |= 1u << j;
-    }
-    if (at.count > k) {  // uniform
-      const uint32_t need = k - red.sum(__popc(listed));
-      uint32_t before = red.before(__popc(ties));
-      for (; ties != 0u; ties &= ties - 1u, ++before)
-        if (before < need) listed |= ties & (0u - ties);
-    } else {
-      listed |= ties;
+      for (int j = 0; j < P; ++j) {
+        if (key[j] > at.hi) listed |= 1u << j;
+        if (key[j] == at.hi) ties |= 1u << j;
+      }
+      if (at.count > k) {  // uniform
+        const uint32_t need = k - red.sum(__popc(listed));
+        uint32_t before = red.before(__popc(ties));
+        for (; ties != 0u; ties &= ties - 1u, ++before)
+          if (before < need) listed |= ties & (0u - ties);
+      } else {
+        listed |= ties;
+      }
     }
   }
 #pragma unroll
@@ -730,31 +926,36 @@ template <int D>
 cudaError_t score_launch(SelectParams& p, cudaStream_t s) {
   cudaError_t e;
   if (p.max_q < kTileQueries) {
-    constexpr int kSmem = kScoreWarps * kScoreBytes, kB = kScoreBlocks<D>;
-    p.sizes_step = kB;
-    // roundings on a product's way into a score, of 2^-24 each: the sum over the heads, a chain of
-    // D / 32 products, the two chains' sum and 5 steps over the lanes; a fiftieth for those of
-    // the bound itself and of the comparisons with it
-    p.err = 1.02f * static_cast<float>(p.group + D / 32 + 8) * 0x1p-24f;
-    e = cudaFuncSetAttribute(score_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const ScorePlan plan(p.H, D, p.max_q);
+    // segments of each sequence that fill the GPU once, of 16 blocks at least
+    const int heads = (p.H + plan.hc - 1) / plan.hc;
+    const int64_t rows = static_cast<int64_t>(p.S) * heads;
+    const int64_t segments = std::max(int64_t{1}, std::min(num_sms() / rows, static_cast<int64_t>(p.most) / 16));
+    p.sizes_n = static_cast<int>(segments);
+    // in units of 2^-23: 16 additions a step of 16 channels, which the tensor cores may round towards
+    // zero, half a unit for each step's sum, one for each part's and half for each head's; two parts: as
+    // much as 2^-18 for what they leave of q
+    p.err = 1.02f * static_cast<float>(16 + D / 16 + 4 + p.group + (p.max_q <= 2 ? 0 : 33)) * 0x1p-23f;
+    e = cudaFuncSetAttribute(score_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 512);
     if (e != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>((p.most + kScoreWarps * kB - 1) / (kScoreWarps * kB)), p.H, p.S);
-    KVQ_LAUNCH("score_kernel", s, score_kernel<D><<<grid, 32 * kScoreWarps, kSmem, s>>>(p); e = cudaGetLastError());
+    const dim3 grid(static_cast<unsigned>(segments), heads, p.S);
+    KVQ_LAUNCH("score_kernel", s, score_kernel<D><<<grid, 32 * (kScoreWarps<D> + 1), plan.smem, s>>>(p); e = cudaGetLastError());
     return e;
   }
   using T = ScoreTile<D>;
   // segments of whole tiles, as many as fill the GPU once
   const int64_t rows = static_cast<int64_t>((p.max_q + T::kM - 1) / T::kM) * p.H, tiles = (p.most + T::kN - 1) / T::kN;
   const int64_t segments = std::max(int64_t{1}, std::min(tiles, num_sms() / (rows * p.S)));
-  p.sizes_step = static_cast<int>((tiles + segments - 1) / segments) * T::kN;
+  p.segment = static_cast<int>((tiles + segments - 1) / segments) * T::kN;
+  p.sizes_n = (p.most + p.segment - 1) / p.segment;
   // in units of 2^-23: 32 additions a step of 16 channels (hi and lo), which the tensor cores may round
   // towards zero, the same again for what hi + lo leaves of q (2^-18), half a unit for each step's sum
   // and for each head's
   p.err = 1.02f * static_cast<float>(64 + D / 16 + p.group) * 0x1p-23f;
   e = cudaFuncSetAttribute(score_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>((p.most + p.sizes_step - 1) / p.sizes_step), p.S);
-  KVQ_LAUNCH("score_tile_kernel", s, score_tile_kernel<D><<<grid, 32 * T::kWarps, T::kSmem, s>>>(p); e = cudaGetLastError());
+  const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>(p.sizes_n), p.S);
+  KVQ_LAUNCH("score_tile_kernel", s, score_tile_kernel<D><<<grid, 32 * (T::kWarps + 1), T::kSmem, s>>>(p); e = cudaGetLastError());
   return e;
 }
 
@@ -776,7 +977,7 @@ cudaError_t select_dim(SelectParams& p, cudaStream_t s) {
 }
 
 int32_t key_pitch(int32_t most) { return (most + 31) / 32 * 32; }
-int32_t sizes_pitch(int32_t most) { return (most + 15) / 16; }  // the smallest step
+int32_t sizes_pitch(int32_t most) { return (most + 15) / 16; }  // parts of 16 blocks or more
 
 }  // namespace
 
