@@ -11,10 +11,11 @@
 // The list is that of the exact scores.  The score kernels work in binary32; their roundings stay
 // within e = err * a, a = sum_d (|q+_d| max |hi_d| + |q-_d| max |lo_d|) (err counts them; the maxima
 // are over the row's blocks).  A score above the best unlisted one by more than 2 e is listed for
-// certain, one below the lowest listed one by as much is not; what lies between is scored again in
-// binary64, by one warp a block, and ranked by the upper and then the lower bits of that.  One row in
-// fifty has such blocks; exact ties go the same way to the index.  What binary32 cannot bound (sums that
-// may overflow) all goes to binary64.
+// certain, one below the lowest listed one by as much is not; what lies between is scored again, by
+// one warp a block: a few blocks in pairs of binary32 numbers (one row in eight has two or three; on this
+// GPU binary64 runs at two operations a cycle and SM, and took 6 us of such a call), more than 32, or what
+// binary32 cannot bound (sums that may overflow), in binary64 and ranked by the upper and then the lower
+// bits of that.  Exact ties go the same way to the index.
 //
 // Both score kernels take the dot products on the tensor cores, q split into bf16 parts: with the blocks
 // as rows and the parts as columns for few queries a sequence (score_kernel; bound: HBM), by tiles of 64
@@ -667,8 +668,22 @@ struct FewTies {
 struct Border {
   uint32_t hi, lo, count;
 };
+// By histograms of the keys' range, each of the part that holds the k-th key, until that has at most 32
+// keys (or one value), which a warp ranks.  Keys that are scores spread well: one histogram does for
+// nearly all rows.  (A search by halves took 16 counts over the thread block, 7500 cycles for 2048 keys.)
+template <int kThreads>
+struct RowHistogram {
+  static constexpr int kBins = kThreads == 32 ? 256 : 1024, kEach = kBins / kThreads;
+  uint32_t bin[kBins];  // from the highest keys down
+  uint32_t list[32];
+  uint32_t listed;
+  uint32_t found[3];  // bin, keys above it, keys in it
+};
 template <int kThreads, int P>
-__device__ __forceinline__ Border find_border(const uint32_t (&key)[P], uint32_t k, RowReduce<kThreads>& red) {
+__device__ __forceinline__ Border find_border(const uint32_t (&key)[P], uint32_t k, RowReduce<kThreads>& red,
+                                              RowHistogram<kThreads>& hist) {
+  using Hist = RowHistogram<kThreads>;
+  const int lane = threadIdx.x & 31, me = threadIdx.x % kThreads;
   uint32_t least = 0xFFFFFFFFu, most = 0u;
 #pragma unroll
   for (int j = 0; j < P; ++j) {
@@ -676,40 +691,82 @@ __device__ __forceinline__ Border find_border(const uint32_t (&key)[P], uint32_t
     least = min(least, key[j]);
     most = max(most, key[j]);
   }
-  // count(>= from) >= k > count(>= to)
-  uint32_t from = red.min(least), to = red.max(most) + 1u;
-  uint32_t at = from, count = 0u;
-  while (to - from > 1u) {
-    const uint32_t mid = from + (to - from) / 2u;
-    uint32_t c = 0u;
+  uint32_t from = red.min(least), to = red.max(most);  // the k-th key lies in from .. to
+  uint32_t above = 0u, inside = 0u;
+  while (true) {
+    const int shift = max(0, 32 - __clz(to - from) - (kThreads == 32 ? 8 : 10));
 #pragma unroll
-    for (int j = 0; j < P; ++j) c += key[j] >= mid ? 1u : 0u;
-    c = red.sum(c);
-    if (c >= k) from = mid;
-    if (c < k) to = mid;
-    if (c == k) break;
-  }
-  at = from;
-  uint32_t hi = 0xFFFFFFFFu, lo = 0u, c = 0u;
+    for (int x = 0; x < Hist::kEach; ++x) hist.bin[me + x * kThreads] = 0u;
+    if (me == 0) hist.listed = 0u;
+    red.sync();
 #pragma unroll
-  for (int j = 0; j < P; ++j) {
-    if (key[j] >= at) {
-      hi = min(hi, key[j]);
-      ++c;
-    } else {
-      lo = max(lo, key[j]);
+    for (int j = 0; j < P; ++j)
+      if (key[j] >= from && key[j] <= to && key[j] != 0u) atomicAdd(&hist.bin[Hist::kBins - 1 - ((key[j] - from) >> shift)], 1u);
+    red.sync();
+    uint32_t each[Hist::kEach], sum = 0u;
+#pragma unroll
+    for (int x = 0; x < Hist::kEach; ++x) sum += each[x] = hist.bin[me * Hist::kEach + x];
+    uint32_t upto = above + red.before(sum);
+    if (upto < k && upto + sum >= k) {
+#pragma unroll
+      for (int x = 0; x < Hist::kEach; ++x) {
+        if (upto < k && upto + each[x] >= k) {
+          hist.found[0] = Hist::kBins - 1 - (me * Hist::kEach + x);
+          hist.found[1] = upto;
+          hist.found[2] = each[x];
+        }
+        upto += each[x];
+      }
     }
+    red.sync();
+    const uint32_t low = from + (hist.found[0] << shift);
+    to = shift == 0 ? low : min(to, low + ((1u << shift) - 1u));
+    from = low;
+    above = hist.found[1];
+    inside = hist.found[2];
+    if (inside <= 32u || from == to) break;
+    red.sync();  // found is read before it is written again
   }
-  count = red.sum(c);
-  hi = red.min(hi);
-  lo = red.max(lo);
-  return Border{hi, count > k ? hi : lo, count};
+  Border at{from, from, above + inside};
+  if (from != to) {
+#pragma unroll
+    for (int j = 0; j < P; ++j)
+      if (key[j] >= from && key[j] <= to) hist.list[atomicAdd(&hist.listed, 1u)] = key[j];
+    red.sync();
+    const uint32_t mine = lane < static_cast<int>(inside) ? hist.list[lane] : 0u;
+    uint32_t greater = 0u, equal = 0u;
+    for (uint32_t x = 0; x < inside; ++x) {
+      const uint32_t other = hist.list[x];
+      greater += other > mine ? 1u : 0u;
+      equal += other == mine ? 1u : 0u;
+    }
+    greater += above;
+    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, lane < static_cast<int>(inside) && greater < k && greater + equal >= k);
+    const int src = __ffs(hit) - 1;
+    at.hi = __shfl_sync(0xFFFFFFFFu, mine, src);
+    at.count = __shfl_sync(0xFFFFFFFFu, greater + equal, src);
+  }
+  at.lo = at.hi;
+  if (at.count == k) {
+    uint32_t lo = 0u;
+#pragma unroll
+    for (int j = 0; j < P; ++j)
+      if (key[j] < at.hi) lo = max(lo, key[j]);
+    at.lo = red.max(lo);
+  }
+  return at;
+}
+
+// s + e = a + b exactly (Knuth's sum of two).
+__device__ __forceinline__ float two_sum(float a, float b, float& e) {
+  const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
+  e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
+  return s;
 }
 
 // The list of one (query token, KV head): of the row's kThreads threads, t holds the keys of P
-// blocks from t P on; a thread block has 128 / kThreads rows, or one.  A search by halves over the
-// keys' range finds the border (it ends as soon as a bound parts k keys from the rest).  Bound: latency
-// of some 15 counts over the row's threads where there are few rows, else their issue.
+// blocks from t P on; a thread block has 128 / kThreads rows, or one.  Bound: latency of a dozen
+// barriers and exchanges between the row's threads.
 template <int D, int kThreads, int P>
 __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) select_kernel(const SelectParams p) {
   constexpr int kC = D / 16, kRows = kThreads < 128 ? 128 / kThreads : 1;
@@ -720,8 +777,10 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) select_kernel
   const int i = static_cast<int>(at_row / p.H), h = static_cast<int>(at_row - static_cast<int64_t>(i) * p.H), s = blockIdx.y;
   __shared__ uint32_t slots[2][32];
   __shared__ FewTies ties_of[kRows];
+  __shared__ RowHistogram<kThreads> hists[kRows];
   RowReduce<kThreads> red{slots, 0};
   FewTies& few = ties_of[threadIdx.x / kThreads];
+  RowHistogram<kThreads>& hist = hists[threadIdx.x / kThreads];
   int q0, n, len;
   const bool ok = select_range(p, s, q0, n, len);
   if (!ok && threadIdx.x == 0 && blockIdx.x == 0) set_status(p.status, 8u);
@@ -766,7 +825,7 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) select_kernel
   uint32_t listed = 0u;  // bits of this thread's blocks
   if (k > 0u) {
     bool done = false;
-    Border at = find_border<kThreads, P>(key, k, red);
+    Border at = find_border<kThreads, P>(key, k, red, hist);
     const bool scored = at.hi > kKeyNan;  // not: blocks without a score fill the list
     const float hi = key_score(at.hi), lo = at.lo > kKeyNan ? key_score(at.lo) : -__int_as_float(0x7F800000);
     if (!bounded || (scored && e > 0.0f && !(hi - lo > 2.0f * e))) {
@@ -822,16 +881,55 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) select_kernel
 #pragma unroll
       for (int j = 0; j < P; ++j) certain += key[j] == kKeyListed ? 1u : 0u;
       const uint32_t m = red.sum(__popc(again)), need = k - red.sum(certain);
-      if (m <= kFewTies && m >= need) {
-        // few: their scores to shared memory, a warp one at a time, and each one's rank among them
+      if (m <= kFewTies && m >= need && size > 0x1p-60f && size < 0x1p100f) {
+        // few, and nothing that overflows or underflows: their scores in pairs of binary32 numbers (48
+        // bits), a warp one at a time, and each one's rank among them
         const uint32_t place = red.before(__popc(again));
         uint32_t left = again;
         for (uint32_t x = place; left != 0u; left &= left - 1u, ++x) few.block[x] = b0 + __ffs(left) - 1;
         red.sync();
-        if (warp < static_cast<int>(m)) load_q();
-        for (uint32_t x = warp; x < m; x += kThreads / 32) {
-          const uint64_t u = score64(few.block[x]);
-          if (lane == 0) few.score[x] = u;
+        if (warp < static_cast<int>(m)) {
+          float qh[kC], ql[kC];
+#pragma unroll
+          for (int x = 0; x < kC; ++x) qh[x] = ql[x] = 0.0f;
+#pragma unroll 4
+          for (int j = 0; j < p.group; ++j) {
+            uint32_t w[D / 32];
+            load_bounds<D>(p.q + (q0 + i) * p.q_row_pitch + (static_cast<int64_t>(h) * p.group + j) * p.q_head_pitch +
+                               (lane % 16) * kC, w);
+#pragma unroll
+            for (int x = 0; x < kC; ++x) {
+              const float v = x % 2 == 0 ? bf16lo(w[x / 2]) : bf16hi(w[x / 2]);
+              float e2;
+              qh[x] = two_sum(qh[x], (lane < 16) != (v > 0.0f) ? v : 0.0f, e2);
+              ql[x] = __fadd_rn(ql[x], e2);
+            }
+          }
+          for (uint32_t y = warp; y < m; y += kThreads / 32) {
+            const int64_t blk = LDX(p.table + static_cast<int64_t>(s) * p.max_blocks + few.block[y]);
+            uint32_t w[D / 32];
+            load_bounds<D>(p.bounds + (blk * p.H + h) * (2 * D) + lane * kC, w);
+            float sum = 0.0f, rest = 0.0f;
+#pragma unroll
+            for (int x = 0; x < kC; ++x) {
+              const float v = x % 2 == 0 ? bf16lo(w[x / 2]) : bf16hi(w[x / 2]);
+              const float t = __fmul_rn(qh[x], v), low = __fmaf_rn(qh[x], v, -t);
+              float e2;
+              sum = two_sum(sum, t, e2);
+              rest = __fadd_rn(rest, __fadd_rn(e2, __fmaf_rn(ql[x], v, low)));
+            }
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) {
+              float e2;
+              const float rest2 = __shfl_xor_sync(0xFFFFFFFFu, rest, o);
+              sum = two_sum(sum, __shfl_xor_sync(0xFFFFFFFFu, sum, o), e2);
+              rest = __fadd_rn(__fadd_rn(rest, rest2), e2);
+            }
+            float tail2;
+            sum = two_sum(sum, rest, tail2);
+            if (lane == 0)
+              few.score[y] = isnan(sum) ? 0ull : static_cast<uint64_t>(score_key(sum)) << 32 | score_key(tail2);
+          }
         }
         red.sync();
         left = again;
@@ -868,7 +966,7 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) select_kernel
                 if (x == j) key[x] = fresh;
             }
           }
-          at = find_border<kThreads, P>(key, k, red);
+          at = find_border<kThreads, P>(key, k, red, hist);
           if (at.count == k || stage == 1 || at.hi <= kKeyNan64) break;
           again = 0u;
 #pragma unroll
