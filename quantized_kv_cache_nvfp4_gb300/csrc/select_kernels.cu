@@ -43,14 +43,6 @@ __device__ __forceinline__ float key_score(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) != 0u ? k & 0x7FFFFFFFu : ~k);
 }
 
-// A bf16 (the upper half of u) in binary64, by its bits: conversions run at the rate of the
-// binary64 unit, two a cycle and SM.
-__device__ __forceinline__ double wide(uint32_t u) {
-  const uint32_t e = (u >> 23) & 0xFFu;
-  if (e == 0u || e == 0xFFu) return static_cast<double>(__uint_as_float(u));  // zeros, subnormal numbers, infinities, NaN
-  return __hiloint2double(static_cast<int>((u & 0x80000000u) | (((u & 0x7FFFFFFFu) >> 3) + (896u << 20))), 0);
-}
-
 constexpr int kScoreQueries = 8;  // of a sequence, at most; more go to the tile kernel
 constexpr int kTileQueries = kScoreQueries + 1;
 
@@ -86,22 +78,6 @@ __device__ __forceinline__ bool select_range(const SelectParams& p, int s, int& 
     return false;
   n = q1 - q0;
   return true;
-}
-
-// The lane's part of a block's bounds, 2 D bf16 over the warp: D / 16 of them, D / 32 words.
-template <int D>
-__device__ __forceinline__ void load_bounds(const uint16_t* at, uint32_t (&w)[D / 32]) {
-  if constexpr (D == 64) {
-    load8B(at, w[0], w[1]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < D / 128; ++i) {
-      uint32_t v[4];
-      load16B(at + 8 * i, v);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[4 * i + j] = v[j];
-    }
-  }
 }
 
 // Sums over the heads of one token's q- and q+ at channels d .. d + 7.
@@ -597,36 +573,25 @@ __global__ void __launch_bounds__(32 * (ScoreTile<D>::kWarps + 1), 1) score_tile
   if (__any_sync(0xFFFFFFFFu, timed_out) && lane == 0) set_status(p.status, 16u);
 }
 
-// Sums, maxima or minima over the threads of a row, the same in all of them.  A row of one warp needs
-// no barrier; wider ones need one each (the slots alternate).
+// What the threads of one list share.  A list of one warp needs no barrier.
+constexpr uint32_t kFewTies = 32u;  // blocks to score again, where they are few
 template <int kThreads>
-struct RowReduce {
-  uint32_t (*slot)[32];
-  int turn;
-  template <typename F>
-  __device__ __forceinline__ uint32_t run(uint32_t v, F warp_reduce, uint32_t none) {
-    constexpr int kWarps = kThreads / 32;
-    v = warp_reduce(v);
-    if constexpr (kWarps == 1) {
-      return v;
-    } else {
-      uint32_t* const at = slot[turn];
-      turn ^= 1;
-      if ((threadIdx.x & 31) == 0) at[threadIdx.x >> 5] = v;
-      __syncthreads();
-      const int lane = threadIdx.x & 31;
-      return warp_reduce(lane < kWarps ? at[lane] : none);
-    }
-  }
-  __device__ __forceinline__ uint32_t sum(uint32_t v) {
-    return run(v, [](uint32_t x) { return __reduce_add_sync(0xFFFFFFFFu, x); }, 0u);
-  }
-  __device__ __forceinline__ uint32_t max(uint32_t v) {
-    return run(v, [](uint32_t x) { return __reduce_max_sync(0xFFFFFFFFu, x); }, 0u);
-  }
-  __device__ __forceinline__ uint32_t min(uint32_t v) {
-    return run(v, [](uint32_t x) { return __reduce_min_sync(0xFFFFFFFFu, x); }, 0xFFFFFFFFu);
-  }
+struct ListShared {
+  static constexpr int kBins = kThreads == 32 ? 256 : 1024;
+  uint32_t slot[2][64];
+  uint32_t bin[kBins];  // from the highest keys down
+  uint32_t found[3];    // bin of the k-th key, keys above it, keys in it
+  uint32_t count;       // entries below
+  uint32_t entry[kFewTies];
+  uint64_t score[kFewTies];
+};
+
+template <int kThreads>
+struct ListThreads {
+  static constexpr int kWarps = kThreads / 32;
+  ListShared<kThreads>& sh;
+  int turn;  // of the slots, so that one barrier does for each exchange
+
   __device__ __forceinline__ void sync() {
     if constexpr (kThreads == 32) {
       __syncwarp();
@@ -634,9 +599,35 @@ struct RowReduce {
       __syncthreads();
     }
   }
-  // Sum over the threads before this one.
+  __device__ __forceinline__ uint32_t sum(uint32_t v) {
+    v = __reduce_add_sync(0xFFFFFFFFu, v);
+    if constexpr (kWarps == 1) return v;
+    return exchange(v, 0u, [](uint32_t x) { return __reduce_add_sync(0xFFFFFFFFu, x); });
+  }
+  __device__ __forceinline__ uint32_t max(uint32_t v) {
+    v = __reduce_max_sync(0xFFFFFFFFu, v);
+    if constexpr (kWarps == 1) return v;
+    return exchange(v, 0u, [](uint32_t x) { return __reduce_max_sync(0xFFFFFFFFu, x); });
+  }
+  // least of lo and largest of hi
+  __device__ __forceinline__ void range(uint32_t& lo, uint32_t& hi) {
+    lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+    hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+    if constexpr (kWarps > 1) {
+      const int lane = threadIdx.x & 31;
+      uint32_t* const at = sh.slot[turn];
+      turn ^= 1;
+      if (lane == 0) {
+        at[threadIdx.x >> 5] = lo;
+        at[32 + (threadIdx.x >> 5)] = hi;
+      }
+      __syncthreads();
+      lo = __reduce_min_sync(0xFFFFFFFFu, lane < kWarps ? at[lane] : 0xFFFFFFFFu);
+      hi = __reduce_max_sync(0xFFFFFFFFu, lane < kWarps ? at[32 + lane] : 0u);
+    }
+  }
+  // sum over the threads before this one
   __device__ __forceinline__ uint32_t before(uint32_t v) {
-    constexpr int kWarps = kThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t upto = v;
 #pragma unroll
@@ -644,116 +635,102 @@ struct RowReduce {
       const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
       if (lane >= o) upto += y;
     }
-    if constexpr (kWarps == 1) {
-      return upto - v;
-    } else {
-      uint32_t* const at = slot[turn];
-      turn ^= 1;
-      if (lane == 31) at[warp] = upto;
-      __syncthreads();
-      return upto - v + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? at[lane] : 0u);
-    }
+    if constexpr (kWarps == 1) return upto - v;
+    uint32_t* const at = sh.slot[turn];
+    turn ^= 1;
+    if (lane == 31) at[warp] = upto;
+    __syncthreads();
+    return upto - v + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? at[lane] : 0u);
+  }
+
+ private:
+  template <typename F>
+  __device__ __forceinline__ uint32_t exchange(uint32_t v, uint32_t none, F reduce) {
+    uint32_t* const at = sh.slot[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) at[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    return reduce(lane < kWarps ? at[lane] : none);
   }
 };
 
-// Blocks to score again, where they are few.
-constexpr uint32_t kFewTies = 32u;
-struct FewTies {
-  uint64_t score[kFewTies];
-  int32_t block[kFewTies];
-};
-
-// The border of the k highest keys: at least k keys are >= hi, fewer are above it; lo is the
-// largest key below hi (0: none) where exactly k are, else hi.
+// The border of the k highest keys (0: none) that lie in from .. to: at least k keys are >= hi, fewer are
+// above it; lo is the largest key below hi (0: none) where exactly k are, else hi.  By histograms of
+// the range, each of the part that holds the k-th key, until that has at most 32 keys (or one value),
+// which a warp ranks.  Keys that are scores spread well: one histogram does for nearly all lists.  (A
+// search by halves took 16 counts over the thread block, 7500 cycles for 2048 keys; keys in shared memory
+// and short loops over them, 3 us more of 58 for 256 lists of 2048.)
 struct Border {
   uint32_t hi, lo, count;
 };
-// By histograms of the keys' range, each of the part that holds the k-th key, until that has at most 32
-// keys (or one value), which a warp ranks.  Keys that are scores spread well: one histogram does for
-// nearly all rows.  (A search by halves took 16 counts over the thread block, 7500 cycles for 2048 keys.)
-template <int kThreads>
-struct RowHistogram {
-  static constexpr int kBins = kThreads == 32 ? 256 : 1024, kEach = kBins / kThreads;
-  uint32_t bin[kBins];  // from the highest keys down
-  uint32_t list[32];
-  uint32_t listed;
-  uint32_t found[3];  // bin, keys above it, keys in it
-};
 template <int kThreads, int P>
-__device__ __forceinline__ Border find_border(const uint32_t (&key)[P], uint32_t k, RowReduce<kThreads>& red,
-                                              RowHistogram<kThreads>& hist) {
-  using Hist = RowHistogram<kThreads>;
+__device__ __forceinline__ Border find_border(const uint32_t (&key)[P], uint32_t k, uint32_t from, uint32_t to,
+                                              ListThreads<kThreads>& th) {
+  ListShared<kThreads>& sh = th.sh;
+  constexpr int kBins = ListShared<kThreads>::kBins, kEach = kBins / kThreads, kBits = kThreads == 32 ? 8 : 10;
   const int lane = threadIdx.x & 31, me = threadIdx.x % kThreads;
-  uint32_t least = 0xFFFFFFFFu, most = 0u;
-#pragma unroll
-  for (int j = 0; j < P; ++j) {
-    if (key[j] == 0u) continue;
-    least = min(least, key[j]);
-    most = max(most, key[j]);
-  }
-  uint32_t from = red.min(least), to = red.max(most);  // the k-th key lies in from .. to
   uint32_t above = 0u, inside = 0u;
   while (true) {
-    const int shift = max(0, 32 - __clz(to - from) - (kThreads == 32 ? 8 : 10));
+    const int shift = max(0, 32 - __clz(to - from) - kBits);
 #pragma unroll
-    for (int x = 0; x < Hist::kEach; ++x) hist.bin[me + x * kThreads] = 0u;
-    if (me == 0) hist.listed = 0u;
-    red.sync();
+    for (int x = 0; x < kEach; ++x) sh.bin[me + x * kThreads] = 0u;
+    if (me == 0) sh.count = 0u;
+    th.sync();
 #pragma unroll
     for (int j = 0; j < P; ++j)
-      if (key[j] >= from && key[j] <= to && key[j] != 0u) atomicAdd(&hist.bin[Hist::kBins - 1 - ((key[j] - from) >> shift)], 1u);
-    red.sync();
-    uint32_t each[Hist::kEach], sum = 0u;
+      if (key[j] - from <= to - from) atomicAdd(&sh.bin[kBins - 1 - ((key[j] - from) >> shift)], 1u);  // from > 0
+    th.sync();
+    uint32_t each[kEach], sum = 0u;
 #pragma unroll
-    for (int x = 0; x < Hist::kEach; ++x) sum += each[x] = hist.bin[me * Hist::kEach + x];
-    uint32_t upto = above + red.before(sum);
+    for (int x = 0; x < kEach; ++x) sum += each[x] = sh.bin[me * kEach + x];
+    uint32_t upto = above + th.before(sum);
     if (upto < k && upto + sum >= k) {
 #pragma unroll
-      for (int x = 0; x < Hist::kEach; ++x) {
+      for (int x = 0; x < kEach; ++x) {
         if (upto < k && upto + each[x] >= k) {
-          hist.found[0] = Hist::kBins - 1 - (me * Hist::kEach + x);
-          hist.found[1] = upto;
-          hist.found[2] = each[x];
+          sh.found[0] = kBins - 1 - (me * kEach + x);
+          sh.found[1] = upto;
+          sh.found[2] = each[x];
         }
         upto += each[x];
       }
     }
-    red.sync();
-    const uint32_t low = from + (hist.found[0] << shift);
+    th.sync();
+    const uint32_t low = from + (sh.found[0] << shift);
     to = shift == 0 ? low : min(to, low + ((1u << shift) - 1u));
     from = low;
-    above = hist.found[1];
-    inside = hist.found[2];
+    above = sh.found[1];
+    inside = sh.found[2];
     if (inside <= 32u || from == to) break;
-    red.sync();  // found is read before it is written again
+    th.sync();  // found is read before it is written again
   }
   Border at{from, from, above + inside};
-  if (from != to) {
+  uint32_t below = 0u;  // the largest key below `from`
 #pragma unroll
-    for (int j = 0; j < P; ++j)
-      if (key[j] >= from && key[j] <= to) hist.list[atomicAdd(&hist.listed, 1u)] = key[j];
-    red.sync();
-    const uint32_t mine = lane < static_cast<int>(inside) ? hist.list[lane] : 0u;
-    uint32_t greater = 0u, equal = 0u;
+  for (int j = 0; j < P; ++j) {
+    if (key[j] < from) below = max(below, key[j]);
+    if (from != to && key[j] - from <= to - from) sh.entry[atomicAdd(&sh.count, 1u)] = key[j];
+  }
+  below = th.max(below);  // (a barrier, or)
+  if constexpr (kThreads == 32) __syncwarp();
+  if (from != to) {
+    const uint32_t mine = lane < static_cast<int>(inside) ? sh.entry[lane] : 0u;
+    uint32_t greater = above, equal = 0u, next = 0u;  // next: the largest entry below mine
+#pragma unroll 1
     for (uint32_t x = 0; x < inside; ++x) {
-      const uint32_t other = hist.list[x];
+      const uint32_t other = sh.entry[x];
       greater += other > mine ? 1u : 0u;
       equal += other == mine ? 1u : 0u;
+      if (other < mine) next = max(next, other);
     }
-    greater += above;
     const uint32_t hit = __ballot_sync(0xFFFFFFFFu, lane < static_cast<int>(inside) && greater < k && greater + equal >= k);
     const int src = __ffs(hit) - 1;
     at.hi = __shfl_sync(0xFFFFFFFFu, mine, src);
     at.count = __shfl_sync(0xFFFFFFFFu, greater + equal, src);
+    below = max(below, __shfl_sync(0xFFFFFFFFu, next, src));
   }
-  at.lo = at.hi;
-  if (at.count == k) {
-    uint32_t lo = 0u;
-#pragma unroll
-    for (int j = 0; j < P; ++j)
-      if (key[j] < at.hi) lo = max(lo, key[j]);
-    at.lo = red.max(lo);
-  }
+  at.lo = at.count == k ? below : at.hi;
   return at;
 }
 
@@ -764,23 +741,83 @@ __device__ __forceinline__ float two_sum(float a, float b, float& e) {
   return s;
 }
 
-// The list of one (query token, KV head): of the row's kThreads threads, t holds the keys of P
-// blocks from t P on; a thread block has 128 / kThreads rows, or one.  Bound: latency of a dozen
-// barriers and exchanges between the row's threads.
-template <int D, int kThreads, int P>
+// The score of one block in twice binary32's precision, by a warp: sum + rest, in all lanes.  Lanes take 8
+// channels of q- . lo, q+ . hi at a time.
+__device__ __noinline__ uint64_t score_pair(const SelectParams& p, int tok, int h, int64_t blk) {
+  const int lane = threadIdx.x & 31;
+  float sum = 0.0f, rest = 0.0f;
+  for (int d = 8 * lane; d < 2 * p.D; d += 256) {
+    const bool low = d < p.D;
+    float qh[8] = {}, ql[8] = {};
+    const uint16_t* const q = p.q + tok * p.q_row_pitch + static_cast<int64_t>(h) * p.group * p.q_head_pitch + (low ? d : d - p.D);
+    uint32_t w[4];
+#pragma unroll 2
+    for (int j = 0; j < p.group; ++j) {
+      load16B(q + j * p.q_head_pitch, w);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const float v = x % 2 == 0 ? bf16lo(w[x / 2]) : bf16hi(w[x / 2]);
+        float e;
+        qh[x] = two_sum(qh[x], low != (v > 0.0f) ? v : 0.0f, e);
+        ql[x] = __fadd_rn(ql[x], e);
+      }
+    }
+    load16B(p.bounds + (blk * p.H + h) * (2 * p.D) + d, w);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const float v = x % 2 == 0 ? bf16lo(w[x / 2]) : bf16hi(w[x / 2]);
+      const float t = __fmul_rn(qh[x], v);
+      float e;
+      sum = two_sum(sum, t, e);
+      rest = __fadd_rn(rest, __fadd_rn(e, __fmaf_rn(ql[x], v, __fmaf_rn(qh[x], v, -t))));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    float e;
+    const float rest2 = __shfl_xor_sync(0xFFFFFFFFu, rest, o);
+    sum = two_sum(sum, __shfl_xor_sync(0xFFFFFFFFu, sum, o), e);
+    rest = __fadd_rn(__fadd_rn(rest, rest2), e);
+  }
+  sum = two_sum(sum, rest, rest);
+  return isnan(sum) ? 0ull : static_cast<uint64_t>(score_key(sum)) << 32 | score_key(rest);
+}
+
+// The same in binary64 (two operations a cycle and SM on this GPU), an ordered integer; NaN: 0.
+__device__ __noinline__ uint64_t score_wide(const SelectParams& p, int tok, int h, int64_t blk) {
+  const int lane = threadIdx.x & 31;
+  double sum = 0.0;
+  for (int d = lane; d < 2 * p.D; d += 32) {
+    const bool low = d < p.D;
+    const uint16_t* const q = p.q + tok * p.q_row_pitch + static_cast<int64_t>(h) * p.group * p.q_head_pitch + (low ? d : d - p.D);
+    double qd = 0.0;
+    for (int j = 0; j < p.group; ++j) {
+      const float v = __uint_as_float(static_cast<uint32_t>(LDX(q + j * p.q_head_pitch)) << 16);
+      if (low != (v > 0.0f)) qd += static_cast<double>(v);
+    }
+    sum = fma(qd, static_cast<double>(__uint_as_float(static_cast<uint32_t>(LDX(p.bounds + (blk * p.H + h) * (2 * p.D) + d)) << 16)), sum);
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(sum + 0.0));
+  return isnan(sum) ? 0ull : (u >> 63) != 0ull ? ~u : u | 0x8000000000000000ull;
+}
+
+// The list of one (query token, KV head): of its kThreads threads, t holds the keys of P blocks from t P on;
+// a thread block has 128 / kThreads lists, or one.  Bound: latency of a dozen barriers and exchanges
+// between the threads, and of the first use of each instruction line.
+template <int kThreads, int P>
 __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) select_kernel(const SelectParams p) {
-  constexpr int kC = D / 16, kRows = kThreads < 128 ? 128 / kThreads : 1;
-  static_assert(kThreads == 32 || kRows == 1, "rows of one warp, or of the block");
-  const int lane = threadIdx.x & 31, warp = kThreads == 32 ? 0 : threadIdx.x >> 5;  // of the row
-  const int me = threadIdx.x % kThreads;
-  const int64_t at_row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kThreads;  // i H + h
+  constexpr int kRows = kThreads < 128 ? 128 / kThreads : 1, kWarps = kThreads / 32;
+  static_assert(kThreads == 32 || kRows == 1, "lists of one warp, or of the block");
+  static_assert(P % 4 == 0 && P <= 32, "vectors of keys, bits of a word");
+  __shared__ ListShared<kThreads> shared[kRows];
+  const int lane = threadIdx.x & 31, warp = kThreads == 32 ? 0 : threadIdx.x >> 5;  // of the list
+  const int me = threadIdx.x % kThreads, mine = threadIdx.x / kThreads;
+  const int64_t at_row = static_cast<int64_t>(blockIdx.x) * kRows + mine;  // i H + h
   const int i = static_cast<int>(at_row / p.H), h = static_cast<int>(at_row - static_cast<int64_t>(i) * p.H), s = blockIdx.y;
-  __shared__ uint32_t slots[2][32];
-  __shared__ FewTies ties_of[kRows];
-  __shared__ RowHistogram<kThreads> hists[kRows];
-  RowReduce<kThreads> red{slots, 0};
-  FewTies& few = ties_of[threadIdx.x / kThreads];
-  RowHistogram<kThreads>& hist = hists[threadIdx.x / kThreads];
+  ListShared<kThreads>& sh = shared[mine];
+  ListThreads<kThreads> th{sh, 0};
   int q0, n, len;
   const bool ok = select_range(p, s, q0, n, len);
   if (!ok && threadIdx.x == 0 && blockIdx.x == 0) set_status(p.status, 8u);
@@ -796,7 +833,14 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) select_kernel
     for (int j = me; j < p.topk; j += kThreads) STX(out + j, j < vis ? j : -1);
     return;
   }
-  // blocks below `head` and from `tail` on are listed in any case
+  float size = 0.0f;  // over the error bound of the scores
+  bool bounded = true;
+  for (int x = lane; x < p.sizes_n; x += 32) {
+    const float y = LDX(p.sizes + row * p.sizes_pitch + x);
+    bounded = bounded && y <= 1e38f;  // not: sums that may overflow, NaN
+    size = fmaxf(size, y);
+  }
+  // blocks below `head` and from `tail` on are listed in any case: their keys become 0
   const int head = min(p.first, vis), tail = max(vis - p.last, head);
   const uint32_t k = static_cast<uint32_t>(p.topk - head - (vis - tail));
   const int b0 = me * P;
@@ -807,166 +851,106 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) select_kernel
     if (b0 + j < vis) v = LDX(reinterpret_cast<const uint4*>(p.keys + row * p.pitch + b0 + j));
     key[j] = v.x, key[j + 1] = v.y, key[j + 2] = v.z, key[j + 3] = v.w;
   }
-  // the error bound of the scores
-  float size = 0.0f;
-  bool bounded = true;
-  for (int at = lane; at < p.sizes_n; at += 32) {
-    const float x = LDX(p.sizes + row * p.sizes_pitch + at);
-    bounded = bounded && x <= 1e38f;  // not: sums that may overflow, NaN
-    size = fmaxf(size, x);
+  uint32_t least = 0xFFFFFFFFu, most = 0u;
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    if (b0 + j < head || b0 + j >= tail) key[j] = 0u;
+    least = min(least, key[j] - 1u);  // 0 as the largest
+    most = max(most, key[j]);
   }
   size = group_max<32>(size);
   bounded = __all_sync(0xFFFFFFFFu, bounded);
   const float e = size > 0.0f ? size * p.err + 0x1p-130f : 0.0f;  // + roundings below the normal numbers
-#pragma unroll
-  for (int j = 0; j < P; ++j)
-    if (b0 + j < head || b0 + j >= tail) key[j] = 0u;  // out of the search
 
-  uint32_t listed = 0u;  // bits of this thread's blocks
+  Border at{kKeyListed, kKeyListed, 0u};  // listed: keys above at.hi, and of those equal to it the first
   if (k > 0u) {
-    bool done = false;
-    Border at = find_border<kThreads, P>(key, k, red, hist);
+    th.range(least, most);
+    at = find_border<kThreads, P>(key, k, least + 1u, most, th);
     const bool scored = at.hi > kKeyNan;  // not: blocks without a score fill the list
     const float hi = key_score(at.hi), lo = at.lo > kKeyNan ? key_score(at.lo) : -__int_as_float(0x7F800000);
     if (!bounded || (scored && e > 0.0f && !(hi - lo > 2.0f * e))) {
-      uint32_t again = 0u;
+      th.sync();  // the entries are read
+      if (me == 0) sh.count = 0u;
+      th.sync();
+      uint32_t again = 0u, certain = 0u;
 #pragma unroll
       for (int j = 0; j < P; ++j) {
         if (key[j] <= kKeyBad || (bounded && key[j] == kKeyNan)) continue;  // last in any case
         const float x = key_score(key[j]);
         if (bounded && x > lo + 2.0f * e) {
           key[j] = kKeyListed;
+          ++certain;
         } else if (bounded && x < hi - 2.0f * e) {
           key[j] = 0u;
         } else {
           again |= 1u << j;
         }
       }
-      // the lane's channels of q+ or q-, in binary64 (a warp's 32 x D / 16 x heads additions take
-      // D heads cycles of this GPU's binary64 unit)
-      double qd[kC];
-      auto load_q = [&]() {
-#pragma unroll
-        for (int x = 0; x < kC; ++x) qd[x] = 0.0;
-#pragma unroll 4
-        for (int j = 0; j < p.group; ++j) {
-          uint32_t w[D / 32];
-          load_bounds<D>(p.q + (q0 + i) * p.q_row_pitch + (static_cast<int64_t>(h) * p.group + j) * p.q_head_pitch +
-                             (lane % 16) * kC, w);
-#pragma unroll
-          for (int x = 0; x < kC; ++x) {
-            const uint32_t v = x % 2 == 0 ? w[x / 2] << 16 : w[x / 2] & 0xFFFF0000u;
-            qd[x] += (lane < 16) != (__uint_as_float(v) > 0.0f) ? wide(v) : 0.0;
-          }
-        }
-      };
-      // the exact score of a block that has one (it lies in the pool), as an ordered integer above 0;
-      // NaN: 0
-      auto score64 = [&](int b) -> uint64_t {
-        const int64_t blk = LDX(p.table + static_cast<int64_t>(s) * p.max_blocks + b);
-        uint32_t w[D / 32];
-        load_bounds<D>(p.bounds + (blk * p.H + h) * (2 * D) + lane * kC, w);
-        double sum = 0.0;
-#pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-          sum = fma(qd[2 * x], wide(w[x] << 16), sum);
-          sum = fma(qd[2 * x + 1], wide(w[x] & 0xFFFF0000u), sum);
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        const uint64_t u = static_cast<uint64_t>(__double_as_longlong(sum + 0.0));
-        return isnan(sum) ? 0ull : (u >> 63) != 0ull ? ~u : u | 0x8000000000000000ull;
-      };
-      uint32_t certain = 0u;
-#pragma unroll
-      for (int j = 0; j < P; ++j) certain += key[j] == kKeyListed ? 1u : 0u;
-      const uint32_t m = red.sum(__popc(again)), need = k - red.sum(certain);
+      for (uint32_t left = again; left != 0u; left &= left - 1u) {
+        const uint32_t place = atomicAdd(&sh.count, 1u);
+        if (place < kFewTies) sh.entry[place] = b0 + __ffs(left) - 1;
+      }
+      const uint32_t need = k - th.sum(certain);
+      th.sync();
+      const uint32_t m = sh.count;
+      const int32_t* const table = p.table + static_cast<int64_t>(s) * p.max_blocks;  // what has a score lies in the pool
       if (m <= kFewTies && m >= need && size > 0x1p-60f && size < 0x1p100f) {
-        // few, and nothing that overflows or underflows: their scores in pairs of binary32 numbers (48
-        // bits), a warp one at a time, and each one's rank among them
-        const uint32_t place = red.before(__popc(again));
-        uint32_t left = again;
-        for (uint32_t x = place; left != 0u; left &= left - 1u, ++x) few.block[x] = b0 + __ffs(left) - 1;
-        red.sync();
-        if (warp < static_cast<int>(m)) {
-          float qh[kC], ql[kC];
-#pragma unroll
-          for (int x = 0; x < kC; ++x) qh[x] = ql[x] = 0.0f;
-#pragma unroll 4
-          for (int j = 0; j < p.group; ++j) {
-            uint32_t w[D / 32];
-            load_bounds<D>(p.q + (q0 + i) * p.q_row_pitch + (static_cast<int64_t>(h) * p.group + j) * p.q_head_pitch +
-                               (lane % 16) * kC, w);
-#pragma unroll
-            for (int x = 0; x < kC; ++x) {
-              const float v = x % 2 == 0 ? bf16lo(w[x / 2]) : bf16hi(w[x / 2]);
-              float e2;
-              qh[x] = two_sum(qh[x], (lane < 16) != (v > 0.0f) ? v : 0.0f, e2);
-              ql[x] = __fadd_rn(ql[x], e2);
-            }
-          }
-          for (uint32_t y = warp; y < m; y += kThreads / 32) {
-            const int64_t blk = LDX(p.table + static_cast<int64_t>(s) * p.max_blocks + few.block[y]);
-            uint32_t w[D / 32];
-            load_bounds<D>(p.bounds + (blk * p.H + h) * (2 * D) + lane * kC, w);
-            float sum = 0.0f, rest = 0.0f;
-#pragma unroll
-            for (int x = 0; x < kC; ++x) {
-              const float v = x % 2 == 0 ? bf16lo(w[x / 2]) : bf16hi(w[x / 2]);
-              const float t = __fmul_rn(qh[x], v), low = __fmaf_rn(qh[x], v, -t);
-              float e2;
-              sum = two_sum(sum, t, e2);
-              rest = __fadd_rn(rest, __fadd_rn(e2, __fmaf_rn(ql[x], v, low)));
-            }
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) {
-              float e2;
-              const float rest2 = __shfl_xor_sync(0xFFFFFFFFu, rest, o);
-              sum = two_sum(sum, __shfl_xor_sync(0xFFFFFFFFu, sum, o), e2);
-              rest = __fadd_rn(__fadd_rn(rest, rest2), e2);
-            }
-            float tail2;
-            sum = two_sum(sum, rest, tail2);
-            if (lane == 0)
-              few.score[y] = isnan(sum) ? 0ull : static_cast<uint64_t>(score_key(sum)) << 32 | score_key(tail2);
-          }
+        // few, and nothing that overflows or underflows: a warp scores one at a time, then each one's rank
+        for (uint32_t x = warp; x < m; x += kWarps) {
+          const uint64_t u = score_pair(p, q0 + i, h, LDX(table + sh.entry[x]));
+          if (lane == 0) sh.score[x] = u;
         }
-        red.sync();
-        left = again;
-        for (uint32_t x = place; left != 0u; left &= left - 1u, ++x) {
-          const uint64_t mine = few.score[x];
+        th.sync();
+        if (me < static_cast<int>(m)) {
+          const uint64_t u = sh.score[me];
+          const uint32_t b = sh.entry[me];
           uint32_t rank = 0u;
-          for (uint32_t y = 0; y < m; ++y) {  // the list is in the order of the blocks
-            const uint64_t other = few.score[y];
-            rank += other > mine || (other == mine && y < x) ? 1u : 0u;
+          for (uint32_t x = 0; x < m; ++x) {
+            const uint64_t other = sh.score[x];
+            rank += other > u || (other == u && sh.entry[x] < b) ? 1u : 0u;
           }
-          if (rank < need) listed |= left & (0u - left);
+          sh.bin[me] = rank < need ? b : 0xFFFFFFFFu;  // the winners
         }
+        th.sync();
 #pragma unroll
         for (int j = 0; j < P; ++j)
-          if (key[j] == kKeyListed) listed |= 1u << j;
-        done = true;
+          if ((again >> j) & 1u) key[j] = 0u;
+        for (uint32_t x = 0; x < m; ++x) {
+          const uint32_t j = sh.bin[x] - static_cast<uint32_t>(b0);
+          if (j < static_cast<uint32_t>(P)) {
+#pragma unroll
+            for (int y = 0; y < P; ++y)
+              if (y == static_cast<int>(j)) key[y] = kKeyListed;
+          }
+        }
+        at = Border{kKeyListed, 0u, k};
       } else {
-        load_q();
 #pragma unroll 1
         for (int stage = 0; stage < 2; ++stage) {
-          uint32_t left = again;
-          while (true) {
+#pragma unroll 1
+          for (uint32_t left = again;;) {
             const uint32_t who = __ballot_sync(0xFFFFFFFFu, left != 0u);
             if (who == 0u) break;
             const int src = __ffs(who) - 1;
             const int j = __shfl_sync(0xFFFFFFFFu, __ffs(left) - 1, src);
-            const uint64_t u = score64((warp * 32 + src) * P + j);
+            const uint64_t u = score_wide(p, q0 + i, h, LDX(table + (warp * 32 + src) * P + j));
             const uint32_t bits = static_cast<uint32_t>(stage == 0 ? u >> 33 : (u >> 2) & 0x7FFFFFFFull);
-            const uint32_t fresh = u == 0ull ? kKeyNan64 : kKeyNan64 + 1u + bits;
             if (lane == src) {
               left &= left - 1u;
 #pragma unroll
               for (int x = 0; x < P; ++x)
-                if (x == j) key[x] = fresh;
+                if (x == j) key[x] = u == 0ull ? kKeyNan64 : kKeyNan64 + 1u + bits;
             }
           }
-          at = find_border<kThreads, P>(key, k, red, hist);
+          least = 0xFFFFFFFFu;
+          most = 0u;
+#pragma unroll
+          for (int j = 0; j < P; ++j) {
+            least = min(least, key[j] - 1u);
+            most = max(most, key[j]);
+          }
+          th.range(least, most);
+          at = find_border<kThreads, P>(key, k, least + 1u, most, th);
           if (at.count == k || stage == 1 || at.hi <= kKeyNan64) break;
           again = 0u;
 #pragma unroll
@@ -977,34 +961,31 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) select_kernel
               key[j] = key[j] > at.hi ? kKeyListed : 0u;
             }
           }
+          th.sync();  // the entries are read
         }
       }
     }
-    if (!done) {  // the keys above the border, and of those on it the first
-      uint32_t ties = 0u;
-#pragma unroll
-      for (int j = 0; j < P; ++j) {
-        if (key[j] > at.hi) listed |= 1u << j;
-        if (key[j] == at.hi) ties |= 1u << j;
-      }
-      if (at.count > k) {  // uniform
-        const uint32_t need = k - red.sum(__popc(listed));
-        uint32_t before = red.before(__popc(ties));
-        for (; ties != 0u; ties &= ties - 1u, ++before)
-          if (before < need) listed |= ties & (0u - ties);
-      } else {
-        listed |= ties;
-      }
-    }
   }
+  // ---- the list, in the order of the blocks ----
+  uint32_t listed = 0u, ties = 0u;
 #pragma unroll
-  for (int j = 0; j < P; ++j)
-    if (b0 + j < vis && (b0 + j < head || b0 + j >= tail)) listed |= 1u << j;
-  uint32_t before = red.before(__popc(listed));
+  for (int j = 0; j < P; ++j) {
+    if (key[j] > at.hi || (b0 + j < vis && (b0 + j < head || b0 + j >= tail))) listed |= 1u << j;
+    if (key[j] == at.hi) ties |= 1u << j;
+  }
+  if (at.count > k) {  // more equal ones than the list takes; uniform
+    const uint32_t left = static_cast<uint32_t>(p.topk) - th.sum(__popc(listed));
+    uint32_t before = th.before(__popc(ties));
+    for (; ties != 0u; ties &= ties - 1u, ++before)
+      if (before < left) listed |= ties & (0u - ties);
+  } else {
+    listed |= ties;
+  }
+  uint32_t before = th.before(__popc(listed));
   for (; listed != 0u; listed &= listed - 1u, ++before) STX(out + before, b0 + __ffs(listed) - 1);
 }
 
-template <int D, int kThreads, int P>
+template <int kThreads, int P>
 cudaError_t select_launch(const SelectParams& p, bool dependent, cudaStream_t s) {
   constexpr int kRows = kThreads < 128 ? 128 / kThreads : 1;
   cudaLaunchConfig_t cfg = {};
@@ -1017,7 +998,7 @@ cudaError_t select_launch(const SelectParams& p, bool dependent, cudaStream_t s)
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = dependent ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, select_kernel<D, kThreads, P>, p);
+  return cudaLaunchKernelEx(&cfg, select_kernel<kThreads, P>, p);
 }
 
 template <int D>
@@ -1062,15 +1043,16 @@ cudaError_t select_dim(SelectParams& p, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   const bool scores = p.most > p.topk;
   if (scores && (e = score_launch<D>(p, s)) != cudaSuccess) return e;
-  if (p.most <= 512) {
-    KVQ_LAUNCH("select_kernel", s, e = (select_launch<D, 32, 16>(p, scores, s)));
-  } else if (p.most <= 1024) {
-    KVQ_LAUNCH("select_kernel", s, e = (select_launch<D, 32, 32>(p, scores, s)));
-  } else if (p.most <= 4096) {
-    KVQ_LAUNCH("select_kernel", s, e = (select_launch<D, 256, 16>(p, scores, s)));
-  } else {
-    KVQ_LAUNCH("select_kernel", s, e = (select_launch<D, 1024, 32>(p, scores, s)));
-  }
+  // threads of a list: a warp where lists are many and short
+  const int64_t lists = static_cast<int64_t>(p.max_q) * p.H * p.S;
+  const bool many = lists >= 8 * num_sms();
+  KVQ_LAUNCH("select_kernel", s,
+             e = many && p.most <= 512    ? select_launch<32, 16>(p, scores, s)
+                 : many && p.most <= 1024 ? select_launch<32, 32>(p, scores, s)
+                 : p.most <= 512          ? select_launch<128, 4>(p, scores, s)
+                 : p.most <= 2048         ? select_launch<256, 8>(p, scores, s)
+                 : p.most <= 8192         ? select_launch<512, 16>(p, scores, s)
+                                          : select_launch<1024, 32>(p, scores, s));
   return e;
 }
 
