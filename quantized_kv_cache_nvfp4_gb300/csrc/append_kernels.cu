@@ -11,13 +11,13 @@
 // and the largest bf16(K') of its rows, channel by channel.
 //
 // Mapping: rows of one page that stand next to each other in slot_ids form a run; one warp
-// serves (run, head, tensor), so scales and bounds need no atomics.  L = D / 16 lanes (rounded
-// up to a power of two) read a row as 32 bytes each, 32 / L rows a pass, kBatch passes' loads in
-// flight; halves of a pair in different lanes meet by shuffles.  Pages up to kBatch passes stay in
-// registers between the maximum and the codes (page scales), larger ones are read twice.
-// Neighbouring warps take the heads of the same tokens, so a token's angles come from L1 but
-// once.  Behind those blocks of the grid, others turn Q: a warp holds a token's angles in
-// registers and walks its heads.
+// serves (run, head, tensor), so scales and bounds need no atomics.  L = D / 8 lanes (rounded up to a
+// power of two; at most 32, with two chunks each above head_dim 256) hold 8 channels of a row each,
+// 32 / L rows a pass, kBatch passes' loads in flight; halves of a pair in different lanes meet by shuffles.
+// Pages up to kBatch passes stay in registers, as they came, between the maximum and the codes
+// (page scales), larger ones are read twice; both turn K twice.  Neighbouring warps take the heads of the
+// same tokens, so a token's angles come from L1 but once.  Behind those blocks of the grid, others
+// turn Q: a warp holds a token's angles in registers and walks its heads.
 #include "page_scale.cuh"
 #include "kvq_params.h"
 
@@ -26,128 +26,123 @@ namespace kvq {
 namespace {
 
 constexpr int kAppendThreads = 128;
-constexpr int kBatch = 4;
 
-// Cosines and sines of a lane's two 8-channel chunks: 8 pairs a chunk where the halves of a
-// pair are rot / 2 apart, 4 where they are neighbours.
-struct Angles {
-  float c[2][8], s[2][8];
-};
-
-// What a lane does for its chunks 2 li and 2 li + 1.
+// What a lane does for its chunk ch of 8 channels: where the chunk's first angle stands (-1: not turned),
+// and, with pairs rot / 2 apart, where the partner chunk is and whether this one holds the b of its pairs.
 struct Turn {
-  int rot;           // channels turned; 0: none
-  bool pairs;        // neighbours
-  bool cross;        // a partner chunk is the other half of its lane's
-  int src[2];        // lane of the partner chunk
-  int at[2];         // first angle of the chunk; -1: not turned
-  bool second[2];    // the chunk holds the b of its pairs
+  int at, lane, slot;
+  bool second;
 };
-
-template <int L>
-__device__ __forceinline__ Turn make_turn(int rot, bool pairs, int lane) {
+__device__ __forceinline__ Turn make_turn(int rot, bool pairs, int ch, int base) {
+  const int half = rot / 16;  // chunks of a half
   Turn t;
-  t.rot = rot;
-  t.pairs = pairs;
-  const int li = lane % L, base = lane - li, half = rot / 16;  // chunks of a half
-  t.cross = !pairs && (half & 1) != 0;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int ch = 2 * li + j;
-    const bool in = ch < 2 * half;
-    t.second[j] = !pairs && in && ch >= half;
-    const int partner = pairs || !in ? ch : (t.second[j] ? ch - half : ch + half);
-    t.src[j] = base + partner / 2;
-    t.at[j] = !in ? -1 : pairs ? 4 * ch : 8 * (t.second[j] ? ch - half : ch);
-  }
+  const bool in = ch < 2 * half;
+  t.second = !pairs && in && ch >= half;
+  const int partner = pairs || !in ? ch : (t.second ? ch - half : ch + half);
+  t.lane = base + partner % 32;
+  t.slot = partner / 32;
+  t.at = !in ? -1 : pairs ? 4 * ch : 8 * (t.second ? ch - half : ch);
   return t;
 }
 
-__device__ __forceinline__ void load_angles(const Turn& t, const float* row, Angles& a) {
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    if (t.at[j] < 0) continue;
-    const float4* const c = reinterpret_cast<const float4*>(row + t.at[j]);
-    const float4* const s = reinterpret_cast<const float4*>(row + t.rot / 2 + t.at[j]);
-    const float4 c0 = LDX(c), s0 = LDX(s);
-    a.c[j][0] = c0.x, a.c[j][1] = c0.y, a.c[j][2] = c0.z, a.c[j][3] = c0.w;
-    a.s[j][0] = s0.x, a.s[j][1] = s0.y, a.s[j][2] = s0.z, a.s[j][3] = s0.w;
-    if (!t.pairs) {
-      const float4 c1 = LDX(c + 1), s1 = LDX(s + 1);
-      a.c[j][4] = c1.x, a.c[j][5] = c1.y, a.c[j][6] = c1.z, a.c[j][7] = c1.w;
-      a.s[j][4] = s1.x, a.s[j][5] = s1.y, a.s[j][6] = s1.z, a.s[j][7] = s1.w;
-    }
+// Cosines and signed sines of the chunk as pairs of neighbouring channels: y = x c + p s with p the
+// partner channel, s negative where the channel is the a of its pair.
+struct Angles {
+  uint64_t c[4], s[4];
+};
+__device__ __forceinline__ void load_angles(const Turn& t, int rot, bool pairs, const float* row, Angles& a) {
+  if (t.at < 0) return;
+  const uint4* const c = reinterpret_cast<const uint4*>(row + t.at);
+  const uint4* const s = reinterpret_cast<const uint4*>(row + rot / 2 + t.at);
+  if (pairs) {
+    const uint4 u = LDX(c), v = LDX(s);
+    constexpr uint32_t kNeg = 0x80000000u;
+    a.c[0] = pack_f32x2(u.x, u.x), a.c[1] = pack_f32x2(u.y, u.y), a.c[2] = pack_f32x2(u.z, u.z), a.c[3] = pack_f32x2(u.w, u.w);
+    a.s[0] = pack_f32x2(v.x ^ kNeg, v.x), a.s[1] = pack_f32x2(v.y ^ kNeg, v.y);
+    a.s[2] = pack_f32x2(v.z ^ kNeg, v.z), a.s[3] = pack_f32x2(v.w ^ kNeg, v.w);
+  } else {
+    const uint4 u0 = LDX(c), u1 = LDX(c + 1), v0 = LDX(s), v1 = LDX(s + 1);
+    const uint32_t n = t.second ? 0u : 0x80000000u;
+    a.c[0] = pack_f32x2(u0.x, u0.y), a.c[1] = pack_f32x2(u0.z, u0.w), a.c[2] = pack_f32x2(u1.x, u1.y), a.c[3] = pack_f32x2(u1.z, u1.w);
+    a.s[0] = pack_f32x2(v0.x ^ n, v0.y ^ n), a.s[1] = pack_f32x2(v0.z ^ n, v0.w ^ n);
+    a.s[2] = pack_f32x2(v1.x ^ n, v1.y ^ n), a.s[3] = pack_f32x2(v1.z ^ n, v1.w ^ n);
   }
 }
 
-// The lane's 16 channels in binary32, turned.  Every lane of the warp takes part.
-__device__ __forceinline__ void turn16(const Turn& t, const Angles& a, const uint32_t (&w)[8], float (&y)[16]) {
+// The lane's chunks in binary32, turned.  Every lane of the warp takes part (rot: uniform, 0 for none).
+template <int C>
+__device__ __forceinline__ void turn8(const Turn (&t)[C], const Angles (&a)[C], int rot, bool pairs, const uint32_t (&w)[C][4],
+                                      float (&y)[C][8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    y[2 * i] = bf16lo(w[i]);
-    y[2 * i + 1] = bf16hi(w[i]);
-  }
-  if (t.rot == 0) return;  // uniform
-  if (t.pairs) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if (t.at[j] < 0) continue;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x0 = y[8 * j + 2 * i], x1 = y[8 * j + 2 * i + 1];
-        y[8 * j + 2 * i] = __fsub_rn(__fmul_rn(x0, a.c[j][i]), __fmul_rn(x1, a.s[j][i]));
-        y[8 * j + 2 * i + 1] = __fadd_rn(__fmul_rn(x1, a.c[j][i]), __fmul_rn(x0, a.s[j][i]));
-      }
-    }
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      o[i] = __shfl_sync(0xFFFFFFFFu, t.cross ? w[4 * (1 - j) + i] : w[4 * j + i], t.src[j]);
-    if (t.at[j] < 0) continue;
+  for (int j = 0; j < C; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float p0 = bf16lo(o[i]), p1 = bf16hi(o[i]);
-      float &y0 = y[8 * j + 2 * i], &y1 = y[8 * j + 2 * i + 1];
-      const float m0 = __fmul_rn(y0, a.c[j][2 * i]), n0 = __fmul_rn(p0, a.s[j][2 * i]);
-      const float m1 = __fmul_rn(y1, a.c[j][2 * i + 1]), n1 = __fmul_rn(p1, a.s[j][2 * i + 1]);
-      y0 = t.second[j] ? __fadd_rn(m0, n0) : __fsub_rn(m0, n0);
-      y1 = t.second[j] ? __fadd_rn(m1, n1) : __fsub_rn(m1, n1);
+      y[j][2 * i] = bf16lo(w[j][i]);
+      y[j][2 * i + 1] = bf16hi(w[j][i]);
+    }
+  if (rot == 0) return;
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (pairs) {
+        o[i] = __byte_perm(w[j][i], 0u, 0x1032);  // the neighbour
+      } else {
+        o[i] = __shfl_sync(0xFFFFFFFFu, w[0][i], t[j].lane);
+        if constexpr (C == 2) {
+          const uint32_t o2 = __shfl_sync(0xFFFFFFFFu, w[1][i], t[j].lane);
+          o[i] = t[j].slot != 0 ? o2 : o[i];
+        }
+      }
+    }
+    if (t[j].at < 0) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t x = pack_f32x2(__float_as_uint(y[j][2 * i]), __float_as_uint(y[j][2 * i + 1]));
+      const uint64_t p = pack_f32x2(o[i] << 16, o[i] & 0xFFFF0000u);
+      // the sums one by one: the packed sum of packed products came out as one rounding
+      uint32_t m0, m1, n0, n1;
+      unpack_f32x2(mul_f32x2(x, a[j].c[i]), m0, m1);
+      unpack_f32x2(mul_f32x2(p, a[j].s[i]), n0, n1);
+      y[j][2 * i] = __fadd_rn(__uint_as_float(m0), __uint_as_float(n0));
+      y[j][2 * i + 1] = __fadd_rn(__uint_as_float(m1), __uint_as_float(n1));
     }
   }
 }
 
-__device__ __forceinline__ float absmax16f(const float (&y)[16]) {
-  float m = 0.0f;
+__device__ __forceinline__ float absmax8(const float (&y)[8]) {
+  float m = fabsf(y[0]);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(y[i]));
+  for (int i = 1; i < 8; ++i) m = fmaxf(m, fabsf(y[i]));
   return m;
 }
 
-// quantize_block and fp8_quantize16 (kvq_device.cuh) of binary32 values.
-__device__ __forceinline__ void quantize_block_f(const float (&y)[16], float s, uint32_t& c0, uint32_t& c1) {
+// quantize_block and fp8_quantize16 (kvq_device.cuh) of 8 binary32 values.
+__device__ __forceinline__ uint32_t quantize8(const float (&y)[8], float s) {
   const float inv = (s != 0.0f) ? __frcp_rn(s) : 0.0f;
-  const bool tiny = isinf(inv);  // the reciprocal overflowed, divide directly
-  uint32_t byte[8];
+  uint32_t byte[4];
+  if (!isinf(inv)) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    byte[i] = tiny ? e2m1x2_from_f32(__fdiv_rn(y[2 * i], s), __fdiv_rn(y[2 * i + 1], s))
-                   : e2m1x2_from_f32(__fmul_rn(y[2 * i], inv), __fmul_rn(y[2 * i + 1], inv));
-  c0 = bytes4(byte[0], byte[1], byte[2], byte[3]);
-  c1 = bytes4(byte[4], byte[5], byte[6], byte[7]);
+    for (int i = 0; i < 4; ++i) byte[i] = e2m1x2_from_f32(__fmul_rn(y[2 * i], inv), __fmul_rn(y[2 * i + 1], inv));
+  } else {  // the reciprocal overflowed, divide directly
+#pragma unroll
+    for (int i = 0; i < 4; ++i) byte[i] = e2m1x2_from_f32(__fdiv_rn(y[2 * i], s), __fdiv_rn(y[2 * i + 1], s));
+  }
+  return bytes4(byte[0], byte[1], byte[2], byte[3]);
 }
-__device__ __forceinline__ void fp8_quantize16_f(const float (&y)[16], float rs, uint32_t (&c)[4]) {
+__device__ __forceinline__ void fp8_quantize8(const float (&y)[8], float rs, uint32_t& c0, uint32_t& c1) {
   const float inv = (rs != 0.0f) ? __frcp_rn(rs) : 0.0f;
-  const bool tiny = isinf(inv);
-  c[0] = c[1] = c[2] = c[3] = 0u;
+  uint32_t w[4];
+  if (!isinf(inv)) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    c[i / 2] |= (tiny ? e4m3x2_from_f32(__fdiv_rn(y[2 * i], rs), __fdiv_rn(y[2 * i + 1], rs))
-                      : e4m3x2_from_f32(__fmul_rn(y[2 * i], inv), __fmul_rn(y[2 * i + 1], inv)))
-                << (16 * (i % 2));
+    for (int i = 0; i < 4; ++i) w[i] = e4m3x2_from_f32(__fmul_rn(y[2 * i], inv), __fmul_rn(y[2 * i + 1], inv));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = e4m3x2_from_f32(__fdiv_rn(y[2 * i], rs), __fdiv_rn(y[2 * i + 1], rs));
+  }
+  c0 = w[0] | w[1] << 16;
+  c1 = w[2] | w[3] << 16;
 }
 
 // bf16 minima and maxima of packed pairs (a NaN loses against a number).
@@ -160,6 +155,17 @@ __device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+
+// 16 bytes that this launch reads once, or (rw) may write too.
+__device__ __forceinline__ void load_row16(const void* p, uint32_t (&w)[4]) {
+  if (!KVQ_OK(p, 16, 16)) {
+    w[0] = w[1] = w[2] = w[3] = 0u;
+    return;
+  }
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "l"(p));
 }
 
 // Slot of token t: -1 where it is skipped.  `report`: the warp that speaks for the token.
@@ -175,12 +181,12 @@ __device__ __forceinline__ int64_t append_slot(const AppendParams& p, int64_t t,
   return s >= p.num_slots ? -1 : s;
 }
 
-template <int L, bool kV8>
+template <int L, int C>
 __device__ __forceinline__ void append_rows(const AppendParams& p, int64_t w) {
-  constexpr int R = 32 / L;  // rows per pass
+  constexpr int R = 32 / L;       // rows per pass
+  constexpr int kBatch = 8 / C;
   const int lane = threadIdx.x & 31;
   const int li = lane % L, sub = lane / L;
-  const bool act = li < p.nb;
   const int per = p.H * p.ntensors;
   const int64_t ci = w / per;
   const int rem = static_cast<int>(w - ci * per);
@@ -188,9 +194,16 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int64_t w) {
   const int64_t t0 = ci * p.chunk;
   if (t0 >= p.T) return;
   const AppendTensor ten = p.ten[tensor];
-  const Turn turn = make_turn<L>(ten.key && p.cos_sin != nullptr ? p.rot : 0, p.pairs, lane);
+  const int rot = ten.key && p.cos_sin != nullptr ? p.rot : 0;
+  const int D = p.D;
   uint16_t* const bounds = ten.key ? p.bounds : nullptr;
-  const int D = 16 * p.nb;
+  Turn turn[C];
+  bool act[C];
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    turn[j] = make_turn(rot, p.pairs, li + 32 * j, lane - li);
+    act[j] = 8 * (li + 32 * j) < D;
+  }
 
   auto page_of = [&](int64_t slot) -> int64_t { return slot < 0 ? -1 : slot / p.block_size; };
   const int64_t slot = append_slot(p, t0 + lane, rem == 0);
@@ -224,105 +237,121 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int64_t w) {
     float s0 = 0.0f;
     if (paged && !begins && lane == 0) s0 = LDX(ten.dst.rscale + prow);
     s0 = __shfl_sync(0xFFFFFFFFu, s0, 0);
-    const uint16_t* const x = ten.x + ts * ten.row_pitch + h * ten.head_pitch + 16 * li;
-    const int code_bytes = ten.fmt == 1 ? D / 2 : D;
+    const uint16_t* const x = ten.x + ts * ten.row_pitch + h * ten.head_pitch + 8 * li;
 
-    auto load = [&](int r, uint32_t (&v)[8]) {
+    uint32_t raw[kBatch][C][4];
+    auto load = [&](int r, uint32_t (&v)[C][4]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0u;
-      if (act && r < n) load32B<kV8, true>(x + r * ten.row_pitch, v);
+      for (int j = 0; j < C; ++j) {
+        v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0u;
+        if (act[j] && r < n) load_row16(x + r * ten.row_pitch + 256 * j, v[j]);
+      }
     };
-    auto turned = [&](int r, const uint32_t (&v)[8], float (&y)[16]) {
-      Angles a;
-      if (turn.rot != 0 && r < n)
-        load_angles(turn, p.cos_sin + static_cast<int64_t>(LDX(p.positions + ts + r)) * p.rot, a);
-      turn16(turn, a, v, y);
+    auto turned = [&](int r, const uint32_t (&v)[C][4], float (&y)[C][8]) {
+      Angles a[C];
+      if (rot != 0 && r < n) {
+        const float* const row = p.cos_sin + static_cast<int64_t>(LDX(p.positions + ts + r)) * rot;
+#pragma unroll
+        for (int j = 0; j < C; ++j) load_angles(turn[j], rot, p.pairs, row, a[j]);
+      }
+      turn8<C>(turn, a, rot, p.pairs, v, y);
     };
     auto row_of = [&](int r) -> int64_t { return LDX(p.slot_ids + ts + r) * p.H + h; };
 
-    uint32_t lo[8], hi[8];
+    uint32_t lo[C][4], hi[C][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      lo[i] = 0x7F807F80u;
-      hi[i] = 0xFF80FF80u;
-    }
-    float held[kBatch][16];
+    for (int j = 0; j < C; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lo[j][i] = 0x7F807F80u;
+        hi[j][i] = 0xFF80FF80u;
+      }
     float am = 0.0f;
     for (int k0 = 0; k0 * R < n; k0 += kBatch) {  // uniform
-      uint32_t raw[kBatch][8];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) load((k0 + k) * R + sub, raw[k]);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int r = (k0 + k) * R + sub;
         if ((k0 + k) * R >= n) break;  // uniform
-        float y[16];
+        float y[C][8];
         turned(r, raw[k], y);
-        const bool live = act && r < n;
-        if (bounds != nullptr && live) {
+        if (bounds != nullptr && r < n) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t b2 = pack_bf16x2(y[2 * i], y[2 * i + 1]);
-            lo[i] = bf16x2_min(lo[i], b2);
-            hi[i] = bf16x2_max(hi[i], b2);
-          }
+          for (int j = 0; j < C; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t b2 = pack_bf16x2(y[j][2 * i], y[j][2 * i + 1]);
+              lo[j][i] = bf16x2_min(lo[j][i], b2);
+              hi[j][i] = bf16x2_max(hi[j][i], b2);
+            }
         }
-        const float vb = absmax16f(y);  // 0 in lanes without a row
-        if (paged) {
-          am = fmaxf(am, vb);
-          if (k0 == 0) {
+        float vb[C];  // 0 in lanes without a row
+        float row_max = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) held[k][i] = y[i];
-          }
+        for (int j = 0; j < C; ++j) {
+          vb[j] = absmax8(y[j]);
+          row_max = fmaxf(row_max, vb[j]);
+        }
+        if (paged) {
+          am = fmaxf(am, row_max);
           continue;
         }
-        const float amax = group_max<L>(vb);
+        const float amax = group_max<L>(row_max);
         if (ten.fmt == 3) {
           const float rs = __fdiv_rn(amax, kE4M3Max);
-          uint32_t c[4];
-          fp8_quantize16_f(y, rs, c);
-          if (live) {
-            const int64_t row = row_of(r);
-            store16B(ten.dst.codes + row * code_bytes + 16 * li, c);
-            if (li == 0) STX(ten.dst.rscale + row, rs);
+          const int64_t row = r < n ? row_of(r) : 0;
+#pragma unroll
+          for (int j = 0; j < C; ++j) {
+            uint32_t c0, c1;
+            fp8_quantize8(y[j], rs, c0, c1);
+            if (act[j] && r < n) store8B(ten.dst.codes + row * D + 8 * (li + 32 * j), c0, c1);
           }
+          if (li == 0 && r < n) STX(ten.dst.rscale + row, rs);
         } else {
           const float rs = __fdiv_rn(amax, kE2M1Max * kE4M3Max);
           const float rinv = (rs != 0.0f) ? __frcp_rn(rs) : 0.0f;
-          const uint32_t bsb = block_scale_code(vb, rs, rinv);
-          uint32_t c0, c1;
-          quantize_block_f(y, __fmul_rn(e4m3_to_f32(bsb), rs), c0, c1);
-          if (live) {
-            const int64_t row = row_of(r);
-            store8B(ten.dst.codes + row * code_bytes + 8 * li, c0, c1);
-            STX(ten.dst.bscale + row * p.nb + li, static_cast<uint8_t>(bsb));
-            if (li == 0) STX(ten.dst.rscale + row, rs);
+          const int64_t row = r < n ? row_of(r) : 0;
+#pragma unroll
+          for (int j = 0; j < C; ++j) {
+            const float block = fmaxf(vb[j], __shfl_xor_sync(0xFFFFFFFFu, vb[j], 1));
+            const uint32_t bsb = block_scale_code(block, rs, rinv);
+            const uint32_t c = quantize8(y[j], __fmul_rn(e4m3_to_f32(bsb), rs));
+            if (act[j] && r < n) {
+              const int ch = li + 32 * j;
+              STX(reinterpret_cast<uint32_t*>(ten.dst.codes + row * (D / 2)) + ch, c);
+              if (ch % 2 == 0) STX(ten.dst.bscale + row * (D / 16) + ch / 2, static_cast<uint8_t>(bsb));
+            }
           }
+          if (li == 0 && r < n) STX(ten.dst.rscale + row, rs);
         }
       }
     }
 
     if (bounds != nullptr) {
 #pragma unroll
-      for (int o = L; o < 32; o <<= 1)
+      for (int j = 0; j < C; ++j) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          lo[i] = bf16x2_min(lo[i], __shfl_xor_sync(0xFFFFFFFFu, lo[i], o));
-          hi[i] = bf16x2_max(hi[i], __shfl_xor_sync(0xFFFFFFFFu, hi[i], o));
+        for (int o = L; o < 32; o <<= 1)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            lo[j][i] = bf16x2_min(lo[j][i], __shfl_xor_sync(0xFFFFFFFFu, lo[j][i], o));
+            hi[j][i] = bf16x2_max(hi[j][i], __shfl_xor_sync(0xFFFFFFFFu, hi[j][i], o));
+          }
+        if (act[j] && sub == 0) {
+          uint16_t* const at = bounds + prow * 2 * D + 8 * (li + 32 * j);
+          if (!begins) {
+            uint32_t was[4];
+            load16B_rw(at, was);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) lo[j][i] = bf16x2_min(lo[j][i], was[i]);
+            load16B_rw(at + D, was);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) hi[j][i] = bf16x2_max(hi[j][i], was[i]);
+          }
+          store16B(at, lo[j]);
+          store16B(at + D, hi[j]);
         }
-      if (act && sub == 0) {
-        uint16_t* const at = bounds + prow * 2 * D + 16 * li;
-        if (!begins) {
-          uint32_t was[8];
-          load32B<false, false>(at, was);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) lo[i] = bf16x2_min(lo[i], was[i]);
-          load32B<false, false>(at + D, was);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) hi[i] = bf16x2_max(hi[i], was[i]);
-        }
-        store32B<false>(at, lo);
-        store32B<false>(at + D, hi);
       }
     }
     if (!paged) continue;
@@ -332,58 +361,67 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int64_t w) {
       am = 0.0f;
       for (int k = 0; k * R < n; ++k) {
         const int r = k * R + sub;
-        uint32_t v[8];
-        float y[16];
+        uint32_t v[C][4];
+        float y[C][8];
         load(r, v);
         turned(r, v, y);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) am = fmaxf(am, fabsf(y[i]) <= 3.4028235e38f ? fabsf(y[i]) : 0.0f);
+        for (int j = 0; j < C; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) am = fmaxf(am, fabsf(y[j][i]) <= 3.4028235e38f ? fabsf(y[j][i]) : 0.0f);
       }
       am = group_max<32>(am);
     }
     if (!(s0 > 0.0f && s0 <= 3.4028235e38f)) s0 = 0.0f;  // no scale stored yet
     const float s = fmaxf(s0, page_scale_need(am));
-    uint8_t* const cp = ten.dst.codes + (pg * p.block_size * p.H + h) * D + 16 * li;
     const int64_t cpitch = static_cast<int64_t>(p.H) * D;
     if (s0 > 0.0f && s > s0) {  // the rows that the page holds, under the new scale
       const float f = __fdiv_rn(s0, s);
-      for (int r = sub; r < p.block_size; r += R) {
-        if (!act) continue;
+      uint8_t* const cp = ten.dst.codes + (pg * p.block_size * p.H + h) * D;
+      const int each = D / 16;  // 16-byte pieces of a row
+      for (int at = lane; at < p.block_size * each; at += 32) {
+        uint8_t* const to = cp + (at / each) * cpitch + 16 * (at % each);
         uint32_t c[4];
-        load16B_rw(cp + r * cpitch, c);
+        load16B_rw(to, c);
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[i] = rescale4(c[i], f);
-        store16B(cp + r * cpitch, c);
+        store16B(to, c);
       }
       __syncwarp();  // before the call's own rows go over them
     }
     if (lane == 0 && s != s0) STX(ten.dst.rscale + prow, s);
-    auto put = [&](const float (&y)[16], int r) {
-      if (!(act && r < n)) return;
-      uint32_t c[4];
-      fp8_quantize16_f(y, s, c);
-      store16B(ten.dst.codes + row_of(r) * D + 16 * li, c);
-    };
+    const bool kept = n <= kBatch * R;  // in raw
+    for (int k0 = 0; k0 * R < n; k0 += kBatch) {
+      if (!kept) {
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) put(held[k], k * R + sub);
-    for (int k = kBatch; k * R < n; ++k) {
-      const int r = k * R + sub;
-      uint32_t v[8];
-      float y[16];
-      load(r, v);
-      turned(r, v, y);
-      put(y, r);
+        for (int k = 0; k < kBatch; ++k) load((k0 + k) * R + sub, raw[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int r = (k0 + k) * R + sub;
+        if ((k0 + k) * R >= n) break;  // uniform
+        float y[C][8];
+        turned(r, raw[k], y);
+        if (r >= n) continue;
+        const int64_t row = row_of(r);
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+          uint32_t c0, c1;
+          fp8_quantize8(y[j], s, c0, c1);
+          if (act[j]) store8B(ten.dst.codes + row * D + 8 * (li + 32 * j), c0, c1);
+        }
+      }
     }
   }
 }
 
 // Q: warp w takes heads first .. of one token, 32 / L at a time.
-template <int L, bool kV8>
+template <int L, int C>
 __device__ __forceinline__ void append_turn_q(const AppendParams& p, int64_t w) {
   constexpr int R = 32 / L;
+  constexpr int kBatch = 4 / C;
   const int lane = threadIdx.x & 31;
   const int li = lane % L, sub = lane / L;
-  const bool act = li < p.nb;
   const int64_t t = w / p.q_parts;
   if (t >= p.T) return;
   const int first = static_cast<int>(w - t * p.q_parts) * p.q_heads;
@@ -393,50 +431,61 @@ __device__ __forceinline__ void append_turn_q(const AppendParams& p, int64_t w) 
     if (lane == 0 && first == 0) set_status(p.status, 4u);
     return;
   }
-  const Turn turn = make_turn<L>(p.rot, p.pairs, lane);
-  Angles a;
-  if (act) load_angles(turn, p.cos_sin + static_cast<int64_t>(pos) * p.rot, a);
-  const uint16_t* const x = p.q + t * p.q_row_pitch + 16 * li;
-  uint16_t* const y_at = p.q_out + t * p.qo_row_pitch + 16 * li;
+  Turn turn[C];
+  Angles a[C];
+  bool act[C];
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    turn[j] = make_turn(p.rot, p.pairs, li + 32 * j, lane - li);
+    act[j] = 8 * (li + 32 * j) < p.D;
+    load_angles(turn[j], p.rot, p.pairs, p.cos_sin + static_cast<int64_t>(pos) * p.rot, a[j]);
+  }
+  const uint16_t* const x = p.q + t * p.q_row_pitch + 8 * li;
+  uint16_t* const y_at = p.q_out + t * p.qo_row_pitch + 8 * li;
   const int end = min(first + p.q_heads, p.Hq);
   for (int h0 = first; h0 < end; h0 += kBatch * R) {
-    uint32_t raw[kBatch][8];
+    uint32_t raw[kBatch][C][4];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int h = h0 + k * R + sub;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) raw[k][i] = 0u;
-      if (act && h < end) load32B<kV8, false>(x + h * p.q_head_pitch, raw[k]);
+      for (int j = 0; j < C; ++j) {
+        raw[k][j][0] = raw[k][j][1] = raw[k][j][2] = raw[k][j][3] = 0u;
+        if (act[j] && h < end) load16B_rw(x + h * p.q_head_pitch + 256 * j, raw[k][j]);
+      }
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int h = h0 + k * R + sub;
-      float y[16];
-      turn16(turn, a, raw[k], y);
-      uint32_t o[8];
+      float y[C][8];
+      turn8<C>(turn, a, p.rot, p.pairs, raw[k], y);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
-      if (act && h < end) store32B<kV8>(y_at + h * p.qo_head_pitch, o);
+      for (int j = 0; j < C; ++j) {
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(y[j][2 * i], y[j][2 * i + 1]);
+        if (act[j] && h < end) store16B(y_at + h * p.qo_head_pitch + 256 * j, o);
+      }
     }
   }
 }
 
-template <int L, bool kV8>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
+template <int L, int C>
+__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendParams p) {
   const int64_t warp = threadIdx.x >> 5;
   const int64_t block = blockIdx.x;
   if (block < p.row_blocks) {
-    append_rows<L, kV8>(p, block * (kAppendThreads / 32) + warp);
+    append_rows<L, C>(p, block * (kAppendThreads / 32) + warp);
   } else {
-    append_turn_q<L, kV8>(p, (block - p.row_blocks) * (kAppendThreads / 32) + warp);
+    append_turn_q<L, C>(p, (block - p.row_blocks) * (kAppendThreads / 32) + warp);
   }
 }
 
-template <int L, bool kV8>
+template <int L, int C>
 cudaError_t append_launch(const AppendParams& p_in, cudaStream_t s) {
   AppendParams p = p_in;
   constexpr int kW = kAppendThreads / 32, R = 32 / L;
-  auto k = append_kernel<L, kV8>;
+  auto k = append_kernel<L, C>;
   // tokens per warp: as many as leave 16 warps an SM (one token a warp in a decode step, whose
   // runs are single rows; 32 in a prompt)
   const int64_t rows = static_cast<int64_t>(p.T) * p.H * p.ntensors, fill = 16ll * num_sms();
@@ -460,14 +509,17 @@ cudaError_t append_launch(const AppendParams& p_in, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_append(const AppendParams& p, bool v8, cudaStream_t s) {
-  int L = 1;
-  while (L < p.nb) L <<= 1;
-#define KVQ_APPEND(N) \
-  if (L == N) return v8 ? append_launch<N, true>(p, s) : append_launch<N, false>(p, s);
-  KVQ_APPEND(1) KVQ_APPEND(2) KVQ_APPEND(4) KVQ_APPEND(8) KVQ_APPEND(16) KVQ_APPEND(32)
-#undef KVQ_APPEND
-  return cudaErrorInvalidValue;
+cudaError_t launch_append(const AppendParams& p, cudaStream_t s) {
+  if (p.D > 256) return append_launch<32, 2>(p, s);
+  int L = 2;
+  while (8 * L < p.D) L <<= 1;
+  switch (L) {
+    case 2: return append_launch<2, 1>(p, s);
+    case 4: return append_launch<4, 1>(p, s);
+    case 8: return append_launch<8, 1>(p, s);
+    case 16: return append_launch<16, 1>(p, s);
+  }
+  return append_launch<32, 1>(p, s);
 }
 
 }  // namespace kvq

@@ -834,7 +834,7 @@ KVQ_API kvq_status kvq_append(const kvq_bf16_in* k, const kvq_bf16_in* v, int32_
   if (dev_status != nullptr && (st = check_dev(dev_status, "dev_status")) != KVQ_OK) return st;
   p.T = num_tokens;
   p.H = H;
-  p.nb = D / 16;
+  p.D = D;
   p.slot_ids = slot_ids;
   p.num_slots = pool->num_slots;
   p.block_size = pool->block_size;
@@ -864,7 +864,7 @@ KVQ_API kvq_status kvq_append(const kvq_bf16_in* k, const kvq_bf16_in* v, int32_
   }
   dbg_add(key_bounds, pool->num_slots / pool->block_size * H * 4 * D, "key_bounds");
   dbg_add(dev_status, 4, "status");
-  return launched(launch_append(p, v8, reinterpret_cast<cudaStream_t>(stream)));
+  return launched(launch_append(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 KVQ_API size_t kvq_select_blocks_workspace(int32_t num_tokens, int32_t num_heads, int32_t max_seq_len, int32_t block_size) {

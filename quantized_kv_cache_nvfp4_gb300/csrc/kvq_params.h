@@ -202,7 +202,7 @@ struct AppendTensor {
 struct AppendParams {
   AppendTensor ten[2];
   int32_t ntensors;         // 0 to 2
-  int32_t T, H, nb;         // tokens, KV heads, D / 16
+  int32_t T, H, D;          // tokens, KV heads, head_dim
   const int64_t* slot_ids;  // [T]
   int64_t num_slots;
   int32_t block_size;
@@ -222,7 +222,7 @@ struct AppendParams {
   int32_t q_heads, q_parts; // heads of a token that one warp turns, and how many such parts it has,
   int64_t row_blocks;       // thread blocks of K and V; those behind turn Q
 };
-cudaError_t launch_append(const AppendParams& p, bool v8, cudaStream_t s);
+cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // Blocks of the highest score bounds.
