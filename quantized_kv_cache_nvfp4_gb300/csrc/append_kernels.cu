@@ -10,14 +10,14 @@
 // would round twice.  Q' is rounded to bf16 once.  The bounds of (block, head) are the least
 // and the largest bf16(K') of its rows, channel by channel.
 //
-// Mapping: rows of one page that stand next to each other in slot_ids form a run; one warp
-// serves (run, head, tensor), so scales and bounds need no atomics.  L = D / 8 lanes (rounded up to a
-// power of two; at most 32, with two chunks each above head_dim 256) hold 8 channels of a row each,
-// 32 / L rows a pass, kBatch passes' loads in flight; halves of a pair in different lanes meet by shuffles.
-// Pages up to kBatch passes stay in registers, as they came, between the maximum and the codes
-// (page scales), larger ones are read twice; both turn K twice.  Neighbouring warps take the heads of the
-// same tokens, so a token's angles come from L1 but once.  Behind those blocks of the grid, others
-// turn Q: a warp holds a token's angles in registers and walks its heads.
+// Mapping: rows of one page that stand next to each other in slot_ids form a run; one warp serves
+// (run, head, tensor), so scales and bounds need no atomics.  A thread block looks the runs of a chunk of
+// tokens up once and shares them, heads fastest, among its warps.  D / 16 lanes (rounded up to a power of
+// two) hold a row, 8 channels of a half and their partners of the other half each, so that pairs need no
+// exchange and share their angles; 32 / lanes rows a pass, the next pass's loads in flight.  Page scales need
+// the maximum before the codes, and read (from L2) and turn the rows twice: kept in unrolled registers
+// the code outgrew the instruction cache.  Behind those blocks of the grid, others turn Q: a warp
+// holds a token's angles in registers and walks its heads.
 #include "page_scale.cuh"
 #include "kvq_params.h"
 
@@ -25,88 +25,94 @@ namespace kvq {
 
 namespace {
 
-constexpr int kAppendThreads = 128;
+constexpr int kAppendWarps = 8;
+constexpr int kChunk = 32;  // most tokens of a block
 
-// What a lane does for its chunk ch of 8 channels: where the chunk's first angle stands (-1: not turned),
-// and, with pairs rot / 2 apart, where the partner chunk is and whether this one holds the b of its pairs.
-struct Turn {
-  int at, lane, slot;
-  bool second;
+// The two 8-channel chunks of a lane: c and c + half of the turned channels where those are rot / 2 apart
+// (half chunks each), else neighbours.  at: the first angle of each (-1: not turned).
+struct Lane {
+  int ch[2], at[2];
+  bool act;    // the lane has channels
+  bool apart;  // ch[0] and ch[1] are partners
 };
-__device__ __forceinline__ Turn make_turn(int rot, bool pairs, int ch, int base) {
-  const int half = rot / 16;  // chunks of a half
-  Turn t;
-  const bool in = ch < 2 * half;
-  t.second = !pairs && in && ch >= half;
-  const int partner = pairs || !in ? ch : (t.second ? ch - half : ch + half);
-  t.lane = base + partner % 32;
-  t.slot = partner / 32;
-  t.at = !in ? -1 : pairs ? 4 * ch : 8 * (t.second ? ch - half : ch);
-  return t;
+__device__ __forceinline__ Lane make_lane(int rot, bool pairs, int li, int D) {
+  const int half = pairs ? 0 : rot / 16;
+  Lane l;
+  l.act = 16 * li < D;
+  l.apart = li < half;
+  l.ch[0] = l.apart ? li : 2 * li;
+  l.ch[1] = l.apart ? li + half : 2 * li + 1;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) l.at[j] = pairs ? (8 * l.ch[j] < rot ? 4 * l.ch[j] : -1) : l.apart ? 8 * li : -1;
+  return l;
 }
 
-// Cosines and signed sines of the chunk as pairs of neighbouring channels: y = x c + p s with p the
-// partner channel, s negative where the channel is the a of its pair.
+// Angles of the lane at a position, from its row of the table: apart, 8 cosines and 8 sines for both
+// chunks; neighbours, 4 and 4 for each.
 struct Angles {
-  uint64_t c[4], s[4];
+  uint4 c[2], s[2];
 };
-__device__ __forceinline__ void load_angles(const Turn& t, int rot, bool pairs, const float* row, Angles& a) {
-  if (t.at < 0) return;
-  const uint4* const c = reinterpret_cast<const uint4*>(row + t.at);
-  const uint4* const s = reinterpret_cast<const uint4*>(row + rot / 2 + t.at);
-  if (pairs) {
-    const uint4 u = LDX(c), v = LDX(s);
-    constexpr uint32_t kNeg = 0x80000000u;
-    a.c[0] = pack_f32x2(u.x, u.x), a.c[1] = pack_f32x2(u.y, u.y), a.c[2] = pack_f32x2(u.z, u.z), a.c[3] = pack_f32x2(u.w, u.w);
-    a.s[0] = pack_f32x2(v.x ^ kNeg, v.x), a.s[1] = pack_f32x2(v.y ^ kNeg, v.y);
-    a.s[2] = pack_f32x2(v.z ^ kNeg, v.z), a.s[3] = pack_f32x2(v.w ^ kNeg, v.w);
-  } else {
-    const uint4 u0 = LDX(c), u1 = LDX(c + 1), v0 = LDX(s), v1 = LDX(s + 1);
-    const uint32_t n = t.second ? 0u : 0x80000000u;
-    a.c[0] = pack_f32x2(u0.x, u0.y), a.c[1] = pack_f32x2(u0.z, u0.w), a.c[2] = pack_f32x2(u1.x, u1.y), a.c[3] = pack_f32x2(u1.z, u1.w);
-    a.s[0] = pack_f32x2(v0.x ^ n, v0.y ^ n), a.s[1] = pack_f32x2(v0.z ^ n, v0.w ^ n);
-    a.s[2] = pack_f32x2(v1.x ^ n, v1.y ^ n), a.s[3] = pack_f32x2(v1.z ^ n, v1.w ^ n);
+__device__ __forceinline__ void load_angles(const Lane& l, int rot, bool pairs, const float* row, Angles& a) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int at = pairs ? l.at[j] : l.at[0] + 4 * j;
+    if (l.at[pairs ? j : 0] < 0) continue;
+    a.c[j] = LDX(reinterpret_cast<const uint4*>(row + at));
+    a.s[j] = LDX(reinterpret_cast<const uint4*>(row + rot / 2 + at));
   }
 }
 
-// The lane's chunks in binary32, turned.  Every lane of the warp takes part (rot: uniform, 0 for none).
-template <int C>
-__device__ __forceinline__ void turn8(const Turn (&t)[C], const Angles (&a)[C], int rot, bool pairs, const uint32_t (&w)[C][4],
-                                      float (&y)[C][8]) {
+// Products and sums one rounding each: packed products, single sums (a packed sum of packed products comes
+// out as one rounding).
+__device__ __forceinline__ void mul2(float a0, float a1, uint32_t b0, uint32_t b1, float& r0, float& r1) {
+  uint32_t u, v;
+  unpack_f32x2(mul_f32x2(pack_f32x2(__float_as_uint(a0), __float_as_uint(a1)), pack_f32x2(b0, b1)), u, v);
+  r0 = __uint_as_float(u);
+  r1 = __uint_as_float(v);
+}
+
+// The lane's 16 channels in binary32, turned (rot: uniform, 0 for none).
+__device__ __forceinline__ void turn16(const Lane& l, const Angles& a, int rot, bool pairs, const uint32_t (&w)[2][4],
+                                       float (&y)[2][8]) {
 #pragma unroll
-  for (int j = 0; j < C; ++j)
+  for (int j = 0; j < 2; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       y[j][2 * i] = bf16lo(w[j][i]);
       y[j][2 * i + 1] = bf16hi(w[j][i]);
     }
   if (rot == 0) return;
+  if (pairs) {
 #pragma unroll
-  for (int j = 0; j < C; ++j) {
-    uint32_t o[4];
+    for (int j = 0; j < 2; ++j) {
+      if (l.at[j] < 0) continue;
+      const uint32_t c[4] = {a.c[j].x, a.c[j].y, a.c[j].z, a.c[j].w}, s[4] = {a.s[j].x, a.s[j].y, a.s[j].z, a.s[j].w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (pairs) {
-        o[i] = __byte_perm(w[j][i], 0u, 0x1032);  // the neighbour
-      } else {
-        o[i] = __shfl_sync(0xFFFFFFFFu, w[0][i], t[j].lane);
-        if constexpr (C == 2) {
-          const uint32_t o2 = __shfl_sync(0xFFFFFFFFu, w[1][i], t[j].lane);
-          o[i] = t[j].slot != 0 ? o2 : o[i];
-        }
+      for (int i = 0; i < 4; ++i) {
+        float ac, bc, as, bs;
+        mul2(y[j][2 * i], y[j][2 * i + 1], c[i], c[i], ac, bc);
+        mul2(y[j][2 * i], y[j][2 * i + 1], s[i], s[i], as, bs);
+        y[j][2 * i] = __fsub_rn(ac, bs);
+        y[j][2 * i + 1] = __fadd_rn(bc, as);
       }
     }
-    if (t[j].at < 0) continue;
+  } else if (l.apart) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint64_t x = pack_f32x2(__float_as_uint(y[j][2 * i]), __float_as_uint(y[j][2 * i + 1]));
-      const uint64_t p = pack_f32x2(o[i] << 16, o[i] & 0xFFFF0000u);
-      // the sums one by one: the packed sum of packed products came out as one rounding
-      uint32_t m0, m1, n0, n1;
-      unpack_f32x2(mul_f32x2(x, a[j].c[i]), m0, m1);
-      unpack_f32x2(mul_f32x2(p, a[j].s[i]), n0, n1);
-      y[j][2 * i] = __fadd_rn(__uint_as_float(m0), __uint_as_float(n0));
-      y[j][2 * i + 1] = __fadd_rn(__uint_as_float(m1), __uint_as_float(n1));
+    for (int j = 0; j < 2; ++j) {  // channels 4 j .. 4 j + 3 of both chunks
+      const uint32_t c[4] = {a.c[j].x, a.c[j].y, a.c[j].z, a.c[j].w}, s[4] = {a.s[j].x, a.s[j].y, a.s[j].z, a.s[j].w};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float &a0 = y[0][4 * j + 2 * i], &a1 = y[0][4 * j + 2 * i + 1], &b0 = y[1][4 * j + 2 * i], &b1 = y[1][4 * j + 2 * i + 1];
+        float ac0, ac1, as0, as1, bc0, bc1, bs0, bs1;
+        mul2(a0, a1, c[2 * i], c[2 * i + 1], ac0, ac1);
+        mul2(a0, a1, s[2 * i], s[2 * i + 1], as0, as1);
+        mul2(b0, b1, c[2 * i], c[2 * i + 1], bc0, bc1);
+        mul2(b0, b1, s[2 * i], s[2 * i + 1], bs0, bs1);
+        a0 = __fsub_rn(ac0, bs0);
+        a1 = __fsub_rn(ac1, bs1);
+        b0 = __fadd_rn(bc0, as0);
+        b1 = __fadd_rn(bc1, as1);
+      }
     }
   }
 }
@@ -118,31 +124,45 @@ __device__ __forceinline__ float absmax8(const float (&y)[8]) {
   return m;
 }
 
-// quantize_block and fp8_quantize16 (kvq_device.cuh) of 8 binary32 values.
-__device__ __forceinline__ uint32_t quantize8(const float (&y)[8], float s) {
-  const float inv = (s != 0.0f) ? __frcp_rn(s) : 0.0f;
+// quantize_block and fp8_quantize16 (kvq_device.cuh) of 8 binary32 values; inv = 1 / s (0 when s is 0).
+__device__ __forceinline__ float inverse(float s) { return (s != 0.0f) ? __frcp_rn(s) : 0.0f; }
+__device__ __forceinline__ uint32_t quantize8(const float (&y)[8], float s, float inv) {
   uint32_t byte[4];
   if (!isinf(inv)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) byte[i] = e2m1x2_from_f32(__fmul_rn(y[2 * i], inv), __fmul_rn(y[2 * i + 1], inv));
+    for (int i = 0; i < 4; ++i) {
+      float q0, q1;
+      mul2(y[2 * i], y[2 * i + 1], __float_as_uint(inv), __float_as_uint(inv), q0, q1);
+      byte[i] = e2m1x2_from_f32(q0, q1);
+    }
   } else {  // the reciprocal overflowed, divide directly
-#pragma unroll
-    for (int i = 0; i < 4; ++i) byte[i] = e2m1x2_from_f32(__fdiv_rn(y[2 * i], s), __fdiv_rn(y[2 * i + 1], s));
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      const float a = i == 0 ? y[0] : i == 1 ? y[2] : i == 2 ? y[4] : y[6], b = i == 0 ? y[1] : i == 1 ? y[3] : i == 2 ? y[5] : y[7];
+      const uint32_t v = e2m1x2_from_f32(__fdiv_rn(a, s), __fdiv_rn(b, s));
+      byte[0] = i == 0 ? v : byte[0], byte[1] = i == 1 ? v : byte[1], byte[2] = i == 2 ? v : byte[2], byte[3] = i == 3 ? v : byte[3];
+    }
   }
   return bytes4(byte[0], byte[1], byte[2], byte[3]);
 }
-__device__ __forceinline__ void fp8_quantize8(const float (&y)[8], float rs, uint32_t& c0, uint32_t& c1) {
-  const float inv = (rs != 0.0f) ? __frcp_rn(rs) : 0.0f;
+__device__ __forceinline__ uint2 fp8_quantize8(const float (&y)[8], float s, float inv) {
   uint32_t w[4];
   if (!isinf(inv)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = e4m3x2_from_f32(__fmul_rn(y[2 * i], inv), __fmul_rn(y[2 * i + 1], inv));
+    for (int i = 0; i < 4; ++i) {
+      float q0, q1;
+      mul2(y[2 * i], y[2 * i + 1], __float_as_uint(inv), __float_as_uint(inv), q0, q1);
+      w[i] = e4m3x2_from_f32(q0, q1);
+    }
   } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = e4m3x2_from_f32(__fdiv_rn(y[2 * i], rs), __fdiv_rn(y[2 * i + 1], rs));
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      const float a = i == 0 ? y[0] : i == 1 ? y[2] : i == 2 ? y[4] : y[6], b = i == 0 ? y[1] : i == 1 ? y[3] : i == 2 ? y[5] : y[7];
+      const uint32_t v = e4m3x2_from_f32(__fdiv_rn(a, s), __fdiv_rn(b, s));
+      w[0] = i == 0 ? v : w[0], w[1] = i == 1 ? v : w[1], w[2] = i == 2 ? v : w[2], w[3] = i == 3 ? v : w[3];
+    }
   }
-  c0 = w[0] | w[1] << 16;
-  c1 = w[2] | w[3] << 16;
+  return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
 // bf16 minima and maxima of packed pairs (a NaN loses against a number).
@@ -157,269 +177,267 @@ __device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
   return r;
 }
 
-// 16 bytes that this launch reads once, or (rw) may write too.
-__device__ __forceinline__ void load_row16(const void* p, uint32_t (&w)[4]) {
-  if (!KVQ_OK(p, 16, 16)) {
-    w[0] = w[1] = w[2] = w[3] = 0u;
-    return;
-  }
-  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-               : "l"(p));
-}
-
-// Slot of token t: -1 where it is skipped.  `report`: the warp that speaks for the token.
-__device__ __forceinline__ int64_t append_slot(const AppendParams& p, int64_t t, bool report) {
+// Slot of token t: -1 where it is skipped.  `report`: the block that speaks for the token.
+__device__ __forceinline__ int64_t append_slot(const AppendParams& p, int64_t t, bool report, int& pos) {
+  pos = 0;
   if (t < 0 || t >= p.T) return -1;
   const int64_t s = LDX(p.slot_ids + t);
   if (s >= p.num_slots && report) set_status(p.status, 1u);
   if (p.cos_sin != nullptr) {
-    const int32_t pos = LDX(p.positions + t);
+    pos = LDX(p.positions + t);
     if (pos >= p.num_positions && report) set_status(p.status, 4u);
     if (pos < 0 || pos >= p.num_positions) return -1;
   }
   return s >= p.num_slots ? -1 : s;
 }
 
-template <int L, int C>
-__device__ __forceinline__ void append_rows(const AppendParams& p, int64_t w) {
-  constexpr int R = 32 / L;       // rows per pass
-  constexpr int kBatch = 8 / C;
+// The runs that begin in a chunk of tokens, and the chunk's tokens.
+struct Chunk {
+  int64_t page[kChunk];  // of a run
+  int start[kChunk];     // its first token, from the chunk's
+  int length[kChunk];
+  bool begins[kChunk];   // holds the page's first slot
+  int place[kChunk];     // of a token in its page
+  int pos[kChunk];
+  int runs;
+};
+__device__ __forceinline__ void find_runs(const AppendParams& p, int64_t t0, bool report, Chunk& ck) {  // one warp
   const int lane = threadIdx.x & 31;
-  const int li = lane % L, sub = lane / L;
-  const int per = p.H * p.ntensors;
-  const int64_t ci = w / per;
-  const int rem = static_cast<int>(w - ci * per);
-  const int tensor = rem / p.H, h = rem - tensor * p.H;
-  const int64_t t0 = ci * p.chunk;
-  if (t0 >= p.T) return;
-  const AppendTensor ten = p.ten[tensor];
-  const int rot = ten.key && p.cos_sin != nullptr ? p.rot : 0;
-  const int D = p.D;
-  uint16_t* const bounds = ten.key ? p.bounds : nullptr;
-  Turn turn[C];
-  bool act[C];
-#pragma unroll
-  for (int j = 0; j < C; ++j) {
-    turn[j] = make_turn(rot, p.pairs, li + 32 * j, lane - li);
-    act[j] = 8 * (li + 32 * j) < D;
-  }
-
-  auto page_of = [&](int64_t slot) -> int64_t { return slot < 0 ? -1 : slot / p.block_size; };
-  const int64_t slot = append_slot(p, t0 + lane, rem == 0);
-  const int64_t before = lane == 0 ? page_of(append_slot(p, t0 - 1, false)) : -1;
+  auto page_of = [&](int64_t slot) -> int64_t {
+    return slot < 0 ? -1 : p.small ? static_cast<int64_t>(p.div_bs.div(static_cast<uint32_t>(slot))) : slot / p.block_size;
+  };
+  int pos, unused;
+  const int64_t slot = append_slot(p, t0 + lane, report, pos);
   const int64_t page = page_of(slot);
+  const int64_t before = lane == 0 ? page_of(append_slot(p, t0 - 1, false, unused)) : -1;
   int64_t prev = __shfl_up_sync(0xFFFFFFFFu, page, 1);
   if (lane == 0) prev = before;
-  uint32_t leaders = __ballot_sync(0xFFFFFFFFu, lane < p.chunk && page >= 0 && page != prev);
-  const uint32_t firsts = __ballot_sync(0xFFFFFFFFu, page >= 0 && slot - page * p.block_size == 0);
-
-  while (leaders != 0u) {
-    const int b = __ffs(leaders) - 1;
-    leaders &= leaders - 1;
-    const int64_t pg = __shfl_sync(0xFFFFFFFFu, page, b);
-    const int64_t ts = t0 + b;
-    // run length, and whether it holds the page's first slot
-    int n = run_bits(__ballot_sync(0xFFFFFFFFu, page == pg) >> b);  // zeros come in from the top
-    bool begins = ((firsts >> b) & (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u)) != 0u;
-    if (b + n == 32) {
-      for (int64_t t = t0 + 32; t < p.T; t += 32) {
-        const int64_t s2 = append_slot(p, t + lane, false);
-        const int64_t p2 = page_of(s2);
-        const int m = run_bits(__ballot_sync(0xFFFFFFFFu, p2 == pg));
-        begins = begins || __any_sync(0xFFFFFFFFu, lane < m && s2 == pg * p.block_size);
-        n += m;
-        if (m < 32) break;
-      }
+  const int place = page < 0 ? 0 : static_cast<int>(slot - page * p.block_size);
+  ck.place[lane] = place;
+  ck.pos[lane] = pos;
+  const uint32_t leaders = __ballot_sync(0xFFFFFFFFu, lane < p.chunk && page >= 0 && page != prev);
+  const uint32_t same = __ballot_sync(0xFFFFFFFFu, page >= 0 && page == prev);  // goes on with the token before
+  const uint32_t firsts = __ballot_sync(0xFFFFFFFFu, page >= 0 && place == 0);
+  if ((leaders >> lane) & 1u) {
+    const int n = 1 + (lane == 31 ? 0 : run_bits(same >> (lane + 1)));
+    const int at = __popc(leaders & ((1u << lane) - 1u));
+    ck.page[at] = page;
+    ck.start[at] = lane;
+    ck.length[at] = min(n, 32 - lane);
+    ck.begins[at] = ((firsts >> lane) & (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u)) != 0u;
+  }
+  if (lane == 0) ck.runs = __popc(leaders);
+  __syncwarp();
+  if (leaders == 0u) return;
+  // the last run may go on behind the 32 tokens
+  const int last = __popc(leaders) - 1, b = 31 - __clz(leaders);
+  const int64_t pg = __shfl_sync(0xFFFFFFFFu, page, b);
+  if (b + ck.length[last] == 32) {
+    int n = ck.length[last];
+    bool begins = ck.begins[last];
+    for (int64_t t = t0 + 32; t < p.T; t += 32) {
+      const int64_t s2 = append_slot(p, t + lane, false, unused);
+      const int64_t p2 = page_of(s2);
+      const int m = run_bits(__ballot_sync(0xFFFFFFFFu, p2 == pg));
+      begins = begins || __any_sync(0xFFFFFFFFu, lane < m && s2 == pg * p.block_size);
+      n += m;
+      if (m < 32) break;
     }
-    const bool paged = ten.fmt == 5;
-    const int64_t prow = pg * p.H + h;
-    float s0 = 0.0f;
-    if (paged && !begins && lane == 0) s0 = LDX(ten.dst.rscale + prow);
-    s0 = __shfl_sync(0xFFFFFFFFu, s0, 0);
-    const uint16_t* const x = ten.x + ts * ten.row_pitch + h * ten.head_pitch + 8 * li;
-
-    uint32_t raw[kBatch][C][4];
-    auto load = [&](int r, uint32_t (&v)[C][4]) {
-#pragma unroll
-      for (int j = 0; j < C; ++j) {
-        v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0u;
-        if (act[j] && r < n) load_row16(x + r * ten.row_pitch + 256 * j, v[j]);
-      }
-    };
-    auto turned = [&](int r, const uint32_t (&v)[C][4], float (&y)[C][8]) {
-      Angles a[C];
-      if (rot != 0 && r < n) {
-        const float* const row = p.cos_sin + static_cast<int64_t>(LDX(p.positions + ts + r)) * rot;
-#pragma unroll
-        for (int j = 0; j < C; ++j) load_angles(turn[j], rot, p.pairs, row, a[j]);
-      }
-      turn8<C>(turn, a, rot, p.pairs, v, y);
-    };
-    auto row_of = [&](int r) -> int64_t { return LDX(p.slot_ids + ts + r) * p.H + h; };
-
-    uint32_t lo[C][4], hi[C][4];
-#pragma unroll
-    for (int j = 0; j < C; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lo[j][i] = 0x7F807F80u;
-        hi[j][i] = 0xFF80FF80u;
-      }
-    float am = 0.0f;
-    for (int k0 = 0; k0 * R < n; k0 += kBatch) {  // uniform
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) load((k0 + k) * R + sub, raw[k]);
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int r = (k0 + k) * R + sub;
-        if ((k0 + k) * R >= n) break;  // uniform
-        float y[C][8];
-        turned(r, raw[k], y);
-        if (bounds != nullptr && r < n) {
-#pragma unroll
-          for (int j = 0; j < C; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t b2 = pack_bf16x2(y[j][2 * i], y[j][2 * i + 1]);
-              lo[j][i] = bf16x2_min(lo[j][i], b2);
-              hi[j][i] = bf16x2_max(hi[j][i], b2);
-            }
-        }
-        float vb[C];  // 0 in lanes without a row
-        float row_max = 0.0f;
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-          vb[j] = absmax8(y[j]);
-          row_max = fmaxf(row_max, vb[j]);
-        }
-        if (paged) {
-          am = fmaxf(am, row_max);
-          continue;
-        }
-        const float amax = group_max<L>(row_max);
-        if (ten.fmt == 3) {
-          const float rs = __fdiv_rn(amax, kE4M3Max);
-          const int64_t row = r < n ? row_of(r) : 0;
-#pragma unroll
-          for (int j = 0; j < C; ++j) {
-            uint32_t c0, c1;
-            fp8_quantize8(y[j], rs, c0, c1);
-            if (act[j] && r < n) store8B(ten.dst.codes + row * D + 8 * (li + 32 * j), c0, c1);
-          }
-          if (li == 0 && r < n) STX(ten.dst.rscale + row, rs);
-        } else {
-          const float rs = __fdiv_rn(amax, kE2M1Max * kE4M3Max);
-          const float rinv = (rs != 0.0f) ? __frcp_rn(rs) : 0.0f;
-          const int64_t row = r < n ? row_of(r) : 0;
-#pragma unroll
-          for (int j = 0; j < C; ++j) {
-            const float block = fmaxf(vb[j], __shfl_xor_sync(0xFFFFFFFFu, vb[j], 1));
-            const uint32_t bsb = block_scale_code(block, rs, rinv);
-            const uint32_t c = quantize8(y[j], __fmul_rn(e4m3_to_f32(bsb), rs));
-            if (act[j] && r < n) {
-              const int ch = li + 32 * j;
-              STX(reinterpret_cast<uint32_t*>(ten.dst.codes + row * (D / 2)) + ch, c);
-              if (ch % 2 == 0) STX(ten.dst.bscale + row * (D / 16) + ch / 2, static_cast<uint8_t>(bsb));
-            }
-          }
-          if (li == 0 && r < n) STX(ten.dst.rscale + row, rs);
-        }
-      }
-    }
-
-    if (bounds != nullptr) {
-#pragma unroll
-      for (int j = 0; j < C; ++j) {
-#pragma unroll
-        for (int o = L; o < 32; o <<= 1)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            lo[j][i] = bf16x2_min(lo[j][i], __shfl_xor_sync(0xFFFFFFFFu, lo[j][i], o));
-            hi[j][i] = bf16x2_max(hi[j][i], __shfl_xor_sync(0xFFFFFFFFu, hi[j][i], o));
-          }
-        if (act[j] && sub == 0) {
-          uint16_t* const at = bounds + prow * 2 * D + 8 * (li + 32 * j);
-          if (!begins) {
-            uint32_t was[4];
-            load16B_rw(at, was);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) lo[j][i] = bf16x2_min(lo[j][i], was[i]);
-            load16B_rw(at + D, was);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) hi[j][i] = bf16x2_max(hi[j][i], was[i]);
-          }
-          store16B(at, lo[j]);
-          store16B(at + D, hi[j]);
-        }
-      }
-    }
-    if (!paged) continue;
-
-    am = group_max<32>(am);
-    if (am > 3.4028235e38f) {  // an infinity among them, the same in all lanes: once more without
-      am = 0.0f;
-      for (int k = 0; k * R < n; ++k) {
-        const int r = k * R + sub;
-        uint32_t v[C][4];
-        float y[C][8];
-        load(r, v);
-        turned(r, v, y);
-#pragma unroll
-        for (int j = 0; j < C; ++j)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) am = fmaxf(am, fabsf(y[j][i]) <= 3.4028235e38f ? fabsf(y[j][i]) : 0.0f);
-      }
-      am = group_max<32>(am);
-    }
-    if (!(s0 > 0.0f && s0 <= 3.4028235e38f)) s0 = 0.0f;  // no scale stored yet
-    const float s = fmaxf(s0, page_scale_need(am));
-    const int64_t cpitch = static_cast<int64_t>(p.H) * D;
-    if (s0 > 0.0f && s > s0) {  // the rows that the page holds, under the new scale
-      const float f = __fdiv_rn(s0, s);
-      uint8_t* const cp = ten.dst.codes + (pg * p.block_size * p.H + h) * D;
-      const int each = D / 16;  // 16-byte pieces of a row
-      for (int at = lane; at < p.block_size * each; at += 32) {
-        uint8_t* const to = cp + (at / each) * cpitch + 16 * (at % each);
-        uint32_t c[4];
-        load16B_rw(to, c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = rescale4(c[i], f);
-        store16B(to, c);
-      }
-      __syncwarp();  // before the call's own rows go over them
-    }
-    if (lane == 0 && s != s0) STX(ten.dst.rscale + prow, s);
-    const bool kept = n <= kBatch * R;  // in raw
-    for (int k0 = 0; k0 * R < n; k0 += kBatch) {
-      if (!kept) {
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) load((k0 + k) * R + sub, raw[k]);
-      }
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int r = (k0 + k) * R + sub;
-        if ((k0 + k) * R >= n) break;  // uniform
-        float y[C][8];
-        turned(r, raw[k], y);
-        if (r >= n) continue;
-        const int64_t row = row_of(r);
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-          uint32_t c0, c1;
-          fp8_quantize8(y[j], s, c0, c1);
-          if (act[j]) store8B(ten.dst.codes + row * D + 8 * (li + 32 * j), c0, c1);
-        }
-      }
+    __syncwarp();
+    if (lane == 0) {
+      ck.length[last] = n;
+      ck.begins[last] = begins;
     }
   }
 }
 
+template <int L>
+__device__ __forceinline__ void append_run(const AppendParams& p, const Chunk& ck, int64_t t0, int run, int tensor, int h) {
+  constexpr int R = 32 / L;  // rows per pass
+  const int lane = threadIdx.x & 31, li = lane % L, sub = lane / L;
+  const AppendTensor& ten = p.ten[tensor];
+  const int rot = ten.key && p.cos_sin != nullptr ? p.rot : 0;
+  const int D = p.D, n = ck.length[run], b = ck.start[run];
+  const int64_t pg = ck.page[run], prow = pg * p.H + h;
+  const bool begins = ck.begins[run], paged = ten.fmt == 5;
+  uint16_t* const bounds = ten.key ? p.bounds : nullptr;
+  const Lane ln = make_lane(rot, p.pairs, li, D);
+  float s0 = 0.0f;
+  if (paged && !begins && lane == 0) s0 = LDX(ten.dst.rscale + prow);
+  s0 = __shfl_sync(0xFFFFFFFFu, s0, 0);
+  const uint16_t* const x = ten.x + (t0 + b) * ten.row_pitch + h * ten.head_pitch;
+  const int64_t row0 = pg * p.block_size;
+
+  auto load = [&](int r, uint32_t (&v)[2][4]) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0u;
+      if (ln.act && r < n) load16B(x + r * ten.row_pitch + 8 * ln.ch[j], v[j]);
+    }
+  };
+  // the rows, turned, with whether the lane has one and the pool's number of it
+  auto each_row = [&](auto&& f) {
+    uint32_t next[2][4];
+    load(sub, next);
+#pragma unroll 1
+    for (int r0 = 0; r0 < n; r0 += R) {
+      const int r = r0 + sub;
+      int at, pos;
+      if (b + r < kChunk) {
+        at = ck.place[b + r];
+        pos = ck.pos[b + r];
+      } else {
+        at = r < n ? static_cast<int>(LDX(p.slot_ids + t0 + b + r) - row0) : 0;
+        pos = rot != 0 && r < n ? LDX(p.positions + t0 + b + r) : 0;
+      }
+      Angles a;
+      if (rot != 0 && r < n) load_angles(ln, rot, p.pairs, p.cos_sin + static_cast<int64_t>(pos) * rot, a);
+      uint32_t v[2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] = next[j][i];
+      load(r + R, next);
+      float y[2][8];
+      turn16(ln, a, rot, p.pairs, v, y);
+      f(y, r < n, (row0 + at) * p.H + h);
+    }
+  };
+
+  uint32_t lo[2][4], hi[2][4];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo[j][i] = 0x7F807F80u;
+      hi[j][i] = 0xFF80FF80u;
+    }
+  float am = 0.0f;
+  each_row([&](const float (&y)[2][8], bool live, int64_t row) {
+    if (bounds != nullptr && live) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t b2 = pack_bf16x2(y[j][2 * i], y[j][2 * i + 1]);
+          lo[j][i] = bf16x2_min(lo[j][i], b2);
+          hi[j][i] = bf16x2_max(hi[j][i], b2);
+        }
+    }
+    const float vb[2] = {absmax8(y[0]), absmax8(y[1])};  // 0 in lanes without a row
+    if (paged) {
+      am = fmaxf(am, fmaxf(vb[0], vb[1]));
+      return;
+    }
+    const float amax = group_max<L>(fmaxf(vb[0], vb[1]));
+    const float rs = __fdiv_rn(amax, ten.fmt == 3 ? kE4M3Max : kE2M1Max * kE4M3Max);
+    const float rinv = inverse(rs);
+    live = live && ln.act;
+    if (ten.fmt == 3) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint2 c = fp8_quantize8(y[j], rs, rinv);
+        if (live) store8B(ten.dst.codes + row * D + 8 * ln.ch[j], c.x, c.y);
+      }
+    } else {
+      // a block of 16 is chunks 2 k and 2 k + 1: the other one's lane and place there
+      float other[2] = {vb[1], vb[0]};
+      if (rot != 0 && !p.pairs) {  // uniform
+        const int half = rot / 16, base = lane - li;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int c = ln.ch[j] ^ 1;
+          const int src = c < half ? c : c < 2 * half ? c - half : c / 2;
+          const float o0 = __shfl_sync(0xFFFFFFFFu, vb[0], base + src % L), o1 = __shfl_sync(0xFFFFFFFFu, vb[1], base + src % L);
+          other[j] = (c < half ? 0 : c < 2 * half ? 1 : c % 2) == 0 ? o0 : o1;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t bsb = block_scale_code(fmaxf(vb[j], other[j]), rs, rinv);
+        const float s = __fmul_rn(e4m3_to_f32(bsb), rs);
+        const uint32_t c = quantize8(y[j], s, inverse(s));
+        if (live) {
+          STX(reinterpret_cast<uint32_t*>(ten.dst.codes + row * (D / 2)) + ln.ch[j], c);
+          if (ln.ch[j] % 2 == 0) STX(ten.dst.bscale + row * (D / 16) + ln.ch[j] / 2, static_cast<uint8_t>(bsb));
+        }
+      }
+    }
+    if (li == 0 && live) STX(ten.dst.rscale + row, rs);
+  });
+
+  if (bounds != nullptr) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int o = L; o < 32; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          lo[j][i] = bf16x2_min(lo[j][i], __shfl_xor_sync(0xFFFFFFFFu, lo[j][i], o));
+          hi[j][i] = bf16x2_max(hi[j][i], __shfl_xor_sync(0xFFFFFFFFu, hi[j][i], o));
+        }
+      if (ln.act && sub == 0) {
+        uint16_t* const at = bounds + prow * 2 * D + 8 * ln.ch[j];
+        if (!begins) {
+          uint32_t was[4];
+          load16B_rw(at, was);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) lo[j][i] = bf16x2_min(lo[j][i], was[i]);
+          load16B_rw(at + D, was);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) hi[j][i] = bf16x2_max(hi[j][i], was[i]);
+        }
+        store16B(at, lo[j]);
+        store16B(at + D, hi[j]);
+      }
+    }
+  }
+  if (!paged) return;
+
+  am = group_max<32>(am);
+  if (am > 3.4028235e38f) {  // an infinity among them, the same in all lanes: once more without
+    am = 0.0f;
+    each_row([&](const float (&y)[2][8], bool, int64_t) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) am = fmaxf(am, fabsf(y[j][i]) <= 3.4028235e38f ? fabsf(y[j][i]) : 0.0f);
+    });
+    am = group_max<32>(am);
+  }
+  if (!(s0 > 0.0f && s0 <= 3.4028235e38f)) s0 = 0.0f;  // no scale stored yet
+  const float s = fmaxf(s0, page_scale_need(am));
+  if (s0 > 0.0f && s > s0) {  // the rows that the page holds, under the new scale
+    const float f = __fdiv_rn(s0, s);
+    uint8_t* const cp = ten.dst.codes + (row0 * p.H + h) * D;
+    const int64_t cpitch = static_cast<int64_t>(p.H) * D;
+    const int each = D / 16;  // 16-byte pieces of a row
+    for (int at = lane; at < p.block_size * each; at += 32) {
+      uint8_t* const to = cp + (at / each) * cpitch + 16 * (at % each);
+      uint32_t c[4];
+      load16B_rw(to, c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i] = rescale4(c[i], f);
+      store16B(to, c);
+    }
+    __syncwarp();  // before the call's own rows go over them
+  }
+  if (lane == 0 && s != s0) STX(ten.dst.rscale + prow, s);
+  const float inv = inverse(s);
+  each_row([&](const float (&y)[2][8], bool live, int64_t row) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint2 c = fp8_quantize8(y[j], s, inv);
+      if (live && ln.act) store8B(ten.dst.codes + row * D + 8 * ln.ch[j], c.x, c.y);
+    }
+  });
+}
+
 // Q: warp w takes heads first .. of one token, 32 / L at a time.
-template <int L, int C>
+template <int L>
 __device__ __forceinline__ void append_turn_q(const AppendParams& p, int64_t w) {
   constexpr int R = 32 / L;
-  constexpr int kBatch = 4 / C;
+  constexpr int kBatch = 2;
   const int lane = threadIdx.x & 31;
   const int li = lane % L, sub = lane / L;
   const int64_t t = w / p.q_parts;
@@ -431,95 +449,104 @@ __device__ __forceinline__ void append_turn_q(const AppendParams& p, int64_t w) 
     if (lane == 0 && first == 0) set_status(p.status, 4u);
     return;
   }
-  Turn turn[C];
-  Angles a[C];
-  bool act[C];
-#pragma unroll
-  for (int j = 0; j < C; ++j) {
-    turn[j] = make_turn(p.rot, p.pairs, li + 32 * j, lane - li);
-    act[j] = 8 * (li + 32 * j) < p.D;
-    load_angles(turn[j], p.rot, p.pairs, p.cos_sin + static_cast<int64_t>(pos) * p.rot, a[j]);
-  }
-  const uint16_t* const x = p.q + t * p.q_row_pitch + 8 * li;
-  uint16_t* const y_at = p.q_out + t * p.qo_row_pitch + 8 * li;
+  const Lane ln = make_lane(p.rot, p.pairs, li, p.D);
+  Angles a;
+  load_angles(ln, p.rot, p.pairs, p.cos_sin + static_cast<int64_t>(pos) * p.rot, a);
+  const uint16_t* const x = p.q + t * p.q_row_pitch;
+  uint16_t* const y_at = p.q_out + t * p.qo_row_pitch;
   const int end = min(first + p.q_heads, p.Hq);
+#pragma unroll 1
   for (int h0 = first; h0 < end; h0 += kBatch * R) {
-    uint32_t raw[kBatch][C][4];
+    uint32_t raw[kBatch][2][4];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int h = h0 + k * R + sub;
 #pragma unroll
-      for (int j = 0; j < C; ++j) {
-        raw[k][j][0] = raw[k][j][1] = raw[k][j][2] = raw[k][j][3] = 0u;
-        if (act[j] && h < end) load16B_rw(x + h * p.q_head_pitch + 256 * j, raw[k][j]);
-      }
+      for (int j = 0; j < 2; ++j)
+        if (ln.act && h < end) load16B_rw(x + h * p.q_head_pitch + 8 * ln.ch[j], raw[k][j]);
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int h = h0 + k * R + sub;
-      float y[C][8];
-      turn8<C>(turn, a, p.rot, p.pairs, raw[k], y);
+      if (!(ln.act && h < end)) continue;
+      float y[2][8];
+      turn16(ln, a, p.rot, p.pairs, raw[k], y);
 #pragma unroll
-      for (int j = 0; j < C; ++j) {
+      for (int j = 0; j < 2; ++j) {
         uint32_t o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(y[j][2 * i], y[j][2 * i + 1]);
-        if (act[j] && h < end) store16B(y_at + h * p.qo_head_pitch + 256 * j, o);
+        store16B(y_at + h * p.qo_head_pitch + 8 * ln.ch[j], o);
       }
     }
   }
 }
 
-template <int L, int C>
-__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendParams p) {
-  const int64_t warp = threadIdx.x >> 5;
+template <int L>
+__global__ void __launch_bounds__(32 * kAppendWarps, 3) append_kernel(const AppendParams p) {
+  __shared__ Chunk ck;
+  const int warp = threadIdx.x >> 5;
   const int64_t block = blockIdx.x;
-  if (block < p.row_blocks) {
-    append_rows<L, C>(p, block * (kAppendThreads / 32) + warp);
-  } else {
-    append_turn_q<L, C>(p, (block - p.row_blocks) * (kAppendThreads / 32) + warp);
+  if (block >= p.row_blocks) {
+    append_turn_q<L>(p, (block - p.row_blocks) * kAppendWarps + warp);
+    return;
+  }
+  const int64_t chunk = block / p.parts;
+  const int part = static_cast<int>(block - chunk * p.parts);
+  const int64_t t0 = chunk * p.chunk;
+  if (warp == 0) find_runs(p, t0, part == 0, ck);
+  __syncthreads();
+  const int per = p.H * p.ntensors, items = ck.runs * per;
+  for (int it = part * kAppendWarps + warp; it < items; it += p.parts * kAppendWarps) {
+    const int run = it / per, rem = it - run * per, tensor = rem / p.H;
+    append_run<L>(p, ck, t0, run, tensor, rem - tensor * p.H);
   }
 }
 
-template <int L, int C>
+template <int L>
 cudaError_t append_launch(const AppendParams& p_in, cudaStream_t s) {
   AppendParams p = p_in;
-  constexpr int kW = kAppendThreads / 32, R = 32 / L;
-  auto k = append_kernel<L, C>;
-  // tokens per warp: as many as leave 16 warps an SM (one token a warp in a decode step, whose
-  // runs are single rows; 32 in a prompt)
-  const int64_t rows = static_cast<int64_t>(p.T) * p.H * p.ntensors, fill = 16ll * num_sms();
-  p.chunk = 32;
-  while (p.chunk > 1 && rows < p.chunk * fill) p.chunk >>= 1;
-  const int64_t warps = (static_cast<int64_t>(p.T) + p.chunk - 1) / p.chunk * p.H * p.ntensors;
-  p.row_blocks = (warps + kW - 1) / kW;
-  int64_t blocks = p.row_blocks;
+  constexpr int R = 32 / L;
+  auto k = append_kernel<L>;
+  const int64_t per = static_cast<int64_t>(p.H) * p.ntensors, fill = 16ll * num_sms();
+  int64_t blocks = 0;
+  p.parts = 1;
+  if (p.ntensors > 0) {
+    // tokens per block: as many as leave 16 warps an SM; below one token a block (a decode step, whose runs
+    // are single rows) its heads are shared by several
+    p.chunk = kChunk;
+    while (p.chunk > 1 && static_cast<int64_t>(p.T) * kAppendWarps < p.chunk * fill) p.chunk >>= 1;
+    const int64_t chunks = (static_cast<int64_t>(p.T) + p.chunk - 1) / p.chunk;
+    while (chunks * p.parts * kAppendWarps < fill && p.parts * kAppendWarps < per * p.chunk) p.parts <<= 1;
+    p.row_blocks = chunks * p.parts;
+    blocks = p.row_blocks;
+  }
   if (p.q != nullptr) {
     // heads per warp, in whole passes: likewise
     p.q_heads = (p.Hq + R - 1) / R * R;
     while (p.q_heads > R && static_cast<int64_t>(p.T) * ((p.Hq + p.q_heads - 1) / p.q_heads) < fill)
       p.q_heads = (p.q_heads / R + 1) / 2 * R;
     p.q_parts = (p.Hq + p.q_heads - 1) / p.q_heads;
-    blocks += (static_cast<int64_t>(p.T) * p.q_parts + kW - 1) / kW;
+    blocks += (static_cast<int64_t>(p.T) * p.q_parts + kAppendWarps - 1) / kAppendWarps;
   }
   cudaError_t e = cudaSuccess;
-  KVQ_LAUNCH("append_kernel", s, k<<<static_cast<unsigned>(blocks), kAppendThreads, 0, s>>>(p); e = cudaGetLastError());
+  KVQ_LAUNCH("append_kernel", s, k<<<static_cast<unsigned>(blocks), 32 * kAppendWarps, 0, s>>>(p); e = cudaGetLastError());
   return e;
 }
 
 }  // namespace
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s) {
-  if (p.D > 256) return append_launch<32, 2>(p, s);
-  int L = 2;
-  while (8 * L < p.D) L <<= 1;
+  int L = 1;
+  while (16 * L < p.D) L <<= 1;
   switch (L) {
-    case 2: return append_launch<2, 1>(p, s);
-    case 4: return append_launch<4, 1>(p, s);
-    case 8: return append_launch<8, 1>(p, s);
-    case 16: return append_launch<16, 1>(p, s);
+    case 1: return append_launch<1>(p, s);
+    case 2: return append_launch<2>(p, s);
+    case 4: return append_launch<4>(p, s);
+    case 8: return append_launch<8>(p, s);
+    case 16: return append_launch<16>(p, s);
   }
-  return append_launch<32, 1>(p, s);
+  return append_launch<32>(p, s);
 }
 
 }  // namespace kvq

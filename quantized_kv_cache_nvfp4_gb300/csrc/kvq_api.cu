@@ -838,6 +838,8 @@ KVQ_API kvq_status kvq_append(const kvq_bf16_in* k, const kvq_bf16_in* v, int32_
   p.slot_ids = slot_ids;
   p.num_slots = pool->num_slots;
   p.block_size = pool->block_size;
+  p.small = fits_u31(pool->num_slots);
+  p.div_bs = FastDiv(static_cast<uint32_t>(pool->block_size));
   if (turns) {
     p.cos_sin = rotation->cos_sin;
     p.positions = rotation->positions;

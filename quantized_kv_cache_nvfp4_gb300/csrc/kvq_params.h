@@ -218,7 +218,9 @@ struct AppendParams {
   int64_t qo_row_pitch, qo_head_pitch;
   int32_t Hq;
   uint32_t* status;
-  int32_t chunk;            // set by the launcher: tokens whose runs one warp serves (<= 32),
+  bool small;               // slots and their number fit 31 bits: pages by div_bs
+  FastDiv div_bs;
+  int32_t chunk, parts;     // set by the launcher: tokens whose runs a thread block looks up, blocks that share them,
   int32_t q_heads, q_parts; // heads of a token that one warp turns, and how many such parts it has,
   int64_t row_blocks;       // thread blocks of K and V; those behind turn Q
 };
