@@ -14,10 +14,11 @@
 // (run, head, tensor), so scales and bounds need no atomics.  A thread block looks the runs of a chunk of
 // tokens up once and shares them, heads fastest, among its warps.  D / 16 lanes (rounded up to a power of
 // two) hold a row, 8 channels of a half and their partners of the other half each, so that pairs need no
-// exchange and share their angles; 32 / lanes rows a pass, the next pass's loads in flight.  Page scales need
-// the maximum before the codes, and read (from L2) and turn the rows twice: kept in unrolled registers
-// the code outgrew the instruction cache.  Behind those blocks of the grid, others turn Q: a warp
-// holds a token's angles in registers and walks its heads.
+// exchange and share their angles; 32 / lanes rows a pass.  The rows come through shared memory, a run or
+// 4 KB of it ahead of the arithmetic: in registers, one pass ahead left too little in flight (27,000
+// tokens, 8 heads, head_dim 128: K alone 40 us), and a whole run unrolled outgrew the instruction cache
+// (48).  Page scales need the maximum before the codes, and take a run twice.  Behind those
+// blocks of the grid, others turn Q: a warp holds a token's angles in registers and walks its heads.
 #include "page_scale.cuh"
 #include "kvq_params.h"
 
@@ -251,186 +252,265 @@ __device__ __forceinline__ void find_runs(const AppendParams& p, int64_t t0, boo
   }
 }
 
+// The rows of a warp's items (run, tensor, head) pass through two stages of its own in shared memory,
+// up to kStageBytes of rows each: one is filled by cp.async while the other is worked on.  An item of page
+// scales that takes more than one stage passes twice.
+constexpr int kStageBytes = 4096;
+
 template <int L>
-__device__ __forceinline__ void append_run(const AppendParams& p, const Chunk& ck, int64_t t0, int run, int tensor, int h) {
+__device__ __forceinline__ void append_items(const AppendParams& p, const Chunk& ck, int64_t t0, int first, int step,
+                                             unsigned char* stages) {
   constexpr int R = 32 / L;  // rows per pass
   const int lane = threadIdx.x & 31, li = lane % L, sub = lane / L;
-  const AppendTensor& ten = p.ten[tensor];
-  const int rot = ten.key && p.cos_sin != nullptr ? p.rot : 0;
-  const int D = p.D, n = ck.length[run], b = ck.start[run];
-  const int64_t pg = ck.page[run], prow = pg * p.H + h;
-  const bool begins = ck.begins[run], paged = ten.fmt == 5;
-  uint16_t* const bounds = ten.key ? p.bounds : nullptr;
-  const Lane ln = make_lane(rot, p.pairs, li, D);
-  float s0 = 0.0f;
-  if (paged && !begins && lane == 0) s0 = LDX(ten.dst.rscale + prow);
-  s0 = __shfl_sync(0xFFFFFFFFu, s0, 0);
-  const uint16_t* const x = ten.x + (t0 + b) * ten.row_pitch + h * ten.head_pitch;
-  const int64_t row0 = pg * p.block_size;
+  const int D = p.D, per = p.H * p.ntensors, items = ck.runs * per, rows = kStageBytes / (2 * D), pieces = D / 8;
 
-  auto load = [&](int r, uint32_t (&v)[2][4]) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0u;
-      if (ln.act && r < n) load16B(x + r * ten.row_pitch + 8 * ln.ch[j], v[j]);
-    }
+  struct Place {  // in the sequence of stages
+    int it, r0;   // item and first row
+    bool again;   // the second time through the item
   };
-  // the rows, turned, with whether the lane has one and the pool's number of it
-  auto each_row = [&](auto&& f) {
-    uint32_t next[2][4];
-    load(sub, next);
-#pragma unroll 1
-    for (int r0 = 0; r0 < n; r0 += R) {
-      const int r = r0 + sub;
-      int at, pos;
-      if (b + r < kChunk) {
-        at = ck.place[b + r];
-        pos = ck.pos[b + r];
+  Place now{first, 0, false};
+  struct Item {
+    int run, tensor, h;
+  };
+  auto item_of = [&](int it) {
+    Item m;
+    uint32_t run, rem;
+    p.div_per.divmod(static_cast<uint32_t>(it), run, rem);
+    m.run = static_cast<int>(run);
+    m.tensor = static_cast<int>(rem) >= p.H ? 1 : 0;
+    m.h = static_cast<int>(rem) - m.tensor * p.H;
+    return m;
+  };
+  auto after = [&](Place c, int length, bool paged) {
+    c.r0 += rows;
+    if (c.r0 < length) return c;
+    c.again = !c.again && length > rows && paged;
+    c.r0 = 0;
+    if (!c.again) c.it += step;
+    return c;
+  };
+  auto fetch = [&](const Place& c, unsigned char* to) {
+    if (c.it < items) {
+      const Item m = item_of(c.it);
+      const AppendTensor& ten = p.ten[m.tensor];
+      const int n = min(rows, ck.length[m.run] - c.r0);
+      const int64_t pitch = ten.row_pitch;
+      const uint16_t* x = ten.x + (t0 + ck.start[m.run] + c.r0) * pitch + m.h * ten.head_pitch;
+      if constexpr (L <= 16) {  // a lane copies one piece of every (16 / L)-th row
+        const int c8 = lane % (2 * L), r = lane / (2 * L);
+        x += r * pitch + 8 * c8;
+        to += 16 * (r * pieces + c8);
+        for (int q = r; q < n; q += 16 / L, x += (16 / L) * pitch, to += 16 * (16 / L) * pieces)
+          if (c8 < pieces) cp_async16(to, x);
       } else {
-        at = r < n ? static_cast<int>(LDX(p.slot_ids + t0 + b + r) - row0) : 0;
-        pos = rot != 0 && r < n ? LDX(p.positions + t0 + b + r) : 0;
+        for (int q = 0; q < n; ++q, x += pitch, to += 16 * pieces)
+          for (int c8 = lane; c8 < pieces; c8 += 32) cp_async16(to + 16 * c8, x + 8 * c8);
       }
-      Angles a;
-      if (rot != 0 && r < n) load_angles(ln, rot, p.pairs, p.cos_sin + static_cast<int64_t>(pos) * rot, a);
-      uint32_t v[2][4];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[j][i] = next[j][i];
-      load(r + R, next);
-      float y[2][8];
-      turn16(ln, a, rot, p.pairs, v, y);
-      f(y, r < n, (row0 + at) * p.H + h);
     }
+    cp_async_commit();
   };
+  fetch(now, stages);
 
   uint32_t lo[2][4], hi[2][4];
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      lo[j][i] = 0x7F807F80u;
-      hi[j][i] = 0xFF80FF80u;
-    }
-  float am = 0.0f;
-  each_row([&](const float (&y)[2][8], bool live, int64_t row) {
-    if (bounds != nullptr && live) {
+  float am = 0.0f, s0 = 0.0f, s = 0.0f;
+#pragma unroll 1
+  for (int stage = 0; now.it < items; stage ^= 1) {
+    const Item item = item_of(now.it);
+    const int run = item.run, tensor = item.tensor, h = item.h;
+    const Place next = after(now, ck.length[run], p.ten[tensor].fmt == 5);
+    fetch(next, stages + (stage ^ 1) * kStageBytes);
+    const bool key = p.ten[tensor].key;
+    const int fmt = p.ten[tensor].fmt;
+    const Nvfp4Planes dst = p.ten[tensor].dst;
+    const int rot = key && p.cos_sin != nullptr ? p.rot : 0;
+    const int length = ck.length[run], n = min(rows, length - now.r0), b = ck.start[run] + now.r0;
+    const int64_t prow = ck.page[run] * p.H + h, row0 = ck.page[run] * p.block_size;
+    const bool begins = ck.begins[run], paged = fmt == 5;
+    uint16_t* const bounds = key ? p.bounds : nullptr;
+    const Lane ln = make_lane(rot, p.pairs, li, D);
+    if (now.r0 == 0 && !now.again) {
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t b2 = pack_bf16x2(y[j][2 * i], y[j][2 * i + 1]);
-          lo[j][i] = bf16x2_min(lo[j][i], b2);
-          hi[j][i] = bf16x2_max(hi[j][i], b2);
+          lo[j][i] = 0x7F807F80u;
+          hi[j][i] = 0xFF80FF80u;
         }
+      am = s0 = 0.0f;
+      if (paged && !begins && lane == 0) s0 = LDX(dst.rscale + prow);
     }
-    const float vb[2] = {absmax8(y[0]), absmax8(y[1])};  // 0 in lanes without a row
-    if (paged) {
-      am = fmaxf(am, fmaxf(vb[0], vb[1]));
-      return;
-    }
-    const float amax = group_max<L>(fmaxf(vb[0], vb[1]));
-    const float rs = __fdiv_rn(amax, ten.fmt == 3 ? kE4M3Max : kE2M1Max * kE4M3Max);
-    const float rinv = inverse(rs);
-    live = live && ln.act;
-    if (ten.fmt == 3) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint2 c = fp8_quantize8(y[j], rs, rinv);
-        if (live) store8B(ten.dst.codes + row * D + 8 * ln.ch[j], c.x, c.y);
-      }
-    } else {
-      // a block of 16 is chunks 2 k and 2 k + 1: the other one's lane and place there
-      float other[2] = {vb[1], vb[0]};
-      if (rot != 0 && !p.pairs) {  // uniform
-        const int half = rot / 16, base = lane - li;
+    const unsigned char* const at_stage = stages + stage * kStageBytes + 2 * D * sub;
+    // the stage's rows, turned, with whether the lane has one and the pool's number of it
+    auto each_row = [&](auto&& f) {
+#pragma unroll 1
+      for (int q = 0; q < n; q += R) {
+        const int r = q + sub;
+        int at = 0, pos = 0;
+        if (b + r < kChunk) {
+          at = ck.place[b + r];
+          pos = ck.pos[b + r];
+        } else if (r < n) {
+          at = static_cast<int>(LDX(p.slot_ids + t0 + b + r) - row0);
+          if (rot != 0) pos = LDX(p.positions + t0 + b + r);
+        }
+        Angles a;
+        if (rot != 0 && r < n) load_angles(ln, rot, p.pairs, p.cos_sin + static_cast<int64_t>(pos) * rot, a);
+        uint32_t v[2][4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int c = ln.ch[j] ^ 1;
-          const int src = c < half ? c : c < 2 * half ? c - half : c / 2;
-          const float o0 = __shfl_sync(0xFFFFFFFFu, vb[0], base + src % L), o1 = __shfl_sync(0xFFFFFFFFu, vb[1], base + src % L);
-          other[j] = (c < half ? 0 : c < 2 * half ? 1 : c % 2) == 0 ? o0 : o1;
+          const uint4 u = ln.act && r < n ? *reinterpret_cast<const uint4*>(at_stage + 2 * D * q + 16 * ln.ch[j]) : make_uint4(0u, 0u, 0u, 0u);
+          v[j][0] = u.x, v[j][1] = u.y, v[j][2] = u.z, v[j][3] = u.w;
+        }
+        f(v, a, r < n, (row0 + at) * p.H + h);
+      }
+    };
+    cp_async_wait<1>();
+    __syncwarp();
+    bool turned = rot != 0 || !paged;
+    if (!now.again && !turned) {  // page scales of rows as they are: maxima of packed bf16
+      uint32_t m = 0u;
+      each_row([&](const uint32_t (&v)[2][4], const Angles&, bool, int64_t) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(v[j][i]));
+      });
+      m &= 0x7FFF7FFFu;
+      const float most = fmaxf(bf16lo(m), bf16hi(m));
+      turned = __any_sync(0xFFFFFFFFu, most > 3.4028235e38f);  // an infinity: the other way
+      if (!turned) am = fmaxf(am, most);
+      if (bounds != nullptr) turned = true;  // (K as it is, with its bounds)
+    }
+    if (!now.again && turned) {
+      each_row([&](const uint32_t (&v)[2][4], const Angles& a, bool live, int64_t row) {
+        float y[2][8];
+        turn16(ln, a, rot, p.pairs, v, y);
+        if (bounds != nullptr && live) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t b2 = pack_bf16x2(y[j][2 * i], y[j][2 * i + 1]);
+              lo[j][i] = bf16x2_min(lo[j][i], b2);
+              hi[j][i] = bf16x2_max(hi[j][i], b2);
+            }
+        }
+        const float vb[2] = {absmax8(y[0]), absmax8(y[1])};  // 0 in lanes without a row
+        if (paged) {  // the largest finite one: an infinity costs its own element only
+          if (fmaxf(vb[0], vb[1]) <= 3.4028235e38f) {
+            am = fmaxf(am, fmaxf(vb[0], vb[1]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) am = fmaxf(am, fabsf(y[j][i]) <= 3.4028235e38f ? fabsf(y[j][i]) : 0.0f);
+          }
+          return;
+        }
+        const float amax = group_max<L>(fmaxf(vb[0], vb[1]));
+        const float rs = __fdiv_rn(amax, fmt == 3 ? kE4M3Max : kE2M1Max * kE4M3Max);
+        const float rinv = inverse(rs);
+        live = live && ln.act;
+        if (fmt == 3) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint2 c = fp8_quantize8(y[j], rs, rinv);
+            if (live) store8B(dst.codes + row * D + 8 * ln.ch[j], c.x, c.y);
+          }
+        } else {
+          // a block of 16 is chunks 2 k and 2 k + 1: the other one's lane and place there
+          float other[2] = {vb[1], vb[0]};
+          if (rot != 0 && !p.pairs) {  // uniform
+            const int half = rot / 16, base = lane - li;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int c = ln.ch[j] ^ 1;
+              const int src = c < half ? c : c < 2 * half ? c - half : c / 2;
+              const float o0 = __shfl_sync(0xFFFFFFFFu, vb[0], base + src % L), o1 = __shfl_sync(0xFFFFFFFFu, vb[1], base + src % L);
+              other[j] = (c < half ? 0 : c < 2 * half ? 1 : c % 2) == 0 ? o0 : o1;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t bsb = block_scale_code(fmaxf(vb[j], other[j]), rs, rinv);
+            const float bs = __fmul_rn(e4m3_to_f32(bsb), rs);
+            const uint32_t c = quantize8(y[j], bs, inverse(bs));
+            if (live) {
+              STX(reinterpret_cast<uint32_t*>(dst.codes + row * (D / 2)) + ln.ch[j], c);
+              if (ln.ch[j] % 2 == 0) STX(dst.bscale + row * (D / 16) + ln.ch[j] / 2, static_cast<uint8_t>(bsb));
+            }
+          }
+        }
+        if (li == 0 && live) STX(dst.rscale + row, rs);
+      });
+    }
+    if (!now.again) {
+      if (now.r0 + rows >= length) {  // all of the item's rows
+        if (bounds != nullptr) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int o = L; o < 32; o <<= 1)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                lo[j][i] = bf16x2_min(lo[j][i], __shfl_xor_sync(0xFFFFFFFFu, lo[j][i], o));
+                hi[j][i] = bf16x2_max(hi[j][i], __shfl_xor_sync(0xFFFFFFFFu, hi[j][i], o));
+              }
+            if (ln.act && sub == 0) {
+              uint16_t* const at = bounds + prow * 2 * D + 8 * ln.ch[j];
+              if (!begins) {
+                uint32_t was[4];
+                load16B_rw(at, was);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) lo[j][i] = bf16x2_min(lo[j][i], was[i]);
+                load16B_rw(at + D, was);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) hi[j][i] = bf16x2_max(hi[j][i], was[i]);
+              }
+              store16B(at, lo[j]);
+              store16B(at + D, hi[j]);
+            }
+          }
+        }
+        if (paged) {
+          s0 = __shfl_sync(0xFFFFFFFFu, s0, 0);
+          if (!(s0 > 0.0f && s0 <= 3.4028235e38f)) s0 = 0.0f;  // no scale stored yet
+          s = fmaxf(s0, page_scale_need(group_max<32>(am)));
+          if (s0 > 0.0f && s > s0) {  // the rows that the page holds, under the new scale
+            const float f = __fdiv_rn(s0, s);
+            uint8_t* const cp = dst.codes + (row0 * p.H + h) * D;
+            const int64_t cpitch = static_cast<int64_t>(p.H) * D;
+            const int each = D / 16;  // 16-byte pieces of a row
+            for (int at = lane; at < p.block_size * each; at += 32) {
+              uint8_t* const to = cp + (at / each) * cpitch + 16 * (at % each);
+              uint32_t c[4];
+              load16B_rw(to, c);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) c[i] = rescale4(c[i], f);
+              store16B(to, c);
+            }
+            __syncwarp();  // before the call's own rows go over them
+          }
+          if (lane == 0 && s != s0) STX(dst.rscale + prow, s);
         }
       }
+    }
+    if (paged && (now.again || length <= rows)) {
+      const float inv = inverse(s);
+      each_row([&](const uint32_t (&v)[2][4], const Angles& a, bool live, int64_t row) {
+        float y[2][8];
+        turn16(ln, a, rot, p.pairs, v, y);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t bsb = block_scale_code(fmaxf(vb[j], other[j]), rs, rinv);
-        const float s = __fmul_rn(e4m3_to_f32(bsb), rs);
-        const uint32_t c = quantize8(y[j], s, inverse(s));
-        if (live) {
-          STX(reinterpret_cast<uint32_t*>(ten.dst.codes + row * (D / 2)) + ln.ch[j], c);
-          if (ln.ch[j] % 2 == 0) STX(ten.dst.bscale + row * (D / 16) + ln.ch[j] / 2, static_cast<uint8_t>(bsb));
+        for (int j = 0; j < 2; ++j) {
+          const uint2 c = fp8_quantize8(y[j], s, inv);
+          if (live && ln.act) store8B(dst.codes + row * D + 8 * ln.ch[j], c.x, c.y);
         }
-      }
+      });
     }
-    if (li == 0 && live) STX(ten.dst.rscale + row, rs);
-  });
-
-  if (bounds != nullptr) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-#pragma unroll
-      for (int o = L; o < 32; o <<= 1)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          lo[j][i] = bf16x2_min(lo[j][i], __shfl_xor_sync(0xFFFFFFFFu, lo[j][i], o));
-          hi[j][i] = bf16x2_max(hi[j][i], __shfl_xor_sync(0xFFFFFFFFu, hi[j][i], o));
-        }
-      if (ln.act && sub == 0) {
-        uint16_t* const at = bounds + prow * 2 * D + 8 * ln.ch[j];
-        if (!begins) {
-          uint32_t was[4];
-          load16B_rw(at, was);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) lo[j][i] = bf16x2_min(lo[j][i], was[i]);
-          load16B_rw(at + D, was);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) hi[j][i] = bf16x2_max(hi[j][i], was[i]);
-        }
-        store16B(at, lo[j]);
-        store16B(at + D, hi[j]);
-      }
-    }
+    __syncwarp();  // the stage is read
+    now = next;
   }
-  if (!paged) return;
-
-  am = group_max<32>(am);
-  if (am > 3.4028235e38f) {  // an infinity among them, the same in all lanes: once more without
-    am = 0.0f;
-    each_row([&](const float (&y)[2][8], bool, int64_t) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) am = fmaxf(am, fabsf(y[j][i]) <= 3.4028235e38f ? fabsf(y[j][i]) : 0.0f);
-    });
-    am = group_max<32>(am);
-  }
-  if (!(s0 > 0.0f && s0 <= 3.4028235e38f)) s0 = 0.0f;  // no scale stored yet
-  const float s = fmaxf(s0, page_scale_need(am));
-  if (s0 > 0.0f && s > s0) {  // the rows that the page holds, under the new scale
-    const float f = __fdiv_rn(s0, s);
-    uint8_t* const cp = ten.dst.codes + (row0 * p.H + h) * D;
-    const int64_t cpitch = static_cast<int64_t>(p.H) * D;
-    const int each = D / 16;  // 16-byte pieces of a row
-    for (int at = lane; at < p.block_size * each; at += 32) {
-      uint8_t* const to = cp + (at / each) * cpitch + 16 * (at % each);
-      uint32_t c[4];
-      load16B_rw(to, c);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = rescale4(c[i], f);
-      store16B(to, c);
-    }
-    __syncwarp();  // before the call's own rows go over them
-  }
-  if (lane == 0 && s != s0) STX(ten.dst.rscale + prow, s);
-  const float inv = inverse(s);
-  each_row([&](const float (&y)[2][8], bool live, int64_t row) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint2 c = fp8_quantize8(y[j], s, inv);
-      if (live && ln.act) store8B(ten.dst.codes + row * D + 8 * ln.ch[j], c.x, c.y);
-    }
-  });
+  cp_async_wait<0>();
 }
 
 // Q: warp w takes heads first .. of one token, 32 / L at a time.
@@ -483,8 +563,9 @@ __device__ __forceinline__ void append_turn_q(const AppendParams& p, int64_t w) 
 }
 
 template <int L>
-__global__ void __launch_bounds__(32 * kAppendWarps, 3) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(32 * kAppendWarps, 2) append_kernel(const AppendParams p) {
   __shared__ Chunk ck;
+  extern __shared__ __align__(16) unsigned char stages[];
   const int warp = threadIdx.x >> 5;
   const int64_t block = blockIdx.x;
   if (block >= p.row_blocks) {
@@ -496,11 +577,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 3) append_kernel(const Appe
   const int64_t t0 = chunk * p.chunk;
   if (warp == 0) find_runs(p, t0, part == 0, ck);
   __syncthreads();
-  const int per = p.H * p.ntensors, items = ck.runs * per;
-  for (int it = part * kAppendWarps + warp; it < items; it += p.parts * kAppendWarps) {
-    const int run = it / per, rem = it - run * per, tensor = rem / p.H;
-    append_run<L>(p, ck, t0, run, tensor, rem - tensor * p.H);
-  }
+  append_items<L>(p, ck, t0, part * kAppendWarps + warp, p.parts * kAppendWarps, stages + warp * 2 * kStageBytes);
 }
 
 template <int L>
@@ -510,6 +587,7 @@ cudaError_t append_launch(const AppendParams& p_in, cudaStream_t s) {
   auto k = append_kernel<L>;
   const int64_t per = static_cast<int64_t>(p.H) * p.ntensors, fill = 16ll * num_sms();
   int64_t blocks = 0;
+  p.div_per = FastDiv(static_cast<uint32_t>(per > 0 ? per : 1));
   p.parts = 1;
   if (p.ntensors > 0) {
     // tokens per block: as many as leave 16 warps an SM; below one token a block (a decode step, whose runs
@@ -530,7 +608,15 @@ cudaError_t append_launch(const AppendParams& p_in, cudaStream_t s) {
     blocks += (static_cast<int64_t>(p.T) * p.q_parts + kAppendWarps - 1) / kAppendWarps;
   }
   cudaError_t e = cudaSuccess;
-  KVQ_LAUNCH("append_kernel", s, k<<<static_cast<unsigned>(blocks), 32 * kAppendWarps, 0, s>>>(p); e = cudaGetLastError());
+  constexpr int kSmem = kAppendWarps * 2 * kStageBytes;
+  static bool told[64];  // of each device: the shared memory
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !told[dev]) {
+    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) told[dev] = true;
+  }
+  KVQ_LAUNCH("append_kernel", s, k<<<static_cast<unsigned>(blocks), 32 * kAppendWarps, kSmem, s>>>(p); e = cudaGetLastError());
   return e;
 }
 
