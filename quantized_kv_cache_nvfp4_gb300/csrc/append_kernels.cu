@@ -17,8 +17,9 @@
 // exchange and share their angles; 32 / lanes rows a pass.  The rows come through shared memory, a run or
 // 4 KB of it ahead of the arithmetic: in registers, one pass ahead left too little in flight (27,000
 // tokens, 8 heads, head_dim 128: K alone 40 us), and a whole run unrolled outgrew the instruction cache
-// (48).  Page scales need the maximum before the codes, and take a run twice.  Behind those
-// blocks of the grid, others turn Q: a warp holds a token's angles in registers and walks its heads.
+// (48).  Page scales need the maximum before the codes, and take a run twice.  The blocks behind
+// turn Q: a warp holds a token's angles in registers and walks its heads (evenly among the others: 155 us of
+// 27,000 tokens, 32 and 8 heads; behind them 148).
 #include "page_scale.cuh"
 #include "kvq_params.h"
 
@@ -311,7 +312,6 @@ __device__ __forceinline__ void append_items(const AppendParams& p, const Chunk&
   };
   fetch(now, stages);
 
-  uint32_t lo[2][4], hi[2][4];
   float am = 0.0f, s0 = 0.0f, s = 0.0f;
 #pragma unroll 1
   for (int stage = 0; now.it < items; stage ^= 1) {
@@ -329,18 +329,14 @@ __device__ __forceinline__ void append_items(const AppendParams& p, const Chunk&
     uint16_t* const bounds = key ? p.bounds : nullptr;
     const Lane ln = make_lane(rot, p.pairs, li, D);
     if (now.r0 == 0 && !now.again) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          lo[j][i] = 0x7F807F80u;
-          hi[j][i] = 0xFF80FF80u;
-        }
       am = s0 = 0.0f;
       if (paged && !begins && lane == 0) s0 = LDX(dst.rscale + prow);
     }
-    const unsigned char* const at_stage = stages + stage * kStageBytes + 2 * D * sub;
-    // the stage's rows, turned, with whether the lane has one and the pool's number of it
+    unsigned char* const at_stage = stages + stage * kStageBytes + 2 * D * sub;
+    // row 0 of the page: a row's bytes are `at` times the row's of all heads behind it
+    const int row_bytes = fmt == 1 ? D / 2 : D, codes_pitch = p.H * row_bytes;
+    uint8_t* const codes = dst.codes + (row0 * p.H + h) * row_bytes;
+    // the stage's rows: the lane's channels and angles, the row, its place in the page
     auto each_row = [&](auto&& f) {
 #pragma unroll 1
       for (int q = 0; q < n; q += R) {
@@ -361,15 +357,24 @@ __device__ __forceinline__ void append_items(const AppendParams& p, const Chunk&
           const uint4 u = ln.act && r < n ? *reinterpret_cast<const uint4*>(at_stage + 2 * D * q + 16 * ln.ch[j]) : make_uint4(0u, 0u, 0u, 0u);
           v[j][0] = u.x, v[j][1] = u.y, v[j][2] = u.z, v[j][3] = u.w;
         }
-        f(v, a, r < n, (row0 + at) * p.H + h);
+        f(v, a, r, at);
       }
+    };
+    // turned rows in bf16 over the rows as they came, for the bounds
+    auto put_back = [&](const float (&y)[2][8], int r) {
+      if (!(ln.act && r < n)) return;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        *reinterpret_cast<uint4*>(at_stage + 2 * D * (r - sub) + 16 * ln.ch[j]) =
+            make_uint4(pack_bf16x2(y[j][0], y[j][1]), pack_bf16x2(y[j][2], y[j][3]), pack_bf16x2(y[j][4], y[j][5]),
+                       pack_bf16x2(y[j][6], y[j][7]));
     };
     cp_async_wait<1>();
     __syncwarp();
     bool turned = rot != 0 || !paged;
     if (!now.again && !turned) {  // page scales of rows as they are: maxima of packed bf16
       uint32_t m = 0u;
-      each_row([&](const uint32_t (&v)[2][4], const Angles&, bool, int64_t) {
+      each_row([&](const uint32_t (&v)[2][4], const Angles&, int, int) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -379,23 +384,14 @@ __device__ __forceinline__ void append_items(const AppendParams& p, const Chunk&
       const float most = fmaxf(bf16lo(m), bf16hi(m));
       turned = __any_sync(0xFFFFFFFFu, most > 3.4028235e38f);  // an infinity: the other way
       if (!turned) am = fmaxf(am, most);
-      if (bounds != nullptr) turned = true;  // (K as it is, with its bounds)
     }
     if (!now.again && turned) {
-      each_row([&](const uint32_t (&v)[2][4], const Angles& a, bool live, int64_t row) {
+      each_row([&](const uint32_t (&v)[2][4], const Angles& a, int r, int at) {
         float y[2][8];
         turn16(ln, a, rot, p.pairs, v, y);
-        if (bounds != nullptr && live) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t b2 = pack_bf16x2(y[j][2 * i], y[j][2 * i + 1]);
-              lo[j][i] = bf16x2_min(lo[j][i], b2);
-              hi[j][i] = bf16x2_max(hi[j][i], b2);
-            }
-        }
+        const bool live = ln.act && r < n;
         const float vb[2] = {absmax8(y[0]), absmax8(y[1])};  // 0 in lanes without a row
+        if (bounds != nullptr && !paged) put_back(y, r);
         if (paged) {  // the largest finite one: an infinity costs its own element only
           if (fmaxf(vb[0], vb[1]) <= 3.4028235e38f) {
             am = fmaxf(am, fmaxf(vb[0], vb[1]));
@@ -410,12 +406,11 @@ __device__ __forceinline__ void append_items(const AppendParams& p, const Chunk&
         const float amax = group_max<L>(fmaxf(vb[0], vb[1]));
         const float rs = __fdiv_rn(amax, fmt == 3 ? kE4M3Max : kE2M1Max * kE4M3Max);
         const float rinv = inverse(rs);
-        live = live && ln.act;
         if (fmt == 3) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint2 c = fp8_quantize8(y[j], rs, rinv);
-            if (live) store8B(dst.codes + row * D + 8 * ln.ch[j], c.x, c.y);
+            if (live) store8B(codes + static_cast<int64_t>(at) * codes_pitch + 8 * ln.ch[j], c.x, c.y);
           }
         } else {
           // a block of 16 is chunks 2 k and 2 k + 1: the other one's lane and place there
@@ -436,42 +431,17 @@ __device__ __forceinline__ void append_items(const AppendParams& p, const Chunk&
             const float bs = __fmul_rn(e4m3_to_f32(bsb), rs);
             const uint32_t c = quantize8(y[j], bs, inverse(bs));
             if (live) {
-              STX(reinterpret_cast<uint32_t*>(dst.codes + row * (D / 2)) + ln.ch[j], c);
-              if (ln.ch[j] % 2 == 0) STX(dst.bscale + row * (D / 16) + ln.ch[j] / 2, static_cast<uint8_t>(bsb));
+              STX(reinterpret_cast<uint32_t*>(codes + static_cast<int64_t>(at) * codes_pitch) + ln.ch[j], c);
+              if (ln.ch[j] % 2 == 0)
+                STX(dst.bscale + ((row0 + at) * p.H + h) * (D / 16) + ln.ch[j] / 2, static_cast<uint8_t>(bsb));
             }
           }
         }
-        if (li == 0 && live) STX(dst.rscale + row, rs);
+        if (li == 0 && live) STX(dst.rscale + (row0 + at) * p.H + h, rs);
       });
     }
     if (!now.again) {
       if (now.r0 + rows >= length) {  // all of the item's rows
-        if (bounds != nullptr) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-#pragma unroll
-            for (int o = L; o < 32; o <<= 1)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                lo[j][i] = bf16x2_min(lo[j][i], __shfl_xor_sync(0xFFFFFFFFu, lo[j][i], o));
-                hi[j][i] = bf16x2_max(hi[j][i], __shfl_xor_sync(0xFFFFFFFFu, hi[j][i], o));
-              }
-            if (ln.act && sub == 0) {
-              uint16_t* const at = bounds + prow * 2 * D + 8 * ln.ch[j];
-              if (!begins) {
-                uint32_t was[4];
-                load16B_rw(at, was);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) lo[j][i] = bf16x2_min(lo[j][i], was[i]);
-                load16B_rw(at + D, was);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) hi[j][i] = bf16x2_max(hi[j][i], was[i]);
-              }
-              store16B(at, lo[j]);
-              store16B(at + D, hi[j]);
-            }
-          }
-        }
         if (paged) {
           s0 = __shfl_sync(0xFFFFFFFFu, s0, 0);
           if (!(s0 > 0.0f && s0 <= 3.4028235e38f)) s0 = 0.0f;  // no scale stored yet
@@ -497,15 +467,48 @@ __device__ __forceinline__ void append_items(const AppendParams& p, const Chunk&
     }
     if (paged && (now.again || length <= rows)) {
       const float inv = inverse(s);
-      each_row([&](const uint32_t (&v)[2][4], const Angles& a, bool live, int64_t row) {
+      each_row([&](const uint32_t (&v)[2][4], const Angles& a, int r, int at) {
         float y[2][8];
         turn16(ln, a, rot, p.pairs, v, y);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const uint2 c = fp8_quantize8(y[j], s, inv);
-          if (live && ln.act) store8B(dst.codes + row * D + 8 * ln.ch[j], c.x, c.y);
+          if (ln.act && r < n) store8B(codes + static_cast<int64_t>(at) * codes_pitch + 8 * ln.ch[j], c.x, c.y);
         }
+        if (bounds != nullptr) put_back(y, r);
       });
+    }
+    // ---- bounds of the stage's rows, a lane 8 channels, with the stored ones but where the item's first
+    // rows start the block over ----
+    if (bounds != nullptr && (!paged || now.again || length <= rows)) {
+      __syncwarp();
+      for (int c8 = lane; c8 < pieces; c8 += 32) {
+        uint16_t* const at = bounds + prow * 2 * D + 8 * c8;
+        uint32_t lo[4], hi[4];
+        if (begins && now.r0 == 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            lo[i] = 0x7F807F80u;
+            hi[i] = 0xFF80FF80u;
+          }
+        } else {
+          load16B_rw(at, lo);
+          load16B_rw(at + D, hi);
+        }
+        const unsigned char* from = stages + stage * kStageBytes + 16 * c8;
+#pragma unroll 4
+        for (int r = 0; r < n; ++r, from += 2 * D) {
+          const uint4 u = *reinterpret_cast<const uint4*>(from);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            lo[i] = bf16x2_min(lo[i], w[i]);
+            hi[i] = bf16x2_max(hi[i], w[i]);
+          }
+        }
+        store16B(at, lo);
+        store16B(at + D, hi);
+      }
     }
     __syncwarp();  // the stage is read
     now = next;

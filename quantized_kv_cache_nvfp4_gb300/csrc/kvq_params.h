@@ -220,8 +220,8 @@ struct AppendParams {
   uint32_t* status;
   bool small;               // slots and their number fit 31 bits: pages by div_bs
   FastDiv div_bs;
-  FastDiv div_per;          // set by the launcher: by H x ntensors;
-  int32_t chunk, parts;     //: tokens whose runs a thread block looks up, blocks that share them,
+  FastDiv div_per;          // set by the launcher: by H x ntensors,
+  int32_t chunk, parts;     // tokens whose runs a thread block looks up, blocks that share them,
   int32_t q_heads, q_parts; // heads of a token that one warp turns, and how many such parts it has,
   int64_t row_blocks;       // thread blocks of K and V; those behind turn Q
 };
