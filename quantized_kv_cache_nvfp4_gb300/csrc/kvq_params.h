@@ -398,6 +398,7 @@ struct SparseAttnParams {
   QueryAttnParams q;         // no bias, window, prefix or key starts
   const int32_t* selected;   // [num_tokens][H][topk]
   int32_t topk;
+  bool whole;                // set by the launcher: blocks are whole 16-token tiles
 };
 constexpr int kSparseMostBlocks = 4096;
 size_t sparse_attn_workspace_bytes(int32_t T, int32_t H, int32_t Hq, int32_t D, int32_t block_size, int32_t topk);

@@ -48,16 +48,29 @@ struct SparseMod {
   }
 };
 
+// The ring and shared memory of a thread block.  Two stages where a tile is over 4 KB: four blocks an SM
+// instead of three, and one tile a warp ahead (32 lists of 128 16-token blocks, 8 KV heads, head_dim
+// 128, page scales: XX us; with three stages YY).
+template <int D, int kFK, int kFV>
+struct SparseRing {
+  using T = AttnTile<D, kFK, kFV>;
+  static constexpr int kStages = D == 256 && T::kBytes > 4096 ? 3 : T::kBytes > 4096 ? 2 : 4;
+  static constexpr int kRing = kAttnWarps * kStages * T::kBytes;
+  static constexpr int kSmem = T::kQ + (kRing > T::kMerge ? kRing : T::kMerge);
+};
+
 template <int D, int kFK, int kFV, int kNH>
 __global__ void __launch_bounds__(kAttnThreads) sparse_rows_kernel(const SparseAttnParams sp) {
   using T = AttnTile<D, kFK, kFV>;
+  using Ring = SparseRing<D, kFK, kFV>;
+  constexpr int kStages = Ring::kStages;
   const QueryAttnParams& qp = sp.q;
   const AttnParams& p = qp.a;
   constexpr int kKS = D / 16, kMT = D / 16, kRows = 8 * kNH;
   constexpr bool kQReg = kNH * kKS <= 8;
   extern __shared__ __align__(16) unsigned char smem[];
-  int2* const entries = reinterpret_cast<int2*>(smem + T::kSmem);  // {block of the pool or -1, first token}
-  __shared__ uint32_t seen[kAttnWarps][T::kStages];
+  int2* const entries = reinterpret_cast<int2*>(smem + Ring::kSmem);  // {block of the pool or -1, first token}
+  __shared__ uint32_t seen[kAttnWarps][kStages];
   __shared__ int last_entry;
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -143,14 +156,47 @@ __global__ void __launch_bounds__(kAttnThreads) sparse_rows_kernel(const SparseA
   };
 
   // ---- the warp's tiles through its cp.async ring ----
-  unsigned char* const ring = smem + T::kQ + warp * T::kStages * T::kBytes;
+  unsigned char* const ring = smem + T::kQ + warp * kStages * T::kBytes;
   const bool lane_page = lane < 16 ? p.k_page : p.v_page;
   // copies of the warp's tile number `it` into stage st; keys out of sight become zeros
   auto issue = [&](int it, int st) {
     const int kt = warp + it * kAttnWarps;
     if (kt >= ntile) return;
     unsigned char* const sb = ring + st * T::kBytes;
-    const int v = v_begin + kt * 16 + (lane & 15);
+    const int tt = lane & 15;
+    constexpr int kPK = T::kCK / 16, kPV = T::kCV / 16;
+    if (sp.whole) {  // the tile lies in one block
+      uint32_t e, off;
+      p.div_bs.divmod(static_cast<uint32_t>(v_begin + kt * 16), e, off);
+      const int2 at = entries[e - e0];
+      if (at.x < 0 || at.y + static_cast<int>(off) > pos) {
+        if (lane == 0) seen[warp][st] = 0u;
+        return;
+      }
+      if (at.y + static_cast<int>(off) + 15 <= pos) {  // and in sight: rows a fixed pitch apart
+        const int64_t r0 = (static_cast<int64_t>(at.x) * p.block_size + off) * p.H + h;
+        const int pk = p.H * T::kCK, pv = p.H * T::kCV;
+        const uint8_t* ks = p.k.codes + r0 * T::kCK + (lane / kPK) * pk + (lane % kPK) * 16;
+        const uint8_t* vs = p.v.codes + r0 * T::kCV + (lane / kPV) * pv + (lane % kPV) * 16;
+        unsigned char* const kd = sb + T::kOffKC + (lane / kPK) * T::kSK + (lane % kPK) * 16;
+        unsigned char* const vd = sb + T::kOffVC + (lane / kPV) * T::kSV + (lane % kPV) * 16;
+#pragma unroll
+        for (int x = 0; x < kPK / 2; ++x) cp_async16(kd + x * (32 / kPK) * T::kSK, ks + static_cast<int64_t>(x * (32 / kPK)) * pk);
+#pragma unroll
+        for (int x = 0; x < kPV / 2; ++x) cp_async16(vd + x * (32 / kPV) * T::kSV, vs + static_cast<int64_t>(x * (32 / kPV)) * pv);
+        const int64_t row = r0 + static_cast<int64_t>(tt) * p.H, srow = lane_page ? static_cast<int64_t>(at.x) * p.H + h : row;
+        if (lane < 16) {
+          if constexpr (T::kBK > 0) cp_async_n<T::kBK>(sb + T::kOffKB + tt * T::kBK, p.k.bscale + row * T::kBK);
+          cp_async_small<4>(sb + T::kOffKR + tt * 4, p.k.rscale + srow);
+        } else {
+          if constexpr (T::kBV > 0) cp_async_n<T::kBV>(sb + T::kOffVB + tt * T::kBV, p.v.bscale + row * T::kBV);
+          cp_async_small<4>(sb + T::kOffVR + tt * 4, p.v.rscale + srow);
+        }
+        if (lane == 0) seen[warp][st] = 0xFFFFu;
+        return;
+      }
+    }
+    const int v = v_begin + kt * 16 + tt;
     int64_t row = -1, srow = 0;
     if (v < v_end) {
       uint32_t e, off;
@@ -164,8 +210,6 @@ __global__ void __launch_bounds__(kAttnThreads) sparse_rows_kernel(const SparseA
     const uint32_t keys = __ballot_sync(0xFFFFFFFFu, row >= 0) & 0xFFFFu;
     if (lane == 0) seen[warp][st] = keys;
     if (keys == 0u) return;
-    const int tt = lane & 15;
-    constexpr int kPK = T::kCK / 16, kPV = T::kCV / 16;
     auto piece = [&](unsigned char* dst, const uint8_t* src, int64_t rr) {
       if (rr >= 0) cp_async16(dst, src);
       else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
@@ -196,15 +240,15 @@ __global__ void __launch_bounds__(kAttnThreads) sparse_rows_kernel(const SparseA
   AttnState<D, kNH> st;
   st.init(kNoKey);
 #pragma unroll
-  for (int j = 0; j < T::kStages - 1; ++j) {
+  for (int j = 0; j < kStages - 1; ++j) {
     issue(j, j);
     cp_async_commit();
   }
   const int my_tiles = ntile > warp ? (ntile - warp + kAttnWarps - 1) / kAttnWarps : 0;
   for (int it = 0; it < my_tiles; ++it) {
-    cp_async_wait<T::kStages - 2>();
+    cp_async_wait<kStages - 2>();
     __syncwarp();
-    const int stage = it % T::kStages;
+    const int stage = it % kStages;
     const unsigned char* const sb = ring + stage * T::kBytes;
     mod.keys = seen[warp][stage];
     if (mod.keys != 0u) {
@@ -213,7 +257,7 @@ __global__ void __launch_bounds__(kAttnThreads) sparse_rows_kernel(const SparseA
       attn_tile<D, kFK, kFV, kNH>(tv, qb, qmul, lane, 16, st, mod);
     }
     __syncwarp();
-    issue(it + T::kStages - 1, (it + T::kStages - 1) % T::kStages);
+    issue(it + kStages - 1, (it + kStages - 1) % kStages);
     cp_async_commit();
   }
   cp_async_wait<0>();
@@ -277,12 +321,11 @@ __global__ void __launch_bounds__(kAttnThreads) sparse_rows_kernel(const SparseA
 
 template <int D, int kFK, int kFV, int kNH>
 cudaError_t sparse_launch(const SparseAttnParams& p, cudaStream_t s) {
-  using T = AttnTile<D, kFK, kFV>;
   auto k = sparse_rows_kernel<D, kFK, kFV, kNH>;
   const int64_t keys = static_cast<int64_t>(p.topk) * p.q.a.block_size;
   const int64_t per = ((keys + p.q.a.nsplit - 1) / p.q.a.nsplit + 63) / 64 * 64;
   const int64_t entries = std::min(static_cast<int64_t>(p.topk), per / p.q.a.block_size + 2);
-  const size_t smem = T::kSmem + static_cast<size_t>(entries) * sizeof(int2);
+  const size_t smem = SparseRing<D, kFK, kFV>::kSmem + static_cast<size_t>(entries) * sizeof(int2);
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(p.q.max_q) * p.q.a.nsplit), p.q.a.H, p.q.a.S);
@@ -304,23 +347,24 @@ cudaError_t sparse_dim(const SparseAttnParams& p, cudaStream_t s) {
   return p.q.a.group <= 8 ? sparse_fmt<D, 1>(p, s) : sparse_fmt<D, 2>(p, s);
 }
 
-int sparse_splits(int32_t T, int32_t H, int32_t topk, int32_t block_size) {
+int sparse_splits(int32_t T, int32_t H, int32_t D, int32_t topk, int32_t block_size) {
   const int64_t keys = std::min(static_cast<int64_t>(topk) * block_size, int64_t{0x7FFF0000});
-  return fill_splits(static_cast<int64_t>(T) * H, 4ll * num_sms(), static_cast<int32_t>(keys), 256, 256);
+  return fill_splits(static_cast<int64_t>(T) * H, (D == 256 ? 2ll : 4ll) * num_sms(), static_cast<int32_t>(keys), 256, 256);
 }
 
 }  // namespace
 
 size_t sparse_attn_workspace_bytes(int32_t T, int32_t H, int32_t Hq, int32_t D, int32_t block_size, int32_t topk) {
   if (T <= 0 || H <= 0 || Hq < H || D <= 0 || block_size <= 0 || topk <= 0) return 0;
-  const int n = sparse_splits(T, H, topk, block_size);
+  const int n = sparse_splits(T, H, D, topk, block_size);
   return n <= 1 ? 0 : static_cast<size_t>(T) * Hq * n * (D + 2) * sizeof(float);
 }
 
 cudaError_t launch_sparse_attention(const SparseAttnParams& p_in, cudaStream_t s) {
   SparseAttnParams p = p_in;
   AttnParams& a = p.q.a;
-  a.nsplit = sparse_splits(p.q.num_tokens, a.H, p.topk, a.block_size);
+  p.whole = a.block_size % 16 == 0;
+  a.nsplit = sparse_splits(p.q.num_tokens, a.H, a.D, p.topk, a.block_size);
   const cudaError_t e = a.D == 64 ? sparse_dim<64>(p, s) : a.D == 128 ? sparse_dim<128>(p, s) : sparse_dim<256>(p, s);
   return e == cudaSuccess ? launch_query_merge_splits(p.q, s) : e;
 }
