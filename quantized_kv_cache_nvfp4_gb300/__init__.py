@@ -478,38 +478,45 @@ def kvq_append(k: Optional[torch.Tensor], v: Optional[torch.Tensor], slot_ids: O
     src = k if k is not None else v if v is not None else q
     if src is None:
         raise ValueError("k, v and q are all None")
-    T, H, D = src.size(0), pool.num_heads, pool.head_dim
-    for t, name, heads in ((k, "k", H), (v, "v", H), (q, "q", None), (q_out, "q_out", None if q is None else q.size(1))):
-        if t is not None and (t.dim() != 3 or t.size(0) != T or t.size(2) != D or (heads is not None and t.size(1) != heads)):
-            raise ValueError(f"{name} must be [{T}, {'heads' if heads is None else heads}, {D}]")
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out come together")
-    rot = None
+    ps = pool._struct()
+    T, H, D = src.size(0), ps.num_heads, ps.head_dim
+    rows = (T, H, D)
+    if (k is not None and k.shape != rows) or (v is not None and v.shape != rows):
+        raise ValueError(f"k and v must be [{T}, {H}, {D}]")
+    kin = vin = qin = qo = rot = slots = bounds = None
+    Hq = 0
+    if k is not None:
+        kin = ctypes.byref(_bf16_in(k, "k"))
+    if v is not None:
+        vin = ctypes.byref(_bf16_in(v, "v"))
+    if k is not None or v is not None:
+        slots = _vec(slot_ids, torch.int64, "slot_ids", T)
+    if q is not None or q_out is not None:
+        if q is None or q_out is None:
+            raise ValueError("q and q_out come together")
+        if q.dim() != 3 or q.shape != q_out.shape or q.size(0) != T or q.size(2) != D:
+            raise ValueError(f"q and q_out must be [{T}, query heads, {D}]")
+        Hq, qin, qo = q.size(1), ctypes.byref(_bf16_in(q, "q")), ctypes.byref(_bf16_out(q_out, "q_out"))
     if cos_sin is not None:
         if positions is None:
             raise ValueError("cos_sin needs positions")
         if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
             raise ValueError("cos_sin must be a contiguous [positions, rot_dim] float32 tensor")
-        rot = _abi.Rotation(cos_sin.data_ptr(), cos_sin.size(0), cos_sin.size(1), int(interleaved),
-                            _vec(positions, torch.int32, "positions", T))
+        rot = ctypes.byref(_abi.Rotation(cos_sin.data_ptr(), cos_sin.size(0), cos_sin.size(1), 1 if interleaved else 0,
+                                         _vec(positions, torch.int32, "positions", T)))
     if key_bounds is not None:
-        _bounds_shape(key_bounds, pool.num_slots // pool.block_size, H, D)
-    slots = None if k is None and v is None else _vec(slot_ids, torch.int64, "slot_ids", T)
-    kin = _bf16_in(k, "k") if k is not None else None
-    vin = _bf16_in(v, "v") if v is not None else None
-    qin, qo = (_bf16_in(q, "q"), _bf16_out(q_out, "q_out")) if q is not None else (None, None)
-    ps = pool._struct()
-    ref = lambda x: None if x is None else ctypes.byref(x)
-    _check(_lib().kvq_append(ref(kin), ref(vin), T, slots, ctypes.byref(ps), ref(rot), ref(qin), ref(qo),
-                             0 if q is None else q.size(1), _ptr(key_bounds), _ptr(dev_status), _stream(stream)))
+        _bounds_shape(key_bounds, ps.num_slots // ps.block_size, H, D)
+        bounds = key_bounds.data_ptr()
+    _check(_lib().kvq_append(kin, vin, T, slots, ctypes.byref(ps), rot, qin, qo, Hq, bounds, _ptr(dev_status),
+                             _stream(stream)))
     return q_out
 
 
-def _bounds_shape(t: torch.Tensor, blocks: Optional[int], H: Optional[int], D: Optional[int]) -> None:
+def _bounds_shape(t: torch.Tensor, blocks: Optional[int], H: Optional[int], D: int) -> None:
     if t.dtype != torch.bfloat16:
         raise TypeError("key_bounds must be bfloat16")
-    if (t.dim() != 4 or not t.is_contiguous() or t.size(2) != 2
-            or any(n is not None and t.size(i) != n for i, n in ((0, blocks), (1, H), (3, D)))):
+    if (t.dim() != 4 or t.shape != (t.size(0) if blocks is None else blocks, t.size(1) if H is None else H, 2, D)
+            or not t.is_contiguous()):
         raise ValueError("key_bounds must be a contiguous [blocks, heads, 2, head_dim] tensor")
 
 
@@ -552,7 +559,7 @@ def kvq_select_blocks(key_bounds: torch.Tensor, block_table: torch.Tensor, seq_l
 def _lists(t: torch.Tensor, T: int, H: int):
     if t.dtype != torch.int32:
         raise TypeError("selected must be int32")
-    if t.dim() != 3 or t.size(0) != T or t.size(1) != H or not t.is_contiguous():
+    if t.dim() != 3 or t.shape[:2] != (T, H) or not t.is_contiguous():
         raise ValueError(f"selected must be a contiguous [{T}, {H}, topk] tensor")
     return t.data_ptr()
 
@@ -577,10 +584,11 @@ def kvq_sparse_attention(pool: KvPool, block_table: torch.Tensor, seq_lens: torc
     qi, oo = _bf16_in(q, "q"), _bf16_out(out, "out")
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
+    ps = pool._struct()
     T, Hq, D = q.shape
-    if D != pool.head_dim:
-        raise ValueError(f"q has head_dim {D}, the pool {pool.head_dim}")
-    H = pool.num_heads
+    H = ps.num_heads
+    if D != ps.head_dim:
+        raise ValueError(f"q has head_dim {D}, the pool {ps.head_dim}")
     sel = _lists(selected, T, H)
     topk = selected.size(2)
     if workspace is None:
@@ -588,7 +596,6 @@ def kvq_sparse_attention(pool: KvPool, block_table: torch.Tensor, seq_lens: torc
         if need > 0:
             workspace = _workspace(need, q.device, stream)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    ps = pool._struct()
     _check(_lib().kvq_sparse_attention(
         ctypes.byref(ps), block_table.data_ptr(), S, max_blocks, _vec(seq_lens, torch.int32, "seq_lens", S),
         max_seq_len, ctypes.byref(qi), _vec(query_starts, torch.int32, "query_starts", S + 1), T, max_query_len, Hq,

@@ -612,13 +612,8 @@ cudaError_t append_launch(const AppendParams& p_in, cudaStream_t s) {
   }
   cudaError_t e = cudaSuccess;
   constexpr int kSmem = kAppendWarps * 2 * kStageBytes;
-  static bool told[64];  // of each device: the shared memory
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64 || !told[dev]) {
-    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) told[dev] = true;
-  }
+  struct Tag {};
+  if ((e = allow_smem<Tag>(reinterpret_cast<const void*>(k), kSmem)) != cudaSuccess) return e;
   KVQ_LAUNCH("append_kernel", s, k<<<static_cast<unsigned>(blocks), 32 * kAppendWarps, kSmem, s>>>(p); e = cudaGetLastError());
   return e;
 }

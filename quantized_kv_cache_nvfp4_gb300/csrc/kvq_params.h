@@ -398,7 +398,8 @@ struct SparseAttnParams {
   QueryAttnParams q;         // no bias, window, prefix or key starts
   const int32_t* selected;   // [num_tokens][H][topk]
   int32_t topk;
-  bool whole;                // set by the launcher: blocks are whole 16-token tiles
+  bool whole;                // set by the launcher: blocks are whole 16-token tiles,
+  bool cluster;              // a list's splits are a thread-block cluster
 };
 constexpr int kSparseMostBlocks = 4096;
 size_t sparse_attn_workspace_bytes(int32_t T, int32_t H, int32_t Hq, int32_t D, int32_t block_size, int32_t topk);
@@ -408,6 +409,19 @@ cudaError_t launch_query_tiles(const QueryAttnParams& p, cudaStream_t s);
 cudaError_t launch_payload_decode(const UnpackParams& p, int lanes, bool v8, cudaStream_t s);
 
 int num_sms();
+
+// Allows a kernel `bytes` of dynamic shared memory on the current device; once for each Tag (a kernel's own
+// type), so that eager calls do not repeat the attribute's call.
+template <typename Tag>
+cudaError_t allow_smem(const void* kernel, size_t bytes) {
+  static bool told[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && told[dev]) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess && dev >= 0 && dev < 64) told[dev] = true;
+  return e;
+}
 
 // Resident blocks per SM of a kernel at a block size and dynamic shared memory, on the
 // current device; queried once per (kernel, block size, shared memory, device) and

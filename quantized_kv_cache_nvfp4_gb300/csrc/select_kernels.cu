@@ -1015,7 +1015,8 @@ cudaError_t score_launch(SelectParams& p, cudaStream_t s) {
     // zero, half a unit for each step's sum, one for each part's and half for each head's; two parts: as
     // much as 2^-18 for what they leave of q
     p.err = 1.02f * static_cast<float>(16 + D / 16 + 4 + p.group + (p.max_q <= 2 ? 0 : 33)) * 0x1p-23f;
-    e = cudaFuncSetAttribute(score_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 512);
+    struct Tag {};
+    e = allow_smem<Tag>(reinterpret_cast<const void*>(score_kernel<D>), 227 * 1024 - 512);
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(segments), heads, p.S);
     KVQ_LAUNCH("score_kernel", s, score_kernel<D><<<grid, 32 * (kScoreWarps<D> + 1), plan.smem, s>>>(p); e = cudaGetLastError());
@@ -1031,7 +1032,8 @@ cudaError_t score_launch(SelectParams& p, cudaStream_t s) {
   // towards zero, the same again for what hi + lo leaves of q (2^-18), half a unit for each step's sum
   // and for each head's
   p.err = 1.02f * static_cast<float>(64 + D / 16 + p.group) * 0x1p-23f;
-  e = cudaFuncSetAttribute(score_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
+  struct Tag {};
+  e = allow_smem<Tag>(reinterpret_cast<const void*>(score_tile_kernel<D>), T::kSmem);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>(p.sizes_n), p.S);
   KVQ_LAUNCH("score_tile_kernel", s, score_tile_kernel<D><<<grid, 32 * (T::kWarps + 1), T::kSmem, s>>>(p); e = cudaGetLastError());

@@ -9,8 +9,8 @@
 // rows of the tiles, since they alone share a list.  It first looks its entries up (list and block
 // table, all at once) into shared memory; then its 4 warps take 16 of the listed keys in turn
 // through cp.async rings with the tile arithmetic of the other attention kernels (attn_tile.cuh).
-// Keys outside the row's sight become zeros in shared memory and -inf among the scores.  Splits
-// merge through the caller's workspace in the merge kernel of kvq_attention.
+// Keys outside the row's sight become zeros in shared memory and -inf among the scores.  Up to 8 splits
+// of a list merge as a cluster, more through the caller's workspace in the merge kernel of kvq_attention.
 #include <algorithm>
 
 #include "query_attn.cuh"
@@ -59,8 +59,27 @@ struct SparseRing {
   static constexpr int kSmem = T::kQ + (kRing > T::kMerge ? kRing : T::kMerge);
 };
 
+// Up to this many splits of a list are one thread-block cluster and merge through each other's shared
+// memory: a second kernel costs 4 us.
+constexpr int kClusterSplits = 8;
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A float of this thread block's shared memory, read in block `rank` of the cluster.
+__device__ __forceinline__ float peer_float(const float* mine, uint32_t rank) {
+  uint32_t at;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(at)
+               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(mine))), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
 template <int D, int kFK, int kFV, int kNH>
-__global__ void __launch_bounds__(kAttnThreads) sparse_rows_kernel(const SparseAttnParams sp) {
+__global__ void __launch_bounds__(kAttnThreads, D == 128 && kNH == 1 ? 4 : 1) sparse_rows_kernel(const SparseAttnParams sp) {
   using T = AttnTile<D, kFK, kFV>;
   using Ring = SparseRing<D, kFK, kFV>;
   constexpr int kStages = Ring::kStages;
@@ -261,7 +280,7 @@ __global__ void __launch_bounds__(kAttnThreads) sparse_rows_kernel(const SparseA
     cp_async_commit();
   }
   cp_async_wait<0>();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!sp.cluster) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 #pragma unroll
   for (int off = 4; off <= 16; off <<= 1)
 #pragma unroll
@@ -289,7 +308,8 @@ __global__ void __launch_bounds__(kAttnThreads) sparse_rows_kernel(const SparseA
       }
   }
   __syncthreads();
-  const float* const mall = reinterpret_cast<const float*>(smem + T::kQ);
+  float* const mall = reinterpret_cast<float*>(smem + T::kQ);
+  __shared__ float merged[2 * kRows];  // of a cluster: M, then L
   for (int idx = threadIdx.x; idx < rows * D; idx += kAttnThreads) {
     const int row = idx / D, d = idx % D;
     float M = kNoKey;
@@ -302,21 +322,59 @@ __global__ void __launch_bounds__(kAttnThreads) sparse_rows_kernel(const SparseA
       L += mall[(w * kRows + row) * (D + 2) + D + 1] * f;
       O += mall[(w * kRows + row) * (D + 2) + d] * f;
     }
+    const float mark = cta_bad ? __int_as_float(0x7FC00000) : M;  // NaN marks a bad block entry (M never is one)
     const int qh = h * p.group + row;
     if (p.nsplit == 1) {
       if (cta_bad) continue;
       const float y = L == 0.0f ? 0.0f : O / L;
       STX(p.out + tok * p.o_row_pitch + static_cast<int64_t>(qh) * p.o_head_pitch + d,
           static_cast<uint16_t>(pack_bf16x2(y, 0.0f) & 0xFFFFu));
+    } else if (sp.cluster) {
+      mall[row * (D + 2) + d] = O;  // what no other thread reads
+      if (d == 0) {
+        merged[row] = mark;
+        merged[kRows + row] = L;
+      }
     } else {
       float* const wsr = p.ws + ((tok * p.Hq + qh) * p.nsplit + split) * (D + 2);
       STX(wsr + d, O);
       if (d == 0) {
-        STX(wsr + D, cta_bad ? __int_as_float(0x7FC00000) : M);  // NaN marks a bad block entry (M never is one)
+        STX(wsr + D, mark);
         STX(wsr + D + 1, L);
       }
     }
   }
+  if (!sp.cluster) return;
+  cluster_sync();
+  // pairs of channels, shared among the cluster's blocks (block `split` of it is this one)
+  for (int idx = split * kAttnThreads + static_cast<int>(threadIdx.x); idx < rows * (D / 2); idx += p.nsplit * kAttnThreads) {
+    const int row = idx / (D / 2), d = 2 * (idx % (D / 2));
+    float m[kClusterSplits], l[kClusterSplits], o0[kClusterSplits], o1[kClusterSplits], M = kNoKey;
+    bool skip = false;
+#pragma unroll
+    for (int x = 0; x < kClusterSplits; ++x) {
+      if (x >= p.nsplit) break;
+      m[x] = peer_float(merged + row, x);
+      l[x] = peer_float(merged + kRows + row, x);
+      o0[x] = peer_float(mall + row * (D + 2) + d, x);
+      o1[x] = peer_float(mall + row * (D + 2) + d + 1, x);
+      skip = skip || isnan(m[x]);
+      M = fmaxf(M, m[x]);
+    }
+    float L = 0.0f, a = 0.0f, b = 0.0f;
+#pragma unroll
+    for (int x = 0; x < kClusterSplits; ++x) {
+      if (x >= p.nsplit) break;
+      const float f = ex2(m[x] - M);
+      L = __fmaf_rn(l[x], f, L);
+      a = __fmaf_rn(o0[x], f, a);
+      b = __fmaf_rn(o1[x], f, b);
+    }
+    if (skip) continue;
+    STX(reinterpret_cast<uint32_t*>(p.out + tok * p.o_row_pitch + static_cast<int64_t>(h * p.group + row) * p.o_head_pitch + d),
+        L == 0.0f ? 0u : pack_bf16x2(a / L, b / L));
+  }
+  cluster_sync();  // its shared memory is read
 }
 
 template <int D, int kFK, int kFV, int kNH>
@@ -326,10 +384,22 @@ cudaError_t sparse_launch(const SparseAttnParams& p, cudaStream_t s) {
   const int64_t per = ((keys + p.q.a.nsplit - 1) / p.q.a.nsplit + 63) / 64 * 64;
   const int64_t entries = std::min(static_cast<int64_t>(p.topk), per / p.q.a.block_size + 2);
   const size_t smem = SparseRing<D, kFK, kFV>::kSmem + static_cast<size_t>(entries) * sizeof(int2);
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+  struct Tag {};
+  cudaError_t e = allow_smem<Tag>(reinterpret_cast<const void*>(k), 200 * 1024);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(p.q.max_q) * p.q.a.nsplit), p.q.a.H, p.q.a.S);
-  KVQ_LAUNCH("sparse_rows_kernel", s, k<<<grid, kAttnThreads, smem, s>>>(p); e = cudaGetLastError());
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kAttnThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(p.q.a.nsplit);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.cluster ? 1 : 0;
+  KVQ_LAUNCH("sparse_rows_kernel", s, e = cudaLaunchKernelEx(&cfg, k, p));
   return e;
 }
 
@@ -349,15 +419,19 @@ cudaError_t sparse_dim(const SparseAttnParams& p, cudaStream_t s) {
 
 int sparse_splits(int32_t T, int32_t H, int32_t D, int32_t topk, int32_t block_size) {
   const int64_t keys = std::min(static_cast<int64_t>(topk) * block_size, int64_t{0x7FFF0000});
-  return fill_splits(static_cast<int64_t>(T) * H, (D == 256 ? 2ll : 4ll) * num_sms(), static_cast<int32_t>(keys), 256, 256);
+  return fill_splits(static_cast<int64_t>(T) * H, (D == 256 ? 2ll : 4ll) * num_sms(), static_cast<int32_t>(keys), 128, 256);
 }
+
+// Not at head_dim 256 (27 lists of 64 16-token blocks in 2 splits: 24.7 us as clusters, 16.3 with the merge
+// kernel).
+bool use_cluster(int32_t D, int nsplit) { return nsplit > 1 && nsplit <= kClusterSplits && D <= 128; }
 
 }  // namespace
 
 size_t sparse_attn_workspace_bytes(int32_t T, int32_t H, int32_t Hq, int32_t D, int32_t block_size, int32_t topk) {
   if (T <= 0 || H <= 0 || Hq < H || D <= 0 || block_size <= 0 || topk <= 0) return 0;
   const int n = sparse_splits(T, H, D, topk, block_size);
-  return n <= 1 ? 0 : static_cast<size_t>(T) * Hq * n * (D + 2) * sizeof(float);
+  return n <= 1 || use_cluster(D, n) ? 0 : static_cast<size_t>(T) * Hq * n * (D + 2) * sizeof(float);
 }
 
 cudaError_t launch_sparse_attention(const SparseAttnParams& p_in, cudaStream_t s) {
@@ -365,8 +439,9 @@ cudaError_t launch_sparse_attention(const SparseAttnParams& p_in, cudaStream_t s
   AttnParams& a = p.q.a;
   p.whole = a.block_size % 16 == 0;
   a.nsplit = sparse_splits(p.q.num_tokens, a.H, a.D, p.topk, a.block_size);
+  p.cluster = use_cluster(a.D, a.nsplit);
   const cudaError_t e = a.D == 64 ? sparse_dim<64>(p, s) : a.D == 128 ? sparse_dim<128>(p, s) : sparse_dim<256>(p, s);
-  return e == cudaSuccess ? launch_query_merge_splits(p.q, s) : e;
+  return e == cudaSuccess && !p.cluster ? launch_query_merge_splits(p.q, s) : e;
 }
 
 }  // namespace kvq

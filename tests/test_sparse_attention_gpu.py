@@ -73,12 +73,14 @@ def test_formats(fmt_k, fmt_v, D, bs, softcap):
     _check(c, lists, out, softcap)
 
 
-@pytest.mark.parametrize("topk,bs", [(40, 64), (300, 16), (1000, 4)])
+@pytest.mark.parametrize("topk,bs", [(40, 64), (300, 16), (1000, 4), (10, 64), (25, 32), (50, 16), (75, 7)])
 @pytest.mark.parametrize("fmt", [PG, NV])
-def test_long_lists_in_splits(topk, bs, fmt):
-    """Few rows with long lists: the list is split over thread blocks and joined again."""
-    c = Paged([5000, 700], [1, 2], 2, 4, 128, bs, fmt, seed=topk)
-    assert kvq.kvq_sparse_attention_workspace(c.T, 2, 8, 128, bs, topk) > 0
+@pytest.mark.parametrize("group,D", [(4, 128), (11, 256), (16, 64)])
+def test_long_lists_in_splits(topk, bs, fmt, group, D):
+    """Few rows with long lists: the list is split over thread blocks and joined again, up to 8 splits
+    in a cluster, more through the workspace."""
+    c = Paged([5000, 700], [1, 2], 2, group, D, bs, fmt, seed=topk)
+    assert (kvq.kvq_sparse_attention_workspace(c.T, 2, 2 * group, D, bs, topk) > 0) == (topk * bs > 1024 or D == 256)
     lists = _lists(c, topk)
     out, st = _run(c, lists)
     assert st == 0 and c.untouched(out, slice(c.starts[-1], c.T))
@@ -194,9 +196,10 @@ def test_nan_scores_reach_their_own_output():
     assert st == 0 and nan[1, 2] and nan.sum() == 1
 
 
-def test_views_graphs_and_streams():
-    c = Paged([3000, 700], [1, 2], 2, 4, 128, 16, seed=12)
-    lists = _lists(c, 100)
+@pytest.mark.parametrize("topk", [50, 300])  # splits that merge in a cluster, and through the workspace
+def test_views_graphs_and_streams(topk):
+    c = Paged([5000, 700], [1, 2], 2, 4, 128, 16, seed=12)
+    lists = _lists(c, topk)
     want, _ = _run(c, lists)
     _check(c, lists, want)
     wide = torch.zeros((c.T, 20, 128), dtype=torch.bfloat16, device=DEV)
@@ -205,14 +208,14 @@ def test_views_graphs_and_streams():
     assert torch.equal(got.view(torch.int16), want.view(torch.int16))
     i32 = lambda v: torch.tensor(np.asarray(v), dtype=torch.int32, device=DEV)
     table, lens, starts, q, sel = c.table.to(DEV), i32(c.lens), i32(c.starts), c.q.to(DEV), i32(lists)
-    size = kvq.kvq_sparse_attention_workspace(c.T, 2, 8, 128, 16, 100)
-    assert size > 0
+    size = kvq.kvq_sparse_attention_workspace(c.T, 2, 8, 128, 16, topk)
+    assert (size > 0) == (topk > 64)
     outs, graphs = [poison_bf16(tuple(c.q.shape)) for _ in range(2)], []
     for o in outs:
-        ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+        ws = torch.empty(max(size, 16), dtype=torch.uint8, device=DEV)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            kvq.kvq_sparse_attention(c.pool, table, lens, 3000, q, starts, 2, sel, c.scale, o, workspace=ws)
+            kvq.kvq_sparse_attention(c.pool, table, lens, 5000, q, starts, 2, sel, c.scale, o, workspace=ws)
         graphs.append((g, ws))
     for g, _ in graphs * 2:
         g.replay()
