@@ -56,7 +56,8 @@ struct SparseRing {
   using T = AttnTile<D, kFK, kFV>;
   static constexpr int kStages = D == 256 && T::kBytes > 4096 ? 3 : T::kBytes > 4096 ? 2 : 4;
   static constexpr int kRing = kAttnWarps * kStages * T::kBytes;
-  static constexpr int kSmem = T::kQ + (kRing > T::kMerge ? kRing : T::kMerge);
+  static constexpr int kMerge = kAttnWarps * 16 * (D + 4) * 4;
+  static constexpr int kSmem = T::kQ + (kRing > kMerge ? kRing : kMerge);
 };
 
 // Up to this many splits of a list are one thread-block cluster and merge through each other's shared
@@ -75,6 +76,19 @@ __device__ __forceinline__ float peer_float(const float* mine, uint32_t rank) {
                : "=r"(at)
                : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(mine))), "r"(rank));
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float4 peer_float4(const float* mine, uint32_t rank) {
+  uint32_t at;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(at)
+               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(mine))), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
   return v;
 }
 
@@ -288,91 +302,89 @@ __global__ void __launch_bounds__(kAttnThreads, D == 128 && kNH == 1 ? 4 : 1) sp
       st.l[nh][0] += __shfl_xor_sync(0xFFFFFFFFu, st.l[nh][0], off);
       st.l[nh][1] += __shfl_xor_sync(0xFFFFFFFFu, st.l[nh][1], off);
     }
-  __syncthreads();  // the ring is free
-
-  float* const mo = reinterpret_cast<float*>(smem + T::kQ) + warp * kRows * (D + 2);
-#pragma unroll
-  for (int q = 0; q < kMT; ++q)
-#pragma unroll
-    for (int nh = 0; nh < kNH; ++nh)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        mo[(8 * nh + 2 * c + (e & 1)) * (D + 2) + g * (D / 8) + 2 * q + (e >> 1)] = st.o[q][nh][e] * st.R;
+  // ---- the warps' parts, on one reference: M of the four, then O and L scaled as they are written ----
+  constexpr int kPitch = D + 4;  // floats of a row
+  __shared__ float warp_m[kAttnWarps][kRows], warp_l[kAttnWarps][kRows];
+  __shared__ __align__(16) float merged[2 * kRows];  // M, then L
   if (g == 0) {
 #pragma unroll
     for (int nh = 0; nh < kNH; ++nh)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        mo[(8 * nh + 2 * c + e) * (D + 2) + D] = st.m[nh][e];
-        mo[(8 * nh + 2 * c + e) * (D + 2) + D + 1] = st.l[nh][e];
-      }
+      for (int e = 0; e < 2; ++e) warp_m[warp][8 * nh + 2 * c + e] = st.m[nh][e];
   }
-  __syncthreads();
-  float* const mall = reinterpret_cast<float*>(smem + T::kQ);
-  __shared__ float merged[2 * kRows];  // of a cluster: M, then L
-  for (int idx = threadIdx.x; idx < rows * D; idx += kAttnThreads) {
-    const int row = idx / D, d = idx % D;
-    float M = kNoKey;
+  __syncthreads();  // and the ring is free
+  float* const mo = reinterpret_cast<float*>(smem + T::kQ);  // [warp][row][kPitch]
 #pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) M = fmaxf(M, mall[(w * kRows + row) * (D + 2) + D]);
-    float L = 0.0f, O = 0.0f;
+  for (int nh = 0; nh < kNH; ++nh)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int row = 8 * nh + 2 * c + e;
+      float M = kNoKey;
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; ++w) M = fmaxf(M, warp_m[w][row]);
+      const float f = ex2(st.m[nh][e] - M), fo = f * st.R;
+      if (g == 0) {
+        warp_l[warp][row] = st.l[nh][e] * f;
+        if (warp == 0) merged[row] = cta_bad ? __int_as_float(0x7FC00000) : M;  // NaN marks a bad block entry (M never is one)
+      }
+      float* const to = mo + (warp * kRows + row) * kPitch + g * (D / 8);
+#pragma unroll
+      for (int q = 0; q < kMT; q += 2)
+        *reinterpret_cast<float4*>(to + 2 * q) = make_float4(st.o[q][nh][e] * fo, st.o[q][nh][e + 2] * fo,
+                                                             st.o[q + 1][nh][e] * fo, st.o[q + 1][nh][e + 2] * fo);
+    }
+  __syncthreads();
+  auto put = [&](int row, int d, float4 o, float L) {
+    uint32_t* const out = reinterpret_cast<uint32_t*>(p.out + tok * p.o_row_pitch +
+                                                      static_cast<int64_t>(h * p.group + row) * p.o_head_pitch + d);
+    const bool none = L == 0.0f;  // a NaN goes on
+    STX(reinterpret_cast<uint2*>(out), make_uint2(none ? 0u : pack_bf16x2(o.x / L, o.y / L), none ? 0u : pack_bf16x2(o.z / L, o.w / L)));
+  };
+  for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kAttnThreads) {
+    const int row = idx / (D / 4), d = 4 * (idx % (D / 4));
+    float L = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int w = 0; w < kAttnWarps; ++w) {
-      const float f = ex2(mall[(w * kRows + row) * (D + 2) + D] - M);
-      L += mall[(w * kRows + row) * (D + 2) + D + 1] * f;
-      O += mall[(w * kRows + row) * (D + 2) + d] * f;
+      const float4 x = *reinterpret_cast<const float4*>(mo + (w * kRows + row) * kPitch + d);
+      L += warp_l[w][row];
+      o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
     }
-    const float mark = cta_bad ? __int_as_float(0x7FC00000) : M;  // NaN marks a bad block entry (M never is one)
-    const int qh = h * p.group + row;
     if (p.nsplit == 1) {
-      if (cta_bad) continue;
-      const float y = L == 0.0f ? 0.0f : O / L;
-      STX(p.out + tok * p.o_row_pitch + static_cast<int64_t>(qh) * p.o_head_pitch + d,
-          static_cast<uint16_t>(pack_bf16x2(y, 0.0f) & 0xFFFFu));
+      if (!cta_bad) put(row, d, o, L);
     } else if (sp.cluster) {
-      mall[row * (D + 2) + d] = O;  // what no other thread reads
-      if (d == 0) {
-        merged[row] = mark;
-        merged[kRows + row] = L;
-      }
+      *reinterpret_cast<float4*>(mo + row * kPitch + d) = o;  // what no other thread reads
+      if (d == 0) merged[kRows + row] = L;
     } else {
-      float* const wsr = p.ws + ((tok * p.Hq + qh) * p.nsplit + split) * (D + 2);
-      STX(wsr + d, O);
-      if (d == 0) {
-        STX(wsr + D, mark);
-        STX(wsr + D + 1, L);
-      }
+      float* const wsr = p.ws + ((tok * p.Hq + h * p.group + row) * p.nsplit + split) * (D + 2);
+      STX(reinterpret_cast<float2*>(wsr + d), make_float2(o.x, o.y));
+      STX(reinterpret_cast<float2*>(wsr + d + 2), make_float2(o.z, o.w));
+      if (d == 0) STX(reinterpret_cast<float2*>(wsr + D), make_float2(merged[row], L));
     }
   }
   if (!sp.cluster) return;
   cluster_sync();
-  // pairs of channels, shared among the cluster's blocks (block `split` of it is this one)
-  for (int idx = split * kAttnThreads + static_cast<int>(threadIdx.x); idx < rows * (D / 2); idx += p.nsplit * kAttnThreads) {
-    const int row = idx / (D / 2), d = 2 * (idx % (D / 2));
-    float m[kClusterSplits], l[kClusterSplits], o0[kClusterSplits], o1[kClusterSplits], M = kNoKey;
+  // four channels a thread, shared among the cluster's blocks (block `split` of it is this one)
+  for (int idx = split * kAttnThreads + static_cast<int>(threadIdx.x); idx < rows * (D / 4); idx += p.nsplit * kAttnThreads) {
+    const int row = idx / (D / 4), d = 4 * (idx % (D / 4));
+    float m[kClusterSplits], M = kNoKey;
     bool skip = false;
 #pragma unroll
     for (int x = 0; x < kClusterSplits; ++x) {
-      if (x >= p.nsplit) break;
-      m[x] = peer_float(merged + row, x);
-      l[x] = peer_float(merged + kRows + row, x);
-      o0[x] = peer_float(mall + row * (D + 2) + d, x);
-      o1[x] = peer_float(mall + row * (D + 2) + d + 1, x);
+      m[x] = x < p.nsplit ? peer_float(merged + row, x) : kNegInf;
       skip = skip || isnan(m[x]);
       M = fmaxf(M, m[x]);
     }
-    float L = 0.0f, a = 0.0f, b = 0.0f;
-#pragma unroll
-    for (int x = 0; x < kClusterSplits; ++x) {
-      if (x >= p.nsplit) break;
-      const float f = ex2(m[x] - M);
-      L = __fmaf_rn(l[x], f, L);
-      a = __fmaf_rn(o0[x], f, a);
-      b = __fmaf_rn(o1[x], f, b);
+    float L = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+    for (int x = 0; x < p.nsplit; ++x) {
+      const float4 y = peer_float4(mo + row * kPitch + d, x);
+      float f = ex2(peer_float(merged + row, x) - M);
+      L = __fmaf_rn(peer_float(merged + kRows + row, x), f, L);
+      o.x = __fmaf_rn(y.x, f, o.x), o.y = __fmaf_rn(y.y, f, o.y), o.z = __fmaf_rn(y.z, f, o.z), o.w = __fmaf_rn(y.w, f, o.w);
     }
-    if (skip) continue;
-    STX(reinterpret_cast<uint32_t*>(p.out + tok * p.o_row_pitch + static_cast<int64_t>(h * p.group + row) * p.o_head_pitch + d),
-        L == 0.0f ? 0u : pack_bf16x2(a / L, b / L));
+    if (!skip) put(row, d, o, L);
   }
   cluster_sync();  // its shared memory is read
 }
