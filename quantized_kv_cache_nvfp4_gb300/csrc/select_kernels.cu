@@ -349,13 +349,13 @@ struct ScoreTile {
   static constexpr int kStage = kN * kPitch;
   static constexpr int kOffTop = kOffB + 2 * kStage;  // largest |bound| of each channel, f32
   static constexpr int kSmem = kOffTop + 2 * D * 4;
-  static constexpr int kWarps = 8;  // and one that copies
+  static constexpr int kWarps = D == 256 ? 8 : 16;  // 2 by kWarps / 2 over the tile; and one that copies
 };
 
 template <int D>
 __global__ void __launch_bounds__(32 * (ScoreTile<D>::kWarps + 1), 1) score_tile_kernel(const SelectParams p) {
   using T = ScoreTile<D>;
-  constexpr int kMT = T::kM / 32, kNT = T::kN / 32, kThreads = 32 * T::kWarps;
+  constexpr int kMT = T::kM / 32, kNT = T::kN / (4 * T::kWarps), kThreads = 32 * T::kWarps;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ __align__(8) uint64_t bars[4];  // full and empty, a stage each
   __shared__ uint32_t have[2][T::kN / 32];
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(32 * (ScoreTile<D>::kWarps + 1), 1) score_tile
   }
   together();
 
-  const int m0 = (warp & 1) * (T::kM / 2), n0 = (warp >> 1) * (T::kN / 4);
+  const int m0 = (warp & 1) * (T::kM / 2), n0 = (warp >> 1) * (8 * kNT);
   const uint32_t a_at = base + (m0 + (lane & 15)) * T::kPitch + (lane >> 4) * 16;
   const uint32_t b_row = (n0 + (lane & 7) + ((lane >> 4) << 3)) * T::kPitch + ((lane >> 3) & 1) * 16;
   uint32_t top[2 * D / kThreads > 0 ? 2 * D / kThreads : 1] = {};
@@ -520,21 +520,23 @@ __global__ void __launch_bounds__(32 * (ScoreTile<D>::kWarps + 1), 1) score_tile
             : "=r"(top[x])
             : "r"(top[x]), "r"(*reinterpret_cast<const uint32_t*>(tile + r * T::kPitch + 4 * word)));
     }
-    const int g = lane >> 2, c = lane & 3;
+    const int g = lane >> 2, c = lane & 3, col0 = n0 + 2 * c, left = last - (first + t * T::kN);
+    uint32_t* const to = p.keys + (static_cast<int64_t>(tok0 + m0 + g) * p.H + h) * p.pitch + first + t * T::kN;
+    const int64_t rows8 = static_cast<int64_t>(8 * p.H) * p.pitch;
 #pragma unroll
-    for (int a = 0; a < kMT; ++a)
+    for (int b = 0; b < kNT; ++b) {
+      const int col = col0 + 8 * b;
+      const uint32_t ok = have[st][col / 32] >> (col % 32);
 #pragma unroll
-      for (int b = 0; b < kNT; ++b)
+      for (int a = 0; a < kMT; ++a)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int i = m0 + 16 * a + g + 8 * e, col = n0 + 8 * b + 2 * c, at = first + t * T::kN + col;
-          if (i >= nq || at >= last) continue;
-          uint32_t* const to = p.keys + (static_cast<int64_t>(tok0 + i) * p.H + h) * p.pitch + at;
-          const uint32_t ok = have[st][col / 32] >> (col % 32);
-          const uint2 v = make_uint2(ok & 1u ? score_key(acc[a][b][2 * e]) : kKeyBad,
-                                     ok & 2u ? score_key(acc[a][b][2 * e + 1]) : kKeyBad);
-          STX(reinterpret_cast<uint2*>(to), v);  // pitch is even: the pair lies in the row
+          if (m0 + 16 * a + g + 8 * e >= nq || col >= left) continue;
+          uint2 v = make_uint2(score_key(acc[a][b][2 * e]), score_key(acc[a][b][2 * e + 1]));
+          if ((ok & 3u) != 3u) v = make_uint2(ok & 1u ? v.x : kKeyBad, ok & 2u ? v.y : kKeyBad);
+          STX(reinterpret_cast<uint2*>(to + (2 * a + e) * rows8 + col), v);  // pitch is even: the pair lies in the row
         }
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(empty0 + 8 * st);  // this warp has read the stage, and its notes
   }
@@ -1045,7 +1047,8 @@ cudaError_t select_dim(SelectParams& p, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   const bool scores = p.most > p.topk;
   if (scores && (e = score_launch<D>(p, s)) != cudaSuccess) return e;
-  // threads of a list: a warp where lists are many and short
+  // threads of a list: a warp where lists are many and short (8192 lists of 1024 blocks: 91 us with their scores,
+  // 101 by 128 threads, 96 by 64; 32 lists of 375: 10.6 by 128, 12.3 by a warp)
   const int64_t lists = static_cast<int64_t>(p.max_q) * p.H * p.S;
   const bool many = lists >= 8 * num_sms();
   KVQ_LAUNCH("select_kernel", s,

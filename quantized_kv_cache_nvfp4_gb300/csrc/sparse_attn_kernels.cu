@@ -49,8 +49,9 @@ struct SparseMod {
 };
 
 // The ring and shared memory of a thread block.  Two stages where a tile is over 4 KB: four blocks an SM
-// instead of three, and one tile a warp ahead (32 lists of 128 16-token blocks, 8 KV heads, head_dim
-// 128, page scales: XX us; with three stages YY).
+// instead of three, and one tile a warp ahead (32 x 8 lists of 128 16-token blocks, head_dim 128, page
+// scales: 36.6 us, with three stages 38.2; 512 x 8 lists of 32 64-token blocks 282 and 316).  Three at
+// head_dim 256, where two blocks fit either way (27 x 4 lists 16.1 us, with two stages 18.5).
 template <int D, int kFK, int kFV>
 struct SparseRing {
   using T = AttnTile<D, kFK, kFV>;
@@ -429,6 +430,8 @@ cudaError_t sparse_dim(const SparseAttnParams& p, cudaStream_t s) {
   return p.q.a.group <= 8 ? sparse_fmt<D, 1>(p, s) : sparse_fmt<D, 2>(p, s);
 }
 
+// Splits of a list: as many as the resident blocks take at once, of 128 keys or more (4 x 8 lists of 512 keys:
+// 7.9 us, of 256 keys or more 9.1; 16 x 8 lists of up to 1536 do as well with half as many, 19.7 against 21.9).
 int sparse_splits(int32_t T, int32_t H, int32_t D, int32_t topk, int32_t block_size) {
   const int64_t keys = std::min(static_cast<int64_t>(topk) * block_size, int64_t{0x7FFF0000});
   return fill_splits(static_cast<int64_t>(T) * H, (D == 256 ? 2ll : 4ll) * num_sms(), static_cast<int32_t>(keys), 128, 256);

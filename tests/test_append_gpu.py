@@ -262,3 +262,48 @@ def test_graph_and_side_stream():
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     assert c.append(_rows(2, H, D, 90), _rows(2, H, D, 91), [20, 52], [20, 21], cs, q=_rows(2, Hq, D, 92), stream=side) == 0
+
+
+def test_overlapping_queries_are_refused():
+    """q_out may be q itself or lie elsewhere, beside it in a fused row too; nothing in between."""
+    H, D, bs, T = 2, 64, 16, 8
+    pool = kvq.KvPool.empty(32, H, D, bs, fill=0, fmt=F8)
+    x = _rows(T + 1, 8, D, 1).to(DEV)
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)
+    call = lambda q, o, k: kvq.kvq_append(k, k, torch.arange(T, device=DEV), pool, cos_sin=X.angles(T, D).to(DEV), positions=pos,
+                                          q=q, q_out=o)
+    other = _rows(T, H, D, 2).to(DEV)
+    for q, o, k in ((x[:T, :4], x[1:, :4], other), (x[:T, :4], x[:T, 1:5], other), (x[:T, :4], x[:T, 3:7], other),
+                    (x[:T, :2], x[:T, 4:6], x[:T, 5:7]), (other, x[:T, :2], x[:T, 1:3])):
+        with pytest.raises(kvq.KvqError, match="overlaps"):
+            call(q, o, k)
+    before = x.clone()
+    call(x[:T, :2], x[:T, 4:6], x[:T, 6:])  # side by side in one row
+    torch.cuda.synchronize()
+    want = torch.tensor(X.turned(before[:T, :2].float().cpu().numpy(), X.angles(T, D).numpy(), False)).to(torch.bfloat16)
+    assert torch.equal(x[:T, 4:6].cpu(), want) and torch.equal(x[:T, :4], before[:T, :4]) and torch.equal(x[:T, 6:], before[:T, 6:])
+
+
+def test_host_memory_is_refused():
+    H, D, T = 2, 64, 4
+    pool = kvq.KvPool.empty(32, H, D, 16, fill=0, fmt=F8)
+    k, slots = _rows(T, H, D, 1), torch.arange(T)
+    for args in ((k, k.to(DEV), slots.to(DEV)), (k.to(DEV), k.to(DEV), slots)):
+        with pytest.raises(kvq.KvqError, match="NOT_DEVICE_PTR"):
+            kvq.kvq_append(*args, pool)
+
+
+@pytest.mark.parametrize("rows", [33, 64, 100, 161])
+@pytest.mark.parametrize("D", [64, 256, 512])
+def test_blocks_of_many_rows(rows, D):
+    """Blocks of 160 tokens, longer than a warp's stage and than a chunk of tokens, begun, continued and
+    rescaled."""
+    H, bs = 2, 160
+    c = Cache(4, H, D, bs, PG, PG)
+    cs = X.angles(400, D)
+    at = 0
+    for i, f in enumerate((1.0, 5.0, 0.5)):
+        slots = np.arange(at, at + rows) + 7
+        st = c.append(_rows(rows, H, D, i, f), _rows(rows, H, D, 9 + i, 2 * f), slots, np.arange(at, at + rows) % 400, cs)
+        assert st == 0
+        at += rows

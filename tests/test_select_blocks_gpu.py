@@ -48,9 +48,10 @@ class Case:
         np.testing.assert_array_equal(got, self.want(topk, first, last))
 
 
-@pytest.mark.parametrize("lens,new", [([1], [1]), ([16, 17, 700], [1, 1, 1]), ([900, 0, 333], [4, 0, 7]), ([500], [300]),
+@pytest.mark.parametrize("lens,new", [([1], [1]), ([800, 90], [3, 4]), ([800, 90], [2, 1]), ([1600, 40], [8, 5]), ([16, 17, 700], [1, 1, 1]), ([900, 0, 333], [4, 0, 7]), ([500], [300]),
                                       ([64, 2000], [64, 9])])
-@pytest.mark.parametrize("H,g,D,bs", [(2, 4, 128, 16), (1, 16, 64, 8), (3, 7, 256, 32), (8, 1, 128, 64), (2, 3, 64, 1)])
+@pytest.mark.parametrize("H,g,D,bs", [(2, 4, 128, 16), (1, 16, 64, 8), (3, 7, 256, 32), (8, 1, 128, 64), (2, 3, 64, 1),
+                                      (12, 2, 64, 16), (11, 1, 128, 16), (5, 2, 256, 16)])
 def test_lists(lens, new, H, g, D, bs):
     c = Case(lens, new, H, g, D, bs, seed=D + bs)
     for topk, first, last in ((5, 1, 2), (16, 0, 0), (1, 1, 0), (40, 20, 20)):
