@@ -85,16 +85,22 @@ __device__ __forceinline__ void sum_heads(const SelectParams& p, int tok, int h,
   const uint16_t* const x = p.q + tok * p.q_row_pitch + static_cast<int64_t>(h) * p.group * p.q_head_pitch + d;
 #pragma unroll
   for (int i = 0; i < 8; ++i) minus[i] = plus[i] = 0.0f;
-#pragma unroll 4
-  for (int j = 0; j < p.group; ++j) {
-    uint32_t v[4];
-    load16B(x + j * p.q_head_pitch, v);
+#pragma unroll 1
+  for (int j0 = 0; j0 < p.group; j0 += 8) {  // 8 heads' loads at a time: the loop waits for memory
+    uint32_t v[8][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float y = i % 2 == 0 ? bf16lo(v[i / 2]) : bf16hi(v[i / 2]);
-      minus[i] = __fadd_rn(minus[i], y > 0.0f ? 0.0f : y);  // a NaN goes on
-      plus[i] = __fadd_rn(plus[i], y > 0.0f ? y : 0.0f);
+    for (int j = 0; j < 8; ++j) {
+      v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0u;
+      if (j0 + j < p.group) load16B(x + (j0 + j) * p.q_head_pitch, v[j]);
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float y = i % 2 == 0 ? bf16lo(v[j][i / 2]) : bf16hi(v[j][i / 2]);
+        minus[i] = __fadd_rn(minus[i], y > 0.0f ? 0.0f : y);  // a NaN goes on
+        plus[i] = __fadd_rn(plus[i], y > 0.0f ? y : 0.0f);
+      }
   }
 }
 
@@ -743,36 +749,56 @@ __device__ __forceinline__ float two_sum(float a, float b, float& e) {
   return s;
 }
 
-// The score of one block in twice binary32's precision, by a warp: sum + rest, in all lanes.  Lanes take 8
-// channels of q- . lo, q+ . hi at a time.
+// The score of one block in twice binary32's precision, by a warp, as an ordered integer; NaN: 0.  Lanes take 8
+// channels of q- . lo, q+ . hi at a time, with kC such chunks' (2 at head_dim 256) and kJ heads' loads in flight
+// (one and two where many lists share an SM: two and four cost the kernel 40 registers, 8192 lists 10 us).
+template <int kC, int kJ>
 __device__ __noinline__ uint64_t score_pair(const SelectParams& p, int tok, int h, int64_t blk) {
   const int lane = threadIdx.x & 31;
+  const uint16_t* const q = p.q + tok * p.q_row_pitch + static_cast<int64_t>(h) * p.group * p.q_head_pitch;
   float sum = 0.0f, rest = 0.0f;
-  for (int d = 8 * lane; d < 2 * p.D; d += 256) {
-    const bool low = d < p.D;
-    float qh[8] = {}, ql[8] = {};
-    const uint16_t* const q = p.q + tok * p.q_row_pitch + static_cast<int64_t>(h) * p.group * p.q_head_pitch + (low ? d : d - p.D);
-    uint32_t w[4];
-#pragma unroll 2
-    for (int j = 0; j < p.group; ++j) {
-      load16B(q + j * p.q_head_pitch, w);
+#pragma unroll 1
+  for (int d0 = 8 * lane; d0 < 2 * p.D; d0 += 256 * kC) {
+    uint32_t w[kC][4] = {};
+    float qh[kC][8] = {}, ql[kC][8] = {};
+#pragma unroll
+    for (int c = 0; c < kC; ++c)
+      if (d0 + 256 * c < 2 * p.D) load16B(p.bounds + (blk * p.H + h) * (2 * p.D) + d0 + 256 * c, w[c]);
+#pragma unroll 1
+    for (int j0 = 0; j0 < p.group; j0 += kJ) {
+      uint32_t v[kJ][kC][4];
+#pragma unroll
+      for (int j = 0; j < kJ; ++j)
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+          const int d = d0 + 256 * c;
+          v[j][c][0] = v[j][c][1] = v[j][c][2] = v[j][c][3] = 0u;
+          if (d < 2 * p.D && j0 + j < p.group) load16B(q + (j0 + j) * p.q_head_pitch + (d < p.D ? d : d - p.D), v[j][c]);
+        }
+#pragma unroll
+      for (int j = 0; j < kJ; ++j)
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+          const bool low = d0 + 256 * c < p.D;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const float y = x % 2 == 0 ? bf16lo(v[j][c][x / 2]) : bf16hi(v[j][c][x / 2]);
+            float e;
+            qh[c][x] = two_sum(qh[c][x], low != (y > 0.0f) ? y : 0.0f, e);
+            ql[c][x] = __fadd_rn(ql[c][x], e);
+          }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < kC; ++c)
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
-        const float v = x % 2 == 0 ? bf16lo(w[x / 2]) : bf16hi(w[x / 2]);
+        const float y = x % 2 == 0 ? bf16lo(w[c][x / 2]) : bf16hi(w[c][x / 2]);
+        const float t = __fmul_rn(qh[c][x], y);
         float e;
-        qh[x] = two_sum(qh[x], low != (v > 0.0f) ? v : 0.0f, e);
-        ql[x] = __fadd_rn(ql[x], e);
+        sum = two_sum(sum, t, e);
+        rest = __fadd_rn(rest, __fadd_rn(e, __fmaf_rn(ql[c][x], y, __fmaf_rn(qh[c][x], y, -t))));
       }
-    }
-    load16B(p.bounds + (blk * p.H + h) * (2 * p.D) + d, w);
-#pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      const float v = x % 2 == 0 ? bf16lo(w[x / 2]) : bf16hi(w[x / 2]);
-      const float t = __fmul_rn(qh[x], v);
-      float e;
-      sum = two_sum(sum, t, e);
-      rest = __fadd_rn(rest, __fadd_rn(e, __fmaf_rn(ql[x], v, __fmaf_rn(qh[x], v, -t))));
-    }
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) {
@@ -899,7 +925,7 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) select_kernel
       if (m <= kFewTies && m >= need && size > 0x1p-60f && size < 0x1p100f) {
         // few, and nothing that overflows or underflows: a warp scores one at a time, then each one's rank
         for (uint32_t x = warp; x < m; x += kWarps) {
-          const uint64_t u = score_pair(p, q0 + i, h, LDX(table + sh.entry[x]));
+          const uint64_t u = score_pair<kThreads == 32 ? 1 : 2, kThreads == 32 ? 2 : 4>(p, q0 + i, h, LDX(table + sh.entry[x]));
           if (lane == 0) sh.score[x] = u;
         }
         th.sync();
