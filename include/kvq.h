@@ -101,7 +101,7 @@ typedef enum { KVQ_KIND_KEY = 0, KVQ_KIND_VALUE = 1 } kvq_kind;
 #define KVQ_DEV_BAD_POS 4u    /* position outside [0, rows) or not strictly increasing; append: past the angles */
 #define KVQ_DEV_BAD_SEQLEN 8u /* seq_lens[s] outside [0, min(max_seq_len, blocks*block_size)] */
 #define KVQ_DEV_NO_SPACE 32u  /* page plan: the free list or the token arrays ran out (request refused) */
-#define KVQ_DEV_TIMEOUT 16u   /* decode attention: a bounded wait for a copy ran out (results unspecified) */
+#define KVQ_DEV_TIMEOUT 16u   /* attention, block choice: a bounded wait for a copy ran out (results unspecified) */
 
 /* A bf16 view: element (r, h, d) is ptr[r*row_pitch + h*head_pitch + d].
  * ptr must be 16-byte aligned and both pitches multiples of 8 elements. */
@@ -450,8 +450,9 @@ KVQ_API size_t kvq_attention_workspace(int32_t num_seqs, int32_t num_tokens, int
  *   topk; sequences of up to 32768 blocks (any number where topk reaches for all of them).
  *   workspace      device memory of kvq_select_blocks_workspace(...) bytes, 16-byte aligned;
  *                  caller-owned; one for each call that may run at the same time.
- * The list is that of the exact scores: what binary32 cannot tell apart is scored again in
- * binary64 (equal up to its rounding counts as equal).  A NaN score ranks below all numbers, and a
+ * The list is that of the exact scores: what binary32 cannot tell apart is scored again, in pairs of
+ * binary32 numbers or in binary64 (scores of unlike blocks that agree to 2^-38 of their terms' size may go
+ * either way).  A NaN score ranks below all numbers, and a
  * block whose table entry lies outside the pool below that (KVQ_DEV_BAD_BLOCK, where scores are needed).
  * Two kernel launches (one where topk reaches for all blocks of max_seq_len); may be captured in
  * a CUDA graph. */
