@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace kvq {
 
 // Exact unsigned division of n < 2^31 by a fixed divisor d >= 1 with one
@@ -414,7 +416,7 @@ int num_sms();
 // type), so that eager calls do not repeat the attribute's call.
 template <typename Tag>
 cudaError_t allow_smem(const void* kernel, size_t bytes) {
-  static bool told[64];
+  static std::atomic<bool> told[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && told[dev]) return cudaSuccess;

@@ -679,7 +679,7 @@ __device__ __forceinline__ Border find_border(const uint32_t (&key)[P], uint32_t
   constexpr int kBins = ListShared<kThreads>::kBins, kEach = kBins / kThreads, kBits = kThreads == 32 ? 8 : 10;
   const int lane = threadIdx.x & 31, me = threadIdx.x % kThreads;
   uint32_t above = 0u, inside = 0u;
-  while (true) {
+  for (int round = 0;; ++round) {
     const int shift = max(0, 32 - __clz(to - from) - kBits);
 #pragma unroll
     for (int x = 0; x < kEach; ++x) sh.bin[me + x * kThreads] = 0u;
@@ -710,15 +710,17 @@ __device__ __forceinline__ Border find_border(const uint32_t (&key)[P], uint32_t
     from = low;
     above = sh.found[1];
     inside = sh.found[2];
-    if (inside <= 32u || from == to) break;
+    // four rounds narrow 32 bits; keys that another call overwrote (a shared workspace) end here as well
+    if (inside <= 32u || from >= to || round == 4) break;
     th.sync();  // found is read before it is written again
   }
+  inside = from != to ? min(inside, 32u) : inside;
   Border at{from, from, above + inside};
   uint32_t below = 0u;  // the largest key below `from`
 #pragma unroll
   for (int j = 0; j < P; ++j) {
     if (key[j] < from) below = max(below, key[j]);
-    if (from != to && key[j] - from <= to - from) sh.entry[atomicAdd(&sh.count, 1u)] = key[j];
+    if (from != to && key[j] - from <= to - from) sh.entry[atomicAdd(&sh.count, 1u) % kFewTies] = key[j];
   }
   below = th.max(below);  // (a barrier, or)
   if constexpr (kThreads == 32) __syncwarp();
