@@ -753,7 +753,8 @@ __device__ __forceinline__ float two_sum(float a, float b, float& e) {
 
 // The score of one block in twice binary32's precision, by a warp, as an ordered integer; NaN: 0.  Lanes take 8
 // channels of q- . lo, q+ . hi at a time, with kC such chunks' (2 at head_dim 256) and kJ heads' loads in flight
-// (one and two where many lists share an SM: two and four cost the kernel 40 registers, 8192 lists 10 us).
+// (one and two where many lists share an SM, or where 1024 threads have 64 registers each: two and four cost
+// 40 registers, 8192 lists 10 us, 32 lists of 30,000 blocks 10 of 127).
 template <int kC, int kJ>
 __device__ __noinline__ uint64_t score_pair(const SelectParams& p, int tok, int h, int64_t blk) {
   const int lane = threadIdx.x & 31;
@@ -927,7 +928,8 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) select_kernel
       if (m <= kFewTies && m >= need && size > 0x1p-60f && size < 0x1p100f) {
         // few, and nothing that overflows or underflows: a warp scores one at a time, then each one's rank
         for (uint32_t x = warp; x < m; x += kWarps) {
-          const uint64_t u = score_pair<kThreads == 32 ? 1 : 2, kThreads == 32 ? 2 : 4>(p, q0 + i, h, LDX(table + sh.entry[x]));
+          constexpr bool kNarrow = kThreads == 32 || kThreads == 1024;
+          const uint64_t u = score_pair<kNarrow ? 1 : 2, kNarrow ? 2 : 4>(p, q0 + i, h, LDX(table + sh.entry[x]));
           if (lane == 0) sh.score[x] = u;
         }
         th.sync();
@@ -1076,7 +1078,8 @@ cudaError_t select_dim(SelectParams& p, cudaStream_t s) {
   const bool scores = p.most > p.topk;
   if (scores && (e = score_launch<D>(p, s)) != cudaSuccess) return e;
   // threads of a list: a warp where lists are many and short (8192 lists of 1024 blocks: 91 us with their scores,
-  // 101 by 128 threads, 96 by 64; 32 lists of 375: 10.6 by 128, 12.3 by a warp)
+  // 101 by 128 threads, 96 by 64; 32 lists of 375: 10.6 by 128, 12.3 by a warp).  1024 threads have 64 registers
+  // each and spill, so they take only the longest (32 lists of 12,500: 61.5, by 1024 threads 72.7)
   const int64_t lists = static_cast<int64_t>(p.max_q) * p.H * p.S;
   const bool many = lists >= 8 * num_sms();
   KVQ_LAUNCH("select_kernel", s,
@@ -1085,6 +1088,7 @@ cudaError_t select_dim(SelectParams& p, cudaStream_t s) {
                  : p.most <= 512          ? select_launch<128, 4>(p, scores, s)
                  : p.most <= 2048         ? select_launch<256, 8>(p, scores, s)
                  : p.most <= 8192         ? select_launch<512, 16>(p, scores, s)
+                 : p.most <= 16384        ? select_launch<512, 32>(p, scores, s)
                                           : select_launch<1024, 32>(p, scores, s));
   return e;
 }

@@ -58,7 +58,8 @@ def test_lists(lens, new, H, g, D, bs):
         c.check(topk, first, last)
 
 
-@pytest.mark.parametrize("blocks,topk", [(512, 100), (513, 100), (4096, 64), (4097, 64), (20000, 300), (32768, 2000)])
+@pytest.mark.parametrize("blocks,topk", [(512, 100), (513, 100), (4096, 64), (4097, 64), (8193, 64), (16384, 100),
+                                         (16385, 100), (20000, 300), (32768, 2000)])
 def test_many_blocks(blocks, topk):
     """At and past the sizes at which a wider thread block takes over."""
     bs = 16 if blocks < 20000 else 2
