@@ -184,18 +184,24 @@ __device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Slot of token t: -1 where it is skipped.  `report`: the block that speaks for the token.
-__device__ __forceinline__ int64_t append_slot(const AppendParams& p, int64_t t, bool report, int& pos) {
-  pos = 0;
-  if (t < 0 || t >= p.T) return -1;
-  const int64_t s = LDX(p.slot_ids + t);
-  if (s >= p.num_slots && report) set_status(p.status, 1u);
-  if (p.cos_sin != nullptr) {
-    pos = LDX(p.positions + t);
-    if (pos >= p.num_positions && report) set_status(p.status, 4u);
-    if (pos < 0 || pos >= p.num_positions) return -1;
-  }
-  return s >= p.num_slots ? -1 : s;
+// A token's slot and position as they stand in memory; nothing (a negative slot) for tokens outside the call.
+struct Token {
+  int64_t slot;
+  int pos;
+};
+__device__ __forceinline__ Token load_token(const AppendParams& p, int64_t t) {
+  Token k{-1, 0};
+  if (t < 0 || t >= p.T) return k;
+  k.slot = LDX(p.slot_ids + t);
+  if (p.cos_sin != nullptr) k.pos = LDX(p.positions + t);
+  return k;
+}
+// Its slot: -1 where it is skipped.  `report`: the block that speaks for the token.
+__device__ __forceinline__ int64_t token_slot(const AppendParams& p, const Token& k, bool report) {
+  if (k.slot >= p.num_slots && report) set_status(p.status, 1u);
+  if (k.pos >= p.num_positions && p.cos_sin != nullptr && report) set_status(p.status, 4u);
+  const bool turned = p.cos_sin == nullptr || (k.pos >= 0 && k.pos < p.num_positions);
+  return k.slot >= p.num_slots || !turned ? -1 : k.slot;
 }
 
 // The runs that begin in a chunk of tokens, and the chunk's tokens.
@@ -213,15 +219,17 @@ __device__ __forceinline__ void find_runs(const AppendParams& p, int64_t t0, boo
   auto page_of = [&](int64_t slot) -> int64_t {
     return slot < 0 ? -1 : p.small ? static_cast<int64_t>(p.div_bs.div(static_cast<uint32_t>(slot))) : slot / p.block_size;
   };
-  int pos, unused;
-  const int64_t slot = append_slot(p, t0 + lane, report, pos);
+  // all loads at once (one behind the other they were most of a block's start: K of 27,000 tokens XX us, YY)
+  const Token token = load_token(p, t0 + lane), ahead = load_token(p, lane == 0 ? t0 - 1 : -1);
+  Token behind = load_token(p, t0 + 32 + lane);
+  const int64_t slot = token_slot(p, token, report);
   const int64_t page = page_of(slot);
-  const int64_t before = lane == 0 ? page_of(append_slot(p, t0 - 1, false, unused)) : -1;
+  const int64_t before = page_of(token_slot(p, ahead, false));
   int64_t prev = __shfl_up_sync(0xFFFFFFFFu, page, 1);
   if (lane == 0) prev = before;
   const int place = page < 0 ? 0 : static_cast<int>(slot - page * p.block_size);
   ck.place[lane] = place;
-  ck.pos[lane] = pos;
+  ck.pos[lane] = token.pos;
   const uint32_t leaders = __ballot_sync(0xFFFFFFFFu, lane < p.chunk && page >= 0 && page != prev);
   const uint32_t same = __ballot_sync(0xFFFFFFFFu, page >= 0 && page == prev);  // goes on with the token before
   const uint32_t firsts = __ballot_sync(0xFFFFFFFFu, page >= 0 && place == 0);
@@ -243,12 +251,13 @@ __device__ __forceinline__ void find_runs(const AppendParams& p, int64_t t0, boo
     int n = ck.length[last];
     bool begins = ck.begins[last];
     for (int64_t t = t0 + 32; t < p.T; t += 32) {
-      const int64_t s2 = append_slot(p, t + lane, false, unused);
+      const int64_t s2 = token_slot(p, behind, false);
       const int64_t p2 = page_of(s2);
       const int m = run_bits(__ballot_sync(0xFFFFFFFFu, p2 == pg));
       begins = begins || __any_sync(0xFFFFFFFFu, lane < m && s2 == pg * p.block_size);
       n += m;
       if (m < 32) break;
+      behind = load_token(p, t + 32 + lane);
     }
     __syncwarp();
     if (lane == 0) {
