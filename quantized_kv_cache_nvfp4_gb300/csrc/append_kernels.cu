@@ -21,10 +21,10 @@
 // turn Q: a warp holds a token's angles in registers and walks its heads (evenly among the others it took 5%
 // longer).
 //
-// Bound: HBM for Q, issue and the two resident blocks an SM (128 registers a thread) for K and V.
+// Bound: HBM for Q, issue and 16 resident warps an SM (128 registers a thread) for K and V.
 // Measured: 27,000 tokens of 24 prompts, 32 and 8 heads, head_dim 128, FP8 rows of K and pages of V, 16-token
-// blocks, with bounds: 139 us, 4.5 TB/s, 67% of a plain copy's rate; Q alone 73 us (91%), K 53, V
-// 32; 64 single tokens 5 us.  (Without packed products 2 us more; stages of 8 KB, one block an SM: 236.)
+// blocks, with bounds: 128 us, 4.8 TB/s, 72% of a plain copy's rate; Q alone 71 us (93%), K 54, V
+// 32; 64 single tokens 5 us.  (Without packed products 2 us more; stages of 8 KB, half the warps: 236.)
 #include "page_scale.cuh"
 #include "kvq_params.h"
 
@@ -32,7 +32,9 @@ namespace kvq {
 
 namespace {
 
-constexpr int kAppendWarps = 8;
+// Four warps a block, four blocks an SM (24 prompts as above: 128 us; eight warps and two blocks 136, two and
+// eight 135: Q's blocks start as those of K and V end one by one).
+constexpr int kAppendWarps = 4, kAppendBlocks = 4;
 constexpr int kChunk = 32;  // most tokens of a block
 
 // The two 8-channel chunks of a lane: c and c + half of the turned channels where those are rot / 2 apart
@@ -219,7 +221,7 @@ __device__ __forceinline__ void find_runs(const AppendParams& p, int64_t t0, boo
   auto page_of = [&](int64_t slot) -> int64_t {
     return slot < 0 ? -1 : p.small ? static_cast<int64_t>(p.div_bs.div(static_cast<uint32_t>(slot))) : slot / p.block_size;
   };
-  // all loads at once (one behind the other they were most of a block's start: K of 27,000 tokens XX us, YY)
+  // all loads at once (one behind the other they were most of a block's start; K of 27,000 tokens 39.6 us, 36.6)
   const Token token = load_token(p, t0 + lane), ahead = load_token(p, lane == 0 ? t0 - 1 : -1);
   Token behind = load_token(p, t0 + 32 + lane);
   const int64_t slot = token_slot(p, token, report);
@@ -580,7 +582,7 @@ __device__ __forceinline__ void append_turn_q(const AppendParams& p, int64_t w) 
 }
 
 template <int L>
-__global__ void __launch_bounds__(32 * kAppendWarps, 2) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(32 * kAppendWarps, kAppendBlocks) append_kernel(const AppendParams p) {
   __shared__ Chunk ck;
   extern __shared__ __align__(16) unsigned char stages[];
   const int warp = threadIdx.x >> 5;
@@ -607,17 +609,19 @@ cudaError_t append_launch(const AppendParams& p_in, cudaStream_t s) {
   p.div_per = FastDiv(static_cast<uint32_t>(per > 0 ? per : 1));
   p.parts = 1;
   if (p.ntensors > 0) {
-    // tokens per block: as many as leave 16 warps an SM; below one token a block (a decode step, whose runs
-    // are single rows) its heads are shared by several
-    p.chunk = kChunk;
-    while (p.chunk > 1 && static_cast<int64_t>(p.T) * kAppendWarps < p.chunk * fill) p.chunk >>= 1;
+    // tokens per block: even turns of the resident blocks, as few as chunks of 32 allow (27,000 tokens, K alone: 54 us,
+    // by whole chunks of 32 60); below one token a block (a decode step, whose runs are single rows) its heads are
+    // shared by several
+    const int64_t slots = static_cast<int64_t>(kAppendBlocks) * num_sms();
+    const int64_t turns = (p.T + kChunk * slots - 1) / (kChunk * slots);
+    p.chunk = static_cast<int>((p.T + slots * turns - 1) / (slots * turns));
     const int64_t chunks = (static_cast<int64_t>(p.T) + p.chunk - 1) / p.chunk;
-    while (chunks * p.parts * kAppendWarps < fill && p.parts * kAppendWarps < per * p.chunk) p.parts <<= 1;
+    while (2 * chunks * p.parts <= slots && p.parts * kAppendWarps < per * p.chunk) p.parts <<= 1;
     p.row_blocks = chunks * p.parts;
     blocks = p.row_blocks;
   }
   if (p.q != nullptr) {
-    // heads per warp, in whole passes: likewise
+    // heads per warp, in whole passes: as many as leave 16 warps an SM
     p.q_heads = (p.Hq + R - 1) / R * R;
     while (p.q_heads > R && static_cast<int64_t>(p.T) * ((p.Hq + p.q_heads - 1) / p.q_heads) < fill)
       p.q_heads = (p.q_heads / R + 1) / 2 * R;
