@@ -138,10 +138,17 @@ __global__ void __launch_bounds__(kAttnThreads, D == 128 && kNH == 1 ? 4 : 1) sp
   const int32_t* const list = sp.selected + (tok * p.H + h) * sp.topk;
   if (threadIdx.x == 0) last_entry = 0;
   __syncthreads();
+  const int32_t* const table = p.block_table + static_cast<int64_t>(s) * p.max_blocks;
   int upto = 0;
+  int32_t first_b = -1, first_blk = -1;  // of entry threadIdx.x, whose table entry is not waited for here
   for (int e = threadIdx.x; e < sp.topk; e += kAttnThreads) {
     const int32_t b = LDX(list + e);
-    if (b >= 0 && b <= own_block) upto = e + 1;
+    const bool in = b >= 0 && b <= own_block;
+    if (in) upto = e + 1;
+    if (e < kAttnThreads) {
+      first_b = b;
+      if (in) first_blk = LDX(table + b);
+    }
   }
   upto = __reduce_max_sync(0xFFFFFFFFu, upto);
   if (lane == 0 && upto > 0) atomicMax(&last_entry, upto);
@@ -154,11 +161,12 @@ __global__ void __launch_bounds__(kAttnThreads, D == 128 && kNH == 1 ? 4 : 1) sp
   const int e0 = static_cast<int>(p.div_bs.div(static_cast<uint32_t>(v_begin)));
   const int e1 = v_end > v_begin ? static_cast<int>(p.div_bs.div(static_cast<uint32_t>(v_end - 1))) + 1 : e0;
   bool bad = false;
-  for (int e = e0 + threadIdx.x; e < e1; e += kAttnThreads) {
-    const int32_t b = LDX(list + e);
+  for (int e = threadIdx.x; e < e1; e += kAttnThreads) {
+    if (e < e0) continue;
+    const int32_t b = e < kAttnThreads ? first_b : LDX(list + e);
     int2 at = make_int2(-1, 0);
     if (b >= 0 && b <= own_block) {
-      const int32_t blk = LDX(p.block_table + static_cast<int64_t>(s) * p.max_blocks + b);
+      const int32_t blk = e < kAttnThreads ? first_blk : LDX(table + b);
       if (blk < 0 || blk >= p.num_blocks) {
         bad = true;
       } else {
@@ -278,6 +286,7 @@ __global__ void __launch_bounds__(kAttnThreads, D == 128 && kNH == 1 ? 4 : 1) sp
     issue(j, j);
     cp_async_commit();
   }
+
   const int my_tiles = ntile > warp ? (ntile - warp + kAttnWarps - 1) / kAttnWarps : 0;
   for (int it = 0; it < my_tiles; ++it) {
     cp_async_wait<kStages - 2>();
