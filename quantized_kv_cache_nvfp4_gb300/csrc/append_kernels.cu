@@ -25,6 +25,8 @@
 // Measured: 27,000 tokens of 24 prompts, 32 and 8 heads, head_dim 128, FP8 rows of K and pages of V, 16-token
 // blocks, with bounds: 128 us, 4.8 TB/s, 72% of a plain copy's rate; Q alone 71 us (93%), K 54, V
 // 32; 64 single tokens 5 us.  (Without packed products 2 us more; stages of 8 KB, half the warps: 236.)
+#include <algorithm>
+
 #include "page_scale.cuh"
 #include "kvq_params.h"
 
@@ -610,13 +612,15 @@ cudaError_t append_launch(const AppendParams& p_in, cudaStream_t s) {
   p.parts = 1;
   if (p.ntensors > 0) {
     // tokens per block: even turns of the resident blocks, as few as chunks of 32 allow (27,000 tokens, K alone: 54 us,
-    // by whole chunks of 32 60); below one token a block (a decode step, whose runs are single rows) its heads are
-    // shared by several
+    // by whole chunks of 32 60).  Where that is less than a common page, chunks of 32 whose runs and heads several
+    // blocks share: short chunks leave the runs to a few of them (1000 tokens in 64-token pages, 8 heads of 256:
+    // 60 us, by chunks of 2 185; 64 single tokens take 0.2 of 5 us more)
     const int64_t slots = static_cast<int64_t>(kAppendBlocks) * num_sms();
     const int64_t turns = (p.T + kChunk * slots - 1) / (kChunk * slots);
-    p.chunk = static_cast<int>((p.T + slots * turns - 1) / (slots * turns));
+    p.chunk = 2ll * p.T > kChunk * slots ? static_cast<int>((p.T + slots * turns - 1) / (slots * turns)) : kChunk;
     const int64_t chunks = (static_cast<int64_t>(p.T) + p.chunk - 1) / p.chunk;
-    while (2 * chunks * p.parts <= slots && p.parts * kAppendWarps < per * p.chunk) p.parts <<= 1;
+    const int64_t most = (std::min<int64_t>(p.chunk, p.T) * per + kAppendWarps - 1) / kAppendWarps;  // an item a warp
+    p.parts = static_cast<int>(std::max(int64_t{1}, std::min(slots / chunks, most)));
     p.row_blocks = chunks * p.parts;
     blocks = p.row_blocks;
   }
