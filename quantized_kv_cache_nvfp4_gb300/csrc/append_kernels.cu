@@ -614,7 +614,7 @@ cudaError_t append_launch(const AppendParams& p_in, cudaStream_t s) {
     // tokens per block: even turns of the resident blocks, as few as chunks of 32 allow (27,000 tokens, K alone: 54 us,
     // by whole chunks of 32 60).  Where that is less than a common page, chunks of 32 whose runs and heads several
     // blocks share: short chunks leave the runs to a few of them (1000 tokens in 64-token pages, 8 heads of 256:
-    // 60 us, by chunks of 2 185; 64 single tokens take 0.2 of 5 us more)
+    // 59 us, by chunks of 2 185; 64 single tokens take 0.2 of 5 us more)
     const int64_t slots = static_cast<int64_t>(kAppendBlocks) * num_sms();
     const int64_t turns = (p.T + kChunk * slots - 1) / (kChunk * slots);
     p.chunk = 2ll * p.T > kChunk * slots ? static_cast<int>((p.T + slots * turns - 1) / (slots * turns)) : kChunk;
