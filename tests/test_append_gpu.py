@@ -99,7 +99,7 @@ def test_without_a_rotation_it_is_the_store(fk, fv):
     _same_pool(b, _host(a))
 
 
-@pytest.mark.parametrize("tokens", [1, 40, 700, 5000])
+@pytest.mark.parametrize("tokens", [1, 40, 700, 5000, 11000, 21000])
 @pytest.mark.parametrize("fk,fv", [(PG, PG), (NV, F8)])
 def test_ragged_requests(tokens, fk, fv):
     """Several requests in one call, each beginning and ending inside a block, from a fused
