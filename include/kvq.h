@@ -231,9 +231,11 @@ typedef struct {
  * A token whose position is negative is skipped whole (kvq_plan_pages marks those behind the last
  * with -1), as is one at num_positions or beyond (KVQ_DEV_BAD_POS); one whose slot is negative or
  * past the pool (KVQ_DEV_BAD_SLOT) has its q turned only.
- * All rows of a block in one call must stand next to each other in slot_ids, as for FP8_PAGE pools,
- * where that is the pool's format or key_bounds is given (else what the block holds of scale, codes
- * or bounds is unspecified).  The inputs overlap no output but q_out. */
+ * Where the pool's format is FP8_PAGE or key_bounds is given, all rows of a block in one call must stand
+ * next to each other: from the first to the last of them slot_ids holds slots of that block only
+ * (tokens skipped for their position among them count for nothing; a token without a slot ends the
+ * rows).  Else what the block holds of scale, codes or bounds is unspecified, as after duplicate
+ * ids.  The inputs overlap no output but q_out. */
 KVQ_API kvq_status kvq_append(const kvq_bf16_in* k, const kvq_bf16_in* v, int32_t num_tokens, const int64_t* slot_ids,
                               const kvq_pool* pool, const kvq_rotation* rotation, const kvq_bf16_in* q,
                               const kvq_bf16_out* q_out, int32_t num_q_heads, void* key_bounds, uint32_t* dev_status,

@@ -10,7 +10,7 @@
 // would round twice.  Q' is rounded to bf16 once.  The bounds of (block, head) are the least
 // and the largest bf16(K') of its rows, channel by channel.
 //
-// Mapping: rows of one page that stand next to each other in slot_ids form a run; one warp serves
+// Mapping: tokens of one page that stand next to each other in slot_ids form a run; one warp serves
 // (run, head, tensor), so scales and bounds need no atomics.  A thread block looks the runs of a chunk of
 // tokens up once and shares them, heads fastest, among its warps.  D / 16 lanes (rounded up to a power of
 // two) hold a row, 8 channels of a half and their partners of the other half each, so that pairs need no
@@ -23,8 +23,8 @@
 //
 // Bound: HBM for Q, issue and 16 resident warps an SM (128 registers a thread) for K and V.
 // Measured: 27,000 tokens of 24 prompts, 32 and 8 heads, head_dim 128, FP8 rows of K and pages of V, 16-token
-// blocks, with bounds: 128 us, 4.8 TB/s, 72% of a plain copy's rate; Q alone 71 us (93%), K 54, V
-// 32; 64 single tokens 5 us.  (Without packed products 2 us more; stages of 8 KB, half the warps: 236.)
+// blocks, with bounds: 127 us, 4.9 TB/s, 73% of a plain copy's rate; Q alone 71 us (93%), K 54, V
+// 32; 64 single tokens 5.1 us.  (Without packed products 2 us more; stages of 8 KB, half the warps: 236.)
 #include <algorithm>
 
 #include "page_scale.cuh"
@@ -200,21 +200,27 @@ __device__ __forceinline__ Token load_token(const AppendParams& p, int64_t t) {
   if (p.cos_sin != nullptr) k.pos = LDX(p.positions + t);
   return k;
 }
-// Its slot: -1 where it is skipped.  `report`: the block that speaks for the token.
+// Its slot: -1 where it has none in the pool.  `report`: the block that speaks for the token.
 __device__ __forceinline__ int64_t token_slot(const AppendParams& p, const Token& k, bool report) {
   if (k.slot >= p.num_slots && report) set_status(p.status, 1u);
   if (k.pos >= p.num_positions && p.cos_sin != nullptr && report) set_status(p.status, 4u);
-  const bool turned = p.cos_sin == nullptr || (k.pos >= 0 && k.pos < p.num_positions);
-  return k.slot >= p.num_slots || !turned ? -1 : k.slot;
+  return k.slot >= p.num_slots ? -1 : k.slot;
+}
+// Whether its position lets it in.
+__device__ __forceinline__ bool turnable(const AppendParams& p, int pos) {
+  return p.cos_sin == nullptr || (pos >= 0 && pos < p.num_positions);
 }
 
-// The runs that begin in a chunk of tokens, and the chunk's tokens.
+// The runs that begin in a chunk of tokens, and the chunk's tokens.  A run goes by slots alone: a token that its
+// position keeps out stays in it as a row that is not live (a run cut there would give a page's scale and
+// bounds to two warps at once).  A run without a live row is none.
 struct Chunk {
   int64_t page[kChunk];  // of a run
   int start[kChunk];     // its first token, from the chunk's
   int length[kChunk];
-  bool begins[kChunk];   // holds the page's first slot
-  int place[kChunk];     // of a token in its page
+  bool begins[kChunk];   // a live row holds the page's first slot
+  bool whole[kChunk];    // all its rows are live
+  int place[kChunk];     // of a token in its page, -1: not live
   int pos[kChunk];
   int runs;
 };
@@ -231,44 +237,47 @@ __device__ __forceinline__ void find_runs(const AppendParams& p, int64_t t0, boo
   const int64_t before = page_of(token_slot(p, ahead, false));
   int64_t prev = __shfl_up_sync(0xFFFFFFFFu, page, 1);
   if (lane == 0) prev = before;
-  const int place = page < 0 ? 0 : static_cast<int>(slot - page * p.block_size);
+  const bool live = page >= 0 && turnable(p, token.pos);
+  const int place = live ? static_cast<int>(slot - page * p.block_size) : -1;
   ck.place[lane] = place;
-  ck.pos[lane] = token.pos;
+  ck.pos[lane] = live ? token.pos : 0;  // any that has angles, as a live row of the run does
   const uint32_t leaders = __ballot_sync(0xFFFFFFFFu, lane < p.chunk && page >= 0 && page != prev);
   const uint32_t same = __ballot_sync(0xFFFFFFFFu, page >= 0 && page == prev);  // goes on with the token before
-  const uint32_t firsts = __ballot_sync(0xFFFFFFFFu, page >= 0 && place == 0);
-  if ((leaders >> lane) & 1u) {
-    const int n = 1 + (lane == 31 ? 0 : run_bits(same >> (lane + 1)));
-    const int at = __popc(leaders & ((1u << lane) - 1u));
-    ck.page[at] = page;
-    ck.start[at] = lane;
-    ck.length[at] = min(n, 32 - lane);
-    ck.begins[at] = ((firsts >> lane) & (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u)) != 0u;
-  }
-  if (lane == 0) ck.runs = __popc(leaders);
-  __syncwarp();
-  if (leaders == 0u) return;
-  // the last run may go on behind the 32 tokens
-  const int last = __popc(leaders) - 1, b = 31 - __clz(leaders);
-  const int64_t pg = __shfl_sync(0xFFFFFFFFu, page, b);
-  if (b + ck.length[last] == 32) {
-    int n = ck.length[last];
-    bool begins = ck.begins[last];
+  const uint32_t firsts = __ballot_sync(0xFFFFFFFFu, place == 0), lives = __ballot_sync(0xFFFFFFFFu, live);
+  const bool leads = ((leaders >> lane) & 1u) != 0u;
+  int n = leads ? min(1 + (lane == 31 ? 0 : run_bits(same >> (lane + 1))), 32 - lane) : 0;
+  const uint32_t mine = n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+  bool any = ((lives >> lane) & mine) != 0u, whole = ((~lives >> lane) & mine) == 0u, begins = ((firsts >> lane) & mine) != 0u;
+  const uint32_t reach = __ballot_sync(0xFFFFFFFFu, leads && lane + n == 32);
+  if (reach != 0u) {  // the last run may go on behind the 32 tokens
+    const int b = __ffs(reach) - 1;
+    const int64_t pg = __shfl_sync(0xFFFFFFFFu, page, b);
     for (int64_t t = t0 + 32; t < p.T; t += 32) {
       const int64_t s2 = token_slot(p, behind, false);
-      const int64_t p2 = page_of(s2);
-      const int m = run_bits(__ballot_sync(0xFFFFFFFFu, p2 == pg));
-      begins = begins || __any_sync(0xFFFFFFFFu, lane < m && s2 == pg * p.block_size);
-      n += m;
+      const int m = run_bits(__ballot_sync(0xFFFFFFFFu, page_of(s2) == pg));
+      const bool in = lane < m && turnable(p, behind.pos);
+      const bool more = __any_sync(0xFFFFFFFFu, in), gap = __any_sync(0xFFFFFFFFu, lane < m && !in);
+      const bool first = __any_sync(0xFFFFFFFFu, in && s2 == pg * p.block_size);
+      if (lane == b) {
+        n += m;
+        any = any || more;
+        whole = whole && !gap;
+        begins = begins || first;
+      }
       if (m < 32) break;
       behind = load_token(p, t + 32 + lane);
     }
-    __syncwarp();
-    if (lane == 0) {
-      ck.length[last] = n;
-      ck.begins[last] = begins;
-    }
   }
+  const uint32_t runs = __ballot_sync(0xFFFFFFFFu, leads && any);
+  if (leads && any) {
+    const int at = __popc(runs & ((1u << lane) - 1u));
+    ck.page[at] = page;
+    ck.start[at] = lane;
+    ck.length[at] = n;
+    ck.begins[at] = begins;
+    ck.whole[at] = whole;
+  }
+  if (lane == 0) ck.runs = __popc(runs);
 }
 
 // The rows of a warp's items (run, tensor, head) pass through two stages of its own in shared memory,
@@ -343,7 +352,7 @@ __device__ __forceinline__ void append_items(const AppendParams& p, const Chunk&
     const int rot = key && p.cos_sin != nullptr ? p.rot : 0;
     const int length = ck.length[run], n = min(rows, length - now.r0), b = ck.start[run] + now.r0;
     const int64_t prow = ck.page[run] * p.H + h, row0 = ck.page[run] * p.block_size;
-    const bool begins = ck.begins[run], paged = fmt == 5;
+    const bool begins = ck.begins[run], whole = ck.whole[run], paged = fmt == 5;
     uint16_t* const bounds = key ? p.bounds : nullptr;
     const Lane ln = make_lane(rot, p.pairs, li, D);
     if (now.r0 == 0 && !now.again) {
@@ -354,7 +363,16 @@ __device__ __forceinline__ void append_items(const AppendParams& p, const Chunk&
     // row 0 of the page: a row's bytes are `at` times the row's of all heads behind it
     const int row_bytes = fmt == 1 ? D / 2 : D, codes_pitch = p.H * row_bytes;
     uint8_t* const codes = dst.codes + (row0 * p.H + h) * row_bytes;
-    // the stage's rows: the lane's channels and angles, the row, its place in the page
+    // rows of the stage that are not live, filled with a word (rare: a uniform branch beside the loops)
+    auto fill_dead = [&](uint32_t word) {
+      for (int r = 0; r < n; ++r) {
+        if (b + r < kChunk ? ck.place[b + r] >= 0 : turnable(p, LDX(p.positions + t0 + b + r))) continue;
+        for (int c8 = lane; c8 < pieces; c8 += 32)
+          *reinterpret_cast<uint4*>(stages + stage * kStageBytes + 2 * D * r + 16 * c8) = make_uint4(word, word, word, word);
+      }
+      __syncwarp();
+    };
+    // the stage's rows: the lane's channels and angles, the row, its place in the page (below 0: not live)
     auto each_row = [&](auto&& f) {
 #pragma unroll 1
       for (int q = 0; q < n; q += R) {
@@ -365,7 +383,8 @@ __device__ __forceinline__ void append_items(const AppendParams& p, const Chunk&
           pos = ck.pos[b + r];
         } else if (r < n) {
           at = static_cast<int>(LDX(p.slot_ids + t0 + b + r) - row0);
-          if (rot != 0) pos = LDX(p.positions + t0 + b + r);
+          if (rot != 0 || !whole) pos = LDX(p.positions + t0 + b + r);
+          if (!whole && !turnable(p, pos)) at = -1, pos = 0;
         }
         Angles a;
         if (rot != 0 && r < n) load_angles(ln, rot, p.pairs, p.cos_sin + static_cast<int64_t>(pos) * rot, a);
@@ -389,6 +408,7 @@ __device__ __forceinline__ void append_items(const AppendParams& p, const Chunk&
     };
     cp_async_wait<1>();
     __syncwarp();
+    if (!whole) fill_dead(0u);  // no part in the maxima
     bool turned = rot != 0 || !paged;
     if (!now.again && !turned) {  // page scales of rows as they are: maxima of packed bf16
       uint32_t m = 0u;
@@ -407,7 +427,7 @@ __device__ __forceinline__ void append_items(const AppendParams& p, const Chunk&
       each_row([&](const uint32_t (&v)[2][4], const Angles& a, int r, int at) {
         float y[2][8];
         turn16(ln, a, rot, p.pairs, v, y);
-        const bool live = ln.act && r < n;
+        const bool live = ln.act && r < n && at >= 0;
         const float vb[2] = {absmax8(y[0]), absmax8(y[1])};  // 0 in lanes without a row
         if (bounds != nullptr && !paged) put_back(y, r);
         if (paged) {  // the largest finite one: an infinity costs its own element only
@@ -491,7 +511,7 @@ __device__ __forceinline__ void append_items(const AppendParams& p, const Chunk&
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const uint2 c = fp8_quantize8(y[j], s, inv);
-          if (ln.act && r < n) store8B(codes + static_cast<int64_t>(at) * codes_pitch + 8 * ln.ch[j], c.x, c.y);
+          if (ln.act && r < n && at >= 0) store8B(codes + static_cast<int64_t>(at) * codes_pitch + 8 * ln.ch[j], c.x, c.y);
         }
         if (bounds != nullptr) put_back(y, r);
       });
@@ -500,6 +520,7 @@ __device__ __forceinline__ void append_items(const AppendParams& p, const Chunk&
     // rows start the block over ----
     if (bounds != nullptr && (!paged || now.again || length <= rows)) {
       __syncwarp();
+      if (!whole) fill_dead(0x7FFF7FFFu);  // NaN: no part in the bounds
       for (int c8 = lane; c8 < pieces; c8 += 32) {
         uint16_t* const at = bounds + prow * 2 * D + 8 * c8;
         uint32_t lo[4], hi[4];
