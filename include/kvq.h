@@ -491,8 +491,9 @@ KVQ_API kvq_status kvq_sparse_attention(const kvq_pool* pool, const int32_t* blo
                                         void* workspace, size_t workspace_bytes, uint32_t* dev_status,
                                         kvq_stream_t stream);
 
-/* Workspace bytes kvq_sparse_attention needs for these sizes on the current device (0 when the
- * call runs without one).  Host-only query. */
+/* Workspace bytes that are enough for kvq_sparse_attention at these sizes, and at any smaller
+ * num_tokens and topk, on the current device (0 when all those calls run without one): one buffer sized for the
+ * largest step serves every step.  A call refuses only less than it uses itself.  Host-only query. */
 KVQ_API size_t kvq_sparse_attention_workspace(int32_t num_tokens, int32_t num_heads, int32_t num_q_heads, int32_t head_dim,
                                               int32_t block_size, int32_t topk);
 

@@ -1219,7 +1219,7 @@ KVQ_API kvq_status kvq_attention(const kvq_pool* pool, const int32_t* block_tabl
 
 KVQ_API size_t kvq_sparse_attention_workspace(int32_t num_tokens, int32_t num_heads, int32_t num_q_heads, int32_t head_dim,
                                               int32_t block_size, int32_t topk) {
-  return sparse_attn_workspace_bytes(num_tokens, num_heads, num_q_heads, head_dim, block_size, topk);
+  return sparse_attn_workspace_bound(num_tokens, num_heads, num_q_heads, head_dim, block_size, topk);
 }
 
 KVQ_API kvq_status kvq_sparse_attention(const kvq_pool* pool, const int32_t* block_table, int32_t num_seqs,
@@ -1272,7 +1272,7 @@ KVQ_API kvq_status kvq_sparse_attention(const kvq_pool* pool, const int32_t* blo
   if ((st = check_dev(query_starts, "query_starts")) != KVQ_OK) return st;
   if ((st = check_dev(selected, "selected")) != KVQ_OK) return st;
   if (dev_status != nullptr && (st = check_dev(dev_status, "dev_status")) != KVQ_OK) return st;
-  const size_t need = kvq_sparse_attention_workspace(num_tokens, H, num_q_heads, D, pool->block_size, topk);
+  const size_t need = sparse_attn_workspace_bytes(num_tokens, H, num_q_heads, D, pool->block_size, topk);
   if (need > 0) {
     if ((st = check_dev(workspace, "workspace")) != KVQ_OK) return st;
     if (!aligned(workspace, 16)) return fail(KVQ_ERR_MISALIGNED, "workspace must be 16-byte aligned");

@@ -404,7 +404,9 @@ struct SparseAttnParams {
   bool cluster;              // a list's splits are a thread-block cluster
 };
 constexpr int kSparseMostBlocks = 4096;
+// What one call needs, and what is enough for any call of up to so many tokens and listed blocks.
 size_t sparse_attn_workspace_bytes(int32_t T, int32_t H, int32_t Hq, int32_t D, int32_t block_size, int32_t topk);
+size_t sparse_attn_workspace_bound(int32_t T, int32_t H, int32_t Hq, int32_t D, int32_t block_size, int32_t topk);
 cudaError_t launch_sparse_attention(const SparseAttnParams& p, cudaStream_t s);
 int query_tile_rows(int32_t D);  // rows a CTA of the tile kernel takes
 cudaError_t launch_query_tiles(const QueryAttnParams& p, cudaStream_t s);

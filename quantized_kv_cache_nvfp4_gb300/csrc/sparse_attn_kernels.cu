@@ -441,9 +441,14 @@ cudaError_t sparse_dim(const SparseAttnParams& p, cudaStream_t s) {
 
 // Splits of a list: as many as the resident blocks take at once, of 128 keys or more (4 x 8 lists of 512 keys:
 // 7.9 us, of 256 keys or more 9.1; 16 x 8 lists of up to 1536 do as well with half as many, 19.7 against 21.9).
+constexpr int kLeastKeys = 128;  // of a split
+int64_t list_keys(int32_t topk, int32_t block_size) {
+  return std::min(static_cast<int64_t>(topk) * block_size, int64_t{0x7FFF0000});
+}
+int64_t sparse_slots(int32_t D) { return (D == 256 ? 2ll : 4ll) * num_sms(); }
 int sparse_splits(int32_t T, int32_t H, int32_t D, int32_t topk, int32_t block_size) {
-  const int64_t keys = std::min(static_cast<int64_t>(topk) * block_size, int64_t{0x7FFF0000});
-  return fill_splits(static_cast<int64_t>(T) * H, (D == 256 ? 2ll : 4ll) * num_sms(), static_cast<int32_t>(keys), 128, 256);
+  return fill_splits(static_cast<int64_t>(T) * H, sparse_slots(D), static_cast<int32_t>(list_keys(topk, block_size)), kLeastKeys,
+                     2 * kLeastKeys);
 }
 
 // Not at head_dim 256 (27 lists of 64 16-token blocks in 2 splits: 24.7 us as clusters, 16.3 with the merge
@@ -456,6 +461,17 @@ size_t sparse_attn_workspace_bytes(int32_t T, int32_t H, int32_t Hq, int32_t D, 
   if (T <= 0 || H <= 0 || Hq < H || D <= 0 || block_size <= 0 || topk <= 0) return 0;
   const int n = sparse_splits(T, H, D, topk, block_size);
   return n <= 1 || use_cluster(D, n) ? 0 : static_cast<size_t>(T) * Hq * n * (D + 2) * sizeof(float);
+}
+
+// Fewer tokens take more splits, so what a call needs does not grow with them.  Split lists fill at most two waves
+// of the resident blocks (fill_splits), by at most as many splits as a list has room for: that grows with
+// both, and is the same for every larger batch.
+size_t sparse_attn_workspace_bound(int32_t T, int32_t H, int32_t Hq, int32_t D, int32_t block_size, int32_t topk) {
+  if (T <= 0 || H <= 0 || Hq < H || D <= 0 || block_size <= 0 || topk <= 0) return 0;
+  const int64_t most = std::min((list_keys(topk, block_size) + kLeastKeys - 1) / kLeastKeys, int64_t{256});
+  if (most <= 1 || use_cluster(D, static_cast<int>(most))) return 0;
+  const int64_t parts = std::min(static_cast<int64_t>(T) * H * most, 2 * sparse_slots(D));
+  return static_cast<size_t>((parts * Hq + H - 1) / H) * (D + 2) * sizeof(float);
 }
 
 cudaError_t launch_sparse_attention(const SparseAttnParams& p_in, cudaStream_t s) {
