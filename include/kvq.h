@@ -207,7 +207,7 @@ KVQ_API kvq_status kvq_quant_scatter(const kvq_bf16_in* k, const kvq_bf16_in* v,
 typedef struct {
   const float* cos_sin;     /* device f32 [num_positions][rot_dim], 16-byte aligned: the rot_dim / 2 cosines of a
                                position, then its sines (scaled frequencies and factors are the caller's
-                               matter); NULL: nothing is turned */
+                               matter); NULL, with the other fields 0: nothing is turned */
   int32_t num_positions;
   int32_t rot_dim;          /* a multiple of 16, at most head_dim; channels behind it pass */
   int32_t interleaved;      /* 0: pairs (i, i + rot_dim / 2); else (2i, 2i + 1) */

@@ -502,8 +502,12 @@ def kvq_append(k: Optional[torch.Tensor], v: Optional[torch.Tensor], slot_ids: O
             raise ValueError("cos_sin needs positions")
         if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
             raise ValueError("cos_sin must be a contiguous [positions, rot_dim] float32 tensor")
+        if cos_sin.size(0) == 0:  # its pointer is null, which means no rotation
+            raise ValueError("cos_sin has no positions")
         rot = ctypes.byref(_abi.Rotation(cos_sin.data_ptr(), cos_sin.size(0), cos_sin.size(1), 1 if interleaved else 0,
                                          _vec(positions, torch.int32, "positions", T)))
+    elif positions is not None:
+        raise ValueError("positions need cos_sin")
     if key_bounds is not None:
         _bounds_shape(key_bounds, ps.num_slots // ps.block_size, H, D)
         bounds = key_bounds.data_ptr()

@@ -774,6 +774,8 @@ KVQ_API kvq_status kvq_append(const kvq_bf16_in* k, const kvq_bf16_in* v, int32_
     return fail(KVQ_ERR_UNSUPPORTED, "num_tokens x num_heads too large");
   if (key_bounds != nullptr && k == nullptr) return fail(KVQ_ERR_INVALID_ARG, "key_bounds needs k");
   const bool turns = rotation != nullptr && rotation->cos_sin != nullptr;
+  if (rotation != nullptr && !turns && (rotation->rot_dim != 0 || rotation->num_positions != 0 || rotation->positions != nullptr))
+    return fail(KVQ_ERR_INVALID_ARG, "rotation without cos_sin: the other fields must be 0");
   if ((q != nullptr) != (q_out != nullptr)) return fail(KVQ_ERR_INVALID_ARG, "q and q_out come together");
   if (q != nullptr) {
     if (!turns) return fail(KVQ_ERR_INVALID_ARG, "q needs a rotation");
