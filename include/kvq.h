@@ -223,7 +223,8 @@ typedef struct {
  *   rotation   host struct, read during the call; NULL: K goes in as it is.
  *   q, q_out   bf16 [num_tokens][num_q_heads][head_dim]: q_out = bf16(turned q); both NULL or
  *              neither; needs a rotation.  q_out may be exactly q (same pointer and pitches);
- *              otherwise it overlaps no element of q, k or v (KVQ_ERR_INVALID_ARG).
+ *              otherwise it overlaps no element of q, k or v (KVQ_ERR_INVALID_ARG; views of unlike row
+ *              pitches are refused where their spans meet).
  *   key_bounds NULL, or device bf16 [num_slots / block_size][num_heads][2][head_dim], 16-byte
  *              aligned: [0] and [1] become the least and the largest bf16(turned k) of the block's rows, channel
  *              by channel: of this call's rows alone where they hold the block's first slot, else

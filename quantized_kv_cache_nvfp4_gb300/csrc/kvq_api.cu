@@ -742,19 +742,36 @@ KVQ_API kvq_status kvq_decode_residual(const kvq_packed* payload, const int32_t*
                                         reinterpret_cast<cudaStream_t>(stream)));
 }
 
-// Whether two strided views [rows][heads][dim] of bf16 may share an element: never where their
-// spans are apart, nor where both have one row pitch and each row's span lies in a part of that
-// pitch of its own (views of a fused projection's output).
+// Whether two strided views [rows][heads][dim] of bf16 share an element.  Exact where both have one row
+// pitch (or one row) and there are no more than 2^16 distances between their heads: heads a distance d
+// apart share one where d + k pitch is shorter than a head for some number k of rows between them.  Else
+// views whose spans meet count as sharing.
 static bool views_meet(const void* a, int64_t a_row, int64_t a_head, int64_t a_heads, const void* b, int64_t b_row,
                        int64_t b_head, int64_t b_heads, int64_t rows, int64_t dim) {
   const int64_t ra = 2 * ((a_heads - 1) * a_head + dim), rb = 2 * ((b_heads - 1) * b_head + dim);  // of one row
   const int64_t a0 = reinterpret_cast<int64_t>(a), b0 = reinterpret_cast<int64_t>(b);
   const int64_t sa = 2 * (rows - 1) * a_row + ra, sb = 2 * (rows - 1) * b_row + rb;
   if (a0 + sa <= b0 || b0 + sb <= a0) return false;
-  const int64_t pitch = 2 * a_row;
-  if (a_row != b_row || pitch <= 0) return true;
-  const int64_t off = ((b0 - a0) % pitch + pitch) % pitch;  // b's rows begin this far behind a's
-  return off < ra || off + rb > pitch;
+  if (rows > 1 && a_row != b_row) return true;
+  const int64_t pitch = rows > 1 ? 2 * a_row : 0, bytes = 2 * dim;
+  if (pitch > 0) {  // each row's span in a part of the pitch of its own (views of a fused projection)
+    const int64_t off = ((b0 - a0) % pitch + pitch) % pitch;  // b's rows begin this far behind a's
+    if (off >= ra && off + rb <= pitch) return false;
+  }
+  auto floor_div = [](int64_t n, int64_t d) { return n / d - (n % d < 0 ? 1 : 0); };
+  auto near = [&](int64_t d) {
+    if (pitch == 0) return std::abs(d) < bytes;
+    const int64_t least = floor_div(-bytes - d, pitch) + 1, most = -floor_div(d - bytes, pitch) - 1;  // k
+    return std::max(least, 1 - rows) <= std::min(most, rows - 1);
+  };
+  const bool one_pitch = a_head == b_head;  // distances go by the difference of the heads alone
+  if ((one_pitch ? a_heads + b_heads : a_heads * b_heads) > 65536) return true;
+  for (int64_t i = 0; i < a_heads; ++i)
+    for (int64_t j = 0; j < b_heads; ++j) {
+      if (one_pitch && i > 0 && j > 0) break;
+      if (near(b0 - a0 + 2 * (j * b_head - i * a_head))) return true;
+    }
+  return false;
 }
 
 KVQ_API kvq_status kvq_append(const kvq_bf16_in* k, const kvq_bf16_in* v, int32_t num_tokens, const int64_t* slot_ids,
