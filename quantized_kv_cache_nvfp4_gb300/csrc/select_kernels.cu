@@ -295,7 +295,8 @@ __global__ void __launch_bounds__(32 * (kScoreWarps<D> + 1), 1) score_kernel(con
   }
   // ---- sizes: sum_d |q_d| top_d.  Lanes of one c hold the same channels: their maxima, then lane g
   // adds up query g's.  2^-100 on both sides covers what the tensor cores may take for zero (subnormal
-  // parts); 0 only for a query of zeros.
+  // parts); 0 only for a query of zeros.  A NaN in q would make the size one (those of the bounds do not count
+  // in top); fmaxf makes it 2^-149, which does no harm: all of that query's scores are NaN, in any precision.
   float* const sizes = reinterpret_cast<float*>(smem + off_zero + 4 * D);  // [warp][query]
   float size = 0.0f;
   bool none = true;
@@ -329,14 +330,8 @@ __global__ void __launch_bounds__(32 * (kScoreWarps<D> + 1), 1) score_kernel(con
   for (int at = threadIdx.x; at < n * hn; at += 32 * kW) {
     const int i = at / hn, hh = at - i * hn;
     float a = 0.0f;
-    bool nan = false;
-    for (int x = 0; x < plan.part; ++x) {
-      const float y = sizes[(x * plan.hc + hh) * kScoreQueries + i];
-      nan = nan || isnan(y);
-      a = fmaxf(a, y);
-    }
-    STX(p.sizes + (static_cast<int64_t>(q0 + i) * p.H + h0 + hh) * p.sizes_pitch + segment,
-        nan ? __int_as_float(0x7FC00000) : a);
+    for (int x = 0; x < plan.part; ++x) a = fmaxf(a, sizes[(x * plan.hc + hh) * kScoreQueries + i]);
+    STX(p.sizes + (static_cast<int64_t>(q0 + i) * p.H + h0 + hh) * p.sizes_pitch + segment, a);
   }
   if (__any_sync(0xFFFFFFFFu, timed_out) && lane == 0) set_status(p.status, 16u);
 }
@@ -547,7 +542,7 @@ __global__ void __launch_bounds__(32 * (ScoreTile<D>::kWarps + 1), 1) score_tile
     if (lane == 0) mbar_arrive(empty0 + 8 * st);  // this warp has read the stage, and its notes
   }
   // ---- sizes: sum_d |q_d| top_d; what the tensor cores may take for zero (subnormal parts) is
-  // covered by 2^-100 on both sides ----
+  // covered by 2^-100 on both sides; a NaN as in score_kernel ----
   float* const tops = reinterpret_cast<float*>(smem + T::kOffTop);
   constexpr int kShare = kThreads > kWords ? kThreads / kWords : 1;
   for (int share = 0; share < kShare; ++share) {
@@ -868,7 +863,7 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) select_kernel
   bool bounded = true;
   for (int x = lane; x < p.sizes_n; x += 32) {
     const float y = LDX(p.sizes + row * p.sizes_pitch + x);
-    bounded = bounded && y <= 1e38f;  // not: sums that may overflow, NaN
+    bounded = bounded && y <= 1e38f;  // not: sums that may overflow, an infinite q or bound
     size = fmaxf(size, y);
   }
   // blocks below `head` and from `tail` on are listed in any case: their keys become 0
