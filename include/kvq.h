@@ -494,9 +494,15 @@ KVQ_API kvq_status kvq_sparse_attention(const kvq_pool* pool, const int32_t* blo
 
 /* Workspace bytes that are enough for kvq_sparse_attention at these sizes, and at any smaller
  * num_tokens and topk, on the current device (0 when all those calls run without one): one buffer sized for the
- * largest step serves every step.  A call refuses only less than it uses itself.  Host-only query. */
+ * largest step serves every step.  A call refuses only less than it uses itself, which
+ * kvq_sparse_attention_workspace_exact tells.  Host-only query. */
 KVQ_API size_t kvq_sparse_attention_workspace(int32_t num_tokens, int32_t num_heads, int32_t num_q_heads, int32_t head_dim,
                                               int32_t block_size, int32_t topk);
+
+/* Workspace bytes that a call at exactly these sizes uses, on the current device: for a caller that allocates for
+ * each call (most calls use none, and fewer tokens may use more).  Host-only query. */
+KVQ_API size_t kvq_sparse_attention_workspace_exact(int32_t num_tokens, int32_t num_heads, int32_t num_q_heads,
+                                                    int32_t head_dim, int32_t block_size, int32_t topk);
 
 /* Page plan of a step: block tables, slot maps and lengths from request lengths, on the
  * GPU, ready for kvq_quant_scatter, kvq_decode_attention and kvq_attention.

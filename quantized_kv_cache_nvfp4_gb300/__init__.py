@@ -570,6 +570,7 @@ def _lists(t: torch.Tensor, T: int, H: int):
 
 def kvq_sparse_attention_workspace(num_tokens: int, num_heads: int, num_q_heads: int, head_dim: int, block_size: int,
                                    topk: int) -> int:
+    """Bytes that are enough at these sizes and at any smaller num_tokens and topk."""
     return int(_lib().kvq_sparse_attention_workspace(num_tokens, num_heads, num_q_heads, head_dim, block_size, topk))
 
 
@@ -596,7 +597,7 @@ def kvq_sparse_attention(pool: KvPool, block_table: torch.Tensor, seq_lens: torc
     sel = _lists(selected, T, H)
     topk = selected.size(2)
     if workspace is None:
-        need = kvq_sparse_attention_workspace(T, H, Hq, D, pool.block_size, topk)
+        need = int(_lib().kvq_sparse_attention_workspace_exact(T, H, Hq, D, pool.block_size, topk))
         if need > 0:
             workspace = _workspace(need, q.device, stream)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()

@@ -128,6 +128,7 @@ SIGNATURES = {
                                    _I32, _I32, _P, _I32, ctypes.c_float, ctypes.c_float, ctypes.POINTER(Bf16Out), _P,
                                    ctypes.c_size_t, _P, _P]),
     "kvq_sparse_attention_workspace": (ctypes.c_size_t, [_I32] * 6),
+    "kvq_sparse_attention_workspace_exact": (ctypes.c_size_t, [_I32] * 6),
     "kvq_plan_pages": (_ST, [_P, _P, _I32, _P, _I32, _I32, _P, _I32, _P, _P, _P, _P, _I32, _P, _P, _P]),
     "kvq_storage_bytes": (ctypes.c_size_t, [_ST, _ST, _I32, _I64, _I32, _I32]),
     "kvq_status_string": (ctypes.c_char_p, [_ST]),

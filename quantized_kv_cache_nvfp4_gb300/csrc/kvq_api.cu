@@ -1241,6 +1241,11 @@ KVQ_API size_t kvq_sparse_attention_workspace(int32_t num_tokens, int32_t num_he
   return sparse_attn_workspace_bound(num_tokens, num_heads, num_q_heads, head_dim, block_size, topk);
 }
 
+KVQ_API size_t kvq_sparse_attention_workspace_exact(int32_t num_tokens, int32_t num_heads, int32_t num_q_heads,
+                                                    int32_t head_dim, int32_t block_size, int32_t topk) {
+  return sparse_attn_workspace_bytes(num_tokens, num_heads, num_q_heads, head_dim, block_size, topk);
+}
+
 KVQ_API kvq_status kvq_sparse_attention(const kvq_pool* pool, const int32_t* block_table, int32_t num_seqs,
                                         int32_t max_blocks, const int32_t* seq_lens, int32_t max_seq_len,
                                         const kvq_bf16_in* q, const int32_t* query_starts, int32_t num_tokens,

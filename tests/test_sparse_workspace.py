@@ -44,3 +44,18 @@ def test_smaller_steps_in_the_largest_steps_workspace(D, most):
         assert st == 0 and (room[size:] == 0xA5).all()
         rows = np.unique(np.linspace(0, T - 1, 6).astype(int))
         _check(c, lists, out, rows=rows)
+
+
+def test_the_bound_covers_what_each_call_uses(kvq_lib_path):
+    from quantized_kv_cache_nvfp4_gb300 import _abi
+
+    lib = _abi.load()
+    falls = 0
+    for H, Hq, D, bs, topk in ((8, 32, 128, 16, 512), (8, 16, 256, 16, 64), (1, 16, 64, 1, 4096), (5, 35, 128, 33, 77)):
+        exact = [lib.kvq_sparse_attention_workspace_exact(T, H, Hq, D, bs, topk) for T in range(1, 1500)]
+        bound = [lib.kvq_sparse_attention_workspace(T, H, Hq, D, bs, topk) for T in range(1, 1500)]
+        assert all(e <= b for e, b in zip(exact, bound)) and bound == sorted(bound)
+        falls += exact != sorted(exact)
+    assert falls > 0  # why the bound is asked for, and not the largest step's own use
+    assert lib.kvq_sparse_attention_workspace_exact(0, 2, 8, 128, 16, 4) == 0
+    assert lib.kvq_sparse_attention_workspace_exact(8, 2, 1, 128, 16, 4) == 0
