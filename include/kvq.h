@@ -440,8 +440,9 @@ KVQ_API size_t kvq_attention_workspace(int32_t num_seqs, int32_t num_tokens, int
  * score.  With the g = num_q_heads / num_heads query heads of KV head h and the bounds lo, hi of a
  * block's keys (kvq_append),
  *   score(block) = sum_d [ (sum_g max(q_gd, 0)) hi_d + (sum_g min(q_gd, 0)) lo_d ]  >=  sum_g q_g . k_t
- * for every key t of the block (up to the rounding of the bounds).  A query at position p chooses among blocks
- * 0 to p / block_size: the first_blocks first and the last_blocks last of them in any case, then the
+ * for every key t of the block as kvq_append turned it (up to the rounding of the bounds; the key that
+ * attention reads is that one rounded to the pool's format, and may lie outside them by as much).  A query
+ * at position p chooses among blocks 0 to p / block_size: the first_blocks first and the last_blocks last of them in any case, then the
  * highest scores until topk are listed (all of them where there are no more than topk); equal scores
  * go by the lower index.
  *   key_bounds     device bf16 [num_blocks][num_heads][2][head_dim], 16-byte aligned.
@@ -452,7 +453,13 @@ KVQ_API size_t kvq_attention_workspace(int32_t num_seqs, int32_t num_tokens, int
  *   head_dim 64, 128 or 256; at most 16 query heads per KV head; first_blocks + last_blocks <=
  *   topk; sequences of up to 32768 blocks (any number where topk reaches for all of them).
  *   workspace      device memory of kvq_select_blocks_workspace(...) bytes, 16-byte aligned;
- *                  caller-owned; one for each call that may run at the same time.
+ *                  caller-owned; one for each call that may run at the same time.  It holds every score:
+ *                  about 4 bytes for each (query token, KV head, block of max_seq_len), 2.3 GB for 8192 tokens
+ *                  over 131,072 in 16-token blocks and 8 heads.  A long chunk may come in pieces, each with
+ *                  the sequence's length up to its own last token: the lists are the same.
+ * max_query_len picks the kernels and the grid for all sequences of a call: many single tokens beside a long
+ * chunk are faster as two calls (512 tokens at the end of 32768 and 63 single tokens over 8192 each, 16-token
+ * blocks, 8 heads, head_dim 128, 64 listed: 547 us as one call, 157 as two).
  * The list is that of the exact scores: what binary32 cannot tell apart is scored again, in pairs of
  * binary32 numbers or in binary64 (scores of unlike blocks that agree to 2^-38 of their terms' size may go
  * either way).  A NaN score ranks below all numbers, and a
@@ -477,7 +484,8 @@ KVQ_API size_t kvq_select_blocks_workspace(int32_t num_tokens, int32_t num_heads
  *              or behind the query's own block counts for nothing, one that stands there twice
  *              counts twice.  topk at most 4096.
  * A query at position p sees the keys t <= p of its blocks; a row that sees none gets zeros.  Keys
- * of other blocks are not read.
+ * of other blocks are not read.  The grid goes by max_query_len: many single tokens beside a long chunk are faster
+ * as two calls (the step above: 365 us as one call, 190 as two).
  *   softcap    0, or 2^-10 to 2^10: logits become softcap * tanh(logit / softcap).
  *   workspace  device memory of kvq_sparse_attention_workspace(...) bytes, 16-byte aligned (may be
  *              NULL when that is 0); caller-owned; one for each call that may run at the same time.

@@ -34,7 +34,7 @@ namespace kvq {
 
 namespace {
 
-// Four warps a block, four blocks an SM (24 prompts as above: 128 us; eight warps and two blocks 136, two and
+// Four warps a block, four blocks an SM (24 prompts as above: 127 us; eight warps and two blocks 136, two and
 // eight 135: Q's blocks start as those of K and V end one by one).
 constexpr int kAppendWarps = 4, kAppendBlocks = 4;
 constexpr int kChunk = 32;  // most tokens of a block
